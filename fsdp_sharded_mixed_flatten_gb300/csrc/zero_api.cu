@@ -3,11 +3,10 @@
 // constants in double precision, packing of the per-rank pointer tables into
 // the launch arguments, dispatch to the kernels, and the stream ordering of
 // the host-buffer step.  The library allocates no memory.  Its only state is
-// a per-thread error message, per-device caches of kernel attributes and
+// a per-thread error message (zero_status.cu), per-device caches of kernel attributes and
 // occupancy, and (device side) the status word and the scratch array of the
 // no-alloc clipped step.
 #include <cmath>
-#include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -18,8 +17,7 @@
 #include "zero_flat.h"
 #include "zero_host.cuh"
 #include "zero_kernels.cuh"
-
-#define ZERO_API extern "C" __attribute__((visibility("default")))
+#include "zero_status.cuh"
 
 static_assert(zf::kMaxRanks == ZERO_MAX_RANKS, "rank limit mismatch");
 static_assert(zf::kMaxUnits == ZERO_UNITS_PER_LAUNCH && zf::kMaxPtrs == ZERO_POINTERS_PER_LAUNCH,
@@ -34,20 +32,11 @@ static_assert(5 * ZERO_MAX_RANKS + ZERO_MAX_RANKS <= ZERO_POINTERS_PER_LAUNCH,
 
 namespace {
 
-thread_local char g_err[512] = "";
-
-int fail(int code, const char* fmt, ...) {
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(g_err, sizeof g_err, fmt, ap);
-    va_end(ap);
-    return code;
-}
-
-int ok() {
-    g_err[0] = '\0';
-    return ZERO_OK;
-}
+using zf::cuda_call;
+using zf::cuda_status;
+using zf::fail;
+using zf::injected;
+using zf::ok;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -133,29 +122,6 @@ zf::AdamConsts derive_consts(const zero_adamw_t* hp, double divisor) {
     k.inv_sqrt_bc2 = static_cast<float>(1.0 / std::sqrt(bc2));
     k.divisor = static_cast<float>(divisor);
     return k;
-}
-
-int cuda_status(cudaError_t e, const char* what) {
-    if (e != cudaSuccess)
-        return fail(ZERO_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
-    return ok();
-}
-
-// Host-side failure injection for tests of the error paths: while the
-// environment variable ZERO_INJECT_FAILURE is set, a CUDA call (a launch, a
-// copy, a stream ordering) whose label contains its value is not made, and
-// the entry point returns ZERO_ERR_CUDA as it would for a failed call.  Read
-// at every call.
-bool injected(const char* what) {
-    const char* v = std::getenv("ZERO_INJECT_FAILURE");
-    return v != nullptr && v[0] != '\0' && std::strstr(what, v) != nullptr;
-}
-
-// One CUDA call with its status converted, unless a test injects its failure.
-template <class F>
-int cuda_call(const char* what, F&& call) {
-    if (injected(what)) return fail(ZERO_ERR_CUDA, "%s: injected failure", what);
-    return cuda_status(call(), what);
 }
 
 // Label of a staged launch, by mode.
@@ -446,7 +412,6 @@ int run_units(const UnitView* units, int n_units, int32_t micro_step, int32_t n_
 
 ZERO_API int32_t zero_abi_version(void) { return 1; }
 
-ZERO_API const char* zero_last_error(void) { return g_err; }
 
 ZERO_API int zero_flat_layout(const int64_t* numels, int64_t n_tensors, int32_t n_ranks,
                               int64_t* offsets_out, zero_layout_t* layout_out) {

@@ -1,0 +1,506 @@
+// Token table: y[t] = s W[id_t], and its gradient dW[v] = s sum_{t: id_t = v} dy[t],
+// summed in fp32 in the order of the tokens and rounded once.  Ids outside
+// [0, vocab) give a zero row and no gradient.
+//
+// The gradient sorts the tokens by id (stable, so the order within an id is
+// the order of the tokens, whatever the machine does), then adds up runs of
+// equal ids:
+//   sort launch: one cluster of 8 CTAs runs a radix sort of (id, token), 2 to
+//     4 passes of at most 9 bits; the other clusters write zeros to the rows
+//     of dW that no token has.
+//   sum launch: a warp takes kChunk sorted places and 256 columns.  A run
+//     inside the chunk is added up and written; a run over several chunks
+//     leaves one partial row per chunk in the workspace, and the chunk that
+//     finishes last adds the partials in chunk order.  No order depends on
+//     timing, so neither does any result.
+#include "zero_ops.cuh"
+
+#include <cooperative_groups.h>
+
+namespace cg = cooperative_groups;
+
+namespace zf {
+
+namespace {
+
+// -------------------------------------------------------------- lookup ------
+
+__device__ __forceinline__ int64_t ld_id(const void* ids, int id64, int64_t t) {
+    return id64 ? static_cast<const int64_t*>(ids)[t]
+                : static_cast<int64_t>(static_cast<const int32_t*>(ids)[t]);
+}
+
+template <class W, class Y, int VEC>
+__global__ void __launch_bounds__(256) embed_kernel(const __grid_constant__ EmbedArgs a) {
+    const int64_t per_row = a.dim / VEC;
+    const int64_t n = a.n_tokens * per_row;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+         i += step) {
+        const int64_t t = i / per_row, col = (i - t * per_row) * VEC;
+        const int64_t id = ld_id(a.ids, a.id64, t);
+        float y[VEC];
+        if (id >= 0 && id < a.vocab) {
+            const Pack<W, VEC> p =
+                ld_pack<W, VEC>(static_cast<const W*>(a.weight) + id * a.dim + col);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) y[e] = widen<W>(p.x[e]) * a.scale;
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) y[e] = 0.0f;
+        }
+        st_pack<Y, VEC>(static_cast<Y*>(a.out) + t * a.out_stride + col, pack<Y, VEC>(y));
+    }
+}
+
+// ---------------------------------------------------------------- sort ------
+
+constexpr int kSortCtas = 8;        // the cluster
+constexpr int kSortThreads = 1024;  // one token a thread and tile
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kDigitBits = 9;
+constexpr int kDigits = 1 << kDigitBits;
+constexpr int kFillRows = 32768;    // rows of one bitmap of used rows (4 KB)
+
+constexpr int kChunk = 32;          // sorted places per warp of the sum launch
+constexpr int kCols = 256;          // columns per warp
+
+// Workspace: two buffers of keys and tokens, the run counters of the sum
+// launch and its partial rows (two per chunk).
+struct Workspace {
+    int32_t* key[2];
+    int32_t* tok[2];
+    uint32_t* done;       // [chunks][column groups]
+    float* partial;       // [chunks][2][dim]
+    int64_t bytes;
+};
+
+__host__ __device__ inline int64_t up16(int64_t x) { return (x + 15) / 16 * 16; }
+__host__ __device__ inline int64_t chunks_of(int64_t n_tokens) {
+    return (n_tokens + kChunk - 1) / kChunk;
+}
+__host__ __device__ inline int64_t groups_of(int64_t dim) { return (dim + kCols - 1) / kCols; }
+
+__host__ __device__ inline Workspace workspace(void* base, int64_t n_tokens, int64_t dim) {
+    Workspace w;
+    char* p = static_cast<char*>(base);
+    char* const start = p;
+    const int64_t one = up16(n_tokens * 4);
+    for (int i = 0; i < 2; ++i) {
+        w.key[i] = reinterpret_cast<int32_t*>(p);
+        p += one;
+        w.tok[i] = reinterpret_cast<int32_t*>(p);
+        p += one;
+    }
+    w.done = reinterpret_cast<uint32_t*>(p);
+    p += up16(chunks_of(n_tokens) * groups_of(dim) * 4);
+    w.partial = reinterpret_cast<float*>(p);
+    p += chunks_of(n_tokens) * 2 * dim * 4;
+    w.bytes = p - start;
+    return w;
+}
+
+struct SortPlan {
+    int passes;
+    int bits;       // of one digit
+};
+
+__host__ __device__ inline SortPlan sort_plan(int64_t vocab) {
+    int bits = 1;                                   // keys 0 .. vocab (vocab: no row)
+    while (bits < 31 && (int64_t{1} << bits) <= vocab) ++bits;
+    const int passes = (bits + kDigitBits - 1) / kDigitBits;
+    return {passes, (bits + passes - 1) / passes};
+}
+
+struct SortSmem {
+    uint32_t hist[2][kDigits];              // this CTA's digit counts, by pass parity
+    uint32_t base[kDigits];                 // next place of each digit
+    uint16_t warp[kSortWarps][kDigits];     // the tile's counts, then offsets, per warp
+    uint32_t scan[32];
+};
+
+// The cluster's radix sort.  Pass 0 reads the ids, pass p > 0 buffer
+// (p + 1) % 2; pass p writes buffer p % 2.
+__device__ void sort_cluster(const EmbedGradArgs& a, const Workspace& ws, SortSmem& sm) {
+    cg::cluster_group cluster = cg::this_cluster();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = static_cast<int>(cluster.block_rank());
+    const SortPlan plan = sort_plan(a.vocab);
+    const int64_t share = (a.n_tokens + kSortCtas - 1) / kSortCtas;
+    const int64_t lo = rank * share < a.n_tokens ? rank * share : a.n_tokens;
+    const int64_t hi = lo + share < a.n_tokens ? lo + share : a.n_tokens;
+    const uint32_t mask = (1u << plan.bits) - 1u;
+    for (int pass = 0; pass < plan.passes; ++pass) {
+        const int shift = pass * plan.bits;
+        const bool odd = (pass & 1) != 0;
+        const int32_t* src_key = odd ? ws.key[0] : ws.key[1];
+        const int32_t* src_tok = odd ? ws.tok[0] : ws.tok[1];
+        int32_t* dst_key = odd ? ws.key[1] : ws.key[0];
+        int32_t* dst_tok = odd ? ws.tok[1] : ws.tok[0];
+        uint32_t* hist = sm.hist[pass & 1];
+        auto key_at = [&](int64_t i) -> uint32_t {
+            if (pass > 0) return static_cast<uint32_t>(src_key[i]);
+            const int64_t id = ld_id(a.ids, a.id64, i);
+            return static_cast<uint32_t>(id >= 0 && id < a.vocab ? id : a.vocab);
+        };
+        if (tid < kDigits) hist[tid] = 0;
+        __syncthreads();
+        for (int64_t i = lo + tid; i < hi; i += kSortThreads)
+            atomicAdd(&hist[(key_at(i) >> shift) & mask], 1u);
+        cluster.sync();
+        // first place of each digit for this CTA: all smaller digits, then
+        // the same digit in the CTAs before it
+        uint32_t before = 0, total = 0;
+        if (tid < kDigits) {
+            for (int r = 0; r < kSortCtas; ++r) {
+                const uint32_t h = cluster.map_shared_rank(hist, r)[tid];
+                if (r < rank) before += h;
+                total += h;
+            }
+        }
+        uint32_t incl = total;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) sm.scan[warp] = incl;
+        __syncthreads();
+        if (tid < kDigits) {
+            uint32_t s = incl - total + before;
+            for (int w = 0; w < warp; ++w) s += sm.scan[w];
+            sm.base[tid] = s;
+        }
+        for (int64_t tile = lo; tile < hi; tile += kSortThreads) {
+            const int64_t i = tile + tid;
+            const bool in = i < hi;
+            for (int d = lane; d < kDigits; d += 32) sm.warp[warp][d] = 0;
+            __syncwarp();
+            uint32_t key = 0, digit = 0;
+            int32_t tok = 0;
+            if (in) {
+                key = key_at(i);
+                tok = pass > 0 ? src_tok[i] : static_cast<int32_t>(i);
+                digit = (key >> shift) & mask;
+            }
+            // the lanes with the same digit, and this lane's place among them
+            uint32_t peers = __ballot_sync(0xFFFFFFFFu, in);
+            if (!in) peers = ~peers;
+            for (int b = 0; b < plan.bits; ++b) {
+                const uint32_t set = __ballot_sync(0xFFFFFFFFu, (digit >> b) & 1u);
+                peers &= (digit >> b) & 1u ? set : ~set;
+            }
+            const uint32_t below = __popc(peers & ((1u << lane) - 1u));
+            if (in && below == 0) sm.warp[warp][digit] = static_cast<uint16_t>(__popc(peers));
+            __syncthreads();
+            if (tid < kDigits) {
+                uint32_t s = 0;
+                for (int w = 0; w < kSortWarps; ++w) {
+                    const uint32_t n = sm.warp[w][tid];
+                    sm.warp[w][tid] = static_cast<uint16_t>(s);
+                    s += n;
+                }
+                incl = s;      // the tile's count of this digit
+            }
+            __syncthreads();
+            if (in) {
+                const uint32_t at = sm.base[digit] + sm.warp[warp][digit] + below;
+                dst_key[at] = static_cast<int32_t>(key);
+                dst_tok[at] = tok;
+            }
+            __syncthreads();
+            if (tid < kDigits) sm.base[tid] += incl;
+        }
+        __threadfence();
+        cluster.sync();
+    }
+}
+
+// Zeros to the rows of dW in [lo, hi) that no token has.
+template <class G, int VEC>
+__device__ void fill_unused(const EmbedGradArgs& a, int64_t lo, int64_t hi, uint32_t* used) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int64_t r0 = lo; r0 < hi; r0 += kFillRows) {
+        const int64_t n = hi - r0 < kFillRows ? hi - r0 : kFillRows;
+        __syncthreads();
+        for (int i = tid; i < (n + 31) / 32; i += kSortThreads) used[i] = 0;
+        __syncthreads();
+        for (int64_t t = tid; t < a.n_tokens; t += kSortThreads) {
+            const int64_t v = ld_id(a.ids, a.id64, t) - r0;
+            if (v >= 0 && v < n) atomicOr(&used[v >> 5], 1u << (v & 31));
+        }
+        __syncthreads();
+        float zero[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) zero[e] = 0.0f;
+        const Pack<G, VEC> z = pack<G, VEC>(zero);
+        for (int64_t r = warp; r < n; r += kSortWarps) {
+            if ((used[r >> 5] >> (r & 31)) & 1u) continue;
+            G* row = static_cast<G*>(a.grad_weight) + (r0 + r) * a.dim;
+            for (int64_t c = static_cast<int64_t>(lane) * VEC; c < a.dim; c += 32 * VEC)
+                st_pack<G, VEC>(row + c, z);
+        }
+    }
+}
+
+template <class G, int VEC>
+__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads)
+embed_sort_kernel(const __grid_constant__ EmbedGradArgs a) {
+    __shared__ SortSmem sm;
+    const Workspace ws = workspace(a.workspace, a.n_tokens, a.dim);
+    if (blockIdx.x < kSortCtas) {
+        const int64_t n_done = chunks_of(a.n_tokens) * groups_of(a.dim);
+        for (int64_t i = blockIdx.x * kSortThreads + threadIdx.x; i < n_done;
+             i += kSortCtas * kSortThreads)
+            ws.done[i] = 0;
+        sort_cluster(a, ws, sm);
+    } else {
+        const int64_t ctas = gridDim.x - kSortCtas, i = blockIdx.x - kSortCtas;
+        const int64_t per = (a.vocab + ctas - 1) / ctas;
+        const int64_t lo = i * per, hi = lo + per < a.vocab ? lo + per : a.vocab;
+        if (lo < hi) fill_unused<G, VEC>(a, lo, hi, reinterpret_cast<uint32_t*>(&sm));
+    }
+}
+
+static_assert(sizeof(SortSmem) >= kFillRows / 8, "the bitmap shares the sort's memory");
+
+// ----------------------------------------------------------------- sum ------
+
+// Lane columns: N groups of VEC, group n at (32 n + lane) VEC.
+template <class Y, class G, int VEC>
+__global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ EmbedGradArgs a) {
+    constexpr int kPer = kCols / 32;
+    constexpr int N = kPer / VEC;
+    constexpr int kAhead = 8;
+    const int lane = threadIdx.x & 31;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32;
+    const int64_t groups = groups_of(a.dim), n_chunks = chunks_of(a.n_tokens);
+    const int64_t chunk = unit / groups, group = unit - chunk * groups;
+    if (chunk >= n_chunks) return;
+    const Workspace ws = workspace(a.workspace, a.n_tokens, a.dim);
+    const bool odd = sort_plan(a.vocab).passes % 2 != 0;      // the last pass's buffer
+    const int32_t* key = odd ? ws.key[0] : ws.key[1];
+    const int32_t* tok = odd ? ws.tok[0] : ws.tok[1];
+    const int64_t col0 = group * kCols;
+    const int64_t first = chunk * kChunk;
+    const int n = static_cast<int>(a.n_tokens - first < kChunk ? a.n_tokens - first : kChunk);
+    const int32_t none = static_cast<int32_t>(a.vocab);
+
+    // this lane's place of the chunk, and the neighbours' keys
+    const int32_t my_key = lane < n ? key[first + lane] : none;
+    const int32_t my_tok = lane < n ? tok[first + lane] : 0;
+    const int32_t key_before = first > 0 ? key[first - 1] : -1;
+    const int32_t key_after = first + n < a.n_tokens ? key[first + n] : -1;
+
+    const int live = __popc(__ballot_sync(0xFFFFFFFFu, my_key != none));   // a prefix
+
+    float acc[kPer];
+    auto clear = [&] {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = 0.0f;
+    };
+    auto write_row = [&](int32_t k) {
+        G* row = static_cast<G*>(a.grad_weight) + static_cast<int64_t>(k) * a.dim;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int64_t c = col0 + (j * 32 + lane) * VEC;
+            if (c >= a.dim) continue;
+            float y[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) y[e] = acc[j * VEC + e] * a.scale;
+            if (a.accumulate) {
+                const Pack<G, VEC> old = ld_pack<G, VEC>(row + c);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) y[e] += widen<G>(old.x[e]);
+            }
+            st_pack<G, VEC>(row + c, pack<G, VEC>(y));
+        }
+    };
+    auto put_partial = [&](int slot) {
+        float* p = ws.partial + (chunk * 2 + slot) * a.dim;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const int64_t c = col0 + (j * 32 + lane) * VEC + e;
+                if (c < a.dim) __stcg(p + c, acc[j * VEC + e]);
+            }
+        }
+    };
+    // A run of key k over several chunks, `first_chunk` .. `last_chunk`, of
+    // which this one has left its partial: the last to come adds them up.
+    auto join = [&](int32_t k, int64_t first_chunk, int64_t last_chunk) {
+        __threadfence();
+        __syncwarp();
+        uint32_t seen = 0;
+        if (lane == 0) seen = atomicAdd(&ws.done[first_chunk * groups + group], 1u);
+        seen = __shfl_sync(0xFFFFFFFFu, seen, 0);
+        if (seen != static_cast<uint32_t>(last_chunk - first_chunk)) return;
+        __threadfence();
+        clear();
+        for (int64_t q = first_chunk; q <= last_chunk; ++q) {
+            // the run starts in its first chunk's second slot, unless the
+            // chunk's first place starts it; later chunks use the first slot
+            const int slot = q == first_chunk ? 1 : 0;
+            const float* p = ws.partial + (q * 2 + slot) * a.dim;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const int64_t c = col0 + (j * 32 + lane) * VEC + e;
+                    if (c < a.dim) acc[j * VEC + e] += __ldcg(p + c);
+                }
+            }
+        }
+        write_row(k);
+    };
+    // The chunk in which the run of k that enters this chunk starts.
+    auto run_start = [&](int32_t k) -> int64_t {
+        for (int64_t q = chunk - 1;; q -= 32) {
+            // chunk q - lane: does the run enter it from the one before?
+            const int64_t c = q - lane;
+            const bool goes_on = c > 0 && key[c * kChunk - 1] == k;
+            const uint32_t stop = __ballot_sync(0xFFFFFFFFu, !goes_on);
+            if (stop != 0) return q - (__ffs(stop) - 1);
+        }
+    };
+    // The chunk in which the run of k that leaves this chunk ends.
+    auto run_end = [&](int32_t k) -> int64_t {
+        for (int64_t q = chunk + 1;; q += 32) {
+            const int64_t c = q + lane, next = (c + 1) * kChunk;
+            const bool goes_on = next < a.n_tokens && key[next] == k;
+            const uint32_t stop = __ballot_sync(0xFFFFFFFFu, !goes_on);
+            if (stop != 0) return q + (__ffs(stop) - 1);
+        }
+    };
+
+    clear();
+    int begin = 0;                                  // first place of the current run
+    for (int i0 = 0; i0 < live; i0 += kAhead) {
+        Pack<Y, VEC> v[kAhead][N];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int32_t t = __shfl_sync(0xFFFFFFFFu, my_tok, (i0 + u) & 31);
+            if (i0 + u < live) {
+                const Y* row = static_cast<const Y*>(a.grad_out) + t * a.grad_stride;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const int64_t c = col0 + (j * 32 + lane) * VEC;
+                    if (c < a.dim) v[u][j] = ld_pack<Y, VEC>(row + c);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int i = i0 + u;
+            if (i >= live) break;
+            const int32_t k = __shfl_sync(0xFFFFFFFFu, my_key, i);
+            const int32_t after = __shfl_sync(0xFFFFFFFFu, my_key, (i + 1) & 31);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int64_t c = col0 + (j * 32 + lane) * VEC;
+                if (c < a.dim) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) acc[j * VEC + e] += widen<Y>(v[u][j].x[e]);
+                }
+            }
+            if (i + 1 < n && after == k) continue;
+            // the run ends here, or goes on in the next chunk
+            const bool enters = begin == 0 && key_before == k;
+            const bool leaves = i + 1 == n && key_after == k;
+            if (!enters && !leaves) {
+                write_row(k);
+            } else {
+                put_partial(enters ? 0 : 1);
+                const int64_t from = enters ? run_start(k) : chunk;
+                const int64_t to = leaves ? run_end(k) : chunk;
+                join(k, from, to);
+            }
+            clear();
+            begin = i + 1;
+        }
+    }
+}
+
+template <class W, class Y>
+cudaError_t embed(const EmbedArgs& a, int want, cudaStream_t stream) {
+    const bool vec = aligned_to(a.weight, want * static_cast<int64_t>(sizeof(W))) &&
+                     aligned_to(a.out, want * static_cast<int64_t>(sizeof(Y))) &&
+                     a.dim % want == 0 && a.out_stride % want == 0;
+    const int64_t n = a.n_tokens * (vec ? a.dim / want : a.dim);
+    const int64_t most = static_cast<int64_t>(device_sms()) * 64;
+    const int64_t blocks = (n + 255) / 256;
+    const unsigned g = static_cast<unsigned>(blocks < most ? blocks : most);
+    constexpr int kV = sizeof(W) == 2 && sizeof(Y) == 2 ? 8 : 4;
+    if (vec) {
+        embed_kernel<W, Y, kV><<<g, 256, 0, stream>>>(a);
+    } else {
+        embed_kernel<W, Y, 1><<<g, 256, 0, stream>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+template <class Y, class G>
+cudaError_t embed_sum(const EmbedGradArgs& a, cudaStream_t stream) {
+    constexpr int kV = sizeof(Y) == 2 && sizeof(G) == 2 ? 8 : 4;
+    const bool vec = aligned_to(a.grad_out, kV * static_cast<int64_t>(sizeof(Y))) &&
+                     aligned_to(a.grad_weight, kV * static_cast<int64_t>(sizeof(G))) &&
+                     a.dim % kV == 0 && a.grad_stride % kV == 0;
+    const int64_t warps = chunks_of(a.n_tokens) * groups_of(a.dim);
+    const unsigned g = static_cast<unsigned>((warps + 7) / 8);
+    if (vec) {
+        embed_sum_kernel<Y, G, kV><<<g, 256, 0, stream>>>(a);
+    } else {
+        embed_sum_kernel<Y, G, 1><<<g, 256, 0, stream>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_embed(const EmbedArgs& a, int weight_bytes, int out_bytes,
+                         cudaStream_t stream) {
+    if (weight_bytes == 2)
+        return out_bytes == 2 ? embed<uint16_t, uint16_t>(a, 8, stream)
+                              : embed<uint16_t, float>(a, 4, stream);
+    return out_bytes == 2 ? embed<float, uint16_t>(a, 4, stream)
+                          : embed<float, float>(a, 4, stream);
+}
+
+int64_t embed_grad_workspace(int64_t n_tokens, int64_t dim) {
+    return workspace(nullptr, n_tokens, dim).bytes;
+}
+
+cudaError_t launch_embed_sort(const EmbedGradArgs& a, int grad_weight_bytes, cudaStream_t stream) {
+    // one cluster sorts; where every row is written, the rest of the GPU
+    // writes zeros meanwhile
+    int clusters = 1;
+    if (!a.accumulate) {
+        const int64_t rows = (a.vocab + kSortWarps - 1) / kSortWarps;
+        const int64_t most = 2 * device_sms() / kSortCtas - 1;
+        const int64_t need = (rows + kSortCtas - 1) / kSortCtas;
+        clusters += static_cast<int>(need < most ? need : most);
+    }
+    const unsigned g = static_cast<unsigned>(clusters * kSortCtas);
+    const int want = 16 / grad_weight_bytes;
+    const bool vec = aligned_to(a.grad_weight, 16) && a.dim % want == 0;
+    if (grad_weight_bytes == 4) {
+        if (vec) embed_sort_kernel<float, 4><<<g, kSortThreads, 0, stream>>>(a);
+        else embed_sort_kernel<float, 1><<<g, kSortThreads, 0, stream>>>(a);
+    } else {
+        if (vec) embed_sort_kernel<uint16_t, 8><<<g, kSortThreads, 0, stream>>>(a);
+        else embed_sort_kernel<uint16_t, 1><<<g, kSortThreads, 0, stream>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_embed_sum(const EmbedGradArgs& a, int grad_bytes, int grad_weight_bytes,
+                             cudaStream_t stream) {
+    if (grad_bytes == 2)
+        return grad_weight_bytes == 2 ? embed_sum<uint16_t, uint16_t>(a, stream)
+                                      : embed_sum<uint16_t, float>(a, stream);
+    return grad_weight_bytes == 2 ? embed_sum<float, uint16_t>(a, stream)
+                                  : embed_sum<float, float>(a, stream);
+}
+
+}  // namespace zf

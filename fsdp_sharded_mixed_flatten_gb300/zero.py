@@ -120,6 +120,23 @@ def load() -> ctypes.CDLL:
         lib.zero_device_status.restype = ctypes.c_int
         lib.zero_selftest_wait_timeout.argtypes = [i64, p]
         lib.zero_selftest_wait_timeout.restype = ctypes.c_int
+        f64, out64 = ctypes.c_double, ctypes.POINTER(ctypes.c_int64)
+        for name, args in {
+            "zero_embedding": [p, i32, i64, p, i32, i64, i64, f64, p, i32, i64, p],
+            "zero_embedding_grad": [p, i32, i64, p, i32, i64, f64, p, i32, i64, i64, i32, p, i64,
+                                    p],
+            "zero_embedding_grad_workspace_bytes": [i64, i64, i64, out64],
+            "zero_layer_norm": [p, i32, i64, i64, i64, p, p, i32, f64, p, i64, p, p, p],
+            "zero_layer_norm_grad": [p, p, i32, i64, i64, i64, i64, p, i32, p, p, p, i64, p, p, p,
+                                     i64, p],
+            "zero_layer_norm_grad_workspace_bytes": [i64, i64, out64],
+            "zero_distill_loss": [p, i32, i64, i64, i64, p, p, i32, i64, p, f64, p, p],
+            "zero_distill_loss_grad": [p, i32, i64, i64, i64, p, p, i32, i64, p, f64, p, p, i64,
+                                       p],
+        }.items():
+            fn = getattr(lib, name)
+            fn.argtypes = args
+            fn.restype = ctypes.c_int
         lib.zero_last_error.argtypes = []
         lib.zero_last_error.restype = ctypes.c_char_p
         lib.zero_abi_version.argtypes = []

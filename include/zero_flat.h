@@ -52,7 +52,8 @@
  *     kernel fault are observed by synchronising the stream.
  *   - Pointer arrays (`const T* const* x`) are HOST arrays of DEVICE pointers;
  *     they are copied into the launch, so they may be freed on return.
- *   - Every device pointer must be 16-byte aligned (ZERO_ERR_MISALIGNED).
+ *   - Every device pointer must be 16-byte aligned (ZERO_ERR_MISALIGNED),
+ *     except in the operators around the root unit at the end of this file.
  *   - Offsets and sizes are element counts (int64_t).
  *   - Elements [P, P_pad) -- the tail padding -- of the gradients, master, m
  *     and v must be zero on entry; they then stay zero.
@@ -467,6 +468,142 @@ int zero1_accumulate(const uint16_t* const* grads, float* const* full_accum, int
 int zero1_step(const float* const* full_accum, int32_t n_micro, float* const* master,
                float* const* m, float* const* v, uint16_t* const* full_params, int32_t n_out,
                const zero_layout_t* layout, const zero_adamw_t* hp, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Operators around the root unit.  FSDP's root unit holds the token table,
+ * the position table and the final layer norm ([LA] section 9.1); these entry
+ * points run its forward and backward pass up to the head's matrix products,
+ * reading parameters from a flat parameter buffer and writing gradients into a
+ * rank's flat gradient.  No counterpart on the pages, which start from the
+ * ranks' gradients.
+ *
+ * Conventions, besides those above:
+ *   - An array's type is its element size: 2 for bf16, 4 for fp32 (ids: 4 for
+ *     int32, 8 for int64).  Sums, softmax statistics and norms are held in
+ *     fp32, and each result is rounded once to its array's type.
+ *   - Arrays need only the alignment of their element type, since a tensor of
+ *     a flat buffer starts at any element; rows and addresses on 16-byte
+ *     boundaries use wide accesses.  Workspaces are 16-byte aligned.
+ *   - A matrix has contiguous rows, `..._stride` elements apart; a stride must
+ *     be at least the row's length, and what lies between rows is not touched.
+ *   - A call with no tokens or rows is valid: it writes zeros to gradients
+ *     that are sums over them, and nothing else.
+ *   - Results do not depend on timing: the same call on the same inputs gives
+ *     the same bits on the same kind of GPU.
+ *   - Output arrays must not overlap inputs or each other, but for the places
+ *     named below.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * zero_embedding -- device.  Token lookup with scaling:
+ *   out[t] = scale * weight[ids[t]],   0 where ids[t] is outside [0, vocab).
+ *   ids[n_tokens]          int32 or int64
+ *   weight                 [vocab][dim] contiguous
+ *   out                    n_tokens rows of dim
+ * Errors: INVALID_ARG, MISALIGNED, SIZE (n_tokens, vocab or dim beyond 32
+ * bits, a stride below dim), CUDA.
+ */
+int zero_embedding(const void* ids, int32_t id_bytes, int64_t n_tokens, const void* weight,
+                   int32_t weight_bytes, int64_t vocab, int64_t dim, double scale, void* out,
+                   int32_t out_bytes, int64_t out_stride, void* stream);
+
+/*
+ * zero_embedding_grad -- device.  Gradient of zero_embedding:
+ *   grad_weight[v] = scale * sum_{t: ids[t] = v} grad_out[t]
+ * summed in fp32 in a fixed order over the tokens sorted by id, and rounded
+ * once.  Ids outside [0, vocab) contribute nothing (their rows of grad_out are
+ * not read).
+ *   accumulate == 0   every row of grad_weight is written, rows without a
+ *                     token with zeros
+ *   accumulate == 1   the sum is added to grad_weight (a table tied with the
+ *                     head holds the head's gradient already); rows without a
+ *                     token are not touched
+ *   workspace         caller-owned device scratch of at least the bytes
+ *                     zero_embedding_grad_workspace_bytes reports, 16-byte
+ *                     aligned, of any content; calls that may overlap on the
+ *                     GPU need one each
+ * Errors: as zero_embedding; ZERO_ERR_SIZE if the workspace is too small.
+ */
+int zero_embedding_grad(const void* ids, int32_t id_bytes, int64_t n_tokens, const void* grad_out,
+                        int32_t grad_out_bytes, int64_t grad_out_stride, double scale,
+                        void* grad_weight, int32_t grad_weight_bytes, int64_t vocab, int64_t dim,
+                        int32_t accumulate, void* workspace, int64_t workspace_bytes,
+                        void* stream);
+
+/* zero_embedding_grad_workspace_bytes -- host. */
+int zero_embedding_grad_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t dim,
+                                        int64_t* bytes);
+
+/*
+ * zero_layer_norm -- device.  For every row x of dim values:
+ *   mean = sum(x) / dim,  rstd = 1 / sqrt(sum((x - mean)^2) / dim + eps),
+ *   out = (x - mean) * rstd * weight + bias
+ *   x, out            n_rows rows of dim, of type act_bytes; out may be x
+ *                     (with the same stride)
+ *   weight, bias      dim values of type param_bytes; NULL: ones, zeros
+ *   mean, rstd        n_rows fp32 each, or NULL where no backward pass follows
+ * Errors: INVALID_ARG, MISALIGNED, SIZE (dim > ZERO_MAX_NORM_DIM), CUDA.
+ */
+#define ZERO_MAX_NORM_DIM 16384
+int zero_layer_norm(const void* x, int32_t act_bytes, int64_t n_rows, int64_t dim,
+                    int64_t x_stride, const void* weight, const void* bias, int32_t param_bytes,
+                    double eps, void* out, int64_t out_stride, float* mean, float* rstd,
+                    void* stream);
+
+/*
+ * zero_layer_norm_grad -- device.  Gradient of zero_layer_norm from the
+ * forward's mean and rstd, with xh = (x - mean) * rstd and g = grad_out * weight:
+ *   grad_x = rstd * (g - sum(g)/dim - xh * sum(g * xh)/dim)
+ *   grad_weight = sum_rows grad_out * xh,   grad_bias = sum_rows grad_out
+ *   grad_x            may be grad_out or x (with the same stride)
+ *   grad_weight, grad_bias   dim values of type param_bytes; NULL: not wanted
+ *   workspace         device scratch of at least the bytes
+ *                     zero_layer_norm_grad_workspace_bytes reports for the
+ *                     current device, 16-byte aligned, of any content
+ * Errors: as zero_layer_norm; ZERO_ERR_SIZE if the workspace is too small.
+ */
+int zero_layer_norm_grad(const void* grad_out, const void* x, int32_t act_bytes, int64_t n_rows,
+                         int64_t dim, int64_t grad_out_stride, int64_t x_stride,
+                         const void* weight, int32_t param_bytes, const float* mean,
+                         const float* rstd, void* grad_x, int64_t grad_x_stride,
+                         void* grad_weight, void* grad_bias, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+
+/* zero_layer_norm_grad_workspace_bytes -- host. */
+int zero_layer_norm_grad_workspace_bytes(int64_t n_rows, int64_t dim, int64_t* bytes);
+
+/*
+ * zero_distill_loss -- device.  Distillation from a teacher's top logits.  For
+ * a row of student logits z and the teacher's entries (id_k, l_k), k < top:
+ *   p = softmax(l / temperature) over the row's entries with an id in [0, vocab),
+ *   q = softmax(z / temperature) over the whole row,
+ *   loss = weight * temperature^2 * sum_k p_k * (log p_k - log q[id_k])
+ * A row with weight 0 or without an entry (no id in range, or every l_k there
+ * -inf) has loss 0, whatever its logits hold.  Entries with p_k = 0 add
+ * nothing; equal ids are entries of their own.
+ *   logits            n_rows rows of vocab, of type logits_bytes
+ *   teacher_ids       [n_rows][top] int32, contiguous (1 <= top <= ZERO_MAX_TEACHER)
+ *   teacher_logits    [n_rows][top], contiguous, of type teacher_bytes
+ *   weights           n_rows fp32, or NULL (ones)
+ *   loss              n_rows fp32
+ *
+ * zero_distill_loss_grad writes the gradient with respect to the logits too,
+ *   grad_logits[v] = weight * temperature * (q_v - sum_{k: id_k = v} p_k)
+ * (0 in rows whose loss is 0 for want of weight or entries), of the logits'
+ * type; grad_logits may be logits (with the same stride).
+ * Errors: INVALID_ARG (temperature not positive and finite, ...), MISALIGNED,
+ * SIZE, CUDA.
+ */
+#define ZERO_MAX_TEACHER 1024
+int zero_distill_loss(const void* logits, int32_t logits_bytes, int64_t n_rows, int64_t vocab,
+                      int64_t logits_stride, const int32_t* teacher_ids,
+                      const void* teacher_logits, int32_t teacher_bytes, int64_t top,
+                      const float* weights, double temperature, float* loss, void* stream);
+int zero_distill_loss_grad(const void* logits, int32_t logits_bytes, int64_t n_rows,
+                           int64_t vocab, int64_t logits_stride, const int32_t* teacher_ids,
+                           const void* teacher_logits, int32_t teacher_bytes, int64_t top,
+                           const float* weights, double temperature, float* loss,
+                           void* grad_logits, int64_t grad_logits_stride, void* stream);
 
 /* Message for the last non-OK return on the calling thread ("" if none). */
 const char* zero_last_error(void);
