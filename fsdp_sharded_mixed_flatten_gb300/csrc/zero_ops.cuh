@@ -72,6 +72,55 @@ __device__ __forceinline__ void st_param(void* p, bool f32, int64_t i, float x) 
     }
 }
 
+// Pairs of fp32 in one 64-bit register, from end to end, so that no moves
+// form them.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ float2 unpair(Pair p) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair p;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
+    return p;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair p;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
+    return p;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair p;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(a), "l"(b), "l"(c));
+    return p;
+}
+// Two bf16 of a word (the lower one first) as fp32, and back.
+__device__ __forceinline__ Pair widen2(uint32_t w) {
+    Pair p;
+    asm("{\n\t.reg .b32 lo, hi;\n\t"
+        "shl.b32 lo, %1, 16;\n\t"
+        "and.b32 hi, %1, 0xFFFF0000;\n\t"
+        "mov.b64 %0, {lo, hi};\n\t}"
+        : "=l"(p)
+        : "r"(w));
+    return p;
+}
+__device__ __forceinline__ uint32_t narrow2(Pair p) {
+    uint32_t w;
+    asm("{\n\t.reg .f32 a, b;\n\t"
+        "mov.b64 {a, b}, %1;\n\t"
+        "cvt.rn.bf16x2.f32 %0, b, a;\n\t}"
+        : "=r"(w)
+        : "l"(p));
+    return w;
+}
+
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
@@ -140,6 +189,7 @@ struct NormArgs {
     int64_t out_stride;
     int32_t dim;
     int32_t param_f32;        // weight, bias and their gradients are fp32
+    int32_t group_threads;    // threads that hold a row (set by the launch)
     float eps;
 };
 
@@ -171,6 +221,9 @@ struct DistillArgs {
     float c;                  // log2(e) / temperature
     float tau;
     float tau2;
+    int32_t ranks;            // CTAs of a row (set by the launch)
+    int32_t stage_words;      // 16-byte words of a row that a CTA keeps
+    int32_t section;          // words a thread of one of its copy groups
 };
 
 cudaError_t launch_distill(const DistillArgs& a, int logits_bytes, cudaStream_t stream);
