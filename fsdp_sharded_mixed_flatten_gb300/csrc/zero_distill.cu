@@ -4,18 +4,23 @@
 //   loss = w tau^2 sum_k p_k (log p_k - log q_{id_k}),
 //   dloss/dz_v = w tau (q_v - sum_{k: id_k = v} p_k).
 //
-// A cluster of CTAs holds a row in shared memory, each CTA a slice, and stays
-// for many rows.  DRAM sees one read and one write of the logits:
-//   - every thread copies its own 16-byte words with cp.async and is the only
+// A CTA holds a row in shared memory, two CTAs an SM, and works through many
+// rows.  DRAM sees one read and one write of the logits:
+//   - every worker copies its own 16-byte words with cp.async and is the only
 //     one to read them, so no barrier separates copy and use;
-//   - it adds up the exponentials as the words arrive; one cluster barrier
-//     exchanges the warps' sums through distributed shared memory;
+//   - it adds up the exponentials as the words arrive; one barrier a row
+//     exchanges the warps' sums, the teacher's with the student's;
 //   - it forms the gradient from the copy, and into each word it has used up
-//     it copies the same word of the CTA's next row, so that reads and writes
-//     of memory overlap all the time;
-//   - one more warp reads the teacher's entries, a row ahead, and sets the
-//     gradient's entries right once the plain values are written.
-// Words beyond shared memory are read again from L2.
+//     goes the same word of the CTA's next row, so that reads and writes of
+//     memory overlap;
+//   - warps of their own hold the teacher's entries, one a thread, fetched a row
+//     ahead.  The entries of the gradient are written, and the loss added up,
+//     after the next row's barrier, when every plain value of the row is there.
+// Words beyond shared memory are read again, from L2.  Where rows are fewer
+// than SMs a cluster of CTAs takes a row, each a slice, and the sums go through
+// distributed shared memory; with many rows that costs more than it gives (a
+// cluster barrier waits for the gradient's stores to arrive: 4096 x 50257 took
+// 221 us with clusters of one CTA and a split barrier).
 //
 // Exponentials are 2^(z c - M), c = log2(e) / tau: one fused multiply-add and
 // one ex2 each.  M is an integer, ceil(c max z) of what a thread has seen, so
@@ -34,16 +39,16 @@ namespace zf {
 
 namespace {
 
-constexpr int kWorkers = 384;                    // threads that hold the slice
-constexpr int kWorkerWarps = kWorkers / 32;
-constexpr int kRowThreads = kWorkers + 32;       // and the teacher's warp
 constexpr int kMaxCluster = 8;
 constexpr int kSections = 3;                     // copy groups of a row
-constexpr int kPatchAlone = 128;                 // entries the teacher's warp patches by itself
-constexpr int kSliceBytes = 68 * 1024;           // a CTA's slice with 3 CTAs an SM
-constexpr int kMostBytes = 176 * 1024;           // what one CTA an SM holds
+constexpr int kRing = 4;                         // rows whose entries are kept
+constexpr int kWorkerWarps = 14;
+constexpr int kEntryWarps = 2;
+constexpr int kSmallRow = 24 * 1024;             // rows up to this take CTAs of 8 warps
+constexpr int kMostBytes = 110 * 1024;           // of a CTA: the words and the entries
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kFar = 1e30f;
+constexpr float kNone = -4e30f;                  // off of a sum without terms
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -120,11 +125,18 @@ struct Word<float> {
 // A sum of 2^(z c - off) with an integer off.
 struct Running {
     float off, s;
+    __device__ __forceinline__ void raise(float to) {
+        if (to > off) {
+            s *= ex2(off - to);
+            off = to;
+        }
+    }
 };
 
 // Joined over a warp: the largest off, every sum scaled to it.
 __device__ __forceinline__ Running warp_join(Running r) {
-    const float off = warp_max(r.off);
+    float off;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(off) : "f"(r.off));
     return {off, warp_sum(r.s * ex2(r.off - off))};
 }
 
@@ -137,43 +149,36 @@ struct Exponent {
     }
 };
 
-// This CTA's slice of a row: n 16-byte words from `words` on, of which the
-// first `staged` are in shared memory, and the row's single elements before
-// its first 16-byte boundary (rank 0) and after its last (the last rank).
+// This CTA's slice of a row, elements [lo, hi): n 16-byte words from element
+// `first` on, of which the first `staged` are in shared memory, and single
+// elements before (rank 0: up to the row's first 16-byte boundary) and after
+// them (the last rank).
 template <class T>
 struct Slice {
     static constexpr int kV = 16 / sizeof(T);
     const T* z;             // the row
-    int first;              // the slice's first element (of its words)
-    int n, staged;
-    int single, single_n;   // this CTA's single elements: [single, single + single_n)
-    int head;
+    int first, n, staged, lo, hi;
 
-    __device__ Slice(const DistillArgs& a, int64_t row, int rank) {
-        z = static_cast<const T*>(a.logits) + row * a.logits_stride;
+    __device__ Slice(const DistillArgs& a, const T* at, int rank) {
+        z = at;
         const int vocab = static_cast<int>(a.vocab);
         const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(z) % 16) / sizeof(T);
-        head = mis == 0 ? 0 : kV - mis;
-        if (head > vocab) head = vocab;
+        const int head = min(vocab, mis == 0 ? 0 : kV - mis);
         const int words = (vocab - head) / kV;
-        const int per = (words + a.ranks - 1) / a.ranks;
-        const int v0 = rank * per < words ? rank * per : words;
-        n = words - v0 < per ? words - v0 : per;
-        staged = n < a.stage_words ? n : a.stage_words;
+        const int per = (words + a.ranks - 1) >> a.rank_shift;
+        const int v0 = min(rank * per, words);
+        n = min(words - v0, per);
+        staged = min(n, a.stage_words);
         first = head + v0 * kV;
-        // with one rank both ends are its own: then the head is handled with
-        // the tail, as head_n() more elements
-        single = rank == a.ranks - 1 ? head + words * kV : 0;
-        single_n = rank == a.ranks - 1 ? vocab - single : 0;
-        if (rank != 0) head = 0;
+        lo = rank == 0 ? 0 : first;
+        hi = rank == a.ranks - 1 ? vocab : first + n * kV;
     }
     __device__ const T* word(int i) const { return z + first + static_cast<int64_t>(i) * kV; }
-    // single element j of this CTA (j < head + single_n), as an index of the row
-    __device__ int single_at(int j) const { return j < head ? j : single + (j - head); }
-    __device__ int singles() const { return head + single_n; }
+    __device__ int singles() const { return hi - lo - n * kV; }
+    __device__ int single_at(int j) const { return lo + j < first ? lo + j : lo + j + n * kV; }
 };
 
-// Maximum or sum of a value over the cluster's workers, for the rows that take
+// Maximum or sum of a value over the cluster's threads, for the rows that take
 // the difference first.
 template <bool MAX>
 __device__ float cluster_all(float x, float* red, float* slots, int rank, int ranks) {
@@ -183,7 +188,8 @@ __device__ float cluster_all(float x, float* red, float* slots, int rank, int ra
     if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = x;
     __syncthreads();
     x = red[0];
-    for (int i = 1; i < kWorkerWarps; ++i) x = MAX ? fmaxf(x, red[i]) : x + red[i];
+    for (int i = 1; i < static_cast<int>(blockDim.x) / 32; ++i)
+        x = MAX ? fmaxf(x, red[i]) : x + red[i];
     if (static_cast<int>(threadIdx.x) < ranks)
         cluster.map_shared_rank(slots, threadIdx.x)[rank] = x;
     cluster.sync();
@@ -192,217 +198,362 @@ __device__ float cluster_all(float x, float* red, float* slots, int rank, int ra
     return x;
 }
 
-// One row's teacher entries in shared memory.
-struct Teacher {
-    float* p;        // probabilities
-    float* z;        // the student's logits there
-    int32_t* id;     // -1: absent
+// The teacher's entries of a row in shared memory: those in this CTA's slice.
+struct Entries {
+    int32_t* id;     // -1: absent, or in another CTA's slice
+    float* l2;       // l c; later w tau p
+    float* z;        // the student's logit there; later w tau q
 };
 
-// The teacher's warp: entries of a row, p, sum p log p and whether there is any.
-template <class T>
-__device__ void read_teacher(const DistillArgs& a, int64_t row, const Teacher& t, float* terms) {
-    const int lane = threadIdx.x % 32;
-    const T* z = static_cast<const T*>(a.logits) + row * a.logits_stride;
-    const int64_t t0 = row * a.top;
-    float best = -kInf;
-    for (int k = lane; k < a.top; k += 32) {
-        const int32_t id = a.ids[t0 + k];
-        const float raw = ld_param(a.teacher, a.teacher_f32, t0 + k);
-        const bool in = id >= 0 && id < a.vocab;
-        const float l = in ? raw * a.inv_tau : -kInf;
-        t.id[k] = in ? id : -1;
-        t.z[k] = in ? widen<T>(z[id]) : 0.0f;
-        t.p[k] = l;
-        best = fmaxf(best, l);
-    }
-    for (int k = a.top + lane; k < (a.top + 3) / 4 * 4; k += 32) t.id[k] = -1;
-    best = warp_max(best);
-    const float top = best == -kInf ? 0.0f : best;
-    float sum = 0.0f;
-    for (int k = lane; k < a.top; k += 32) sum += expf(t.p[k] - top);
-    sum = warp_sum(sum);
-    const float log_sum = logf(sum), inv = 1.0f / sum;
-    float acc = 0.0f;
-    for (int k = lane; k < a.top; k += 32) {
-        const float l = t.p[k] - top;
-        const float p = best == -kInf ? 0.0f : expf(l) * inv;
-        if (p != 0.0f) acc += p * (l - log_sum);
-        t.p[k] = p;
-    }
-    acc = warp_sum(acc);
-    if (lane == 0) {
-        terms[0] = acc;
-        terms[1] = best == -kInf ? 0.0f : 1.0f;
-    }
-    __syncwarp();
-}
+// An entry that a thread holds.
+struct Entry {
+    int32_t id;
+    float l, z;
+};
 
-// The gradient's entries k, k + step, ... that lie in [lo, hi): q - p, equal
-// ids added up in the order of the entries and written by the first of them.
-template <class T>
-__device__ __forceinline__ void patch(const DistillArgs& a, const Teacher& t, T* dz, int lo, int hi,
-                                      int k, int step, const Exponent& ex, float s, float w) {
-    for (; k < a.top; k += step) {
-        const int32_t id = t.id[k];
-        if (id < lo || id >= hi) continue;
-        float p = 0.0f;
-        bool earlier = false;
-        for (int j = 0; j < a.top; j += 4) {
-            const int4 v = *reinterpret_cast<const int4*>(t.id + j);
-            if (v.x != id && v.y != id && v.z != id && v.w != id) continue;
-            if (v.x == id) p += t.p[j];
-            if (v.y == id) p += t.p[j + 1];
-            if (v.z == id) p += t.p[j + 2];
-            if (v.w == id) p += t.p[j + 3];
-            const int at = v.x == id ? j : v.y == id ? j + 1 : v.z == id ? j + 2 : j + 3;
-            earlier |= at < k;
-        }
-        if (!earlier) dz[id] = narrow<T>(a.tau * w * (ex2(ex.log2q(t.z[k])) / s - p));
-    }
-}
-
-template <class T, bool GRAD>
-__global__ void __launch_bounds__(kRowThreads, 3)
+// WW warps of workers, which hold the slice, and EW of the teacher's entries.
+template <class T, bool GRAD, int WW, int EW>
+__global__ void __launch_bounds__(32 * (WW + EW), WW == kWorkerWarps ? 2 : 4)
 distill_kernel(const __grid_constant__ DistillArgs a) {
     using W = Word<T>;
     constexpr int kV = 16 / sizeof(T);
     constexpr int kP = W::kPairs;
-    extern __shared__ __align__(16) uint4 mem[];         // the slice, then two rows of entries
-    __shared__ Running sums[2][kMaxCluster * kWorkerWarps];   // written by the cluster's CTAs
-    __shared__ float far_red[kRowThreads / 32], far_max[kMaxCluster], far_sum[kMaxCluster];
-    __shared__ float terms[2][2];
+    constexpr int kWorkers = 32 * WW, kEntryThreads = 32 * EW;
+    extern __shared__ __align__(16) uint4 mem[];      // the slice, then kRing rows of entries
+    // written by the cluster's CTAs
+    __shared__ Running sums[2][kMaxCluster * WW], entry_sums[2][kMaxCluster * EW];
+    __shared__ float losses[kRing][kMaxCluster * EW];                       // of rank 0
+    __shared__ float far_red[WW + EW], far_slots[3][kMaxCluster];
+    __shared__ int64_t row_of[kRing];
+    __shared__ float weight_of[kRing];
+    __shared__ int equal[kRing];        // the last row (its number) there with equal ids
 
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = a.ranks, rank = static_cast<int>(cluster.block_rank());
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const bool worker = warp < kWorkerWarps;
+    const bool worker = warp < WW;
+    const int et = tid - kWorkers;                       // of the entries' threads
     const int64_t stride = gridDim.x / ranks;
     const int top4 = (a.top + 3) / 4 * 4;
-    auto teacher_of = [&](int parity) {
-        float* base = reinterpret_cast<float*>(mem + a.stage_words) + parity * 3 * top4;
-        return Teacher{base, base + top4, reinterpret_cast<int32_t*>(base + 2 * top4)};
-    };
-    const uint32_t my_mem = static_cast<uint32_t>(__cvta_generic_to_shared(mem)) + 16u * tid;
     const int section = a.section * kWorkers;            // words of a copy group
+    const uint32_t my_mem = static_cast<uint32_t>(__cvta_generic_to_shared(mem)) + 16u * tid;
 
-    // the copies of one group of a row, as one commit group
-    auto copy_section = [&](const Slice<T>& sl, int sec) {
-        const int end = sec == kSections - 1 ? sl.staged
-                                             : min(sl.staged, (sec + 1) * section);
-        for (int i = sec * section + tid; i < end; i += kWorkers)
-            cp_async16(my_mem + 16u * (i - tid), sl.word(i));
-        cp_async_commit();
+    auto entries_of = [&](int number) {
+        int32_t* base =
+            reinterpret_cast<int32_t*>(mem + a.stage_words) + (number % kRing) * 3 * top4;
+        return Entries{base, reinterpret_cast<float*>(base + top4),
+                       reinterpret_cast<float*>(base + 2 * top4)};
+    };
+    auto slice_of = [&](int64_t row) {
+        return Slice<T>(a, static_cast<const T*>(a.logits) + row * a.logits_stride, rank);
+    };
+    auto copy_row = [&](const Slice<T>& sl) {
+#pragma unroll
+        for (int sec = 0; sec < kSections; ++sec) {
+            const int end = sec == kSections - 1 ? sl.staged
+                                                 : min(sl.staged, (sec + 1) * section);
+            for (int i = sec * section + tid; i < end; i += kWorkers)
+                cp_async16(my_mem + 16u * (i - tid), sl.word(i));
+            cp_async_commit();
+        }
+    };
+    // Entry k of a row.
+    auto fetch_entry = [&](int64_t row, int k) {
+        const int64_t at = row * a.top + k;
+        return Entry{a.ids[at], ld_param(a.teacher, a.teacher_f32, at), 0.0f};
+    };
+    // the student's logit of an entry in this CTA's slice; others are absent
+    auto fetch_logit = [&](const Slice<T>& sl, Entry& e) {
+        if (e.id >= sl.lo && e.id < sl.hi) e.z = widen<T>(sl.z[e.id]);
+        else e.id = -1;
     };
 
-    int64_t row = blockIdx.x / ranks;
-    float w = a.weights != nullptr ? a.weights[row] : 1.0f;
-    Slice<T> sl(a, row, rank);
-    if (worker && w != 0.0f) {
-#pragma unroll
-        for (int sec = 0; sec < kSections; ++sec) copy_section(sl, sec);
-    }
-    if (!worker && w != 0.0f) read_teacher<T>(a, row, teacher_of(0), terms[0]);
-    if (ranks > 1) cluster.sync();       // every CTA runs: their memory may be written to
-
-    int parity = 0;           // of the row: the teacher's entries
-    int flip = 0;             // of the rows read: the exchanged sums
-    for (; row < a.n_rows; row += stride, parity ^= 1) {
-        const int64_t next_row = row + stride;
-        float next_w = 0.0f;
-        if (next_row < a.n_rows) next_w = a.weights != nullptr ? a.weights[next_row] : 1.0f;
-        const Teacher t = teacher_of(parity);
-        T* dz = GRAD ? static_cast<T*>(a.grad) + row * a.grad_stride : nullptr;
-        const bool read = w != 0.0f;
-        bool live = false;
-        Running r{-kFar, 0.0f};
-        if (read) {
-            if (worker) {
-                const Pair c2 = pair(a.c, a.c);
-                Pair s2 = 0;
-                auto add_word = [&](uint4 v) {
-                    const float t0 = ceilf(W::top(v) * a.c);
-                    const float off = fmaxf(r.off, fminf(t0, kFar));
-                    const float f = ex2(r.off - off);
-                    r.off = off;
-                    const Pair m2 = pair(-off, -off);
-                    s2 = mul2(s2, pair(f, f));
-                    Pair x[kP];
-                    W::split(v, x);
-#pragma unroll
-                    for (int j = 0; j < kP; ++j) s2 = add2(s2, ex2_fma2(x[j], c2, m2));
-                };
-                int i = tid;
-                cp_async_wait<2>();
-                for (const int end = min(sl.staged, section); i < end; i += kWorkers)
-                    add_word(mem[i]);
-                cp_async_wait<1>();
-                for (const int end = min(sl.staged, 2 * section); i < end; i += kWorkers)
-                    add_word(mem[i]);
-                cp_async_wait<0>();
-                for (; i < sl.staged; i += kWorkers) add_word(mem[i]);
-                for (; i < sl.n; i += kWorkers)
-                    add_word(*reinterpret_cast<const uint4*>(sl.word(i)));
-                const float2 s = unpair(s2);
-                r.s = s.x + s.y;
-                for (int j = tid; j < sl.singles(); j += kWorkers) {
-                    const float x = widen<T>(sl.z[sl.single_at(j)]);
-                    const float off = fmaxf(r.off, fminf(ceilf(x * a.c), kFar));
-                    r.s = r.s * ex2(r.off - off) + ex2(__fmaf_rn(x, a.c, -off));
-                    r.off = off;
-                }
-                r = warp_join(r);
-                Running* slot = sums[flip] + rank * kWorkerWarps + warp;
-                if (lane < ranks) *cluster.map_shared_rank(slot, lane) = r;
+    // The next row from `row` on that has a weight (n_rows or more: none); the
+    // rows before it get their zeros.
+    auto next_row = [&](int64_t row, float& w) {
+        for (; row < a.n_rows; row += stride) {
+            w = a.weights != nullptr ? a.weights[row] : 1.0f;
+            if (w != 0.0f) break;
+            if (rank == 0 && tid == 0) a.loss[row] = 0.0f;
+            if (GRAD && worker) {
+                T* dz = static_cast<T*>(a.grad) + row * a.grad_stride;
+                const Slice<T> sl(a, dz, rank);
+                const uint4 zero = make_uint4(0, 0, 0, 0);
+                for (int i = tid; i < sl.n; i += kWorkers)
+                    *reinterpret_cast<uint4*>(dz + sl.first + static_cast<int64_t>(i) * kV) = zero;
+                for (int j = tid; j < sl.singles(); j += kWorkers)
+                    dz[sl.single_at(j)] = narrow<T>(0.0f);
             }
-            if (ranks > 1) cluster.sync();
-            else __syncthreads();
-            r = {-kFar, 0.0f};
-            for (int i = lane; i < ranks * kWorkerWarps; i += 32) {
-                const Running o = sums[flip][i];
-                const float off = fmaxf(r.off, o.off);
-                r.s = r.s * ex2(r.off - off) + o.s * ex2(o.off - off);
-                r.off = off;
-            }
-            r = warp_join(r);
-            flip ^= 1;
-            live = terms[parity][1] != 0.0f;
-        } else {
-            __syncthreads();      // every row has one: entries are kept for two rows
         }
+        return row;
+    };
+
+    // The exponentials of the row held, this worker's part.
+    auto add_up = [&](const Slice<T>& sl) {
+        Running r{-kFar, 0.0f};
+        const Pair c2 = pair(a.c, a.c);
+        Pair s0 = 0, s1 = 0;
+        auto raise = [&](float top) {
+            const float t = top * a.c;
+            if (t > r.off) {
+                const float off = fminf(ceilf(t), kFar);
+                const float f = ex2(r.off - off);
+                r.off = off;
+                s0 = mul2(s0, pair(f, f));
+                s1 = mul2(s1, pair(f, f));
+            }
+        };
+        auto add_word = [&](uint4 v) {
+            raise(W::top(v));
+            const Pair m2 = pair(-r.off, -r.off);
+            Pair x[kP];
+            W::split(v, x);
+#pragma unroll
+            for (int j = 0; j < kP; j += 2) {
+                s0 = add2(s0, ex2_fma2(x[j], c2, m2));
+                s1 = add2(s1, ex2_fma2(x[j + 1], c2, m2));
+            }
+        };
+        auto add_words = [&](uint4 u, uint4 v) {
+            raise(fmaxf(W::top(u), W::top(v)));
+            const Pair m2 = pair(-r.off, -r.off);
+            Pair x[kP], y[kP];
+            W::split(u, x);
+            W::split(v, y);
+#pragma unroll
+            for (int j = 0; j < kP; ++j) {
+                s0 = add2(s0, ex2_fma2(x[j], c2, m2));
+                s1 = add2(s1, ex2_fma2(y[j], c2, m2));
+            }
+        };
+        int i = tid;
+        auto add_to = [&](int end) {
+            for (; i + kWorkers < end; i += 2 * kWorkers) add_words(mem[i], mem[i + kWorkers]);
+            if (i < end) {
+                add_word(mem[i]);
+                i += kWorkers;
+            }
+        };
+        cp_async_wait<2>();
+        add_to(min(sl.staged, section));
+        cp_async_wait<1>();
+        add_to(min(sl.staged, 2 * section));
+        cp_async_wait<0>();
+        add_to(sl.staged);
+        for (; i < sl.n; i += kWorkers) add_word(*reinterpret_cast<const uint4*>(sl.word(i)));
+        const float2 both = unpair(add2(s0, s1));
+        r.s = both.x + both.y;
+        for (int j = tid; j < sl.singles(); j += kWorkers) {
+            const float x = widen<T>(sl.z[sl.single_at(j)]);
+            r.raise(fminf(ceilf(x * a.c), kFar));
+            r.s += ex2(__fmaf_rn(x, a.c, -r.off));
+        }
+        return warp_join(r);
+    };
+
+    // A row's entries to shared memory, and their sum of this warp.
+    auto take_entries = [&](int64_t row, const Slice<T>& sl, const Entry& mine, int number) {
+        const Entries t = entries_of(number);
+        Running r{kNone, 0.0f};
+        for (int k = et; k < top4; k += kEntryThreads) {
+            Entry e = mine;
+            if (k >= kEntryThreads) {
+                e = k < a.top ? fetch_entry(row, k) : Entry{-1, 0.0f, 0.0f};
+                fetch_logit(sl, e);
+            }
+            if (k >= a.top || e.l == -kInf) e.id = -1;
+            const float l2 = e.l * a.c;
+            if (e.id >= 0) {
+                r.raise(fminf(fmaxf(ceilf(l2), -kFar), kFar));
+                r.s += ex2(l2 - r.off);
+            }
+            t.id[k] = e.id;
+            t.l2[k] = l2;
+            t.z[k] = e.z;
+        }
+        return warp_join(r);
+    };
+
+    // This warp's sum of row `number` to the CTAs of the cluster.
+    auto publish = [&](const Running& r, int number) {
+        if (lane < ranks) {
+            if (worker) cluster.map_shared_rank(sums[number & 1], lane)[rank * WW + warp] = r;
+            else cluster.map_shared_rank(entry_sums[number & 1], lane)[rank * EW + warp - WW] = r;
+        }
+    };
+    auto join_all = [&](const Running* from, int n, float none) {
+        Running r{none, 0.0f};
+        for (int j = lane; j < n; j += 32) {
+            const Running o = from[j];
+            r.raise(o.off);
+            r.s += o.s * ex2(o.off - r.off);
+        }
+        return warp_join(r);
+    };
+
+    // The entries' threads, after every plain value of row `number` is
+    // written: its entries of the gradient, and its loss.
+    auto finish = [&](int number) {
+        if (number < 0) return;
+        const int f = number % kRing;
+        const int64_t row = row_of[f];
+        if (GRAD) {
+            T* dz = static_cast<T*>(a.grad) + row * a.grad_stride;
+            const Entries t = entries_of(number);
+            const bool equal_ids = equal[f] == number;
+            for (int k = et; k < a.top; k += kEntryThreads) {
+                const int32_t id = t.id[k];
+                if (id < 0) continue;
+                float p = t.l2[k];
+                if (equal_ids) {
+                    // equal ids add up in the order of the entries; the first writes
+                    p = 0.0f;
+                    bool first = true;
+                    for (int j = 0; j < a.top; ++j) {
+                        if (t.id[j] != id) continue;
+                        first &= j >= k;
+                        p += t.l2[j];
+                    }
+                    if (!first) continue;
+                }
+                dz[id] = narrow<T>(t.z[k] - p);
+            }
+        }
+        if (rank == 0 && warp == WW) {
+            float loss = 0.0f;
+            for (int i = lane; i < ranks * EW; i += 32) loss += losses[f][i];
+            loss = warp_sum(loss);
+            if (lane == 0) a.loss[row] = weight_of[f] * a.tau2 * 0.69314718f * loss;
+        }
+    };
+
+    float w = 0.0f;
+    int64_t row = next_row(blockIdx.x / ranks, w);
+    if (row >= a.n_rows) return;                 // none with a weight: for all of the cluster
+    Slice<T> sl = slice_of(row);
+    Entry mine{-1, 0.0f, 0.0f};
+    if (worker) {
+        copy_row(sl);
+    } else if (et < a.top) {
+        mine = fetch_entry(row, et);
+        fetch_logit(sl, mine);
+    }
+    if (tid < kRing) equal[tid] = -1;
+    if (ranks > 1) cluster.sync();               // every CTA runs: their memory may be written to
+    auto barrier = [&] {
+        if (ranks > 1) cluster.sync();
+        else __syncthreads();
+    };
+
+    int number = 0;                              // of this row among the cluster's
+    for (;; ++number) {
+        const int buf = number & 1;
+        const Entries t = entries_of(number);
+        publish(worker ? add_up(sl) : take_entries(row, sl, mine, number), number);
+        barrier();
+        Running r = join_all(sums[buf], ranks * WW, -kFar);
         Exponent ex{a.c, r.off, !(fabsf(r.off) < kFar)};
+        Running rt{kNone, 0.0f};
+        bool live = false, far_entries = false;       // the row has an entry
+        for (int j = lane; j < ranks * EW; j += 32) {
+            const float off = entry_sums[buf][j].off;
+            live |= off != kNone;
+            far_entries |= off != kNone && !(fabsf(off) < kFar);
+        }
+        live = __any_sync(0xFFFFFFFFu, live);
+        far_entries = __any_sync(0xFFFFFFFFu, far_entries);
+        if (!worker) {
+            rt = join_all(entry_sums[buf], ranks * EW, kNone);
+            finish(number - 1);
+        }
         if (live && ex.far) {
-            float m = -kInf, s = 0.0f;
-            auto word_of = [&](int i) {
-                return i < sl.staged ? mem[i] : *reinterpret_cast<const uint4*>(sl.word(i));
+            float m = -kInf;
+            auto word_of = [&](int j) {
+                return j < sl.staged ? mem[j] : *reinterpret_cast<const uint4*>(sl.word(j));
             };
             if (worker) {
-                for (int i = tid; i < sl.n; i += kWorkers) m = fmaxf(m, W::top(word_of(i)));
+                for (int j = tid; j < sl.n; j += kWorkers) m = fmaxf(m, W::top(word_of(j)));
                 for (int j = tid; j < sl.singles(); j += kWorkers)
                     m = fmaxf(m, widen<T>(sl.z[sl.single_at(j)]));
             }
-            ex.off = cluster_all<true>(m, far_red, far_max, rank, ranks);
+            ex.off = cluster_all<true>(m, far_red, far_slots[0], rank, ranks);
+            float sum = 0.0f;
             if (worker) {
-                for (int i = tid; i < sl.n; i += kWorkers) {
+                for (int j = tid; j < sl.n; j += kWorkers) {
                     Pair x[kP];
-                    W::split(word_of(i), x);
+                    W::split(word_of(j), x);
 #pragma unroll
-                    for (int j = 0; j < kP; ++j) {
-                        const float2 v = unpair(x[j]);
-                        s += ex2(ex.log2q(v.x)) + ex2(ex.log2q(v.y));
+                    for (int p = 0; p < kP; ++p) {
+                        const float2 v = unpair(x[p]);
+                        sum += ex2(ex.log2q(v.x)) + ex2(ex.log2q(v.y));
                     }
                 }
                 for (int j = tid; j < sl.singles(); j += kWorkers)
-                    s += ex2(ex.log2q(widen<T>(sl.z[sl.single_at(j)])));
+                    sum += ex2(ex.log2q(widen<T>(sl.z[sl.single_at(j)])));
             }
-            r.s = cluster_all<false>(s, far_red, far_sum, rank, ranks);
+            r.s = cluster_all<false>(sum, far_red, far_slots[1], rank, ranks);
         }
-        const Slice<T> next(a, next_row < a.n_rows ? next_row : row, rank);
-        if (worker) {
-            const float f = live ? a.tau * w / r.s : 0.0f;
-            const bool copy = next_w != 0.0f;
-            // the slice's gradient from its copy, word by word; then the next
-            // row's copy into the word
+        if (far_entries) {
+            // an entry's l c is beyond kFar: differences of l itself
+            float m = -kInf;
+            auto l_of = [&](int k) { return ld_param(a.teacher, a.teacher_f32, row * a.top + k); };
+            if (!worker) {
+                for (int k = et; k < a.top; k += kEntryThreads) {
+                    if (t.id[k] >= 0) m = fmaxf(m, l_of(k));
+                }
+            }
+            m = cluster_all<true>(m, far_red, far_slots[2], rank, ranks);
+            float sum = 0.0f;
+            if (!worker) {
+                for (int k = et; k < a.top; k += kEntryThreads) {
+                    if (t.id[k] < 0) continue;
+                    t.l2[k] = (l_of(k) - m) * a.c;
+                    sum += ex2(t.l2[k]);
+                }
+            }
+            rt.off = 0.0f;
+            rt.s = cluster_all<false>(sum, far_red, far_slots[0], rank, ranks);
+        }
+        float next_w = 0.0f;
+        const int64_t next = next_row(row + stride, next_w);
+        const bool copy = next < a.n_rows;
+        const Slice<T> next_sl = slice_of(copy ? next : row);
+        const float f = live ? a.tau * w / r.s : 0.0f;
+        if (!worker) {
+            if (copy && et < a.top) mine = fetch_entry(next, et);
+            // the entries: w tau q and w tau p, and their part of the loss
+            if (et == 0) {
+                row_of[number % kRing] = row;
+                weight_of[number % kRing] = w;
+            }
+            float loss = 0.0f;
+            const float log_s = log2f(r.s), log_t = log2f(rt.s);
+            const float inv_t = 1.0f / rt.s, tau_w = a.tau * w;
+            for (int k = et; k < a.top; k += kEntryThreads) {
+                const int32_t id = t.id[k];
+                if (id < 0) continue;
+                const float l2 = t.l2[k] - rt.off, p = ex2(l2) * inv_t, lq = ex.log2q(t.z[k]);
+                if (p != 0.0f) loss += p * ((l2 - log_t) - (lq - log_s));
+                t.l2[k] = tau_w * p;
+                t.z[k] = ex2(lq) * f;
+                if (!GRAD) continue;
+                // is any other id the same?
+                bool found = false;
+                for (int j = 0; j < top4; j += 4) {
+                    const int4 v = *reinterpret_cast<const int4*>(t.id + j);
+                    found |= (v.x == id && j != k) || (v.y == id && j + 1 != k) ||
+                             (v.z == id && j + 2 != k) || (v.w == id && j + 3 != k);
+                }
+                if (found) equal[number % kRing] = number;
+            }
+            loss = warp_sum(loss);
+            if (lane == 0)
+                cluster.map_shared_rank(losses[number % kRing], 0)[rank * EW + warp - WW] = loss;
+            if (copy && et < a.top) fetch_logit(next_sl, mine);
+        } else {
+            // the slice's gradient from its copy, word by word, and the copy of
+            // the next row into the words used up
+            T* dz = GRAD ? static_cast<T*>(a.grad) + row * a.grad_stride : nullptr;
             auto write_words = [&](auto&& grad_word) {
                 T* out = dz + sl.first;
                 int i = tid;
@@ -410,17 +561,18 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
                 for (int sec = 0; sec < kSections; ++sec) {
                     const int limit = sec == kSections - 1 ? a.stage_words : (sec + 1) * section;
                     if (GRAD) {
+#pragma unroll 2
                         for (const int end = min(sl.staged, limit); i < end; i += kWorkers) {
                             *reinterpret_cast<uint4*>(out + static_cast<int64_t>(i) * kV) =
                                 grad_word(mem[i]);
-                            if (copy && i < next.staged)
-                                cp_async16(my_mem + 16u * (i - tid), next.word(i));
+                            if (copy && i < next_sl.staged)
+                                cp_async16(my_mem + 16u * (i - tid), next_sl.word(i));
                         }
                     }
                     if (copy) {
                         int j = GRAD ? i : sec * section + tid;
-                        for (const int end = min(next.staged, limit); j < end; j += kWorkers)
-                            cp_async16(my_mem + 16u * (j - tid), next.word(j));
+                        for (const int end = min(next_sl.staged, limit); j < end; j += kWorkers)
+                            cp_async16(my_mem + 16u * (j - tid), next_sl.word(j));
                         cp_async_commit();
                     }
                 }
@@ -458,21 +610,16 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
                 }
             } else {
                 // the gradient's rows lie otherwise on the 16-byte grid: single
-                // elements, which other threads have copied
-                asm volatile("bar.sync 2, %0;" ::"n"(kWorkers) : "memory");
-                const T* held = reinterpret_cast<const T*>(mem);
+                // elements, which other workers have copied
+                asm volatile("bar.sync 1, %0;" ::"n"(kWorkers) : "memory");
+                const T* elements = reinterpret_cast<const T*>(mem);
                 const int in_copy = sl.staged * kV;
                 for (int i = tid; i < sl.n * kV; i += kWorkers) {
-                    float y = 0.0f;
-                    if (live)
-                        y = ex2(ex.log2q(widen<T>(i < in_copy ? held[i] : sl.z[sl.first + i]))) * f;
-                    dz[sl.first + i] = narrow<T>(y);
+                    const float z = widen<T>(i < in_copy ? elements[i] : sl.z[sl.first + i]);
+                    dz[sl.first + i] = narrow<T>(live ? ex2(ex.log2q(z)) * f : 0.0f);
                 }
-                asm volatile("bar.sync 2, %0;" ::"n"(kWorkers) : "memory");
-                if (copy) {
-#pragma unroll
-                    for (int sec = 0; sec < kSections; ++sec) copy_section(next, sec);
-                }
+                asm volatile("bar.sync 1, %0;" ::"n"(kWorkers) : "memory");
+                if (copy) copy_row(next_sl);
             }
             if (GRAD) {
                 for (int j = tid; j < sl.singles(); j += kWorkers) {
@@ -480,52 +627,21 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
                     dz[i] = narrow<T>(live ? ex2(ex.log2q(widen<T>(sl.z[i]))) * f : 0.0f);
                 }
             }
-        } else {
-            if (rank == 0) {
-                float loss = 0.0f;
-                if (live) {
-                    // sum_k p_k (log p_k - ln 2 (log2 of the term k)) + log sum
-                    float acc = 0.0f;
-                    for (int k = lane; k < a.top; k += 32) {
-                        if (t.p[k] != 0.0f) acc += t.p[k] * ex.log2q(t.z[k]);
-                    }
-                    acc = warp_sum(acc);
-                    loss = w * a.tau2 * (terms[parity][0] - acc * 0.69314718f + logf(r.s));
-                }
-                if (lane == 0) a.loss[row] = loss;
-            }
-            if (next_w != 0.0f)
-                read_teacher<T>(a, next_row, teacher_of(parity ^ 1), terms[parity ^ 1]);
         }
-        if (GRAD && read) {
-            // the CTA's plain values are written: now the teacher's entries
-            const int lo = rank == 0 ? 0 : sl.first;
-            const int hi = rank == ranks - 1 ? static_cast<int>(a.vocab) : sl.first + sl.n * kV;
-            if (a.top <= kPatchAlone) {
-                if (worker) {
-                    __threadfence_block();
-                    asm volatile("bar.arrive 1, %0;" ::"n"(kRowThreads) : "memory");
-                } else {
-                    asm volatile("bar.sync 1, %0;" ::"n"(kRowThreads) : "memory");
-                    if (live) patch(a, t, dz, lo, hi, lane, 32, ex, r.s, w);
-                }
-            } else {
-                __syncthreads();
-                if (live) patch(a, t, dz, lo, hi, tid, kRowThreads, ex, r.s, w);
-            }
-        }
+        if (!copy) break;
+        row = next;
         w = next_w;
-        sl = next;
+        sl = next_sl;
     }
+    barrier();
+    if (!worker) finish(number);
 }
 
-// CTAs of a row: enough for its slices to fit three to an SM, and more where
-// rows are few, so that a row's read is spread over the GPU.
+// CTAs of a row: more than one only where rows are few, so that a row's read
+// is spread over the GPU.
 int ranks_for(int64_t rows, int64_t row_bytes) {
     int ranks = 1;
-    while (ranks < kMaxCluster &&
-           (row_bytes > static_cast<int64_t>(ranks) * kSliceBytes ||
-            (rows * ranks * 2 <= device_sms() && row_bytes > ranks * 8192)))
+    while (ranks < kMaxCluster && rows * ranks * 2 <= device_sms() && row_bytes > ranks * 8192)
         ranks *= 2;
     return ranks;
 }
@@ -552,7 +668,7 @@ struct Resident {
             }
         }
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kMostBytes + 24 * static_cast<int>(kMaxTeacher));
+                                             kMostBytes);
         if (e != cudaSuccess) return e;
         e = cudaOccupancyMaxActiveClusters(clusters, kernel, &cfg);
         if (e != cudaSuccess) return e;
@@ -563,23 +679,25 @@ struct Resident {
     }
 };
 
-template <class T, bool GRAD>
-cudaError_t launch(DistillArgs a, cudaStream_t stream) {
+template <class T, bool GRAD, int WW, int EW>
+cudaError_t launch_shape(DistillArgs a, cudaStream_t stream) {
     static Resident resident;
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
-    const auto kernel = distill_kernel<T, GRAD>;
+    const auto kernel = distill_kernel<T, GRAD, WW, EW>;
     const int64_t row_bytes = a.vocab * static_cast<int64_t>(sizeof(T));
-    a.ranks = ranks_for(a.n_rows, row_bytes);
+    a.rank_shift = 0;
+    while ((1 << a.rank_shift) < a.ranks) ++a.rank_shift;
     const int64_t slice = (row_bytes / 16 + a.ranks - 1) / a.ranks;
-    a.stage_words = static_cast<int32_t>(slice < kMostBytes / 16 ? slice : kMostBytes / 16);
-    const int per_thread = (a.stage_words + kWorkers - 1) / kWorkers;
+    const int64_t entries = (static_cast<int64_t>(a.top) + 3) / 4 * 4 * 12 * kRing;
+    const int64_t room = (kMostBytes - entries) / 16;
+    a.stage_words = static_cast<int32_t>(slice < room ? slice : room);
+    const int per_thread = (a.stage_words + 32 * WW - 1) / (32 * WW);
     a.section = (per_thread + kSections - 1) / kSections;
-    const size_t top4 = (static_cast<size_t>(a.top) + 3) / 4 * 4;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(a.ranks));
-    cfg.blockDim = dim3(kRowThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(a.stage_words) * 16 + 24 * top4;
+    cfg.blockDim = dim3(32 * (WW + EW));
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.stage_words * 16 + entries);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -596,6 +714,16 @@ cudaError_t launch(DistillArgs a, cudaStream_t stream) {
     const int64_t n = a.n_rows < clusters ? a.n_rows : clusters;
     cfg.gridDim = dim3(static_cast<unsigned>(n * a.ranks));
     return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+// Rows of up to kSmallRow take small CTAs, several to an SM: a row is soon
+// done, and what it costs besides its words overlaps with other rows'.
+template <class T, bool GRAD>
+cudaError_t launch(DistillArgs a, cudaStream_t stream) {
+    const int64_t row_bytes = a.vocab * static_cast<int64_t>(sizeof(T));
+    a.ranks = ranks_for(a.n_rows, row_bytes);
+    if (row_bytes <= kSmallRow) return launch_shape<T, GRAD, 6, 2>(a, stream);
+    return launch_shape<T, GRAD, kWorkerWarps, kEntryWarps>(a, stream);
 }
 
 }  // namespace
