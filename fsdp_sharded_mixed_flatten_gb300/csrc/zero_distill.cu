@@ -56,8 +56,23 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Copies and stores carry an L2 policy: where a row does not fit shared memory,
+// what is not read again leaves L2 first, so that the words that are stay.
+__device__ __forceinline__ uint64_t l2_policy(bool first_out) {
+    uint64_t p;
+    if (first_out) asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    else asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst),
+                 "l"(src), "l"(policy)
+                 : "memory");
+}
+__device__ __forceinline__ void store16(void* dst, uint4 v, uint64_t policy) {
+    asm volatile("st.global.L2::cache_hint.v4.b32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(dst), "r"(v.x),
+                 "r"(v.y), "r"(v.z), "r"(v.w), "l"(policy)
+                 : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -236,6 +251,8 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
     const int64_t stride = gridDim.x / ranks;
     const int top4 = (a.top + 3) / 4 * 4;
     const int section = a.section * kWorkers;            // words of a copy group
+    const uint64_t policy = l2_policy(static_cast<int64_t>(a.stage_words) * ranks * 16 <
+                                      a.vocab * static_cast<int64_t>(sizeof(T)) - 32 * ranks);
     const uint32_t my_mem = static_cast<uint32_t>(__cvta_generic_to_shared(mem)) + 16u * tid;
 
     auto entries_of = [&](int number) {
@@ -253,7 +270,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
             const int end = sec == kSections - 1 ? sl.staged
                                                  : min(sl.staged, (sec + 1) * section);
             for (int i = sec * section + tid; i < end; i += kWorkers)
-                cp_async16(my_mem + 16u * (i - tid), sl.word(i));
+                cp_async16(my_mem + 16u * (i - tid), sl.word(i), policy);
             cp_async_commit();
         }
     };
@@ -327,11 +344,14 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
             }
         };
         int i = tid;
+        const uint4* at = mem + tid;
         auto add_to = [&](int end) {
-            for (; i + kWorkers < end; i += 2 * kWorkers) add_words(mem[i], mem[i + kWorkers]);
+            for (; i + kWorkers < end; i += 2 * kWorkers, at += 2 * kWorkers)
+                add_words(at[0], at[kWorkers]);
             if (i < end) {
-                add_word(mem[i]);
+                add_word(*at);
                 i += kWorkers;
+                at += kWorkers;
             }
         };
         cp_async_wait<2>();
@@ -340,7 +360,17 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
         add_to(min(sl.staged, 2 * section));
         cp_async_wait<0>();
         add_to(sl.staged);
-        for (; i < sl.n; i += kWorkers) add_word(*reinterpret_cast<const uint4*>(sl.word(i)));
+        if (i < sl.n) {
+            // words beyond shared memory, four loads under way
+            const uint4* far = reinterpret_cast<const uint4*>(sl.word(i));
+            for (; i + 3 * kWorkers < sl.n; i += 4 * kWorkers, far += 4 * kWorkers) {
+                const uint4 v0 = far[0], v1 = far[kWorkers], v2 = far[2 * kWorkers],
+                            v3 = far[3 * kWorkers];
+                add_words(v0, v1);
+                add_words(v2, v3);
+            }
+            for (; i < sl.n; i += kWorkers, far += kWorkers) add_word(*far);
+        }
         const float2 both = unpair(add2(s0, s1));
         r.s = both.x + both.y;
         for (int j = tid; j < sl.singles(); j += kWorkers) {
@@ -555,31 +585,54 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
             // the next row into the words used up
             T* dz = GRAD ? static_cast<T*>(a.grad) + row * a.grad_stride : nullptr;
             auto write_words = [&](auto&& grad_word) {
-                T* out = dz + sl.first;
+                uint4* out = reinterpret_cast<uint4*>(dz + sl.first) + tid;
+                const uint4* from = reinterpret_cast<const uint4*>(next_sl.word(0)) + tid;
+                const uint4* at = mem + tid;
+                uint32_t to = my_mem;
                 int i = tid;
+                const int n_copy = copy ? next_sl.staged : 0;
 #pragma unroll
                 for (int sec = 0; sec < kSections; ++sec) {
                     const int limit = sec == kSections - 1 ? a.stage_words : (sec + 1) * section;
-                    if (GRAD) {
-#pragma unroll 2
-                        for (const int end = min(sl.staged, limit); i < end; i += kWorkers) {
-                            *reinterpret_cast<uint4*>(out + static_cast<int64_t>(i) * kV) =
-                                grad_word(mem[i]);
-                            if (copy && i < next_sl.staged)
-                                cp_async16(my_mem + 16u * (i - tid), next_sl.word(i));
-                        }
+                    const int end = GRAD ? min(sl.staged, limit) : 0;
+                    for (; i + kWorkers < min(end, n_copy); i += 2 * kWorkers) {
+                        const uint4 v0 = at[0], v1 = at[kWorkers];
+                        store16(out, grad_word(v0), policy);
+                        store16(out + kWorkers, grad_word(v1), policy);
+                        cp_async16(to, from, policy);
+                        cp_async16(to + 16 * kWorkers, from + kWorkers, policy);
+                        at += 2 * kWorkers;
+                        out += 2 * kWorkers;
+                        from += 2 * kWorkers;
+                        to += 32 * kWorkers;
                     }
-                    if (copy) {
-                        int j = GRAD ? i : sec * section + tid;
-                        for (const int end = min(next_sl.staged, limit); j < end; j += kWorkers)
-                            cp_async16(my_mem + 16u * (j - tid), next_sl.word(j));
-                        cp_async_commit();
+                    for (; i < max(end, min(n_copy, limit)); i += kWorkers) {
+                        if (i < end) store16(out, grad_word(*at), policy);
+                        if (i < n_copy) cp_async16(to, from, policy);
+                        at += kWorkers;
+                        out += kWorkers;
+                        from += kWorkers;
+                        to += 16 * kWorkers;
                     }
+                    if (copy) cp_async_commit();
                 }
-                if (GRAD) {
-                    for (; i < sl.n; i += kWorkers)
-                        *reinterpret_cast<uint4*>(out + static_cast<int64_t>(i) * kV) =
-                            grad_word(*reinterpret_cast<const uint4*>(sl.word(i)));
+                if (GRAD && sl.staged < sl.n) {
+                    // a shared word beyond the slice's own may have been passed
+                    i = (sl.staged - tid + kWorkers - 1) / kWorkers * kWorkers + tid;
+                    out = reinterpret_cast<uint4*>(dz + sl.first) + i;
+                    const uint4* far = reinterpret_cast<const uint4*>(sl.word(i));
+                    for (; i + 3 * kWorkers < sl.n; i += 4 * kWorkers) {
+                        const uint4 v0 = far[0], v1 = far[kWorkers], v2 = far[2 * kWorkers],
+                                    v3 = far[3 * kWorkers];
+                        store16(out, grad_word(v0), policy);
+                        store16(out + kWorkers, grad_word(v1), policy);
+                        store16(out + 2 * kWorkers, grad_word(v2), policy);
+                        store16(out + 3 * kWorkers, grad_word(v3), policy);
+                        far += 4 * kWorkers;
+                        out += 4 * kWorkers;
+                    }
+                    for (; i < sl.n; i += kWorkers, far += kWorkers, out += kWorkers)
+                        store16(out, grad_word(*far), policy);
                 }
             };
             const bool same_grid = !GRAD || ((reinterpret_cast<uintptr_t>(sl.z) ^
