@@ -17,6 +17,8 @@
 
 #include <cooperative_groups.h>
 
+#include <mutex>
+
 namespace cg = cooperative_groups;
 
 namespace zf {
@@ -294,6 +296,10 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
 
     const int live = __popc(__ballot_sync(0xFFFFFFFFu, my_key != none));   // a prefix
 
+    auto column = [&](int j) -> int64_t {       // of a load: in the row
+        const int64_t c = col0 + (j * 32 + lane) * VEC;
+        return c < a.dim ? c : 0;
+    };
     float acc[kPer];
     auto clear = [&] {
 #pragma unroll
@@ -338,18 +344,22 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
         if (seen != static_cast<uint32_t>(last_chunk - first_chunk)) return;
         __threadfence();
         clear();
-        for (int64_t q = first_chunk; q <= last_chunk; ++q) {
-            // the run starts in its first chunk's second slot, unless the
-            // chunk's first place starts it; later chunks use the first slot
-            const int slot = q == first_chunk ? 1 : 0;
-            const float* p = ws.partial + (q * 2 + slot) * a.dim;
+        for (int64_t q = first_chunk; q <= last_chunk; q += 4) {
+            float v[4][kPer];
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
+            for (int u = 0; u < 4; ++u) {
+                // the run starts in its first chunk's second slot; later chunks
+                // use the first
+                const int64_t at = q + u <= last_chunk ? q + u : last_chunk;
+                const float* p = ws.partial + (at * 2 + (at == first_chunk ? 1 : 0)) * a.dim;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const int64_t c = col0 + (j * 32 + lane) * VEC + e;
-                    if (c < a.dim) acc[j * VEC + e] += __ldcg(p + c);
-                }
+                for (int e = 0; e < kPer; ++e) v[u][e] = __ldcg(p + column(e / VEC) + e % VEC);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (q + u > last_chunk) break;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) acc[e] += v[u][e];
             }
         }
         write_row(k);
@@ -380,15 +390,12 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
         Pack<Y, VEC> v[kAhead][N];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int32_t t = __shfl_sync(0xFFFFFFFFu, my_tok, (i0 + u) & 31);
-            if (i0 + u < live) {
-                const Y* row = static_cast<const Y*>(a.grad_out) + t * a.grad_stride;
+            // without conditions, so that all are under way: past the end the
+            // last place again, beyond the row its first column
+            const int32_t t = __shfl_sync(0xFFFFFFFFu, my_tok, i0 + u < live ? i0 + u : live - 1);
+            const Y* row = static_cast<const Y*>(a.grad_out) + t * a.grad_stride;
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const int64_t c = col0 + (j * 32 + lane) * VEC;
-                    if (c < a.dim) v[u][j] = ld_pack<Y, VEC>(row + c);
-                }
-            }
+            for (int j = 0; j < N; ++j) v[u][j] = ld_pack<Y, VEC>(row + column(j));
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
@@ -398,11 +405,8 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
             const int32_t after = __shfl_sync(0xFFFFFFFFu, my_key, (i + 1) & 31);
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const int64_t c = col0 + (j * 32 + lane) * VEC;
-                if (c < a.dim) {
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) acc[j * VEC + e] += widen<Y>(v[u][j].x[e]);
-                }
+                for (int e = 0; e < VEC; ++e) acc[j * VEC + e] += widen<Y>(v[u][j].x[e]);
             }
             if (i + 1 < n && after == k) continue;
             // the run ends here, or goes on in the next chunk
@@ -420,6 +424,346 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
             begin = i + 1;
         }
     }
+}
+
+// ------------------------------------------------------------- buckets ------
+//
+// For up to kBucketTokens tokens one launch does it all.  A CTA owns the rows
+// of a bucket (1 of B: the low bits of the id, mixed with a hash of the high
+// ones) and 256 columns (128 with fp32).  It reads all ids, keeps its own tokens in order,
+// counts them by row, groups them (a row's tokens stay in order), and its
+// warps add up equal parts of the grouped tokens; runs over several parts are
+// joined from shared memory in order.  Where every row is written, the rows
+// without a token get their zeros on the way.
+
+constexpr int kBucketThreads = 512;
+constexpr int kBucketWarps = kBucketThreads / 32;
+constexpr int kTokenBits = 14;
+constexpr int64_t kBucketTokens = 1 << kTokenBits;
+constexpr int kBucketSmem = 160 * 1024;              // beside 33 KB of static memory
+
+struct Bucket {
+    int bits;            // B = 1 << bits
+    int64_t rows;        // of a bucket, at most: ceil(vocab / B)
+    int64_t smem;        // list, order, row starts (the partial rows are static)
+};
+
+// Tokens of a warp: whole groups of 32.
+__host__ __device__ inline int bucket_share(int64_t n_tokens) {
+    return static_cast<int>((n_tokens + kBucketWarps * 32 - 1) / (kBucketWarps * 32) * 32);
+}
+
+__host__ __device__ inline uint32_t bucket_mix(uint32_t high, int bits) {
+    return bits == 0 ? 0u : (high * 2654435761u) >> (32 - bits);
+}
+
+// Columns of a CTA: 16 bytes a lane of the wider type.
+__host__ __device__ constexpr int bucket_cols(int widest) { return 512 / widest; }
+
+Bucket bucket_for(int64_t n_tokens, int64_t vocab, int64_t dim, int widest) {
+    const int64_t most = 2 * device_sms() / ((dim + bucket_cols(widest) - 1) / bucket_cols(widest));
+    Bucket b{0, vocab, 0};
+    while ((int64_t{2} << b.bits) <= most || b.rows > 8192) {
+        if (b.bits == 16) break;
+        ++b.bits;
+        b.rows = ((vocab - 1) >> b.bits) + 1;
+    }
+    b.smem = kBucketWarps * bucket_share(n_tokens) * 6 + up16((b.rows + 1) * 4);
+    return b;
+}
+
+// Whether a gradient takes the one launch: the list of a bucket could hold all
+// tokens.  Measured against the sort: 8192 x 768 tokens into 50257 rows, added
+// to the table: 33 us with the sort.
+bool takes_buckets(int64_t n_tokens, int64_t vocab, int64_t dim) {
+    if (n_tokens > kBucketTokens) return false;
+    const Bucket b = bucket_for(n_tokens, vocab, dim, 4);
+    return b.rows < (1 << (32 - kTokenBits)) && b.smem <= kBucketSmem &&
+           dim <= 65535 * int64_t{bucket_cols(4)};
+}
+
+template <class Y, class G, int VEC, bool ACC>
+__global__ void __launch_bounds__(kBucketThreads, 2)
+embed_bucket_kernel(const __grid_constant__ EmbedGradArgs a, int bits, int n_rows) {
+    constexpr int kPer = bucket_cols(sizeof(Y) > sizeof(G) ? sizeof(Y) : sizeof(G)) / 32;
+    constexpr int kWidth = 32 * kPer;
+    constexpr int N = kPer / VEC;
+    constexpr int kAhead = VEC == 1 && kPer == 8 ? 2 : ACC ? 4 : 8;
+    constexpr uint32_t kTokenMask = (1u << kTokenBits) - 1;
+    extern __shared__ __align__(16) char smem[];
+    __shared__ float partial[kBucketWarps][2][256];      // before: the rows with several tokens
+    __shared__ int warp_n[kBucketWarps], through[kBucketWarps];
+    __shared__ uint32_t warp_sums[kBucketWarps];
+    __shared__ int n_several;
+    const int T = static_cast<int>(a.n_tokens);
+    const int share = bucket_share(T);                   // of a warp: its tokens and list
+    uint32_t* list = reinterpret_cast<uint32_t*>(smem);  // row << 14 | token, by warp
+    uint16_t* order = reinterpret_cast<uint16_t*>(list + kBucketWarps * share);
+    uint32_t* start = reinterpret_cast<uint32_t*>(order + kBucketWarps * share);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t bucket = blockIdx.x;
+    const uint32_t low = (1u << bits) - 1u;
+    const int64_t col0 = static_cast<int64_t>(blockIdx.y) * kWidth;
+
+    for (int i = tid; i <= n_rows; i += kBucketThreads) start[i] = 0;
+    if (tid == 0) n_several = 0;
+    __syncthreads();
+
+    // this bucket's tokens among the warp's, in order, and their rows' counts
+    const int t0 = warp * share;
+    int mine = 0;
+    for (int it = 0; it * 32 < share; it += 8) {
+        // loads without conditions (at a clamped place), so that all are under way
+        int64_t id[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int t = t0 + (it + u) * 32 + lane;
+            id[u] = ld_id(a.ids, a.id64, t < T ? t : T - 1);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int t = t0 + (it + u) * 32 + lane;
+            const uint32_t high = static_cast<uint32_t>(id[u]) >> bits;
+            const bool in = t < T && t < t0 + share && id[u] >= 0 && id[u] < a.vocab &&
+                            ((static_cast<uint32_t>(id[u]) & low) ^ bucket_mix(high, bits)) == bucket;
+            const uint32_t m = __ballot_sync(0xFFFFFFFFu, in);
+            if (in) {
+                list[t0 + mine + __popc(m & ((1u << lane) - 1u))] =
+                    high << kTokenBits | static_cast<uint32_t>(t);
+                atomicAdd(&start[high], 1u);
+            }
+            mine += __popc(m);
+        }
+    }
+    if (lane == 0) warp_n[warp] = mine;
+    __syncthreads();
+
+    // rows' counts to first places; the rows with several tokens
+    const int rows_per = (n_rows + kBucketThreads) / kBucketThreads;     // n_rows + 1 of them
+    const int r0 = tid * rows_per < n_rows + 1 ? tid * rows_per : n_rows + 1;
+    const int r1 = r0 + rows_per < n_rows + 1 ? r0 + rows_per : n_rows + 1;
+    uint32_t sum = 0;
+    for (int r = r0; r < r1; ++r) sum += start[r];
+    uint32_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sums[warp] = incl;
+    __syncthreads();
+    uint32_t first = incl - sum;
+    for (int w = 0; w < warp; ++w) first += warp_sums[w];
+    uint32_t* several = reinterpret_cast<uint32_t*>(&partial[0][0][0]);
+    for (int r = r0; r < r1; ++r) {
+        const uint32_t c = start[r];
+        start[r] = first;
+        first += c;
+        if (c > 1) several[atomicAdd(&n_several, 1)] = static_cast<uint32_t>(r);
+    }
+    __syncthreads();
+    const int n = static_cast<int>(start[n_rows]);
+
+    auto row_at = [&](uint32_t r) -> G* {       // row r of the bucket in the table
+        const int64_t id = (static_cast<int64_t>(r) << bits) | (bucket ^ bucket_mix(r, bits));
+        return static_cast<G*>(a.grad_weight) + id * a.dim;
+    };
+    // zeros to the rows of [lo, hi) without a token
+    auto fill = [&](int lo, int hi) {
+        float zero[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) zero[e] = 0.0f;
+        const Pack<G, VEC> z = pack<G, VEC>(zero);
+        for (int r = lo + warp; r < hi; r += kBucketWarps) {
+            if (start[r] != start[r + 1]) continue;
+            const int64_t id = (static_cast<int64_t>(r) << bits) |
+                               (bucket ^ bucket_mix(static_cast<uint32_t>(r), bits));
+            if (id >= a.vocab) continue;
+            G* row = static_cast<G*>(a.grad_weight) + id * a.dim;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int64_t c = col0 + (j * 32 + lane) * VEC;
+                if (c < a.dim) st_pack<G, VEC>(row + c, z);
+            }
+        }
+    };
+    // half of the zeros now, half while the first loads are under way
+    if (!ACC) fill(0, n_rows / 2);
+
+    // the tokens grouped by row: single ones by themselves, a row with several
+    // by a warp that walks the lists
+    for (int i = lane; i < mine; i += 32) {
+        const uint32_t r = list[t0 + i] >> kTokenBits;
+        if (start[r + 1] - start[r] == 1) order[start[r]] = static_cast<uint16_t>(t0 + i);
+    }
+    for (int k = warp; k < n_several; k += kBucketWarps) {
+        const uint32_t r = several[k];
+        uint32_t to = start[r];
+        const uint32_t end = start[r + 1];
+        for (int w = 0; w < kBucketWarps && to < end; ++w) {
+            for (int i0 = 0; i0 < warp_n[w]; i0 += 32) {
+                const int i = i0 + lane;
+                const bool same = i < warp_n[w] && list[w * share + i] >> kTokenBits == r;
+                const uint32_t m = __ballot_sync(0xFFFFFFFFu, same);
+                if (same)
+                    order[to + __popc(m & ((1u << lane) - 1u))] = static_cast<uint16_t>(w * share + i);
+                to += __popc(m);
+            }
+        }
+    }
+    __syncthreads();
+
+    // equal parts of the grouped tokens, one a warp
+    const int per = (n + kBucketWarps - 1) / kBucketWarps;
+    const int p0 = warp * per < n ? warp * per : n;
+    const int p1 = p0 + per < n ? p0 + per : n;
+    auto entry = [&](int p) { return list[order[p]]; };
+    float acc[kPer];
+    auto clear = [&] {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = 0.0f;
+    };
+    auto column = [&](int j) -> int64_t {       // of a load: in the row
+        const int64_t c = col0 + (j * 32 + lane) * VEC;
+        return c < a.dim ? c : 0;
+    };
+    auto load_row = [&](Pack<G, VEC> (&old)[N], const G* row) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) old[j] = ld_pack<G, VEC>(row + column(j));
+    };
+    auto write_row = [&](G* row, const Pack<G, VEC> (&old)[N]) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int64_t c = col0 + (j * 32 + lane) * VEC;
+            if (c >= a.dim) continue;
+            float y[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                y[e] = acc[j * VEC + e] * a.scale;
+                if (ACC) y[e] += widen<G>(old[j].x[e]);
+            }
+            st_pack<G, VEC>(row + c, pack<G, VEC>(y));
+        }
+    };
+    int passes = 0, leaves = -1;                // the run goes through the part; leaves it
+    bool filled = ACC;
+    clear();
+    if (p0 < p1) {
+        const int before = p0 > 0 ? static_cast<int>(entry(p0 - 1) >> kTokenBits) : -1;
+        int begin = p0;                          // of the current run in the part
+        for (int q = p0; q < p1; q += 32) {
+            const uint32_t my = entry(q + lane < p1 ? q + lane : p1 - 1);
+            // places at which a run is over
+            const uint32_t over = __ballot_sync(
+                0xFFFFFFFFu, q + lane < p1 && start[(my >> kTokenBits) + 1] == q + lane + 1u);
+            for (int u0 = 0; u0 < 32 && q + u0 < p1; u0 += kAhead) {
+                Pack<Y, VEC> v[kAhead][N];
+                Pack<G, VEC> old[ACC ? kAhead : 1][N];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    // without conditions: past the end the last place again,
+                    // beyond the row its first column
+                    const uint32_t e = __shfl_sync(0xFFFFFFFFu, my, u0 + u);
+                    const Y* row = static_cast<const Y*>(a.grad_out) +
+                                   static_cast<int64_t>(e & kTokenMask) * a.grad_stride;
+#pragma unroll
+                    for (int j = 0; j < N; ++j) v[u][j] = ld_pack<Y, VEC>(row + column(j));
+                }
+                if (ACC && ((over >> u0) & ((1u << kAhead) - 1u)) != 0) {
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u) {
+                        const uint32_t e = __shfl_sync(0xFFFFFFFFu, my, u0 + u);
+                        load_row(old[ACC ? u : 0], row_at(e >> kTokenBits));
+                    }
+                }
+                if (!filled) {
+                    fill(n_rows / 2, n_rows);
+                    filled = true;
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int p = q + u0 + u;
+                    if (p >= p1) break;
+                    const uint32_t r = __shfl_sync(0xFFFFFFFFu, my, u0 + u) >> kTokenBits;
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) acc[j * VEC + e] += widen<Y>(v[u][j].x[e]);
+                    }
+                    const bool ends = (over >> (u0 + u)) & 1u;
+                    if (!ends && p + 1 < p1) continue;
+                    const bool enters = begin == p0 && before == static_cast<int>(r);
+                    if (ends && !enters) {
+                        write_row(row_at(r), old[ACC ? u : 0]);
+                    } else {
+                        float* to = partial[warp][enters ? 0 : 1];
+#pragma unroll
+                        for (int e = 0; e < kPer; ++e) to[(e / VEC * 32 + lane) * VEC + e % VEC] = acc[e];
+                        if (!ends) {
+                            if (enters) passes = 1;
+                            else leaves = static_cast<int>(r);
+                        }
+                    }
+                    clear();
+                    begin = p + 1;
+                }
+            }
+        }
+    }
+    if (!filled) fill(n_rows / 2, n_rows);
+    if (lane == 0) through[warp] = passes;
+    __syncthreads();
+    // the run that leaves this part for the next ones: joined in order
+    if (leaves >= 0) {
+        G* row = row_at(static_cast<uint32_t>(leaves));
+        Pack<G, VEC> old[N];
+        if (ACC) load_row(old, row);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+            acc[e] = partial[warp][1][(e / VEC * 32 + lane) * VEC + e % VEC];
+        for (int w = warp + 1; w < kBucketWarps; ++w) {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+                acc[e] += partial[w][0][(e / VEC * 32 + lane) * VEC + e % VEC];
+            if (!through[w]) break;
+        }
+        write_row(row, old);
+    }
+}
+
+template <class Y, class G, int VEC, bool ACC>
+cudaError_t embed_buckets_as(const EmbedGradArgs& a, cudaStream_t stream) {
+    constexpr int kWidth = bucket_cols(sizeof(Y) > sizeof(G) ? sizeof(Y) : sizeof(G));
+    const Bucket b = bucket_for(a.n_tokens, a.vocab, a.dim, 512 / kWidth);
+    const dim3 grid(1u << b.bits, static_cast<unsigned>((a.dim + kWidth - 1) / kWidth));
+    const auto kernel = embed_bucket_kernel<Y, G, VEC, ACC>;
+    // more than 48 KB of shared memory need asking for
+    static std::once_flag once[64];
+    static cudaError_t set[64];
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::call_once(once[dev], [&] {
+        set[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        kBucketSmem);
+    });
+    if (set[dev] != cudaSuccess) return set[dev];
+    kernel<<<grid, kBucketThreads, static_cast<size_t>(b.smem), stream>>>(
+        a, b.bits, static_cast<int>(b.rows));
+    return cudaGetLastError();
+}
+
+template <class Y, class G>
+cudaError_t embed_buckets(const EmbedGradArgs& a, cudaStream_t stream) {
+    constexpr int kV = sizeof(Y) == 2 && sizeof(G) == 2 ? 8 : 4;
+    const bool vec = aligned_to(a.grad_out, kV * static_cast<int64_t>(sizeof(Y))) &&
+                     aligned_to(a.grad_weight, kV * static_cast<int64_t>(sizeof(G))) &&
+                     a.dim % kV == 0 && a.grad_stride % kV == 0;
+    if (a.accumulate)
+        return vec ? embed_buckets_as<Y, G, kV, true>(a, stream)
+                   : embed_buckets_as<Y, G, 1, true>(a, stream);
+    return vec ? embed_buckets_as<Y, G, kV, false>(a, stream)
+               : embed_buckets_as<Y, G, 1, false>(a, stream);
 }
 
 template <class W, class Y>
@@ -467,8 +811,21 @@ cudaError_t launch_embed(const EmbedArgs& a, int weight_bytes, int out_bytes,
                           : embed<float, float>(a, 4, stream);
 }
 
-int64_t embed_grad_workspace(int64_t n_tokens, int64_t dim) {
-    return workspace(nullptr, n_tokens, dim).bytes;
+int64_t embed_grad_workspace(int64_t n_tokens, int64_t vocab, int64_t dim) {
+    return embed_grad_in_one(n_tokens, vocab, dim) ? 0 : workspace(nullptr, n_tokens, dim).bytes;
+}
+
+bool embed_grad_in_one(int64_t n_tokens, int64_t vocab, int64_t dim) {
+    return takes_buckets(n_tokens, vocab, dim);
+}
+
+cudaError_t launch_embed_buckets(const EmbedGradArgs& a, int grad_bytes, int grad_weight_bytes,
+                                 cudaStream_t stream) {
+    if (grad_bytes == 2)
+        return grad_weight_bytes == 2 ? embed_buckets<uint16_t, uint16_t>(a, stream)
+                                      : embed_buckets<uint16_t, float>(a, stream);
+    return grad_weight_bytes == 2 ? embed_buckets<float, uint16_t>(a, stream)
+                                  : embed_buckets<float, float>(a, stream);
 }
 
 cudaError_t launch_embed_sort(const EmbedGradArgs& a, int grad_weight_bytes, cudaStream_t stream) {

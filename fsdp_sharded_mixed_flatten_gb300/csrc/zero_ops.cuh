@@ -163,7 +163,11 @@ struct EmbedGradArgs {
     void* workspace;
 };
 
-int64_t embed_grad_workspace(int64_t n_tokens, int64_t dim);
+int64_t embed_grad_workspace(int64_t n_tokens, int64_t vocab, int64_t dim);
+// One launch (few tokens), or a sort launch and a sum launch over a workspace.
+bool embed_grad_in_one(int64_t n_tokens, int64_t vocab, int64_t dim);
+cudaError_t launch_embed_buckets(const EmbedGradArgs& a, int grad_bytes, int grad_weight_bytes,
+                                 cudaStream_t stream);
 cudaError_t launch_embed_sort(const EmbedGradArgs& a, int grad_weight_bytes, cudaStream_t stream);
 cudaError_t launch_embed_sum(const EmbedGradArgs& a, int grad_bytes, int grad_weight_bytes,
                              cudaStream_t stream);

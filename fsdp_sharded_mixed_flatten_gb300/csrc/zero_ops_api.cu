@@ -200,7 +200,7 @@ ZERO_API int zero_embedding_grad_workspace_bytes(int64_t n_tokens, int64_t vocab
                                                  int64_t* bytes) {
     if (bytes == nullptr) return fail(ZERO_ERR_INVALID_ARG, "bytes is NULL");
     if (int rc = check_table(n_tokens, vocab, dim, 1.0)) return rc;
-    *bytes = zf::embed_grad_workspace(n_tokens, dim);
+    *bytes = zf::embed_grad_workspace(n_tokens, vocab, dim);
     return ok();
 }
 
@@ -221,7 +221,7 @@ ZERO_API int zero_embedding_grad(const void* ids, int32_t id_bytes, int64_t n_to
     if (accumulate != 0 && accumulate != 1)
         return fail(ZERO_ERR_INVALID_ARG, "accumulate = %d (0 or 1)", accumulate);
     if (int rc = check_workspace(workspace, workspace_bytes,
-                                 zf::embed_grad_workspace(n_tokens, dim)))
+                                 zf::embed_grad_workspace(n_tokens, vocab, dim)))
         return rc;
     if (n_tokens == 0 && accumulate) return ok();
     zf::EmbedGradArgs a{};
@@ -237,6 +237,10 @@ ZERO_API int zero_embedding_grad(const void* ids, int32_t id_bytes, int64_t n_to
     a.scale = static_cast<float>(scale);
     a.workspace = workspace;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (zf::embed_grad_in_one(n_tokens, vocab, dim))
+        return cuda_call("embedding gradient launch", [&] {
+            return zf::launch_embed_buckets(a, grad_out_bytes, grad_weight_bytes, s);
+        });
     if (int rc = cuda_call("embedding gradient sort launch",
                            [&] { return zf::launch_embed_sort(a, grad_weight_bytes, s); }))
         return rc;

@@ -63,6 +63,8 @@ TABLES = [
     # tokens, vocab, dim, pad columns, flat offset
     (1, 1, 1, 0, 0), (1, 50257, 768, 0, 0), (7, 5, 3, 1, 1), (33, 11, 257, 0, 3),
     (129, 4096, 520, 8, 8), (1000, 300, 64, 0, 0), (2049, 1000, 770, 2, 5), (4096, 50257, 256, 0, 0),
+    # beyond the bucket launch's tokens: sorted
+    (16385, 1000, 40, 0, 0), (20011, 50257, 73, 1, 3), (33000, 7, 264, 0, 0),
 ]
 
 
@@ -156,6 +158,24 @@ def test_embedding_grad_repeats_bit_for_bit(n):
             ref, bound = R.embedding_grad(ids, dy, (200, 264), 1.0)
             R.check(dw, ref, bound, "grad_weight")
         assert torch.equal(_bits(dw), _bits(first))
+
+
+@pytest.mark.parametrize("label", ["embedding gradient sort", "embedding gradient sum"])
+def test_embedding_grad_failure_and_retry(monkeypatch, label):
+    ids = torch.randint(0, 500, (18000,), generator=_gen("retry")).cuda()
+    dy = torch.randn((18000, 48), generator=_gen("retry-dy")).cuda()
+    nbytes = zf.zero_embedding_grad_workspace_bytes(18000, 500, 48)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    dw = [torch.zeros((500, 48), device="cuda") for _ in range(2)]
+    zf.zero_embedding_grad(ids, dy, dw[0], 1.0, True, ws, nbytes)
+    monkeypatch.setenv("ZERO_INJECT_FAILURE", label)
+    with pytest.raises(zf.ZeroError) as ei:
+        zf.zero_embedding_grad(ids, dy, dw[1], 1.0, True, ws, nbytes)
+    assert ei.value.code == -4 and label in str(ei.value)
+    assert not dw[1].any()
+    monkeypatch.delenv("ZERO_INJECT_FAILURE")
+    zf.zero_embedding_grad(ids, dy, dw[1], 1.0, True, ws, nbytes)
+    assert torch.equal(dw[0], dw[1])
 
 
 def test_embedding_of_no_tokens():
@@ -547,8 +567,8 @@ def test_capture_into_a_graph():
         assert torch.equal(_bits(a), _bits(b))
 
 
-@pytest.mark.parametrize("label", ["embedding gradient sort", "embedding gradient sum",
-                                   "layer norm gradient launch", "layer norm gradient reduction",
+@pytest.mark.parametrize("label", ["embedding gradient launch", "layer norm gradient launch",
+                                   "layer norm gradient reduction",
                                    "distillation loss and gradient"])
 def test_injected_failure_is_reported_and_a_retry_is_clean(monkeypatch, label):
     ref_call, ref = _mixed_calls()
