@@ -227,9 +227,18 @@ __device__ void fill_unused(const EmbedGradArgs& a, int64_t lo, int64_t hi, uint
         __syncthreads();
         for (int i = tid; i < (n + 31) / 32; i += kSortThreads) used[i] = 0;
         __syncthreads();
-        for (int64_t t = tid; t < a.n_tokens; t += kSortThreads) {
-            const int64_t v = ld_id(a.ids, a.id64, t) - r0;
-            if (v >= 0 && v < n) atomicOr(&used[v >> 5], 1u << (v & 31));
+        for (int64_t t = tid; t < a.n_tokens; t += 8 * kSortThreads) {
+            // loads without conditions, so that all are under way
+            int64_t v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int64_t at = t + u * kSortThreads;
+                v[u] = ld_id(a.ids, a.id64, at < a.n_tokens ? at : a.n_tokens - 1) - r0;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (v[u] >= 0 && v[u] < n) atomicOr(&used[v[u] >> 5], 1u << (v[u] & 31));
+            }
         }
         __syncthreads();
         float zero[VEC];
@@ -269,11 +278,12 @@ static_assert(sizeof(SortSmem) >= kFillRows / 8, "the bitmap shares the sort's m
 // ----------------------------------------------------------------- sum ------
 
 // Lane columns: N groups of VEC, group n at (32 n + lane) VEC.
-template <class Y, class G, int VEC>
-__global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ EmbedGradArgs a) {
+template <class Y, class G, int VEC, bool ACC>
+__global__ void __launch_bounds__(256, VEC == 1 ? 2 : 3)
+embed_sum_kernel(const __grid_constant__ EmbedGradArgs a) {
     constexpr int kPer = kCols / 32;
     constexpr int N = kPer / VEC;
-    constexpr int kAhead = 8;
+    constexpr int kAhead = ACC || sizeof(Y) == 4 || VEC == 1 ? 4 : 8;
     const int lane = threadIdx.x & 31;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32;
     const int64_t groups = groups_of(a.dim), n_chunks = chunks_of(a.n_tokens);
@@ -305,7 +315,12 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
 #pragma unroll
         for (int e = 0; e < kPer; ++e) acc[e] = 0.0f;
     };
-    auto write_row = [&](int32_t k) {
+    auto load_row = [&](Pack<G, VEC> (&old)[N], int32_t k) {
+        const G* row = static_cast<const G*>(a.grad_weight) + static_cast<int64_t>(k) * a.dim;
+#pragma unroll
+        for (int j = 0; j < N; ++j) old[j] = ld_pack<G, VEC>(row + column(j));
+    };
+    auto write_row = [&](int32_t k, const Pack<G, VEC> (&old)[N]) {
         G* row = static_cast<G*>(a.grad_weight) + static_cast<int64_t>(k) * a.dim;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
@@ -313,11 +328,9 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
             if (c >= a.dim) continue;
             float y[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) y[e] = acc[j * VEC + e] * a.scale;
-            if (a.accumulate) {
-                const Pack<G, VEC> old = ld_pack<G, VEC>(row + c);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) y[e] += widen<G>(old.x[e]);
+            for (int e = 0; e < VEC; ++e) {
+                y[e] = acc[j * VEC + e] * a.scale;
+                if (ACC) y[e] += widen<G>(old[j].x[e]);
             }
             st_pack<G, VEC>(row + c, pack<G, VEC>(y));
         }
@@ -362,7 +375,9 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
                 for (int e = 0; e < kPer; ++e) acc[e] += v[u][e];
             }
         }
-        write_row(k);
+        Pack<G, VEC> old[N];
+        if (ACC) load_row(old, k);
+        write_row(k, old);
     };
     // The chunk in which the run of k that enters this chunk starts.
     auto run_start = [&](int32_t k) -> int64_t {
@@ -386,6 +401,10 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
 
     clear();
     int begin = 0;                                  // first place of the current run
+    // places at which a run is over, or leaves the chunk
+    const int32_t key_next = __shfl_down_sync(0xFFFFFFFFu, my_key, 1);
+    const uint32_t over =
+        __ballot_sync(0xFFFFFFFFu, lane < live && (lane + 1 == n || key_next != my_key));
     for (int i0 = 0; i0 < live; i0 += kAhead) {
         Pack<Y, VEC> v[kAhead][N];
 #pragma unroll
@@ -397,23 +416,29 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
 #pragma unroll
             for (int j = 0; j < N; ++j) v[u][j] = ld_pack<Y, VEC>(row + column(j));
         }
+        Pack<G, VEC> old[ACC ? kAhead : 1][N];
+        if (ACC && ((over >> i0) & ((1u << kAhead) - 1u)) != 0) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                load_row(old[ACC ? u : 0],
+                         __shfl_sync(0xFFFFFFFFu, my_key, i0 + u < live ? i0 + u : live - 1));
+        }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int i = i0 + u;
             if (i >= live) break;
-            const int32_t k = __shfl_sync(0xFFFFFFFFu, my_key, i);
-            const int32_t after = __shfl_sync(0xFFFFFFFFu, my_key, (i + 1) & 31);
 #pragma unroll
             for (int j = 0; j < N; ++j) {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) acc[j * VEC + e] += widen<Y>(v[u][j].x[e]);
             }
-            if (i + 1 < n && after == k) continue;
+            if (!((over >> i) & 1u)) continue;
+            const int32_t k = __shfl_sync(0xFFFFFFFFu, my_key, i);
             // the run ends here, or goes on in the next chunk
             const bool enters = begin == 0 && key_before == k;
             const bool leaves = i + 1 == n && key_after == k;
             if (!enters && !leaves) {
-                write_row(k);
+                write_row(k, old[ACC ? u : 0]);
             } else {
                 put_partial(enters ? 0 : 1);
                 const int64_t from = enters ? run_start(k) : chunk;
@@ -792,10 +817,12 @@ cudaError_t embed_sum(const EmbedGradArgs& a, cudaStream_t stream) {
                      a.dim % kV == 0 && a.grad_stride % kV == 0;
     const int64_t warps = chunks_of(a.n_tokens) * groups_of(a.dim);
     const unsigned g = static_cast<unsigned>((warps + 7) / 8);
-    if (vec) {
-        embed_sum_kernel<Y, G, kV><<<g, 256, 0, stream>>>(a);
+    if (a.accumulate) {
+        if (vec) embed_sum_kernel<Y, G, kV, true><<<g, 256, 0, stream>>>(a);
+        else embed_sum_kernel<Y, G, 1, true><<<g, 256, 0, stream>>>(a);
     } else {
-        embed_sum_kernel<Y, G, 1><<<g, 256, 0, stream>>>(a);
+        if (vec) embed_sum_kernel<Y, G, kV, false><<<g, 256, 0, stream>>>(a);
+        else embed_sum_kernel<Y, G, 1, false><<<g, 256, 0, stream>>>(a);
     }
     return cudaGetLastError();
 }
