@@ -7,12 +7,15 @@
 // equal ids:
 //   sort launch: one cluster of 8 CTAs runs a radix sort of (id, token), 2 to
 //     4 passes of at most 9 bits; the other clusters write zeros to the rows
-//     of dW that no token has.
+//     that no token has.
 //   sum launch: a warp takes kChunk sorted places and 256 columns.  A run
 //     inside the chunk is added up and written; a run over several chunks
 //     leaves one partial row per chunk in the workspace, and the chunk that
 //     finishes last adds the partials in chunk order.  No order depends on
 //     timing, so neither does any result.
+// Zeros alone take memory to 4.7 TB/s at most (4.0 in torch's fill).  Writing
+// them from CTAs of the sum launch, beside its reads, was slower: 65536 tokens
+// of 4096 columns into 131072 rows took 408 us instead of 325.
 #include "zero_ops.cuh"
 
 #include <cooperative_groups.h>
@@ -147,8 +150,18 @@ __device__ void sort_cluster(const EmbedGradArgs& a, const Workspace& ws, SortSm
         };
         if (tid < kDigits) hist[tid] = 0;
         __syncthreads();
-        for (int64_t i = lo + tid; i < hi; i += kSortThreads)
-            atomicAdd(&hist[(key_at(i) >> shift) & mask], 1u);
+        for (int64_t i = lo + tid; i < hi; i += 8 * kSortThreads) {
+            uint32_t key[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int64_t at = i + u * kSortThreads;
+                key[u] = key_at(at < hi ? at : hi - 1);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (i + u * kSortThreads < hi) atomicAdd(&hist[(key[u] >> shift) & mask], 1u);
+            }
+        }
         cluster.sync();
         // first place of each digit for this CTA: all smaller digits, then
         // the same digit in the CTAs before it
@@ -173,18 +186,22 @@ __device__ void sort_cluster(const EmbedGradArgs& a, const Workspace& ws, SortSm
             for (int w = 0; w < warp; ++w) s += sm.scan[w];
             sm.base[tid] = s;
         }
+        auto load = [&](int64_t i, uint32_t& key, int32_t& tok) {
+            const int64_t at = i < hi ? i : hi - 1;
+            key = key_at(at);
+            tok = pass > 0 ? src_tok[at] : static_cast<int32_t>(at);
+        };
+        uint32_t next_key = 0;
+        int32_t next_tok = 0;
+        if (lo < hi) load(lo + tid, next_key, next_tok);
         for (int64_t tile = lo; tile < hi; tile += kSortThreads) {
-            const int64_t i = tile + tid;
-            const bool in = i < hi;
-            for (int d = lane; d < kDigits; d += 32) sm.warp[warp][d] = 0;
+            const bool in = tile + tid < hi;
+            const uint32_t key = next_key, digit = (key >> shift) & mask;
+            const int32_t tok = next_tok;
+            if (tile + kSortThreads < hi) load(tile + kSortThreads + tid, next_key, next_tok);
+            for (int d = lane; d < kDigits / 2; d += 32)
+                reinterpret_cast<uint32_t*>(sm.warp[warp])[d] = 0;
             __syncwarp();
-            uint32_t key = 0, digit = 0;
-            int32_t tok = 0;
-            if (in) {
-                key = key_at(i);
-                tok = pass > 0 ? src_tok[i] : static_cast<int32_t>(i);
-                digit = (key >> shift) & mask;
-            }
             // the lanes with the same digit, and this lane's place among them
             uint32_t peers = __ballot_sync(0xFFFFFFFFu, in);
             if (!in) peers = ~peers;
@@ -196,11 +213,14 @@ __device__ void sort_cluster(const EmbedGradArgs& a, const Workspace& ws, SortSm
             if (in && below == 0) sm.warp[warp][digit] = static_cast<uint16_t>(__popc(peers));
             __syncthreads();
             if (tid < kDigits) {
+                uint32_t c[kSortWarps];
+#pragma unroll
+                for (int w = 0; w < kSortWarps; ++w) c[w] = sm.warp[w][tid];
                 uint32_t s = 0;
+#pragma unroll
                 for (int w = 0; w < kSortWarps; ++w) {
-                    const uint32_t n = sm.warp[w][tid];
                     sm.warp[w][tid] = static_cast<uint16_t>(s);
-                    s += n;
+                    s += c[w];
                 }
                 incl = s;      // the tile's count of this digit
             }
@@ -224,8 +244,9 @@ __device__ void fill_unused(const EmbedGradArgs& a, int64_t lo, int64_t hi, uint
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int64_t r0 = lo; r0 < hi; r0 += kFillRows) {
         const int64_t n = hi - r0 < kFillRows ? hi - r0 : kFillRows;
+        const int words = static_cast<int>((n + 31) / 32);
         __syncthreads();
-        for (int i = tid; i < (n + 31) / 32; i += kSortThreads) used[i] = 0;
+        for (int i = tid; i < words; i += kSortThreads) used[i] = 0;
         __syncthreads();
         for (int64_t t = tid; t < a.n_tokens; t += 8 * kSortThreads) {
             // loads without conditions, so that all are under way
@@ -277,176 +298,207 @@ static_assert(sizeof(SortSmem) >= kFillRows / 8, "the bitmap shares the sort's m
 
 // ----------------------------------------------------------------- sum ------
 
-// Lane columns: N groups of VEC, group n at (32 n + lane) VEC.
+// Pairs of a pack's values in fp32.
+template <class T, int VEC>
+__device__ __forceinline__ Pair pair_of(const Pack<T, VEC>& p, int i) {
+    if constexpr (sizeof(T) == 2) return widen2(reinterpret_cast<const uint32_t*>(&p)[i]);
+    else return pair(p.x[2 * i], p.x[2 * i + 1]);
+}
+
+// acc += the N packs of a row.
+template <class T, int VEC, int N, int PER>
+__device__ __forceinline__ void add_row(Pair (&acc)[PER / 2], const Pack<T, VEC> (&v)[N]) {
+    if constexpr (VEC == 1) {
+#pragma unroll
+        for (int i = 0; i < PER / 2; ++i)
+            acc[i] = add2(acc[i], pair(widen<T>(v[2 * i].x[0]), widen<T>(v[2 * i + 1].x[0])));
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER / 2; ++i)
+            acc[i] = add2(acc[i], pair_of(v[2 * i / VEC], i % (VEC / 2)));
+    }
+}
+
+// What the sort leaves to the sum launch.
+struct Sorted {
+    const int32_t* key;
+    const int32_t* tok;
+    uint32_t* done;
+    float* partial;
+    int32_t groups;       // of columns
+};
+
+// A warp: a chunk (block z) and a group of columns (block y).  Lane columns: N
+// groups of VEC, group n at (32 n + lane) VEC.
 template <class Y, class G, int VEC, bool ACC>
 __global__ void __launch_bounds__(256, VEC == 1 ? 2 : 3)
-embed_sum_kernel(const __grid_constant__ EmbedGradArgs a) {
+embed_sum_kernel(const __grid_constant__ EmbedGradArgs a, const __grid_constant__ Sorted s) {
     constexpr int kPer = kCols / 32;
     constexpr int N = kPer / VEC;
     constexpr int kAhead = ACC || sizeof(Y) == 4 || VEC == 1 ? 4 : 8;
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32;
-    const int64_t groups = groups_of(a.dim), n_chunks = chunks_of(a.n_tokens);
-    const int64_t chunk = unit / groups, group = unit - chunk * groups;
-    if (chunk >= n_chunks) return;
-    const Workspace ws = workspace(a.workspace, a.n_tokens, a.dim);
-    const bool odd = sort_plan(a.vocab).passes % 2 != 0;      // the last pass's buffer
-    const int32_t* key = odd ? ws.key[0] : ws.key[1];
-    const int32_t* tok = odd ? ws.tok[0] : ws.tok[1];
-    const int64_t col0 = group * kCols;
-    const int64_t first = chunk * kChunk;
-    const int n = static_cast<int>(a.n_tokens - first < kChunk ? a.n_tokens - first : kChunk);
+    const int lane = threadIdx.x;
+    const int chunk = blockIdx.x * blockDim.z + threadIdx.z;
+    const int group = blockIdx.y * blockDim.y + threadIdx.y;
+    const int T = static_cast<int>(a.n_tokens);
+    const int64_t col0 = static_cast<int64_t>(group) * kCols;
+    const int first = chunk * kChunk;
+    if (first >= T || col0 >= a.dim) return;
     const int32_t none = static_cast<int32_t>(a.vocab);
-
+    const int n = T - first < kChunk ? T - first : kChunk;
     // this lane's place of the chunk, and the neighbours' keys
-    const int32_t my_key = lane < n ? key[first + lane] : none;
-    const int32_t my_tok = lane < n ? tok[first + lane] : 0;
-    const int32_t key_before = first > 0 ? key[first - 1] : -1;
-    const int32_t key_after = first + n < a.n_tokens ? key[first + n] : -1;
-
+    const int at = first + (lane < n ? lane : n - 1);
+    const int32_t place_key = s.key[at], my_tok = s.tok[at];
+    const int32_t key_before = first > 0 ? s.key[first - 1] : -1;
+    const int32_t key_after = first + n < T ? s.key[first + n] : -1;
+    const int32_t my_key = lane < n ? place_key : none;
     const int live = __popc(__ballot_sync(0xFFFFFFFFu, my_key != none));   // a prefix
-
-    auto column = [&](int j) -> int64_t {       // of a load: in the row
-        const int64_t c = col0 + (j * 32 + lane) * VEC;
-        return c < a.dim ? c : 0;
-    };
-    float acc[kPer];
-    auto clear = [&] {
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = 0.0f;
-    };
-    auto load_row = [&](Pack<G, VEC> (&old)[N], int32_t k) {
-        const G* row = static_cast<const G*>(a.grad_weight) + static_cast<int64_t>(k) * a.dim;
-#pragma unroll
-        for (int j = 0; j < N; ++j) old[j] = ld_pack<G, VEC>(row + column(j));
-    };
-    auto write_row = [&](int32_t k, const Pack<G, VEC> (&old)[N]) {
-        G* row = static_cast<G*>(a.grad_weight) + static_cast<int64_t>(k) * a.dim;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
+    {
+        auto column = [&](int j) -> int64_t {       // of a load: in the row
             const int64_t c = col0 + (j * 32 + lane) * VEC;
-            if (c >= a.dim) continue;
-            float y[VEC];
+            return c < a.dim ? c : 0;
+        };
+        Pair acc[kPer / 2];
+        auto clear = [&] {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                y[e] = acc[j * VEC + e] * a.scale;
-                if (ACC) y[e] += widen<G>(old[j].x[e]);
+            for (int i = 0; i < kPer / 2; ++i) acc[i] = 0;
+        };
+        auto load_row = [&](Pack<G, VEC> (&old)[N], int32_t k) {
+            const G* row = static_cast<const G*>(a.grad_weight) + static_cast<int64_t>(k) * a.dim;
+#pragma unroll
+            for (int j = 0; j < N; ++j) old[j] = ld_pack<G, VEC>(row + column(j));
+        };
+        auto write_row = [&](int32_t k, const Pack<G, VEC> (&old)[N]) {
+            G* row = static_cast<G*>(a.grad_weight) + static_cast<int64_t>(k) * a.dim;
+            float sum[kPer];
+#pragma unroll
+            for (int i = 0; i < kPer / 2; ++i) {
+                const float2 f = unpair(acc[i]);
+                sum[2 * i] = f.x * a.scale;
+                sum[2 * i + 1] = f.y * a.scale;
             }
-            st_pack<G, VEC>(row + c, pack<G, VEC>(y));
-        }
-    };
-    auto put_partial = [&](int slot) {
-        float* p = ws.partial + (chunk * 2 + slot) * a.dim;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const int64_t c = col0 + (j * 32 + lane) * VEC + e;
-                if (c < a.dim) __stcg(p + c, acc[j * VEC + e]);
-            }
-        }
-    };
-    // A run of key k over several chunks, `first_chunk` .. `last_chunk`, of
-    // which this one has left its partial: the last to come adds them up.
-    auto join = [&](int32_t k, int64_t first_chunk, int64_t last_chunk) {
-        __threadfence();
-        __syncwarp();
-        uint32_t seen = 0;
-        if (lane == 0) seen = atomicAdd(&ws.done[first_chunk * groups + group], 1u);
-        seen = __shfl_sync(0xFFFFFFFFu, seen, 0);
-        if (seen != static_cast<uint32_t>(last_chunk - first_chunk)) return;
-        __threadfence();
-        clear();
-        for (int64_t q = first_chunk; q <= last_chunk; q += 4) {
-            float v[4][kPer];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                // the run starts in its first chunk's second slot; later chunks
-                // use the first
-                const int64_t at = q + u <= last_chunk ? q + u : last_chunk;
-                const float* p = ws.partial + (at * 2 + (at == first_chunk ? 1 : 0)) * a.dim;
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) v[u][e] = __ldcg(p + column(e / VEC) + e % VEC);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (q + u > last_chunk) break;
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) acc[e] += v[u][e];
-            }
-        }
-        Pack<G, VEC> old[N];
-        if (ACC) load_row(old, k);
-        write_row(k, old);
-    };
-    // The chunk in which the run of k that enters this chunk starts.
-    auto run_start = [&](int32_t k) -> int64_t {
-        for (int64_t q = chunk - 1;; q -= 32) {
-            // chunk q - lane: does the run enter it from the one before?
-            const int64_t c = q - lane;
-            const bool goes_on = c > 0 && key[c * kChunk - 1] == k;
-            const uint32_t stop = __ballot_sync(0xFFFFFFFFu, !goes_on);
-            if (stop != 0) return q - (__ffs(stop) - 1);
-        }
-    };
-    // The chunk in which the run of k that leaves this chunk ends.
-    auto run_end = [&](int32_t k) -> int64_t {
-        for (int64_t q = chunk + 1;; q += 32) {
-            const int64_t c = q + lane, next = (c + 1) * kChunk;
-            const bool goes_on = next < a.n_tokens && key[next] == k;
-            const uint32_t stop = __ballot_sync(0xFFFFFFFFu, !goes_on);
-            if (stop != 0) return q + (__ffs(stop) - 1);
-        }
-    };
-
-    clear();
-    int begin = 0;                                  // first place of the current run
-    // places at which a run is over, or leaves the chunk
-    const int32_t key_next = __shfl_down_sync(0xFFFFFFFFu, my_key, 1);
-    const uint32_t over =
-        __ballot_sync(0xFFFFFFFFu, lane < live && (lane + 1 == n || key_next != my_key));
-    for (int i0 = 0; i0 < live; i0 += kAhead) {
-        Pack<Y, VEC> v[kAhead][N];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            // without conditions, so that all are under way: past the end the
-            // last place again, beyond the row its first column
-            const int32_t t = __shfl_sync(0xFFFFFFFFu, my_tok, i0 + u < live ? i0 + u : live - 1);
-            const Y* row = static_cast<const Y*>(a.grad_out) + t * a.grad_stride;
-#pragma unroll
-            for (int j = 0; j < N; ++j) v[u][j] = ld_pack<Y, VEC>(row + column(j));
-        }
-        Pack<G, VEC> old[ACC ? kAhead : 1][N];
-        if (ACC && ((over >> i0) & ((1u << kAhead) - 1u)) != 0) {
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-                load_row(old[ACC ? u : 0],
-                         __shfl_sync(0xFFFFFFFFu, my_key, i0 + u < live ? i0 + u : live - 1));
-        }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int i = i0 + u;
-            if (i >= live) break;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
+                const int64_t c = col0 + (j * 32 + lane) * VEC;
+                if (c >= a.dim) continue;
+                float y[VEC];
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) acc[j * VEC + e] += widen<Y>(v[u][j].x[e]);
+                for (int e = 0; e < VEC; ++e) {
+                    y[e] = sum[j * VEC + e];
+                    if (ACC) y[e] += widen<G>(old[j].x[e]);
+                }
+                st_pack<G, VEC>(row + c, pack<G, VEC>(y));
             }
-            if (!((over >> i) & 1u)) continue;
-            const int32_t k = __shfl_sync(0xFFFFFFFFu, my_key, i);
-            // the run ends here, or goes on in the next chunk
-            const bool enters = begin == 0 && key_before == k;
-            const bool leaves = i + 1 == n && key_after == k;
-            if (!enters && !leaves) {
-                write_row(k, old[ACC ? u : 0]);
-            } else {
-                put_partial(enters ? 0 : 1);
-                const int64_t from = enters ? run_start(k) : chunk;
-                const int64_t to = leaves ? run_end(k) : chunk;
-                join(k, from, to);
+        };
+        auto put_partial = [&](int slot) {
+            float* p = s.partial + (static_cast<int64_t>(chunk) * 2 + slot) * a.dim;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                const int64_t c = col0 + (e / VEC * 32 + lane) * VEC + e % VEC;
+                const float2 f = unpair(acc[e / 2]);
+                if (c < a.dim) __stcg(p + c, e % 2 == 0 ? f.x : f.y);
             }
+        };
+        // A run of key k over several chunks, `first_chunk` .. `last_chunk`, of
+        // which this one has left its partial: the last to come adds them up.
+        auto join = [&](int32_t k, int first_chunk, int last_chunk) {
+            __threadfence();
+            __syncwarp();
+            uint32_t seen = 0;
+            if (lane == 0) seen = atomicAdd(&s.done[static_cast<int64_t>(first_chunk) * s.groups + group], 1u);
+            seen = __shfl_sync(0xFFFFFFFFu, seen, 0);
+            if (seen != static_cast<uint32_t>(last_chunk - first_chunk)) return;
+            __threadfence();
             clear();
-            begin = i + 1;
+            for (int q = first_chunk; q <= last_chunk; q += 4) {
+                float v[4][kPer];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    // the run starts in its first chunk's second slot; later chunks
+                    // use the first
+                    const int at = q + u <= last_chunk ? q + u : last_chunk;
+                    const float* p =
+                        s.partial + (static_cast<int64_t>(at) * 2 + (at == first_chunk ? 1 : 0)) * a.dim;
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) v[u][e] = __ldcg(p + column(e / VEC) + e % VEC);
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (q + u > last_chunk) break;
+#pragma unroll
+                    for (int i = 0; i < kPer / 2; ++i)
+                        acc[i] = add2(acc[i], pair(v[u][2 * i], v[u][2 * i + 1]));
+                }
+            }
+            Pack<G, VEC> old[N];
+            if (ACC) load_row(old, k);
+            write_row(k, old);
+        };
+        // The chunk in which the run of k that enters this chunk starts.
+        auto run_start = [&](int32_t k) -> int {
+            for (int q = chunk - 1;; q -= 32) {
+                // chunk q - lane: does the run enter it from the one before?
+                const int c = q - lane;
+                const bool goes_on = c > 0 && s.key[c * kChunk - 1] == k;
+                const uint32_t stop = __ballot_sync(0xFFFFFFFFu, !goes_on);
+                if (stop != 0) return q - (__ffs(stop) - 1);
+            }
+        };
+        // The chunk in which the run of k that leaves this chunk ends.
+        auto run_end = [&](int32_t k) -> int {
+            for (int q = chunk + 1;; q += 32) {
+                const int64_t next = (static_cast<int64_t>(q) + lane + 1) * kChunk;
+                const bool goes_on = next < T && s.key[next] == k;
+                const uint32_t stop = __ballot_sync(0xFFFFFFFFu, !goes_on);
+                if (stop != 0) return q + (__ffs(stop) - 1);
+            }
+        };
+
+        clear();
+        int begin = 0;                                  // first place of the current run
+        // places at which a run is over, or leaves the chunk
+        const int32_t key_next = __shfl_down_sync(0xFFFFFFFFu, my_key, 1);
+        const uint32_t over =
+            __ballot_sync(0xFFFFFFFFu, lane < live && (lane + 1 == n || key_next != my_key));
+        for (int i0 = 0; i0 < live; i0 += kAhead) {
+            Pack<Y, VEC> v[kAhead][N];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                // without conditions, so that all are under way: past the end the
+                // last place again, beyond the row its first column
+                const int32_t t =
+                    __shfl_sync(0xFFFFFFFFu, my_tok, i0 + u < live ? i0 + u : live - 1);
+                const Y* row = static_cast<const Y*>(a.grad_out) + t * a.grad_stride;
+#pragma unroll
+                for (int j = 0; j < N; ++j) v[u][j] = ld_pack<Y, VEC>(row + column(j));
+            }
+            Pack<G, VEC> old[ACC ? kAhead : 1][N];
+            if (ACC && ((over >> i0) & ((1u << kAhead) - 1u)) != 0) {
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u)
+                    load_row(old[ACC ? u : 0],
+                             __shfl_sync(0xFFFFFFFFu, my_key, i0 + u < live ? i0 + u : live - 1));
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int i = i0 + u;
+                if (i >= live) break;
+                add_row<Y, VEC, N, kPer>(acc, v[u]);
+                if (!((over >> i) & 1u)) continue;
+                const int32_t k = __shfl_sync(0xFFFFFFFFu, my_key, i);
+                // the run ends here, or goes on in the next chunk
+                const bool enters = begin == 0 && key_before == k;
+                const bool leaves = i + 1 == n && key_after == k;
+                if (!enters && !leaves) {
+                    write_row(k, old[ACC ? u : 0]);
+                } else {
+                    put_partial(enters ? 0 : 1);
+                    const int from = enters ? run_start(k) : chunk;
+                    const int to = leaves ? run_end(k) : chunk;
+                    join(k, from, to);
+                }
+                clear();
+                begin = i + 1;
+            }
         }
     }
 }
@@ -815,14 +867,21 @@ cudaError_t embed_sum(const EmbedGradArgs& a, cudaStream_t stream) {
     const bool vec = aligned_to(a.grad_out, kV * static_cast<int64_t>(sizeof(Y))) &&
                      aligned_to(a.grad_weight, kV * static_cast<int64_t>(sizeof(G))) &&
                      a.dim % kV == 0 && a.grad_stride % kV == 0;
-    const int64_t warps = chunks_of(a.n_tokens) * groups_of(a.dim);
-    const unsigned g = static_cast<unsigned>((warps + 7) / 8);
+    const Workspace ws = workspace(a.workspace, a.n_tokens, a.dim);
+    const int last = (sort_plan(a.vocab).passes - 1) % 2;
+    const int groups = static_cast<int>(groups_of(a.dim));
+    const Sorted sorted{ws.key[last], ws.tok[last], ws.done, ws.partial, groups};
+    // 8 warps: the groups of a chunk side by side, then chunks
+    const int gy = groups < 8 ? groups : 8, cz = 8 / gy;
+    const dim3 block(32, gy, cz);
+    const dim3 grid(static_cast<unsigned>((chunks_of(a.n_tokens) + cz - 1) / cz),
+                    static_cast<unsigned>((groups + gy - 1) / gy));
     if (a.accumulate) {
-        if (vec) embed_sum_kernel<Y, G, kV, true><<<g, 256, 0, stream>>>(a);
-        else embed_sum_kernel<Y, G, 1, true><<<g, 256, 0, stream>>>(a);
+        if (vec) embed_sum_kernel<Y, G, kV, true><<<grid, block, 0, stream>>>(a, sorted);
+        else embed_sum_kernel<Y, G, 1, true><<<grid, block, 0, stream>>>(a, sorted);
     } else {
-        if (vec) embed_sum_kernel<Y, G, kV, false><<<g, 256, 0, stream>>>(a);
-        else embed_sum_kernel<Y, G, 1, false><<<g, 256, 0, stream>>>(a);
+        if (vec) embed_sum_kernel<Y, G, kV, false><<<grid, block, 0, stream>>>(a, sorted);
+        else embed_sum_kernel<Y, G, 1, false><<<grid, block, 0, stream>>>(a, sorted);
     }
     return cudaGetLastError();
 }

@@ -74,9 +74,9 @@ int check_table(int64_t n_tokens, int64_t vocab, int64_t dim, double scale) {
         return fail(ZERO_ERR_SIZE, "n_tokens, vocab and dim must fit 32 bits");
     if (vocab > std::numeric_limits<int64_t>::max() / 8 / dim)
         return fail(ZERO_ERR_SIZE, "the table's size overflows int64");
-    // the gradient's sum launch: a warp for 32 tokens and 256 columns
-    if ((n_tokens / 32 + 1) * (dim / 256 + 1) > 8 * kMax32 - 8)
-        return fail(ZERO_ERR_SIZE, "n_tokens * dim is too large");
+    // the gradient's sum launch: 8 groups of 256 columns a block row
+    if (dim > 8 * 256 * int64_t{65535})
+        return fail(ZERO_ERR_SIZE, "dim = %lld is too large", (long long)dim);
     return ZERO_OK;
 }
 
