@@ -6,16 +6,19 @@
 //
 // A row lives in the registers of a group of threads, E elements each, so that
 // every byte of x, dy and the output crosses memory once.  A CTA holds several
-// groups, which work through the rows independently, kBatch rows at a time:
-// one group barrier then serves the sums of several rows, and the next batch's
-// loads are under way meanwhile.  The parameters stay in registers over all
-// rows, and so do the backward pass's columns of dw and db; each CTA writes
-// one pair of partial rows, which a second launch adds up in CTA order.
+// groups, which work through the rows independently; the next row's loads are
+// under way while a row is worked on.  The parameters stay in registers or, to
+// leave room for more warps, in shared memory (each thread its own columns: no
+// barrier), and the backward pass's columns of dw and db in registers over all
+// rows; each CTA writes one pair of partial rows, which a second launch adds up
+// in CTA order.
 //
 // The variance is taken about a mean at every step: a warp's squares about the
 // warp's mean, then sum (M2_w + n_w (mean_w - mu)^2) over the warps of the
 // row, so that a mean far from zero costs no digits and one exchange is enough.
 #include "zero_ops.cuh"
+
+#include <mutex>
 
 namespace zf {
 
@@ -23,10 +26,10 @@ namespace {
 
 constexpr int kNormThreads = 512;      // of a CTA, at most
 constexpr int kNormWarps = kNormThreads / 32;
-constexpr int kSmallThreads = 384;     // of the forward pass at E = 8: 768 an SM, 80 registers
+constexpr int kGradThreads = 384;      // of the backward pass at E = 8, two CTAs an SM
 
-// Rows per batch, as far as 128 registers a thread go.
-__host__ __device__ constexpr int batch_of(int e) { return e == 8 ? 2 : 1; }
+// Rows worked on at a time.
+__host__ __device__ constexpr int batch_of(int) { return 1; }
 
 // The group of threads that holds a row.
 struct Group {
@@ -44,18 +47,19 @@ struct Group {
     }
 };
 
-// This thread's columns: pack n holds columns n * group * VEC + t * VEC ...;
-// `ok` says which packs there are.
+// This thread's columns: pack n holds columns n * group * VEC + t * VEC ..., of
+// which the first left[n] exist.
 template <int VEC, int E>
 struct Columns {
     static constexpr int N = E / VEC;
     int first, step;
-    bool ok[N];
+    int left[N];
     __device__ Columns(const Group& g, int dim) : first(g.t * VEC), step(g.threads * VEC) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) ok[n] = first + n * step < dim;
+        for (int n = 0; n < N; ++n) left[n] = min(max(dim - at(n), 0), VEC);
     }
     __device__ __forceinline__ int at(int n) const { return first + n * step; }
+    __device__ __forceinline__ bool ok(int n, int e) const { return e < left[n]; }
 };
 
 // A row's E elements as loaded, zeros where there are none.
@@ -67,7 +71,15 @@ struct Row {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             p[n] = Pack<T, VEC>{};
-            if (in && c.ok[n]) p[n] = ld_pack<T, VEC>(at + n * c.step);
+            if (in && c.left[n] == VEC) p[n] = ld_pack<T, VEC>(at + n * c.step);
+            if constexpr (VEC > 1) {
+                if (in && c.left[n] > 0 && c.left[n] < VEC) {     // the row's last elements
+#pragma unroll
+                    for (int e = 0; e < VEC - 1; ++e) {
+                        if (e < c.left[n]) p[n].x[e] = at[n * c.step + e];
+                    }
+                }
+            }
         }
     }
     // element pairs (2 i, 2 i + 1) in fp32
@@ -88,7 +100,7 @@ template <class T, int VEC, int E>
 __device__ __forceinline__ void store_row(T* at, const Pair (&y)[E / 2], const Columns<VEC, E>& c) {
 #pragma unroll
     for (int n = 0; n < E / VEC; ++n) {
-        if (!c.ok[n]) continue;
+        if (c.left[n] == 0) continue;
         Pack<T, VEC> v;
         if constexpr (VEC == 1) {
             const float2 f = unpair(y[n / 2]);
@@ -105,25 +117,63 @@ __device__ __forceinline__ void store_row(T* at, const Pair (&y)[E / 2], const C
                 v.x[2 * i + 1] = narrow<T>(f.y);
             }
         }
-        st_pack<T, VEC>(at + n * c.step, v);
+        if (c.left[n] == VEC) {
+            st_pack<T, VEC>(at + n * c.step, v);
+        } else if constexpr (VEC > 1) {
+#pragma unroll
+            for (int e = 0; e < VEC - 1; ++e) {
+                if (e < c.left[n]) at[n * c.step + e] = v.x[e];
+            }
+        }
     }
 }
 
 // The parameters of this thread's columns (`missing` where there is no array
-// or no column).
+// or no column).  Loads without conditions, at a clamped place, so that all are
+// under way at once.
+template <class PT, int VEC, int E>
+__device__ __forceinline__ void ld_params_as(float (&v)[E], const void* p, int dim,
+                                             const Columns<VEC, E>& c) {
+    PT raw[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+        raw[i] = static_cast<const PT*>(p)[min(c.at(i / VEC) + i % VEC, dim - 1)];
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = widen<PT>(raw[i]);
+}
+
 template <int VEC, int E>
-__device__ __forceinline__ void ld_params(Pair (&w)[E / 2], const void* p, bool f32,
+__device__ __forceinline__ void ld_params(Pair (&w)[E / 2], const void* p, const NormArgs& a,
                                           const Columns<VEC, E>& c, float missing) {
     float v[E];
+    if (p == nullptr) {
 #pragma unroll
-    for (int n = 0; n < E / VEC; ++n) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            v[n * VEC + e] = p != nullptr && c.ok[n] ? ld_param(p, f32, c.at(n) + e) : missing;
+        for (int i = 0; i < E; ++i) v[i] = missing;
+    } else if (a.param_f32) {
+        ld_params_as<float>(v, p, a.dim, c);
+    } else {
+        ld_params_as<uint16_t>(v, p, a.dim, c);
     }
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = c.ok(i / VEC, i % VEC) ? v[i] : missing;
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) w[i] = pair(v[2 * i], v[2 * i + 1]);
 }
+
+// Pairs of this thread's columns in shared memory, 16 bytes a thread at a time.
+template <int E>
+struct Kept {
+    ulonglong2* at;
+    int step;
+    __device__ Kept(void* base, int array)
+        : at(static_cast<ulonglong2*>(base) + array * (E / 4) * blockDim.x + threadIdx.x),
+          step(blockDim.x) {}
+    __device__ __forceinline__ void put(const Pair (&w)[E / 2]) const {
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) at[i * step] = make_ulonglong2(w[2 * i], w[2 * i + 1]);
+    }
+    __device__ __forceinline__ ulonglong2 operator[](int i) const { return at[i * step]; }
+};
 
 __device__ __forceinline__ float both(Pair p) {
     const float2 v = unpair(p);
@@ -131,6 +181,13 @@ __device__ __forceinline__ float both(Pair p) {
 }
 
 __device__ __forceinline__ Pair splat(float x) { return pair(x, x); }
+
+// 1 / sqrt(x): the approximation and one Newton step.
+__device__ __forceinline__ float inv_sqrt(float x) {
+    const float y = rsqrtf(x);
+    const float z = y * __fmaf_rn(-0.5f * x * y, y, 1.5f);
+    return y == __builtin_huge_valf() ? y : z;
+}
 
 // Sums of K pairs of values over a group, in a fixed order: lanes, then warps.
 // `red` has two halves that are used in turn: one barrier a call is enough.
@@ -156,8 +213,9 @@ __device__ __forceinline__ void group_sum(const Group& g, float2 (&x)[K],
 }
 
 template <class T, int VEC, int E>
-__global__ void __launch_bounds__(E == 8 ? kSmallThreads : kNormThreads, E == 8 ? 2 : 1)
+__global__ void __launch_bounds__(kNormThreads, E == 32 ? 1 : 2)
 norm_kernel(const __grid_constant__ NormArgs a) {
+    extern __shared__ __align__(16) char params[];           // weight, bias
     constexpr int kBatch = batch_of(E), P = E / 2;
     __shared__ float2 red[2][kBatch][kNormWarps];
     int half = 0;
@@ -176,9 +234,15 @@ norm_kernel(const __grid_constant__ NormArgs a) {
     const float inv_n = 1.0f / fmaxf(columns_of(g.t / 32), 1.0f);
     const float lane_n = columns_of(lane);
     const float lane_inv_n = 1.0f / fmaxf(lane_n, 1.0f);
-    Pair w[P], b[P];
-    ld_params<VEC, E>(w, a.weight, a.param_f32, c, 1.0f);
-    ld_params<VEC, E>(b, a.bias, a.param_f32, c, 0.0f);
+    const Kept<E> w(params, 0), b(params, 1);
+    {
+        Pair v[P];
+        ld_params<VEC, E>(v, a.weight, a, c, 1.0f);
+        w.put(v);
+        ld_params<VEC, E>(v, a.bias, a, c, 0.0f);
+        b.put(v);
+    }
+    const bool ragged = a.dim % VEC != 0;
     const int64_t step = static_cast<int64_t>(gridDim.x) * g.per_cta * kBatch;
     int64_t row = (static_cast<int64_t>(blockIdx.x) * g.per_cta + g.index) * kBatch;
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride + c.first;
@@ -209,11 +273,12 @@ norm_kernel(const __grid_constant__ NormArgs a) {
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 Pair d = add2(v[i][j], m);
-                if constexpr (VEC == 1) {
+                if (VEC == 1 || ragged) {
                     const float2 f = unpair(d);
-                    d = pair(c.ok[2 * j] ? f.x : 0.0f, c.ok[2 * j + 1] ? f.y : 0.0f);
+                    d = pair(c.ok(2 * j / VEC, 2 * j % VEC) ? f.x : 0.0f,
+                             c.ok((2 * j + 1) / VEC, (2 * j + 1) % VEC) ? f.y : 0.0f);
                 } else {
-                    d = c.ok[2 * j / VEC] ? d : 0;
+                    d = c.left[2 * j / VEC] != 0 ? d : 0;
                 }
                 q = fma2(d, d, q);
             }
@@ -240,33 +305,45 @@ norm_kernel(const __grid_constant__ NormArgs a) {
         for (int i = 0; i < kBatch; ++i) {
             if (row + i >= a.n_rows) break;
             const float mu = s[i].x * inv_d;
-            const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fmaf_rn(s[i].y, inv_d, a.eps)));
+            const float r = inv_sqrt(__fmaf_rn(s[i].y, inv_d, a.eps));
             if (g.t == 0) {
                 if (a.mean != nullptr) a.mean[row + i] = mu;
                 if (a.rstd != nullptr) a.rstd[row + i] = r;
             }
             const Pair m2 = splat(-mu), r2 = splat(r);
 #pragma unroll
-            for (int j = 0; j < P; ++j) v[i][j] = fma2(mul2(add2(v[i][j], m2), r2), w[j], b[j]);
+            for (int j = 0; j < P / 2; ++j) {
+                const ulonglong2 wj = w[j], bj = b[j];
+                Pair *y0 = &v[i][2 * j], *y1 = &v[i][2 * j + 1];
+                *y0 = fma2(mul2(add2(*y0, m2), r2), wj.x, bj.x);
+                *y1 = fma2(mul2(add2(*y1, m2), r2), wj.y, bj.y);
+            }
             store_row<T, VEC, E>(out + i * a.out_stride, v[i], c);
         }
     }
 }
 
 template <class T, int VEC, int E>
-__global__ void __launch_bounds__(kNormThreads, 1)
+__global__ void __launch_bounds__(E == 8 ? kGradThreads : kNormThreads, E == 8 ? 2 : 1)
 norm_grad_kernel(const __grid_constant__ NormArgs a) {
-    constexpr int kBatch = batch_of(E), P = E / 2;
-    extern __shared__ float cols[];          // [groups][dim] where a CTA has several
+    constexpr int kBatch = 1, P = E / 2;
+    constexpr bool kKeep = E > 8;            // the weight in shared memory
+    extern __shared__ __align__(16) char dyn[];
+    float* cols = reinterpret_cast<float*>(dyn);     // [groups][dim] where a CTA has several;
+                                                     // before, the weight
     __shared__ float2 red[2][kBatch][kNormWarps];
     int half = 0;
     const Group g(a.group_threads);
     const Columns<VEC, E> c(g, a.dim);
     const float inv_d = 1.0f / static_cast<float>(a.dim);
     Pair w[P], dw[P], db[P];
-    ld_params<VEC, E>(w, a.weight, a.param_f32, c, 1.0f);
+    ld_params<VEC, E>(w, a.weight, a, c, 1.0f);
+    const Kept<E> kept(dyn, 0);
+    if (kKeep) kept.put(w);
 #pragma unroll
     for (int j = 0; j < P; ++j) dw[j] = db[j] = 0;
+    // the reduction's launch may be set up from now on
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t step = static_cast<int64_t>(gridDim.x) * g.per_cta * kBatch;
     int64_t row = (static_cast<int64_t>(blockIdx.x) * g.per_cta + g.index) * kBatch;
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride + c.first;
@@ -298,8 +375,10 @@ norm_grad_kernel(const __grid_constant__ NormArgs a) {
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 const Pair d = next_y[i][j];
+                Pair wj = w[j];
+                if (kKeep) wj = j % 2 == 0 ? kept[j / 2].x : kept[j / 2].y;
                 xh[i][j] = mul2(add2(next_x[i][j], m2), r2);
-                gr[i][j] = mul2(d, w[j]);
+                gr[i][j] = mul2(d, wj);
                 dw[j] = fma2(d, xh[i][j], dw[j]);
                 db[j] = add2(db[j], d);
                 s1 = add2(s1, gr[i][j]);
@@ -328,8 +407,8 @@ norm_grad_kernel(const __grid_constant__ NormArgs a) {
         for (int j = 0; j < P; ++j) {
             const float2 f = unpair(acc[j]);
             const int n0 = 2 * j / VEC, n1 = (2 * j + 1) / VEC;
-            if (c.ok[n0]) to[c.at(n0) + 2 * j % VEC] = f.x;
-            if (c.ok[n1]) to[c.at(n1) + (2 * j + 1) % VEC] = f.y;
+            if (c.ok(n0, 2 * j % VEC)) to[c.at(n0) + 2 * j % VEC] = f.x;
+            if (c.ok(n1, (2 * j + 1) % VEC)) to[c.at(n1) + (2 * j + 1) % VEC] = f.y;
         }
     };
     if (g.per_cta == 1) {
@@ -358,6 +437,7 @@ constexpr int kStrandLoads = 5;
 __global__ void __launch_bounds__(32 * kStrands)
 norm_grad_reduce_kernel(const __grid_constant__ NormArgs a, int n_parts) {
     __shared__ float sum[kStrands][33];
+    asm volatile("griddepcontrol.wait;" ::: "memory");       // the partial rows are there
     const int lane = threadIdx.x % 32, strand = threadIdx.x / 32;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;   // of 2 dim columns
     const int64_t width = 2 * static_cast<int64_t>(a.dim);
@@ -394,24 +474,44 @@ struct Shape {
 Shape shape_for(int64_t dim, bool back) {
     const int e = dim <= 2048 ? 8 : dim <= 16 * kNormThreads ? 16 : 32;
     const int group = static_cast<int>((dim + e * 32 - 1) / (e * 32) * 32);
-    int per_cta = (back || e != 8 ? kNormThreads : kSmallThreads) / group;
+    int per_cta = (back && e == 8 ? kGradThreads : kNormThreads) / group;
     if (per_cta > 8) per_cta = 8;               // 16 hardware barriers a CTA
     return {e, group, per_cta};
 }
 
+// CTAs: what the registers of an SM hold (launch bounds), or what the rows need.
 int64_t ctas_for(const Shape& s, int64_t rows, bool back) {
     const int threads = s.group * s.per_cta;
-    const int per_sm = back || s.e != 8 ? kNormThreads / threads : 2 * kSmallThreads / threads;
-    const int64_t per = static_cast<int64_t>(s.per_cta) * batch_of(s.e);
+    const int per_sm = back ? (s.e == 8 ? 2 * kGradThreads / threads : 1)
+                            : (s.e == 32 ? 1 : 2 * kNormThreads / threads);
+    const int64_t per = static_cast<int64_t>(s.per_cta) * (back ? 1 : batch_of(s.e));
     const int64_t need = rows > 0 ? (rows + per - 1) / per : 1;
     const int64_t most = static_cast<int64_t>(device_sms()) * per_sm;
     return need < most ? need : most;
 }
 
-// Whether every row of a matrix allows accesses of 16 bytes.
-bool wide_rows(int elem, const void* p, int64_t stride, int64_t dim) {
-    const int want = 16 / elem;
-    return aligned_to(p, 16) && stride % want == 0 && dim % want == 0;
+// Whether every row of a matrix starts on a 16-byte boundary.
+bool wide_rows(int elem, const void* p, int64_t stride) {
+    return aligned_to(p, 16) && stride % (16 / elem) == 0;
+}
+
+template <class T, int VEC, int E, bool BACK>
+cudaError_t launch_e(const NormArgs& a, unsigned grid, int threads, size_t smem,
+                     cudaStream_t stream) {
+    const auto kernel = BACK ? norm_grad_kernel<T, VEC, E> : norm_kernel<T, VEC, E>;
+    // more than 48 KB of shared memory need asking for
+    static std::once_flag once[64];
+    static cudaError_t set[64];
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::call_once(once[dev], [&] {
+        set[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        2 * sizeof(float) * E * kNormThreads);
+    });
+    if (set[dev] != cudaSuccess) return set[dev];
+    kernel<<<grid, threads, smem, stream>>>(a);
+    return cudaGetLastError();
 }
 
 template <class T, int VEC, bool BACK>
@@ -420,27 +520,24 @@ cudaError_t launch_shape(NormArgs a, cudaStream_t stream) {
     a.group_threads = s.group;
     const unsigned g = static_cast<unsigned>(ctas_for(s, a.n_rows, BACK));
     const int threads = s.group * s.per_cta;
-    const size_t smem =
-        BACK && s.per_cta > 1 ? static_cast<size_t>(s.per_cta) * a.dim * sizeof(float) : 0;
-#define ZF_NORM(E)                                                            \
-    do {                                                                      \
-        if constexpr (BACK)                                                   \
-            norm_grad_kernel<T, VEC, E><<<g, threads, smem, stream>>>(a);     \
-        else                                                                  \
-            norm_kernel<T, VEC, E><<<g, threads, 0, stream>>>(a);             \
-        return cudaGetLastError();                                            \
-    } while (0)
-    if (s.e == 8) ZF_NORM(8);
-    if (s.e == 16) ZF_NORM(16);
-    ZF_NORM(32);
-#undef ZF_NORM
+    size_t smem = 0;
+    if (BACK) {
+        const size_t kept = s.e > 8 ? sizeof(float) * s.e * threads : 0;
+        const size_t cols = s.per_cta > 1 ? sizeof(float) * s.per_cta * a.dim : 0;
+        smem = kept > cols ? kept : cols;
+    } else {
+        smem = 2 * sizeof(float) * s.e * threads;
+    }
+    if (s.e == 8) return launch_e<T, VEC, 8, BACK>(a, g, threads, smem, stream);
+    if (s.e == 16) return launch_e<T, VEC, 16, BACK>(a, g, threads, smem, stream);
+    return launch_e<T, VEC, 32, BACK>(a, g, threads, smem, stream);
 }
 
 template <bool BACK>
 cudaError_t dispatch(const NormArgs& a, int act_bytes, cudaStream_t stream) {
-    const bool wide = wide_rows(act_bytes, a.x, a.x_stride, a.dim) &&
-                      wide_rows(act_bytes, a.out, a.out_stride, a.dim) &&
-                      (!BACK || wide_rows(act_bytes, a.grad_out, a.grad_out_stride, a.dim));
+    const bool wide = wide_rows(act_bytes, a.x, a.x_stride) &&
+                      wide_rows(act_bytes, a.out, a.out_stride) &&
+                      (!BACK || wide_rows(act_bytes, a.grad_out, a.grad_out_stride));
     if (act_bytes == 4)
         return wide ? launch_shape<float, 4, BACK>(a, stream)
                     : launch_shape<float, 1, BACK>(a, stream);
@@ -464,9 +561,17 @@ cudaError_t launch_norm_grad(const NormArgs& a, int act_bytes, cudaStream_t stre
 
 cudaError_t launch_norm_grad_reduce(const NormArgs& a, cudaStream_t stream) {
     const int64_t width = 2 * static_cast<int64_t>(a.dim);
-    norm_grad_reduce_kernel<<<static_cast<unsigned>((width + 31) / 32), 32 * kStrands, 0, stream>>>(
-        a, norm_grad_ctas(a.n_rows, a.dim));
-    return cudaGetLastError();
+    // its blocks may be set up while the partial rows are still being added up
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>((width + 31) / 32));
+    cfg.blockDim = dim3(32 * kStrands);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, norm_grad_reduce_kernel, a, norm_grad_ctas(a.n_rows, a.dim));
 }
 
 }  // namespace zf
