@@ -6,8 +6,10 @@
 //
 // A row lives in the registers of a group of threads, E elements each, so that
 // every byte of x, dy and the output crosses memory once.  A CTA holds several
-// groups, which work through the rows independently; the next row's loads are
-// under way while a row is worked on.  The parameters stay in registers or, to
+// groups, which work through the rows independently; the next rows' loads are
+// under way while a row is worked on (cp.async to shared memory, each thread
+// its own words, so that no barrier separates copy and use; a row takes about
+// 2 us from load to store, and one row ahead kept a third of memory's rate).  The parameters stay in registers or, to
 // leave room for more warps, in shared memory (each thread its own columns: no
 // barrier), and the backward pass's columns of dw and db in registers over all
 // rows; each CTA writes one pair of partial rows, which a second launch adds up
@@ -24,12 +26,13 @@ namespace zf {
 
 namespace {
 
-constexpr int kNormThreads = 512;      // of a CTA, at most
-constexpr int kNormWarps = kNormThreads / 32;
-constexpr int kGradThreads = 384;      // of the backward pass at E = 8, two CTAs an SM
+constexpr int kNormThreads = 512;      // of a CTA, but for the backward pass at E = 8
+constexpr int kNormWarps = 24;         // of a CTA, at most
 
-// Rows worked on at a time.
-__host__ __device__ constexpr int batch_of(int) { return 1; }
+// Of the backward pass at E = 8: one CTA of 768 threads an SM with bf16 (80
+// registers), two of 256 with fp32 (128), whose rows take twice as many.
+__host__ __device__ constexpr int grad_threads(int elem) { return elem == 2 ? 768 : 256; }
+__host__ __device__ constexpr int grad_ctas(int elem) { return elem == 2 ? 1 : 2; }
 
 // The group of threads that holds a row.
 struct Group {
@@ -46,6 +49,28 @@ struct Group {
         asm volatile("bar.sync %0, %1;" ::"r"(index + 1), "r"(threads) : "memory");
     }
 };
+
+// Rows under way at a time in shared memory (0: one, in registers), for `arrays`
+// matrices: as far as shared memory goes, with the CTAs an SM that the launch
+// bounds allow.
+__host__ __device__ constexpr int depth_of(int vec, int e, int elem, int arrays) {
+    if (vec == 1) return 0;
+    if (e == 8) return 4;
+    if (e == 16) return arrays == 1 ? (elem == 2 ? 2 : 3) : elem == 2 ? 4 : 2;
+    return elem == 2 ? 2 : 0;
+}
+
+__device__ __forceinline__ void cp_async16_fill(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // This thread's columns: pack n holds columns n * group * VEC + t * VEC ..., of
 // which the first left[n] exist.
@@ -81,6 +106,20 @@ struct Row {
                 }
             }
         }
+    }
+    // the same through shared memory: this thread's words of one row
+    __device__ static __forceinline__ void copy(uint32_t to, const T* at, bool in,
+                                                const Columns<VEC, E>& c) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int bytes = in ? c.left[n] * static_cast<int>(sizeof(T)) : 0;
+            cp_async16_fill(to + 16u * n * blockDim.x, at + (bytes != 0 ? n * c.step : 0), bytes);
+        }
+    }
+    __device__ __forceinline__ void read(const char* from) {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            p[n] = *reinterpret_cast<const Pack<T, VEC>*>(from + 16u * n * blockDim.x);
     }
     // element pairs (2 i, 2 i + 1) in fp32
     __device__ __forceinline__ Pair operator[](int i) const {
@@ -189,34 +228,46 @@ __device__ __forceinline__ float inv_sqrt(float x) {
     return y == __builtin_huge_valf() ? y : z;
 }
 
-// Sums of K pairs of values over a group, in a fixed order: lanes, then warps.
-// `red` has two halves that are used in turn: one barrier a call is enough.
-template <int K>
-__device__ __forceinline__ void group_sum(const Group& g, float2 (&x)[K],
-                                          float2 (*red)[K][kNormWarps], int& half) {
+// Sums of a pair of values over a group, in a fixed order: lanes, then warps.
+// The first exchange leaves one value to each half of the warp, so that five
+// steps add up both.  `red` has two halves that are used in turn: one barrier a
+// call is enough.
+__device__ __forceinline__ float2 group_sum2(const Group& g, float x, float y,
+                                             float (*red)[2][kNormWarps], int& half) {
+    const int lane = threadIdx.x % 32;
+    const bool low = lane < 16;
+    float v = low ? x : y;
+    v += __shfl_xor_sync(0xFFFFFFFFu, low ? y : x, 16);
 #pragma unroll
-    for (int k = 0; k < K; ++k) x[k] = make_float2(warp_sum(x[k].x), warp_sum(x[k].y));
-    if (g.warps == 1) return;
-    float2(*slot)[kNormWarps] = red[half];
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (g.warps == 1)
+        return make_float2(__shfl_sync(0xFFFFFFFFu, v, 0), __shfl_sync(0xFFFFFFFFu, v, 16));
+    float(*slot)[kNormWarps] = red[half];
     half ^= 1;
-    const int w0 = g.index * g.warps, lane = threadIdx.x % 32;
-    if (lane == 0) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) slot[k][w0 + g.t / 32] = x[k];
-    }
+    const int w0 = g.index * g.warps;
+    if (lane % 16 == 0) slot[low ? 0 : 1][w0 + g.t / 32] = v;
     g.sync();
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const float2 v = lane < g.warps ? slot[k][w0 + lane] : make_float2(0.0f, 0.0f);
-        x[k] = make_float2(warp_sum(v.x), warp_sum(v.y));
+    if (g.warps <= 6) {
+        x = y = 0.0f;
+        for (int w = 0; w < g.warps; ++w) {
+            x += slot[0][w0 + w];
+            y += slot[1][w0 + w];
+        }
+        return make_float2(x, y);
     }
+    v = lane % 16 < g.warps ? slot[low ? 0 : 1][w0 + lane % 16] : 0.0f;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return make_float2(__shfl_sync(0xFFFFFFFFu, v, 0), __shfl_sync(0xFFFFFFFFu, v, 16));
 }
 
 template <class T, int VEC, int E>
 __global__ void __launch_bounds__(kNormThreads, E == 32 ? 1 : 2)
 norm_kernel(const __grid_constant__ NormArgs a) {
-    extern __shared__ __align__(16) char params[];           // weight, bias
-    constexpr int kBatch = batch_of(E), P = E / 2;
+    constexpr int kDepth = depth_of(VEC, E, sizeof(T), 1);
+    constexpr bool kAsync = kDepth > 0;
+    extern __shared__ __align__(16) char params[];           // weight, bias, rows
+    constexpr int kBatch = 1, P = E / 2;
     __shared__ float2 red[2][kBatch][kNormWarps];
     int half = 0;
     const Group g(a.group_threads);
@@ -248,19 +299,43 @@ norm_kernel(const __grid_constant__ NormArgs a) {
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride + c.first;
     T* out = static_cast<T*>(a.out) + row * a.out_stride + c.first;
     Row<T, VEC, E> next[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) next[i].load(x + i * a.x_stride, row + i < a.n_rows, c);
+    // this thread's words of row slot k: at held + k * slot
+    const char* held = params + 2 * sizeof(float) * E * blockDim.x + 16 * threadIdx.x;
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(held));
+    const uint32_t slot = sizeof(T) * E * blockDim.x;
+    int64_t ahead = row;                                     // the next row to copy
+    int put = 0, get = 0;
+    // (a row beyond the last: nothing is read, from an address that is)
+    auto copy_next = [&] {
+        Row<T, VEC, E>::copy(to + put * slot,
+                             ahead < a.n_rows ? x : static_cast<const T*>(a.x), ahead < a.n_rows, c);
+        cp_async_commit();
+        x += step * a.x_stride;
+        ahead += step;
+        put = put + 1 == kDepth ? 0 : put + 1;
+    };
+    if constexpr (kAsync) {
+        for (int k = 0; k < kDepth - 1; ++k) copy_next();
+    } else {
+        next[0].load(x, row < a.n_rows, c);
+    }
     for (; row < a.n_rows; row += step, out += step * a.out_stride) {
+        if constexpr (kAsync) {
+            copy_next();
+            cp_async_wait<kDepth - 1 < 0 ? 0 : kDepth - 1>();
+            next[0].read(held + get * slot);
+            get = get + 1 == kDepth ? 0 : get + 1;
+        }
         Pair v[kBatch][P];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
 #pragma unroll
             for (int j = 0; j < P; ++j) v[i][j] = next[i][j];
         }
-        x += step * a.x_stride;
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            next[i].load(x + i * a.x_stride, row + step + i < a.n_rows, c);
+        if constexpr (!kAsync) {
+            x += step * a.x_stride;
+            next[0].load(x, row + step < a.n_rows, c);
+        }
         float2 s[kBatch];        // a warp's sum, and its squares about its mean
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
@@ -324,14 +399,16 @@ norm_kernel(const __grid_constant__ NormArgs a) {
 }
 
 template <class T, int VEC, int E>
-__global__ void __launch_bounds__(E == 8 ? kGradThreads : kNormThreads, E == 8 ? 2 : 1)
+__global__ void __launch_bounds__(E == 8 ? grad_threads(sizeof(T)) : kNormThreads, E == 8 ? grad_ctas(sizeof(T)) : 1)
 norm_grad_kernel(const __grid_constant__ NormArgs a) {
-    constexpr int kBatch = 1, P = E / 2;
+    constexpr int P = E / 2;
     constexpr bool kKeep = E > 8;            // the weight in shared memory
+    constexpr int kDepth = depth_of(VEC, E, sizeof(T), 2);
+    constexpr bool kAsync = kDepth > 0;
     extern __shared__ __align__(16) char dyn[];
     float* cols = reinterpret_cast<float*>(dyn);     // [groups][dim] where a CTA has several;
-                                                     // before, the weight
-    __shared__ float2 red[2][kBatch][kNormWarps];
+                                                     // before, the weight and the rows
+    __shared__ float red[2][2][kNormWarps];
     int half = 0;
     const Group g(a.group_threads);
     const Columns<VEC, E> c(g, a.dim);
@@ -344,65 +421,102 @@ norm_grad_kernel(const __grid_constant__ NormArgs a) {
     for (int j = 0; j < P; ++j) dw[j] = db[j] = 0;
     // the reduction's launch may be set up from now on
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t step = static_cast<int64_t>(gridDim.x) * g.per_cta * kBatch;
-    int64_t row = (static_cast<int64_t>(blockIdx.x) * g.per_cta + g.index) * kBatch;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * g.per_cta;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * g.per_cta + g.index;
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride + c.first;
     const T* dy = static_cast<const T*>(a.grad_out) + row * a.grad_out_stride + c.first;
     T* out = static_cast<T*>(a.out) + row * a.out_stride + c.first;
-    Row<T, VEC, E> next_x[kBatch], next_y[kBatch];
-    float next_mu[kBatch], next_r[kBatch];
-    auto load = [&](int64_t at) {
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const bool in = at + i < a.n_rows;
-            next_x[i].load(x + i * a.x_stride, in, c);
-            next_y[i].load(dy + i * a.grad_out_stride, in, c);
-            next_mu[i] = in ? a.mean[at + i] : 0.0f;
-            next_r[i] = in ? a.rstd[at + i] : 0.0f;
-        }
-    };
-    load(row);
-    for (; row < a.n_rows; row += step, out += step * a.out_stride) {
-        Pair xh[kBatch][P], gr[kBatch][P];
-        float r[kBatch];
-        float2 s[kBatch];
-        // dy is 0 where there is no row or column, and adds nothing there
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const Pair m2 = splat(-next_mu[i]), r2 = splat(next_r[i]);
-            r[i] = next_r[i];
-            Pair s1 = 0, s2 = 0;
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                const Pair d = next_y[i][j];
-                Pair wj = w[j];
-                if (kKeep) wj = j % 2 == 0 ? kept[j / 2].x : kept[j / 2].y;
-                xh[i][j] = mul2(add2(next_x[i][j], m2), r2);
-                gr[i][j] = mul2(d, wj);
-                dw[j] = fma2(d, xh[i][j], dw[j]);
-                db[j] = add2(db[j], d);
-                s1 = add2(s1, gr[i][j]);
-                s2 = fma2(gr[i][j], xh[i][j], s2);
-            }
-            s[i] = make_float2(both(s1), both(s2));
-        }
+    Row<T, VEC, E> next_x, next_y;
+    float next_mu = 0.0f, next_r = 0.0f;
+    // this thread's words of row slot k: at held + k * slot, x then dy
+    const char* held = dyn + (kKeep ? sizeof(float) * E * blockDim.x : 0) + 16 * threadIdx.x;
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(held));
+    const uint32_t one = sizeof(T) * E * blockDim.x, slot = 2 * one;
+    int64_t ahead = row;                                     // the next row to copy
+    int put_at = 0, get = 0;
+    // (a row beyond the last: nothing is read, from an address that is)
+    auto copy_next = [&] {
+        const bool in = ahead < a.n_rows;
+        Row<T, VEC, E>::copy(to + put_at * slot, in ? x : static_cast<const T*>(a.x), in, c);
+        Row<T, VEC, E>::copy(to + put_at * slot + one, in ? dy : static_cast<const T*>(a.grad_out),
+                             in, c);
+        cp_async_commit();
         x += step * a.x_stride;
         dy += step * a.grad_out_stride;
-        load(row + step);
-        group_sum<kBatch>(g, s, red, half);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (row + i >= a.n_rows) break;
-            const Pair r2 = splat(r[i]), m1 = splat(-s[i].x * inv_d * r[i]);
-            const Pair m2 = splat(-s[i].y * inv_d * r[i]);
-#pragma unroll
-            for (int j = 0; j < P; ++j)
-                gr[i][j] = fma2(xh[i][j], m2, fma2(gr[i][j], r2, m1));
-            store_row<T, VEC, E>(out + i * a.out_stride, gr[i], c);
+        ahead += step;
+        put_at = put_at + 1 == kDepth ? 0 : put_at + 1;
+    };
+    auto load_stats = [&](int64_t at) {
+        if (at < a.n_rows) {
+            next_mu = a.mean[at];
+            next_r = a.rstd[at];
         }
+    };
+    auto load = [&](int64_t at) {
+        next_x.load(x, at < a.n_rows, c);
+        next_y.load(dy, at < a.n_rows, c);
+    };
+    load_stats(row);
+    if constexpr (kAsync) {
+        for (int k = 0; k < kDepth - 1; ++k) copy_next();
+    } else {
+        load(row);
     }
+    for (; row < a.n_rows; row += step, out += step * a.out_stride) {
+        if constexpr (kAsync) {
+            copy_next();
+            cp_async_wait<kDepth - 1 < 0 ? 0 : kDepth - 1>();
+            next_x.read(held + get * slot);
+            next_y.read(held + get * slot + one);
+            get = get + 1 == kDepth ? 0 : get + 1;
+        }
+        Pair xh[P], gr[P];
+        // dy is 0 where there is no column, and adds nothing there
+        const float r = next_r;
+        const Pair mu2 = splat(-next_mu), r2 = splat(r);
+        Pair s1 = 0, s2 = 0;
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            const Pair d = next_y[j];
+            Pair wj = w[j];
+            if (kKeep) wj = j % 2 == 0 ? kept[j / 2].x : kept[j / 2].y;
+            xh[j] = mul2(add2(next_x[j], mu2), r2);
+            gr[j] = mul2(d, wj);
+            dw[j] = fma2(d, xh[j], dw[j]);
+            db[j] = add2(db[j], d);
+            s1 = add2(s1, gr[j]);
+            s2 = fma2(gr[j], xh[j], s2);
+        }
+        if constexpr (!kAsync) {
+            x += step * a.x_stride;
+            dy += step * a.grad_out_stride;
+            load(row + step);
+        }
+        load_stats(row + step);
+        const float2 s = group_sum2(g, both(s1), both(s2), red, half);
+        const Pair m1 = splat(-s.x * inv_d * r), m2 = splat(-s.y * inv_d * r);
+#pragma unroll
+        for (int j = 0; j < P; ++j) gr[j] = fma2(xh[j], m2, fma2(gr[j], r2, m1));
+        store_row<T, VEC, E>(out, gr, c);
+    }
+    if constexpr (kAsync) cp_async_wait<0>();        // nothing is to come in the columns' place
     float* part = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.dim;
     auto put = [&](const Pair (&acc)[P], float* to) {
+        if constexpr (VEC >= 4) {
+            if (a.dim % 4 == 0) {
+                // 16 bytes at a time: single values 8 columns apart would meet
+                // in the same banks
+#pragma unroll
+                for (int j = 0; j < P; j += 2) {
+                    const int n = 2 * j / VEC, e = 2 * j % VEC;
+                    const float2 f = unpair(acc[j]), h = unpair(acc[j + 1]);
+                    if (c.ok(n, e))
+                        *reinterpret_cast<float4*>(to + c.at(n) + e) =
+                            make_float4(f.x, f.y, h.x, h.y);
+                }
+                return;
+            }
+        }
 #pragma unroll
         for (int j = 0; j < P; ++j) {
             const float2 f = unpair(acc[j]);
@@ -471,21 +585,34 @@ struct Shape {
     int e, group, per_cta;
 };
 
-Shape shape_for(int64_t dim, bool back) {
+Shape shape_for(int64_t dim, int elem, bool back) {
     const int e = dim <= 2048 ? 8 : dim <= 16 * kNormThreads ? 16 : 32;
     const int group = static_cast<int>((dim + e * 32 - 1) / (e * 32) * 32);
-    int per_cta = (back && e == 8 ? kGradThreads : kNormThreads) / group;
+    int per_cta = (back && e == 8 ? grad_threads(elem) : kNormThreads) / group;
     if (per_cta > 8) per_cta = 8;               // 16 hardware barriers a CTA
     return {e, group, per_cta};
 }
 
-// CTAs: what the registers of an SM hold (launch bounds), or what the rows need.
-int64_t ctas_for(const Shape& s, int64_t rows, bool back) {
+size_t smem_of(const Shape& s, int64_t dim, int elem, int vec, bool back) {
+    const size_t threads = s.group * s.per_cta;
+    const size_t rows = static_cast<size_t>(depth_of(vec, s.e, elem, back ? 2 : 1)) * elem * s.e *
+                        (back ? 2 : 1) * threads;
+    if (!back) return 2 * sizeof(float) * s.e * threads + rows;
+    const size_t kept = s.e > 8 ? sizeof(float) * s.e * threads : 0;
+    const size_t cols = s.per_cta > 1 ? sizeof(float) * s.per_cta * dim : 0;
+    return kept + rows > cols ? kept + rows : cols;
+}
+
+// CTAs: what the registers (launch bounds) and the shared memory of an SM hold,
+// or what the rows need.
+int64_t ctas_for(const Shape& s, int64_t rows, int64_t dim, int elem, int vec, bool back) {
     const int threads = s.group * s.per_cta;
-    const int per_sm = back ? (s.e == 8 ? 2 * kGradThreads / threads : 1)
-                            : (s.e == 32 ? 1 : 2 * kNormThreads / threads);
-    const int64_t per = static_cast<int64_t>(s.per_cta) * (back ? 1 : batch_of(s.e));
-    const int64_t need = rows > 0 ? (rows + per - 1) / per : 1;
+    int per_sm = back ? (s.e == 8 ? grad_ctas(elem) * grad_threads(elem) / threads : 1)
+                      : (s.e == 32 ? 1 : 2 * kNormThreads / threads);
+    const int by_smem =
+        static_cast<int>(225 * 1024 / (smem_of(s, dim, elem, vec, back) + 2048));
+    if (by_smem < per_sm) per_sm = by_smem > 0 ? by_smem : 1;
+    const int64_t need = rows > 0 ? (rows + s.per_cta - 1) / s.per_cta : 1;
     const int64_t most = static_cast<int64_t>(device_sms()) * per_sm;
     return need < most ? need : most;
 }
@@ -507,7 +634,7 @@ cudaError_t launch_e(const NormArgs& a, unsigned grid, int threads, size_t smem,
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     std::call_once(once[dev], [&] {
         set[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        2 * sizeof(float) * E * kNormThreads);
+                                        224 * 1024);
     });
     if (set[dev] != cudaSuccess) return set[dev];
     kernel<<<grid, threads, smem, stream>>>(a);
@@ -516,28 +643,29 @@ cudaError_t launch_e(const NormArgs& a, unsigned grid, int threads, size_t smem,
 
 template <class T, int VEC, bool BACK>
 cudaError_t launch_shape(NormArgs a, cudaStream_t stream) {
-    const Shape s = shape_for(a.dim, BACK);
+    const Shape s = shape_for(a.dim, sizeof(T), BACK);
     a.group_threads = s.group;
-    const unsigned g = static_cast<unsigned>(ctas_for(s, a.n_rows, BACK));
+    const unsigned g =
+        static_cast<unsigned>(ctas_for(s, a.n_rows, a.dim, sizeof(T), VEC, BACK));
     const int threads = s.group * s.per_cta;
-    size_t smem = 0;
-    if (BACK) {
-        const size_t kept = s.e > 8 ? sizeof(float) * s.e * threads : 0;
-        const size_t cols = s.per_cta > 1 ? sizeof(float) * s.per_cta * a.dim : 0;
-        smem = kept > cols ? kept : cols;
-    } else {
-        smem = 2 * sizeof(float) * s.e * threads;
-    }
+    const size_t smem = smem_of(s, a.dim, sizeof(T), VEC, BACK);
     if (s.e == 8) return launch_e<T, VEC, 8, BACK>(a, g, threads, smem, stream);
     if (s.e == 16) return launch_e<T, VEC, 16, BACK>(a, g, threads, smem, stream);
     return launch_e<T, VEC, 32, BACK>(a, g, threads, smem, stream);
 }
 
+// Elements of an access: 16 bytes where every row allows it.
 template <bool BACK>
-cudaError_t dispatch(const NormArgs& a, int act_bytes, cudaStream_t stream) {
+int vec_of(const NormArgs& a, int act_bytes) {
     const bool wide = wide_rows(act_bytes, a.x, a.x_stride) &&
                       wide_rows(act_bytes, a.out, a.out_stride) &&
                       (!BACK || wide_rows(act_bytes, a.grad_out, a.grad_out_stride));
+    return wide ? 16 / act_bytes : 1;
+}
+
+template <bool BACK>
+cudaError_t dispatch(const NormArgs& a, int act_bytes, cudaStream_t stream) {
+    const bool wide = vec_of<BACK>(a, act_bytes) > 1;
     if (act_bytes == 4)
         return wide ? launch_shape<float, 4, BACK>(a, stream)
                     : launch_shape<float, 1, BACK>(a, stream);
@@ -547,8 +675,17 @@ cudaError_t dispatch(const NormArgs& a, int act_bytes, cudaStream_t stream) {
 
 }  // namespace
 
+// The most of any type and alignment.
 int norm_grad_ctas(int64_t n_rows, int64_t dim) {
-    return static_cast<int>(ctas_for(shape_for(dim, true), n_rows, true));
+    int64_t most = 1;
+    for (int elem = 2; elem <= 4; elem += 2) {
+        const Shape s = shape_for(dim, elem, true);
+        for (int vec : {1, 16 / elem}) {
+            const int64_t n = ctas_for(s, n_rows, dim, elem, vec, true);
+            if (n > most) most = n;
+        }
+    }
+    return static_cast<int>(most);
 }
 
 cudaError_t launch_norm(const NormArgs& a, int act_bytes, cudaStream_t stream) {
@@ -559,7 +696,7 @@ cudaError_t launch_norm_grad(const NormArgs& a, int act_bytes, cudaStream_t stre
     return dispatch<true>(a, act_bytes, stream);
 }
 
-cudaError_t launch_norm_grad_reduce(const NormArgs& a, cudaStream_t stream) {
+cudaError_t launch_norm_grad_reduce(const NormArgs& a, int act_bytes, cudaStream_t stream) {
     const int64_t width = 2 * static_cast<int64_t>(a.dim);
     // its blocks may be set up while the partial rows are still being added up
     cudaLaunchConfig_t cfg{};
@@ -571,7 +708,10 @@ cudaError_t launch_norm_grad_reduce(const NormArgs& a, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, norm_grad_reduce_kernel, a, norm_grad_ctas(a.n_rows, a.dim));
+    return cudaLaunchKernelEx(&cfg, norm_grad_reduce_kernel, a, 
+                              static_cast<int>(ctas_for(shape_for(a.dim, act_bytes, true), a.n_rows,
+                                                        a.dim, act_bytes, vec_of<true>(a, act_bytes),
+                                                        true)));
 }
 
 }  // namespace zf

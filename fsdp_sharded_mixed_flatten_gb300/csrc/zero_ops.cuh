@@ -197,12 +197,12 @@ struct NormArgs {
     float eps;
 };
 
-// CTAs of the backward launch, which writes one pair of partial column sums
-// each.
+// CTAs of the backward launch at most, which writes one pair of partial column
+// sums each.
 int norm_grad_ctas(int64_t n_rows, int64_t dim);
 cudaError_t launch_norm(const NormArgs& a, int act_bytes, cudaStream_t stream);
 cudaError_t launch_norm_grad(const NormArgs& a, int act_bytes, cudaStream_t stream);
-cudaError_t launch_norm_grad_reduce(const NormArgs& a, cudaStream_t stream);
+cudaError_t launch_norm_grad_reduce(const NormArgs& a, int act_bytes, cudaStream_t stream);
 
 // --------------------------------------------------- distillation loss ------
 

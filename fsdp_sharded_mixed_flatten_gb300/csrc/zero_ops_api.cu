@@ -333,7 +333,7 @@ ZERO_API int zero_layer_norm_grad(const void* grad_out, const void* x, int32_t a
         return rc;
     if (!params) return ok();
     return cuda_call("layer norm gradient reduction launch",
-                     [&] { return zf::launch_norm_grad_reduce(a, s); });
+                     [&] { return zf::launch_norm_grad_reduce(a, act_bytes, s); });
 }
 
 ZERO_API int zero_distill_loss(const void* logits, int32_t logits_bytes, int64_t n_rows,
