@@ -74,6 +74,21 @@ __device__ __forceinline__ void store16(void* dst, uint4 v, uint64_t policy) {
                  "r"(v.y), "r"(v.z), "r"(v.w), "l"(policy)
                  : "memory");
 }
+// Words beyond shared memory: kept in L2 from the first reading, let go at the
+// second.
+__device__ __forceinline__ uint64_t l2_keep() {
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint4 load16(const void* p, uint64_t policy) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.b32 {%0, %1, %2, %3}, [%4], %5;"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p), "l"(policy)
+                 : "memory");
+    return v;
+}
 __device__ __forceinline__ void cp_async_commit() {
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
@@ -362,14 +377,16 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
         add_to(sl.staged);
         if (i < sl.n) {
             // words beyond shared memory, four loads under way
+            const uint64_t keep = l2_keep();
             const uint4* far = reinterpret_cast<const uint4*>(sl.word(i));
             for (; i + 3 * kWorkers < sl.n; i += 4 * kWorkers, far += 4 * kWorkers) {
-                const uint4 v0 = far[0], v1 = far[kWorkers], v2 = far[2 * kWorkers],
-                            v3 = far[3 * kWorkers];
+                const uint4 v0 = load16(far, keep), v1 = load16(far + kWorkers, keep),
+                            v2 = load16(far + 2 * kWorkers, keep),
+                            v3 = load16(far + 3 * kWorkers, keep);
                 add_words(v0, v1);
                 add_words(v2, v3);
             }
-            for (; i < sl.n; i += kWorkers, far += kWorkers) add_word(*far);
+            for (; i < sl.n; i += kWorkers, far += kWorkers) add_word(load16(far, keep));
         }
         const float2 both = unpair(add2(s0, s1));
         r.s = both.x + both.y;
@@ -622,8 +639,9 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
                     out = reinterpret_cast<uint4*>(dz + sl.first) + i;
                     const uint4* far = reinterpret_cast<const uint4*>(sl.word(i));
                     for (; i + 3 * kWorkers < sl.n; i += 4 * kWorkers) {
-                        const uint4 v0 = far[0], v1 = far[kWorkers], v2 = far[2 * kWorkers],
-                                    v3 = far[3 * kWorkers];
+                        const uint4 v0 = load16(far, policy), v1 = load16(far + kWorkers, policy),
+                                    v2 = load16(far + 2 * kWorkers, policy),
+                                    v3 = load16(far + 3 * kWorkers, policy);
                         store16(out, grad_word(v0), policy);
                         store16(out + kWorkers, grad_word(v1), policy);
                         store16(out + 2 * kWorkers, grad_word(v2), policy);
@@ -632,7 +650,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
                         out += 4 * kWorkers;
                     }
                     for (; i < sl.n; i += kWorkers, far += kWorkers, out += kWorkers)
-                        store16(out, grad_word(*far), policy);
+                        store16(out, grad_word(load16(far, policy)), policy);
                 }
             };
             const bool same_grid = !GRAD || ((reinterpret_cast<uintptr_t>(sl.z) ^
