@@ -56,20 +56,29 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Copies and stores carry an L2 policy: where a row does not fit shared memory,
-// what is not read again leaves L2 first, so that the words that are stay.
-__device__ __forceinline__ uint64_t l2_policy(bool first_out) {
+// Where a row does not fit shared memory (!WHOLE), copies and stores carry an L2
+// policy: what is not read again leaves L2 first, so that the words that are stay.
+__device__ __forceinline__ uint64_t l2_policy() {
     uint64_t p;
-    if (first_out) asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-    else asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
     return p;
 }
+template <bool WHOLE>
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint64_t policy) {
+    if (WHOLE) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+        return;
+    }
     asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst),
                  "l"(src), "l"(policy)
                  : "memory");
 }
+template <bool WHOLE>
 __device__ __forceinline__ void store16(void* dst, uint4 v, uint64_t policy) {
+    if (WHOLE) {
+        *static_cast<uint4*>(dst) = v;
+        return;
+    }
     asm volatile("st.global.L2::cache_hint.v4.b32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(dst), "r"(v.x),
                  "r"(v.y), "r"(v.z), "r"(v.w), "l"(policy)
                  : "memory");
@@ -242,7 +251,8 @@ struct Entry {
 };
 
 // WW warps of workers, which hold the slice, and EW of the teacher's entries.
-template <class T, bool GRAD, int WW, int EW>
+// WHOLE: every word of a row fits the CTA's shared memory.
+template <class T, bool GRAD, int WW, int EW, bool WHOLE>
 __global__ void __launch_bounds__(32 * (WW + EW), WW == kWorkerWarps ? 2 : 4)
 distill_kernel(const __grid_constant__ DistillArgs a) {
     using W = Word<T>;
@@ -266,8 +276,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
     const int64_t stride = gridDim.x / ranks;
     const int top4 = (a.top + 3) / 4 * 4;
     const int section = a.section * kWorkers;            // words of a copy group
-    const uint64_t policy = l2_policy(static_cast<int64_t>(a.stage_words) * ranks * 16 <
-                                      a.vocab * static_cast<int64_t>(sizeof(T)) - 32 * ranks);
+    const uint64_t policy = WHOLE ? 0 : l2_policy();
     const uint32_t my_mem = static_cast<uint32_t>(__cvta_generic_to_shared(mem)) + 16u * tid;
 
     auto entries_of = [&](int number) {
@@ -285,7 +294,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
             const int end = sec == kSections - 1 ? sl.staged
                                                  : min(sl.staged, (sec + 1) * section);
             for (int i = sec * section + tid; i < end; i += kWorkers)
-                cp_async16(my_mem + 16u * (i - tid), sl.word(i), policy);
+                cp_async16<WHOLE>(my_mem + 16u * (i - tid), sl.word(i), policy);
             cp_async_commit();
         }
     };
@@ -375,7 +384,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
         add_to(min(sl.staged, 2 * section));
         cp_async_wait<0>();
         add_to(sl.staged);
-        if (i < sl.n) {
+        if (!WHOLE && i < sl.n) {
             // words beyond shared memory, four loads under way
             const uint64_t keep = l2_keep();
             const uint4* far = reinterpret_cast<const uint4*>(sl.word(i));
@@ -614,18 +623,18 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
                     const int end = GRAD ? min(sl.staged, limit) : 0;
                     for (; i + kWorkers < min(end, n_copy); i += 2 * kWorkers) {
                         const uint4 v0 = at[0], v1 = at[kWorkers];
-                        store16(out, grad_word(v0), policy);
-                        store16(out + kWorkers, grad_word(v1), policy);
-                        cp_async16(to, from, policy);
-                        cp_async16(to + 16 * kWorkers, from + kWorkers, policy);
+                        store16<WHOLE>(out, grad_word(v0), policy);
+                        store16<WHOLE>(out + kWorkers, grad_word(v1), policy);
+                        cp_async16<WHOLE>(to, from, policy);
+                        cp_async16<WHOLE>(to + 16 * kWorkers, from + kWorkers, policy);
                         at += 2 * kWorkers;
                         out += 2 * kWorkers;
                         from += 2 * kWorkers;
                         to += 32 * kWorkers;
                     }
                     for (; i < max(end, min(n_copy, limit)); i += kWorkers) {
-                        if (i < end) store16(out, grad_word(*at), policy);
-                        if (i < n_copy) cp_async16(to, from, policy);
+                        if (i < end) store16<WHOLE>(out, grad_word(*at), policy);
+                        if (i < n_copy) cp_async16<WHOLE>(to, from, policy);
                         at += kWorkers;
                         out += kWorkers;
                         from += kWorkers;
@@ -633,7 +642,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
                     }
                     if (copy) cp_async_commit();
                 }
-                if (GRAD && sl.staged < sl.n) {
+                if (!WHOLE && GRAD && sl.staged < sl.n) {
                     // a shared word beyond the slice's own may have been passed
                     i = (sl.staged - tid + kWorkers - 1) / kWorkers * kWorkers + tid;
                     out = reinterpret_cast<uint4*>(dz + sl.first) + i;
@@ -642,15 +651,15 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
                         const uint4 v0 = load16(far, policy), v1 = load16(far + kWorkers, policy),
                                     v2 = load16(far + 2 * kWorkers, policy),
                                     v3 = load16(far + 3 * kWorkers, policy);
-                        store16(out, grad_word(v0), policy);
-                        store16(out + kWorkers, grad_word(v1), policy);
-                        store16(out + 2 * kWorkers, grad_word(v2), policy);
-                        store16(out + 3 * kWorkers, grad_word(v3), policy);
+                        store16<WHOLE>(out, grad_word(v0), policy);
+                        store16<WHOLE>(out + kWorkers, grad_word(v1), policy);
+                        store16<WHOLE>(out + 2 * kWorkers, grad_word(v2), policy);
+                        store16<WHOLE>(out + 3 * kWorkers, grad_word(v3), policy);
                         far += 4 * kWorkers;
                         out += 4 * kWorkers;
                     }
                     for (; i < sl.n; i += kWorkers, far += kWorkers, out += kWorkers)
-                        store16(out, grad_word(load16(far, policy)), policy);
+                        store16<WHOLE>(out, grad_word(load16(far, policy)), policy);
                 }
             };
             const bool same_grid = !GRAD || ((reinterpret_cast<uintptr_t>(sl.z) ^
@@ -752,10 +761,9 @@ struct Resident {
 
 template <class T, bool GRAD, int WW, int EW>
 cudaError_t launch_shape(DistillArgs a, cudaStream_t stream) {
-    static Resident resident;
+    static Resident resident[2];
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
-    const auto kernel = distill_kernel<T, GRAD, WW, EW>;
     const int64_t row_bytes = a.vocab * static_cast<int64_t>(sizeof(T));
     a.rank_shift = 0;
     while ((1 << a.rank_shift) < a.ranks) ++a.rank_shift;
@@ -763,6 +771,9 @@ cudaError_t launch_shape(DistillArgs a, cudaStream_t stream) {
     const int64_t entries = (static_cast<int64_t>(a.top) + 3) / 4 * 4 * 12 * kRing;
     const int64_t room = (kMostBytes - entries) / 16;
     a.stage_words = static_cast<int32_t>(slice < room ? slice : room);
+    const bool whole = slice <= room;
+    const auto kernel = whole ? distill_kernel<T, GRAD, WW, EW, true>
+                              : distill_kernel<T, GRAD, WW, EW, false>;
     const int per_thread = (a.stage_words + 32 * WW - 1) / (32 * WW);
     a.section = (per_thread + kSections - 1) / kSections;
     cudaLaunchConfig_t cfg{};
@@ -778,7 +789,7 @@ cudaError_t launch_shape(DistillArgs a, cudaStream_t stream) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int clusters = 0;
-    if (cudaError_t e = resident.get(reinterpret_cast<const void*>(kernel), cfg, dev, a.ranks,
+    if (cudaError_t e = resident[whole].get(reinterpret_cast<const void*>(kernel), cfg, dev, a.ranks,
                                      &clusters);
         e != cudaSuccess)
         return e;
