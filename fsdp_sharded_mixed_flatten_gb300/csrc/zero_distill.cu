@@ -42,8 +42,7 @@ namespace {
 constexpr int kMaxCluster = 8;
 constexpr int kSections = 3;                     // copy groups of a row
 constexpr int kRing = 4;                         // rows whose entries are kept
-constexpr int kWorkerWarps = 14;
-constexpr int kEntryWarps = 2;
+constexpr int kRowWarps = 16;                    // of a CTA, two of them an SM
 constexpr int kSmallRow = 24 * 1024;             // rows up to this take CTAs of 8 warps
 constexpr int kMostBytes = 110 * 1024;           // of a CTA: the words and the entries
 constexpr float kInf = __builtin_huge_valf();
@@ -190,8 +189,8 @@ struct Exponent {
 
 // This CTA's slice of a row, elements [lo, hi): n 16-byte words from element
 // `first` on, of which the first `staged` are in shared memory, and single
-// elements before (rank 0: up to the row's first 16-byte boundary) and after
-// them (the last rank).
+// elements before (rank 0: up to the row's first 128-byte boundary) and after
+// them (the last rank): fewer than the workers.
 template <class T>
 struct Slice {
     static constexpr int kV = 16 / sizeof(T);
@@ -201,8 +200,10 @@ struct Slice {
     __device__ Slice(const DistillArgs& a, const T* at, int rank) {
         z = at;
         const int vocab = static_cast<int>(a.vocab);
-        const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(z) % 16) / sizeof(T);
-        const int head = min(vocab, mis == 0 ? 0 : kV - mis);
+        // words from a 128-byte boundary on: a warp's 512 bytes are whole lines
+        // (rows that start 16 bytes off one took 10 % longer)
+        const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(z) % 128) / sizeof(T);
+        const int head = min(vocab, mis == 0 ? 0 : 8 * kV - mis);
         const int words = (vocab - head) / kV;
         const int per = (words + a.ranks - 1) >> a.rank_shift;
         const int v0 = min(rank * per, words);
@@ -253,7 +254,7 @@ struct Entry {
 // WW warps of workers, which hold the slice, and EW of the teacher's entries.
 // WHOLE: every word of a row fits the CTA's shared memory.
 template <class T, bool GRAD, int WW, int EW, bool WHOLE>
-__global__ void __launch_bounds__(32 * (WW + EW), WW == kWorkerWarps ? 2 : 4)
+__global__ void __launch_bounds__(32 * (WW + EW), WW + EW == kRowWarps ? 2 : 4)
 distill_kernel(const __grid_constant__ DistillArgs a) {
     using W = Word<T>;
     constexpr int kV = 16 / sizeof(T);
@@ -322,15 +323,18 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
                 const uint4 zero = make_uint4(0, 0, 0, 0);
                 for (int i = tid; i < sl.n; i += kWorkers)
                     *reinterpret_cast<uint4*>(dz + sl.first + static_cast<int64_t>(i) * kV) = zero;
-                for (int j = tid; j < sl.singles(); j += kWorkers)
-                    dz[sl.single_at(j)] = narrow<T>(0.0f);
+                if (tid < sl.singles()) dz[sl.single_at(tid)] = narrow<T>(0.0f);
             }
         }
         return row;
     };
 
-    // The exponentials of the row held, this worker's part.
+    // The exponentials of the row held, this worker's part; `single`: its single
+    // element, if it has one.
+    float single = 0.0f;
     auto add_up = [&](const Slice<T>& sl) {
+        const bool has_single = tid < sl.singles();
+        single = widen<T>(sl.z[has_single ? sl.single_at(tid) : 0]);
         Running r{-kFar, 0.0f};
         const Pair c2 = pair(a.c, a.c);
         Pair s0 = 0, s1 = 0;
@@ -399,10 +403,9 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
         }
         const float2 both = unpair(add2(s0, s1));
         r.s = both.x + both.y;
-        for (int j = tid; j < sl.singles(); j += kWorkers) {
-            const float x = widen<T>(sl.z[sl.single_at(j)]);
-            r.raise(fminf(ceilf(x * a.c), kFar));
-            r.s += ex2(__fmaf_rn(x, a.c, -r.off));
+        if (has_single) {
+            r.raise(fminf(ceilf(single * a.c), kFar));
+            r.s += ex2(__fmaf_rn(single, a.c, -r.off));
         }
         return warp_join(r);
     };
@@ -529,8 +532,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
             };
             if (worker) {
                 for (int j = tid; j < sl.n; j += kWorkers) m = fmaxf(m, W::top(word_of(j)));
-                for (int j = tid; j < sl.singles(); j += kWorkers)
-                    m = fmaxf(m, widen<T>(sl.z[sl.single_at(j)]));
+                if (tid < sl.singles()) m = fmaxf(m, single);
             }
             ex.off = cluster_all<true>(m, far_red, far_slots[0], rank, ranks);
             float sum = 0.0f;
@@ -544,8 +546,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
                         sum += ex2(ex.log2q(v.x)) + ex2(ex.log2q(v.y));
                     }
                 }
-                for (int j = tid; j < sl.singles(); j += kWorkers)
-                    sum += ex2(ex.log2q(widen<T>(sl.z[sl.single_at(j)])));
+                if (tid < sl.singles()) sum += ex2(ex.log2q(single));
             }
             r.s = cluster_all<false>(sum, far_red, far_slots[1], rank, ranks);
         }
@@ -594,13 +595,12 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
                 t.z[k] = ex2(lq) * f;
                 if (!GRAD) continue;
                 // is any other id the same?
-                bool found = false;
+                int same = 0;
                 for (int j = 0; j < top4; j += 4) {
                     const int4 v = *reinterpret_cast<const int4*>(t.id + j);
-                    found |= (v.x == id && j != k) || (v.y == id && j + 1 != k) ||
-                             (v.z == id && j + 2 != k) || (v.w == id && j + 3 != k);
+                    same += (v.x == id) + (v.y == id) + (v.z == id) + (v.w == id);
                 }
-                if (found) equal[number % kRing] = number;
+                if (same > 1) equal[number % kRing] = number;
             }
             loss = warp_sum(loss);
             if (lane == 0)
@@ -702,10 +702,8 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
                 if (copy) copy_row(next_sl);
             }
             if (GRAD) {
-                for (int j = tid; j < sl.singles(); j += kWorkers) {
-                    const int i = sl.single_at(j);
-                    dz[i] = narrow<T>(live ? ex2(ex.log2q(widen<T>(sl.z[i]))) * f : 0.0f);
-                }
+                if (tid < sl.singles())
+                    dz[sl.single_at(tid)] = narrow<T>(live ? ex2(ex.log2q(single)) * f : 0.0f);
             }
         }
         if (!copy) break;
@@ -805,7 +803,10 @@ cudaError_t launch(DistillArgs a, cudaStream_t stream) {
     const int64_t row_bytes = a.vocab * static_cast<int64_t>(sizeof(T));
     a.ranks = ranks_for(a.n_rows, row_bytes);
     if (row_bytes <= kSmallRow) return launch_shape<T, GRAD, 6, 2>(a, stream);
-    return launch_shape<T, GRAD, kWorkerWarps, kEntryWarps>(a, stream);
+    // more entries than two warps hold cost the row's critical path: with 128 of
+    // them 4096 x 131072 took 435 us, with 32 407
+    if (a.top > 64) return launch_shape<T, GRAD, kRowWarps - 4, 4>(a, stream);
+    return launch_shape<T, GRAD, kRowWarps - 2, 2>(a, stream);
 }
 
 }  // namespace
