@@ -43,8 +43,9 @@ constexpr int kMaxCluster = 8;
 constexpr int kSections = 3;                     // copy groups of a row
 constexpr int kRing = 4;                         // rows whose entries are kept
 constexpr int kRowWarps = 16;                    // of a CTA, two of them an SM
-constexpr int kSmallRow = 24 * 1024;             // rows up to this take CTAs of 8 warps
-constexpr int kMostBytes = 110 * 1024;           // of a CTA: the words and the entries
+constexpr int kSmallRow = 46 * 1024;             // rows up to this take CTAs of 8 warps
+constexpr int kTinyRow = 24 * 1024;              // and up to this of 4
+constexpr int kMostBytes = 110 * 1024;           // of a CTA of 16 warps: words and entries
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kFar = 1e30f;
 constexpr float kNone = -4e30f;                  // off of a sum without terms
@@ -254,7 +255,7 @@ struct Entry {
 // WW warps of workers, which hold the slice, and EW of the teacher's entries.
 // WHOLE: every word of a row fits the CTA's shared memory.
 template <class T, bool GRAD, int WW, int EW, bool WHOLE>
-__global__ void __launch_bounds__(32 * (WW + EW), WW + EW == kRowWarps ? 2 : 4)
+__global__ void __launch_bounds__(32 * (WW + EW), 32 / (WW + EW))
 distill_kernel(const __grid_constant__ DistillArgs a) {
     using W = Word<T>;
     constexpr int kV = 16 / sizeof(T);
@@ -715,11 +716,12 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
     if (!worker) finish(number);
 }
 
-// CTAs of a row: more than one only where rows are few, so that a row's read
-// is spread over the GPU.
+// CTAs of a row: more than one only where the rows leave SMs idle even so.
+// (Several rows a cluster, to even out the last round of 1021 x 32003 in fp32,
+// took 134 us instead of 56: its barrier waits for the gradient's stores.)
 int ranks_for(int64_t rows, int64_t row_bytes) {
     int ranks = 1;
-    while (ranks < kMaxCluster && rows * ranks * 2 <= device_sms() && row_bytes > ranks * 8192)
+    while (ranks < kMaxCluster && rows * ranks <= device_sms() && row_bytes > ranks * 8192)
         ranks *= 2;
     return ranks;
 }
@@ -767,7 +769,7 @@ cudaError_t launch_shape(DistillArgs a, cudaStream_t stream) {
     while ((1 << a.rank_shift) < a.ranks) ++a.rank_shift;
     const int64_t slice = (row_bytes / 16 + a.ranks - 1) / a.ranks;
     const int64_t entries = (static_cast<int64_t>(a.top) + 3) / 4 * 4 * 12 * kRing;
-    const int64_t room = (kMostBytes - entries) / 16;
+    const int64_t room = (kMostBytes * (WW + EW) / kRowWarps - entries) / 16;
     a.stage_words = static_cast<int32_t>(slice < room ? slice : room);
     const bool whole = slice <= room;
     const auto kernel = whole ? distill_kernel<T, GRAD, WW, EW, true>
@@ -796,13 +798,19 @@ cudaError_t launch_shape(DistillArgs a, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// Rows of up to kSmallRow take small CTAs, several to an SM: a row is soon
-// done, and what it costs besides its words overlaps with other rows'.
+// Shorter rows take smaller CTAs, more to an SM, where there are enough of them:
+// what a row costs besides its words then overlaps with more other rows' (8192
+// rows of 4000 bf16: 73 us with CTAs of 8 warps, 50 with 4).
 template <class T, bool GRAD>
 cudaError_t launch(DistillArgs a, cudaStream_t stream) {
     const int64_t row_bytes = a.vocab * static_cast<int64_t>(sizeof(T));
+    const bool many = a.n_rows > 2 * device_sms();
+    a.ranks = 1;
+    if (row_bytes <= kTinyRow && a.top <= 64 && many)
+        return launch_shape<T, GRAD, 3, 1>(a, stream);
+    if (row_bytes <= kSmallRow && a.top <= 128 && many)
+        return launch_shape<T, GRAD, 6, 2>(a, stream);
     a.ranks = ranks_for(a.n_rows, row_bytes);
-    if (row_bytes <= kSmallRow) return launch_shape<T, GRAD, 6, 2>(a, stream);
     // more entries than two warps hold cost the row's critical path: with 128 of
     // them 4096 x 131072 took 435 us, with 32 407
     if (a.top > 64) return launch_shape<T, GRAD, kRowWarps - 4, 4>(a, stream);

@@ -377,12 +377,17 @@ def test_distill(n, vocab, top, pad, offset, dtype, teacher, tau):
     z.check_guard("logits")
 
 
-@pytest.mark.parametrize("vocab", [1000, 50257])
-def test_distill_many_rows(vocab):
-    """More rows than the GPU holds at once; repeats bit for bit."""
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("top", [24, 100, 300])
+@pytest.mark.parametrize("vocab", [1000, 16001, 50257])
+def test_distill_many_rows(vocab, top, dtype):
+    """More rows than the GPU holds at once, in every CTA shape; masked rows
+    among them, rows with equal ids; repeats bit for bit."""
     n = 700
-    z, ids, t, w = _distill_inputs(n, vocab, 24, 0, 0, BF16, BF16, ("many",))
+    z, ids, t, w = _distill_inputs(n, vocab, top, 0, 0, dtype, dtype, ("many",))
     w[::3] = 0.0
+    w[5:60] = 0.0
+    ids[7] = -1
     ref = R.distill(z.t, ids, t, w, 2.0)
     runs = [_run_distill(z.t, ids, t, w, 2.0) for _ in range(3)]
     alone, loss, dz = runs[0]
@@ -392,6 +397,24 @@ def test_distill_many_rows(vocab):
     for r in runs[1:]:
         for a, b in zip(runs[0], r):
             assert torch.equal(_bits(a), _bits(b))
+
+
+def test_distill_teacher_at_the_ends_of_its_range():
+    """Teacher logits of the type's lowest value only (a row of equal ones), far
+    beyond the exponents' range, and one entry at +-inf."""
+    n, vocab, top = 5, 3000, 8
+    z, ids, t, w = _distill_inputs(n, vocab, top, 0, 0, F32, F32, ("teacher",))
+    ids[:] = torch.arange(top, dtype=torch.int32, device="cuda") * 11
+    t[0] = torch.finfo(F32).min
+    t[1] = torch.arange(top, device="cuda") * 1e30
+    t[2, 1:] = torch.finfo(F32).min
+    t[3] = 1e31
+    t[4, 2] = float("-inf")
+    ref = R.distill(z.t, ids, t, w, 0.5)
+    alone, loss, dz = _run_distill(z.t, ids, t, w, 0.5)
+    R.check(alone, ref["loss"], ref["d_loss"], "alone")
+    R.check(loss, ref["loss"], ref["d_loss"], "loss")
+    R.check(dz, ref["grad"], ref["d_grad"], "grad")
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
