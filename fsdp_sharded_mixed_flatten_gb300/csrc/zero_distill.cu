@@ -43,8 +43,6 @@ constexpr int kMaxCluster = 8;
 constexpr int kSections = 3;                     // copy groups of a row
 constexpr int kRing = 4;                         // rows whose entries are kept
 constexpr int kRowWarps = 16;                    // of a CTA, two of them an SM
-constexpr int kSmallRow = 46 * 1024;             // rows up to this take CTAs of 8 warps
-constexpr int kTinyRow = 24 * 1024;              // and up to this of 4
 constexpr int kMostBytes = 110 * 1024;           // of a CTA of 16 warps: words and entries
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kFar = 1e30f;
@@ -253,8 +251,9 @@ struct Entry {
 };
 
 // WW warps of workers, which hold the slice, and EW of the teacher's entries.
-// WHOLE: every word of a row fits the CTA's shared memory.
-template <class T, bool GRAD, int WW, int EW, bool WHOLE>
+// WHOLE: every word of a row fits the CTA's shared memory.  HASH: how equal ids
+// are found.
+template <class T, bool GRAD, int WW, int EW, bool WHOLE, bool HASH>
 __global__ void __launch_bounds__(32 * (WW + EW), 32 / (WW + EW))
 distill_kernel(const __grid_constant__ DistillArgs a) {
     using W = Word<T>;
@@ -434,6 +433,46 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
         return warp_join(r);
     };
 
+    // Whether an id of this thread's entries is another entry's too, by hashing:
+    // every entry puts its number into a hashed place and reads who is there:
+    // itself, an equal id, or another one; the last try again in a second table,
+    // and what is left even then (1 of 100) compares with all.
+    // The tables lie where row number + 2 will have its entries: those of row
+    // number - 2 are done with, and a barrier of the row comes before either.
+    auto any_equal_hashed = [&](const Entries& t, int number) {
+        bool same = false;
+        uint16_t* table = reinterpret_cast<uint16_t*>(entries_of(number + 2).id);
+        const uint32_t size = 3 * static_cast<uint32_t>(top4);       // of one table
+        uint32_t open = 0xFFFFFFFFu;                                 // a bit for each entry
+#pragma unroll
+        for (int stage = 0; stage < 2; ++stage) {
+            auto place = [&](int32_t id) {
+                const uint32_t h = static_cast<uint32_t>(id) * (stage == 0 ? 2654435761u : 2246822519u);
+                return table + stage * size + __umulhi(h, size);
+            };
+            for (int k = et, r = 0; k < a.top; k += kEntryThreads, ++r) {
+                const int32_t id = t.id[k];
+                if (id < 0) open &= ~(1u << r);
+                if ((open >> r) & 1u) *place(id) = static_cast<uint16_t>(k);
+            }
+            if (EW == 1) __syncwarp();
+            else asm volatile("bar.sync 2, %0;" ::"n"(kEntryThreads) : "memory");
+            for (int k = et, r = 0; k < a.top; k += kEntryThreads, ++r) {
+                if (!((open >> r) & 1u)) continue;
+                const int32_t id = t.id[k];
+                const int there = *place(id);
+                const bool equal_id = there != k && t.id[there] == id;
+                same |= equal_id;
+                if (there == k || equal_id) open &= ~(1u << r);
+            }
+        }
+        for (int k = et, r = 0; k < a.top; k += kEntryThreads, ++r) {
+            if (!((open >> r) & 1u)) continue;
+            for (int j = 0; j < a.top; ++j) same |= j != k && t.id[j] == t.id[k];
+        }
+        return same;
+    };
+
     // This warp's sum of row `number` to the CTAs of the cluster.
     auto publish = [&](const Running& r, int number) {
         if (lane < ranks) {
@@ -594,8 +633,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
                 if (p != 0.0f) loss += p * ((l2 - log_t) - (lq - log_s));
                 t.l2[k] = tau_w * p;
                 t.z[k] = ex2(lq) * f;
-                if (!GRAD) continue;
-                // is any other id the same?
+                if (!GRAD || HASH) continue;
                 int same = 0;
                 for (int j = 0; j < top4; j += 4) {
                     const int4 v = *reinterpret_cast<const int4*>(t.id + j);
@@ -603,6 +641,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
                 }
                 if (same > 1) equal[number % kRing] = number;
             }
+            if (GRAD && HASH && any_equal_hashed(t, number)) equal[number % kRing] = number;
             loss = warp_sum(loss);
             if (lane == 0)
                 cluster.map_shared_rank(losses[number % kRing], 0)[rank * EW + warp - WW] = loss;
@@ -759,9 +798,23 @@ struct Resident {
     }
 };
 
+// Bytes of a row's words in the shared memory of a CTA of `warps`, beside the entries.
+int64_t room_for(int warps, int64_t top) {
+    return (kMostBytes * warps / kRowWarps - (top + 3) / 4 * 4 * 12 * kRing) / 16 * 16;
+}
+
+// Whether a kernel finds equal ids by hashing: from 64 steps of comparing a
+// thread on.  8192 rows of 4000 bf16 in us, comparing / hashing: 64 entries 58 / 60,
+// 128 entries 86 / 77, 256 entries 168 / 119.  Not where words are read again, with
+// time to compare meanwhile: 4096 x 131072 with 256 entries 461 / 495.
+bool hashes(int entry_warps, int64_t top, bool whole) {
+    const int64_t rounds = (top + 32 * entry_warps - 1) / (32 * entry_warps);
+    return whole && rounds * ((top + 3) / 4) >= 64;
+}
+
 template <class T, bool GRAD, int WW, int EW>
 cudaError_t launch_shape(DistillArgs a, cudaStream_t stream) {
-    static Resident resident[2];
+    static Resident resident[3];
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
     const int64_t row_bytes = a.vocab * static_cast<int64_t>(sizeof(T));
@@ -769,11 +822,23 @@ cudaError_t launch_shape(DistillArgs a, cudaStream_t stream) {
     while ((1 << a.rank_shift) < a.ranks) ++a.rank_shift;
     const int64_t slice = (row_bytes / 16 + a.ranks - 1) / a.ranks;
     const int64_t entries = (static_cast<int64_t>(a.top) + 3) / 4 * 4 * 12 * kRing;
-    const int64_t room = (kMostBytes * (WW + EW) / kRowWarps - entries) / 16;
+    const int64_t room = room_for(WW + EW, a.top) / 16;
     a.stage_words = static_cast<int32_t>(slice < room ? slice : room);
     const bool whole = slice <= room;
-    const auto kernel = whole ? distill_kernel<T, GRAD, WW, EW, true>
-                              : distill_kernel<T, GRAD, WW, EW, false>;
+    auto kernel = distill_kernel<T, GRAD, WW, EW, true, false>;
+    int which = 0;
+    if constexpr (WW + EW == kRowWarps) {        // smaller CTAs take whole rows alone
+        if (!whole) {
+            kernel = distill_kernel<T, GRAD, WW, EW, false, false>;
+            which = 1;
+        }
+    }
+    if constexpr (GRAD && WW != kRowWarps - 2) {     // that one has 64 entries at most
+        if (hashes(EW, a.top, whole)) {
+            kernel = distill_kernel<T, GRAD, WW, EW, true, true>;
+            which = 2;
+        }
+    }
     const int per_thread = (a.stage_words + 32 * WW - 1) / (32 * WW);
     a.section = (per_thread + kSections - 1) / kSections;
     cudaLaunchConfig_t cfg{};
@@ -789,8 +854,8 @@ cudaError_t launch_shape(DistillArgs a, cudaStream_t stream) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int clusters = 0;
-    if (cudaError_t e = resident[whole].get(reinterpret_cast<const void*>(kernel), cfg, dev, a.ranks,
-                                     &clusters);
+    if (cudaError_t e = resident[which].get(reinterpret_cast<const void*>(kernel), cfg, dev,
+                                               a.ranks, &clusters);
         e != cudaSuccess)
         return e;
     const int64_t n = a.n_rows < clusters ? a.n_rows : clusters;
@@ -806,9 +871,9 @@ cudaError_t launch(DistillArgs a, cudaStream_t stream) {
     const int64_t row_bytes = a.vocab * static_cast<int64_t>(sizeof(T));
     const bool many = a.n_rows > 2 * device_sms();
     a.ranks = 1;
-    if (row_bytes <= kTinyRow && a.top <= 64 && many)
+    if (row_bytes <= room_for(4, a.top) && many)
         return launch_shape<T, GRAD, 3, 1>(a, stream);
-    if (row_bytes <= kSmallRow && a.top <= 128 && many)
+    if (row_bytes <= room_for(8, a.top) && many)
         return launch_shape<T, GRAD, 6, 2>(a, stream);
     a.ranks = ranks_for(a.n_rows, row_bytes);
     // more entries than two warps hold cost the row's critical path: with 128 of

@@ -399,6 +399,24 @@ def test_distill_many_rows(vocab, top, dtype):
             assert torch.equal(_bits(a), _bits(b))
 
 
+@pytest.mark.parametrize("vocab,top", [(4000, 128), (20000, 130), (50257, 200)])
+def test_distill_equal_ids_among_many(vocab, top):
+    """Rows with more entries than are compared one by one: all distinct, two of
+    one id at the ends, every id twice, one id only."""
+    n = 640
+    z, ids, t, w = _distill_inputs(n, vocab, top, 0, 0, BF16, F32, ("equal",))
+    ids[:] = torch.arange(top, dtype=torch.int32, device="cuda") * 29 \
+        + torch.arange(n, dtype=torch.int32, device="cuda")[:, None] % 97
+    ids %= vocab
+    ids[1::4, -1] = ids[1::4, 0]
+    ids[2::4, 1::2] = ids[2::4, 0::2]
+    ids[3::4] = ids[3::4, :1]
+    ref = R.distill(z.t, ids, t, w, 1.0)
+    _, loss, dz = _run_distill(z.t, ids, t, w, 1.0)
+    R.check(loss, ref["loss"], ref["d_loss"], "loss")
+    R.check(dz, ref["grad"], ref["d_grad"], "grad_logits")
+
+
 def test_distill_teacher_at_the_ends_of_its_range():
     """Teacher logits of the type's lowest value only (a row of equal ones), far
     beyond the exponents' range, and one entry at +-inf."""
