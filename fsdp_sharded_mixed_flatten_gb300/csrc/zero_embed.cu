@@ -35,27 +35,68 @@ __device__ __forceinline__ int64_t ld_id(const void* ids, int id64, int64_t t) {
                 : static_cast<int64_t>(static_cast<const int32_t*>(ids)[t]);
 }
 
-template <class W, class Y, int VEC>
+// A warp takes R tokens and 32 N packs of columns: R N loads are under way at
+// once, without conditions (an id outside the table reads row 0, a column beyond
+// the row column 0).  One element a thread, its place found by division, took
+// 58.7 us for 16384 x 1259 in fp32 from an odd element on, so it takes 29.7 (5.6 TB/s);
+// 16384 x 768 bf16 8.7 us instead of 12.8.
+template <class W, class Y, int VEC, int R, int N>
 __global__ void __launch_bounds__(256) embed_kernel(const __grid_constant__ EmbedArgs a) {
-    const int64_t per_row = a.dim / VEC;
-    const int64_t n = a.n_tokens * per_row;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
-         i += step) {
-        const int64_t t = i / per_row, col = (i - t * per_row) * VEC;
-        const int64_t id = ld_id(a.ids, a.id64, t);
-        float y[VEC];
-        if (id >= 0 && id < a.vocab) {
-            const Pack<W, VEC> p =
-                ld_pack<W, VEC>(static_cast<const W*>(a.weight) + id * a.dim + col);
+    const int lane = threadIdx.x;
+    const int64_t per_cta = R * static_cast<int64_t>(blockDim.y);
+    const int64_t width = 32 * N * VEC;
+    for (int64_t col0 = blockIdx.y * width; col0 < a.dim; col0 += gridDim.y * width) {
+        for (int64_t t0 = blockIdx.x * per_cta + R * threadIdx.y; t0 < a.n_tokens;
+             t0 += gridDim.x * per_cta) {
+            int64_t id[R];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) y[e] = widen<W>(p.x[e]) * a.scale;
-        } else {
+            for (int r = 0; r < R; ++r)
+                id[r] = ld_id(a.ids, a.id64, t0 + r < a.n_tokens ? t0 + r : a.n_tokens - 1);
+            Pack<W, VEC> p[R][N];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) y[e] = 0.0f;
+            for (int r = 0; r < R; ++r) {
+                const bool known = id[r] >= 0 && id[r] < a.vocab;
+                const W* row = static_cast<const W*>(a.weight) + (known ? id[r] : 0) * a.dim;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const int64_t c = col0 + (j * 32 + lane) * VEC;
+                    p[r][j] = ld_pack<W, VEC>(row + (c < a.dim ? c : 0));
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (t0 + r >= a.n_tokens) break;
+                const bool known = id[r] >= 0 && id[r] < a.vocab;
+                Y* out = static_cast<Y*>(a.out) + (t0 + r) * a.out_stride;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const int64_t c = col0 + (j * 32 + lane) * VEC;
+                    if (c >= a.dim) continue;
+                    float y[VEC];
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        y[e] = known ? widen<W>(p[r][j].x[e]) * a.scale : 0.0f;
+                    st_pack<Y, VEC>(out + c, pack<Y, VEC>(y));
+                }
+            }
         }
-        st_pack<Y, VEC>(static_cast<Y*>(a.out) + t * a.out_stride + col, pack<Y, VEC>(y));
     }
+}
+
+// Zeros to n elements, by a warp: 16 bytes a lane from the first boundary on
+// (by single elements, 20000 tokens into 50257 bf16 rows of 768
+// from an odd element on took 79 us, so 70).
+template <class G>
+__device__ __forceinline__ void zero_span(G* to, int64_t n, int lane) {
+    constexpr int kV = 16 / sizeof(G);
+    const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(to) % 16) / sizeof(G);
+    const int64_t head = mis == 0 ? 0 : n < kV - mis ? n : kV - mis;
+    const int64_t words = (n - head) / kV;
+    if (lane < head) to[lane] = narrow<G>(0.0f);
+    for (int64_t i = lane; i < words; i += 32)
+        reinterpret_cast<uint4*>(to + head)[i] = make_uint4(0, 0, 0, 0);
+    const int64_t tail = head + words * kV;
+    if (lane < n - tail) to[tail + lane] = narrow<G>(0.0f);
 }
 
 // ---------------------------------------------------------------- sort ------
@@ -239,7 +280,7 @@ __device__ void sort_cluster(const EmbedGradArgs& a, const Workspace& ws, SortSm
 }
 
 // Zeros to the rows of dW in [lo, hi) that no token has.
-template <class G, int VEC>
+template <class G>
 __device__ void fill_unused(const EmbedGradArgs& a, int64_t lo, int64_t hi, uint32_t* used) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int64_t r0 = lo; r0 < hi; r0 += kFillRows) {
@@ -262,20 +303,14 @@ __device__ void fill_unused(const EmbedGradArgs& a, int64_t lo, int64_t hi, uint
             }
         }
         __syncthreads();
-        float zero[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) zero[e] = 0.0f;
-        const Pack<G, VEC> z = pack<G, VEC>(zero);
         for (int64_t r = warp; r < n; r += kSortWarps) {
             if ((used[r >> 5] >> (r & 31)) & 1u) continue;
-            G* row = static_cast<G*>(a.grad_weight) + (r0 + r) * a.dim;
-            for (int64_t c = static_cast<int64_t>(lane) * VEC; c < a.dim; c += 32 * VEC)
-                st_pack<G, VEC>(row + c, z);
+            zero_span(static_cast<G*>(a.grad_weight) + (r0 + r) * a.dim, a.dim, lane);
         }
     }
 }
 
-template <class G, int VEC>
+template <class G>
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads)
 embed_sort_kernel(const __grid_constant__ EmbedGradArgs a) {
     __shared__ SortSmem sm;
@@ -290,7 +325,7 @@ embed_sort_kernel(const __grid_constant__ EmbedGradArgs a) {
         const int64_t ctas = gridDim.x - kSortCtas, i = blockIdx.x - kSortCtas;
         const int64_t per = (a.vocab + ctas - 1) / ctas;
         const int64_t lo = i * per, hi = lo + per < a.vocab ? lo + per : a.vocab;
-        if (lo < hi) fill_unused<G, VEC>(a, lo, hi, reinterpret_cast<uint32_t*>(&sm));
+        if (lo < hi) fill_unused<G>(a, lo, hi, reinterpret_cast<uint32_t*>(&sm));
     }
 }
 
@@ -517,6 +552,8 @@ constexpr int kBucketThreads = 512;
 constexpr int kBucketWarps = kBucketThreads / 32;
 constexpr int kTokenBits = 14;
 constexpr int64_t kBucketTokens = 1 << kTokenBits;
+constexpr int64_t kFewTokens = 8192;                 // up to here always
+constexpr int64_t kBucketElements = 10 << 20;        // and up to here beyond
 constexpr int kBucketSmem = 160 * 1024;              // beside 33 KB of static memory
 
 struct Bucket {
@@ -549,11 +586,18 @@ Bucket bucket_for(int64_t n_tokens, int64_t vocab, int64_t dim, int widest) {
     return b;
 }
 
-// Whether a gradient takes the one launch: the list of a bucket could hold all
-// tokens.  Measured against the sort: 8192 x 768 tokens into 50257 rows, added
-// to the table: 33 us with the sort.
+// Whether a gradient takes the one launch.  Every CTA reads all ids, and above
+// kFewTokens its lists leave an SM one CTA; what that costs grows with the
+// elements.  In us, buckets / sort, added to a table of 50257 bf16 rows:
+//   tokens    dim 128      768          2048         4096
+//    4096     12.7 / 29.1  14.8 / 29.1  18.4 / 29.8   28.0 / 35.4
+//    8192     16.9 / 29.8  23.0 / 30.0  34.1 / 37.9   55.1 / 52.4
+//   12288     22.1 / 33.1  32.3 / 34.5  56.0 / 45.5  102.6 / 63.3
+//   16384     28.1 / 35.3  39.9 / 37.3  80.5 / 55.5  137.5 / 74.4
+// (4096 fp32 columns: 6144 tokens 60.2 / 69.9, 8192 92.8 / 86.5).
 bool takes_buckets(int64_t n_tokens, int64_t vocab, int64_t dim) {
-    if (n_tokens > kBucketTokens) return false;
+    if (n_tokens > kBucketTokens || (n_tokens > kFewTokens && n_tokens * dim > kBucketElements))
+        return false;
     const Bucket b = bucket_for(n_tokens, vocab, dim, 4);
     return b.rows < (1 << (32 - kTokenBits)) && b.smem <= kBucketSmem &&
            dim <= 65535 * int64_t{bucket_cols(4)};
@@ -848,15 +892,16 @@ cudaError_t embed(const EmbedArgs& a, int want, cudaStream_t stream) {
     const bool vec = aligned_to(a.weight, want * static_cast<int64_t>(sizeof(W))) &&
                      aligned_to(a.out, want * static_cast<int64_t>(sizeof(Y))) &&
                      a.dim % want == 0 && a.out_stride % want == 0;
-    const int64_t n = a.n_tokens * (vec ? a.dim / want : a.dim);
-    const int64_t most = static_cast<int64_t>(device_sms()) * 64;
-    const int64_t blocks = (n + 255) / 256;
-    const unsigned g = static_cast<unsigned>(blocks < most ? blocks : most);
     constexpr int kV = sizeof(W) == 2 && sizeof(Y) == 2 ? 8 : 4;
+    const int tokens = 8 * (vec ? 4 : 2), width = 32 * (vec ? kV : 4);
+    const int64_t most = static_cast<int64_t>(device_sms()) * 64;
+    const int64_t x = (a.n_tokens + tokens - 1) / tokens, y = (a.dim + width - 1) / width;
+    const dim3 grid(static_cast<unsigned>(x < most ? x : most),
+                    static_cast<unsigned>(y < 65535 ? y : 65535));
     if (vec) {
-        embed_kernel<W, Y, kV><<<g, 256, 0, stream>>>(a);
+        embed_kernel<W, Y, kV, 4, 1><<<grid, dim3(32, 8), 0, stream>>>(a);
     } else {
-        embed_kernel<W, Y, 1><<<g, 256, 0, stream>>>(a);
+        embed_kernel<W, Y, 1, 2, 4><<<grid, dim3(32, 8), 0, stream>>>(a);
     }
     return cudaGetLastError();
 }
@@ -925,15 +970,8 @@ cudaError_t launch_embed_sort(const EmbedGradArgs& a, int grad_weight_bytes, cud
         clusters += static_cast<int>(need < most ? need : most);
     }
     const unsigned g = static_cast<unsigned>(clusters * kSortCtas);
-    const int want = 16 / grad_weight_bytes;
-    const bool vec = aligned_to(a.grad_weight, 16) && a.dim % want == 0;
-    if (grad_weight_bytes == 4) {
-        if (vec) embed_sort_kernel<float, 4><<<g, kSortThreads, 0, stream>>>(a);
-        else embed_sort_kernel<float, 1><<<g, kSortThreads, 0, stream>>>(a);
-    } else {
-        if (vec) embed_sort_kernel<uint16_t, 8><<<g, kSortThreads, 0, stream>>>(a);
-        else embed_sort_kernel<uint16_t, 1><<<g, kSortThreads, 0, stream>>>(a);
-    }
+    if (grad_weight_bytes == 4) embed_sort_kernel<float><<<g, kSortThreads, 0, stream>>>(a);
+    else embed_sort_kernel<uint16_t><<<g, kSortThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
