@@ -406,7 +406,7 @@ norm_grad_kernel(const __grid_constant__ NormArgs a) {
     constexpr int kDepth = depth_of(VEC, E, sizeof(T), 2);
     constexpr bool kAsync = kDepth > 0;
     extern __shared__ __align__(16) char dyn[];
-    float* cols = reinterpret_cast<float*>(dyn);     // [groups][dim] where a CTA has several;
+    float* cols = reinterpret_cast<float*>(dyn);     // [groups][dim] at the end;
                                                      // before, the weight and the rows
     __shared__ float red[2][2][kNormWarps];
     int half = 0;
@@ -525,7 +525,10 @@ norm_grad_kernel(const __grid_constant__ NormArgs a) {
             if (c.ok(n1, (2 * j + 1) % VEC)) to[c.at(n1) + (2 * j + 1) % VEC] = f.y;
         }
     };
-    if (g.per_cta == 1) {
+    // no other CTA's partial rows: the sums themselves (not where a thread holds 32
+    // columns: one row of 16384 bf16 25.4 us, with the second launch 21.3)
+    const bool alone = E < 32 && gridDim.x == 1;
+    if (g.per_cta == 1 && !alone) {
         put(dw, part);
         put(db, part + a.dim);
         return;
@@ -538,7 +541,9 @@ norm_grad_kernel(const __grid_constant__ NormArgs a) {
         for (int k = threadIdx.x; k < a.dim; k += blockDim.x) {
             float t = 0.0f;
             for (int i = 0; i < g.per_cta; ++i) t += cols[i * a.dim + k];
-            part[which * a.dim + k] = t;
+            void* to = which == 0 ? a.grad_weight : a.grad_bias;
+            if (!alone) part[which * a.dim + k] = t;
+            else if (to != nullptr) st_param(to, a.param_f32, k, t);
         }
     }
 }
@@ -599,8 +604,19 @@ size_t smem_of(const Shape& s, int64_t dim, int elem, int vec, bool back) {
                         (back ? 2 : 1) * threads;
     if (!back) return 2 * sizeof(float) * s.e * threads + rows;
     const size_t kept = s.e > 8 ? sizeof(float) * s.e * threads : 0;
-    const size_t cols = s.per_cta > 1 ? sizeof(float) * s.per_cta * dim : 0;
+    const size_t cols = sizeof(float) * s.per_cta * dim;
     return kept + rows > cols ? kept + rows : cols;
+}
+
+// Rows of the backward pass that one CTA takes by itself: what it adds up are
+// the sums, and the second launch is saved.  Up to 2048 columns 8 rounds of its
+// groups and 24576 elements (one launch / two, in us: bf16 32 x 768 9.6 / 11.1,
+// 64 x 768 13.0 / 11.8, fp32 32 x 768 in 16 rounds 14.8 / 11.6), beyond one round
+// (8 x 4096 bf16 in four 12.8 / 11.6).  The short ones are held up by the host.
+int64_t rows_alone(const Shape& s, int64_t dim) {
+    if (s.e > 8) return s.per_cta;
+    const int64_t by_size = 24576 / dim;
+    return by_size < 8 * s.per_cta ? by_size : 8 * s.per_cta;
 }
 
 // CTAs: what the registers (launch bounds) and the shared memory of an SM hold,
@@ -612,7 +628,8 @@ int64_t ctas_for(const Shape& s, int64_t rows, int64_t dim, int elem, int vec, b
     const int by_smem =
         static_cast<int>(225 * 1024 / (smem_of(s, dim, elem, vec, back) + 2048));
     if (by_smem < per_sm) per_sm = by_smem > 0 ? by_smem : 1;
-    const int64_t need = rows > 0 ? (rows + s.per_cta - 1) / s.per_cta : 1;
+    const int64_t few = back ? rows_alone(s, dim) : 0;
+    const int64_t need = rows > few ? (rows + s.per_cta - 1) / s.per_cta : 1;
     const int64_t most = static_cast<int64_t>(device_sms()) * per_sm;
     return need < most ? need : most;
 }
@@ -698,6 +715,9 @@ cudaError_t launch_norm_grad(const NormArgs& a, int act_bytes, cudaStream_t stre
 
 cudaError_t launch_norm_grad_reduce(const NormArgs& a, int act_bytes, cudaStream_t stream) {
     const int64_t width = 2 * static_cast<int64_t>(a.dim);
+    const Shape s = shape_for(a.dim, act_bytes, true);
+    const int64_t parts = ctas_for(s, a.n_rows, a.dim, act_bytes, vec_of<true>(a, act_bytes), true);
+    if (parts == 1 && s.e < 32) return cudaSuccess;      // the sums themselves are there
     // its blocks may be set up while the partial rows are still being added up
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>((width + 31) / 32));
@@ -708,10 +728,7 @@ cudaError_t launch_norm_grad_reduce(const NormArgs& a, int act_bytes, cudaStream
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, norm_grad_reduce_kernel, a, 
-                              static_cast<int>(ctas_for(shape_for(a.dim, act_bytes, true), a.n_rows,
-                                                        a.dim, act_bytes, vec_of<true>(a, act_bytes),
-                                                        true)));
+    return cudaLaunchKernelEx(&cfg, norm_grad_reduce_kernel, a, static_cast<int>(parts));
 }
 
 }  // namespace zf
