@@ -70,6 +70,8 @@ def library_path() -> str:
 def load() -> ctypes.CDLL:
     """Load the CUDA library; raise if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
