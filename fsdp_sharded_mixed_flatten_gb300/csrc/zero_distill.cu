@@ -22,6 +22,12 @@
 // cluster barrier waits for the gradient's stores to arrive: 4096 x 50257 took
 // 221 us with clusters of one CTA and a split barrier).
 //
+// Measured, loss and gradient: 4096 x 50257 bf16 with 64 entries 141 us (5.8 TB/s),
+// 4096 x 25000 fp32 6.2 TB/s, 8192 x 131072 bf16 with 128 entries 854 us (5.0 TB/s; its
+// words beyond shared memory come from L2 a second time), 1021 x 32003 fp32
+// 55.5 us (4.7 TB/s: 3.4 rounds of 304 CTAs take as long as 4), 16 x 50257 the loss
+// alone 8.2 us, as long as the host takes for a call.
+//
 // Exponentials are 2^(z c - M), c = log2(e) / tau: one fused multiply-add and
 // one ex2 each.  M is an integer, ceil(c max z) of what a thread has seen, so
 // that moving from one M to another scales by an exact power of two.  Rows
@@ -44,6 +50,7 @@ constexpr int kSections = 3;                     // copy groups of a row
 constexpr int kRing = 4;                         // rows whose entries are kept
 constexpr int kRowWarps = 16;                    // of a CTA, two of them an SM
 constexpr int kMostBytes = 110 * 1024;           // of a CTA of 16 warps: words and entries
+constexpr int kShortRow = 48 * 1024;             // rows up to this take one CTA
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kFar = 1e30f;
 constexpr float kNone = -4e30f;                  // off of a sum without terms
@@ -755,14 +762,22 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
     if (!worker) finish(number);
 }
 
-// CTAs of a row: more than one only where the rows leave SMs idle even so.
+// CTAs of a row: more than one only where the rows leave SMs idle even so, and a
+// row is long enough to pay for the cluster's barriers.  In us by CTAs of a row (1,
+// 2, 4, 8), bf16, 32 entries:
+//     8 rows of  18000   8.4   9.2   9.2   9.0
+//     8 rows of  50257  10.9  10.9  10.3   9.1
+//    38 rows of  50257  11.0  11.0  10.9  14.8
+//    76 rows of  50257  11.0  12.7  14.9  19.1
+//     8 rows of 131072  17.2  15.0  10.9  10.3
+//    76 rows of 131072  19.0  17.0  19.0  21.2
 // (Several rows a cluster, to even out the last round of 1021 x 32003 in fp32,
 // took 134 us instead of 56: its barrier waits for the gradient's stores.)
 int ranks_for(int64_t rows, int64_t row_bytes) {
+    if (row_bytes <= kShortRow) return 1;
     int ranks = 1;
-    while (ranks < kMaxCluster && rows * ranks <= device_sms() && row_bytes > ranks * 8192)
-        ranks *= 2;
-    return ranks;
+    while (ranks < kMaxCluster && rows * ranks * 2 <= device_sms()) ranks *= 2;
+    return ranks == 2 && row_bytes <= kMostBytes ? 1 : ranks;
 }
 
 // Clusters of a launch's shape that the GPU holds at once; the last shapes
@@ -864,8 +879,10 @@ cudaError_t launch_shape(DistillArgs a, cudaStream_t stream) {
 }
 
 // Shorter rows take smaller CTAs, more to an SM, where there are enough of them:
-// what a row costs besides its words then overlaps with more other rows' (8192
-// rows of 4000 bf16: 73 us with CTAs of 8 warps, 50 with 4).
+// what a row costs besides its words then overlaps with more other rows'.  1500
+// rows of 4000 bf16: 14.8 us with CTAs of 4 warps, 25.3 with 16 (8192 rows: 48, with
+// 8 warps 73); 1500 rows of 18000: 29.8 us with 8 warps, 35.6 with 16.  64 rows of 9000
+// with 256 entries: 14.2 us with 4 warps, 10.9 with 16.
 template <class T, bool GRAD>
 cudaError_t launch(DistillArgs a, cudaStream_t stream) {
     const int64_t row_bytes = a.vocab * static_cast<int64_t>(sizeof(T));
@@ -876,8 +893,9 @@ cudaError_t launch(DistillArgs a, cudaStream_t stream) {
     if (row_bytes <= room_for(8, a.top) && many)
         return launch_shape<T, GRAD, 6, 2>(a, stream);
     a.ranks = ranks_for(a.n_rows, row_bytes);
-    // more entries than two warps hold cost the row's critical path: with 128 of
-    // them 4096 x 131072 took 435 us, with 32 407
+    // more entries than two warps hold cost the row's critical path: 4096 x 50257
+    // with 128 of them 148 us with four warps, 158 with two (with 64 of 131072
+    // 427 and 415)
     if (a.top > 64) return launch_shape<T, GRAD, kRowWarps - 4, 4>(a, stream);
     return launch_shape<T, GRAD, kRowWarps - 2, 2>(a, stream);
 }
