@@ -7,13 +7,17 @@
 // A row lives in the registers of a group of threads, E elements each, so that
 // every byte of x, dy and the output crosses memory once.  A CTA holds several
 // groups, which work through the rows independently; the next rows' loads are
-// under way while a row is worked on (cp.async to shared memory, each thread
-// its own words, so that no barrier separates copy and use; a row takes about
-// 2 us from load to store, and one row ahead kept a third of memory's rate).  The parameters stay in registers or, to
-// leave room for more warps, in shared memory (each thread its own columns: no
-// barrier), and the backward pass's columns of dw and db in registers over all
-// rows; each CTA writes one pair of partial rows, which a second launch adds up
-// in CTA order.
+// under way while a row is worked on (cp.async to shared memory, each thread its
+// own words, so that no barrier separates copy and use).  The parameters stay in
+// registers or, to leave room for more warps, in shared memory (each thread its
+// own columns: no barrier), and the backward pass's columns of dw and db in
+// registers over all rows; each CTA writes one pair of partial rows, which a
+// second launch adds up in CTA order.
+//
+// Bound by memory where rows are many: forward of 16384 x 4096 bf16 50 us (5.4 TB/s),
+// backward of 8192 x 8192 bf16 78 us (5.1 TB/s), of 8192 x 768 bf16 15 us (2.5 TB/s: the
+// launch, the first rows and the second launch are most of it).  Few rows take as
+// long as the host's call: 8 x 768 7.2 us forward, 9.5 us backward.
 //
 // The variance is taken about a mean at every step: a warp's squares about the
 // warp's mean, then sum (M2_w + n_w (mean_w - mu)^2) over the warps of the
@@ -30,9 +34,9 @@ constexpr int kNormThreads = 512;      // of a CTA, but for the backward pass at
 constexpr int kNormWarps = 24;         // of a CTA, at most
 
 // Of the backward pass at E = 8: one CTA of 768 threads an SM with bf16 (80
-// registers), two of 256 with fp32 (128), whose rows take twice as many.
-__host__ __device__ constexpr int grad_threads(int elem) { return elem == 2 ? 768 : 256; }
-__host__ __device__ constexpr int grad_ctas(int elem) { return elem == 2 ? 1 : 2; }
+// registers), of 512 with fp32 (128), whose rows take twice as many.  8192 x 768:
+// bf16 15.2 us, with two CTAs of 256 17.2; fp32 20.9 us, with two of 256 23.2.
+__host__ __device__ constexpr int grad_threads(int elem) { return elem == 2 ? 768 : 512; }
 
 // The group of threads that holds a row.
 struct Group {
@@ -51,12 +55,16 @@ struct Group {
 };
 
 // Rows under way at a time in shared memory (0: one, in registers), for `arrays`
-// matrices: as far as shared memory goes, with the CTAs an SM that the launch
-// bounds allow.
+// matrices.  In us by rows under way (1, 2, 3, 4):
+//   forward of 16384 rows: 768 bf16 20.7, 17.1, 17.1, 17.2; 2048 fp32 58.8, 45.8,
+//     48.6, 50.8; 4096 bf16 65.0, 51.0, 80.0 (no room for a second CTA), 71.9;
+//     8192 fp32 180.9, 179.2, 164.9, 165.8
+//   backward of 8192 rows: 768 bf16 15.9, 14.8, 15.1, 15.2; 2048 fp32 53.1, 39.7,
+//     40.2, 40.8; 4096 bf16 65.6, 44.2, 43.6, 53.2; 8192 fp32 158.6, 133.4, 137.2
 __host__ __device__ constexpr int depth_of(int vec, int e, int elem, int arrays) {
     if (vec == 1) return 0;
-    if (e == 8) return 4;
-    if (e == 16) return arrays == 1 ? (elem == 2 ? 2 : 3) : elem == 2 ? 4 : 2;
+    if (e == 8) return 2;
+    if (e == 16) return (arrays == 1) == (elem == 4) ? 3 : 2;
     return elem == 2 ? 2 : 0;
 }
 
@@ -399,7 +407,7 @@ norm_kernel(const __grid_constant__ NormArgs a) {
 }
 
 template <class T, int VEC, int E>
-__global__ void __launch_bounds__(E == 8 ? grad_threads(sizeof(T)) : kNormThreads, E == 8 ? grad_ctas(sizeof(T)) : 1)
+__global__ void __launch_bounds__(E == 8 ? grad_threads(sizeof(T)) : kNormThreads, 1)
 norm_grad_kernel(const __grid_constant__ NormArgs a) {
     constexpr int P = E / 2;
     constexpr bool kKeep = E > 8;            // the weight in shared memory
@@ -623,7 +631,7 @@ int64_t rows_alone(const Shape& s, int64_t dim) {
 // or what the rows need.
 int64_t ctas_for(const Shape& s, int64_t rows, int64_t dim, int elem, int vec, bool back) {
     const int threads = s.group * s.per_cta;
-    int per_sm = back ? (s.e == 8 ? grad_ctas(elem) * grad_threads(elem) / threads : 1)
+    int per_sm = back ? (s.e == 8 ? grad_threads(elem) / threads : 1)
                       : (s.e == 32 ? 1 : 2 * kNormThreads / threads);
     const int by_smem =
         static_cast<int>(225 * 1024 / (smem_of(s, dim, elem, vec, back) + 2048));
