@@ -519,9 +519,10 @@ int zero_embedding(const void* ids, int32_t id_bytes, int64_t n_tokens, const vo
  *                     head holds the head's gradient already); rows without a
  *                     token are not touched
  *   workspace         caller-owned device scratch of at least the bytes
- *                     zero_embedding_grad_workspace_bytes reports, 16-byte
- *                     aligned, of any content; calls that may overlap on the
- *                     GPU need one each
+ *                     zero_embedding_grad_workspace_bytes reports for the
+ *                     current device, 16-byte aligned, of any content; calls
+ *                     that may overlap on the GPU need one each; NULL where it
+ *                     reports 0 (few tokens)
  * Errors: as zero_embedding; ZERO_ERR_SIZE if the workspace is too small.
  */
 int zero_embedding_grad(const void* ids, int32_t id_bytes, int64_t n_tokens, const void* grad_out,
