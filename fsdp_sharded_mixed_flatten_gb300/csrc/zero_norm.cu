@@ -15,7 +15,7 @@
 // second launch adds up in CTA order.
 //
 // Bound by memory where rows are many: forward of 16384 x 4096 bf16 50 us (5.4 TB/s),
-// backward of 8192 x 8192 bf16 78 us (5.1 TB/s), of 8192 x 768 bf16 15 us (2.5 TB/s: the
+// backward of 8192 x 8192 bf16 78 us (5.1 TB/s), of 8192 x 768 bf16 14.4 us (2.6 TB/s: the
 // launch, the first rows and the second launch are most of it).  Few rows take as
 // long as the host's call: 8 x 768 7.2 us forward, 9.5 us backward.
 //
@@ -52,7 +52,25 @@ struct Group {
     __device__ void sync() const {
         asm volatile("bar.sync %0, %1;" ::"r"(index + 1), "r"(threads) : "memory");
     }
+    __device__ void sync_any() const {
+        if (warps == 1) __syncwarp();
+        else sync();
+    }
 };
+
+// How a row's elements are reached: by 16-byte words; by words, shifted, where
+// rows do not start on 16-byte boundaries; by single elements.  Shifting costs a
+// row two barriers more, and pays where a row's elements keep a thread busy: 8192
+// rows, in us, shifted / single:
+//            1500 bf16  4001 bf16  8190 bf16  1501 fp32  4001 fp32  8190 fp32
+//   forward   25 / 21    46 / 68    85 / 138   29 / 24    72 / 81   155 / 165
+//   backward  33 / 49    65 / 133  140 / 272   44 / 39    91 / 119  179 / 242
+// Beyond 8192 columns shared memory has no room for it.
+enum Access { kWide, kShift, kSingle };
+__host__ __device__ constexpr Access access_of(bool wide, int e, int elem, bool back) {
+    if (wide) return kWide;
+    return e == 16 || (e == 8 && elem == 2 && back) ? kShift : kSingle;
+}
 
 // Rows under way at a time in shared memory (0: one, in registers), for `arrays`
 // matrices.  In us by rows under way (1, 2, 3, 4):
@@ -61,9 +79,10 @@ struct Group {
 //     8192 fp32 180.9, 179.2, 164.9, 165.8
 //   backward of 8192 rows: 768 bf16 15.9, 14.8, 15.1, 15.2; 2048 fp32 53.1, 39.7,
 //     40.2, 40.8; 4096 bf16 65.6, 44.2, 43.6, 53.2; 8192 fp32 158.6, 133.4, 137.2
-__host__ __device__ constexpr int depth_of(int vec, int e, int elem, int arrays) {
-    if (vec == 1) return 0;
-    if (e == 8) return 2;
+// (Through shifts a row's slot serves its result too: one more for as many.)
+__host__ __device__ constexpr int depth_of(Access access, int e, int elem, int arrays) {
+    if (access == kSingle) return 0;
+    if (e == 8) return access == kWide ? 2 : 3;
     if (e == 16) return (arrays == 1) == (elem == 4) ? 3 : 2;
     return elem == 2 ? 2 : 0;
 }
@@ -175,6 +194,96 @@ __device__ __forceinline__ void store_row(T* at, const Pair (&y)[E / 2], const C
     }
 }
 
+// Rows through shifts: the group copies the aligned words that hold the row, each
+// thread takes its 16 bytes from two of them, and the result goes through the
+// row's slot to aligned words again, its ends by single elements.  Of the first
+// word the bytes before the row are read, and not used.
+
+// Bytes `by` (0 to 15) and on of the 32 in lo, hi.
+template <class T>
+__device__ __forceinline__ uint4 shifted(uint4 lo, uint4 hi, int by) {
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (by & 8) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (by & 4) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    if (sizeof(T) == 2) {
+        const int bits = 8 * (by & 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ int off_grid(const void* p) {
+    return static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16);
+}
+
+template <class T, int E>
+struct Shift {
+    static constexpr int V = 16 / sizeof(T), N = E / V;
+    // Words of a slot: those of the row and one more.
+    __device__ static __forceinline__ int words(const Group& g) { return N * g.threads + 1; }
+    __device__ static __forceinline__ void copy(uint32_t slot, const T* row, bool in, int dim,
+                                                const Group& g) {
+        const int mis = off_grid(row);
+        const char* from = reinterpret_cast<const char*>(row) - mis;
+        const int bytes = in ? mis + dim * static_cast<int>(sizeof(T)) : 0;
+        auto word = [&](int w) {
+            const int n = min(max(bytes - 16 * w, 0), 16);
+            cp_async16_fill(slot + 16u * w, from + (n != 0 ? 16 * w : 0), n);
+        };
+#pragma unroll
+        for (int n = 0; n < N; ++n) word(n * g.threads + g.t);
+        if (g.t == 0) word(N * g.threads);
+    }
+    __device__ static __forceinline__ void read(Row<T, V, E>& r, const uint4* slot, const T* row,
+                                                const Group& g) {
+        const int mis = off_grid(row);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const uint4* at = slot + n * g.threads + g.t;
+            *reinterpret_cast<uint4*>(&r.p[n]) = shifted<T>(at[0], at[1], mis);
+        }
+    }
+    // The slot has been read by all of the group.
+    __device__ static __forceinline__ void store(T* row, const Pair (&y)[E / 2], uint4* slot,
+                                                 int dim, const Group& g) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            uint4 v;
+            if constexpr (sizeof(T) == 2) {
+                v = make_uint4(narrow2(y[4 * n]), narrow2(y[4 * n + 1]), narrow2(y[4 * n + 2]),
+                               narrow2(y[4 * n + 3]));
+            } else {
+                const float2 lo = unpair(y[2 * n]), hi = unpair(y[2 * n + 1]);
+                v = make_uint4(__float_as_uint(lo.x), __float_as_uint(lo.y),
+                               __float_as_uint(hi.x), __float_as_uint(hi.y));
+            }
+            slot[n * g.threads + g.t] = v;
+        }
+        g.sync_any();
+        const int mis = off_grid(row);
+        const int head = min(dim, mis == 0 ? 0 : V - mis / static_cast<int>(sizeof(T)));
+        const int full = (dim - head) / V, by = head * static_cast<int>(sizeof(T));
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int q = n * g.threads + g.t;
+            if (q < full)
+                *reinterpret_cast<uint4*>(row + head + q * V) =
+                    shifted<T>(slot[q], slot[q + 1], by);
+        }
+        const T* at = reinterpret_cast<const T*>(slot);
+        const int tail = head + full * V;
+        if (g.t < head) row[g.t] = at[g.t];
+        if (g.t < dim - tail) row[tail + g.t] = at[tail + g.t];
+    }
+};
+
 // The parameters of this thread's columns (`missing` where there is no array
 // or no column).  Loads without conditions, at a clamped place, so that all are
 // under way at once.
@@ -269,10 +378,10 @@ __device__ __forceinline__ float2 group_sum2(const Group& g, float x, float y,
     return make_float2(__shfl_sync(0xFFFFFFFFu, v, 0), __shfl_sync(0xFFFFFFFFu, v, 16));
 }
 
-template <class T, int VEC, int E>
+template <class T, int VEC, int E, bool SHIFT>
 __global__ void __launch_bounds__(kNormThreads, E == 32 ? 1 : 2)
 norm_kernel(const __grid_constant__ NormArgs a) {
-    constexpr int kDepth = depth_of(VEC, E, sizeof(T), 1);
+    constexpr int kDepth = depth_of(SHIFT ? kShift : VEC > 1 ? kWide : kSingle, E, sizeof(T), 1);
     constexpr bool kAsync = kDepth > 0;
     extern __shared__ __align__(16) char params[];           // weight, bias, rows
     constexpr int kBatch = 1, P = E / 2;
@@ -304,19 +413,23 @@ norm_kernel(const __grid_constant__ NormArgs a) {
     const bool ragged = a.dim % VEC != 0;
     const int64_t step = static_cast<int64_t>(gridDim.x) * g.per_cta * kBatch;
     int64_t row = (static_cast<int64_t>(blockIdx.x) * g.per_cta + g.index) * kBatch;
-    const T* x = static_cast<const T*>(a.x) + row * a.x_stride + c.first;
-    T* out = static_cast<T*>(a.out) + row * a.out_stride + c.first;
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride + (SHIFT ? 0 : c.first);
+    T* out = static_cast<T*>(a.out) + row * a.out_stride + (SHIFT ? 0 : c.first);
+    const T* here = x;                                       // the row worked on
     Row<T, VEC, E> next[kBatch];
-    // this thread's words of row slot k: at held + k * slot
-    const char* held = params + 2 * sizeof(float) * E * blockDim.x + 16 * threadIdx.x;
+    // this thread's words of row slot k, or with SHIFT its group's: at held + k * slot
+    const uint32_t slot = SHIFT ? 16 * Shift<T, E>::words(g) : sizeof(T) * E * blockDim.x;
+    char* held = params + 2 * sizeof(float) * E * blockDim.x +
+                 (SHIFT ? kDepth * slot * g.index : 16 * threadIdx.x);
     const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(held));
-    const uint32_t slot = sizeof(T) * E * blockDim.x;
     int64_t ahead = row;                                     // the next row to copy
     int put = 0, get = 0;
     // (a row beyond the last: nothing is read, from an address that is)
     auto copy_next = [&] {
-        Row<T, VEC, E>::copy(to + put * slot,
-                             ahead < a.n_rows ? x : static_cast<const T*>(a.x), ahead < a.n_rows, c);
+        const bool in = ahead < a.n_rows;
+        const T* from = in ? x : static_cast<const T*>(a.x);
+        if constexpr (SHIFT) Shift<T, E>::copy(to + put * slot, from, in, a.dim, g);
+        else Row<T, VEC, E>::copy(to + put * slot, from, in, c);
         cp_async_commit();
         x += step * a.x_stride;
         ahead += step;
@@ -328,7 +441,16 @@ norm_kernel(const __grid_constant__ NormArgs a) {
         next[0].load(x, row < a.n_rows, c);
     }
     for (; row < a.n_rows; row += step, out += step * a.out_stride) {
-        if constexpr (kAsync) {
+        uint4* const words = reinterpret_cast<uint4*>(held + get * slot);
+        if constexpr (SHIFT) {
+            // the row has come, and all have done with the slot that the next copy takes
+            cp_async_wait<kDepth - 2 < 0 ? 0 : kDepth - 2>();
+            g.sync_any();
+            copy_next();
+            Shift<T, E>::read(next[0], words, here, g);
+            here += step * a.x_stride;
+            get = get + 1 == kDepth ? 0 : get + 1;
+        } else if constexpr (kAsync) {
             copy_next();
             cp_async_wait<kDepth - 1 < 0 ? 0 : kDepth - 1>();
             next[0].read(held + get * slot);
@@ -401,17 +523,22 @@ norm_kernel(const __grid_constant__ NormArgs a) {
                 *y0 = fma2(mul2(add2(*y0, m2), r2), wj.x, bj.x);
                 *y1 = fma2(mul2(add2(*y1, m2), r2), wj.y, bj.y);
             }
-            store_row<T, VEC, E>(out + i * a.out_stride, v[i], c);
+            if constexpr (SHIFT) {
+                if (g.warps == 1) __syncwarp();          // the others: at the sums
+                Shift<T, E>::store(out, v[0], words, a.dim, g);
+            } else {
+                store_row<T, VEC, E>(out + i * a.out_stride, v[i], c);
+            }
         }
     }
 }
 
-template <class T, int VEC, int E>
+template <class T, int VEC, int E, bool SHIFT>
 __global__ void __launch_bounds__(E == 8 ? grad_threads(sizeof(T)) : kNormThreads, 1)
 norm_grad_kernel(const __grid_constant__ NormArgs a) {
     constexpr int P = E / 2;
     constexpr bool kKeep = E > 8;            // the weight in shared memory
-    constexpr int kDepth = depth_of(VEC, E, sizeof(T), 2);
+    constexpr int kDepth = depth_of(SHIFT ? kShift : VEC > 1 ? kWide : kSingle, E, sizeof(T), 2);
     constexpr bool kAsync = kDepth > 0;
     extern __shared__ __align__(16) char dyn[];
     float* cols = reinterpret_cast<float*>(dyn);     // [groups][dim] at the end;
@@ -431,23 +558,34 @@ norm_grad_kernel(const __grid_constant__ NormArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t step = static_cast<int64_t>(gridDim.x) * g.per_cta;
     int64_t row = static_cast<int64_t>(blockIdx.x) * g.per_cta + g.index;
-    const T* x = static_cast<const T*>(a.x) + row * a.x_stride + c.first;
-    const T* dy = static_cast<const T*>(a.grad_out) + row * a.grad_out_stride + c.first;
-    T* out = static_cast<T*>(a.out) + row * a.out_stride + c.first;
+    const int first = SHIFT ? 0 : c.first;
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride + first;
+    const T* dy = static_cast<const T*>(a.grad_out) + row * a.grad_out_stride + first;
+    T* out = static_cast<T*>(a.out) + row * a.out_stride + first;
+    const T *x_here = x, *dy_here = dy;                      // the row worked on
     Row<T, VEC, E> next_x, next_y;
     float next_mu = 0.0f, next_r = 0.0f;
-    // this thread's words of row slot k: at held + k * slot, x then dy
-    const char* held = dyn + (kKeep ? sizeof(float) * E * blockDim.x : 0) + 16 * threadIdx.x;
+    // this thread's words of row slot k, or with SHIFT its group's: at held + k * slot,
+    // x then dy
+    const uint32_t one = SHIFT ? 16 * Shift<T, E>::words(g) : sizeof(T) * E * blockDim.x;
+    const uint32_t slot = 2 * one;
+    char* held = dyn + (kKeep ? sizeof(float) * E * blockDim.x : 0) +
+                 (SHIFT ? kDepth * slot * g.index : 16 * threadIdx.x);
     const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(held));
-    const uint32_t one = sizeof(T) * E * blockDim.x, slot = 2 * one;
     int64_t ahead = row;                                     // the next row to copy
     int put_at = 0, get = 0;
     // (a row beyond the last: nothing is read, from an address that is)
     auto copy_next = [&] {
         const bool in = ahead < a.n_rows;
-        Row<T, VEC, E>::copy(to + put_at * slot, in ? x : static_cast<const T*>(a.x), in, c);
-        Row<T, VEC, E>::copy(to + put_at * slot + one, in ? dy : static_cast<const T*>(a.grad_out),
-                             in, c);
+        const T* from_x = in ? x : static_cast<const T*>(a.x);
+        const T* from_y = in ? dy : static_cast<const T*>(a.grad_out);
+        if constexpr (SHIFT) {
+            Shift<T, E>::copy(to + put_at * slot, from_x, in, a.dim, g);
+            Shift<T, E>::copy(to + put_at * slot + one, from_y, in, a.dim, g);
+        } else {
+            Row<T, VEC, E>::copy(to + put_at * slot, from_x, in, c);
+            Row<T, VEC, E>::copy(to + put_at * slot + one, from_y, in, c);
+        }
         cp_async_commit();
         x += step * a.x_stride;
         dy += step * a.grad_out_stride;
@@ -471,7 +609,17 @@ norm_grad_kernel(const __grid_constant__ NormArgs a) {
         load(row);
     }
     for (; row < a.n_rows; row += step, out += step * a.out_stride) {
-        if constexpr (kAsync) {
+        uint4* const words = reinterpret_cast<uint4*>(held + get * slot);
+        if constexpr (SHIFT) {
+            cp_async_wait<kDepth - 2 < 0 ? 0 : kDepth - 2>();
+            g.sync_any();
+            copy_next();
+            Shift<T, E>::read(next_x, words, x_here, g);
+            Shift<T, E>::read(next_y, words + one / 16, dy_here, g);
+            x_here += step * a.x_stride;
+            dy_here += step * a.grad_out_stride;
+            get = get + 1 == kDepth ? 0 : get + 1;
+        } else if constexpr (kAsync) {
             copy_next();
             cp_async_wait<kDepth - 1 < 0 ? 0 : kDepth - 1>();
             next_x.read(held + get * slot);
@@ -505,7 +653,12 @@ norm_grad_kernel(const __grid_constant__ NormArgs a) {
         const Pair m1 = splat(-s.x * inv_d * r), m2 = splat(-s.y * inv_d * r);
 #pragma unroll
         for (int j = 0; j < P; ++j) gr[j] = fma2(xh[j], m2, fma2(gr[j], r2, m1));
-        store_row<T, VEC, E>(out, gr, c);
+        if constexpr (SHIFT) {
+            if (g.warps == 1) __syncwarp();              // the others: at the sums
+            Shift<T, E>::store(out, gr, words, a.dim, g);
+        } else {
+            store_row<T, VEC, E>(out, gr, c);
+        }
     }
     if constexpr (kAsync) cp_async_wait<0>();        // nothing is to come in the columns' place
     float* part = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.dim;
@@ -606,10 +759,12 @@ Shape shape_for(int64_t dim, int elem, bool back) {
     return {e, group, per_cta};
 }
 
-size_t smem_of(const Shape& s, int64_t dim, int elem, int vec, bool back) {
+size_t smem_of(const Shape& s, int64_t dim, int elem, bool wide, bool back) {
     const size_t threads = s.group * s.per_cta;
-    const size_t rows = static_cast<size_t>(depth_of(vec, s.e, elem, back ? 2 : 1)) * elem * s.e *
-                        (back ? 2 : 1) * threads;
+    const Access access = access_of(wide, s.e, elem, back);
+    const size_t slot = elem * s.e * threads + (access == kShift ? 16 * s.per_cta : 0);
+    const size_t rows =
+        static_cast<size_t>(depth_of(access, s.e, elem, back ? 2 : 1)) * (back ? 2 : 1) * slot;
     if (!back) return 2 * sizeof(float) * s.e * threads + rows;
     const size_t kept = s.e > 8 ? sizeof(float) * s.e * threads : 0;
     const size_t cols = sizeof(float) * s.per_cta * dim;
@@ -629,12 +784,12 @@ int64_t rows_alone(const Shape& s, int64_t dim) {
 
 // CTAs: what the registers (launch bounds) and the shared memory of an SM hold,
 // or what the rows need.
-int64_t ctas_for(const Shape& s, int64_t rows, int64_t dim, int elem, int vec, bool back) {
+int64_t ctas_for(const Shape& s, int64_t rows, int64_t dim, int elem, bool wide, bool back) {
     const int threads = s.group * s.per_cta;
     int per_sm = back ? (s.e == 8 ? grad_threads(elem) / threads : 1)
                       : (s.e == 32 ? 1 : 2 * kNormThreads / threads);
     const int by_smem =
-        static_cast<int>(225 * 1024 / (smem_of(s, dim, elem, vec, back) + 2048));
+        static_cast<int>(225 * 1024 / (smem_of(s, dim, elem, wide, back) + 2048));
     if (by_smem < per_sm) per_sm = by_smem > 0 ? by_smem : 1;
     const int64_t few = back ? rows_alone(s, dim) : 0;
     const int64_t need = rows > few ? (rows + s.per_cta - 1) / s.per_cta : 1;
@@ -647,10 +802,12 @@ bool wide_rows(int elem, const void* p, int64_t stride) {
     return aligned_to(p, 16) && stride % (16 / elem) == 0;
 }
 
-template <class T, int VEC, int E, bool BACK>
+template <class T, int E, Access ACCESS, bool BACK>
 cudaError_t launch_e(const NormArgs& a, unsigned grid, int threads, size_t smem,
                      cudaStream_t stream) {
-    const auto kernel = BACK ? norm_grad_kernel<T, VEC, E> : norm_kernel<T, VEC, E>;
+    constexpr int VEC = ACCESS == kSingle ? 1 : 16 / sizeof(T);
+    const auto kernel = BACK ? norm_grad_kernel<T, VEC, E, ACCESS == kShift>
+                             : norm_kernel<T, VEC, E, ACCESS == kShift>;
     // more than 48 KB of shared memory need asking for
     static std::once_flag once[64];
     static cudaError_t set[64];
@@ -666,36 +823,35 @@ cudaError_t launch_e(const NormArgs& a, unsigned grid, int threads, size_t smem,
     return cudaGetLastError();
 }
 
-template <class T, int VEC, bool BACK>
+template <class T, bool WIDE, bool BACK>
 cudaError_t launch_shape(NormArgs a, cudaStream_t stream) {
-    const Shape s = shape_for(a.dim, sizeof(T), BACK);
+    constexpr int B = sizeof(T);
+    const Shape s = shape_for(a.dim, B, BACK);
     a.group_threads = s.group;
-    const unsigned g =
-        static_cast<unsigned>(ctas_for(s, a.n_rows, a.dim, sizeof(T), VEC, BACK));
+    const unsigned g = static_cast<unsigned>(ctas_for(s, a.n_rows, a.dim, B, WIDE, BACK));
     const int threads = s.group * s.per_cta;
-    const size_t smem = smem_of(s, a.dim, sizeof(T), VEC, BACK);
-    if (s.e == 8) return launch_e<T, VEC, 8, BACK>(a, g, threads, smem, stream);
-    if (s.e == 16) return launch_e<T, VEC, 16, BACK>(a, g, threads, smem, stream);
-    return launch_e<T, VEC, 32, BACK>(a, g, threads, smem, stream);
+    const size_t smem = smem_of(s, a.dim, B, WIDE, BACK);
+    if (s.e == 8) return launch_e<T, 8, access_of(WIDE, 8, B, BACK), BACK>(a, g, threads, smem, stream);
+    if (s.e == 16)
+        return launch_e<T, 16, access_of(WIDE, 16, B, BACK), BACK>(a, g, threads, smem, stream);
+    return launch_e<T, 32, access_of(WIDE, 32, B, BACK), BACK>(a, g, threads, smem, stream);
 }
 
-// Elements of an access: 16 bytes where every row allows it.
+// Whether every row of every matrix starts on a 16-byte boundary.
 template <bool BACK>
-int vec_of(const NormArgs& a, int act_bytes) {
-    const bool wide = wide_rows(act_bytes, a.x, a.x_stride) &&
-                      wide_rows(act_bytes, a.out, a.out_stride) &&
-                      (!BACK || wide_rows(act_bytes, a.grad_out, a.grad_out_stride));
-    return wide ? 16 / act_bytes : 1;
+bool wide(const NormArgs& a, int act_bytes) {
+    return wide_rows(act_bytes, a.x, a.x_stride) && wide_rows(act_bytes, a.out, a.out_stride) &&
+           (!BACK || wide_rows(act_bytes, a.grad_out, a.grad_out_stride));
 }
 
 template <bool BACK>
 cudaError_t dispatch(const NormArgs& a, int act_bytes, cudaStream_t stream) {
-    const bool wide = vec_of<BACK>(a, act_bytes) > 1;
+    const bool w = wide<BACK>(a, act_bytes);
     if (act_bytes == 4)
-        return wide ? launch_shape<float, 4, BACK>(a, stream)
-                    : launch_shape<float, 1, BACK>(a, stream);
-    return wide ? launch_shape<uint16_t, 8, BACK>(a, stream)
-                : launch_shape<uint16_t, 1, BACK>(a, stream);
+        return w ? launch_shape<float, true, BACK>(a, stream)
+                 : launch_shape<float, false, BACK>(a, stream);
+    return w ? launch_shape<uint16_t, true, BACK>(a, stream)
+             : launch_shape<uint16_t, false, BACK>(a, stream);
 }
 
 }  // namespace
@@ -705,8 +861,8 @@ int norm_grad_ctas(int64_t n_rows, int64_t dim) {
     int64_t most = 1;
     for (int elem = 2; elem <= 4; elem += 2) {
         const Shape s = shape_for(dim, elem, true);
-        for (int vec : {1, 16 / elem}) {
-            const int64_t n = ctas_for(s, n_rows, dim, elem, vec, true);
+        for (bool w : {false, true}) {
+            const int64_t n = ctas_for(s, n_rows, dim, elem, w, true);
             if (n > most) most = n;
         }
     }
@@ -724,7 +880,7 @@ cudaError_t launch_norm_grad(const NormArgs& a, int act_bytes, cudaStream_t stre
 cudaError_t launch_norm_grad_reduce(const NormArgs& a, int act_bytes, cudaStream_t stream) {
     const int64_t width = 2 * static_cast<int64_t>(a.dim);
     const Shape s = shape_for(a.dim, act_bytes, true);
-    const int64_t parts = ctas_for(s, a.n_rows, a.dim, act_bytes, vec_of<true>(a, act_bytes), true);
+    const int64_t parts = ctas_for(s, a.n_rows, a.dim, act_bytes, wide<true>(a, act_bytes), true);
     if (parts == 1 && s.e < 32) return cudaSuccess;      // the sums themselves are there
     // its blocks may be set up while the partial rows are still being added up
     cudaLaunchConfig_t cfg{};

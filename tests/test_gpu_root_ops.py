@@ -305,6 +305,42 @@ def test_layer_norm_grad_of_many_rows(n, dim):
             assert torch.equal(_bits(a), _bits(b))
 
 
+@pytest.mark.parametrize("act", [BF16, F32])
+@pytest.mark.parametrize("n,dim", [(2, 3), (700, 33), (900, 1501), (7, 2049), (900, 4001),
+                                   (400, 8190), (3, 9001)])
+def test_layer_norm_of_rows_off_the_16_byte_grid(n, dim, act):
+    """Every matrix at a start and a stride of its own; in place; the same bits
+    from call to call."""
+    g = _gen("off the grid", n, dim)
+    x = Guarded(n, dim, act, 1, 1, torch.randn((n, dim), generator=g) * 2 + 0.5)
+    dy = Guarded(n, dim, act, 3, 2, torch.randn((n, dim), generator=g) * 0.1)
+    out, dx = Guarded(n, dim, act, 2, 3), Guarded(n, dim, act, 4, 5)
+    w, b = (torch.randn(dim, generator=g).to(act).cuda() for _ in range(2))
+    mean, rstd = (torch.empty(n, device="cuda") for _ in range(2))
+    zf.zero_layer_norm(x.t, w, b, 1e-5, out.t, mean, rstd)
+    ref = R.layer_norm(x.t, w, b, 1e-5)
+    R.check(out.t, ref["out"], ref["d_out"], "out")
+    out.check_guard("out")
+    nbytes = zf.zero_layer_norm_grad_workspace_bytes(n, dim)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    dw, db = torch.empty_like(w), torch.empty_like(w)
+    zf.zero_layer_norm_grad(dy.t, x.t, w, mean, rstd, dx.t, dw, db, ws, nbytes)
+    ref = R.layer_norm_grad(dy.t, x.t, w, mean, rstd, max(1, nbytes // (8 * dim)))
+    R.check(dx.t, ref["grad_x"], ref["d_x"], "grad_x")
+    R.check(dw, ref["grad_weight"], ref["d_weight"], "grad_weight")
+    R.check(db, ref["grad_bias"], ref["d_bias"], "grad_bias")
+    dx.check_guard("grad_x")
+    again, dw2, db2 = dx.t.clone(), torch.empty_like(w), torch.empty_like(w)
+    zf.zero_layer_norm_grad(dy.t, x.t, w, mean, rstd, dy.t, dw2, db2, ws, nbytes)
+    for p, q in ((dy.t, again), (dw2, dw), (db2, db)):
+        assert torch.equal(_bits(p), _bits(q))
+    dy.check_guard("grad_out")
+    again = out.t.clone()
+    zf.zero_layer_norm(x.t, w, b, 1e-5, x.t)
+    assert torch.equal(_bits(x.t), _bits(again))
+    x.check_guard("x")
+
+
 def test_layer_norm_of_no_rows():
     none = torch.empty((0, 12), device="cuda")
     stat = torch.empty(0, device="cuda")
