@@ -84,7 +84,7 @@ __host__ __device__ constexpr int depth_of(Access access, int e, int elem, int a
     if (access == kSingle) return 0;
     if (e == 8) return access == kWide ? 2 : 3;
     if (e == 16) return (arrays == 1) == (elem == 4) ? 3 : 2;
-    return elem == 2 ? 2 : 0;
+    return elem == 2 ? 2 : arrays - 1;
 }
 
 __device__ __forceinline__ void cp_async16_fill(uint32_t dst, const void* src, int bytes) {
@@ -162,34 +162,41 @@ struct Row {
     }
 };
 
+// The first `left` of a pack's values.
+template <class T, int VEC>
+__device__ __forceinline__ void store_pack(T* at, const Pair* y, int left) {
+    if (left == 0) return;
+    Pack<T, VEC> v;
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) reinterpret_cast<uint32_t*>(&v)[i] = narrow2(y[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+            const float2 f = unpair(y[i]);
+            v.x[2 * i] = narrow<T>(f.x);
+            v.x[2 * i + 1] = narrow<T>(f.y);
+        }
+    }
+    if (left == VEC) {
+        st_pack<T, VEC>(at, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC - 1; ++e) {
+            if (e < left) at[e] = v.x[e];
+        }
+    }
+}
+
 template <class T, int VEC, int E>
 __device__ __forceinline__ void store_row(T* at, const Pair (&y)[E / 2], const Columns<VEC, E>& c) {
 #pragma unroll
     for (int n = 0; n < E / VEC; ++n) {
-        if (c.left[n] == 0) continue;
-        Pack<T, VEC> v;
         if constexpr (VEC == 1) {
             const float2 f = unpair(y[n / 2]);
-            v.x[0] = narrow<T>(n % 2 == 0 ? f.x : f.y);
-        } else if constexpr (sizeof(T) == 2) {
-#pragma unroll
-            for (int i = 0; i < VEC / 2; ++i)
-                reinterpret_cast<uint32_t*>(&v)[i] = narrow2(y[n * VEC / 2 + i]);
+            if (c.left[n] != 0) at[n * c.step] = narrow<T>(n % 2 == 0 ? f.x : f.y);
         } else {
-#pragma unroll
-            for (int i = 0; i < VEC / 2; ++i) {
-                const float2 f = unpair(y[n * VEC / 2 + i]);
-                v.x[2 * i] = narrow<T>(f.x);
-                v.x[2 * i + 1] = narrow<T>(f.y);
-            }
-        }
-        if (c.left[n] == VEC) {
-            st_pack<T, VEC>(at + n * c.step, v);
-        } else if constexpr (VEC > 1) {
-#pragma unroll
-            for (int e = 0; e < VEC - 1; ++e) {
-                if (e < c.left[n]) at[n * c.step + e] = v.x[e];
-            }
+            store_pack<T, VEC>(at + n * c.step, y + n * VEC / 2, c.left[n]);
         }
     }
 }
@@ -540,6 +547,10 @@ norm_grad_kernel(const __grid_constant__ NormArgs a) {
     constexpr bool kKeep = E > 8;            // the weight in shared memory
     constexpr int kDepth = depth_of(SHIFT ? kShift : VEC > 1 ? kWide : kSingle, E, sizeof(T), 2);
     constexpr bool kAsync = kDepth > 0;
+    // 32 columns of dw and db leave no registers for the row: it is read from its
+    // slot twice, before and after its sums (8192 x 16384: bf16 181 us, 4.5 TB/s, kept
+    // in registers 308; fp32 334 us, 4.8 TB/s, in registers 771)
+    constexpr bool kTwice = E == 32 && kAsync;
     extern __shared__ __align__(16) char dyn[];
     float* cols = reinterpret_cast<float*>(dyn);     // [groups][dim] at the end;
                                                      // before, the weight and the rows
@@ -604,7 +615,7 @@ norm_grad_kernel(const __grid_constant__ NormArgs a) {
     };
     load_stats(row);
     if constexpr (kAsync) {
-        for (int k = 0; k < kDepth - 1; ++k) copy_next();
+        for (int k = 0; k < (kDepth == 1 ? 1 : kDepth - 1); ++k) copy_next();
     } else {
         load(row);
     }
@@ -619,6 +630,46 @@ norm_grad_kernel(const __grid_constant__ NormArgs a) {
             x_here += step * a.x_stride;
             dy_here += step * a.grad_out_stride;
             get = get + 1 == kDepth ? 0 : get + 1;
+        } else if constexpr (kTwice) {
+            // (one slot: the next row is copied when this one has been used up)
+            if (kDepth > 1) copy_next();
+            cp_async_wait<kDepth - 1 < 0 ? 0 : kDepth - 1>();
+            const char* const at = held + get * slot;
+            const float r = next_r;
+            const Pair mu2 = splat(-next_mu), r2 = splat(r);
+            // f(pair, pair of its pack, xh, dy, g), done(pack)
+            auto each = [&](auto&& f, auto&& done) {
+#pragma unroll
+                for (int n = 0; n < E / VEC; ++n) {
+                    Row<T, VEC, VEC> px, py;
+                    px.read(at + 16u * n * blockDim.x);
+                    py.read(at + one + 16u * n * blockDim.x);
+#pragma unroll
+                    for (int i = 0; i < VEC / 2; ++i) {
+                        const int j = n * VEC / 2 + i;
+                        const Pair wj = j % 2 == 0 ? kept[j / 2].x : kept[j / 2].y;
+                        f(j, i, mul2(add2(px[i], mu2), r2), py[i], mul2(py[i], wj));
+                    }
+                    done(n);
+                }
+            };
+            Pair s1 = 0, s2 = 0;
+            each([&](int, int, Pair xh, Pair, Pair gr) {
+                s1 = add2(s1, gr);
+                s2 = fma2(gr, xh, s2);
+            }, [](int) {});
+            load_stats(row + step);
+            const float2 s = group_sum2(g, both(s1), both(s2), red, half);
+            const Pair m1 = splat(-s.x * inv_d * r), m2 = splat(-s.y * inv_d * r);
+            Pair y[VEC / 2];
+            each([&](int j, int i, Pair xh, Pair d, Pair gr) {
+                dw[j] = fma2(d, xh, dw[j]);
+                db[j] = add2(db[j], d);
+                y[i] = fma2(xh, m2, fma2(gr, r2, m1));
+            }, [&](int n) { store_pack<T, VEC>(out + n * c.step, y, c.left[n]); });
+            get = get + 1 == kDepth ? 0 : get + 1;
+            if (kDepth == 1) copy_next();
+            continue;
         } else if constexpr (kAsync) {
             copy_next();
             cp_async_wait<kDepth - 1 < 0 ? 0 : kDepth - 1>();
@@ -687,7 +738,7 @@ norm_grad_kernel(const __grid_constant__ NormArgs a) {
         }
     };
     // no other CTA's partial rows: the sums themselves (not where a thread holds 32
-    // columns: one row of 16384 bf16 25.4 us, with the second launch 21.3)
+    // columns: one row of 16384 bf16 25.4 us, with the second launch 21.3 then)
     const bool alone = E < 32 && gridDim.x == 1;
     if (g.per_cta == 1 && !alone) {
         put(dw, part);

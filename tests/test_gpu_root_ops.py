@@ -306,6 +306,28 @@ def test_layer_norm_grad_of_many_rows(n, dim):
 
 
 @pytest.mark.parametrize("act", [BF16, F32])
+@pytest.mark.parametrize("n,dim", [(500, 9000), (350, 16384)])
+def test_layer_norm_grad_of_wide_rows(n, dim, act):
+    """Several rows a CTA where a thread holds the most columns; in place."""
+    x, w, _, dy = _norm_inputs(n, dim, act, F32, 0, 0)
+    xd = x.t.double()
+    mean = xd.mean(1).float()
+    rstd = torch.rsqrt(xd.var(1, unbiased=False) + 1e-5).float()
+    nbytes = zf.zero_layer_norm_grad_workspace_bytes(n, dim)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    ref = R.layer_norm_grad(dy.t, x.t, w.t[0], mean, rstd, max(1, nbytes // (8 * dim)))
+    dx = Guarded(n, dim, act, 0, 0)
+    dw, db = (torch.empty(dim, device="cuda") for _ in range(2))
+    zf.zero_layer_norm_grad(dy.t, x.t, w.t[0], mean, rstd, dx.t, dw, db, ws, nbytes)
+    R.check(dx.t, ref["grad_x"], ref["d_x"], "grad_x")
+    R.check(dw, ref["grad_weight"], ref["d_weight"], "grad_weight")
+    R.check(db, ref["grad_bias"], ref["d_bias"], "grad_bias")
+    dx.check_guard("grad_x")
+    zf.zero_layer_norm_grad(dy.t, x.t, w.t[0], mean, rstd, x.t, None, None, ws, nbytes)
+    assert torch.equal(_bits(x.t), _bits(dx.t))
+
+
+@pytest.mark.parametrize("act", [BF16, F32])
 @pytest.mark.parametrize("n,dim", [(2, 3), (700, 33), (900, 1501), (7, 2049), (900, 4001),
                                    (400, 8190), (3, 9001)])
 def test_layer_norm_of_rows_off_the_16_byte_grid(n, dim, act):
