@@ -30,9 +30,13 @@
 //
 // Exponentials are 2^(z c - M), c = log2(e) / tau: one fused multiply-add and
 // one ex2 each.  M is an integer, ceil(c max z) of what a thread has seen, so
-// that moving from one M to another scales by an exact power of two.  Rows
-// whose largest |c z| passes kFar (all logits at the type's lowest value, or
-// infinities) take the difference first: 2^((z - max z) c).
+// that moving from one M to another scales by an exact power of two.  The fused
+// multiply-add takes the exact z c, M comes from the rounded one, and what lies
+// between them is an exponent of two: below kFar a quarter at most, at 2^31 more
+// than an fp32 holds.  So M stays within kFar, and rows whose largest c z lies
+// beyond (every logit a mask's value, some very large, infinities) take the
+// difference first: 2^((z - max z) c).  Logits far below the rest, of whatever
+// size, add 0 to a sum at M >= -kFar.
 #include "zero_ops.cuh"
 
 #include <cooperative_groups.h>
@@ -52,8 +56,8 @@ constexpr int kRowWarps = 16;                    // of a CTA, two of them an SM
 constexpr int kMostBytes = 110 * 1024;           // of a CTA of 16 warps: words and entries
 constexpr int kShortRow = 48 * 1024;             // rows up to this take one CTA
 constexpr float kInf = __builtin_huge_valf();
-constexpr float kFar = 1e30f;
-constexpr float kNone = -4e30f;                  // off of a sum without terms
+constexpr float kFar = 1 << 22;                  // of |c z|, whose ulp is a half there
+constexpr float kNone = -2 * kFar;               // off of a sum without terms
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -560,14 +564,11 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
         Running r = join_all(sums[buf], ranks * WW, -kFar);
         Exponent ex{a.c, r.off, !(fabsf(r.off) < kFar)};
         Running rt{kNone, 0.0f};
-        bool live = false, far_entries = false;       // the row has an entry
-        for (int j = lane; j < ranks * EW; j += 32) {
-            const float off = entry_sums[buf][j].off;
-            live |= off != kNone;
-            far_entries |= off != kNone && !(fabsf(off) < kFar);
-        }
-        live = __any_sync(0xFFFFFFFFu, live);
-        far_entries = __any_sync(0xFFFFFFFFu, far_entries);
+        float entry_off = kNone;
+        for (int j = lane; j < ranks * EW; j += 32) entry_off = fmaxf(entry_off, entry_sums[buf][j].off);
+        asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(entry_off) : "f"(entry_off));
+        const bool live = entry_off != kNone;         // the row has an entry
+        const bool far_entries = live && !(fabsf(entry_off) < kFar);
         if (!worker) {
             rt = join_all(entry_sums[buf], ranks * EW, kNone);
             finish(number - 1);
