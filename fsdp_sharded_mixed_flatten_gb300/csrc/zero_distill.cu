@@ -188,11 +188,13 @@ __device__ __forceinline__ Running warp_join(Running r) {
     return {off, warp_sum(r.s * ex2(r.off - off))};
 }
 
-// The row's exponentials: near: 2^(z c - off), far: 2^((z - off) c).
+// The exponents of the row's or its entries' exponentials: near: z c - off,
+// rounded once, so that logits far from zero lose no digits of their
+// differences; far: (z - off) c.
 struct Exponent {
     float c, off;
     bool far;
-    __device__ __forceinline__ float log2q(float z) const {
+    __device__ __forceinline__ float of(float z) const {
         return far ? (z - off) * c : __fmaf_rn(z, c, -off);
     }
 };
@@ -251,7 +253,7 @@ __device__ float cluster_all(float x, float* red, float* slots, int rank, int ra
 // The teacher's entries of a row in shared memory: those in this CTA's slice.
 struct Entries {
     int32_t* id;     // -1: absent, or in another CTA's slice
-    float* l2;       // l c; later w tau p
+    float* l;        // the teacher's logit; later w tau p
     float* z;        // the student's logit there; later w tau q
 };
 
@@ -432,13 +434,12 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
                 fetch_logit(sl, e);
             }
             if (k >= a.top || e.l == -kInf) e.id = -1;
-            const float l2 = e.l * a.c;
             if (e.id >= 0) {
-                r.raise(fminf(fmaxf(ceilf(l2), -kFar), kFar));
-                r.s += ex2(l2 - r.off);
+                r.raise(fminf(fmaxf(ceilf(e.l * a.c), -kFar), kFar));
+                r.s += ex2(__fmaf_rn(e.l, a.c, -r.off));
             }
             t.id[k] = e.id;
-            t.l2[k] = l2;
+            t.l[k] = e.l;
             t.z[k] = e.z;
         }
         return warp_join(r);
@@ -514,7 +515,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
             for (int k = et; k < a.top; k += kEntryThreads) {
                 const int32_t id = t.id[k];
                 if (id < 0) continue;
-                float p = t.l2[k];
+                float p = t.l[k];
                 if (equal_ids) {
                     // equal ids add up in the order of the entries; the first writes
                     p = 0.0f;
@@ -522,7 +523,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
                     for (int j = 0; j < a.top; ++j) {
                         if (t.id[j] != id) continue;
                         first &= j >= k;
-                        p += t.l2[j];
+                        p += t.l[j];
                     }
                     if (!first) continue;
                 }
@@ -591,32 +592,28 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
 #pragma unroll
                     for (int p = 0; p < kP; ++p) {
                         const float2 v = unpair(x[p]);
-                        sum += ex2(ex.log2q(v.x)) + ex2(ex.log2q(v.y));
+                        sum += ex2(ex.of(v.x)) + ex2(ex.of(v.y));
                     }
                 }
-                if (tid < sl.singles()) sum += ex2(ex.log2q(single));
+                if (tid < sl.singles()) sum += ex2(ex.of(single));
             }
             r.s = cluster_all<false>(sum, far_red, far_slots[1], rank, ranks);
         }
+        Exponent entry_ex{a.c, rt.off, far_entries};
         if (far_entries) {
-            // an entry's l c is beyond kFar: differences of l itself
             float m = -kInf;
-            auto l_of = [&](int k) { return ld_param(a.teacher, a.teacher_f32, row * a.top + k); };
             if (!worker) {
                 for (int k = et; k < a.top; k += kEntryThreads) {
-                    if (t.id[k] >= 0) m = fmaxf(m, l_of(k));
+                    if (t.id[k] >= 0) m = fmaxf(m, t.l[k]);
                 }
             }
-            m = cluster_all<true>(m, far_red, far_slots[2], rank, ranks);
+            entry_ex.off = cluster_all<true>(m, far_red, far_slots[2], rank, ranks);
             float sum = 0.0f;
             if (!worker) {
                 for (int k = et; k < a.top; k += kEntryThreads) {
-                    if (t.id[k] < 0) continue;
-                    t.l2[k] = (l_of(k) - m) * a.c;
-                    sum += ex2(t.l2[k]);
+                    if (t.id[k] >= 0) sum += ex2(entry_ex.of(t.l[k]));
                 }
             }
-            rt.off = 0.0f;
             rt.s = cluster_all<false>(sum, far_red, far_slots[0], rank, ranks);
         }
         float next_w = 0.0f;
@@ -637,9 +634,9 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
             for (int k = et; k < a.top; k += kEntryThreads) {
                 const int32_t id = t.id[k];
                 if (id < 0) continue;
-                const float l2 = t.l2[k] - rt.off, p = ex2(l2) * inv_t, lq = ex.log2q(t.z[k]);
-                if (p != 0.0f) loss += p * ((l2 - log_t) - (lq - log_s));
-                t.l2[k] = tau_w * p;
+                const float lp = entry_ex.of(t.l[k]), p = ex2(lp) * inv_t, lq = ex.of(t.z[k]);
+                if (p != 0.0f) loss += p * ((lp - log_t) - (lq - log_s));
+                t.l[k] = tau_w * p;
                 t.z[k] = ex2(lq) * f;
                 if (!GRAD || HASH) continue;
                 int same = 0;
@@ -731,7 +728,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
 #pragma unroll
                         for (int j = 0; j < kP; ++j) {
                             const float2 y = unpair(x[j]);
-                            x[j] = pair(ex2(ex.log2q(y.x)) * f, ex2(ex.log2q(y.y)) * f);
+                            x[j] = pair(ex2(ex.of(y.x)) * f, ex2(ex.of(y.y)) * f);
                         }
                         return W::join(x);
                     });
@@ -744,14 +741,14 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
                 const int in_copy = sl.staged * kV;
                 for (int i = tid; i < sl.n * kV; i += kWorkers) {
                     const float z = widen<T>(i < in_copy ? elements[i] : sl.z[sl.first + i]);
-                    dz[sl.first + i] = narrow<T>(live ? ex2(ex.log2q(z)) * f : 0.0f);
+                    dz[sl.first + i] = narrow<T>(live ? ex2(ex.of(z)) * f : 0.0f);
                 }
                 asm volatile("bar.sync 1, %0;" ::"n"(kWorkers) : "memory");
                 if (copy) copy_row(next_sl);
             }
             if (GRAD) {
                 if (tid < sl.singles())
-                    dz[sl.single_at(tid)] = narrow<T>(live ? ex2(ex.log2q(single)) * f : 0.0f);
+                    dz[sl.single_at(tid)] = narrow<T>(live ? ex2(ex.of(single)) * f : 0.0f);
             }
         }
         if (!copy) break;

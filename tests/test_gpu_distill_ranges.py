@@ -93,3 +93,26 @@ def test_every_row_masked_alike(n, vocab, top, dtype, mask):
     z[0] = mask
     z[1:, :vocab - 900] = mask
     _compare(z, ids, t, w, 1.0)
+
+
+@pytest.mark.parametrize("level", [0.0, 30.0, -700.0, 5e3, -5e3, 3e5, -2e6, 1e8, -1e12])
+@pytest.mark.parametrize("teacher", [BF16, F32])
+@pytest.mark.parametrize("n,vocab,top", [(5, 3001, 24), (320, 4001, 200), (6, 50257, 70)])
+def test_teacher_far_from_zero(n, vocab, top, teacher, level):
+    """A teacher's logits that share a level, as unnormalised ones may: only
+    their differences count."""
+    z, ids, t, w = _inputs(n, vocab, top, F32, F32, "level")
+    t = (t + level).to(teacher)
+    _compare(z, ids, t, w, 0.7)
+
+
+def test_teacher_of_widely_spread_entries():
+    """Entries that lie 1e30 apart, and one among entries of the type's lowest
+    value: the largest takes all, and nothing else is off."""
+    z, ids, t, w = _inputs(4, 3001, 8, F32, F32, "spread")
+    ids[:] = torch.arange(8, dtype=torch.int32, device="cuda") * 11
+    t[0] = torch.arange(8, device="cuda") * 1e30
+    t[1, 1:] = torch.finfo(F32).min
+    t[2, ::2] = -1e9
+    t[3, 3:] = -1e20
+    _compare(z, ids, t, w, 0.5)
