@@ -66,6 +66,15 @@ int check_rows(const void* p, int64_t n, int64_t dim, int64_t stride, int32_t by
     return ZERO_OK;
 }
 
+// An output in place of an input: where rows have different strides, one row's
+// result would lie on another's input.
+int check_in_place(const void* out, int64_t out_stride, const void* in, int64_t in_stride,
+                   int64_t n, const char* name) {
+    if (out == in && out_stride != in_stride && n > 1)
+        return fail(ZERO_ERR_SIZE, "%s in place of an input needs the same row stride", name);
+    return ZERO_OK;
+}
+
 int check_table(int64_t n_tokens, int64_t vocab, int64_t dim, double scale) {
     if (!std::isfinite(scale)) return fail(ZERO_ERR_INVALID_ARG, "scale must be finite");
     if (n_tokens < 0 || vocab < 1 || dim < 1)
@@ -259,6 +268,7 @@ ZERO_API int zero_layer_norm(const void* x, int32_t act_bytes, int64_t n_rows, i
         return fail(ZERO_ERR_INVALID_ARG, "eps must be finite and >= 0");
     if (int rc = check_rows(x, n_rows, dim, x_stride, act_bytes, "x")) return rc;
     if (int rc = check_rows(out, n_rows, dim, out_stride, act_bytes, "out")) return rc;
+    if (int rc = check_in_place(out, out_stride, x, x_stride, n_rows, "out")) return rc;
     if (int rc = check_optional(weight, param_bytes, "weight")) return rc;
     if (int rc = check_optional(bias, param_bytes, "bias")) return rc;
     if (int rc = check_optional(mean, 4, "mean")) return rc;
@@ -300,6 +310,9 @@ ZERO_API int zero_layer_norm_grad(const void* grad_out, const void* x, int32_t a
         return rc;
     if (int rc = check_rows(x, n_rows, dim, x_stride, act_bytes, "x")) return rc;
     if (int rc = check_rows(grad_x, n_rows, dim, grad_x_stride, act_bytes, "grad_x")) return rc;
+    if (int rc = check_in_place(grad_x, grad_x_stride, grad_out, grad_out_stride, n_rows, "grad_x"))
+        return rc;
+    if (int rc = check_in_place(grad_x, grad_x_stride, x, x_stride, n_rows, "grad_x")) return rc;
     if (int rc = check_optional(weight, param_bytes, "weight")) return rc;
     if (int rc = check_optional(grad_weight, param_bytes, "grad_weight")) return rc;
     if (int rc = check_optional(grad_bias, param_bytes, "grad_bias")) return rc;
