@@ -144,8 +144,8 @@ int distill(const void* logits, int32_t logits_bytes, int64_t n_rows, int64_t vo
     if (with_grad) {
         if (int rc = check_rows(grad, n_rows, vocab, grad_stride, logits_bytes, "grad_logits"))
             return rc;
-        if (grad == logits && grad_stride != logits_stride)
-            return fail(ZERO_ERR_SIZE, "grad_logits in place of logits needs the same row stride");
+        if (int rc = check_in_place(grad, grad_stride, logits, logits_stride, n_rows, "grad_logits"))
+            return rc;
     }
     if (n_rows == 0) return ok();
     if (int rc = check_array(ids, 4, "teacher_ids")) return rc;

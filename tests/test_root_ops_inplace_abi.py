@@ -23,6 +23,7 @@ def test_in_place_with_another_stride_is_refused(lib, monkeypatch, call, over): 
     (_distill, dict(dz=A[0])),
     # one row: its stride is of no account
     (_norm, dict(out=A[0], os=24, n=1)), (_norm_grad, dict(dx=A[0], dxs=24, n=1)),
+    (_distill, dict(dz=A[0], ds=104, n=1)),
 ])
 def test_in_place_that_fits_is_taken(lib, monkeypatch, call, over):   # noqa: F811
     """As far as the launch, which is not made."""
