@@ -69,13 +69,17 @@ def _rows(t: torch.Tensor, name: str, func: str):
     else:
         d, inner = t.shape[-1], t.stride(-1)
         n = t.numel() // d if d else 0
-        stride = t.stride(-2)
-        step = stride
-        for size, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
-            if size != 1 and s != step:
-                _refuse(_SIZE, func, f"{name}: leading dimensions {tuple(t.shape)} with strides "
-                        f"{t.stride()} are not rows of one stride")
-            step *= size
+        stride, step = t.stride(-2), 0          # of the rows, and of the next dimension
+        if n > 1:
+            for size, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+                if size == 1:                   # its stride is of no account
+                    continue
+                if step == 0:
+                    stride = step = s
+                if s != step or s == 0:
+                    _refuse(_SIZE, func, f"{name}: leading dimensions {tuple(t.shape)} with "
+                            f"strides {t.stride()} are not rows of one stride")
+                step *= size
     if inner != 1 and d > 1:
         _refuse(_SIZE, func, f"{name}: rows are not contiguous (strides {t.stride()})")
     # the stride of a single row is of no account
