@@ -8,7 +8,7 @@ the library.  A parameter or gradient may be a view into a flat buffer at any
 element.  Matrices need contiguous rows, of any stride; tensors of more than
 two dimensions, one stride over all leading ones.  Calls run on the given stream, by
 default torch's current one of the tensors' device, which must be the current
-device.
+device and the same for all of them.
 """
 from __future__ import annotations
 
@@ -24,6 +24,7 @@ ZERO_MAX_TEACHER = 1024
 _INVALID, _SIZE = -1, -3
 _ELEM = {torch.bfloat16: 2, torch.float32: 4}
 _IDS = {torch.int32: 4, torch.int64: 8}
+_I32 = {torch.int32: 4}
 _F32 = {torch.float32: 4}
 # the raw handle without building a Stream object, which costs as much as a call
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
@@ -34,24 +35,40 @@ def _refuse(code: int, func: str, message: str):
     raise ZeroError(code, message, func)
 
 
-def _bytes(t: torch.Tensor, types, name: str, func: str) -> int:
+def _here(t: torch.Tensor, name: str, func: str, device: int):
+    """The kernels reach a tensor only on the call's GPU, `device`.  (Called only
+    where a comparison beforehand leaves a doubt: small calls are host-bound.)"""
+    if t.get_device() != device or not t.is_cuda:
+        _refuse(_INVALID, func, f"{name} is on {t.device}: all tensors of a call have to be on "
+                "one GPU")
+
+
+def _bytes(t: torch.Tensor, types, name: str, func: str, device: int) -> int:
     b = types.get(t.dtype)
     if b is None:
         _refuse(_INVALID, func, f"{name}: type {t.dtype} is not one of "
                 + ", ".join(str(k) for k in types))
-    if not t.is_cuda:
-        _refuse(_INVALID, func, f"{name} is not a CUDA tensor")
+    if t.get_device() != device or device < 0:
+        _here(t, name, func, device)
     return b
 
 
-def _vector(t, n: int, types, name: str, func: str) -> int:
+def _vector(t, n: int, types, name: str, func: str, device: int) -> int:
     """Element size of an optional contiguous vector of n values (0 if None)."""
     if t is None:
         return 0
     if t.numel() != n or not t.is_contiguous():
         _refuse(_SIZE, func, f"{name}: {n} contiguous values are needed, got shape "
                 f"{tuple(t.shape)}, strides {t.stride()}")
-    return _bytes(t, types, name, func)
+    return _bytes(t, types, name, func, device)
+
+
+def _workspace(t, func: str, device: int):
+    if t is None:
+        return None
+    if t.get_device() != device or device < 0:
+        _here(t, "workspace", func, device)
+    return t.data_ptr()
 
 
 def _ptr(t):
@@ -93,9 +110,9 @@ def _table(t: torch.Tensor, name: str, func: str):
     return t.shape
 
 
-def _on(t: torch.Tensor, stream) -> int:
+def _on(device: int, stream) -> int:
     if stream is None:
-        return _current_stream(t.device.index)
+        return _current_stream(device)
     return stream if isinstance(stream, int) else int(stream.cuda_stream)
 
 
@@ -104,15 +121,15 @@ def zero_embedding(ids, weight, out, scale: float = 1.0, stream=None):
 
     ids: int32 or int64, contiguous, any shape; weight: (vocab, dim); out:
     rows of dim, one per id."""
-    f = "zero_embedding"
+    f, dev = "zero_embedding", out.get_device()
     vocab, dim = _table(weight, "weight", f)
     n, d, stride = _rows(out, "out", f)
     if d != dim or n != ids.numel():
         _refuse(_SIZE, f, f"out {tuple(out.shape)} does not hold {ids.numel()} rows of {dim}")
-    _check(load().zero_embedding(ids.data_ptr(), _vector(ids, n, _IDS, "ids", f), n,
-                                 weight.data_ptr(), _bytes(weight, _ELEM, "weight", f), vocab,
-                                 dim, scale, out.data_ptr(), _bytes(out, _ELEM, "out", f),
-                                 stride, _on(out, stream)), f)
+    _check(load().zero_embedding(ids.data_ptr(), _vector(ids, n, _IDS, "ids", f, dev), n,
+                                 weight.data_ptr(), _bytes(weight, _ELEM, "weight", f, dev), vocab,
+                                 dim, scale, out.data_ptr(), _bytes(out, _ELEM, "out", f, dev),
+                                 stride, _on(dev, stream)), f)
 
 
 def zero_embedding_grad_workspace_bytes(n_tokens: int, vocab: int, dim: int) -> int:
@@ -130,17 +147,17 @@ def zero_embedding_grad(ids, grad_out, grad_weight, scale: float = 1.0, accumula
 
     workspace: device buffer of at least
     zero_embedding_grad_workspace_bytes(tokens, vocab, dim) bytes."""
-    f = "zero_embedding_grad"
+    f, dev = "zero_embedding_grad", grad_weight.get_device()
     vocab, dim = _table(grad_weight, "grad_weight", f)
     n, d, stride = _rows(grad_out, "grad_out", f)
     if d != dim or n != ids.numel():
         _refuse(_SIZE, f, f"grad_out {tuple(grad_out.shape)} does not hold {ids.numel()} rows "
                 f"of {dim}")
     _check(load().zero_embedding_grad(
-        ids.data_ptr(), _vector(ids, n, _IDS, "ids", f), n, grad_out.data_ptr(),
-        _bytes(grad_out, _ELEM, "grad_out", f), stride, scale, grad_weight.data_ptr(),
-        _bytes(grad_weight, _ELEM, "grad_weight", f), vocab, dim, 1 if accumulate else 0,
-        _ptr(workspace), workspace_bytes, _on(grad_weight, stream)), f)
+        ids.data_ptr(), _vector(ids, n, _IDS, "ids", f, dev), n, grad_out.data_ptr(),
+        _bytes(grad_out, _ELEM, "grad_out", f, dev), stride, scale, grad_weight.data_ptr(),
+        _bytes(grad_weight, _ELEM, "grad_weight", f, dev), vocab, dim, 1 if accumulate else 0,
+        _workspace(workspace, f, dev), workspace_bytes, _on(dev, stream)), f)
 
 
 def zero_layer_norm(x, weight, bias, eps: float, out, mean=None, rstd=None, stream=None):
@@ -148,20 +165,22 @@ def zero_layer_norm(x, weight, bias, eps: float, out, mean=None, rstd=None, stre
 
     weight, bias: (dim,) of one type, or None (ones, zeros); mean, rstd: fp32,
     one value per row, or None; out may be x."""
-    f = "zero_layer_norm"
+    f, dev = "zero_layer_norm", x.get_device()
     n, d, x_stride = _rows(x, "x", f)
     m, e, out_stride = _rows(out, "out", f)
     if (m, e) != (n, d) or out.dtype != x.dtype:
         _refuse(_SIZE, f, f"out {tuple(out.shape)} {out.dtype} is not x {tuple(x.shape)} {x.dtype}")
-    wb = _vector(weight, d, _ELEM, "weight", f)
-    bb = _vector(bias, d, _ELEM, "bias", f)
+    if out.get_device() != dev or dev < 0:
+        _here(out, "out", f, dev)
+    wb = _vector(weight, d, _ELEM, "weight", f, dev)
+    bb = _vector(bias, d, _ELEM, "bias", f, dev)
     if wb and bb and wb != bb:
         _refuse(_INVALID, f, "weight and bias are of different types")
-    _vector(mean, n, _F32, "mean", f)
-    _vector(rstd, n, _F32, "rstd", f)
-    _check(load().zero_layer_norm(x.data_ptr(), _bytes(x, _ELEM, "x", f), n, d, x_stride,
+    _vector(mean, n, _F32, "mean", f, dev)
+    _vector(rstd, n, _F32, "rstd", f, dev)
+    _check(load().zero_layer_norm(x.data_ptr(), _bytes(x, _ELEM, "x", f, dev), n, d, x_stride,
                                   _ptr(weight), _ptr(bias), wb or bb or 4, eps, out.data_ptr(),
-                                  out_stride, _ptr(mean), _ptr(rstd), _on(x, stream)), f)
+                                  out_stride, _ptr(mean), _ptr(rstd), _on(dev, stream)), f)
 
 
 def zero_layer_norm_grad_workspace_bytes(n_rows: int, dim: int) -> int:
@@ -178,7 +197,7 @@ def zero_layer_norm_grad(grad_out, x, weight, mean, rstd, grad_x, grad_weight=No
     grad_x may be grad_out or x; grad_weight, grad_bias: (dim,) of the
     weight's type, or None; workspace: device buffer of at least
     zero_layer_norm_grad_workspace_bytes(rows, dim) bytes."""
-    f = "zero_layer_norm_grad"
+    f, dev = "zero_layer_norm_grad", x.get_device()
     n, d, x_stride = _rows(x, "x", f)
     my, ey, grad_out_stride = _rows(grad_out, "grad_out", f)
     mx, ex, grad_x_stride = _rows(grad_x, "grad_x", f)
@@ -187,21 +206,25 @@ def zero_layer_norm_grad(grad_out, x, weight, mean, rstd, grad_x, grad_weight=No
                 f"are not of x's shape {tuple(x.shape)}")
     if grad_out.dtype != x.dtype or grad_x.dtype != x.dtype:
         _refuse(_INVALID, f, "grad_out, x and grad_x are of different types")
-    sizes = {b for b in (_vector(weight, d, _ELEM, "weight", f),
-                         _vector(grad_weight, d, _ELEM, "grad_weight", f),
-                         _vector(grad_bias, d, _ELEM, "grad_bias", f)) if b}
+    if grad_out.get_device() != dev or dev < 0:
+        _here(grad_out, "grad_out", f, dev)
+    if grad_x.get_device() != dev or dev < 0:
+        _here(grad_x, "grad_x", f, dev)
+    sizes = {b for b in (_vector(weight, d, _ELEM, "weight", f, dev),
+                         _vector(grad_weight, d, _ELEM, "grad_weight", f, dev),
+                         _vector(grad_bias, d, _ELEM, "grad_bias", f, dev)) if b}
     if len(sizes) > 1:
         _refuse(_INVALID, f, "weight, grad_weight and grad_bias are of different types")
-    _vector(mean, n, _F32, "mean", f)
-    _vector(rstd, n, _F32, "rstd", f)
+    _vector(mean, n, _F32, "mean", f, dev)
+    _vector(rstd, n, _F32, "rstd", f, dev)
     _check(load().zero_layer_norm_grad(
-        grad_out.data_ptr(), x.data_ptr(), _bytes(x, _ELEM, "x", f), n, d, grad_out_stride,
+        grad_out.data_ptr(), x.data_ptr(), _bytes(x, _ELEM, "x", f, dev), n, d, grad_out_stride,
         x_stride, _ptr(weight), sizes.pop() if sizes else 4, _ptr(mean), _ptr(rstd),
-        grad_x.data_ptr(), grad_x_stride, _ptr(grad_weight), _ptr(grad_bias), _ptr(workspace),
-        workspace_bytes, _on(x, stream)), f)
+        grad_x.data_ptr(), grad_x_stride, _ptr(grad_weight), _ptr(grad_bias),
+        _workspace(workspace, f, dev), workspace_bytes, _on(dev, stream)), f)
 
 
-def _teacher(ids, teacher, n: int, func: str):
+def _teacher(ids, teacher, n: int, func: str, device: int):
     if ids.shape != teacher.shape or ids.dim() == 0 or not ids.is_contiguous() or \
             not teacher.is_contiguous():
         _refuse(_SIZE, func, f"teacher_ids {tuple(ids.shape)} and teacher_logits "
@@ -209,9 +232,8 @@ def _teacher(ids, teacher, n: int, func: str):
     top = ids.shape[-1]
     if ids.numel() != n * top:
         _refuse(_SIZE, func, f"teacher_ids {tuple(ids.shape)}: {n} rows are needed")
-    if ids.dtype != torch.int32 or not ids.is_cuda:
-        _refuse(_INVALID, func, "teacher_ids is not an int32 CUDA tensor")
-    return top, _bytes(teacher, _ELEM, "teacher_logits", func)
+    _bytes(ids, _I32, "teacher_ids", func, device)
+    return top, _bytes(teacher, _ELEM, "teacher_logits", func, device)
 
 
 def zero_distill_loss(logits, teacher_ids, teacher_logits, weights, temperature: float, loss,
@@ -223,22 +245,22 @@ def zero_distill_loss(logits, teacher_ids, teacher_logits, weights, temperature:
     teacher_ids (int32) and teacher_logits: (rows, top); entries with an id
     outside [0, vocab) are absent; weights: fp32 (rows,) or None; loss: fp32
     (rows,)."""
-    f = "zero_distill_loss"
+    f, dev = "zero_distill_loss", logits.get_device()
     n, vocab, stride = _rows(logits, "logits", f)
-    top, tb = _teacher(teacher_ids, teacher_logits, n, f)
-    _vector(weights, n, _F32, "weights", f)
-    _vector(loss, n, _F32, "loss", f)
+    top, tb = _teacher(teacher_ids, teacher_logits, n, f, dev)
+    _vector(weights, n, _F32, "weights", f, dev)
+    _vector(loss, n, _F32, "loss", f, dev)
     _check(load().zero_distill_loss(
-        logits.data_ptr(), _bytes(logits, _ELEM, "logits", f), n, vocab, stride,
+        logits.data_ptr(), _bytes(logits, _ELEM, "logits", f, dev), n, vocab, stride,
         teacher_ids.data_ptr(), teacher_logits.data_ptr(), tb, top, _ptr(weights), temperature,
-        _ptr(loss), _on(logits, stream)), f)
+        _ptr(loss), _on(dev, stream)), f)
 
 
 def zero_distill_loss_grad(logits, teacher_ids, teacher_logits, weights, temperature: float, loss,
                            grad_logits, stream=None):
     """zero_distill_loss and its gradient with respect to the logits, in one
     call; grad_logits may be logits."""
-    f = "zero_distill_loss_grad"
+    f, dev = "zero_distill_loss_grad", logits.get_device()
     n, vocab, stride = _rows(logits, "logits", f)
     m, v, grad_stride = _rows(grad_logits, "grad_logits", f)
     if (m, v) != (n, vocab):
@@ -246,10 +268,12 @@ def zero_distill_loss_grad(logits, teacher_ids, teacher_logits, weights, tempera
                 f"{tuple(logits.shape)}")
     if grad_logits.dtype != logits.dtype:
         _refuse(_INVALID, f, "grad_logits is not of logits' type")
-    top, tb = _teacher(teacher_ids, teacher_logits, n, f)
-    _vector(weights, n, _F32, "weights", f)
-    _vector(loss, n, _F32, "loss", f)
+    if grad_logits.get_device() != dev or dev < 0:
+        _here(grad_logits, "grad_logits", f, dev)
+    top, tb = _teacher(teacher_ids, teacher_logits, n, f, dev)
+    _vector(weights, n, _F32, "weights", f, dev)
+    _vector(loss, n, _F32, "loss", f, dev)
     _check(load().zero_distill_loss_grad(
-        logits.data_ptr(), _bytes(logits, _ELEM, "logits", f), n, vocab, stride,
+        logits.data_ptr(), _bytes(logits, _ELEM, "logits", f, dev), n, vocab, stride,
         teacher_ids.data_ptr(), teacher_logits.data_ptr(), tb, top, _ptr(weights), temperature,
-        _ptr(loss), _ptr(grad_logits), grad_stride, _on(logits, stream)), f)
+        _ptr(loss), _ptr(grad_logits), grad_stride, _on(dev, stream)), f)
