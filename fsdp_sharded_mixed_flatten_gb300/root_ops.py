@@ -63,9 +63,13 @@ def _vector(t, n: int, types, name: str, func: str, device: int) -> int:
     return _bytes(t, types, name, func, device)
 
 
-def _workspace(t, func: str, device: int):
+def _workspace(t, nbytes: int, func: str, device: int):
+    """Address of an optional workspace that holds the stated bytes."""
     if t is None:
         return None
+    if t.numel() * t.element_size() < nbytes or not t.is_contiguous():
+        _refuse(_SIZE, func, f"workspace of shape {tuple(t.shape)}, {t.dtype}, does not hold the "
+                f"stated {nbytes} contiguous bytes")
     if t.get_device() != device or device < 0:
         _here(t, "workspace", func, device)
     return t.data_ptr()
@@ -157,7 +161,7 @@ def zero_embedding_grad(ids, grad_out, grad_weight, scale: float = 1.0, accumula
         ids.data_ptr(), _vector(ids, n, _IDS, "ids", f, dev), n, grad_out.data_ptr(),
         _bytes(grad_out, _ELEM, "grad_out", f, dev), stride, scale, grad_weight.data_ptr(),
         _bytes(grad_weight, _ELEM, "grad_weight", f, dev), vocab, dim, 1 if accumulate else 0,
-        _workspace(workspace, f, dev), workspace_bytes, _on(dev, stream)), f)
+        _workspace(workspace, workspace_bytes, f, dev), workspace_bytes, _on(dev, stream)), f)
 
 
 def zero_layer_norm(x, weight, bias, eps: float, out, mean=None, rstd=None, stream=None):
@@ -221,7 +225,7 @@ def zero_layer_norm_grad(grad_out, x, weight, mean, rstd, grad_x, grad_weight=No
         grad_out.data_ptr(), x.data_ptr(), _bytes(x, _ELEM, "x", f, dev), n, d, grad_out_stride,
         x_stride, _ptr(weight), sizes.pop() if sizes else 4, _ptr(mean), _ptr(rstd),
         grad_x.data_ptr(), grad_x_stride, _ptr(grad_weight), _ptr(grad_bias),
-        _workspace(workspace, f, dev), workspace_bytes, _on(dev, stream)), f)
+        _workspace(workspace, workspace_bytes, f, dev), workspace_bytes, _on(dev, stream)), f)
 
 
 def _teacher(ids, teacher, n: int, func: str, device: int):

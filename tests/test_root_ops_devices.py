@@ -1,11 +1,12 @@
 """What the binding refuses because a tensor is not where it has to be: on the
-host, or on another GPU than the rest.  Nothing is launched."""
+host, on another GPU than the rest, or a workspace shorter than its stated
+bytes.  Nothing is launched."""
 import pytest
 import torch
 
 import fsdp_sharded_mixed_flatten_gb300 as zf
 
-INVALID = -1
+INVALID, SIZE = -1, -3
 F32, I32 = torch.float32, torch.int32
 
 
@@ -95,3 +96,12 @@ def test_a_tensor_of_another_gpu_is_refused(call, name):
     t = tensors[name]
     tensors[name] = torch.zeros(t.shape, dtype=t.dtype).as_subclass(_Gpu1)
     assert _code(fn, tensors) == INVALID
+
+
+@pytest.mark.parametrize("call", ["embedding_grad", "layer_norm_grad"])
+def test_a_short_workspace_is_refused(call):
+    fn, tensors = _calls()[call]
+    for ws in (_t((1 << 20) - 1, dtype=torch.uint8), _t(1 << 21, dtype=torch.uint8)[::2],
+               _t((1 << 18) - 1)):
+        assert _code(fn, dict(tensors, workspace=ws)) == SIZE
+    assert _code(fn, dict(tensors, workspace=_t(1 << 18))) == -4      # by its bytes
