@@ -75,8 +75,11 @@ int check_in_place(const void* out, int64_t out_stride, const void* in, int64_t 
     return ZERO_OK;
 }
 
+// A scalar that the kernels use in fp32.
+bool finite_f32(double x) { return std::isfinite(static_cast<float>(x)); }
+
 int check_table(int64_t n_tokens, int64_t vocab, int64_t dim, double scale) {
-    if (!std::isfinite(scale)) return fail(ZERO_ERR_INVALID_ARG, "scale must be finite");
+    if (!finite_f32(scale)) return fail(ZERO_ERR_INVALID_ARG, "scale must be finite in fp32");
     if (n_tokens < 0 || vocab < 1 || dim < 1)
         return fail(ZERO_ERR_INVALID_ARG, "n_tokens >= 0, vocab >= 1 and dim >= 1 are needed");
     if (n_tokens > kMax32 || vocab > kMax32 - 1 || dim > kMax32)
@@ -134,8 +137,7 @@ int distill(const void* logits, int32_t logits_bytes, int64_t n_rows, int64_t vo
     if (top > ZERO_MAX_TEACHER)
         return fail(ZERO_ERR_SIZE, "top = %lld exceeds %d", (long long)top, ZERO_MAX_TEACHER);
     if (!(temperature > 0.0) || !std::isfinite(temperature) ||
-        !std::isfinite(static_cast<float>(1.4426950408889634 / temperature)) ||
-        !std::isfinite(static_cast<float>(temperature * temperature)))
+        !finite_f32(1.4426950408889634 / temperature) || !finite_f32(temperature * temperature))
         return fail(ZERO_ERR_INVALID_ARG, "temperature must be positive and finite");
     if (int rc = check_type(logits_bytes, "logits_bytes")) return rc;
     if (int rc = check_type(teacher_bytes, "teacher_bytes")) return rc;
@@ -264,8 +266,8 @@ ZERO_API int zero_layer_norm(const void* x, int32_t act_bytes, int64_t n_rows, i
                              int32_t param_bytes, double eps, void* out, int64_t out_stride,
                              float* mean, float* rstd, void* stream) {
     if (int rc = check_norm(n_rows, dim, act_bytes, param_bytes)) return rc;
-    if (!(eps >= 0.0) || !std::isfinite(eps))
-        return fail(ZERO_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (!(eps >= 0.0) || !finite_f32(eps))
+        return fail(ZERO_ERR_INVALID_ARG, "eps must be >= 0 and finite in fp32");
     if (int rc = check_rows(x, n_rows, dim, x_stride, act_bytes, "x")) return rc;
     if (int rc = check_rows(out, n_rows, dim, out_stride, act_bytes, "out")) return rc;
     if (int rc = check_in_place(out, out_stride, x, x_stride, n_rows, "out")) return rc;
