@@ -534,7 +534,8 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
             float loss = 0.0f;
             for (int i = lane; i < ranks * EW; i += 32) loss += losses[f][i];
             loss = warp_sum(loss);
-            if (lane == 0) a.loss[row] = weight_of[f] * a.tau2 * 0.69314718f * loss;
+            // (one temperature after the other: their square may be below fp32)
+            if (lane == 0) a.loss[row] = weight_of[f] * a.tau * (a.tau * (0.69314718f * loss));
         }
     };
 

@@ -224,7 +224,6 @@ struct DistillArgs {
     float inv_tau;            // 1 / temperature
     float c;                  // log2(e) / temperature
     float tau;
-    float tau2;
     int32_t ranks;            // CTAs of a row, a power of two (set by the launch)
     int32_t rank_shift;
     int32_t stage_words;      // 16-byte words of a row that a CTA keeps

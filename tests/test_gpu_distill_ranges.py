@@ -116,3 +116,12 @@ def test_teacher_of_widely_spread_entries():
     t[2, ::2] = -1e9
     t[3, 3:] = -1e20
     _compare(z, ids, t, w, 0.5)
+
+
+@pytest.mark.parametrize("tau", [1e-22, 1e-18, 1e-8, 1e-3, 1e4, 1e15])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_temperatures_far_from_one(dtype, tau):
+    """Loss and gradient scale with the temperature, whose square may be too
+    small for fp32."""
+    z, ids, t, w = _inputs(6, 3001, 24, dtype, F32, "temperature")
+    _compare(z, ids, t, w, tau)
