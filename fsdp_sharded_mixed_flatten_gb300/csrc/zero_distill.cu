@@ -772,10 +772,10 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
 //    76 rows of 131072  19.0  17.0  19.0  21.2
 // (Several rows a cluster, to even out the last round of 1021 x 32003 in fp32,
 // took 134 us instead of 56: its barrier waits for the gradient's stores.)
-int ranks_for(int64_t rows, int64_t row_bytes) {
+int ranks_for(int64_t rows, int64_t row_bytes, int sms) {
     if (row_bytes <= kShortRow) return 1;
     int ranks = 1;
-    while (ranks < kMaxCluster && rows * ranks * 2 <= device_sms()) ranks *= 2;
+    while (ranks < kMaxCluster && rows * ranks * 2 <= sms) ranks *= 2;
     return ranks == 2 && row_bytes <= kMostBytes ? 1 : ranks;
 }
 
@@ -885,13 +885,15 @@ cudaError_t launch_shape(DistillArgs a, cudaStream_t stream) {
 template <class T, bool GRAD>
 cudaError_t launch(DistillArgs a, cudaStream_t stream) {
     const int64_t row_bytes = a.vocab * static_cast<int64_t>(sizeof(T));
-    const bool many = a.n_rows > 2 * device_sms();
+    int sms = 0;
+    if (cudaError_t e = device_sms(&sms); e != cudaSuccess) return e;
+    const bool many = a.n_rows > 2 * sms;
     a.ranks = 1;
     if (row_bytes <= room_for(4, a.top) && many)
         return launch_shape<T, GRAD, 3, 1>(a, stream);
     if (row_bytes <= room_for(8, a.top) && many)
         return launch_shape<T, GRAD, 6, 2>(a, stream);
-    a.ranks = ranks_for(a.n_rows, row_bytes);
+    a.ranks = ranks_for(a.n_rows, row_bytes, sms);
     // more entries than two warps hold cost the row's critical path: 4096 x 50257
     // with 128 of them 148 us with four warps, 158 with two (with 64 of 131072
     // 427 and 415)

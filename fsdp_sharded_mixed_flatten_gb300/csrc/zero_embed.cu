@@ -20,6 +20,7 @@
 // (1.6 GB: 176 us the zeros, 137 the sums).  Writing the zeros from CTAs of the sum
 // launch, beside its reads, was slower: 408 us instead of 325 then.
 #include "zero_ops.cuh"
+#include "zero_plan.cuh"
 
 #include <cooperative_groups.h>
 
@@ -104,9 +105,7 @@ __device__ __forceinline__ void zero_span(G* to, int64_t n, int lane) {
 
 // ---------------------------------------------------------------- sort ------
 
-constexpr int kSortCtas = 8;        // the cluster
-constexpr int kSortThreads = 1024;  // one token a thread and tile
-constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortThreads = 32 * kSortWarps;      // one token a thread and tile
 constexpr int kDigitBits = 9;
 constexpr int kDigits = 1 << kDigitBits;
 constexpr int kFillRows = 32768;    // rows of one bitmap of used rows (4 KB)
@@ -577,8 +576,8 @@ __host__ __device__ inline uint32_t bucket_mix(uint32_t high, int bits) {
 // Columns of a CTA: 16 bytes a lane of the wider type.
 __host__ __device__ constexpr int bucket_cols(int widest) { return 512 / widest; }
 
-Bucket bucket_for(int64_t n_tokens, int64_t vocab, int64_t dim, int widest) {
-    const int64_t most = 2 * device_sms() / ((dim + bucket_cols(widest) - 1) / bucket_cols(widest));
+Bucket bucket_for(int64_t n_tokens, int64_t vocab, int64_t dim, int widest, int sms) {
+    const int64_t most = 2 * sms / ((dim + bucket_cols(widest) - 1) / bucket_cols(widest));
     Bucket b{0, vocab, 0};
     while ((int64_t{2} << b.bits) <= most || b.rows > 8192) {
         if (b.bits == 16) break;
@@ -601,7 +600,7 @@ Bucket bucket_for(int64_t n_tokens, int64_t vocab, int64_t dim, int widest) {
 bool takes_buckets(int64_t n_tokens, int64_t vocab, int64_t dim) {
     if (n_tokens > kBucketTokens || (n_tokens > kFewTokens && n_tokens * dim > kBucketElements))
         return false;
-    const Bucket b = bucket_for(n_tokens, vocab, dim, 4);
+    const Bucket b = bucket_for(n_tokens, vocab, dim, 4, device_sms());
     return b.rows < (1 << (32 - kTokenBits)) && b.smem <= kBucketSmem &&
            dim <= 65535 * int64_t{bucket_cols(4)};
 }
@@ -858,7 +857,9 @@ embed_bucket_kernel(const __grid_constant__ EmbedGradArgs a, int bits, int n_row
 template <class Y, class G, int VEC, bool ACC>
 cudaError_t embed_buckets_as(const EmbedGradArgs& a, cudaStream_t stream) {
     constexpr int kWidth = bucket_cols(sizeof(Y) > sizeof(G) ? sizeof(Y) : sizeof(G));
-    const Bucket b = bucket_for(a.n_tokens, a.vocab, a.dim, 512 / kWidth);
+    int sms = 0;
+    if (cudaError_t e = device_sms(&sms); e != cudaSuccess) return e;
+    const Bucket b = bucket_for(a.n_tokens, a.vocab, a.dim, 512 / kWidth, sms);
     const dim3 grid(1u << b.bits, static_cast<unsigned>((a.dim + kWidth - 1) / kWidth));
     const auto kernel = embed_bucket_kernel<Y, G, VEC, ACC>;
     // more than 48 KB of shared memory need asking for
@@ -897,7 +898,9 @@ cudaError_t embed(const EmbedArgs& a, int want, cudaStream_t stream) {
                      a.dim % want == 0 && a.out_stride % want == 0;
     constexpr int kV = sizeof(W) == 2 && sizeof(Y) == 2 ? 8 : 4;
     const int tokens = 8 * (vec ? 4 : 2), width = 32 * (vec ? kV : 4);
-    const int64_t most = static_cast<int64_t>(device_sms()) * 64;
+    int sms = 0;
+    if (cudaError_t e = device_sms(&sms); e != cudaSuccess) return e;
+    const int64_t most = static_cast<int64_t>(sms) * 64;
     const int64_t x = (a.n_tokens + tokens - 1) / tokens, y = (a.dim + width - 1) / width;
     const dim3 grid(static_cast<unsigned>(x < most ? x : most),
                     static_cast<unsigned>(y < 65535 ? y : 65535));
@@ -963,16 +966,10 @@ cudaError_t launch_embed_buckets(const EmbedGradArgs& a, int grad_bytes, int gra
 }
 
 cudaError_t launch_embed_sort(const EmbedGradArgs& a, int grad_weight_bytes, cudaStream_t stream) {
-    // one cluster sorts; where every row is written, the rest of the GPU
-    // writes zeros meanwhile
-    int clusters = 1;
-    if (!a.accumulate) {
-        const int64_t rows = (a.vocab + kSortWarps - 1) / kSortWarps;
-        const int64_t most = 2 * device_sms() / kSortCtas - 1;
-        const int64_t need = (rows + kSortCtas - 1) / kSortCtas;
-        clusters += static_cast<int>(need < most ? need : most);
-    }
-    const unsigned g = static_cast<unsigned>(clusters * kSortCtas);
+    int sms = 0;
+    if (cudaError_t e = device_sms(&sms); e != cudaSuccess) return e;
+    const unsigned g =
+        static_cast<unsigned>(sort_clusters(a.vocab, a.accumulate != 0, sms) * kSortCtas);
     if (grad_weight_bytes == 4) embed_sort_kernel<float><<<g, kSortThreads, 0, stream>>>(a);
     else embed_sort_kernel<uint16_t><<<g, kSortThreads, 0, stream>>>(a);
     return cudaGetLastError();

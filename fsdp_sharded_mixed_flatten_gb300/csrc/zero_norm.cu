@@ -879,6 +879,8 @@ cudaError_t launch_shape(NormArgs a, cudaStream_t stream) {
     constexpr int B = sizeof(T);
     const Shape s = shape_for(a.dim, B, BACK);
     a.group_threads = s.group;
+    int sms = 0;
+    if (cudaError_t e = device_sms(&sms); e != cudaSuccess) return e;
     const unsigned g = static_cast<unsigned>(ctas_for(s, a.n_rows, a.dim, B, WIDE, BACK));
     const int threads = s.group * s.per_cta;
     const size_t smem = smem_of(s, a.dim, B, WIDE, BACK);

@@ -238,7 +238,12 @@ inline bool aligned_to(const void* p, int64_t bytes) {
     return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0;
 }
 
-// SMs of the current device (looked up once per device).
-int device_sms();
+// SMs of the current device (looked up once per device).  Launches take the
+// form that reports a failed look-up; plans without a launch count one SM then.
+cudaError_t device_sms(int* sms);
+inline int device_sms() {
+    int sms = 0;
+    return device_sms(&sms) == cudaSuccess ? sms : 1;
+}
 
 }  // namespace zf

@@ -1,10 +1,10 @@
 // Host side of the operators around the root unit declared in
 // include/zero_flat.h: argument checks, kernel arguments, launches.  Like the
 // rest of the library it allocates no memory and keeps nothing between calls.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <limits>
-#include <mutex>
 
 #include "zero_flat.h"
 #include "zero_ops.cuh"
@@ -15,17 +15,19 @@ static_assert(zf::kMaxTeacher == ZERO_MAX_TEACHER, "teacher entry limit mismatch
 
 namespace zf {
 
-int device_sms() {
-    static std::once_flag once[64];
-    static int sms[64];
+cudaError_t device_sms(int* sms) {
+    static std::atomic<int> known[64];          // 0: not looked up
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-    std::call_once(once[dev], [dev] {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) n = 1;
-        sms[dev] = n > 0 ? n : 1;
-    });
-    return sms[dev];
+    if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        const cudaError_t e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    *sms = n;
+    return cudaSuccess;
 }
 
 }  // namespace zf
