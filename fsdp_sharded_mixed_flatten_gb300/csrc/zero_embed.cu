@@ -892,11 +892,11 @@ cudaError_t embed_buckets(const EmbedGradArgs& a, cudaStream_t stream) {
 }
 
 template <class W, class Y>
-cudaError_t embed(const EmbedArgs& a, int want, cudaStream_t stream) {
-    const bool vec = aligned_to(a.weight, want * static_cast<int64_t>(sizeof(W))) &&
-                     aligned_to(a.out, want * static_cast<int64_t>(sizeof(Y))) &&
-                     a.dim % want == 0 && a.out_stride % want == 0;
+cudaError_t embed(const EmbedArgs& a, cudaStream_t stream) {
     constexpr int kV = sizeof(W) == 2 && sizeof(Y) == 2 ? 8 : 4;
+    const bool vec = aligned_to(a.weight, kV * static_cast<int64_t>(sizeof(W))) &&
+                     aligned_to(a.out, kV * static_cast<int64_t>(sizeof(Y))) &&
+                     a.dim % kV == 0 && a.out_stride % kV == 0;
     const int tokens = 8 * (vec ? 4 : 2), width = 32 * (vec ? kV : 4);
     int sms = 0;
     if (cudaError_t e = device_sms(&sms); e != cudaSuccess) return e;
@@ -942,10 +942,9 @@ cudaError_t embed_sum(const EmbedGradArgs& a, cudaStream_t stream) {
 cudaError_t launch_embed(const EmbedArgs& a, int weight_bytes, int out_bytes,
                          cudaStream_t stream) {
     if (weight_bytes == 2)
-        return out_bytes == 2 ? embed<uint16_t, uint16_t>(a, 8, stream)
-                              : embed<uint16_t, float>(a, 4, stream);
-    return out_bytes == 2 ? embed<float, uint16_t>(a, 4, stream)
-                          : embed<float, float>(a, 4, stream);
+        return out_bytes == 2 ? embed<uint16_t, uint16_t>(a, stream)
+                              : embed<uint16_t, float>(a, stream);
+    return out_bytes == 2 ? embed<float, uint16_t>(a, stream) : embed<float, float>(a, stream);
 }
 
 int64_t embed_grad_workspace(int64_t n_tokens, int64_t vocab, int64_t dim) {

@@ -391,8 +391,8 @@ norm_kernel(const __grid_constant__ NormArgs a) {
     constexpr int kDepth = depth_of(SHIFT ? kShift : VEC > 1 ? kWide : kSingle, E, sizeof(T), 1);
     constexpr bool kAsync = kDepth > 0;
     extern __shared__ __align__(16) char params[];           // weight, bias, rows
-    constexpr int kBatch = 1, P = E / 2;
-    __shared__ float2 red[2][kBatch][kNormWarps];
+    constexpr int P = E / 2;
+    __shared__ float2 red[2][kNormWarps];
     int half = 0;
     const Group g(a.group_threads);
     const Columns<VEC, E> c(g, a.dim);
@@ -418,12 +418,12 @@ norm_kernel(const __grid_constant__ NormArgs a) {
         b.put(v);
     }
     const bool ragged = a.dim % VEC != 0;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * g.per_cta * kBatch;
-    int64_t row = (static_cast<int64_t>(blockIdx.x) * g.per_cta + g.index) * kBatch;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * g.per_cta;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * g.per_cta + g.index;
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride + (SHIFT ? 0 : c.first);
     T* out = static_cast<T*>(a.out) + row * a.out_stride + (SHIFT ? 0 : c.first);
     const T* here = x;                                       // the row worked on
-    Row<T, VEC, E> next[kBatch];
+    Row<T, VEC, E> next;
     // this thread's words of row slot k, or with SHIFT its group's: at held + k * slot
     const uint32_t slot = SHIFT ? 16 * Shift<T, E>::words(g) : sizeof(T) * E * blockDim.x;
     char* held = params + 2 * sizeof(float) * E * blockDim.x +
@@ -445,7 +445,7 @@ norm_kernel(const __grid_constant__ NormArgs a) {
     if constexpr (kAsync) {
         for (int k = 0; k < kDepth - 1; ++k) copy_next();
     } else {
-        next[0].load(x, row < a.n_rows, c);
+        next.load(x, row < a.n_rows, c);
     }
     for (; row < a.n_rows; row += step, out += step * a.out_stride) {
         uint4* const words = reinterpret_cast<uint4*>(held + get * slot);
@@ -454,88 +454,70 @@ norm_kernel(const __grid_constant__ NormArgs a) {
             cp_async_wait<kDepth - 2 < 0 ? 0 : kDepth - 2>();
             g.sync_any();
             copy_next();
-            Shift<T, E>::read(next[0], words, here, g);
+            Shift<T, E>::read(next, words, here, g);
             here += step * a.x_stride;
             get = get + 1 == kDepth ? 0 : get + 1;
         } else if constexpr (kAsync) {
             copy_next();
             cp_async_wait<kDepth - 1 < 0 ? 0 : kDepth - 1>();
-            next[0].read(held + get * slot);
+            next.read(held + get * slot);
             get = get + 1 == kDepth ? 0 : get + 1;
         }
-        Pair v[kBatch][P];
+        Pair v[P];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-#pragma unroll
-            for (int j = 0; j < P; ++j) v[i][j] = next[i][j];
-        }
+        for (int j = 0; j < P; ++j) v[j] = next[j];
         if constexpr (!kAsync) {
             x += step * a.x_stride;
-            next[0].load(x, row + step < a.n_rows, c);
+            next.load(x, row + step < a.n_rows, c);
         }
-        float2 s[kBatch];        // a warp's sum, and its squares about its mean
+        float2 s;                // a warp's sum, and its squares about its mean
+        Pair t = v[0];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            Pair t = v[i][0];
+        for (int j = 1; j < P; ++j) t = add2(t, v[j]);
+        s.x = warp_sum(both(t));
+        const Pair m = splat(-s.x * inv_n);
+        Pair q = 0;
 #pragma unroll
-            for (int j = 1; j < P; ++j) t = add2(t, v[i][j]);
-            s[i].x = warp_sum(both(t));
-            const Pair m = splat(-s[i].x * inv_n);
-            Pair q = 0;
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                Pair d = add2(v[i][j], m);
-                if (VEC == 1 || ragged) {
-                    const float2 f = unpair(d);
-                    d = pair(c.ok(2 * j / VEC, 2 * j % VEC) ? f.x : 0.0f,
-                             c.ok((2 * j + 1) / VEC, (2 * j + 1) % VEC) ? f.y : 0.0f);
-                } else {
-                    d = c.left[2 * j / VEC] != 0 ? d : 0;
-                }
-                q = fma2(d, d, q);
+        for (int j = 0; j < P; ++j) {
+            Pair d = add2(v[j], m);
+            if (VEC == 1 || ragged) {
+                const float2 f = unpair(d);
+                d = pair(c.ok(2 * j / VEC, 2 * j % VEC) ? f.x : 0.0f,
+                         c.ok((2 * j + 1) / VEC, (2 * j + 1) % VEC) ? f.y : 0.0f);
+            } else {
+                d = c.left[2 * j / VEC] != 0 ? d : 0;
             }
-            s[i].y = warp_sum(both(q));
+            q = fma2(d, d, q);
         }
+        s.y = warp_sum(both(q));
         if (g.warps > 1) {
             const int w0 = g.index * g.warps;
-            if (lane == 0) {
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) red[half][i][w0 + g.t / 32] = s[i];
-            }
+            if (lane == 0) red[half][w0 + g.t / 32] = s;
             g.sync();
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const float2 o =
-                    lane < g.warps ? red[half][i][w0 + lane] : make_float2(0.0f, 0.0f);
-                s[i].x = warp_sum(o.x);
-                const float d = __fmaf_rn(o.x, lane_inv_n, -s[i].x * inv_d);
-                s[i].y = warp_sum(lane < g.warps ? __fmaf_rn(lane_n * d, d, o.y) : 0.0f);
-            }
+            const float2 o = lane < g.warps ? red[half][w0 + lane] : make_float2(0.0f, 0.0f);
+            s.x = warp_sum(o.x);
+            const float d = __fmaf_rn(o.x, lane_inv_n, -s.x * inv_d);
+            s.y = warp_sum(lane < g.warps ? __fmaf_rn(lane_n * d, d, o.y) : 0.0f);
             half ^= 1;
         }
+        const float mu = s.x * inv_d;
+        const float r = inv_sqrt(__fmaf_rn(s.y, inv_d, a.eps));
+        if (g.t == 0) {
+            if (a.mean != nullptr) a.mean[row] = mu;
+            if (a.rstd != nullptr) a.rstd[row] = r;
+        }
+        const Pair m2 = splat(-mu), r2 = splat(r);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (row + i >= a.n_rows) break;
-            const float mu = s[i].x * inv_d;
-            const float r = inv_sqrt(__fmaf_rn(s[i].y, inv_d, a.eps));
-            if (g.t == 0) {
-                if (a.mean != nullptr) a.mean[row + i] = mu;
-                if (a.rstd != nullptr) a.rstd[row + i] = r;
-            }
-            const Pair m2 = splat(-mu), r2 = splat(r);
-#pragma unroll
-            for (int j = 0; j < P / 2; ++j) {
-                const ulonglong2 wj = w[j], bj = b[j];
-                Pair *y0 = &v[i][2 * j], *y1 = &v[i][2 * j + 1];
-                *y0 = fma2(mul2(add2(*y0, m2), r2), wj.x, bj.x);
-                *y1 = fma2(mul2(add2(*y1, m2), r2), wj.y, bj.y);
-            }
-            if constexpr (SHIFT) {
-                if (g.warps == 1) __syncwarp();          // the others: at the sums
-                Shift<T, E>::store(out, v[0], words, a.dim, g);
-            } else {
-                store_row<T, VEC, E>(out + i * a.out_stride, v[i], c);
-            }
+        for (int j = 0; j < P / 2; ++j) {
+            const ulonglong2 wj = w[j], bj = b[j];
+            v[2 * j] = fma2(mul2(add2(v[2 * j], m2), r2), wj.x, bj.x);
+            v[2 * j + 1] = fma2(mul2(add2(v[2 * j + 1], m2), r2), wj.y, bj.y);
+        }
+        if constexpr (SHIFT) {
+            if (g.warps == 1) __syncwarp();              // the others: at the sums
+            Shift<T, E>::store(out, v, words, a.dim, g);
+        } else {
+            store_row<T, VEC, E>(out, v, c);
         }
     }
 }

@@ -221,7 +221,6 @@ struct DistillArgs {
     int64_t vocab;
     int32_t top;
     int32_t teacher_f32;
-    float inv_tau;            // 1 / temperature
     float c;                  // log2(e) / temperature
     float tau;
     int32_t ranks;            // CTAs of a row, a power of two (set by the launch)

@@ -169,7 +169,6 @@ int distill(const void* logits, int32_t logits_bytes, int64_t n_rows, int64_t vo
     a.vocab = vocab;
     a.top = static_cast<int32_t>(top);
     a.teacher_f32 = teacher_bytes == 4;
-    a.inv_tau = static_cast<float>(1.0 / temperature);
     a.c = static_cast<float>(1.4426950408889634 / temperature);
     a.tau = static_cast<float>(temperature);
     return cuda_call(with_grad ? "distillation loss and gradient launch"
