@@ -22,11 +22,11 @@
 // cluster barrier waits for the gradient's stores to arrive: 4096 x 50257 took
 // 221 us with clusters of one CTA and a split barrier).
 //
-// Measured, loss and gradient: 4096 x 50257 bf16 with 64 entries 141 us (5.8 TB/s),
-// 4096 x 25000 fp32 6.2 TB/s, 8192 x 131072 bf16 with 128 entries 854 us (5.0 TB/s; its
-// words beyond shared memory come from L2 a second time), 1021 x 32003 fp32
-// 55.5 us (4.7 TB/s: 3.4 rounds of 304 CTAs take as long as 4), 16 x 50257 the loss
-// alone 8.2 us, as long as the host takes for a call.
+// Measured, loss and gradient: 4096 x 50257 bf16 with 64 entries 140 us (5.5 TB/s of
+// the rows that have a weight), 4096 x 25000 fp32 6.2 TB/s, 8192 x 131072 bf16 with 128
+// entries 852 us (5.0 TB/s; its words beyond shared memory come from L2 a second time),
+// 1021 x 32003 fp32 55.7 us (4.6 TB/s: 3.4 rounds of 304 CTAs take as long as 4), 16 x
+// 50257 the loss alone 8.2 us, as long as the host takes for a call.
 //
 // Exponentials are 2^(z c - M), c = log2(e) / tau: one fused multiply-add and
 // one ex2 each.  M is an integer, ceil(c max z) of what a thread has seen, so
@@ -93,7 +93,8 @@ __device__ __forceinline__ void store16(void* dst, uint4 v, uint64_t policy) {
                  : "memory");
 }
 // Words beyond shared memory: kept in L2 from the first reading, let go at the
-// second.
+// second, which is the gradient's.  (The loss alone reads them once, and has them
+// kept all the same.)
 __device__ __forceinline__ uint64_t l2_keep() {
     uint64_t p;
     asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));

@@ -15,10 +15,11 @@
 //     timing, so neither does any result.
 // Few tokens take one launch instead, of buckets (below).
 //
-// Bound by memory's rate for writes where every row is written: zeros alone take
-// it to 4.7 TB/s at most, 65536 tokens of 4096 bf16 columns into 131072 rows 313 us
-// (1.6 GB: 176 us the zeros, 137 the sums).  Writing the zeros from CTAs of the sum
-// launch, beside its reads, was slower: 408 us instead of 325 then.
+// Where every row is written, most of the time goes into zeros: 65536 tokens of
+// 4096 bf16 columns into 131072 rows take 322 us (1.6 GB, 5.0 TB/s), 174 to 182 us of
+// them the sort launch with 0.90 GB of zeros (5.1 TB/s; a fill runs at 7.5), 137 to
+// 140 the sums.  Writing the zeros from CTAs of the
+// sum launch, beside its reads, was slower: 408 us instead of 325 then.
 #include "zero_ops.cuh"
 #include "zero_plan.cuh"
 
@@ -554,7 +555,7 @@ constexpr int kBucketThreads = 512;
 constexpr int kBucketWarps = kBucketThreads / 32;
 constexpr int kTokenBits = 14;
 constexpr int64_t kBucketTokens = 1 << kTokenBits;
-constexpr int64_t kFewTokens = 8192;                 // up to here always
+constexpr int64_t kFewTokens = 8192;                 // up to here whatever the width
 constexpr int64_t kBucketElements = 10 << 20;        // and up to here beyond
 constexpr int kBucketSmem = 160 * 1024;              // beside 33 KB of static memory
 
@@ -596,7 +597,8 @@ Bucket bucket_for(int64_t n_tokens, int64_t vocab, int64_t dim, int widest, int 
 //    8192     16.9 / 29.8  23.0 / 30.0  34.1 / 37.9   55.1 / 52.4
 //   12288     22.1 / 33.1  32.3 / 34.5  56.0 / 45.5  102.6 / 63.3
 //   16384     28.1 / 35.3  39.9 / 37.3  80.5 / 55.5  137.5 / 74.4
-// (4096 fp32 columns: 6144 tokens 60.2 / 69.9, 8192 92.8 / 86.5).
+// (4096 fp32 columns: 6144 tokens 60.2 / 69.9, 8192 92.8 / 86.5).  So at kFewTokens
+// rows of 4096 columns lose 5 to 7 % by the one launch; wider ones are not measured.
 bool takes_buckets(int64_t n_tokens, int64_t vocab, int64_t dim) {
     if (n_tokens > kBucketTokens || (n_tokens > kFewTokens && n_tokens * dim > kBucketElements))
         return false;

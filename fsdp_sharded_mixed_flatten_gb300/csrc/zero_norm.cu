@@ -15,9 +15,9 @@
 // second launch adds up in CTA order.
 //
 // Bound by memory where rows are many: forward of 16384 x 4096 bf16 50 us (5.4 TB/s),
-// backward of 8192 x 8192 bf16 78 us (5.1 TB/s), of 8192 x 768 bf16 14.4 us (2.6 TB/s: the
+// backward of 8192 x 8192 bf16 78 us (5.1 TB/s), of 8192 x 768 bf16 14.6 us (2.6 TB/s: the
 // launch, the first rows and the second launch are most of it).  Few rows take as
-// long as the host's call: 8 x 768 7.2 us forward, 9.5 us backward.
+// long as the host's call: 8 x 768 7.5 us forward, 9.1 us backward.
 //
 // The variance is taken about a mean at every step: a warp's squares about the
 // warp's mean, then sum (M2_w + n_w (mean_w - mu)^2) over the warps of the
@@ -806,9 +806,10 @@ size_t smem_of(const Shape& s, int64_t dim, int elem, bool wide, bool back) {
 
 // Rows of the backward pass that one CTA takes by itself: what it adds up are
 // the sums, and the second launch is saved.  Up to 2048 columns 8 rounds of its
-// groups and 24576 elements (one launch / two, in us: bf16 32 x 768 9.6 / 11.1,
-// 64 x 768 13.0 / 11.8, fp32 32 x 768 in 16 rounds 14.8 / 11.6), beyond one round
-// (8 x 4096 bf16 in four 12.8 / 11.6).  The short ones are held up by the host.
+// groups and 24576 elements (one launch / two, in us: 32 x 768 bf16, four rounds,
+// 9.2 / 10.8, fp32, seven, 10.2 / 10.8, 64 x 768 bf16 13.0 / 11.8), beyond one round
+// (8 x 4096 bf16 in four 12.8 / 11.6).  The host holds these up: replayed from a graph,
+// 16 x 768 takes 4.9 / 5.2 in bf16 and 5.5 / 4.9 in fp32, 32 x 768 6.7 / 5.3 and 7.7 / 5.0.
 int64_t rows_alone(const Shape& s, int64_t dim) {
     if (s.e > 8) return s.per_cta;
     const int64_t by_size = 24576 / dim;

@@ -5,8 +5,8 @@
 // bf16 values travel as uint16_t.  A parameter or its gradient may be a piece
 // of a flat buffer that starts at any element, and rows may have any stride,
 // so every kernel comes in a form with vector accesses (VEC elements, up to 16
-// bytes) and one with single elements (VEC = 1); the host picks the widest
-// that every address and stride of the call allows (vec_elems).
+// bytes) and one with single elements (VEC = 1); the host picks the first where
+// every address and stride of the call allows it.
 #pragma once
 
 #include <cstdint>

@@ -1,6 +1,7 @@
 // Host side of the operators around the root unit declared in
 // include/zero_flat.h: argument checks, kernel arguments, launches.  Like the
-// rest of the library it allocates no memory and keeps nothing between calls.
+// rest of the library it allocates no memory, and keeps nothing of a call but what
+// the device answered (its SMs, a kernel's attributes and resident clusters).
 #include <atomic>
 #include <cmath>
 #include <cstdint>

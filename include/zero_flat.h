@@ -500,8 +500,8 @@ int zero1_step(const float* const* full_accum, int32_t n_micro, float* const* ma
  *   ids[n_tokens]          int32 or int64
  *   weight                 [vocab][dim] contiguous
  *   out                    n_tokens rows of dim
- * Errors: INVALID_ARG, MISALIGNED, SIZE (n_tokens, vocab or dim beyond 32
- * bits, a stride below dim), CUDA.
+ * Errors: INVALID_ARG (scale not finite in fp32, ...), MISALIGNED, SIZE
+ * (n_tokens, vocab or dim beyond 32 bits, a stride below dim), CUDA.
  */
 int zero_embedding(const void* ids, int32_t id_bytes, int64_t n_tokens, const void* weight,
                    int32_t weight_bytes, int64_t vocab, int64_t dim, double scale, void* out,
@@ -543,7 +543,8 @@ int zero_embedding_grad_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t
  *                     (with the same stride)
  *   weight, bias      dim values of type param_bytes; NULL: ones, zeros
  *   mean, rstd        n_rows fp32 each, or NULL where no backward pass follows
- * Errors: INVALID_ARG, MISALIGNED, SIZE (dim > ZERO_MAX_NORM_DIM), CUDA.
+ * Errors: INVALID_ARG (eps negative or not finite in fp32, ...), MISALIGNED,
+ * SIZE (dim > ZERO_MAX_NORM_DIM, in place with another stride), CUDA.
  */
 #define ZERO_MAX_NORM_DIM 16384
 int zero_layer_norm(const void* x, int32_t act_bytes, int64_t n_rows, int64_t dim,
@@ -592,8 +593,10 @@ int zero_layer_norm_grad_workspace_bytes(int64_t n_rows, int64_t dim, int64_t* b
  *   grad_logits[v] = weight * temperature * (q_v - sum_{k: id_k = v} p_k)
  * (0 in rows whose loss is 0 for want of weight or entries), of the logits'
  * type; grad_logits may be logits (with the same stride).
- * Errors: INVALID_ARG (temperature not positive and finite, ...), MISALIGNED,
- * SIZE, CUDA.
+ * Logits and teacher logits may lie anywhere in their types' ranges, masks' finite
+ * values among them; only differences within a row and its entries count.
+ * Errors: INVALID_ARG (temperature not positive, its square or its inverse not
+ * finite in fp32, ...), MISALIGNED, SIZE, CUDA.
  */
 #define ZERO_MAX_TEACHER 1024
 int zero_distill_loss(const void* logits, int32_t logits_bytes, int64_t n_rows, int64_t vocab,
