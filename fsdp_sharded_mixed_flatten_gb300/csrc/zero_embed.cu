@@ -43,8 +43,8 @@ __device__ __forceinline__ int64_t ld_id(const void* ids, int id64, int64_t t) {
 // A warp takes R tokens and 32 N packs of columns: R N loads are under way at
 // once, without conditions (an id outside the table reads row 0, a column beyond
 // the row column 0).  One element a thread, its place found by division, took
-// 58.7 us for 16384 x 1259 in fp32 from an odd element on, so it takes 29.7 (5.6 TB/s);
-// 16384 x 768 bf16 8.7 us instead of 12.8.
+// 58.7 us for 16384 x 1259 in fp32 from an odd element on, so it takes 29.2; 16384 x
+// 768 bf16 8.7 us instead of 12.8 where L2 holds the rows, 10.7 from memory.
 template <class W, class Y, int VEC, int R, int N>
 __global__ void __launch_bounds__(256) embed_kernel(const __grid_constant__ EmbedArgs a) {
     const int lane = threadIdx.x;
