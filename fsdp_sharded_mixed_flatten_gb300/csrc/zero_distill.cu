@@ -185,7 +185,7 @@ struct Running {
 // Joined over a warp: the largest off, every sum scaled to it.
 __device__ __forceinline__ Running warp_join(Running r) {
     float off;
-    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(off) : "f"(r.off));
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(off) : "f"(r.off));
     return {off, warp_sum(r.s * ex2(r.off - off))};
 }
 
@@ -569,7 +569,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
         Running rt{kNone, 0.0f};
         float entry_off = kNone;
         for (int j = lane; j < ranks * EW; j += 32) entry_off = fmaxf(entry_off, entry_sums[buf][j].off);
-        asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(entry_off) : "f"(entry_off));
+        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(entry_off) : "f"(entry_off));
         const bool live = entry_off != kNone;         // the row has an entry
         const bool far_entries = live && !(fabsf(entry_off) < kFar);
         if (!worker) {
