@@ -2,7 +2,7 @@
 FlatParameter, with all N_d logical data-parallel ranks held in one GPU.
 
 The compute lives in the CUDA library declared by ``include/zero_flat.h``;
-``zero`` and ``root_ops`` are its thin ctypes binding (same function names), ``buffers`` lays
+``zero``, ``root_ops`` and ``layer_ops`` are its thin ctypes binding (same function names), ``buffers`` lays
 out per-rank device buffers with PyTorch allocations, ``synthetic`` draws the
 seeded synthetic workloads, and ``build`` compiles the library in-tree.
 """
@@ -18,6 +18,8 @@ from .root_ops import (ZERO_MAX_NORM_DIM, ZERO_MAX_TEACHER, zero_distill_loss,
                        zero_distill_loss_grad, zero_embedding, zero_embedding_grad,
                        zero_embedding_grad_workspace_bytes, zero_layer_norm, zero_layer_norm_grad,
                        zero_layer_norm_grad_workspace_bytes)
+from .layer_ops import (ZERO_EIGHT_BLOCK, zero_pack_rows, zero_rms_norm, zero_rms_norm_grad,
+                        zero_rms_norm_grad_workspace_bytes, zero_unpack_rows)
 
 __all__ = [
     "ZERO_MAX_RANKS", "zero1_accumulate", "zero1_step", "zero_param_layout", "zero_shard_numel", "ZeroAdamW", "ZeroError", "ZeroLayout", "load", "zero_abi_version",
@@ -30,4 +32,6 @@ __all__ = [
     "ZERO_MAX_NORM_DIM", "ZERO_MAX_TEACHER", "zero_distill_loss", "zero_distill_loss_grad",
     "zero_embedding", "zero_embedding_grad", "zero_embedding_grad_workspace_bytes",
     "zero_layer_norm", "zero_layer_norm_grad", "zero_layer_norm_grad_workspace_bytes",
+    "ZERO_EIGHT_BLOCK", "zero_pack_rows", "zero_rms_norm", "zero_rms_norm_grad",
+    "zero_rms_norm_grad_workspace_bytes", "zero_unpack_rows",
 ]

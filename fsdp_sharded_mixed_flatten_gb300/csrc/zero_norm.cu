@@ -345,13 +345,6 @@ __device__ __forceinline__ float both(Pair p) {
 
 __device__ __forceinline__ Pair splat(float x) { return pair(x, x); }
 
-// 1 / sqrt(x): the approximation and one Newton step.
-__device__ __forceinline__ float inv_sqrt(float x) {
-    const float y = rsqrtf(x);
-    const float z = y * __fmaf_rn(-0.5f * x * y, y, 1.5f);
-    return y == __builtin_huge_valf() ? y : z;
-}
-
 // Sums of a pair of values over a group, in a fixed order: lanes, then warps.
 // The first exchange leaves one value to each half of the warp, so that five
 // steps add up both.  `red` has two halves that are used in turn: one barrier a

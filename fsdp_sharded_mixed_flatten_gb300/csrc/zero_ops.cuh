@@ -133,6 +133,13 @@ __device__ __forceinline__ float warp_max(float x) {
     return x;
 }
 
+// 1 / sqrt(x): the approximation and one Newton step.
+__device__ __forceinline__ float inv_sqrt(float x) {
+    const float y = rsqrtf(x);
+    const float z = y * __fmaf_rn(-0.5f * x * y, y, 1.5f);
+    return y == __builtin_huge_valf() ? y : z;
+}
+
 // --------------------------------------------------------- token table ------
 
 struct EmbedArgs {
@@ -203,6 +210,56 @@ int norm_grad_ctas(int64_t n_rows, int64_t dim);
 cudaError_t launch_norm(const NormArgs& a, int act_bytes, cudaStream_t stream);
 cudaError_t launch_norm_grad(const NormArgs& a, int act_bytes, cudaStream_t stream);
 cudaError_t launch_norm_grad_reduce(const NormArgs& a, int act_bytes, cudaStream_t stream);
+
+// -------------------------------- root-mean-square norm, rows in 8 bits ------
+
+struct RmsArgs {
+    const void* x;            // rows of x_stride elements; backward: s, or null where in 8 bits
+    const void* residual;     // forward; may be null
+    const void* grad_out;     // backward
+    const void* grad_total;   // backward; may be null
+    const void* weight;       // dim values, or null (ones)
+    void* total;              // forward: s; may be null
+    void* out;                // forward: the output; backward: the output again; may be null
+    void* grad_x;
+    void* grad_weight;        // dim values, or null
+    uint8_t* out8;            // forward: the output in 8 bits, or null
+    float* out8_scales;
+    uint8_t* total8;          // s in 8 bits: forward written, backward read; or null
+    float* total8_scales;
+    float* rstd;              // n_rows; may be null in the forward
+    float* partials;          // [CTAs][dim] column sums of the backward
+    int64_t n_rows;
+    int64_t x_stride, residual_stride, grad_out_stride, grad_total_stride;
+    int64_t total_stride, out_stride, grad_x_stride, out8_stride, total8_stride;
+    int32_t dim;
+    int32_t blocks;           // scales of a row
+    int32_t param_f32;        // weight and its gradient are fp32
+    int32_t group_threads;    // threads that hold a row (set by the launch)
+    float eps;
+};
+
+// CTAs of the backward launch, which writes a partial row of column sums each.
+int rms_grad_ctas(int64_t n_rows, int64_t dim);
+cudaError_t launch_rms_norm(RmsArgs a, int act_bytes, cudaStream_t stream);
+cudaError_t launch_rms_norm_grad(RmsArgs a, int act_bytes, cudaStream_t stream);
+cudaError_t launch_rms_reduce(const RmsArgs& a, cudaStream_t stream);
+
+struct EightArgs {
+    const void* x;            // rows to pack
+    void* out;                // or to unpack to (then x is null)
+    uint8_t* codes;
+    float* scales;            // [n_rows][blocks]
+    int64_t n_rows;
+    int64_t dim;
+    int64_t blocks;
+    int64_t x_stride;         // of x or out
+    int64_t codes_stride;
+    int64_t section;          // columns of a row that a warp takes (set by the launch)
+    int64_t sections;
+};
+
+cudaError_t launch_eight(EightArgs a, int act_bytes, cudaStream_t stream);
 
 // --------------------------------------------------- distillation loss ------
 

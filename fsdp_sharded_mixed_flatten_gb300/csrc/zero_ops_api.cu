@@ -371,3 +371,217 @@ ZERO_API int zero_distill_loss_grad(const void* logits, int32_t logits_bytes, in
                    teacher_bytes, top, weights, temperature, loss, grad_logits, grad_logits_stride,
                    true, stream);
 }
+
+namespace {
+
+constexpr int64_t kBlock = 128;             // columns of a scale
+
+int check_eight(const void* codes, const void* scales, int64_t n, int64_t dim, int64_t stride,
+                const char* name) {
+    if (int rc = check_rows(codes, n, dim, stride, 1, name)) return rc;
+    if (n > 0) {
+        if (scales == nullptr) return fail(ZERO_ERR_INVALID_ARG, "%s: its scales are NULL", name);
+        if (!zf::aligned_to(scales, 4))
+            return fail(ZERO_ERR_MISALIGNED, "%s: its scales are not aligned", name);
+    }
+    return ZERO_OK;
+}
+
+// An optional matrix: nothing, or rows.
+int check_maybe_rows(const void* p, int64_t n, int64_t dim, int64_t stride, int32_t bytes,
+                     const char* name) {
+    return p == nullptr ? ZERO_OK : check_rows(p, n, dim, stride, bytes, name);
+}
+
+int eight(const void* x, void* out, int32_t bytes, int64_t n_rows, int64_t dim, int64_t stride,
+          uint8_t* codes, int64_t codes_stride, float* scales, void* stream) {
+    const bool pack = out == nullptr;
+    if (n_rows < 0 || dim < 1)
+        return fail(ZERO_ERR_INVALID_ARG, "n_rows >= 0 and dim >= 1 are needed");
+    // as many CTAs as a launch takes
+    if (n_rows > kMax32 || dim > kMax32 || n_rows * ((dim + 1023) / 1024) > kMax32)
+        return fail(ZERO_ERR_SIZE, "n_rows * ceil(dim / 1024) must fit 32 bits");
+    if (int rc = check_type(bytes, pack ? "x_bytes" : "out_bytes")) return rc;
+    if (int rc = check_rows(pack ? x : out, n_rows, dim, stride, bytes, pack ? "x" : "out"))
+        return rc;
+    if (int rc = check_eight(codes, scales, n_rows, dim, codes_stride, "codes")) return rc;
+    if (n_rows == 0) return ok();
+    zf::EightArgs a{};
+    a.x = x;
+    a.out = out;
+    a.codes = codes;
+    a.scales = scales;
+    a.n_rows = n_rows;
+    a.dim = dim;
+    a.blocks = (dim + kBlock - 1) / kBlock;
+    a.x_stride = stride;
+    a.codes_stride = codes_stride;
+    return cuda_call(pack ? "row packing launch" : "row unpacking launch", [&] {
+        return zf::launch_eight(a, bytes, static_cast<cudaStream_t>(stream));
+    });
+}
+
+}  // namespace
+
+ZERO_API int zero_pack_rows(const void* x, int32_t x_bytes, int64_t n_rows, int64_t dim,
+                            int64_t x_stride, uint8_t* codes, int64_t codes_stride, float* scales,
+                            void* stream) {
+    return eight(x, nullptr, x_bytes, n_rows, dim, x_stride, codes, codes_stride, scales, stream);
+}
+
+ZERO_API int zero_unpack_rows(const uint8_t* codes, int64_t codes_stride, const float* scales,
+                              int64_t n_rows, int64_t dim, void* out, int32_t out_bytes,
+                              int64_t out_stride, void* stream) {
+    if (out == nullptr && n_rows > 0) return fail(ZERO_ERR_INVALID_ARG, "out is NULL");
+    return eight(nullptr, out, out_bytes, n_rows, dim, out_stride, const_cast<uint8_t*>(codes),
+                 codes_stride, const_cast<float*>(scales), stream);
+}
+
+ZERO_API int zero_rms_norm(const void* x, const void* residual, int32_t act_bytes, int64_t n_rows,
+                           int64_t dim, int64_t x_stride, int64_t residual_stride,
+                           const void* weight, int32_t param_bytes, double eps, void* out,
+                           int64_t out_stride, void* total, int64_t total_stride, uint8_t* out8,
+                           int64_t out8_stride, float* out8_scales, uint8_t* total8,
+                           int64_t total8_stride, float* total8_scales, float* rstd,
+                           void* stream) {
+    if (int rc = check_norm(n_rows, dim, act_bytes, param_bytes)) return rc;
+    if (!(eps >= 0.0) || !finite_f32(eps))
+        return fail(ZERO_ERR_INVALID_ARG, "eps must be >= 0 and finite in fp32");
+    if (int rc = check_rows(x, n_rows, dim, x_stride, act_bytes, "x")) return rc;
+    if (int rc = check_maybe_rows(residual, n_rows, dim, residual_stride, act_bytes, "residual"))
+        return rc;
+    if (int rc = check_maybe_rows(out, n_rows, dim, out_stride, act_bytes, "out")) return rc;
+    if (int rc = check_maybe_rows(total, n_rows, dim, total_stride, act_bytes, "total")) return rc;
+    if (out8 != nullptr || out8_scales != nullptr) {
+        if (int rc = check_eight(out8, out8_scales, n_rows, dim, out8_stride, "out8")) return rc;
+    }
+    if (total8 != nullptr || total8_scales != nullptr) {
+        if (int rc = check_eight(total8, total8_scales, n_rows, dim, total8_stride, "total8"))
+            return rc;
+    }
+    if (n_rows > 0 && total != nullptr && total == out)
+        return fail(ZERO_ERR_INVALID_ARG, "total and out are the same array");
+    if (out != nullptr && out == residual && n_rows > 0)
+        return fail(ZERO_ERR_INVALID_ARG, "out and residual are the same array");
+    if (total != nullptr) {
+        if (int rc = check_in_place(total, total_stride, x, x_stride, n_rows, "total")) return rc;
+        if (int rc = check_in_place(total, total_stride, residual, residual_stride, n_rows,
+                                    "total"))
+            return rc;
+    }
+    if (out != nullptr) {
+        if (int rc = check_in_place(out, out_stride, x, x_stride, n_rows, "out")) return rc;
+    }
+    if (int rc = check_optional(weight, param_bytes, "weight")) return rc;
+    if (int rc = check_optional(rstd, 4, "rstd")) return rc;
+    if (n_rows == 0) return ok();
+    zf::RmsArgs a{};
+    a.x = x;
+    a.residual = residual;
+    a.weight = weight;
+    a.total = total;
+    a.out = out;
+    a.out8 = out8;
+    a.out8_scales = out8_scales;
+    a.total8 = total8;
+    a.total8_scales = total8_scales;
+    a.rstd = rstd;
+    a.n_rows = n_rows;
+    a.x_stride = x_stride;
+    a.residual_stride = residual_stride;
+    a.total_stride = total_stride;
+    a.out_stride = out_stride;
+    a.out8_stride = out8_stride;
+    a.total8_stride = total8_stride;
+    a.dim = static_cast<int32_t>(dim);
+    a.blocks = static_cast<int32_t>((dim + kBlock - 1) / kBlock);
+    a.param_f32 = param_bytes == 4;
+    a.eps = static_cast<float>(eps);
+    return cuda_call("rms norm launch", [&] {
+        return zf::launch_rms_norm(a, act_bytes, static_cast<cudaStream_t>(stream));
+    });
+}
+
+ZERO_API int zero_rms_norm_grad_workspace_bytes(int64_t n_rows, int64_t dim, int64_t* bytes) {
+    if (bytes == nullptr) return fail(ZERO_ERR_INVALID_ARG, "bytes is NULL");
+    if (int rc = check_norm(n_rows, dim, 2, 2)) return rc;
+    *bytes = static_cast<int64_t>(zf::rms_grad_ctas(n_rows, dim)) * dim * 4;
+    return ok();
+}
+
+ZERO_API int zero_rms_norm_grad(const void* grad_out, const void* total, const uint8_t* total8,
+                                int64_t total8_stride, const float* total8_scales,
+                                int32_t act_bytes, int64_t n_rows, int64_t dim,
+                                int64_t grad_out_stride, int64_t total_stride, const void* weight,
+                                int32_t param_bytes, const float* rstd, const void* grad_total,
+                                int64_t grad_total_stride, void* grad_x, int64_t grad_x_stride,
+                                void* grad_weight, void* out, int64_t out_stride, void* workspace,
+                                int64_t workspace_bytes, void* stream) {
+    if (int rc = check_norm(n_rows, dim, act_bytes, param_bytes)) return rc;
+    if (int rc = check_rows(grad_out, n_rows, dim, grad_out_stride, act_bytes, "grad_out"))
+        return rc;
+    if (total != nullptr) {
+        if (total8 != nullptr || total8_scales != nullptr)
+            return fail(ZERO_ERR_INVALID_ARG, "total and total8: one of the two is needed");
+        if (int rc = check_rows(total, n_rows, dim, total_stride, act_bytes, "total")) return rc;
+    } else if (n_rows > 0) {
+        if (total8 == nullptr) return fail(ZERO_ERR_INVALID_ARG, "total and total8 are NULL");
+        if (int rc = check_eight(total8, total8_scales, n_rows, dim, total8_stride, "total8"))
+            return rc;
+    }
+    if (int rc = check_maybe_rows(grad_total, n_rows, dim, grad_total_stride, act_bytes,
+                                  "grad_total"))
+        return rc;
+    if (int rc = check_rows(grad_x, n_rows, dim, grad_x_stride, act_bytes, "grad_x")) return rc;
+    if (int rc = check_maybe_rows(out, n_rows, dim, out_stride, act_bytes, "out")) return rc;
+    if (int rc = check_in_place(grad_x, grad_x_stride, grad_out, grad_out_stride, n_rows, "grad_x"))
+        return rc;
+    if (int rc = check_in_place(grad_x, grad_x_stride, total, total_stride, n_rows, "grad_x"))
+        return rc;
+    if (int rc = check_in_place(grad_x, grad_x_stride, grad_total, grad_total_stride, n_rows,
+                                "grad_x"))
+        return rc;
+    if (n_rows > 0 && out != nullptr && (out == grad_x || out == grad_out || out == grad_total ||
+                                         out == total))
+        return fail(ZERO_ERR_INVALID_ARG, "out is another array of the call");
+    if (int rc = check_optional(weight, param_bytes, "weight")) return rc;
+    if (int rc = check_optional(grad_weight, param_bytes, "grad_weight")) return rc;
+    if (n_rows > 0) {
+        if (int rc = check_array(rstd, 4, "rstd")) return rc;
+    }
+    if (int rc = check_workspace(
+            workspace, workspace_bytes,
+            grad_weight == nullptr ? 0
+                                   : static_cast<int64_t>(zf::rms_grad_ctas(n_rows, dim)) * dim * 4))
+        return rc;
+    if (n_rows == 0 && grad_weight == nullptr) return ok();
+    zf::RmsArgs a{};
+    a.x = total;
+    a.grad_out = grad_out;
+    a.grad_total = grad_total;
+    a.weight = weight;
+    a.out = out;
+    a.grad_x = grad_x;
+    a.grad_weight = grad_weight;
+    a.total8 = const_cast<uint8_t*>(total8);
+    a.total8_scales = const_cast<float*>(total8_scales);
+    a.rstd = const_cast<float*>(rstd);
+    a.partials = static_cast<float*>(workspace);
+    a.n_rows = n_rows;
+    a.x_stride = total_stride;
+    a.grad_out_stride = grad_out_stride;
+    a.grad_total_stride = grad_total_stride;
+    a.out_stride = out_stride;
+    a.grad_x_stride = grad_x_stride;
+    a.total8_stride = total8_stride;
+    a.dim = static_cast<int32_t>(dim);
+    a.blocks = static_cast<int32_t>((dim + kBlock - 1) / kBlock);
+    a.param_f32 = param_bytes == 4;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (int rc = cuda_call("rms norm gradient launch",
+                           [&] { return zf::launch_rms_norm_grad(a, act_bytes, s); }))
+        return rc;
+    if (grad_weight == nullptr) return ok();
+    return cuda_call("rms norm gradient reduction launch",
+                     [&] { return zf::launch_rms_reduce(a, s); });
+}

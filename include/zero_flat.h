@@ -609,6 +609,83 @@ int zero_distill_loss_grad(const void* logits, int32_t logits_bytes, int64_t n_r
                            const float* weights, double temperature, float* loss,
                            void* grad_logits, int64_t grad_logits_stride, void* stream);
 
+/*
+ * Rows in 8 bits.  A row of dim values is cut into ceil(dim / 128) blocks of 128
+ * columns (the last one shorter).  Each block has one fp32 scale, the smallest power
+ * of two, at least 2^-126, that brings the block's largest finite magnitude to at most
+ * 448; codes are the values divided by it, rounded to nearest e4m3 (ties to even).  A
+ * value stands for code * scale, within 2^-4 of itself, or within 2^-10 of the scale
+ * where it is below 2^-6 of it.  Infinities and NaN become NaN (code 127; e4m3 has no
+ * infinity) and do not count for the scale.
+ *   codes             n_rows rows of dim bytes, codes_stride apart
+ *   scales            [n_rows][ceil(dim / 128)] fp32, contiguous
+ * Every value fits bf16 as it is.  Rows in 8 bits keep activations for a backward pass
+ * at 1.03 bytes a value.
+ *
+ * zero_pack_rows -- device.  codes and scales of the rows of x.
+ * zero_unpack_rows -- device.  out = code * scale, rounded to out's type.
+ *   x, out            n_rows rows of dim, of type x_bytes / out_bytes
+ * Errors: INVALID_ARG, MISALIGNED, SIZE, CUDA.
+ */
+int zero_pack_rows(const void* x, int32_t x_bytes, int64_t n_rows, int64_t dim, int64_t x_stride,
+                   uint8_t* codes, int64_t codes_stride, float* scales, void* stream);
+int zero_unpack_rows(const uint8_t* codes, int64_t codes_stride, const float* scales,
+                     int64_t n_rows, int64_t dim, void* out, int32_t out_bytes,
+                     int64_t out_stride, void* stream);
+
+/*
+ * zero_rms_norm -- device.  Root-mean-square norm with the residual's addition; for
+ * every row
+ *   total = x + residual,  rstd = 1 / sqrt(sum(total^2) / dim + eps),
+ *   out = total * rstd * weight
+ * with the sum as it is in fp32, before any rounding.
+ *   x, residual       n_rows rows of dim, of type act_bytes; residual NULL: total = x
+ *   weight            dim values of type param_bytes; NULL: ones
+ *   out, total        rows of type act_bytes, or NULL: not wanted; total may be x or
+ *                     residual, out may be x (with the same stride), if they are not
+ *                     the same array
+ *   out8, total8      the same in 8 bits (codes; their scales beside them), or NULL
+ *   rstd              n_rows fp32, or NULL where no backward pass follows
+ * Errors: INVALID_ARG (eps negative or not finite in fp32, codes without scales, ...),
+ * MISALIGNED, SIZE (dim > ZERO_MAX_NORM_DIM, in place with another stride), CUDA.
+ */
+int zero_rms_norm(const void* x, const void* residual, int32_t act_bytes, int64_t n_rows,
+                  int64_t dim, int64_t x_stride, int64_t residual_stride, const void* weight,
+                  int32_t param_bytes, double eps, void* out, int64_t out_stride, void* total,
+                  int64_t total_stride, uint8_t* out8, int64_t out8_stride, float* out8_scales,
+                  uint8_t* total8, int64_t total8_stride, float* total8_scales, float* rstd,
+                  void* stream);
+
+/*
+ * zero_rms_norm_grad -- device.  Gradient of zero_rms_norm from the forward's rstd and
+ * total, with xh = total * rstd and g = grad_out * weight:
+ *   grad_x = rstd * (g - xh * sum(g * xh)/dim) + grad_total   (of x and of residual alike)
+ *   grad_weight = sum_rows grad_out * xh
+ *   total             rows of type act_bytes; or, where it is NULL, total8 and
+ *                     total8_scales: the rows in 8 bits
+ *   grad_total        the gradient that reaches total from elsewhere (the residual
+ *                     stream behind the norm), or NULL: none
+ *   grad_x            may be grad_out, total or grad_total (with the same stride)
+ *   grad_weight       dim values of type param_bytes; NULL: not wanted
+ *   out               total * rstd * weight once more, which the weights' gradients of
+ *                     the products behind the norm read; NULL: not wanted
+ *   workspace         device scratch of at least the bytes
+ *                     zero_rms_norm_grad_workspace_bytes reports for the current
+ *                     device, 16-byte aligned, of any content
+ * Errors: as zero_rms_norm; ZERO_ERR_SIZE if the workspace is too small.
+ */
+int zero_rms_norm_grad(const void* grad_out, const void* total, const uint8_t* total8,
+                       int64_t total8_stride, const float* total8_scales, int32_t act_bytes,
+                       int64_t n_rows, int64_t dim, int64_t grad_out_stride,
+                       int64_t total_stride, const void* weight, int32_t param_bytes,
+                       const float* rstd, const void* grad_total, int64_t grad_total_stride,
+                       void* grad_x, int64_t grad_x_stride, void* grad_weight, void* out,
+                       int64_t out_stride, void* workspace, int64_t workspace_bytes,
+                       void* stream);
+
+/* zero_rms_norm_grad_workspace_bytes -- host. */
+int zero_rms_norm_grad_workspace_bytes(int64_t n_rows, int64_t dim, int64_t* bytes);
+
 /* Message for the last non-OK return on the calling thread ("" if none). */
 const char* zero_last_error(void);
 
