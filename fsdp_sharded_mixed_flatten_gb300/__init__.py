@@ -18,7 +18,10 @@ from .root_ops import (ZERO_MAX_NORM_DIM, ZERO_MAX_TEACHER, zero_distill_loss,
                        zero_distill_loss_grad, zero_embedding, zero_embedding_grad,
                        zero_embedding_grad_workspace_bytes, zero_layer_norm, zero_layer_norm_grad,
                        zero_layer_norm_grad_workspace_bytes)
-from .layer_ops import (ZERO_EIGHT_BLOCK, zero_pack_rows, zero_rms_norm, zero_rms_norm_grad,
+from .layer_ops import (ZERO_EIGHT_BLOCK, ZERO_MAX_HEAD_DIM, ZERO_MAX_HEAD_TOKENS,
+                        ZERO_MAX_HEAD_VOCAB, zero_head_loss, zero_head_loss_grad,
+                        zero_head_loss_grad_workspace_bytes, zero_head_loss_workspace_bytes,
+                        zero_pack_rows, zero_rms_norm, zero_rms_norm_grad,
                         zero_rms_norm_grad_workspace_bytes, zero_unpack_rows)
 
 __all__ = [
@@ -34,4 +37,7 @@ __all__ = [
     "zero_layer_norm", "zero_layer_norm_grad", "zero_layer_norm_grad_workspace_bytes",
     "ZERO_EIGHT_BLOCK", "zero_pack_rows", "zero_rms_norm", "zero_rms_norm_grad",
     "zero_rms_norm_grad_workspace_bytes", "zero_unpack_rows",
+    "ZERO_MAX_HEAD_DIM", "ZERO_MAX_HEAD_TOKENS", "ZERO_MAX_HEAD_VOCAB", "zero_head_loss",
+    "zero_head_loss_grad", "zero_head_loss_grad_workspace_bytes",
+    "zero_head_loss_workspace_bytes",
 ]

@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "zero_flat.h"
+#include "zero_head.cuh"
 #include "zero_host.cuh"
 #include "zero_kernels.cuh"
 #include "zero_status.cuh"
@@ -899,7 +900,11 @@ ZERO_API int zero_device_status(void* stream, int32_t* status, int32_t clear) {
     if (int rc = cuda_status(zf::read_device_status(&v, clear != 0, static_cast<cudaStream_t>(stream)),
                              "device status read"))
         return rc;
-    *status = v;
+    int w = 0;
+    if (int rc = cuda_status(zf::read_head_status(&w, clear != 0, static_cast<cudaStream_t>(stream)),
+                             "device status read"))
+        return rc;
+    *status = v != 0 ? v : w;
     return ok();
 }
 

@@ -1,0 +1,851 @@
+// Softmax cross entropy of the head, without keeping the logits: for hidden states h and
+// the table W
+//   z = h W^T,  lse = log sum_v exp z_v,  loss = lse - z[label],
+//   dz = g (exp(z - lse) - 1[v = label]),  dh = dz W,  dW = dz^T h.
+//
+// The products run on the tensor cores (bf16 operands, fp32 sums) by pairs of CTAs on 256 x
+// 256 tiles: one thread streams operands by TMA into a ring in shared memory, one thread of
+// the pair issues the products, four warps turn finished tiles of tensor memory into
+// results while the next tile's products run.  The forward pass leaves a maximum and a sum
+// of exponentials for each row and tile, joined by a second launch.  The backward pass
+// works through the vocabulary in pieces: the piece's z again, its dz in bf16 to the
+// workspace, then dz W, added up in fp32 over the pieces, and dz^T h.
+//
+// dz is rounded to bf16 because the tensor cores multiply bf16: 2^-8 of each term at most, averaged
+// over sums of many terms; its sums are held in fp32.
+//
+// Only live tokens take part (head_rows): their hidden rows are copied side by side, so
+// that a prompt's tokens without a label cost nothing and their values reach nothing.
+#include "zero_head.cuh"
+
+#include <mutex>
+
+#include "zero_kernels.cuh"
+#include "zero_ops.cuh"
+#include "zero_tile.cuh"
+
+namespace zf {
+
+namespace {
+
+using namespace tile;
+
+__device__ int g_head_status = 0;
+
+constexpr int kPairTile = 256;                  // rows and columns of a pair's tile
+constexpr int kTileK = 64;
+constexpr int kHalf = 128;                  // of the tile, a CTA's share of each operand
+constexpr int kStages = 6;
+constexpr uint32_t kOperandBytes = kHalf * kTileK * 2;
+constexpr uint32_t kStageBytes = 2 * kOperandBytes;
+constexpr uint32_t kChunkBytes = kTileK * 128;        // 64 values along M or N, MN-major
+constexpr size_t kHeadSmem = kStages * kStageBytes + 1024;
+constexpr int kEpilogueWarps = 4;
+constexpr int kHeadThreads = 64 + 32 * kEpilogueWarps;
+constexpr uint32_t kTmemColumns = 512;      // two tiles' results
+constexpr uint64_t kHeadWaitNs = 2000000000ull;
+constexpr float kLog2e = 1.4426950408889634f;
+
+enum Mode { kLoss, kDz, kDh, kDw };
+
+struct HeadArgs {
+    const int32_t* counts;        // live tokens
+    const int32_t* label;         // of the live tokens, as the rest
+    const float* lse;
+    const float* grad;
+    float2* parts;                // [rows][parts_pitch]: maximum (times log2 e) and sum of a tile
+    float* picked;                // z[label]
+    uint16_t* dz;                 // [rows][dz_pitch]
+    float* sums;                  // [splits][rows][sums_pitch]
+    uint16_t* grad_table;         // the piece's first row
+    int64_t parts_pitch, dz_pitch, sums_pitch, rows;
+    int32_t first;                // the piece's first row of the table, and its rows
+    int32_t vocab;
+    int32_t dim;
+    int32_t splits;
+    int32_t add;                  // to the sums, or to the table's gradient, that are there
+    int32_t wide;                 // rows of the table's gradient on 16-byte boundaries
+    int32_t group;                // tiles along M that are worked on together
+};
+
+struct Shared {
+    uint64_t full[kStages], empty[kStages], done[2], taken[2];
+    uint32_t tmem;
+    int stop;
+};
+
+// Waits for a phase; false when the pair is to stop: the wait has run out, here or in
+// another role of this CTA.
+__device__ __noinline__ bool wait_long(Shared& sh, uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = now_ns();
+    while (!bar_try(bar, parity)) {
+        if (*static_cast<volatile int*>(&sh.stop)) return false;
+        if (now_ns() - t0 > kHeadWaitNs) {
+            *static_cast<volatile int*>(&sh.stop) = 1;
+            atomicCAS(&g_head_status, kDeviceOk, kDeviceTimeout);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool wait(Shared& sh, uint64_t& bar, uint32_t parity) {
+    const uint32_t b = smem_address(&bar);
+    return bar_try(b, parity) || wait_long(sh, b, parity);
+}
+
+// The tiles of a launch, in the order in which the pairs take them.
+template <int MODE>
+struct Tiles {
+    int m_tiles, n_tiles, steps, splits, group, total;
+    __device__ explicit Tiles(const HeadArgs& a) {
+        const int live = *a.counts;
+        const int m = MODE == kDw ? a.vocab : live;
+        const int n = MODE == kLoss || MODE == kDz ? a.vocab : a.dim;
+        const int k = MODE == kDh ? a.vocab : MODE == kDw ? live : a.dim;
+        m_tiles = (m + kPairTile - 1) / kPairTile;
+        n_tiles = (n + kPairTile - 1) / kPairTile;
+        steps = (k + kTileK - 1) / kTileK;
+        splits = MODE == kDh ? a.splits : 1;
+        group = a.group;
+        total = m_tiles * n_tiles * splits;
+    }
+    struct At {
+        int m, n, split, begin, end;          // rows and columns / 256, steps along K
+    };
+    __device__ __forceinline__ At operator()(int i) const {
+        At t;
+        const int per = m_tiles * n_tiles;
+        t.split = splits == 1 ? 0 : i / per;
+        i -= t.split * per;
+        const int g = i / (group * n_tiles);
+        i -= g * group * n_tiles;
+        const int height = min(group, m_tiles - g * group);
+        t.n = i / height;
+        t.m = g * group + i - t.n * height;
+        t.begin = splits == 1 ? 0 : static_cast<int>(static_cast<int64_t>(steps) * t.split / splits);
+        t.end = splits == 1 ? steps
+                            : static_cast<int>(static_cast<int64_t>(steps) * (t.split + 1) / splits);
+        return t;
+    }
+};
+
+// 32 values of a row to memory.
+__device__ __forceinline__ void put_bf16(uint16_t* to, const float (&v)[32], int left, bool wide) {
+    if (wide && left >= 32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint4 w;
+            w.x = pack_bf16x2(v[8 * i], v[8 * i + 1]);
+            w.y = pack_bf16x2(v[8 * i + 2], v[8 * i + 3]);
+            w.z = pack_bf16x2(v[8 * i + 4], v[8 * i + 5]);
+            w.w = pack_bf16x2(v[8 * i + 6], v[8 * i + 7]);
+            reinterpret_cast<uint4*>(to)[i] = w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            if (i < left) to[i] = float_to_bf16_rn(v[i]);
+        }
+    }
+}
+
+// The result of a tile's row: columns of tensor memory in eight parts of 32.
+template <int MODE>
+struct Epilogue {
+    const HeadArgs& a;
+    int live;
+    __device__ Epilogue(const HeadArgs& args) : a(args), live(*args.counts) {}
+
+    // `row` of the launch's M, this thread's; `load(c, v)` gives columns 32 c ...
+    template <class Load>
+    __device__ __forceinline__ void operator()(int row, int n, int split, Load&& load) const {
+        const int column = n * kPairTile;
+        if constexpr (MODE == kLoss) {
+            const int left = a.vocab - column;           // columns of the tile that exist
+            const int mine = row < live ? a.label[row] - a.first - column : -1;
+            float top = -INFINITY, sum = 0.0f, z = 0.0f;
+#pragma unroll 1
+            for (int c = 0; c < kPairTile / 32; ++c) {
+                float v[32];
+                load(c, v);
+                if (32 * c + 32 > left) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (32 * c + i >= left) v[i] = -INFINITY;
+                }
+                if (mine >= 32 * c && mine < 32 * c + 32) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (mine == 32 * c + i) z = v[i];
+                }
+                float m = v[0];
+#pragma unroll
+                for (int i = 1; i < 32; ++i) m = fmaxf(m, v[i]);
+                m = fmaxf(top, m * kLog2e);
+                // (a tile of -inf alone: no term)
+                const float from = m == -INFINITY ? 0.0f : m;
+                sum *= exp2f(top - from);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) sum += exp2f(__fmaf_rn(v[i], kLog2e, -from));
+                top = m;
+            }
+            if (row < live) {
+                a.parts[row * a.parts_pitch + a.first / kPairTile + n] = make_float2(top, sum);
+                if (mine >= 0 && mine < min(kPairTile, left)) a.picked[row] = z;
+            }
+        } else if constexpr (MODE == kDz) {
+            const bool in = row < live;
+            const int mine = in ? a.label[row] - a.first - column : -1;
+            const float off = in ? -a.lse[row] * kLog2e : 0.0f, g = in ? a.grad[row] : 0.0f;
+            uint16_t* to = a.dz + row * a.dz_pitch + column;
+            const int left = static_cast<int>(a.dz_pitch) - column;   // a multiple of 64
+#pragma unroll 1
+            for (int c = 0; c < kPairTile / 32; ++c) {
+                float v[32];
+                load(c, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    v[i] = in ? g * exp2f(__fmaf_rn(v[i], kLog2e, off)) : 0.0f;
+                if (mine >= 32 * c && mine < 32 * c + 32) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (mine == 32 * c + i) v[i] -= g;
+                }
+                if (32 * c < left) put_bf16(to + 32 * c, v, 32, true);
+            }
+        } else if constexpr (MODE == kDh) {
+            float* to = a.sums + (split * a.rows + row) * a.sums_pitch + column;
+            const int left = static_cast<int>(a.sums_pitch) - column;  // a multiple of 8
+#pragma unroll 1
+            for (int c = 0; c < kPairTile / 32; ++c) {
+                float v[32];
+                load(c, v);
+                if (row >= live) continue;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (32 * c + 4 * i >= left) break;
+                    float4* p = reinterpret_cast<float4*>(to + 32 * c) + i;
+                    float4 w = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    if (a.add) {
+                        const float4 o = *p;
+                        w = make_float4(o.x + w.x, o.y + w.y, o.z + w.z, o.w + w.w);
+                    }
+                    *p = w;
+                }
+            }
+        } else {
+            uint16_t* to = a.grad_table + static_cast<int64_t>(row) * a.dim + column;
+            const int left = a.dim - column;
+#pragma unroll 1
+            for (int c = 0; c < kPairTile / 32; ++c) {
+                float v[32];
+                load(c, v);
+                if (row >= a.vocab || 32 * c >= left) continue;
+                if (a.add) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (32 * c + i < left) v[i] += bf16_to_float(to[32 * c + i]);
+                }
+                put_bf16(to + 32 * c, v, left - 32 * c, a.wide != 0);
+            }
+        }
+    }
+};
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
+head_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+            const __grid_constant__ HeadArgs a) {
+    constexpr bool kAmn = MODE == kDw, kBmn = MODE == kDh || MODE == kDw;
+    extern __shared__ char dyn[];
+    __shared__ Shared sh;
+    const uint32_t ring = (smem_address(dyn) + 1023u) & ~1023u;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            bar_init(smem_address(&sh.full[s]), 1);
+            bar_init(smem_address(&sh.empty[s]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(smem_address(&sh.done[i]), 1);
+            bar_init(smem_address(&sh.taken[i]), 2 * kEpilogueWarps);
+        }
+        sh.stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc(smem_address(&sh.tmem), kTmemColumns);
+    fence_before_sync();
+    __syncthreads();
+    cluster_sync();
+    fence_after_sync();
+    const uint32_t tmem = sh.tmem;
+    const Tiles<MODE> tiles(a);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t phase = 1;
+            bool run = true;
+            for (int i = pair; run && i < tiles.total; i += pairs) {
+                const auto t = tiles(i);
+                const int m0 = t.m * kPairTile + static_cast<int>(rank) * kHalf;
+                const int n0 = t.n * kPairTile + static_cast<int>(rank) * kHalf;
+                for (int k = t.begin; k < t.end; ++k) {
+                    if (!wait(sh, sh.empty[s], phase)) {
+                        run = false;
+                        break;
+                    }
+                    const uint32_t bar = smem_address(&sh.full[s]);
+                    const uint32_t to_a = ring + s * kStageBytes, to_b = to_a + kOperandBytes;
+                    if (rank == 0) bar_expect(bar, 2 * kStageBytes);
+                    if constexpr (kAmn) {
+                        tma_load(to_a, &map_a, m0, k * kTileK, bar);
+                        tma_load(to_a + kChunkBytes, &map_a, m0 + 64, k * kTileK, bar);
+                    } else {
+                        tma_load(to_a, &map_a, k * kTileK, m0, bar);
+                    }
+                    if constexpr (kBmn) {
+                        tma_load(to_b, &map_b, n0, k * kTileK, bar);
+                        tma_load(to_b + kChunkBytes, &map_b, n0 + 64, k * kTileK, bar);
+                    } else {
+                        tma_load(to_b, &map_b, k * kTileK, n0, bar);
+                    }
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            int s = 0, n = 0;
+            uint32_t phase = 0;
+            bool run = true;
+            for (int i = pair; run && i < tiles.total; i += pairs) {
+                const auto t = tiles(i);
+                if (t.begin == t.end) continue;
+                const int slot = n % 2;
+                if (!wait(sh, sh.taken[slot], (n / 2 + 1) % 2)) break;
+                ++n;
+                fence_after_sync();
+                const uint32_t d = tmem + slot * kPairTile;
+                for (int k = t.begin; k < t.end; ++k) {
+                    if (!wait(sh, sh.full[s], phase)) {
+                        run = false;
+                        break;
+                    }
+                    fence_after_sync();
+                    const uint32_t at = ring + s * kStageBytes;
+                    const uint64_t da = operand(at, kAmn ? kChunkBytes : 16);
+                    const uint64_t db = operand(at + kOperandBytes, kBmn ? kChunkBytes : 16);
+#pragma unroll
+                    for (int j = 0; j < kTileK / 16; ++j) {
+                        // 16 values along K: 32 bytes of a row, or 16 rows
+                        product(d, da + (kAmn ? 16 * 128 : 32) / 16 * j,
+                                db + (kBmn ? 16 * 128 : 32) / 16 * j, product_form(kAmn, kBmn),
+                                k != t.begin || j != 0);
+                    }
+                    products_arrive(smem_address(&sh.empty[s]));
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (run) products_arrive(smem_address(&sh.done[slot]));
+            }
+        }
+    } else {
+        const Epilogue<MODE> epilogue(a);
+        const int part = warp % 4;                       // of tensor memory's lanes, this warp's
+        int n = 0;
+        for (int i = pair; i < tiles.total; i += pairs) {
+            const auto t = tiles(i);
+            const int row = t.m * kPairTile + static_cast<int>(rank) * kHalf + part * 32 + lane;
+            if (t.begin == t.end) {                      // a sum of nothing
+                epilogue(row, t.n, t.split, [](int, float (&v)[32]) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+                });
+                continue;
+            }
+            const int slot = n % 2;
+            const bool come = wait(sh, sh.done[slot], (n / 2) % 2);
+            if (!__all_sync(0xFFFFFFFFu, come)) break;
+            ++n;
+            fence_after_sync();
+            const uint32_t from = tmem + slot * kPairTile + (static_cast<uint32_t>(part * 32) << 16);
+            epilogue(row, t.n, t.split, [&](int c, float (&v)[32]) {
+                __syncwarp();
+                tmem_load(v, from + 32 * c);
+                tmem_load_wait();
+            });
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) bar_arrive_in_cluster(in_cta(smem_address(&sh.taken[slot]), 0));
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    if (sh.stop) {
+        // what is still on its way to shared or tensor memory gets time to come
+        const uint64_t t0 = now_ns();
+        while (now_ns() - t0 < 20000000ull) {}
+    }
+    fence_before_sync();
+    cluster_sync();
+    fence_after_sync();
+    if (warp == 1) tmem_free(tmem, kTmemColumns);
+}
+
+// ---------------------------------------------------------------- rows ------
+
+// The live tokens, in order, and what the other launches read of them.
+constexpr int kRowThreads = 1024;
+
+__global__ void __launch_bounds__(kRowThreads)
+head_rows_kernel(const HeadCall c, int32_t* counts, int32_t* index, int32_t* slot, int32_t* label,
+                 float* lse, float* grad, bool back) {
+    __shared__ int32_t warps[32];
+    const int64_t per = (c.n_tokens + kRowThreads - 1) / kRowThreads;
+    const int64_t begin = min(per * threadIdx.x, c.n_tokens), end = min(begin + per, c.n_tokens);
+    auto label_of = [&](int64_t t) {
+        const int64_t y = c.label64 ? static_cast<const int64_t*>(c.labels)[t]
+                                    : static_cast<const int32_t*>(c.labels)[t];
+        return y >= 0 && y < c.vocab ? static_cast<int32_t>(y) : -1;
+    };
+    auto is_live = [&](int64_t t, int32_t y) { return y >= 0 && (!back || c.grad_loss[t] != 0.0f); };
+    int32_t n = 0;
+    for (int64_t t = begin; t < end; ++t) n += is_live(t, label_of(t));
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    int32_t before = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t v = __shfl_up_sync(0xFFFFFFFFu, before, o);
+        if (lane >= o) before += v;
+    }
+    if (lane == 31) warps[warp] = before;
+    __syncthreads();
+    if (warp == 0) {
+        int32_t v = warps[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t w = __shfl_up_sync(0xFFFFFFFFu, v, o);
+            if (lane >= o) v += w;
+        }
+        warps[lane] = v;
+    }
+    __syncthreads();
+    int32_t at = before - n + (warp == 0 ? 0 : warps[warp - 1]);
+    if (threadIdx.x == kRowThreads - 1) *counts = at + n;
+    for (int64_t t = begin; t < end; ++t) {
+        const int32_t y = label_of(t);
+        const bool live = is_live(t, y);
+        slot[t] = live ? at : -1;
+        if (live) {
+            index[at] = static_cast<int32_t>(t);
+            label[at] = y;
+            if (back) {
+                lse[at] = c.lse[t];
+                grad[at] = c.grad_loss[t];
+            }
+            ++at;
+        } else if (!back) {
+            c.loss[t] = 0.0f;
+            if (c.lse != nullptr) c.lse[t] = 0.0f;
+        }
+    }
+}
+
+// Rows of bf16 to rows on 16-byte boundaries, `pitch` apart; a warp a row.  With an index:
+// the live tokens' rows, and zeros up to whole tiles.
+constexpr int kCopyWarps = 8;
+
+template <bool WIDE>
+__global__ void __launch_bounds__(32 * kCopyWarps)
+head_copy_kernel(const uint16_t* from, int64_t stride, const int32_t* index, const int32_t* counts,
+                 int64_t rows, int32_t dim, uint16_t* to, int64_t pitch) {
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kCopyWarps + threadIdx.x / 32;
+    if (row >= rows) return;
+    const int lane = threadIdx.x % 32;
+    const int64_t live = index == nullptr ? rows : *counts;
+    uint16_t* out = to + row * pitch;
+    if (row >= live) {
+        if (row < (live + kPairTile - 1) / kPairTile * kPairTile) {
+            for (int64_t c = 8 * lane; c < pitch; c += 256)
+                *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
+        }
+        return;
+    }
+    const uint16_t* in = from + (index == nullptr ? row : index[row]) * stride;
+    if constexpr (WIDE) {
+#pragma unroll 4
+        for (int c = 8 * lane; c + 8 <= dim; c += 256)
+            *reinterpret_cast<uint4*>(out + c) = *reinterpret_cast<const uint4*>(in + c);
+        const int rest = dim / 8 * 8 + lane;
+        if (rest < dim) out[rest] = in[rest];
+    } else {
+#pragma unroll 4
+        for (int c = lane; c < dim; c += 32) out[c] = in[c];
+    }
+}
+
+// The tiles' maxima and sums of a live row joined: a warp a row, in a fixed order.
+__global__ void __launch_bounds__(256)
+head_join_kernel(const int32_t* counts, const int32_t* index, const float2* parts, int64_t pitch,
+                 int32_t n_parts, const float* picked, float* loss, float* lse) {
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    if (row >= *counts) return;
+    const float2* p = parts + row * pitch;
+    float top = -INFINITY, sum = 0.0f;
+    for (int i = lane; i < n_parts; i += 32) {
+        const float2 v = p[i];
+        const float m = fmaxf(top, v.x), from = m == -INFINITY ? 0.0f : m;
+        sum = sum * exp2f(top - from) + v.y * exp2f(v.x - from);
+        top = m;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float t = __shfl_xor_sync(0xFFFFFFFFu, top, o), s = __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        const float m = fmaxf(top, t), from = m == -INFINITY ? 0.0f : m;
+        // (both lanes of a pair add the same two terms)
+        const float x = sum * exp2f(top - from), y = s * exp2f(t - from);
+        sum = x + y;
+        top = m;
+    }
+    if (lane == 0) {
+        // in 64 bits: the loss is a small difference of two such numbers, and never
+        // negative (the logit of `top` is top divided by the very constant it was
+        // multiplied by)
+        const double l = static_cast<double>(top) / static_cast<double>(kLog2e) +
+                         log(static_cast<double>(sum));
+        const int32_t t = index[row];
+        const double d = l - static_cast<double>(picked[row]);
+        loss[t] = d < 0.0 ? 0.0f : static_cast<float>(d);
+        if (lse != nullptr) lse[t] = static_cast<float>(l);
+    }
+}
+
+// The hidden states' gradient: the splits' sums of live tokens, zeros of the others.
+template <bool WIDE>
+__global__ void __launch_bounds__(256)
+head_finish_kernel(const int32_t* slot, const float* sums, int64_t rows, int64_t pitch,
+                   int32_t splits, int64_t n_tokens, int32_t dim, uint16_t* out, int64_t stride) {
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
+    if (t >= n_tokens) return;
+    const int lane = threadIdx.x % 32;
+    const int32_t j = slot[t];
+    uint16_t* to = out + t * stride;
+    const float* from = sums + static_cast<int64_t>(j < 0 ? 0 : j) * pitch;
+    for (int c = 4 * lane; c < dim; c += 128) {
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (j >= 0) {
+            for (int s = 0; s < splits; ++s) {
+                const float4 w = *reinterpret_cast<const float4*>(from + s * rows * pitch + c);
+                v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+            }
+        }
+        if (WIDE && c + 4 <= dim) {
+            *reinterpret_cast<uint2*>(to + c) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        } else {
+            const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < dim) to[c + e] = float_to_bf16_rn(f[e]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host ------
+
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                            const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                            CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                            CUtensorMapFloatOOBfill);
+
+cudaError_t find_encode(Encode* f) {
+    static std::once_flag once;
+    static Encode found = nullptr;
+    static cudaError_t status;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult how;
+        status = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                                  cudaEnableDefault, &how);
+        if (status == cudaSuccess && how != cudaDriverEntryPointSuccess)
+            status = cudaErrorSymbolNotFound;
+        found = reinterpret_cast<Encode>(p);
+    });
+    *f = found;
+    return status;
+}
+
+// Rows of `inner` bf16 values, `pitch` apart, in boxes of 64 values by `box_rows`; what a
+// box has beyond the matrix is read as zeros.
+cudaError_t make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t rows,
+                     int64_t pitch, int box_rows) {
+    Encode encode = nullptr;
+    if (cudaError_t e = find_encode(&encode); e != cudaSuccess) return e;
+    const cuuint64_t sizes[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)}, ones[2] = {1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
+                              sizes, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <class T>
+T* at(const HeadCall& c, int64_t offset) {
+    return reinterpret_cast<T*>(static_cast<char*>(c.workspace) + offset);
+}
+
+bool table_in_place(const HeadCall& c) { return aligned_to(c.table, 16) && c.dim % 8 == 0; }
+
+int64_t piece_rows(const HeadCall& c, const HeadPlan& p, int64_t first) {
+    return p.piece < c.vocab - first ? p.piece : c.vocab - first;
+}
+
+// The piece's rows of the table: in place, or copied to where TMA reaches them.
+cudaError_t piece_map(CUtensorMap* map, const HeadCall& c, const HeadPlan& p, int64_t first,
+                      int box_rows) {
+    const int64_t rows = piece_rows(c, p, first);
+    return table_in_place(c)
+               ? make_map(map, c.table + first * c.dim, c.dim, rows, c.dim, box_rows)
+               : make_map(map, at<uint16_t>(c, p.table), c.dim, rows, p.pitch, box_rows);
+}
+
+cudaError_t copy_piece(const HeadCall& c, const HeadPlan& p, int64_t first, cudaStream_t stream) {
+    if (table_in_place(c)) return cudaSuccess;
+    const int64_t rows = piece_rows(c, p, first);
+    const uint16_t* from = c.table + first * c.dim;
+    const unsigned grid = static_cast<unsigned>((rows + kCopyWarps - 1) / kCopyWarps);
+    head_copy_kernel<false><<<grid, 32 * kCopyWarps, 0, stream>>>(
+        from, c.dim, nullptr, nullptr, rows, static_cast<int32_t>(c.dim), at<uint16_t>(c, p.table),
+        p.pitch);
+    return cudaGetLastError();
+}
+
+template <int MODE>
+cudaError_t launch_product(const CUtensorMap& map_a, const CUtensorMap& map_b, const HeadArgs& a,
+                           int64_t tiles, cudaStream_t stream) {
+    static std::once_flag once[64];
+    static cudaError_t set[64];
+    static int fit[64];                                  // pairs at a time
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::call_once(once[dev], [&] {
+        const auto kernel = head_kernel<MODE>;
+        set[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(kHeadSmem));
+        if (set[dev] != cudaSuccess) return;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kHeadThreads);
+        cfg.dynamicSmemBytes = kHeadSmem;
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        set[dev] = cudaOccupancyMaxActiveClusters(&fit[dev], kernel, &cfg);
+        if (set[dev] == cudaSuccess && fit[dev] < 1) set[dev] = cudaErrorInvalidConfiguration;
+    });
+    if (set[dev] != cudaSuccess) return set[dev];
+    const int64_t pairs = tiles < fit[dev] ? tiles : fit[dev];
+    head_kernel<MODE><<<static_cast<unsigned>(2 * pairs), kHeadThreads, kHeadSmem, stream>>>(
+        map_a, map_b, a);
+    return cudaGetLastError();
+}
+
+HeadArgs product_args(const HeadCall& c, const HeadPlan& p, int64_t first) {
+    HeadArgs a{};
+    a.counts = at<int32_t>(c, p.counts);
+    a.label = at<int32_t>(c, p.label);
+    a.lse = at<float>(c, p.lse);
+    a.grad = at<float>(c, p.grad);
+    a.parts = at<float2>(c, p.parts);
+    a.picked = at<float>(c, p.picked);
+    a.dz = at<uint16_t>(c, p.dz);
+    a.sums = at<float>(c, p.sums);
+    a.grad_table = c.grad_table == nullptr ? nullptr : c.grad_table + first * c.dim;
+    a.parts_pitch = (c.vocab + kPairTile - 1) / kPairTile;
+    a.dz_pitch = p.piece_pitch;
+    a.sums_pitch = p.pitch;
+    a.rows = p.rows;
+    a.first = static_cast<int32_t>(first);
+    a.vocab = static_cast<int32_t>(piece_rows(c, p, first));
+    a.dim = static_cast<int32_t>(c.dim);
+    a.splits = p.splits;
+    a.group = 8;
+    return a;
+}
+
+int64_t whole(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+int64_t tiles_of(int64_t x) { return (x + kPairTile - 1) / kPairTile; }
+
+}  // namespace
+
+// Pieces of the vocabulary whose gradient, and whose copy of the table where it is off the
+// 16-byte grid, take at most 256 MB each; as even as whole tiles allow.
+HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back) {
+    constexpr int64_t kMost = int64_t{256} << 20;
+    HeadPlan p{};
+    p.rows = whole(n_tokens < 1 ? 1 : n_tokens, kPairTile);
+    p.pitch = whole(dim, 8);
+    const int64_t per_row = 2 * (back && p.rows > p.pitch ? p.rows : p.pitch);
+    int64_t most = kMost / per_row / kPairTile * kPairTile;
+    if (most < kPairTile) most = kPairTile;
+    const int64_t pieces = (vocab + most - 1) / most;
+    p.piece = whole((vocab + pieces - 1) / pieces, kPairTile);
+    p.piece_pitch = whole(p.piece < vocab ? p.piece : vocab, 64);
+    p.splits = 1;
+    if (back) {
+        // the sum over a piece in as many parts as keep the GPU's pairs busy
+        const int64_t tiles = p.rows / kPairTile * tiles_of(dim), steps = whole(p.piece, 64) / 64;
+        const int64_t pairs = device_sms() / 2 > 0 ? device_sms() / 2 : 1;
+        double best = 0.0;
+        for (int64_t s = 1; s <= 64 && s * 4 <= steps && s * p.rows * p.pitch * 4 <= kMost; ++s) {
+            // rounds of tiles, each a share of the sum and the way out of it
+            const double cost =
+                static_cast<double>((tiles * s + pairs - 1) / pairs) * (steps / (double)s + 8.0) +
+                0.25 * s;
+            if (s == 1 || cost < best) {
+                best = cost;
+                p.splits = static_cast<int32_t>(s);
+            }
+        }
+    }
+    int64_t end = 0;
+    auto place = [&](int64_t bytes) {
+        const int64_t here = end;
+        end += whole(bytes, 1024);
+        return here;
+    };
+    const int64_t n = n_tokens < 1 ? 1 : n_tokens;
+    p.counts = place(4);
+    p.index = place(4 * n);
+    p.slot = place(4 * n);
+    p.label = place(4 * n);
+    p.hidden = place(2 * p.rows * p.pitch);
+    p.table = place(2 * p.piece * p.pitch);
+    if (back) {
+        p.lse = place(4 * n);
+        p.grad = place(4 * n);
+        p.dz = place(2 * p.rows * p.piece_pitch);
+        p.sums = place(4 * p.splits * p.rows * p.pitch);
+    } else {
+        p.parts = place(8 * n * tiles_of(vocab));
+        p.picked = place(4 * n);
+    }
+    p.bytes = end;
+    return p;
+}
+
+cudaError_t launch_head_rows(const HeadCall& c, const HeadPlan& p, bool back, cudaStream_t stream) {
+    head_rows_kernel<<<1, kRowThreads, 0, stream>>>(
+        c, at<int32_t>(c, p.counts), at<int32_t>(c, p.index), at<int32_t>(c, p.slot),
+        at<int32_t>(c, p.label), at<float>(c, p.lse), at<float>(c, p.grad), back);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_head_gather(const HeadCall& c, const HeadPlan& p, cudaStream_t stream) {
+    const unsigned grid = static_cast<unsigned>((p.rows + kCopyWarps - 1) / kCopyWarps);
+    const bool wide = aligned_to(c.hidden, 16) && c.hidden_stride % 8 == 0;
+    (wide ? head_copy_kernel<true> : head_copy_kernel<false>)<<<grid, 32 * kCopyWarps, 0, stream>>>(
+        c.hidden, c.hidden_stride, at<int32_t>(c, p.index), at<int32_t>(c, p.counts), p.rows,
+        static_cast<int32_t>(c.dim), at<uint16_t>(c, p.hidden), p.pitch);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_head_loss(const HeadCall& c, const HeadPlan& p, int64_t first,
+                             cudaStream_t stream) {
+    if (cudaError_t e = copy_piece(c, p, first, stream); e != cudaSuccess) return e;
+    CUtensorMap ma, mb;
+    if (cudaError_t e = make_map(&ma, at<uint16_t>(c, p.hidden), c.dim, p.rows, p.pitch, kHalf);
+        e != cudaSuccess)
+        return e;
+    if (cudaError_t e = piece_map(&mb, c, p, first, kHalf); e != cudaSuccess) return e;
+    const HeadArgs a = product_args(c, p, first);
+    return launch_product<kLoss>(ma, mb, a, p.rows / kPairTile * tiles_of(a.vocab), stream);
+}
+
+cudaError_t launch_head_join(const HeadCall& c, const HeadPlan& p, cudaStream_t stream) {
+    const unsigned grid = static_cast<unsigned>((c.n_tokens + 7) / 8);
+    const int64_t parts = tiles_of(c.vocab);
+    head_join_kernel<<<grid, 256, 0, stream>>>(
+        at<int32_t>(c, p.counts), at<int32_t>(c, p.index), at<float2>(c, p.parts), parts,
+        static_cast<int32_t>(parts), at<float>(c, p.picked), c.loss, c.lse);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_head_dz(const HeadCall& c, const HeadPlan& p, int64_t first,
+                           cudaStream_t stream) {
+    if (cudaError_t e = copy_piece(c, p, first, stream); e != cudaSuccess) return e;
+    CUtensorMap ma, mb;
+    if (cudaError_t e = make_map(&ma, at<uint16_t>(c, p.hidden), c.dim, p.rows, p.pitch, kHalf);
+        e != cudaSuccess)
+        return e;
+    if (cudaError_t e = piece_map(&mb, c, p, first, kHalf); e != cudaSuccess) return e;
+    const HeadArgs a = product_args(c, p, first);
+    return launch_product<kDz>(ma, mb, a, p.rows / kPairTile * tiles_of(a.vocab), stream);
+}
+
+cudaError_t launch_head_dh(const HeadCall& c, const HeadPlan& p, int64_t first,
+                           cudaStream_t stream) {
+    HeadArgs a = product_args(c, p, first);
+    a.add = first > 0;
+    CUtensorMap ma, mb;
+    // (columns of dz beyond the piece are not read: zeros in their place)
+    if (cudaError_t e = make_map(&ma, a.dz, a.vocab, p.rows, p.piece_pitch, kHalf); e != cudaSuccess)
+        return e;
+    if (cudaError_t e = piece_map(&mb, c, p, first, kTileK); e != cudaSuccess) return e;
+    return launch_product<kDh>(ma, mb, a, p.rows / kPairTile * tiles_of(c.dim) * p.splits, stream);
+}
+
+cudaError_t launch_head_dw(const HeadCall& c, const HeadPlan& p, int64_t first,
+                           cudaStream_t stream) {
+    HeadArgs a = product_args(c, p, first);
+    a.add = c.accumulate;
+    a.wide = aligned_to(c.grad_table, 16) && c.dim % 8 == 0;
+    CUtensorMap ma, mb;
+    if (cudaError_t e = make_map(&ma, a.dz, a.vocab, p.rows, p.piece_pitch, kTileK);
+        e != cudaSuccess)
+        return e;
+    if (cudaError_t e = make_map(&mb, at<uint16_t>(c, p.hidden), c.dim, p.rows, p.pitch, kTileK);
+        e != cudaSuccess)
+        return e;
+    return launch_product<kDw>(ma, mb, a, tiles_of(a.vocab) * tiles_of(c.dim), stream);
+}
+
+cudaError_t launch_head_finish(const HeadCall& c, const HeadPlan& p, cudaStream_t stream) {
+    const unsigned grid = static_cast<unsigned>((c.n_tokens + 7) / 8);
+    const bool wide = aligned_to(c.grad_hidden, 8) && c.grad_hidden_stride % 4 == 0;
+    (wide ? head_finish_kernel<true> : head_finish_kernel<false>)<<<grid, 256, 0, stream>>>(
+        at<int32_t>(c, p.slot), at<float>(c, p.sums), p.rows, p.pitch, p.splits, c.n_tokens,
+        static_cast<int32_t>(c.dim), c.grad_hidden, c.grad_hidden_stride);
+    return cudaGetLastError();
+}
+
+cudaError_t read_head_status(int* status, int clear, cudaStream_t stream) {
+    int v = 0;
+    cudaError_t e =
+        cudaMemcpyFromSymbolAsync(&v, g_head_status, sizeof(int), 0, cudaMemcpyDeviceToHost, stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    if (e == cudaSuccess && clear) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbolAsync(g_head_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice,
+                                    stream);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    }
+    *status = v;
+    return e;
+}
+
+}  // namespace zf

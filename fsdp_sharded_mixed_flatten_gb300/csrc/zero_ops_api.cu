@@ -8,6 +8,7 @@
 #include <limits>
 
 #include "zero_flat.h"
+#include "zero_head.cuh"
 #include "zero_ops.cuh"
 #include "zero_status.cuh"
 
@@ -584,4 +585,153 @@ ZERO_API int zero_rms_norm_grad(const void* grad_out, const void* total, const u
     if (grad_weight == nullptr) return ok();
     return cuda_call("rms norm gradient reduction launch",
                      [&] { return zf::launch_rms_reduce(a, s); });
+}
+
+namespace {
+
+int check_head(int64_t n_tokens, int64_t vocab, int64_t dim) {
+    if (n_tokens < 0 || vocab < 1 || dim < 1)
+        return fail(ZERO_ERR_INVALID_ARG, "n_tokens >= 0, vocab >= 1 and dim >= 1 are needed");
+    if (n_tokens > ZERO_MAX_HEAD_TOKENS || vocab > ZERO_MAX_HEAD_VOCAB || dim > ZERO_MAX_HEAD_DIM)
+        return fail(ZERO_ERR_SIZE, "n_tokens, vocab or dim is too large (at most %d, %d, %d)",
+                    ZERO_MAX_HEAD_TOKENS, ZERO_MAX_HEAD_VOCAB, ZERO_MAX_HEAD_DIM);
+    return ZERO_OK;
+}
+
+// What both passes read.
+int head_call(zf::HeadCall& c, const uint16_t* hidden, int64_t n_tokens, int64_t dim,
+              int64_t hidden_stride, const uint16_t* table, int64_t vocab, const void* labels,
+              int32_t label_bytes) {
+    if (int rc = check_head(n_tokens, vocab, dim)) return rc;
+    if (int rc = check_rows(hidden, n_tokens, dim, hidden_stride, 2, "hidden")) return rc;
+    if (int rc = check_array(table, 2, "table")) return rc;
+    if (label_bytes != 4 && label_bytes != 8)
+        return fail(ZERO_ERR_INVALID_ARG, "label_bytes = %d (4 or 8)", label_bytes);
+    if (n_tokens > 0) {
+        if (int rc = check_array(labels, label_bytes, "labels")) return rc;
+    }
+    c.hidden = hidden;
+    c.table = table;
+    c.labels = labels;
+    c.n_tokens = n_tokens;
+    c.vocab = vocab;
+    c.dim = dim;
+    c.hidden_stride = hidden_stride;
+    c.label64 = label_bytes == 8;
+    return ZERO_OK;
+}
+
+int head_workspace(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, int64_t* bytes) {
+    if (bytes == nullptr) return fail(ZERO_ERR_INVALID_ARG, "bytes is NULL");
+    if (int rc = check_head(n_tokens, vocab, dim)) return rc;
+    *bytes = zf::head_plan(n_tokens, vocab, dim, back).bytes;
+    return ok();
+}
+
+}  // namespace
+
+ZERO_API int zero_head_loss_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t dim,
+                                            int64_t* bytes) {
+    return head_workspace(n_tokens, vocab, dim, false, bytes);
+}
+
+ZERO_API int zero_head_loss_grad_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t dim,
+                                                 int64_t* bytes) {
+    return head_workspace(n_tokens, vocab, dim, true, bytes);
+}
+
+ZERO_API int zero_head_loss(const uint16_t* hidden, int64_t n_tokens, int64_t dim,
+                            int64_t hidden_stride, const uint16_t* table, int64_t vocab,
+                            const void* labels, int32_t label_bytes, float* loss, float* lse,
+                            void* workspace, int64_t workspace_bytes, void* stream) {
+    zf::HeadCall c{};
+    if (int rc = head_call(c, hidden, n_tokens, dim, hidden_stride, table, vocab, labels,
+                           label_bytes))
+        return rc;
+    if (n_tokens > 0) {
+        if (int rc = check_array(loss, 4, "loss")) return rc;
+    }
+    if (int rc = check_optional(lse, 4, "lse")) return rc;
+    if (n_tokens == 0) return ok();
+    const zf::HeadPlan p = zf::head_plan(n_tokens, vocab, dim, false);
+    if (int rc = check_workspace(workspace, workspace_bytes, p.bytes)) return rc;
+    c.loss = loss;
+    c.lse = lse;
+    c.workspace = workspace;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (int rc = cuda_call("head rows launch",
+                           [&] { return zf::launch_head_rows(c, p, false, s); }))
+        return rc;
+    if (int rc = cuda_call("head gather launch", [&] { return zf::launch_head_gather(c, p, s); }))
+        return rc;
+    for (int64_t first = 0; first < vocab; first += p.piece) {
+        if (int rc = cuda_call("head loss launch",
+                               [&] { return zf::launch_head_loss(c, p, first, s); }))
+            return rc;
+    }
+    return cuda_call("head join launch", [&] { return zf::launch_head_join(c, p, s); });
+}
+
+ZERO_API int zero_head_loss_grad(const uint16_t* hidden, int64_t n_tokens, int64_t dim,
+                                 int64_t hidden_stride, const uint16_t* table, int64_t vocab,
+                                 const void* labels, int32_t label_bytes, const float* lse,
+                                 const float* grad_loss, uint16_t* grad_hidden,
+                                 int64_t grad_hidden_stride, uint16_t* grad_table,
+                                 int32_t accumulate, void* workspace, int64_t workspace_bytes,
+                                 void* stream) {
+    zf::HeadCall c{};
+    if (int rc = head_call(c, hidden, n_tokens, dim, hidden_stride, table, vocab, labels,
+                           label_bytes))
+        return rc;
+    if (n_tokens > 0) {
+        if (int rc = check_array(lse, 4, "lse")) return rc;
+        if (int rc = check_array(grad_loss, 4, "grad_loss")) return rc;
+    }
+    if (int rc = check_maybe_rows(grad_hidden, n_tokens, dim, grad_hidden_stride, 2, "grad_hidden"))
+        return rc;
+    if (grad_hidden != nullptr) {
+        if (int rc = check_in_place(grad_hidden, grad_hidden_stride, hidden, hidden_stride,
+                                    n_tokens, "grad_hidden"))
+            return rc;
+    }
+    if (int rc = check_optional(grad_table, 2, "grad_table")) return rc;
+    if (grad_table != nullptr && grad_table == table)
+        return fail(ZERO_ERR_INVALID_ARG, "grad_table and table are the same array");
+    if (accumulate != 0 && accumulate != 1)
+        return fail(ZERO_ERR_INVALID_ARG, "accumulate = %d (0 or 1)", accumulate);
+    const bool rows = grad_hidden != nullptr && n_tokens > 0;
+    const bool columns = grad_table != nullptr && (n_tokens > 0 || !accumulate);
+    if (!rows && !columns) return ok();
+    const zf::HeadPlan p = zf::head_plan(n_tokens, vocab, dim, true);
+    if (int rc = check_workspace(workspace, workspace_bytes, p.bytes)) return rc;
+    c.lse = const_cast<float*>(lse);
+    c.grad_loss = grad_loss;
+    c.grad_hidden = grad_hidden;
+    c.grad_hidden_stride = grad_hidden_stride;
+    c.grad_table = grad_table;
+    c.accumulate = accumulate;
+    c.workspace = workspace;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (int rc = cuda_call("head rows launch", [&] { return zf::launch_head_rows(c, p, true, s); }))
+        return rc;
+    if (int rc = cuda_call("head gather launch", [&] { return zf::launch_head_gather(c, p, s); }))
+        return rc;
+    for (int64_t first = 0; first < vocab; first += p.piece) {
+        if (int rc = cuda_call("head logits' gradient launch",
+                               [&] { return zf::launch_head_dz(c, p, first, s); }))
+            return rc;
+        if (rows) {
+            if (int rc = cuda_call("head hidden gradient launch",
+                                   [&] { return zf::launch_head_dh(c, p, first, s); }))
+                return rc;
+        }
+        if (columns) {
+            if (int rc = cuda_call("head table gradient launch",
+                                   [&] { return zf::launch_head_dw(c, p, first, s); }))
+                return rc;
+        }
+    }
+    if (!rows) return ok();
+    return cuda_call("head gradient rows launch",
+                     [&] { return zf::launch_head_finish(c, p, s); });
 }

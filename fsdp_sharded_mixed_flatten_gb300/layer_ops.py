@@ -1,5 +1,6 @@
-"""Operators of a decoder layer's norm: the root-mean-square norm with the
-residual's addition, and rows in 8 bits.
+"""Operators of a decoder layer's norm and of the head: the root-mean-square
+norm with the residual's addition, rows in 8 bits, and the softmax cross
+entropy over the vocabulary without the logits in memory.
 
 The same function names as in include/zero_flat.h, and the conventions of
 ``root_ops``: torch CUDA tensors, matrices with contiguous rows of any stride,
@@ -16,12 +17,16 @@ import ctypes
 
 import torch
 
-from .root_ops import (_ELEM, _F32, _INVALID, _SIZE, _bytes, _here, _on, _ptr, _refuse, _rows,
-                       _vector, _workspace)
+from .root_ops import (_ELEM, _F32, _IDS, _INVALID, _SIZE, _bytes, _here, _on, _ptr, _refuse,
+                       _rows, _table, _vector, _workspace)
 from .zero import _check, load
 
 ZERO_EIGHT_BLOCK = 128
+ZERO_MAX_HEAD_TOKENS = 1 << 22
+ZERO_MAX_HEAD_VOCAB = 1 << 22
+ZERO_MAX_HEAD_DIM = 32768
 
+_BF16 = {torch.bfloat16: 2}
 _CODES = {torch.float8_e4m3fn: 1, torch.uint8: 1}
 
 
@@ -138,3 +143,75 @@ def zero_rms_norm_grad(grad_out, total, weight, rstd, grad_x, grad_weight=None, 
         sizes.pop() if sizes else 4, _ptr(rstd), gt, gt_stride, gx, gx_stride, _ptr(grad_weight),
         o, o_stride, _workspace(workspace, workspace_bytes, f, dev), workspace_bytes,
         _on(dev, stream)), f)
+
+
+def zero_head_loss_workspace_bytes(n_tokens: int, vocab: int, dim: int) -> int:
+    out = ctypes.c_int64(0)
+    f = "zero_head_loss_workspace_bytes"
+    _check(load().zero_head_loss_workspace_bytes(n_tokens, vocab, dim, ctypes.byref(out)), f)
+    return int(out.value)
+
+
+def zero_head_loss_grad_workspace_bytes(n_tokens: int, vocab: int, dim: int) -> int:
+    out = ctypes.c_int64(0)
+    f = "zero_head_loss_grad_workspace_bytes"
+    _check(load().zero_head_loss_grad_workspace_bytes(n_tokens, vocab, dim, ctypes.byref(out)), f)
+    return int(out.value)
+
+
+def _head(hidden, table, labels, func: str, device: int):
+    """(tokens, dim, hidden's row stride, vocab, bytes of a label)."""
+    n, d, stride = _rows(hidden, "hidden", func)
+    vocab, dim = _table(table, "table", func)
+    if d != dim:
+        _refuse(_SIZE, func, f"hidden {tuple(hidden.shape)} and table {tuple(table.shape)} are "
+                "of different widths")
+    _bytes(hidden, _BF16, "hidden", func, device)
+    _bytes(table, _BF16, "table", func, device)
+    return n, d, stride, vocab, _vector(labels, n, _IDS, "labels", func, device)
+
+
+def zero_head_loss(hidden, table, labels, loss, lse=None, workspace=None,
+                   workspace_bytes: int = 0, stream=None):
+    """Softmax cross entropy of the head, without the logits in memory:
+    loss = lse - z[label], lse = log sum exp z, z = hidden table^T; 0 for
+    tokens whose label is outside [0, vocab).
+
+    hidden (rows of dim) and table (vocab, dim): bf16; labels: int32 or int64,
+    one per row; loss, lse: fp32, one value per row (lse or None); workspace:
+    device buffer of at least zero_head_loss_workspace_bytes(rows, vocab, dim)
+    bytes."""
+    f, dev = "zero_head_loss", hidden.get_device()
+    n, d, stride, vocab, lb = _head(hidden, table, labels, f, dev)
+    _vector(loss, n, _F32, "loss", f, dev)
+    _vector(lse, n, _F32, "lse", f, dev)
+    _check(load().zero_head_loss(hidden.data_ptr(), n, d, stride, table.data_ptr(), vocab,
+                                 _ptr(labels), lb, _ptr(loss), _ptr(lse),
+                                 _workspace(workspace, workspace_bytes, f, dev), workspace_bytes,
+                                 _on(dev, stream)), f)
+
+
+def zero_head_loss_grad(hidden, table, labels, lse, grad_loss, grad_hidden=None, grad_table=None,
+                        accumulate: bool = False, workspace=None, workspace_bytes: int = 0,
+                        stream=None):
+    """Gradients of zero_head_loss from its lse and each token's gradient of
+    the loss (fp32; 0 for tokens that do not count).
+
+    grad_hidden: of hidden's shape, bf16 (may be hidden), or None; grad_table:
+    (vocab, dim), bf16, or None; with accumulate it is added to; workspace:
+    device buffer of at least zero_head_loss_grad_workspace_bytes(rows, vocab,
+    dim) bytes."""
+    f, dev = "zero_head_loss_grad", hidden.get_device()
+    n, d, stride, vocab, lb = _head(hidden, table, labels, f, dev)
+    _vector(lse, n, _F32, "lse", f, dev)
+    _vector(grad_loss, n, _F32, "grad_loss", f, dev)
+    gh, gh_stride = _like(grad_hidden, n, d, torch.bfloat16, "grad_hidden", f, dev)
+    if grad_table is not None:
+        if tuple(_table(grad_table, "grad_table", f)) != (vocab, d):
+            _refuse(_SIZE, f, f"grad_table {tuple(grad_table.shape)} is not of the table's shape "
+                    f"{(vocab, d)}")
+        _bytes(grad_table, _BF16, "grad_table", f, dev)
+    _check(load().zero_head_loss_grad(
+        hidden.data_ptr(), n, d, stride, table.data_ptr(), vocab, _ptr(labels), lb,
+        _ptr(lse), _ptr(grad_loss), gh, gh_stride, _ptr(grad_table), 1 if accumulate else 0,
+        _workspace(workspace, workspace_bytes, f, dev), workspace_bytes, _on(dev, stream)), f)

@@ -139,6 +139,11 @@ def load() -> ctypes.CDLL:
             "zero_rms_norm_grad": [p, p, p, i64, p, i32, i64, i64, i64, i64, p, i32, p, p, i64, p,
                                    i64, p, p, i64, p, i64, p],
             "zero_rms_norm_grad_workspace_bytes": [i64, i64, out64],
+            "zero_head_loss": [p, i64, i64, i64, p, i64, p, i32, p, p, p, i64, p],
+            "zero_head_loss_grad": [p, i64, i64, i64, p, i64, p, i32, p, p, p, i64, p, i32, p,
+                                    i64, p],
+            "zero_head_loss_workspace_bytes": [i64, i64, i64, out64],
+            "zero_head_loss_grad_workspace_bytes": [i64, i64, i64, out64],
             "zero_distill_loss": [p, i32, i64, i64, i64, p, p, i32, i64, p, f64, p, p],
             "zero_distill_loss_grad": [p, i32, i64, i64, i64, p, p, i32, i64, p, f64, p, p, i64,
                                        p],

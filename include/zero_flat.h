@@ -273,7 +273,7 @@ int zero_step(const uint16_t* const* grads, float* const* master, float* const* 
 /*
  * zero_device_status -- host, synchronous.  Failure detection for the kernels
  * that wait on shared-memory barriers (the bulk-copy staged fused step and
- * reduce-scatter): every such wait gives up after about 2 seconds, records
+ * reduce-scatter, the head's products): every such wait gives up after about 2 seconds, records
  * ZERO_DEVICE_TIMEOUT in a device status word, and the kernel returns early
  * (its outputs are then incomplete).  A dynamically scheduled launch that
  * found its tile counter used by another launch at the same time records
@@ -685,6 +685,59 @@ int zero_rms_norm_grad(const void* grad_out, const void* total, const uint8_t* t
 
 /* zero_rms_norm_grad_workspace_bytes -- host. */
 int zero_rms_norm_grad_workspace_bytes(int64_t n_rows, int64_t dim, int64_t* bytes);
+
+/*
+ * zero_head_loss -- device.  Softmax cross entropy of the head over the vocabulary,
+ * without the logits in memory:
+ *   z = hidden table^T,  lse = log(sum_v exp(z_v)),  loss = lse - z[label]
+ * for tokens with a label in [0, vocab); 0 in loss and lse for the others, whatever
+ * their hidden states hold.  Products of bf16 are summed in fp32.
+ *   hidden            n_tokens rows of dim, bf16
+ *   table             [vocab][dim] contiguous, bf16 (of a flat parameter buffer, at any
+ *                     element; on a 16-byte boundary with dim a multiple of 8 it is read
+ *                     in place, else piece by piece through the workspace)
+ *   labels            n_tokens int32 or int64
+ *   loss              n_tokens fp32
+ *   lse               n_tokens fp32, or NULL where no backward pass follows
+ *   workspace         device scratch of at least the bytes
+ *                     zero_head_loss_workspace_bytes reports for the current device,
+ *                     16-byte aligned, of any content; calls that may overlap on the GPU
+ *                     need one each
+ * Errors: INVALID_ARG, MISALIGNED, SIZE (sizes beyond ZERO_MAX_HEAD_TOKENS,
+ * ZERO_MAX_HEAD_VOCAB, ZERO_MAX_HEAD_DIM, a stride below dim, workspace too small), CUDA.
+ * These kernels wait on barriers: see zero_device_status.
+ *
+ * zero_head_loss_grad -- device.  Its gradients from the forward's lse and the gradient
+ * of each token's loss, with dz = grad_loss * (exp(z - lse) - [v = label]):
+ *   grad_hidden = dz table,   grad_table = dz^T hidden   (added to it, if accumulate)
+ * z is computed again, in pieces of the vocabulary; dz is rounded to bf16, sums are held
+ * in fp32 and rounded once (to bf16).  Tokens without a label in [0, vocab) or with
+ * grad_loss 0 get a gradient of zeros and add nothing, whatever their rows hold.
+ *   grad_loss         n_tokens fp32
+ *   grad_hidden       n_tokens rows of dim, bf16; may be hidden (with the same stride);
+ *                     NULL: not wanted
+ *   grad_table        [vocab][dim] contiguous, bf16, at any element; NULL: not wanted
+ *   accumulate        0 or 1
+ *   workspace         as above, of zero_head_loss_grad_workspace_bytes
+ */
+#define ZERO_MAX_HEAD_TOKENS (1 << 22)
+#define ZERO_MAX_HEAD_VOCAB (1 << 22)
+#define ZERO_MAX_HEAD_DIM 32768
+int zero_head_loss(const uint16_t* hidden, int64_t n_tokens, int64_t dim, int64_t hidden_stride,
+                   const uint16_t* table, int64_t vocab, const void* labels, int32_t label_bytes,
+                   float* loss, float* lse, void* workspace, int64_t workspace_bytes,
+                   void* stream);
+int zero_head_loss_grad(const uint16_t* hidden, int64_t n_tokens, int64_t dim,
+                        int64_t hidden_stride, const uint16_t* table, int64_t vocab,
+                        const void* labels, int32_t label_bytes, const float* lse,
+                        const float* grad_loss, uint16_t* grad_hidden,
+                        int64_t grad_hidden_stride, uint16_t* grad_table, int32_t accumulate,
+                        void* workspace, int64_t workspace_bytes, void* stream);
+
+/* zero_head_loss_workspace_bytes, zero_head_loss_grad_workspace_bytes -- host. */
+int zero_head_loss_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t dim, int64_t* bytes);
+int zero_head_loss_grad_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t dim,
+                                        int64_t* bytes);
 
 /* Message for the last non-OK return on the calling thread ("" if none). */
 const char* zero_last_error(void);

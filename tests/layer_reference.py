@@ -109,3 +109,68 @@ def rms_norm_grad(grad_out, total, weight, rstd, grad_total):
     dw = (dy * xh).sum(0)
     dw_bound = (n + 168 + 3) * U * (dy * xh).abs().sum(0)
     return (dx, bound), (dw, dw_bound), (xh * w, 3 * U * (xh * w).abs())
+
+
+# ------------------------------------------------- cross entropy of the head ----
+#
+# A product of d bf16 pairs is summed on the tensor cores 16 pairs at a time; each step
+# adds them to the running sum in fp32, off by at most 2 units of 2^-23 of the magnitudes
+# added so far: (d / 16 + 1) 2^-22 sum|h w| in all (`chain`).  Exponentials are off by 4 u
+# and 3 u |x| of themselves, their sums go through at most 256 + 32 additions, so lse and
+# loss are off by the logits' bound (the loss twice) and 300 u, and by their own rounding.
+# dz is rounded to bf16 (2^-8 of itself).
+
+def chain(n):
+    return (n / 16 + 1) * 2.0 ** -22
+
+
+def head_logits(hidden, table):
+    """(z, bound) in 64 bits, where the tensors are."""
+    h, w = hidden.to(F64), table.to(F64)
+    return h @ w.t(), chain(h.shape[1]) * (h.abs() @ w.abs().t())
+
+
+def head_loss(hidden, table, labels):
+    """(loss, bound), (lse, bound); 0 where the label is outside the vocabulary."""
+    vocab = table.shape[0]
+    live = (labels >= 0) & (labels < vocab)
+    z, off = head_logits(hidden[live], table)
+    lse = torch.logsumexp(z, 1)
+    at = labels[live].long()[:, None]
+    loss = lse - z.gather(1, at)[:, 0]
+    off = off.amax(1)
+    out = torch.zeros((4, labels.numel()), dtype=F64, device=hidden.device)
+    out[0, live], out[1, live] = loss, 2 * off + 300 * U + 2 * U * loss.abs()
+    out[2, live], out[3, live] = lse, off + 300 * U + 2 * U * lse.abs()
+    return (out[0], out[1]), (out[2], out[3])
+
+
+def head_loss_grad(hidden, table, labels, lse, grad_loss, old=None):
+    """(grad_hidden, bound, bound of its 2-norm), the same for the table (added to old)."""
+    vocab = table.shape[0]
+    live = (labels >= 0) & (labels < vocab) & (grad_loss != 0)
+    h, w, g = hidden[live].to(F64), table.to(F64), grad_loss[live].to(F64)[:, None]
+    z, off = head_logits(hidden[live], table)
+    x = z - lse[live].to(F64)[:, None]
+    p = torch.exp(x)
+    p_off = p * (off + 6 * U + 3 * U * (x.abs() + lse[live].to(F64).abs()[:, None]))
+    dz = p.scatter_add(1, labels[live].long()[:, None], torch.full_like(p[:, :1], -1.0)) * g
+    # to bf16 (below the normal numbers: flushed or rounded by 2^-134)
+    dz_off = (p_off + 2 * U * (p + dz.abs())) * g.abs() + 2.0 ** -8 * dz.abs() + 2.0 ** -126
+    dh, dw = dz @ w, dz.t() @ h
+    n = h.shape[0]
+    dh_off = dz_off @ w.abs() + (chain(vocab) + 80 * U) * (dz.abs() @ w.abs())
+    dw_off = dz_off.t() @ h.abs() + (chain(n) + 2 * U) * (dz.abs().t() @ h.abs())
+    norm = lambda t: float(torch.linalg.vector_norm(t))     # noqa: E731
+    # ||E W||_F <= ||E||_F ||W||_2, and the result's own rounding
+    wide = lambda t: float(torch.linalg.matrix_norm(t, 2)) if t.numel() else 0.0   # noqa: E731
+    dh_norm = norm(dz_off) * wide(w) + norm(dh) * 2.0 ** -8
+    dw_norm = norm(dz_off) * wide(h) + norm(dw) * 2.0 ** -8
+    full = torch.zeros(hidden.shape, dtype=F64, device=hidden.device)
+    full_off = torch.zeros_like(full)
+    full[live], full_off[live] = dh, dh_off
+    if old is not None:
+        dw = dw + old.to(F64)
+        dw_off = dw_off + 2 * U * dw.abs()
+        dw_norm += norm(dw) * 2.0 ** -8
+    return (full, full_off, dh_norm), (dw, dw_off, dw_norm)

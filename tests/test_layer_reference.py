@@ -46,3 +46,21 @@ def test_norm_is_autograds():
     (dx, _), (dw, _), (again, _) = L.rms_norm_grad(dy, x.detach(), w.detach(), rstd, t)
     for a, b in ((out, y), (again, y), (dx, x.grad), (dw, w.grad)):
         assert torch.allclose(a, b.detach(), rtol=1e-12, atol=1e-12)
+
+
+def test_head_loss_is_autograds():
+    g = torch.Generator().manual_seed(7)
+    h = torch.randn((9, 24), generator=g).bfloat16().to(F64).requires_grad_()
+    w = (torch.randn((50, 24), generator=g) * 0.3).bfloat16().to(F64).requires_grad_()
+    y = torch.tensor([3, -100, 49, 0, 50, 7, 7, 8, 1])
+    gl = torch.rand(9, generator=g)
+    gl[5] = 0.0
+    each = torch.nn.functional.cross_entropy(h @ w.t(), torch.where(y < 50, y, -100),
+                                             reduction="none", ignore_index=-100)
+    (each * gl).sum().backward()
+    (loss, _), (lse, _) = L.head_loss(h.detach(), w.detach(), y)
+    assert torch.allclose(loss, each.detach(), rtol=1e-12, atol=1e-12)
+    # the reference takes the rows' fp32 lse; here in full, through a 64-bit tensor
+    (dh, _, _), (dw, _, _) = L.head_loss_grad(h.detach(), w.detach(), y, lse, gl)
+    assert torch.allclose(dh, h.grad, rtol=1e-12, atol=1e-12)
+    assert torch.allclose(dw, w.grad, rtol=1e-12, atol=1e-12)
