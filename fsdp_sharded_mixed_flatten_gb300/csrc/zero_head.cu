@@ -22,6 +22,7 @@
 
 #include "zero_kernels.cuh"
 #include "zero_ops.cuh"
+#include "zero_status.cuh"
 #include "zero_tile.cuh"
 
 namespace zf {
@@ -834,18 +835,7 @@ cudaError_t launch_head_finish(const HeadCall& c, const HeadPlan& p, cudaStream_
 }
 
 cudaError_t read_head_status(int* status, int clear, cudaStream_t stream) {
-    int v = 0;
-    cudaError_t e =
-        cudaMemcpyFromSymbolAsync(&v, g_head_status, sizeof(int), 0, cudaMemcpyDeviceToHost, stream);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-    if (e == cudaSuccess && clear) {
-        const int zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_head_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice,
-                                    stream);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-    }
-    *status = v;
-    return e;
+    return read_status_word(g_head_status, status, clear, stream);
 }
 
 }  // namespace zf

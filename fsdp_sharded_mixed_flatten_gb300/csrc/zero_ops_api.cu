@@ -506,7 +506,7 @@ ZERO_API int zero_rms_norm(const void* x, const void* residual, int32_t act_byte
 ZERO_API int zero_rms_norm_grad_workspace_bytes(int64_t n_rows, int64_t dim, int64_t* bytes) {
     if (bytes == nullptr) return fail(ZERO_ERR_INVALID_ARG, "bytes is NULL");
     if (int rc = check_norm(n_rows, dim, 2, 2)) return rc;
-    *bytes = static_cast<int64_t>(zf::rms_grad_ctas(n_rows, dim)) * dim * 4;
+    *bytes = static_cast<int64_t>(zf::rms_grad_ctas(n_rows)) * dim * 4;
     return ok();
 }
 
@@ -553,7 +553,7 @@ ZERO_API int zero_rms_norm_grad(const void* grad_out, const void* total, const u
     if (int rc = check_workspace(
             workspace, workspace_bytes,
             grad_weight == nullptr ? 0
-                                   : static_cast<int64_t>(zf::rms_grad_ctas(n_rows, dim)) * dim * 4))
+                                   : static_cast<int64_t>(zf::rms_grad_ctas(n_rows)) * dim * 4))
         return rc;
     if (n_rows == 0 && grad_weight == nullptr) return ok();
     zf::RmsArgs a{};
@@ -584,7 +584,7 @@ ZERO_API int zero_rms_norm_grad(const void* grad_out, const void* total, const u
         return rc;
     if (grad_weight == nullptr) return ok();
     return cuda_call("rms norm gradient reduction launch",
-                     [&] { return zf::launch_rms_reduce(a, s); });
+                     [&] { return zf::launch_rms_reduce(a, act_bytes, s); });
 }
 
 namespace {

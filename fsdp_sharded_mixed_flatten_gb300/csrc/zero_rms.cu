@@ -12,7 +12,13 @@
 // over all rows; each CTA writes one partial row, which a second launch adds up in CTA
 // order.
 #include "zero_eight.cuh"
+
+#include <mutex>
+
+#include "zero_kernels.cuh"
 #include "zero_ops.cuh"
+#include "zero_status.cuh"
+#include "zero_tile.cuh"
 
 namespace zf {
 
@@ -192,6 +198,330 @@ rms_norm_grad_kernel(const __grid_constant__ RmsArgs a) {
     }
 }
 
+// The same through shared memory, for whole octets on 16-byte boundaries: every group has
+// a ring of slots, one row's arrays each, that its first thread fills by bulk copies, so
+// that several rows a group are on their way whatever the registers hold.  A slot is
+// filled again when the group's next exchange shows that all have done with it.
+constexpr int kRowsThreads = 512;
+constexpr uint64_t kRowsWaitNs = 2000000000ull;
+
+__device__ int g_rms_status = 0;
+
+struct RowsRing {
+    uint32_t base, slot_bytes, bars;       // in shared memory
+    int slots, at;
+    uint32_t phase;
+    int* stop;
+    __device__ __forceinline__ uint32_t here() const { return base + at * slot_bytes; }
+    __device__ __forceinline__ uint32_t bar(int s) const { return bars + 8 * s; }
+    // The slot's row has come.  When a wait runs out the launch goes on with what is there
+    // (no group is left waiting for a part of itself) and the status tells.
+    __device__ __forceinline__ void wait() const {
+        const uint32_t b = bar(at);
+        if (tile::bar_try(b, phase)) return;
+        const uint64_t t0 = tile::now_ns();
+        while (!tile::bar_try(b, phase)) {
+            if (*static_cast<volatile int*>(stop)) return;
+            if (tile::now_ns() - t0 > kRowsWaitNs) {
+                *static_cast<volatile int*>(stop) = 1;
+                atomicCAS(&g_rms_status, kDeviceOk, kDeviceTimeout);
+                return;
+            }
+        }
+    }
+    __device__ __forceinline__ void next() {
+        if (++at == slots) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+template <class T>
+__device__ __forceinline__ Octet<T> octet_at(uint32_t address) {
+    Octet<T> v;
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(v) / 16); ++i) {
+        uint4& w = reinterpret_cast<uint4*>(&v)[i];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                     : "r"(address + 16 * i));
+    }
+    return v;
+}
+
+__device__ __forceinline__ uint2 codes_at(uint32_t address) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(address));
+    return v;
+}
+
+__device__ __forceinline__ void values_of(float (&y)[8], uint2 codes, float scale) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        const uint32_t w = e < 4 ? codes.x : codes.y;
+        const float2 v = eight_values((w >> (8 * (e % 4))) & 0xFFFFu, scale);
+        y[e] = v.x;
+        y[e + 1] = v.y;
+    }
+}
+
+// Sets up the CTA's rings; the weight goes to shared memory in fp32, [dim] after the rings.
+__device__ __forceinline__ RowsRing rows_begin(const RmsArgs& a, const RmsGroup& g, char* dyn,
+                                               float*& weight, int* stop) {
+    RowsRing r;
+    const uint32_t at = tile::smem_address(dyn);
+    r.slots = a.slots;
+    r.slot_bytes = a.slot_bytes;
+    r.base = at + g.index * a.slots * a.slot_bytes;
+    const uint32_t rings = g.per_cta * a.slots * a.slot_bytes;
+    weight = reinterpret_cast<float*>(dyn + rings);
+    r.bars = at + rings + 4 * a.dim + g.index * a.slots * 8;       // dim is a multiple of 8
+    r.at = 0;
+    r.phase = 0;
+    r.stop = stop;
+    if (threadIdx.x == 0) *stop = 0;
+    if (g.t == 0) {
+        for (int s = 0; s < r.slots; ++s) tile::bar_init(r.bar(s), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    for (int c = threadIdx.x; c < a.dim; c += blockDim.x)
+        weight[c] = a.weight == nullptr ? 1.0f : ld_param(a.weight, a.param_f32, c);
+    __syncthreads();
+    return r;
+}
+
+__device__ __forceinline__ void rows_end(const int* stop) {
+    if (*static_cast<const volatile int*>(stop)) {         // copies under way get time to come
+        const uint64_t t0 = tile::now_ns();
+        while (tile::now_ns() - t0 < 20000000ull) {}
+    }
+}
+
+template <class T, int K>
+__global__ void __launch_bounds__(kRowsThreads, 1)
+rms_rows_kernel(const __grid_constant__ RmsArgs a) {
+    extern __shared__ __align__(128) char dyn[];
+    __shared__ float red[2][kRmsWarps];
+    __shared__ int stop;
+    int half = 0;
+    const RmsGroup g(a.group_threads);
+    const Octets<true, K> c(g.t, g.threads, a.dim);
+    const float inv_d = 1.0f / static_cast<float>(a.dim);
+    float* weight;
+    RowsRing ring = rows_begin(a, g, dyn, weight, &stop);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * g.per_cta;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * g.per_cta + g.index;
+    const uint32_t bytes = a.dim * sizeof(T);
+    auto fill = [&](int64_t at, int s) {
+        if (at >= a.n_rows) return;
+        const uint32_t to = ring.base + s * ring.slot_bytes, bar = ring.bar(s);
+        tile::bar_expect(bar, a.residual != nullptr ? 2 * bytes : bytes);
+        tile::bulk_load(to, static_cast<const T*>(a.x) + at * a.x_stride, bytes, bar);
+        if (a.residual != nullptr)
+            tile::bulk_load(to + bytes,
+                            static_cast<const T*>(a.residual) + at * a.residual_stride, bytes, bar);
+    };
+    if (g.t == 0) {
+        for (int s = 0; s < ring.slots; ++s) fill(row + s * step, s);
+    }
+    for (; row < a.n_rows; row += step) {
+        ring.wait();
+        const uint32_t from = ring.here();
+        float s[K][8];
+        float q = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const bool in = c.at(k, 0) < a.dim;
+            const uint32_t place = from + (in ? c.at(k, 0) : 0) * sizeof(T);
+            const Octet<T> x = octet_at<T>(place);
+            if (a.residual != nullptr) {
+                const Octet<T> r = octet_at<T>(place + bytes);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[k][e] = __fadd_rn(widen<T>(x.x[e]), widen<T>(r.x[e]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[k][e] = widen<T>(x.x[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (!in) s[k][e] = 0.0f;
+                q = __fmaf_rn(s[k][e], s[k][e], q);
+            }
+        }
+        const float r = inv_sqrt(__fmaf_rn(rms_group_sum(g, q, red, half), inv_d, a.eps));
+        if (g.t == 0) {
+            fill(row + ring.slots * step, ring.at);
+            if (a.rstd != nullptr) a.rstd[row] = r;
+        }
+        ring.next();
+        if (a.total != nullptr) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                c.template store<T>(static_cast<T*>(a.total) + row * a.total_stride, k, s[k]);
+        }
+        if (a.total8 != nullptr) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                c.store_eight(a.total8 + row * a.total8_stride, a.total8_scales + row * a.blocks,
+                              k, s[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int col = c.at(k, 0) < a.dim ? c.at(k, 0) : 0;
+            const Octet<float> w = octet_at<float>(tile::smem_address(weight + col));
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = s[k][e] * r * w.x[e];
+            if (a.out != nullptr)
+                c.template store<T>(static_cast<T*>(a.out) + row * a.out_stride, k, y);
+            if (a.out8 != nullptr)
+                c.store_eight(a.out8 + row * a.out8_stride, a.out8_scales + row * a.blocks, k, y);
+        }
+    }
+    __syncthreads();
+    rows_end(&stop);
+}
+
+template <class T, int K, bool EIGHT>
+__global__ void __launch_bounds__(kRowsThreads, 1)
+rms_rows_grad_kernel(const __grid_constant__ RmsArgs a) {
+    extern __shared__ __align__(128) char dyn[];
+    __shared__ float red[2][kRmsWarps];
+    __shared__ int stop;
+    int half = 0;
+    const RmsGroup g(a.group_threads);
+    const Octets<true, K> c(g.t, g.threads, a.dim);
+    const float inv_d = 1.0f / static_cast<float>(a.dim);
+    float* weight;
+    RowsRing ring = rows_begin(a, g, dyn, weight, &stop);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t step = static_cast<int64_t>(gridDim.x) * g.per_cta;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * g.per_cta + g.index;
+    const uint32_t bytes = a.dim * sizeof(T), first = EIGHT ? a.dim : bytes;
+    auto fill = [&](int64_t at, int s) {
+        if (at >= a.n_rows) return;
+        const uint32_t to = ring.base + s * ring.slot_bytes, bar = ring.bar(s);
+        tile::bar_expect(bar, first + (a.grad_total != nullptr ? 2 * bytes : bytes));
+        if constexpr (EIGHT) {
+            tile::bulk_load(to, a.total8 + at * a.total8_stride, first, bar);
+        } else {
+            tile::bulk_load(to, static_cast<const T*>(a.x) + at * a.x_stride, first, bar);
+        }
+        tile::bulk_load(to + first, static_cast<const T*>(a.grad_out) + at * a.grad_out_stride,
+                        bytes, bar);
+        if (a.grad_total != nullptr)
+            tile::bulk_load(to + first + bytes,
+                            static_cast<const T*>(a.grad_total) + at * a.grad_total_stride, bytes,
+                            bar);
+    };
+    if (g.t == 0) {
+        for (int s = 0; s < ring.slots; ++s) fill(row + s * step, s);
+    }
+    float dw[K][8];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[k][e] = 0.0f;
+    }
+    float next_r = 0.0f, scale[K], next_scale[K];
+    auto load_small = [&](int64_t at) {
+        if (at >= a.n_rows) return;
+        next_r = a.rstd[at];
+        if constexpr (EIGHT) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int col = c.at(k, 0) < a.dim ? c.at(k, 0) : 0;
+                next_scale[k] = a.total8_scales[at * a.blocks + col / kEightBlock];
+            }
+        }
+    };
+    load_small(row);
+    int64_t before = -1;                       // the row before, whose slot is to be filled
+    for (; row < a.n_rows; row += step) {
+        ring.wait();
+        const uint32_t from = ring.here();
+        const float r = next_r;
+#pragma unroll
+        for (int k = 0; k < K; ++k) scale[k] = next_scale[k];
+        load_small(row + step);
+        // xh, dy and the weight of octet k (zeros where there is none)
+        auto octet = [&](int k, float (&xh)[8], float (&d)[8], float (&w)[8]) {
+            const bool in = c.at(k, 0) < a.dim;
+            const int col = in ? c.at(k, 0) : 0;
+            if constexpr (EIGHT) {
+                values_of(xh, codes_at(from + col), scale[k]);
+            } else {
+                const Octet<T> x = octet_at<T>(from + col * sizeof(T));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) xh[e] = widen<T>(x.x[e]);
+            }
+            const Octet<T> y = octet_at<T>(from + first + col * sizeof(T));
+            const Octet<float> v = octet_at<float>(tile::smem_address(weight + col));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                xh[e] *= r;
+                d[e] = in ? widen<T>(y.x[e]) : 0.0f;
+                w[e] = v.x[e];
+            }
+        };
+        float q = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float xh[8], d[8], w[8];
+            octet(k, xh, d, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                dw[k][e] = __fmaf_rn(d[e], xh[e], dw[k][e]);
+                q = __fmaf_rn(d[e] * w[e], xh[e], q);
+            }
+        }
+        const float m = -rms_group_sum(g, q, red, half) * inv_d;
+        if (g.t == 0 && before >= 0)
+            fill(before + ring.slots * step, ring.at == 0 ? ring.slots - 1 : ring.at - 1);
+        before = row;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float xh[8], d[8], w[8], y[8];
+            octet(k, xh, d, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = r * __fmaf_rn(xh[e], m, d[e] * w[e]);
+            if (a.grad_total != nullptr) {
+                const int col = c.at(k, 0) < a.dim ? c.at(k, 0) : 0;
+                const Octet<T> t = octet_at<T>(from + first + bytes + col * sizeof(T));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] += widen<T>(t.x[e]);
+            }
+            c.template store<T>(static_cast<T*>(a.grad_x) + row * a.grad_x_stride, k, y);
+            if (a.out != nullptr) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = xh[e] * w[e];
+                c.template store<T>(static_cast<T*>(a.out) + row * a.out_stride, k, y);
+            }
+        }
+        ring.next();
+    }
+    __syncthreads();                           // the rings and the weight have been used up
+    rows_end(&stop);
+    if (a.grad_weight == nullptr) return;
+    float* cols = reinterpret_cast<float*>(dyn);         // [groups][dim]
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if (c.at(k, 0) < a.dim) {
+            float4* to = reinterpret_cast<float4*>(cols + g.index * a.dim + c.at(k, 0));
+            to[0] = make_float4(dw[k][0], dw[k][1], dw[k][2], dw[k][3]);
+            to[1] = make_float4(dw[k][4], dw[k][5], dw[k][6], dw[k][7]);
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.dim; i += blockDim.x) {
+        float t = 0.0f;
+        for (int j = 0; j < g.per_cta; ++j) t += cols[j * a.dim + i];
+        if (gridDim.x == 1) st_param(a.grad_weight, a.param_f32, i, t);
+        else a.partials[static_cast<int64_t>(blockIdx.x) * a.dim + i] = t;
+    }
+}
+
 // Column sums over the CTAs' partial rows: 32 columns a block, 32 strands of CTAs, joined
 // in a fixed order.
 constexpr int kRmsStrands = 32;
@@ -276,6 +606,29 @@ RmsShape rms_shape(int64_t dim) {
     return {k, group, per_cta};
 }
 
+// The form through shared memory: groups and slots a ring that fit an SM.
+constexpr int64_t kRowsSmem = 220 * 1024;
+
+struct RowsShape {
+    int k, group, per_cta, slots;
+    int64_t slot_bytes, smem;
+};
+
+RowsShape rows_shape(int64_t dim, int64_t slot_bytes) {
+    RowsShape s{};
+    s.k = dim <= 1024 ? 1 : dim <= 4096 ? 2 : 4;
+    s.group = static_cast<int>((dim + 256 * s.k - 1) / (256 * s.k) * 32);
+    s.slot_bytes = slot_bytes;
+    const int64_t room = kRowsSmem - 4 * dim - 1024;
+    s.per_cta = kRowsThreads / s.group < 8 ? kRowsThreads / s.group : 8;
+    while (s.per_cta > 1 && room / (s.per_cta * slot_bytes) < 3) --s.per_cta;
+    s.slots = static_cast<int>(room / (s.per_cta * slot_bytes));
+    if (s.slots > 8) s.slots = 8;
+    s.smem = s.per_cta * s.slots * slot_bytes + 4 * dim + 8 * s.per_cta * s.slots;
+    if (s.smem < s.per_cta * dim * 4) s.smem = s.per_cta * dim * 4;
+    return s;
+}
+
 int64_t rms_grid(const RmsShape& s, int64_t rows, int64_t per_sm) {
     const int64_t need = (rows + s.per_cta - 1) / s.per_cta;
     const int64_t most = static_cast<int64_t>(device_sms()) * per_sm;
@@ -309,64 +662,132 @@ bool wide_codes(const void* p, int64_t stride) {
     return p == nullptr || (aligned_to(p, 8) && stride % 8 == 0);
 }
 
+// A kernel's leave to use all of the shared memory, once a device.
+template <class K>
+cudaError_t allow_smem(K kernel, std::once_flag (&once)[64], cudaError_t (&set)[64]) {
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::call_once(once[dev], [&] {
+        set[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(kRowsSmem));
+    });
+    return set[dev];
+}
+
+// What a call takes: rows through shared memory, or straight to registers.
+struct RmsPlan {
+    bool rows, wide;
+    RowsShape through;
+    RmsShape straight;
+    int64_t grid;
+};
+
+RmsPlan forward_plan(const RmsArgs& a, int act_bytes) {
+    RmsPlan p{};
+    p.wide = wide_rows(a.x, a.x_stride, act_bytes) &&
+             wide_rows(a.residual, a.residual_stride, act_bytes) &&
+             wide_rows(a.total, a.total_stride, act_bytes) &&
+             wide_rows(a.out, a.out_stride, act_bytes) && wide_codes(a.out8, a.out8_stride) &&
+             wide_codes(a.total8, a.total8_stride);
+    p.straight = rms_shape(a.dim);
+    p.through = rows_shape(a.dim, static_cast<int64_t>(a.residual != nullptr ? 2 : 1) * act_bytes * a.dim);
+    p.rows = p.wide && a.dim % 8 == 0 && p.through.slots >= 2;
+    p.grid = p.rows ? rms_grid({0, 0, p.through.per_cta}, a.n_rows, 1)
+                    : rms_forward_grid(p.straight, a.n_rows);
+    return p;
+}
+
+RmsPlan backward_plan(const RmsArgs& a, int act_bytes) {
+    RmsPlan p{};
+    const bool eight = a.total8 != nullptr;
+    p.wide = wide_rows(a.x, a.x_stride, act_bytes) &&
+             wide_rows(a.grad_out, a.grad_out_stride, act_bytes) &&
+             wide_rows(a.grad_total, a.grad_total_stride, act_bytes) &&
+             wide_rows(a.grad_x, a.grad_x_stride, act_bytes) &&
+             wide_rows(a.out, a.out_stride, act_bytes) && wide_codes(a.total8, a.total8_stride);
+    p.straight = rms_shape(a.dim);
+    p.through = rows_shape(a.dim, static_cast<int64_t>(a.dim) *
+                                      ((a.grad_total != nullptr ? 2 : 1) * act_bytes +
+                                       (eight ? 1 : act_bytes)));
+    p.rows = p.wide && a.dim % 8 == 0 && p.through.slots >= 2 &&
+             (!eight || (a.dim % 16 == 0 && wide_rows(a.total8, a.total8_stride, 1)));
+    p.grid = p.rows ? rms_grid({0, 0, p.through.per_cta}, a.n_rows, 1)
+                    : rms_backward_grid(p.straight, a.n_rows);
+    return p;
+}
+
+template <class T, int K, bool BACK, bool EIGHT>
+cudaError_t launch_rows(const RmsArgs& a, const RmsPlan& p, cudaStream_t stream) {
+    static std::once_flag once[64];
+    static cudaError_t set[64];
+    const auto kernel = [] {
+        if constexpr (BACK) return rms_rows_grad_kernel<T, K, EIGHT>;
+        else return rms_rows_kernel<T, K>;
+    }();
+    if (cudaError_t e = allow_smem(kernel, once, set); e != cudaSuccess) return e;
+    kernel<<<static_cast<unsigned>(p.grid), p.through.group * p.through.per_cta, p.through.smem,
+             stream>>>(a);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
-int rms_grad_ctas(int64_t n_rows, int64_t dim) {
-    return static_cast<int>(rms_backward_grid(rms_shape(dim), n_rows));
+int rms_grad_ctas(int64_t n_rows) {
+    const int64_t sms = device_sms();
+    return static_cast<int>(n_rows < 1 ? 1 : n_rows < sms ? n_rows : sms);
 }
 
 cudaError_t launch_rms_norm(RmsArgs a, int act_bytes, cudaStream_t stream) {
-    const RmsShape s = rms_shape(a.dim);
-    a.group_threads = s.group;
-    const bool wide = wide_rows(a.x, a.x_stride, act_bytes) &&
-                      wide_rows(a.residual, a.residual_stride, act_bytes) &&
-                      wide_rows(a.total, a.total_stride, act_bytes) &&
-                      wide_rows(a.out, a.out_stride, act_bytes) &&
-                      wide_codes(a.out8, a.out8_stride) && wide_codes(a.total8, a.total8_stride);
-    const unsigned grid = static_cast<unsigned>(rms_forward_grid(s, a.n_rows));
+    const RmsPlan p = forward_plan(a, act_bytes);
+    a.group_threads = p.rows ? p.through.group : p.straight.group;
+    a.slots = p.through.slots;
+    a.slot_bytes = static_cast<uint32_t>(p.through.slot_bytes);
     return by_type(act_bytes, [&](auto t) {
         using T = decltype(t);
-        return by_k(s.k, [&](auto k) {
-            if (wide) rms_norm_kernel<T, k.value, true><<<grid, s.group * s.per_cta, 0, stream>>>(a);
-            else rms_norm_kernel<T, k.value, false><<<grid, s.group * s.per_cta, 0, stream>>>(a);
+        return by_k(p.rows ? p.through.k : p.straight.k, [&](auto k) {
+            constexpr int K = k.value;
+            if (p.rows) return launch_rows<T, K, false, false>(a, p, stream);
+            const unsigned grid = static_cast<unsigned>(p.grid);
+            const int threads = p.straight.group * p.straight.per_cta;
+            if (p.wide) rms_norm_kernel<T, K, true><<<grid, threads, 0, stream>>>(a);
+            else rms_norm_kernel<T, K, false><<<grid, threads, 0, stream>>>(a);
             return cudaGetLastError();
         });
     });
 }
 
 cudaError_t launch_rms_norm_grad(RmsArgs a, int act_bytes, cudaStream_t stream) {
-    const RmsShape s = rms_shape(a.dim);
-    a.group_threads = s.group;
-    const bool wide = wide_rows(a.x, a.x_stride, act_bytes) &&
-                      wide_rows(a.grad_out, a.grad_out_stride, act_bytes) &&
-                      wide_rows(a.grad_total, a.grad_total_stride, act_bytes) &&
-                      wide_rows(a.grad_x, a.grad_x_stride, act_bytes) &&
-                      wide_rows(a.out, a.out_stride, act_bytes) &&
-                      wide_codes(a.total8, a.total8_stride);
-    const unsigned grid = static_cast<unsigned>(rms_backward_grid(s, a.n_rows));
-    const size_t smem = sizeof(float) * s.per_cta * a.dim;
+    const RmsPlan p = backward_plan(a, act_bytes);
+    a.group_threads = p.rows ? p.through.group : p.straight.group;
+    a.slots = p.through.slots;
+    a.slot_bytes = static_cast<uint32_t>(p.through.slot_bytes);
     return by_type(act_bytes, [&](auto t) {
         using T = decltype(t);
-        return by_k(s.k, [&](auto k) {
+        return by_k(p.rows ? p.through.k : p.straight.k, [&](auto k) {
             constexpr int K = k.value;
+            if (p.rows)
+                return a.total8 != nullptr ? launch_rows<T, K, true, true>(a, p, stream)
+                                           : launch_rows<T, K, true, false>(a, p, stream);
             const auto kernel = a.total8 != nullptr
-                                    ? (wide ? rms_norm_grad_kernel<T, K, true, true>
-                                            : rms_norm_grad_kernel<T, K, false, true>)
-                                    : (wide ? rms_norm_grad_kernel<T, K, true, false>
-                                            : rms_norm_grad_kernel<T, K, false, false>);
+                                    ? (p.wide ? rms_norm_grad_kernel<T, K, true, true>
+                                              : rms_norm_grad_kernel<T, K, false, true>)
+                                    : (p.wide ? rms_norm_grad_kernel<T, K, true, false>
+                                              : rms_norm_grad_kernel<T, K, false, false>);
             // at most 64 KB: 4 groups of 4096 columns, 1 of 16384
             if (cudaError_t e = cudaFuncSetAttribute(
                     kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
                 e != cudaSuccess)
                 return e;
-            kernel<<<grid, s.group * s.per_cta, smem, stream>>>(a);
+            kernel<<<static_cast<unsigned>(p.grid), p.straight.group * p.straight.per_cta,
+                     sizeof(float) * p.straight.per_cta * a.dim, stream>>>(a);
             return cudaGetLastError();
         });
     });
 }
 
-cudaError_t launch_rms_reduce(const RmsArgs& a, cudaStream_t stream) {
-    const int64_t parts = rms_backward_grid(rms_shape(a.dim), a.n_rows);
+cudaError_t launch_rms_reduce(const RmsArgs& a, int act_bytes, cudaStream_t stream) {
+    const int64_t parts = backward_plan(a, act_bytes).grid;
     if (parts == 1) return cudaSuccess;                      // the sums themselves are there
     // its blocks may be set up while the partial rows are still being added up
     cudaLaunchConfig_t cfg{};
@@ -379,6 +800,10 @@ cudaError_t launch_rms_reduce(const RmsArgs& a, cudaStream_t stream) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, rms_reduce_kernel, a, static_cast<int>(parts));
+}
+
+cudaError_t read_rms_status(int* status, int clear, cudaStream_t stream) {
+    return read_status_word(g_rms_status, status, clear, stream);
 }
 
 cudaError_t launch_eight(EightArgs a, int act_bytes, cudaStream_t stream) {

@@ -74,6 +74,15 @@ __device__ __forceinline__ uint64_t now_ns() {
 
 // ---------------------------------------------------------------- TMA -------
 
+// Contiguous bytes to shared memory: both addresses and the size are multiples of 16.
+__device__ __forceinline__ void bulk_load(uint32_t to, const void* from, uint32_t bytes,
+                                          uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+        ::"r"(to), "l"(from), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
 // A box of a two-dimensional tensor map to shared memory; x times the element size is a
 // multiple of 16 bytes.  The bytes count on the barrier of the pair's CTA 0, at the same
 // place as `bar` is here.
