@@ -36,12 +36,18 @@ __device__ __forceinline__ float finite_magnitude(float x) {
     return m <= kLargest ? m : 0.0f;                 // 0 for infinities and NaN
 }
 
-// Code pairs of x / scale (low byte first).  Infinities become NaN, as NaN does: e4m3 has
-// no infinity, and a saturated one would pass for a value.
-__device__ __forceinline__ uint32_t eight_codes(float lo, float hi, float inverse, bool top) {
+// Code pairs of x / scale (low byte first); NaN becomes code 127.
+__device__ __forceinline__ uint32_t eight_codes(float lo, float hi, float inverse) {
+    const float2 v = unpair(mul2(pair(lo, hi), pair(inverse, inverse)));
+    return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+}
+// The same where the block holds infinities, which become NaN (e4m3 has none, and a
+// saturated one would pass for a value), or magnitudes next to 2^128 (240 instead of 256:
+// half a step off at most).
+__device__ __noinline__ uint32_t eight_codes_rare(float lo, float hi, float inverse, bool top) {
     lo = fabsf(lo) <= kLargest ? lo * inverse : __int_as_float(0x7FFFFFFF);
     hi = fabsf(hi) <= kLargest ? hi * inverse : __int_as_float(0x7FFFFFFF);
-    if (top) {                       // 240 instead of 256: half a step off at most
+    if (top) {
         lo = lo > 240.0f ? 240.0f : lo < -240.0f ? -240.0f : lo;
         hi = hi > 240.0f ? 240.0f : hi < -240.0f ? -240.0f : hi;
     }
@@ -120,19 +126,33 @@ struct Octets {
     __device__ __forceinline__ void store_eight(uint8_t* row, float* scales, int k,
                                                 const float (&y)[8]) const {
         if constexpr (WIDE) {
+            // (the larger of a number and NaN is the number)
             float m = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_magnitude(y[e]));
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            const uint32_t s = eight_exponent(m);
-            const float inverse = __uint_as_float((254 - s) << 23);
-            const bool top = s == kEightTop;
-            uint32_t w[2];
+            uint32_t s = eight_exponent(m), w[2];
+            if (__any_sync(0xFFFFFFFFu, s >= kEightTop)) {
+                m = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                w[i] = eight_codes(y[4 * i], y[4 * i + 1], inverse, top) |
-                       eight_codes(y[4 * i + 2], y[4 * i + 3], inverse, top) << 16;
+                for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_magnitude(y[e]));
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                s = eight_exponent(m);
+                const float inverse = __uint_as_float((254 - s) << 23);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    w[i] = eight_codes_rare(y[4 * i], y[4 * i + 1], inverse, s == kEightTop) |
+                           eight_codes_rare(y[4 * i + 2], y[4 * i + 3], inverse, s == kEightTop)
+                               << 16;
+            } else {
+                const float inverse = __uint_as_float((254 - s) << 23);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    w[i] = eight_codes(y[4 * i], y[4 * i + 1], inverse) |
+                           eight_codes(y[4 * i + 2], y[4 * i + 3], inverse) << 16;
+            }
             const int c = at(k, 0);
             if (c + 7 < dim) {
                 *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
@@ -149,14 +169,22 @@ struct Octets {
             for (int b = 0; b < 2; ++b) {
                 float m = 0.0f;
 #pragma unroll
-                for (int e = 4 * b; e < 4 * b + 4; ++e) m = fmaxf(m, finite_magnitude(y[e]));
+                for (int e = 4 * b; e < 4 * b + 4; ++e) m = fmaxf(m, fabsf(y[e]));
                 m = warp_max(m);
-                const uint32_t s = eight_exponent(m);
+                uint32_t s = eight_exponent(m);
+                const bool rare = s >= kEightTop;        // of the whole warp
+                if (rare) {
+                    m = 0.0f;
+#pragma unroll
+                    for (int e = 4 * b; e < 4 * b + 4; ++e) m = fmaxf(m, finite_magnitude(y[e]));
+                    s = eight_exponent(warp_max(m));
+                }
                 const float inverse = __uint_as_float((254 - s) << 23);
-                const bool top = s == kEightTop;
 #pragma unroll
                 for (int e = 4 * b; e < 4 * b + 4; e += 2) {
-                    const uint32_t w = eight_codes(y[e], y[e + 1], inverse, top);
+                    const uint32_t w =
+                        rare ? eight_codes_rare(y[e], y[e + 1], inverse, s == kEightTop)
+                             : eight_codes(y[e], y[e + 1], inverse);
                     if (ok(k, e)) row[at(k, e)] = static_cast<uint8_t>(w);
                     if (ok(k, e + 1)) row[at(k, e + 1)] = static_cast<uint8_t>(w >> 8);
                 }

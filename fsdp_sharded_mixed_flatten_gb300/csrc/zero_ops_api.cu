@@ -399,9 +399,9 @@ int eight(const void* x, void* out, int32_t bytes, int64_t n_rows, int64_t dim, 
     const bool pack = out == nullptr;
     if (n_rows < 0 || dim < 1)
         return fail(ZERO_ERR_INVALID_ARG, "n_rows >= 0 and dim >= 1 are needed");
-    // as many CTAs as a launch takes
-    if (n_rows > kMax32 || dim > kMax32 || n_rows * ((dim + 1023) / 1024) > kMax32)
-        return fail(ZERO_ERR_SIZE, "n_rows * ceil(dim / 1024) must fit 32 bits");
+    // as many CTAs as a launch takes, of eight warps that take 512 columns at least
+    if (n_rows > kMax32 || dim > kMax32 - 1024 || n_rows * ((dim + 511) / 512) > kMax32)
+        return fail(ZERO_ERR_SIZE, "n_rows * ceil(dim / 512) must fit 32 bits");
     if (int rc = check_type(bytes, pack ? "x_bytes" : "out_bytes")) return rc;
     if (int rc = check_rows(pack ? x : out, n_rows, dim, stride, bytes, pack ? "x" : "out"))
         return rc;
