@@ -40,8 +40,9 @@ constexpr int kStages = 6;
 constexpr uint32_t kOperandBytes = kHalf * kTileK * 2;
 constexpr uint32_t kStageBytes = 2 * kOperandBytes;
 constexpr uint32_t kChunkBytes = kTileK * 128;        // 64 values along M or N, MN-major
-constexpr size_t kHeadSmem = kStages * kStageBytes + 1024;
-constexpr int kEpilogueWarps = 4;
+constexpr uint32_t kStagingBytes = 4096;      // an epilogue warp's
+constexpr int kEpilogueWarps = 8;
+constexpr size_t kHeadSmem = kStages * kStageBytes + kEpilogueWarps * kStagingBytes + 1024;
 constexpr int kHeadThreads = 64 + 32 * kEpilogueWarps;
 constexpr uint32_t kTmemColumns = 512;      // two tiles' results
 constexpr uint64_t kHeadWaitNs = 2000000000ull;
@@ -75,8 +76,8 @@ struct Shared {
     int stop;
 };
 
-// Waits for a phase; false when the pair is to stop: the wait has run out, here or in
-// another role of this CTA.
+// Waits for a phase; false when the CTA is to stop: the wait has run out, here or in
+// another of its roles.
 __device__ __noinline__ bool wait_long(Shared& sh, uint32_t bar, uint32_t parity) {
     const uint64_t t0 = now_ns();
     while (!bar_try(bar, parity)) {
@@ -130,43 +131,72 @@ struct Tiles {
     }
 };
 
-// 32 values of a row to memory.
-__device__ __forceinline__ void put_bf16(uint16_t* to, const float (&v)[32], int left, bool wide) {
-    if (wide && left >= 32) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint4 w;
-            w.x = pack_bf16x2(v[8 * i], v[8 * i + 1]);
-            w.y = pack_bf16x2(v[8 * i + 2], v[8 * i + 3]);
-            w.z = pack_bf16x2(v[8 * i + 4], v[8 * i + 5]);
-            w.w = pack_bf16x2(v[8 * i + 6], v[8 * i + 7]);
-            reinterpret_cast<uint4*>(to)[i] = w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            if (i < left) to[i] = float_to_bf16_rn(v[i]);
-        }
-    }
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// The result of a tile's row: columns of tensor memory in eight parts of 32.
+// A warp's piece of a tile on its way to memory: 32 rows of 128 bytes in shared memory, the
+// 16-byte words of row r in the order j ^ (r % 8), so that lanes may write a row each and
+// read rows side by side without meeting in a bank.
+struct Stage {
+    char* at;                     // 4 KB of this warp's
+    int lane;
+    __device__ __forceinline__ uint4& word(int r, int j) const {
+        return *reinterpret_cast<uint4*>(at + 128 * r + 16 * (j ^ (r & 7)));
+    }
+    __device__ __forceinline__ float& value(int r, int c) const {       // of 32 fp32 values
+        return *reinterpret_cast<float*>(at + 128 * r + 16 * ((c / 4) ^ (r & 7)) + 4 * (c % 4));
+    }
+    // this lane's row: 32 fp32 values
+    __device__ __forceinline__ void put(const float (&v)[32]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            word(lane, j) = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                       __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+    }
+    // ... or half of 64 bf16 values
+    __device__ __forceinline__ void put_bf16(const float (&v)[32], int half) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            word(lane, 4 * half + j) =
+                make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                           pack_bf16x2(v[8 * j + 4], v[8 * j + 5]),
+                           pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+    }
+};
+
+// The result of a tile, by warps: each has 32 rows (its lanes') and 128 of the columns, in
+// four parts of 32.
 template <int MODE>
 struct Epilogue {
     const HeadArgs& a;
-    int live;
-    __device__ Epilogue(const HeadArgs& args) : a(args), live(*args.counts) {}
+    Stage stage;
+    float2 (*both)[kHalf];        // what the second half of the columns found, by row
+    int live, place, half, lane;  // place: this warp's first row of the CTA's 128
+    __device__ Epilogue(const HeadArgs& args, char* staging, float2 (*found)[kHalf], int warp, int l)
+        : a(args),
+          stage{staging, l},
+          both(found),
+          live(*args.counts),
+          place(warp % 4 * 32),
+          half((warp - 2) / 4),
+          lane(l) {}
 
-    // `row` of the launch's M, this thread's; `load(c, v)` gives columns 32 c ...
+    // `row` of the launch's M: this warp's first; n: columns / 256; `slot`: 0 and 1 in turn;
+    // `load(c, v)` gives columns 32 c ... of this warp's half
     template <class Load>
-    __device__ __forceinline__ void operator()(int row, int n, int split, Load&& load) const {
-        const int column = n * kPairTile;
+    __device__ __forceinline__ void operator()(int row0, int n, int split, int slot,
+                                               Load&& load) const {
+        const int column = n * kPairTile + half * kHalf;
+        const int row = row0 + lane;
         if constexpr (MODE == kLoss) {
-            const int left = a.vocab - column;           // columns of the tile that exist
+            const int left = a.vocab - column;           // columns that exist
             const int mine = row < live ? a.label[row] - a.first - column : -1;
             float top = -INFINITY, sum = 0.0f, z = 0.0f;
-#pragma unroll 1
-            for (int c = 0; c < kPairTile / 32; ++c) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
                 float v[32];
                 load(c, v);
                 if (32 * c + 32 > left) {
@@ -183,71 +213,152 @@ struct Epilogue {
 #pragma unroll
                 for (int i = 1; i < 32; ++i) m = fmaxf(m, v[i]);
                 m = fmaxf(top, m * kLog2e);
-                // (a tile of -inf alone: no term)
+                // (-inf alone: no term)
                 const float from = m == -INFINITY ? 0.0f : m;
-                sum *= exp2f(top - from);
+                const Pair by = pair(kLog2e, kLog2e), minus = pair(-from, -from);
+                sum *= exp2_fast(top - from);
+                Pair t = 0;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) sum += exp2f(__fmaf_rn(v[i], kLog2e, -from));
+                for (int i = 0; i < 32; i += 2) {
+                    const float2 x = unpair(fma2(pair(v[i], v[i + 1]), by, minus));
+                    t = add2(t, pair(exp2_fast(x.x), exp2_fast(x.y)));
+                }
+                const float2 s = unpair(t);
+                sum += s.x + s.y;
                 top = m;
             }
-            if (row < live) {
-                a.parts[row * a.parts_pitch + a.first / kPairTile + n] = make_float2(top, sum);
-                if (mine >= 0 && mine < min(kPairTile, left)) a.picked[row] = z;
+            if (mine >= 0 && mine < min(kHalf, left)) a.picked[row] = z;
+            // the two halves of the columns
+            if (half == 1) both[slot][place + lane] = make_float2(top, sum);
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpilogueWarps) : "memory");
+            if (half == 0 && row < live) {
+                const float2 o = both[slot][place + lane];
+                const float m = fmaxf(top, o.x), from = m == -INFINITY ? 0.0f : m;
+                a.parts[row * a.parts_pitch + a.first / kPairTile + n] = make_float2(
+                    m, sum * exp2_fast(top - from) + o.y * exp2_fast(o.x - from));
             }
         } else if constexpr (MODE == kDz) {
             const bool in = row < live;
             const int mine = in ? a.label[row] - a.first - column : -1;
             const float off = in ? -a.lse[row] * kLog2e : 0.0f, g = in ? a.grad[row] : 0.0f;
-            uint16_t* to = a.dz + row * a.dz_pitch + column;
-            const int left = static_cast<int>(a.dz_pitch) - column;   // a multiple of 64
-#pragma unroll 1
-            for (int c = 0; c < kPairTile / 32; ++c) {
+            const Pair by = pair(kLog2e, kLog2e), minus = pair(off, off), scale = pair(g, g);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
                 float v[32];
                 load(c, v);
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    v[i] = in ? g * exp2f(__fmaf_rn(v[i], kLog2e, off)) : 0.0f;
+                for (int i = 0; i < 32; i += 2) {
+                    const float2 x = unpair(fma2(pair(v[i], v[i + 1]), by, minus));
+                    const float2 y = unpair(mul2(pair(exp2_fast(x.x), exp2_fast(x.y)), scale));
+                    v[i] = in ? y.x : 0.0f;
+                    v[i + 1] = in ? y.y : 0.0f;
+                }
                 if (mine >= 32 * c && mine < 32 * c + 32) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         if (mine == 32 * c + i) v[i] -= g;
                 }
-                if (32 * c < left) put_bf16(to + 32 * c, v, 32, true);
+                stage.put_bf16(v, c % 2);
+                if (c % 2 == 0) continue;
+                __syncwarp();
+                const int first = column + 32 * (c - 1);          // 64 columns: all there, or none
+                if (first < a.dz_pitch) {
+                    uint16_t* to = a.dz + (row0 + lane / 8) * a.dz_pitch + first + lane % 8 * 8;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4*>(to + 4 * i * a.dz_pitch) =
+                            stage.word(lane / 8 + 4 * i, lane % 8);
+                }
+                __syncwarp();
             }
         } else if constexpr (MODE == kDh) {
-            float* to = a.sums + (split * a.rows + row) * a.sums_pitch + column;
-            const int left = static_cast<int>(a.sums_pitch) - column;  // a multiple of 8
-#pragma unroll 1
-            for (int c = 0; c < kPairTile / 32; ++c) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
                 float v[32];
                 load(c, v);
-                if (row >= live) continue;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (32 * c + 4 * i >= left) break;
-                    float4* p = reinterpret_cast<float4*>(to + 32 * c) + i;
-                    float4 w = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                stage.put(v);
+                __syncwarp();
+                const int first = column + 32 * c + lane % 8 * 4;
+                if (first < a.sums_pitch) {
+                    float* to = a.sums + (split * a.rows + row0 + lane / 8) * a.sums_pitch + first;
+                    float4 old[8];
                     if (a.add) {
-                        const float4 o = *p;
-                        w = make_float4(o.x + w.x, o.y + w.y, o.z + w.z, o.w + w.w);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            old[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            if (row0 + lane / 8 + 4 * i < live)
+                                old[i] = *reinterpret_cast<const float4*>(to + 4 * i * a.sums_pitch);
+                        }
                     }
-                    *p = w;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 w = stage.word(lane / 8 + 4 * i, lane % 8);
+                        float4 x = make_float4(__uint_as_float(w.x), __uint_as_float(w.y),
+                                               __uint_as_float(w.z), __uint_as_float(w.w));
+                        if (a.add)
+                            x = make_float4(old[i].x + x.x, old[i].y + x.y, old[i].z + x.z,
+                                            old[i].w + x.w);
+                        if (row0 + lane / 8 + 4 * i < live)
+                            *reinterpret_cast<float4*>(to + 4 * i * a.sums_pitch) = x;
+                    }
                 }
+                __syncwarp();
             }
         } else {
-            uint16_t* to = a.grad_table + static_cast<int64_t>(row) * a.dim + column;
-            const int left = a.dim - column;
-#pragma unroll 1
-            for (int c = 0; c < kPairTile / 32; ++c) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
                 float v[32];
                 load(c, v);
-                if (row >= a.vocab || 32 * c >= left) continue;
-                if (a.add) {
+                stage.put(v);
+                __syncwarp();
+                const int first = column + 32 * c;
+                if (a.wide) {                            // 8 columns a lane, 8 rows at a time
+                    const int col = first + lane % 4 * 8;
+                    if (col < a.dim) {
+                        uint16_t* to =
+                            a.grad_table + static_cast<int64_t>(row0 + lane / 4) * a.dim + col;
+                        const int64_t step = static_cast<int64_t>(8) * a.dim;
+                        uint4 old[4];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (32 * c + i < left) v[i] += bf16_to_float(to[32 * c + i]);
+                        for (int i = 0; i < 4; ++i) {
+                            old[i] = make_uint4(0, 0, 0, 0);
+                            if (a.add && row0 + lane / 4 + 8 * i < a.vocab)
+                                old[i] = *reinterpret_cast<const uint4*>(to + i * step);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = lane / 4 + 8 * i;
+                            const uint4 lo = stage.word(r, lane % 4 * 2);
+                            const uint4 hi = stage.word(r, lane % 4 * 2 + 1);
+                            Pair x[4] = {pair(__uint_as_float(lo.x), __uint_as_float(lo.y)),
+                                         pair(__uint_as_float(lo.z), __uint_as_float(lo.w)),
+                                         pair(__uint_as_float(hi.x), __uint_as_float(hi.y)),
+                                         pair(__uint_as_float(hi.z), __uint_as_float(hi.w))};
+                            if (a.add) {
+                                x[0] = add2(x[0], widen2(old[i].x));
+                                x[1] = add2(x[1], widen2(old[i].y));
+                                x[2] = add2(x[2], widen2(old[i].z));
+                                x[3] = add2(x[3], widen2(old[i].w));
+                            }
+                            if (row0 + r < a.vocab)
+                                *reinterpret_cast<uint4*>(to + i * step) = make_uint4(
+                                    narrow2(x[0]), narrow2(x[1]), narrow2(x[2]), narrow2(x[3]));
+                        }
+                    }
+                } else {                                 // a column a lane, row by row
+                    const int col = first + lane;
+                    if (col < a.dim) {
+                        uint16_t* to = a.grad_table + static_cast<int64_t>(row0) * a.dim + col;
+                        const int rows = min(32, a.vocab - row0);
+#pragma unroll 8
+                        for (int r = 0; r < rows; ++r) {
+                            float x = stage.value(r, lane);
+                            if (a.add) x += bf16_to_float(to[static_cast<int64_t>(r) * a.dim]);
+                            to[static_cast<int64_t>(r) * a.dim] = float_to_bf16_rn(x);
+                        }
+                    }
                 }
-                put_bf16(to + 32 * c, v, left - 32 * c, a.wide != 0);
+                __syncwarp();
             }
         }
     }
@@ -359,33 +470,40 @@ head_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             }
         }
     } else {
-        const Epilogue<MODE> epilogue(a);
-        const int part = warp % 4;                       // of tensor memory's lanes, this warp's
+        // (the forward pass stages nothing: its halves meet there)
+        char* const staging = dyn + (ring - smem_address(dyn)) + kStages * kStageBytes;
+        const Epilogue<MODE> epilogue(a, staging + (warp - 2) * kStagingBytes,
+                                      reinterpret_cast<float2(*)[kHalf]>(staging), warp, lane);
+        const int half = epilogue.half;
         int n = 0;
         for (int i = pair; i < tiles.total; i += pairs) {
             const auto t = tiles(i);
-            const int row = t.m * kPairTile + static_cast<int>(rank) * kHalf + part * 32 + lane;
+            const int row0 = t.m * kPairTile + static_cast<int>(rank) * kHalf + epilogue.place;
             if (t.begin == t.end) {                      // a sum of nothing
-                epilogue(row, t.n, t.split, [](int, float (&v)[32]) {
+                epilogue(row0, t.n, t.split, 0, [](int, float (&v)[32]) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0.0f;
                 });
                 continue;
             }
             const int slot = n % 2;
-            const bool come = wait(sh, sh.done[slot], (n / 2) % 2);
-            if (!__all_sync(0xFFFFFFFFu, come)) break;
+            // (a wait that runs out: on with what is there, so that no warp waits for another)
+            wait(sh, sh.done[slot], (n / 2) % 2);
+            __syncwarp();
             ++n;
             fence_after_sync();
-            const uint32_t from = tmem + slot * kPairTile + (static_cast<uint32_t>(part * 32) << 16);
-            epilogue(row, t.n, t.split, [&](int c, float (&v)[32]) {
+            const uint32_t from =
+                tmem + slot * kPairTile + half * kHalf + (static_cast<uint32_t>(epilogue.place) << 16);
+            epilogue(row0, t.n, t.split, slot, [&](int c, float (&v)[32]) {
                 __syncwarp();
                 tmem_load(v, from + 32 * c);
                 tmem_load_wait();
+                if (c == 3) {                            // the tile's place may be taken
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive_in_cluster(in_cta(smem_address(&sh.taken[slot]), 0));
+                }
             });
-            fence_before_sync();
-            __syncwarp();
-            if (lane == 0) bar_arrive_in_cluster(in_cta(smem_address(&sh.taken[slot]), 0));
         }
     }
     __syncwarp();
@@ -410,49 +528,46 @@ __global__ void __launch_bounds__(kRowThreads)
 head_rows_kernel(const HeadCall c, int32_t* counts, int32_t* index, int32_t* slot, int32_t* label,
                  float* lse, float* grad, bool back) {
     __shared__ int32_t warps[32];
-    const int64_t per = (c.n_tokens + kRowThreads - 1) / kRowThreads;
-    const int64_t begin = min(per * threadIdx.x, c.n_tokens), end = min(begin + per, c.n_tokens);
+    // a warp's tokens: whole runs of 32
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t runs = (c.n_tokens + kRowThreads - 1) / kRowThreads;
+    const int64_t begin = warp * runs * 32;
     auto label_of = [&](int64_t t) {
+        if (t >= c.n_tokens) return -1;
         const int64_t y = c.label64 ? static_cast<const int64_t*>(c.labels)[t]
                                     : static_cast<const int32_t*>(c.labels)[t];
-        return y >= 0 && y < c.vocab ? static_cast<int32_t>(y) : -1;
+        const bool in = y >= 0 && y < c.vocab && (!back || c.grad_loss[t] != 0.0f);
+        return in ? static_cast<int32_t>(y) : -1;
     };
-    auto is_live = [&](int64_t t, int32_t y) { return y >= 0 && (!back || c.grad_loss[t] != 0.0f); };
     int32_t n = 0;
-    for (int64_t t = begin; t < end; ++t) n += is_live(t, label_of(t));
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    int32_t before = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int32_t v = __shfl_up_sync(0xFFFFFFFFu, before, o);
-        if (lane >= o) before += v;
-    }
-    if (lane == 31) warps[warp] = before;
+#pragma unroll 8
+    for (int64_t i = 0; i < runs; ++i)
+        n += __popc(__ballot_sync(0xFFFFFFFFu, label_of(begin + 32 * i + lane) >= 0));
+    if (lane == 0) warps[warp] = n;
     __syncthreads();
-    if (warp == 0) {
-        int32_t v = warps[lane];
+    int32_t at = lane < warp ? warps[lane] : 0, all = warps[lane];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int32_t w = __shfl_up_sync(0xFFFFFFFFu, v, o);
-            if (lane >= o) v += w;
-        }
-        warps[lane] = v;
+    for (int o = 16; o > 0; o >>= 1) {
+        at += __shfl_xor_sync(0xFFFFFFFFu, at, o);
+        all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
     }
-    __syncthreads();
-    int32_t at = before - n + (warp == 0 ? 0 : warps[warp - 1]);
-    if (threadIdx.x == kRowThreads - 1) *counts = at + n;
-    for (int64_t t = begin; t < end; ++t) {
+    if (threadIdx.x == 0) *counts = all;
+#pragma unroll 4
+    for (int64_t i = 0; i < runs; ++i) {
+        const int64_t t = begin + 32 * i + lane;
         const int32_t y = label_of(t);
-        const bool live = is_live(t, y);
-        slot[t] = live ? at : -1;
-        if (live) {
-            index[at] = static_cast<int32_t>(t);
-            label[at] = y;
+        const uint32_t live = __ballot_sync(0xFFFFFFFFu, y >= 0);
+        const int32_t to = at + __popc(live & ((1u << lane) - 1));
+        at += __popc(live);
+        if (t >= c.n_tokens) continue;
+        slot[t] = y >= 0 ? to : -1;
+        if (y >= 0) {
+            index[to] = static_cast<int32_t>(t);
+            label[to] = y;
             if (back) {
-                lse[at] = c.lse[t];
-                grad[at] = c.grad_loss[t];
+                lse[to] = c.lse[t];
+                grad[to] = c.grad_loss[t];
             }
-            ++at;
         } else if (!back) {
             c.loss[t] = 0.0f;
             if (c.lse != nullptr) c.lse[t] = 0.0f;
@@ -460,36 +575,52 @@ head_rows_kernel(const HeadCall c, int32_t* counts, int32_t* index, int32_t* slo
     }
 }
 
-// Rows of bf16 to rows on 16-byte boundaries, `pitch` apart; a warp a row.  With an index:
-// the live tokens' rows, and zeros up to whole tiles.
+// Rows of bf16 to rows on 16-byte boundaries, `pitch` apart; a warp takes up to 512 columns
+// of a row.  With an index: the live tokens' rows, and zeros up to whole tiles.  Rows that
+// start elsewhere are read by the aligned words that hold them, shifted into place (of the
+// first and last word bytes beside the row are read, and not used).
 constexpr int kCopyWarps = 8;
+constexpr int kCopyColumns = 512;
 
-template <bool WIDE>
 __global__ void __launch_bounds__(32 * kCopyWarps)
 head_copy_kernel(const uint16_t* from, int64_t stride, const int32_t* index, const int32_t* counts,
-                 int64_t rows, int32_t dim, uint16_t* to, int64_t pitch) {
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kCopyWarps + threadIdx.x / 32;
+                 int64_t rows, int32_t dim, int32_t sections, uint16_t* to, int64_t pitch) {
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * kCopyWarps + threadIdx.x / 32;
+    const int64_t row = id / sections;
     if (row >= rows) return;
     const int lane = threadIdx.x % 32;
+    const int first = static_cast<int>(id - row * sections) * kCopyColumns + 8 * lane;
     const int64_t live = index == nullptr ? rows : *counts;
     uint16_t* out = to + row * pitch;
     if (row >= live) {
         if (row < (live + kPairTile - 1) / kPairTile * kPairTile) {
-            for (int64_t c = 8 * lane; c < pitch; c += 256)
-                *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < kCopyColumns / 256; ++i)
+                if (first + 256 * i < pitch)
+                    *reinterpret_cast<uint4*>(out + first + 256 * i) = make_uint4(0, 0, 0, 0);
         }
         return;
     }
     const uint16_t* in = from + (index == nullptr ? row : index[row]) * stride;
-    if constexpr (WIDE) {
-#pragma unroll 4
-        for (int c = 8 * lane; c + 8 <= dim; c += 256)
-            *reinterpret_cast<uint4*>(out + c) = *reinterpret_cast<const uint4*>(in + c);
-        const int rest = dim / 8 * 8 + lane;
-        if (rest < dim) out[rest] = in[rest];
-    } else {
-#pragma unroll 4
-        for (int c = lane; c < dim; c += 32) out[c] = in[c];
+    const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(in) % 16);
+    const char* words = reinterpret_cast<const char*>(in) - mis;
+    uint4 lo[kCopyColumns / 256], hi[kCopyColumns / 256];
+#pragma unroll
+    for (int i = 0; i < kCopyColumns / 256; ++i) {
+        const int c = first + 256 * i;
+        if (c + 8 <= dim) {
+            lo[i] = *reinterpret_cast<const uint4*>(words + 2 * c);
+            hi[i] = mis != 0 ? *reinterpret_cast<const uint4*>(words + 2 * c + 16) : lo[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kCopyColumns / 256; ++i) {
+        const int c = first + 256 * i;
+        if (c + 8 <= dim) {
+            *reinterpret_cast<uint4*>(out + c) = shifted<uint16_t>(lo[i], hi[i], mis);
+        } else {
+            for (int e = c; e < dim; ++e) out[e] = in[e];
+        }
     }
 }
 
@@ -620,15 +751,23 @@ cudaError_t piece_map(CUtensorMap* map, const HeadCall& c, const HeadPlan& p, in
                : make_map(map, at<uint16_t>(c, p.table), c.dim, rows, p.pitch, box_rows);
 }
 
+cudaError_t copy_rows(const uint16_t* from, int64_t stride, const int32_t* index,
+                      const int32_t* counts, int64_t rows, int64_t dim, uint16_t* to,
+                      int64_t pitch, cudaStream_t stream) {
+    const int64_t sections = (pitch + kCopyColumns - 1) / kCopyColumns;
+    const unsigned grid = static_cast<unsigned>((rows * sections + kCopyWarps - 1) / kCopyWarps);
+    head_copy_kernel<<<grid, 32 * kCopyWarps, 0, stream>>>(
+        from, stride, index, counts, rows, static_cast<int32_t>(dim),
+        static_cast<int32_t>(sections), to, pitch);
+    return cudaGetLastError();
+}
+
 cudaError_t copy_piece(const HeadCall& c, const HeadPlan& p, int64_t first, cudaStream_t stream) {
     if (table_in_place(c)) return cudaSuccess;
     const int64_t rows = piece_rows(c, p, first);
     const uint16_t* from = c.table + first * c.dim;
-    const unsigned grid = static_cast<unsigned>((rows + kCopyWarps - 1) / kCopyWarps);
-    head_copy_kernel<false><<<grid, 32 * kCopyWarps, 0, stream>>>(
-        from, c.dim, nullptr, nullptr, rows, static_cast<int32_t>(c.dim), at<uint16_t>(c, p.table),
-        p.pitch);
-    return cudaGetLastError();
+    return copy_rows(from, c.dim, nullptr, nullptr, rows, c.dim, at<uint16_t>(c, p.table), p.pitch,
+                     stream);
 }
 
 template <int MODE>
@@ -757,12 +896,8 @@ cudaError_t launch_head_rows(const HeadCall& c, const HeadPlan& p, bool back, cu
 }
 
 cudaError_t launch_head_gather(const HeadCall& c, const HeadPlan& p, cudaStream_t stream) {
-    const unsigned grid = static_cast<unsigned>((p.rows + kCopyWarps - 1) / kCopyWarps);
-    const bool wide = aligned_to(c.hidden, 16) && c.hidden_stride % 8 == 0;
-    (wide ? head_copy_kernel<true> : head_copy_kernel<false>)<<<grid, 32 * kCopyWarps, 0, stream>>>(
-        c.hidden, c.hidden_stride, at<int32_t>(c, p.index), at<int32_t>(c, p.counts), p.rows,
-        static_cast<int32_t>(c.dim), at<uint16_t>(c, p.hidden), p.pitch);
-    return cudaGetLastError();
+    return copy_rows(c.hidden, c.hidden_stride, at<int32_t>(c, p.index), at<int32_t>(c, p.counts),
+                     p.rows, c.dim, at<uint16_t>(c, p.hidden), p.pitch, stream);
 }
 
 cudaError_t launch_head_loss(const HeadCall& c, const HeadPlan& p, int64_t first,

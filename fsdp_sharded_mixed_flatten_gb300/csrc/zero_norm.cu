@@ -206,26 +206,6 @@ __device__ __forceinline__ void store_row(T* at, const Pair (&y)[E / 2], const C
 // row's slot to aligned words again, its ends by single elements.  Of the first
 // word the bytes before the row are read, and not used.
 
-// Bytes `by` (0 to 15) and on of the 32 in lo, hi.
-template <class T>
-__device__ __forceinline__ uint4 shifted(uint4 lo, uint4 hi, int by) {
-    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    if (by & 8) {
-#pragma unroll
-        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-    }
-    if (by & 4) {
-#pragma unroll
-        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-    }
-    if (sizeof(T) == 2) {
-        const int bits = 8 * (by & 2);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 __device__ __forceinline__ int off_grid(const void* p) {
     return static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16);
 }

@@ -133,6 +133,26 @@ __device__ __forceinline__ float warp_max(float x) {
     return x;
 }
 
+// Bytes `by` (0 to 15) and on of the 32 in lo, hi.
+template <class T>
+__device__ __forceinline__ uint4 shifted(uint4 lo, uint4 hi, int by) {
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (by & 8) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (by & 4) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    if (sizeof(T) == 2) {
+        const int bits = 8 * (by & 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // 1 / sqrt(x): the approximation and one Newton step.
 __device__ __forceinline__ float inv_sqrt(float x) {
     const float y = rsqrtf(x);
