@@ -57,14 +57,15 @@ struct HeadArgs {
     const float* grad;
     float2* parts;                // [rows][parts_pitch]: maximum (times log2 e) and sum of a tile
     float* picked;                // z[label]
-    uint16_t* dz;                 // [rows][dz_pitch]
+    uint16_t* dz;                 // [blocks of 64 columns][rows][64]
     float* sums;                  // [splits][rows][sums_pitch]
     uint16_t* grad_table;         // the piece's first row
-    int64_t parts_pitch, dz_pitch, sums_pitch, rows;
+    int64_t parts_pitch, sums_pitch, rows;
     int32_t first;                // the piece's first row of the table, and its rows
     int32_t vocab;
     int32_t dim;
     int32_t splits;
+    int32_t blocks;               // of 64 columns of the piece
     int32_t add;                  // to the sums, or to the table's gradient, that are there
     int32_t wide;                 // rows of the table's gradient on 16-byte boundaries
     int32_t group;                // tiles along M that are worked on together
@@ -156,15 +157,6 @@ struct Stage {
             word(lane, j) = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
                                        __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
     }
-    // ... or half of 64 bf16 values
-    __device__ __forceinline__ void put_bf16(const float (&v)[32], int half) const {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            word(lane, 4 * half + j) =
-                make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                           pack_bf16x2(v[8 * j + 4], v[8 * j + 5]),
-                           pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
-    }
 };
 
 // The result of a tile, by warps: each has 32 rows (its lanes') and 128 of the columns, in
@@ -185,20 +177,17 @@ struct Epilogue {
           lane(l) {}
 
     // `row` of the launch's M: this warp's first; n: columns / 256; `slot`: 0 and 1 in turn;
-    // `load(c, v)` gives columns 32 c ... of this warp's half
-    template <class Load>
+    // `each(f)` calls f(c, v) with columns 32 c ... of this warp's half, c = 0 to 3
+    template <class Each>
     __device__ __forceinline__ void operator()(int row0, int n, int split, int slot,
-                                               Load&& load) const {
+                                               Each&& each) const {
         const int column = n * kPairTile + half * kHalf;
         const int row = row0 + lane;
         if constexpr (MODE == kLoss) {
             const int left = a.vocab - column;           // columns that exist
             const int mine = row < live ? a.label[row] - a.first - column : -1;
             float top = -INFINITY, sum = 0.0f, z = 0.0f;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float v[32];
-                load(c, v);
+            each([&](int c, float (&v)[32]) {
                 if (32 * c + 32 > left) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
@@ -226,7 +215,7 @@ struct Epilogue {
                 const float2 s = unpair(t);
                 sum += s.x + s.y;
                 top = m;
-            }
+            });
             if (mine >= 0 && mine < min(kHalf, left)) a.picked[row] = z;
             // the two halves of the columns
             if (half == 1) both[slot][place + lane] = make_float2(top, sum);
@@ -242,40 +231,45 @@ struct Epilogue {
             const int mine = in ? a.label[row] - a.first - column : -1;
             const float off = in ? -a.lse[row] * kLog2e : 0.0f, g = in ? a.grad[row] : 0.0f;
             const Pair by = pair(kLog2e, kLog2e), minus = pair(off, off), scale = pair(g, g);
+            each([&](int c, float (&v)[32]) {
+                // (rows beyond the live ones are zeros in the hidden states' copy: z = 0, g = 0)
+                Pair y[16];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float v[32];
-                load(c, v);
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    const float2 x = unpair(fma2(pair(v[i], v[i + 1]), by, minus));
-                    const float2 y = unpair(mul2(pair(exp2_fast(x.x), exp2_fast(x.y)), scale));
-                    v[i] = in ? y.x : 0.0f;
-                    v[i + 1] = in ? y.y : 0.0f;
+                for (int i = 0; i < 16; ++i) {
+                    const float2 x = unpair(fma2(pair(v[2 * i], v[2 * i + 1]), by, minus));
+                    y[i] = mul2(pair(exp2_fast(x.x), exp2_fast(x.y)), scale);
                 }
                 if (mine >= 32 * c && mine < 32 * c + 32) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (mine == 32 * c + i) v[i] -= g;
+                    for (int i = 0; i < 16; ++i) {
+                        if (mine / 2 == 16 * c + i)
+                            y[i] = add2(y[i], mine % 2 == 0 ? pair(-g, 0.0f) : pair(0.0f, -g));
+                    }
                 }
-                stage.put_bf16(v, c % 2);
-                if (c % 2 == 0) continue;
-                __syncwarp();
-                const int first = column + 32 * (c - 1);          // 64 columns: all there, or none
-                if (first < a.dz_pitch) {
-                    uint16_t* to = a.dz + (row0 + lane / 8) * a.dz_pitch + first + lane % 8 * 8;
+                const int first = column + 32 * c;
+                if (first >= a.blocks * 64) return;
+                if (first + 32 > a.vocab) {              // the sum over the vocabulary reads on
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<uint4*>(to + 4 * i * a.dz_pitch) =
-                            stage.word(lane / 8 + 4 * i, lane % 8);
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 x = unpair(y[i]);
+                        y[i] = pair(first + 2 * i < a.vocab ? x.x : 0.0f,
+                                    first + 2 * i + 1 < a.vocab ? x.y : 0.0f);
+                    }
                 }
-                __syncwarp();
-            }
+                // 64 bytes of a row's 128 a thread; the warp's are 4 KB side by side
+                uint16_t* to = a.dz + (first / 64 * a.rows + row) * 64 + first % 64;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                                     to + 16 * i),
+                                 "r"(narrow2(y[8 * i])), "r"(narrow2(y[8 * i + 1])),
+                                 "r"(narrow2(y[8 * i + 2])), "r"(narrow2(y[8 * i + 3])),
+                                 "r"(narrow2(y[8 * i + 4])), "r"(narrow2(y[8 * i + 5])),
+                                 "r"(narrow2(y[8 * i + 6])), "r"(narrow2(y[8 * i + 7]))
+                                 : "memory");
+            });
         } else if constexpr (MODE == kDh) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float v[32];
-                load(c, v);
+            each([&](int c, float (&v)[32]) {
                 stage.put(v);
                 __syncwarp();
                 const int first = column + 32 * c + lane % 8 * 4;
@@ -303,12 +297,9 @@ struct Epilogue {
                     }
                 }
                 __syncwarp();
-            }
+            });
         } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float v[32];
-                load(c, v);
+            each([&](int c, float (&v)[32]) {
                 stage.put(v);
                 __syncwarp();
                 const int first = column + 32 * c;
@@ -359,7 +350,7 @@ struct Epilogue {
                     }
                 }
                 __syncwarp();
-            }
+            });
         }
     }
 };
@@ -393,6 +384,8 @@ head_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     cluster_sync();
     fence_after_sync();
     const uint32_t tmem = sh.tmem;
+    let_next_launch_begin();
+    wait_for_launch_before();
     const Tiles<MODE> tiles(a);
 
     if (warp == 0) {
@@ -412,9 +405,11 @@ head_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     const uint32_t bar = smem_address(&sh.full[s]);
                     const uint32_t to_a = ring + s * kStageBytes, to_b = to_a + kOperandBytes;
                     if (rank == 0) bar_expect(bar, 2 * kStageBytes);
-                    if constexpr (kAmn) {
-                        tma_load(to_a, &map_a, m0, k * kTileK, bar);
-                        tma_load(to_a + kChunkBytes, &map_a, m0 + 64, k * kTileK, bar);
+                    if constexpr (MODE == kDw) {
+                        tma_load(to_a, &map_a, 0, k * kTileK, m0 / 64, bar);
+                        tma_load(to_a + kChunkBytes, &map_a, 0, k * kTileK, m0 / 64 + 1, bar);
+                    } else if constexpr (MODE == kDh) {
+                        tma_load(to_a, &map_a, 0, m0, k, bar);
                     } else {
                         tma_load(to_a, &map_a, k * kTileK, m0, bar);
                     }
@@ -480,9 +475,12 @@ head_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             const auto t = tiles(i);
             const int row0 = t.m * kPairTile + static_cast<int>(rank) * kHalf + epilogue.place;
             if (t.begin == t.end) {                      // a sum of nothing
-                epilogue(row0, t.n, t.split, 0, [](int, float (&v)[32]) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+                epilogue(row0, t.n, t.split, 0, [](auto&& f) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        float v[32] = {};
+                        f(c, v);
+                    }
                 });
                 continue;
             }
@@ -494,14 +492,23 @@ head_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             fence_after_sync();
             const uint32_t from =
                 tmem + slot * kPairTile + half * kHalf + (static_cast<uint32_t>(epilogue.place) << 16);
-            epilogue(row0, t.n, t.split, slot, [&](int c, float (&v)[32]) {
-                __syncwarp();
-                tmem_load(v, from + 32 * c);
-                tmem_load_wait();
-                if (c == 3) {                            // the tile's place may be taken
-                    fence_before_sync();
+            epilogue(row0, t.n, t.split, slot, [&](auto&& f) {
+                // the next part is on its way while one is worked on
+                float v[2][32];
+                tmem_load(v[0], from);
+                tmem_load_wait(v[0]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c < 3) tmem_load(v[(c + 1) % 2], from + 32 * (c + 1));
+                    f(c, v[c % 2]);
                     __syncwarp();
-                    if (lane == 0) bar_arrive_in_cluster(in_cta(smem_address(&sh.taken[slot]), 0));
+                    if (c < 3) tmem_load_wait(v[(c + 1) % 2]);
+                    if (c == 2) {                        // the tile's place may be taken
+                        fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0)
+                            bar_arrive_in_cluster(in_cta(smem_address(&sh.taken[slot]), 0));
+                    }
                 }
             });
         }
@@ -521,24 +528,54 @@ head_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 
 // ---------------------------------------------------------------- rows ------
 
-// The live tokens, in order, and what the other launches read of them.
+// The places in the workspace that the first launches fill.
+struct HeadRows {
+    int32_t* counts;
+    int32_t* index;               // token of a live row
+    int32_t* slot;                // live row of a token, or -1
+    int32_t* label;
+    float* lse;
+    float* grad;
+    uint16_t* hidden;
+    int64_t pitch;
+};
+
+// A token's label if it is live, else -1.
+__device__ __forceinline__ int32_t live_label(const HeadCall& c, int64_t t, bool back) {
+    const int64_t y = c.label64 ? static_cast<const int64_t*>(c.labels)[t]
+                                : static_cast<const int32_t*>(c.labels)[t];
+    const bool in = (!back || c.grad_loss[t] != 0.0f) & (y >= 0) & (y < c.vocab);
+    return in ? static_cast<int32_t>(y) : -1;
+}
+
+__device__ __forceinline__ void put_token(const HeadCall& c, const HeadRows& r, int64_t t,
+                                          int32_t y, int32_t to, bool back) {
+    r.slot[t] = y >= 0 ? to : -1;
+    if (y >= 0) {
+        r.index[to] = static_cast<int32_t>(t);
+        r.label[to] = y;
+        if (back) {
+            r.lse[to] = c.lse[t];
+            r.grad[to] = c.grad_loss[t];
+        }
+    } else if (!back) {
+        c.loss[t] = 0.0f;
+        if (c.lse != nullptr) c.lse[t] = 0.0f;
+    }
+}
+
+// The live tokens, in order, and what the other launches read of them: by one CTA.
 constexpr int kRowThreads = 1024;
 
 __global__ void __launch_bounds__(kRowThreads)
-head_rows_kernel(const HeadCall c, int32_t* counts, int32_t* index, int32_t* slot, int32_t* label,
-                 float* lse, float* grad, bool back) {
+head_rows_kernel(const HeadCall c, const HeadRows r, bool back) {
     __shared__ int32_t warps[32];
     // a warp's tokens: whole runs of 32
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int64_t runs = (c.n_tokens + kRowThreads - 1) / kRowThreads;
     const int64_t begin = warp * runs * 32;
-    auto label_of = [&](int64_t t) {
-        if (t >= c.n_tokens) return -1;
-        const int64_t y = c.label64 ? static_cast<const int64_t*>(c.labels)[t]
-                                    : static_cast<const int32_t*>(c.labels)[t];
-        const bool in = y >= 0 && y < c.vocab && (!back || c.grad_loss[t] != 0.0f);
-        return in ? static_cast<int32_t>(y) : -1;
-    };
+    auto label_of = [&](int64_t t) { return t < c.n_tokens ? live_label(c, t, back) : -1; };
+    let_next_launch_begin();
     int32_t n = 0;
 #pragma unroll 8
     for (int64_t i = 0; i < runs; ++i)
@@ -551,7 +588,7 @@ head_rows_kernel(const HeadCall c, int32_t* counts, int32_t* index, int32_t* slo
         at += __shfl_xor_sync(0xFFFFFFFFu, at, o);
         all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
     }
-    if (threadIdx.x == 0) *counts = all;
+    if (threadIdx.x == 0) *r.counts = all;
 #pragma unroll 4
     for (int64_t i = 0; i < runs; ++i) {
         const int64_t t = begin + 32 * i + lane;
@@ -559,26 +596,84 @@ head_rows_kernel(const HeadCall c, int32_t* counts, int32_t* index, int32_t* slo
         const uint32_t live = __ballot_sync(0xFFFFFFFFu, y >= 0);
         const int32_t to = at + __popc(live & ((1u << lane) - 1));
         at += __popc(live);
-        if (t >= c.n_tokens) continue;
-        slot[t] = y >= 0 ? to : -1;
-        if (y >= 0) {
-            index[to] = static_cast<int32_t>(t);
-            label[to] = y;
-            if (back) {
-                lse[to] = c.lse[t];
-                grad[to] = c.grad_loss[t];
-            }
-        } else if (!back) {
-            c.loss[t] = 0.0f;
-            if (c.lse != nullptr) c.lse[t] = 0.0f;
-        }
+        if (t < c.n_tokens) put_token(c, r, t, y, to, back);
+    }
+}
+
+// 16 bytes of a row that starts anywhere, from the aligned words that hold them (of the
+// row's first and last word bytes beside it are read, and not used).  All 16 are the row's.
+__device__ __forceinline__ uint4 row_word(const uint16_t* row, int column) {
+    const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(row) % 16);
+    const char* p = reinterpret_cast<const char*>(row) - mis + 2 * column;
+    const uint4 lo = *reinterpret_cast<const uint4*>(p);
+    if (mis == 0) return lo;
+    return shifted<uint16_t>(lo, *reinterpret_cast<const uint4*>(p + 16), mis);
+}
+
+// The same and the copy of the live tokens' rows in one launch, where tokens are few: a CTA
+// has 8 of them, a warp each, and counts all by itself.
+constexpr int64_t kFewTokens = 8192;
+constexpr int kPrepareThreads = 256;
+constexpr int kPrepareTokens = kPrepareThreads / 32;
+
+__global__ void __launch_bounds__(kPrepareThreads)
+head_prepare_kernel(const HeadCall c, const HeadRows r, bool back) {
+    __shared__ int32_t before[kPrepareTokens], total[kPrepareTokens];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int n = static_cast<int>(c.n_tokens), base = blockIdx.x * kPrepareTokens;
+    let_next_launch_begin();
+    // the CTA's own tokens, for every warp
+    const int32_t mine = lane < kPrepareTokens && base + lane < n ? live_label(c, base + lane, back) : -1;
+    const uint32_t own = __ballot_sync(0xFFFFFFFFu, mine >= 0);
+    int32_t b = 0, all = 0;
+#pragma unroll 8
+    for (int t = threadIdx.x; t < n; t += kPrepareThreads) {
+        const int live = live_label(c, t, back) >= 0;
+        all += live;
+        b += t < base ? live : 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+        all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+    }
+    if (lane == 0) {
+        before[warp] = b;
+        total[warp] = all;
+    }
+    __syncthreads();
+    b = all = 0;
+#pragma unroll
+    for (int w = 0; w < kPrepareTokens; ++w) {
+        b += before[w];
+        all += total[w];
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *r.counts = all;
+    const int32_t y = __shfl_sync(0xFFFFFFFFu, mine, warp);
+    const int32_t j = b + __popc(own & ((1u << warp) - 1));
+    const int t = base + warp;
+    if (lane == 0 && t < n) put_token(c, r, t, y, j, back);
+    const int dim = static_cast<int>(c.dim);
+    if (y >= 0) {
+        const uint16_t* in = c.hidden + t * c.hidden_stride;
+        uint16_t* out = r.hidden + j * r.pitch;
+#pragma unroll 4
+        for (int col = 8 * lane; col + 8 <= dim; col += 256)
+            *reinterpret_cast<uint4*>(out + col) = row_word(in, col);
+        const int rest = dim / 8 * 8 + lane;
+        if (rest < dim) out[rest] = in[rest];
+    }
+    if (!back) return;
+    // zeros up to whole tiles: the sums over tokens go that far
+    const int rows = (all + kPairTile - 1) / kPairTile * kPairTile;
+    for (int z = all + t; z < rows; z += gridDim.x * kPrepareTokens) {
+        for (int col = 8 * lane; col < r.pitch; col += 256)
+            *reinterpret_cast<uint4*>(r.hidden + z * r.pitch + col) = make_uint4(0, 0, 0, 0);
     }
 }
 
 // Rows of bf16 to rows on 16-byte boundaries, `pitch` apart; a warp takes up to 512 columns
-// of a row.  With an index: the live tokens' rows, and zeros up to whole tiles.  Rows that
-// start elsewhere are read by the aligned words that hold them, shifted into place (of the
-// first and last word bytes beside the row are read, and not used).
+// of a row.  With an index: the live tokens' rows, and zeros up to whole tiles.
 constexpr int kCopyWarps = 8;
 constexpr int kCopyColumns = 512;
 
@@ -590,6 +685,8 @@ head_copy_kernel(const uint16_t* from, int64_t stride, const int32_t* index, con
     if (row >= rows) return;
     const int lane = threadIdx.x % 32;
     const int first = static_cast<int>(id - row * sections) * kCopyColumns + 8 * lane;
+    let_next_launch_begin();
+    wait_for_launch_before();
     const int64_t live = index == nullptr ? rows : *counts;
     uint16_t* out = to + row * pitch;
     if (row >= live) {
@@ -602,22 +699,16 @@ head_copy_kernel(const uint16_t* from, int64_t stride, const int32_t* index, con
         return;
     }
     const uint16_t* in = from + (index == nullptr ? row : index[row]) * stride;
-    const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(in) % 16);
-    const char* words = reinterpret_cast<const char*>(in) - mis;
-    uint4 lo[kCopyColumns / 256], hi[kCopyColumns / 256];
+    uint4 v[kCopyColumns / 256];
 #pragma unroll
     for (int i = 0; i < kCopyColumns / 256; ++i) {
-        const int c = first + 256 * i;
-        if (c + 8 <= dim) {
-            lo[i] = *reinterpret_cast<const uint4*>(words + 2 * c);
-            hi[i] = mis != 0 ? *reinterpret_cast<const uint4*>(words + 2 * c + 16) : lo[i];
-        }
+        if (first + 256 * i + 8 <= dim) v[i] = row_word(in, first + 256 * i);
     }
 #pragma unroll
     for (int i = 0; i < kCopyColumns / 256; ++i) {
         const int c = first + 256 * i;
         if (c + 8 <= dim) {
-            *reinterpret_cast<uint4*>(out + c) = shifted<uint16_t>(lo[i], hi[i], mis);
+            *reinterpret_cast<uint4*>(out + c) = v[i];
         } else {
             for (int e = c; e < dim; ++e) out[e] = in[e];
         }
@@ -630,9 +721,11 @@ head_join_kernel(const int32_t* counts, const int32_t* index, const float2* part
                  int32_t n_parts, const float* picked, float* loss, float* lse) {
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
+    wait_for_launch_before();
     if (row >= *counts) return;
     const float2* p = parts + row * pitch;
     float top = -INFINITY, sum = 0.0f;
+#pragma unroll 4
     for (int i = lane; i < n_parts; i += 32) {
         const float2 v = p[i];
         const float m = fmaxf(top, v.x), from = m == -INFINITY ? 0.0f : m;
@@ -661,29 +754,46 @@ head_join_kernel(const int32_t* counts, const int32_t* index, const float2* part
     }
 }
 
-// The hidden states' gradient: the splits' sums of live tokens, zeros of the others.
+// The hidden states' gradient: the splits' sums of live tokens, zeros of the others; a warp
+// takes up to 512 columns of a row.
 template <bool WIDE>
 __global__ void __launch_bounds__(256)
 head_finish_kernel(const int32_t* slot, const float* sums, int64_t rows, int64_t pitch,
-                   int32_t splits, int64_t n_tokens, int32_t dim, uint16_t* out, int64_t stride) {
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
+                   int32_t splits, int64_t n_tokens, int32_t dim, int32_t sections, uint16_t* out,
+                   int64_t stride) {
+    constexpr int N = kCopyColumns / 128;
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
+    const int64_t t = id / sections;
     if (t >= n_tokens) return;
-    const int lane = threadIdx.x % 32;
+    const int first = static_cast<int>(id - t * sections) * kCopyColumns + 4 * (threadIdx.x % 32);
+    wait_for_launch_before();
     const int32_t j = slot[t];
     uint16_t* to = out + t * stride;
-    const float* from = sums + static_cast<int64_t>(j < 0 ? 0 : j) * pitch;
-    for (int c = 4 * lane; c < dim; c += 128) {
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (j >= 0) {
-            for (int s = 0; s < splits; ++s) {
-                const float4 w = *reinterpret_cast<const float4*>(from + s * rows * pitch + c);
-                v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+    float4 v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (j >= 0) {
+        const float* from = sums + j * pitch + first;
+#pragma unroll 4
+        for (int s = 0; s < splits; ++s) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (first + 128 * i < dim) {
+                    const float4 w =
+                        *reinterpret_cast<const float4*>(from + s * rows * pitch + 128 * i);
+                    v[i] = make_float4(v[i].x + w.x, v[i].y + w.y, v[i].z + w.z, v[i].w + w.w);
+                }
             }
         }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int c = first + 128 * i;
         if (WIDE && c + 4 <= dim) {
-            *reinterpret_cast<uint2*>(to + c) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+            *reinterpret_cast<uint2*>(to + c) =
+                make_uint2(pack_bf16x2(v[i].x, v[i].y), pack_bf16x2(v[i].z, v[i].w));
         } else {
-            const float f[4] = {v.x, v.y, v.z, v.w};
+            const float f[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (c + e < dim) to[c + e] = float_to_bf16_rn(f[e]);
@@ -731,6 +841,24 @@ cudaError_t make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// A launch that may be set up while the one before it in the stream ends; the kernel waits
+// for that one's results itself.
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), unsigned grid, int threads, size_t smem,
+                         cudaStream_t stream, A&&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 template <class T>
 T* at(const HeadCall& c, int64_t offset) {
     return reinterpret_cast<T*>(static_cast<char*>(c.workspace) + offset);
@@ -756,10 +884,8 @@ cudaError_t copy_rows(const uint16_t* from, int64_t stride, const int32_t* index
                       int64_t pitch, cudaStream_t stream) {
     const int64_t sections = (pitch + kCopyColumns - 1) / kCopyColumns;
     const unsigned grid = static_cast<unsigned>((rows * sections + kCopyWarps - 1) / kCopyWarps);
-    head_copy_kernel<<<grid, 32 * kCopyWarps, 0, stream>>>(
-        from, stride, index, counts, rows, static_cast<int32_t>(dim),
-        static_cast<int32_t>(sections), to, pitch);
-    return cudaGetLastError();
+    return launch_after(head_copy_kernel, grid, 32 * kCopyWarps, 0, stream, from, stride, index,
+                        counts, rows, dim, sections, to, pitch);
 }
 
 cudaError_t copy_piece(const HeadCall& c, const HeadPlan& p, int64_t first, cudaStream_t stream) {
@@ -768,6 +894,21 @@ cudaError_t copy_piece(const HeadCall& c, const HeadPlan& p, int64_t first, cuda
     const uint16_t* from = c.table + first * c.dim;
     return copy_rows(from, c.dim, nullptr, nullptr, rows, c.dim, at<uint16_t>(c, p.table), p.pitch,
                      stream);
+}
+
+// The piece's gradient of the logits, in boxes of 64 columns by `box_rows`.
+cudaError_t dz_map(CUtensorMap* map, const HeadArgs& a, int box_rows) {
+    Encode encode = nullptr;
+    if (cudaError_t e = find_encode(&encode); e != cudaSuccess) return e;
+    const cuuint64_t sizes[3] = {64, static_cast<cuuint64_t>(a.rows),
+                                 static_cast<cuuint64_t>(a.blocks)};
+    const cuuint64_t strides[2] = {128, static_cast<cuuint64_t>(a.rows) * 128};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1}, ones[3] = {1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.dz, sizes, strides, box,
+                              ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 template <int MODE>
@@ -799,9 +940,8 @@ cudaError_t launch_product(const CUtensorMap& map_a, const CUtensorMap& map_b, c
     });
     if (set[dev] != cudaSuccess) return set[dev];
     const int64_t pairs = tiles < fit[dev] ? tiles : fit[dev];
-    head_kernel<MODE><<<static_cast<unsigned>(2 * pairs), kHeadThreads, kHeadSmem, stream>>>(
-        map_a, map_b, a);
-    return cudaGetLastError();
+    return launch_after(head_kernel<MODE>, static_cast<unsigned>(2 * pairs), kHeadThreads, kHeadSmem,
+                        stream, map_a, map_b, a);
 }
 
 HeadArgs product_args(const HeadCall& c, const HeadPlan& p, int64_t first) {
@@ -816,13 +956,13 @@ HeadArgs product_args(const HeadCall& c, const HeadPlan& p, int64_t first) {
     a.sums = at<float>(c, p.sums);
     a.grad_table = c.grad_table == nullptr ? nullptr : c.grad_table + first * c.dim;
     a.parts_pitch = (c.vocab + kPairTile - 1) / kPairTile;
-    a.dz_pitch = p.piece_pitch;
     a.sums_pitch = p.pitch;
     a.rows = p.rows;
     a.first = static_cast<int32_t>(first);
     a.vocab = static_cast<int32_t>(piece_rows(c, p, first));
     a.dim = static_cast<int32_t>(c.dim);
     a.splits = p.splits;
+    a.blocks = (a.vocab + 63) / 64;
     a.group = 8;
     return a;
 }
@@ -833,9 +973,9 @@ int64_t tiles_of(int64_t x) { return (x + kPairTile - 1) / kPairTile; }
 }  // namespace
 
 // Pieces of the vocabulary whose gradient, and whose copy of the table where it is off the
-// 16-byte grid, take at most 256 MB each; as even as whole tiles allow.
+// 16-byte grid, take at most 512 MB each; as even as whole tiles allow.
 HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back) {
-    constexpr int64_t kMost = int64_t{256} << 20;
+    constexpr int64_t kMost = int64_t{512} << 20;
     HeadPlan p{};
     p.rows = whole(n_tokens < 1 ? 1 : n_tokens, kPairTile);
     p.pitch = whole(dim, 8);
@@ -844,10 +984,11 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back) {
     if (most < kPairTile) most = kPairTile;
     const int64_t pieces = (vocab + most - 1) / most;
     p.piece = whole((vocab + pieces - 1) / pieces, kPairTile);
-    p.piece_pitch = whole(p.piece < vocab ? p.piece : vocab, 64);
     p.splits = 1;
     if (back) {
-        // the sum over a piece in as many parts as keep the GPU's pairs busy
+        // the sum over a piece in as many parts as keep the GPU's pairs busy, in units of
+        // a step's 0.3 us; every part is written and read again, at 6 TB/s
+        const double way = 8.0 * p.rows * p.pitch / 6e12 / 0.3e-6;
         const int64_t tiles = p.rows / kPairTile * tiles_of(dim), steps = whole(p.piece, 64) / 64;
         const int64_t pairs = device_sms() / 2 > 0 ? device_sms() / 2 : 1;
         double best = 0.0;
@@ -855,7 +996,7 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back) {
             // rounds of tiles, each a share of the sum and the way out of it
             const double cost =
                 static_cast<double>((tiles * s + pairs - 1) / pairs) * (steps / (double)s + 8.0) +
-                0.25 * s;
+                way * s;
             if (s == 1 || cost < best) {
                 best = cost;
                 p.splits = static_cast<int32_t>(s);
@@ -878,7 +1019,7 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back) {
     if (back) {
         p.lse = place(4 * n);
         p.grad = place(4 * n);
-        p.dz = place(2 * p.rows * p.piece_pitch);
+        p.dz = place(2 * p.rows * whole(p.piece < vocab ? p.piece : vocab, 64));
         p.sums = place(4 * p.splits * p.rows * p.pitch);
     } else {
         p.parts = place(8 * n * tiles_of(vocab));
@@ -889,13 +1030,21 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back) {
 }
 
 cudaError_t launch_head_rows(const HeadCall& c, const HeadPlan& p, bool back, cudaStream_t stream) {
-    head_rows_kernel<<<1, kRowThreads, 0, stream>>>(
-        c, at<int32_t>(c, p.counts), at<int32_t>(c, p.index), at<int32_t>(c, p.slot),
-        at<int32_t>(c, p.label), at<float>(c, p.lse), at<float>(c, p.grad), back);
+    const HeadRows r{at<int32_t>(c, p.counts), at<int32_t>(c, p.index),  at<int32_t>(c, p.slot),
+                     at<int32_t>(c, p.label),  at<float>(c, p.lse),      at<float>(c, p.grad),
+                     at<uint16_t>(c, p.hidden), p.pitch};
+    if (c.n_tokens > 0 && c.n_tokens <= kFewTokens) {
+        const unsigned grid =
+            static_cast<unsigned>((c.n_tokens + kPrepareTokens - 1) / kPrepareTokens);
+        head_prepare_kernel<<<grid, kPrepareThreads, 0, stream>>>(c, r, back);
+        return cudaGetLastError();
+    }
+    head_rows_kernel<<<1, kRowThreads, 0, stream>>>(c, r, back);
     return cudaGetLastError();
 }
 
 cudaError_t launch_head_gather(const HeadCall& c, const HeadPlan& p, cudaStream_t stream) {
+    if (c.n_tokens <= kFewTokens) return cudaSuccess;     // done with the rows
     return copy_rows(c.hidden, c.hidden_stride, at<int32_t>(c, p.index), at<int32_t>(c, p.counts),
                      p.rows, c.dim, at<uint16_t>(c, p.hidden), p.pitch, stream);
 }
@@ -915,10 +1064,9 @@ cudaError_t launch_head_loss(const HeadCall& c, const HeadPlan& p, int64_t first
 cudaError_t launch_head_join(const HeadCall& c, const HeadPlan& p, cudaStream_t stream) {
     const unsigned grid = static_cast<unsigned>((c.n_tokens + 7) / 8);
     const int64_t parts = tiles_of(c.vocab);
-    head_join_kernel<<<grid, 256, 0, stream>>>(
-        at<int32_t>(c, p.counts), at<int32_t>(c, p.index), at<float2>(c, p.parts), parts,
-        static_cast<int32_t>(parts), at<float>(c, p.picked), c.loss, c.lse);
-    return cudaGetLastError();
+    return launch_after(head_join_kernel, grid, 256, 0, stream, at<int32_t>(c, p.counts),
+                        at<int32_t>(c, p.index), at<float2>(c, p.parts), parts, parts,
+                        at<float>(c, p.picked), c.loss, c.lse);
 }
 
 cudaError_t launch_head_dz(const HeadCall& c, const HeadPlan& p, int64_t first,
@@ -938,9 +1086,7 @@ cudaError_t launch_head_dh(const HeadCall& c, const HeadPlan& p, int64_t first,
     HeadArgs a = product_args(c, p, first);
     a.add = first > 0;
     CUtensorMap ma, mb;
-    // (columns of dz beyond the piece are not read: zeros in their place)
-    if (cudaError_t e = make_map(&ma, a.dz, a.vocab, p.rows, p.piece_pitch, kHalf); e != cudaSuccess)
-        return e;
+    if (cudaError_t e = dz_map(&ma, a, kHalf); e != cudaSuccess) return e;
     if (cudaError_t e = piece_map(&mb, c, p, first, kTileK); e != cudaSuccess) return e;
     return launch_product<kDh>(ma, mb, a, p.rows / kPairTile * tiles_of(c.dim) * p.splits, stream);
 }
@@ -951,9 +1097,7 @@ cudaError_t launch_head_dw(const HeadCall& c, const HeadPlan& p, int64_t first,
     a.add = c.accumulate;
     a.wide = aligned_to(c.grad_table, 16) && c.dim % 8 == 0;
     CUtensorMap ma, mb;
-    if (cudaError_t e = make_map(&ma, a.dz, a.vocab, p.rows, p.piece_pitch, kTileK);
-        e != cudaSuccess)
-        return e;
+    if (cudaError_t e = dz_map(&ma, a, kTileK); e != cudaSuccess) return e;
     if (cudaError_t e = make_map(&mb, at<uint16_t>(c, p.hidden), c.dim, p.rows, p.pitch, kTileK);
         e != cudaSuccess)
         return e;
@@ -961,12 +1105,12 @@ cudaError_t launch_head_dw(const HeadCall& c, const HeadPlan& p, int64_t first,
 }
 
 cudaError_t launch_head_finish(const HeadCall& c, const HeadPlan& p, cudaStream_t stream) {
-    const unsigned grid = static_cast<unsigned>((c.n_tokens + 7) / 8);
+    const int64_t sections = (c.dim + kCopyColumns - 1) / kCopyColumns;
+    const unsigned grid = static_cast<unsigned>((c.n_tokens * sections + 7) / 8);
     const bool wide = aligned_to(c.grad_hidden, 8) && c.grad_hidden_stride % 4 == 0;
-    (wide ? head_finish_kernel<true> : head_finish_kernel<false>)<<<grid, 256, 0, stream>>>(
-        at<int32_t>(c, p.slot), at<float>(c, p.sums), p.rows, p.pitch, p.splits, c.n_tokens,
-        static_cast<int32_t>(c.dim), c.grad_hidden, c.grad_hidden_stride);
-    return cudaGetLastError();
+    return launch_after(wide ? head_finish_kernel<true> : head_finish_kernel<false>, grid, 256, 0,
+                        stream, at<int32_t>(c, p.slot), at<float>(c, p.sums), p.rows, p.pitch,
+                        p.splits, c.n_tokens, c.dim, sections, c.grad_hidden, c.grad_hidden_stride);
 }
 
 cudaError_t read_head_status(int* status, int clear, cudaStream_t stream) {

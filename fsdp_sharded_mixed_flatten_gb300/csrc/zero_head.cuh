@@ -34,7 +34,6 @@ struct HeadPlan {
     int64_t rows;                 // n_tokens rounded up to whole tiles
     int64_t pitch;                // elements of a row of the hidden states' copy
     int64_t piece;                // rows of the table worked on at a time
-    int64_t piece_pitch;          // elements of a row of the piece's gradient
     int32_t splits;               // of the sum over the vocabulary in the hidden gradient
     int64_t counts, index, slot, label, lse, grad, hidden, table, parts, picked, dz, sums;
     int64_t bytes;

@@ -65,7 +65,7 @@ def test_workspaces(lib):
         assert some >= 2 * n * d + 8 * n * ((v + 255) // 256)
         assert zf.zero_head_loss_grad_workspace_bytes(n, v, d) >= 2 * n * d + 4 * n * d
     # the logits' gradient is held in pieces: 2 GB in one
-    assert zf.zero_head_loss_grad_workspace_bytes(8192, 131072, 4096) < 1 << 30
+    assert zf.zero_head_loss_grad_workspace_bytes(8192, 131072, 4096) < 3 << 29
     out = ctypes.c_int64(0)
     for f in (lib.zero_head_loss_workspace_bytes, lib.zero_head_loss_grad_workspace_bytes):
         assert f(1, 8, 8, None) == INVALID
