@@ -51,16 +51,19 @@ constexpr float kLog2e = 1.4426950408889634f;
 enum Mode { kLoss, kDz, kDh, kDw };
 
 struct HeadArgs {
-    const int32_t* counts;        // live tokens
-    const int32_t* label;         // of the live tokens, as the rest
+    const int32_t* counts;        // live tokens; null: tokens are rows as they are, n_rows of them
+    const int32_t* label;         // of the live tokens, as the rest; or null, and
+    const void* labels;           // of all, int32 or int64
     const float* lse;
     const float* grad;
     float2* parts;                // [rows][parts_pitch]: maximum (times log2 e) and sum of a tile
     float* picked;                // z[label]
+    // Row by row 128 bytes, whose 16-byte words are in the order that 128-byte swizzling
+    // gives them in shared memory: word j of row r is at j ^ (r % 8).
     uint16_t* dz;                 // [blocks of 64 columns][rows][64]
-    float* sums;                  // [splits][rows][sums_pitch]
+    float* sums;                  // [splits][blocks of 32 columns][rows][32]
     uint16_t* grad_table;         // the piece's first row
-    int64_t parts_pitch, sums_pitch, rows;
+    int64_t parts_pitch, rows;
     int32_t first;                // the piece's first row of the table, and its rows
     int32_t vocab;
     int32_t dim;
@@ -68,6 +71,8 @@ struct HeadArgs {
     int32_t blocks;               // of 64 columns of the piece
     int32_t add;                  // to the sums, or to the table's gradient, that are there
     int32_t wide;                 // rows of the table's gradient on 16-byte boundaries
+    int32_t n_rows;
+    int32_t label64;
     int32_t group;                // tiles along M that are worked on together
 };
 
@@ -96,12 +101,23 @@ __device__ __forceinline__ bool wait(Shared& sh, uint64_t& bar, uint32_t parity)
     return bar_try(b, parity) || wait_long(sh, b, parity);
 }
 
+__device__ __forceinline__ int live_rows(const HeadArgs& a) {
+    return a.counts != nullptr ? *a.counts : a.n_rows;
+}
+// A row's label in the piece, or another number.
+__device__ __forceinline__ int label_in_piece(const HeadArgs& a, int row) {
+    if (a.label != nullptr) return a.label[row] - a.first;
+    const int64_t y = a.label64 ? static_cast<const int64_t*>(a.labels)[row]
+                                : static_cast<const int32_t*>(a.labels)[row];
+    return y >= a.first && y < a.first + a.vocab ? static_cast<int>(y - a.first) : -1;
+}
+
 // The tiles of a launch, in the order in which the pairs take them.
 template <int MODE>
 struct Tiles {
     int m_tiles, n_tiles, steps, splits, group, total;
     __device__ explicit Tiles(const HeadArgs& a) {
-        const int live = *a.counts;
+        const int live = live_rows(a);
         const int m = MODE == kDw ? a.vocab : live;
         const int n = MODE == kLoss || MODE == kDz ? a.vocab : a.dim;
         const int k = MODE == kDh ? a.vocab : MODE == kDw ? live : a.dim;
@@ -140,7 +156,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 // A warp's piece of a tile on its way to memory: 32 rows of 128 bytes in shared memory, the
 // 16-byte words of row r in the order j ^ (r % 8), so that lanes may write a row each and
-// read rows side by side without meeting in a bank.
+// read rows side by side without meeting in a bank.  (The tensor cores and the copies of
+// operands keep shared memory busy, and what a result costs there it costs the products: a
+// piece goes to memory by one bulk copy where memory is laid out like it.)
 struct Stage {
     char* at;                     // 4 KB of this warp's
     int lane;
@@ -149,6 +167,29 @@ struct Stage {
     }
     __device__ __forceinline__ float& value(int r, int c) const {       // of 32 fp32 values
         return *reinterpret_cast<float*>(at + 128 * r + 16 * ((c / 4) ^ (r & 7)) + 4 * (c % 4));
+    }
+    __device__ __forceinline__ uint16_t& value16(int r, int c) const {  // of 64 bf16 values
+        return *reinterpret_cast<uint16_t*>(at + 128 * r + 16 * ((c / 8) ^ (r & 7)) + 2 * (c % 8));
+    }
+    // half of this lane's row: 32 of 64 bf16 values
+    __device__ __forceinline__ void put_half(const Pair (&v)[16], int half) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            word(lane, 4 * half + j) = make_uint4(narrow2(v[4 * j]), narrow2(v[4 * j + 1]),
+                                                  narrow2(v[4 * j + 2]), narrow2(v[4 * j + 3]));
+    }
+    // All of the warp's rows are there: on their way, and the place to be written again.
+    __device__ __forceinline__ void send(void* to, bool add) const {
+        share_writes();
+        __syncwarp();
+        if (lane == 0) {
+            if (add) bulk_add(static_cast<float*>(to), smem_address(at), 4096);
+            else bulk_store(to, smem_address(at), 4096);
+        }
+    }
+    __device__ __forceinline__ void sent() const {
+        if (lane == 0) bulk_wait_read();
+        __syncwarp();
     }
     // this lane's row: 32 fp32 values
     __device__ __forceinline__ void put(const float (&v)[32]) const {
@@ -171,7 +212,7 @@ struct Epilogue {
         : a(args),
           stage{staging, l},
           both(found),
-          live(*args.counts),
+          live(live_rows(args)),
           place(warp % 4 * 32),
           half((warp - 2) / 4),
           lane(l) {}
@@ -185,7 +226,7 @@ struct Epilogue {
         const int row = row0 + lane;
         if constexpr (MODE == kLoss) {
             const int left = a.vocab - column;           // columns that exist
-            const int mine = row < live ? a.label[row] - a.first - column : -1;
+            const int mine = row < live ? label_in_piece(a, row) - column : -1;
             float top = -INFINITY, sum = 0.0f, z = 0.0f;
             each([&](int c, float (&v)[32]) {
                 if (32 * c + 32 > left) {
@@ -256,44 +297,51 @@ struct Epilogue {
                                     first + 2 * i + 1 < a.vocab ? x.y : 0.0f);
                     }
                 }
-                // 64 bytes of a row's 128 a thread; the warp's are 4 KB side by side
-                uint16_t* to = a.dz + (first / 64 * a.rows + row) * 64 + first % 64;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                                     to + 16 * i),
-                                 "r"(narrow2(y[8 * i])), "r"(narrow2(y[8 * i + 1])),
-                                 "r"(narrow2(y[8 * i + 2])), "r"(narrow2(y[8 * i + 3])),
-                                 "r"(narrow2(y[8 * i + 4])), "r"(narrow2(y[8 * i + 5])),
-                                 "r"(narrow2(y[8 * i + 6])), "r"(narrow2(y[8 * i + 7]))
-                                 : "memory");
+                if (c % 2 == 0) stage.sent();
+                stage.put_half(y, c % 2);
+                if (c % 2 == 1)
+                    stage.send(a.dz + (first / 64 * a.rows + row0) * 64, false);
             });
         } else if constexpr (MODE == kDh) {
+            const int blocks = (a.dim + 31) / 32;
             each([&](int c, float (&v)[32]) {
+                const int block = column / 32 + c;
+                if (block >= blocks) return;
+                stage.sent();
                 stage.put(v);
+                stage.send(a.sums + ((static_cast<int64_t>(split) * blocks + block) * a.rows + row0) * 32,
+                           a.add != 0);
+            });
+        } else if (a.add == 0) {
+            each([&](int c, float (&v)[32]) {
+                Pair y[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[i] = pair(v[2 * i], v[2 * i + 1]);
+                stage.put_half(y, c % 2);
+                if (c % 2 == 0) return;
                 __syncwarp();
-                const int first = column + 32 * c + lane % 8 * 4;
-                if (first < a.sums_pitch) {
-                    float* to = a.sums + (split * a.rows + row0 + lane / 8) * a.sums_pitch + first;
-                    float4 old[8];
-                    if (a.add) {
+                const int first = column + 32 * (c - 1);              // 64 columns
+                if (a.wide) {
+                    const int col = first + lane % 8 * 8;
+                    if (col < a.dim) {
+                        uint16_t* to =
+                            a.grad_table + static_cast<int64_t>(row0 + lane / 8) * a.dim + col;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            old[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            if (row0 + lane / 8 + 4 * i < live)
-                                old[i] = *reinterpret_cast<const float4*>(to + 4 * i * a.sums_pitch);
+                            const int r = lane / 8 + 4 * i;
+                            if (row0 + r < a.vocab)
+                                *reinterpret_cast<uint4*>(to + static_cast<int64_t>(4 * i) * a.dim) =
+                                    stage.word(r, lane % 8);
                         }
                     }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint4 w = stage.word(lane / 8 + 4 * i, lane % 8);
-                        float4 x = make_float4(__uint_as_float(w.x), __uint_as_float(w.y),
-                                               __uint_as_float(w.z), __uint_as_float(w.w));
-                        if (a.add)
-                            x = make_float4(old[i].x + x.x, old[i].y + x.y, old[i].z + x.z,
-                                            old[i].w + x.w);
-                        if (row0 + lane / 8 + 4 * i < live)
-                            *reinterpret_cast<float4*>(to + 4 * i * a.sums_pitch) = x;
+                } else {
+                    uint16_t* to = a.grad_table + static_cast<int64_t>(row0) * a.dim + first + lane;
+                    const int rows = min(32, a.vocab - row0);
+                    const bool one = first + lane < a.dim, two = first + 32 + lane < a.dim;
+#pragma unroll 8
+                    for (int r = 0; r < rows; ++r) {
+                        if (one) to[static_cast<int64_t>(r) * a.dim] = stage.value16(r, lane);
+                        if (two) to[static_cast<int64_t>(r) * a.dim + 32] = stage.value16(r, 32 + lane);
                     }
                 }
                 __syncwarp();
@@ -313,7 +361,7 @@ struct Epilogue {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             old[i] = make_uint4(0, 0, 0, 0);
-                            if (a.add && row0 + lane / 4 + 8 * i < a.vocab)
+                            if (row0 + lane / 4 + 8 * i < a.vocab)
                                 old[i] = *reinterpret_cast<const uint4*>(to + i * step);
                         }
 #pragma unroll
@@ -325,12 +373,10 @@ struct Epilogue {
                                          pair(__uint_as_float(lo.z), __uint_as_float(lo.w)),
                                          pair(__uint_as_float(hi.x), __uint_as_float(hi.y)),
                                          pair(__uint_as_float(hi.z), __uint_as_float(hi.w))};
-                            if (a.add) {
-                                x[0] = add2(x[0], widen2(old[i].x));
-                                x[1] = add2(x[1], widen2(old[i].y));
-                                x[2] = add2(x[2], widen2(old[i].z));
-                                x[3] = add2(x[3], widen2(old[i].w));
-                            }
+                            x[0] = add2(x[0], widen2(old[i].x));
+                            x[1] = add2(x[1], widen2(old[i].y));
+                            x[2] = add2(x[2], widen2(old[i].z));
+                            x[3] = add2(x[3], widen2(old[i].w));
                             if (row0 + r < a.vocab)
                                 *reinterpret_cast<uint4*>(to + i * step) = make_uint4(
                                     narrow2(x[0]), narrow2(x[1]), narrow2(x[2]), narrow2(x[3]));
@@ -343,9 +389,8 @@ struct Epilogue {
                         const int rows = min(32, a.vocab - row0);
 #pragma unroll 8
                         for (int r = 0; r < rows; ++r) {
-                            float x = stage.value(r, lane);
-                            if (a.add) x += bf16_to_float(to[static_cast<int64_t>(r) * a.dim]);
-                            to[static_cast<int64_t>(r) * a.dim] = float_to_bf16_rn(x);
+                            uint16_t& w = to[static_cast<int64_t>(r) * a.dim];
+                            w = float_to_bf16_rn(stage.value(r, lane) + bf16_to_float(w));
                         }
                     }
                 }
@@ -512,6 +557,7 @@ head_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 }
             });
         }
+        if ((MODE == kDz || MODE == kDh) && lane == 0) bulk_wait();
     }
     __syncwarp();
     __syncthreads();
@@ -715,15 +761,23 @@ head_copy_kernel(const uint16_t* from, int64_t stride, const int32_t* index, con
     }
 }
 
-// The tiles' maxima and sums of a live row joined: a warp a row, in a fixed order.
+// The tiles' maxima and sums of a row joined: a warp a row, in a fixed order.
 __global__ void __launch_bounds__(256)
-head_join_kernel(const int32_t* counts, const int32_t* index, const float2* parts, int64_t pitch,
-                 int32_t n_parts, const float* picked, float* loss, float* lse) {
+head_join_kernel(const HeadCall c, const int32_t* counts, const int32_t* index,
+                 const float2* parts, int32_t n_parts, const float* picked) {
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
     wait_for_launch_before();
-    if (row >= *counts) return;
-    const float2* p = parts + row * pitch;
+    const bool as_they_are = counts == nullptr;
+    if (row >= (as_they_are ? c.n_tokens : *counts)) return;
+    if (as_they_are && live_label(c, row, false) < 0) {
+        if (lane == 0) {
+            c.loss[row] = 0.0f;
+            if (c.lse != nullptr) c.lse[row] = 0.0f;
+        }
+        return;
+    }
+    const float2* p = parts + row * n_parts;
     float top = -INFINITY, sum = 0.0f;
 #pragma unroll 4
     for (int i = lane; i < n_parts; i += 32) {
@@ -747,10 +801,10 @@ head_join_kernel(const int32_t* counts, const int32_t* index, const float2* part
         // multiplied by)
         const double l = static_cast<double>(top) / static_cast<double>(kLog2e) +
                          log(static_cast<double>(sum));
-        const int32_t t = index[row];
+        const int64_t t = as_they_are ? row : index[row];
         const double d = l - static_cast<double>(picked[row]);
-        loss[t] = d < 0.0 ? 0.0f : static_cast<float>(d);
-        if (lse != nullptr) lse[t] = static_cast<float>(l);
+        c.loss[t] = d < 0.0 ? 0.0f : static_cast<float>(d);
+        if (c.lse != nullptr) c.lse[t] = static_cast<float>(l);
     }
 }
 
@@ -758,8 +812,8 @@ head_join_kernel(const int32_t* counts, const int32_t* index, const float2* part
 // takes up to 512 columns of a row.
 template <bool WIDE>
 __global__ void __launch_bounds__(256)
-head_finish_kernel(const int32_t* slot, const float* sums, int64_t rows, int64_t pitch,
-                   int32_t splits, int64_t n_tokens, int32_t dim, int32_t sections, uint16_t* out,
+head_finish_kernel(const int32_t* slot, const float* sums, int64_t rows, int32_t splits,
+                   int64_t n_tokens, int32_t dim, int32_t sections, uint16_t* out,
                    int64_t stride) {
     constexpr int N = kCopyColumns / 128;
     const int64_t id = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
@@ -773,14 +827,17 @@ head_finish_kernel(const int32_t* slot, const float* sums, int64_t rows, int64_t
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (j >= 0) {
-        const float* from = sums + j * pitch + first;
+        // (see HeadArgs)
+        const int blocks = (dim + 31) / 32;
+        const float* from =
+            sums + (first / 32 * rows + j) * 32 + 4 * (first % 32 / 4 ^ (j & 7));
 #pragma unroll 4
         for (int s = 0; s < splits; ++s) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 if (first + 128 * i < dim) {
-                    const float4 w =
-                        *reinterpret_cast<const float4*>(from + s * rows * pitch + 128 * i);
+                    const float4 w = *reinterpret_cast<const float4*>(
+                        from + (static_cast<int64_t>(s) * blocks + 4 * i) * rows * 32);
                     v[i] = make_float4(v[i].x + w.x, v[i].y + w.y, v[i].z + w.z, v[i].w + w.w);
                 }
             }
@@ -896,7 +953,8 @@ cudaError_t copy_piece(const HeadCall& c, const HeadPlan& p, int64_t first, cuda
                      stream);
 }
 
-// The piece's gradient of the logits, in boxes of 64 columns by `box_rows`.
+// The piece's gradient of the logits, in boxes of 64 columns by `box_rows` (it is stored as
+// swizzled as it has to be in shared memory).
 cudaError_t dz_map(CUtensorMap* map, const HeadArgs& a, int box_rows) {
     Encode encode = nullptr;
     if (cudaError_t e = find_encode(&encode); e != cudaSuccess) return e;
@@ -905,7 +963,7 @@ cudaError_t dz_map(CUtensorMap* map, const HeadArgs& a, int box_rows) {
     const cuuint64_t strides[2] = {128, static_cast<cuuint64_t>(a.rows) * 128};
     const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1}, ones[3] = {1, 1, 1};
     const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.dz, sizes, strides, box,
-                              ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
@@ -956,7 +1014,6 @@ HeadArgs product_args(const HeadCall& c, const HeadPlan& p, int64_t first) {
     a.sums = at<float>(c, p.sums);
     a.grad_table = c.grad_table == nullptr ? nullptr : c.grad_table + first * c.dim;
     a.parts_pitch = (c.vocab + kPairTile - 1) / kPairTile;
-    a.sums_pitch = p.pitch;
     a.rows = p.rows;
     a.first = static_cast<int32_t>(first);
     a.vocab = static_cast<int32_t>(piece_rows(c, p, first));
@@ -978,7 +1035,7 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back) {
     constexpr int64_t kMost = int64_t{512} << 20;
     HeadPlan p{};
     p.rows = whole(n_tokens < 1 ? 1 : n_tokens, kPairTile);
-    p.pitch = whole(dim, 8);
+    p.pitch = whole(dim, 64);                // rows on 128-byte boundaries: fewer lines a box
     const int64_t per_row = 2 * (back && p.rows > p.pitch ? p.rows : p.pitch);
     int64_t most = kMost / per_row / kPairTile * kPairTile;
     if (most < kPairTile) most = kPairTile;
@@ -1020,13 +1077,20 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back) {
         p.lse = place(4 * n);
         p.grad = place(4 * n);
         p.dz = place(2 * p.rows * whole(p.piece < vocab ? p.piece : vocab, 64));
-        p.sums = place(4 * p.splits * p.rows * p.pitch);
+        p.sums = place(4 * p.splits * p.rows * whole(dim, 32));
     } else {
         p.parts = place(8 * n * tiles_of(vocab));
         p.picked = place(4 * n);
     }
     p.bytes = end;
     return p;
+}
+
+// Forward, one tile of tokens that TMA reaches: nothing is saved by leaving tokens out, and
+// what they hold stays in their rows (32 x 50257 x 768: 41 us with a launch for the rows).
+bool head_rows_as_they_are(const HeadCall& c) {
+    return c.n_tokens <= kPairTile && aligned_to(c.hidden, 16) && c.hidden_stride % 8 == 0 &&
+           c.hidden_stride < int64_t{1} << 32;
 }
 
 cudaError_t launch_head_rows(const HeadCall& c, const HeadPlan& p, bool back, cudaStream_t stream) {
@@ -1052,21 +1116,30 @@ cudaError_t launch_head_gather(const HeadCall& c, const HeadPlan& p, cudaStream_
 cudaError_t launch_head_loss(const HeadCall& c, const HeadPlan& p, int64_t first,
                              cudaStream_t stream) {
     if (cudaError_t e = copy_piece(c, p, first, stream); e != cudaSuccess) return e;
+    const bool as_they_are = head_rows_as_they_are(c);
     CUtensorMap ma, mb;
-    if (cudaError_t e = make_map(&ma, at<uint16_t>(c, p.hidden), c.dim, p.rows, p.pitch, kHalf);
+    if (cudaError_t e = as_they_are ? make_map(&ma, c.hidden, c.dim, c.n_tokens, c.hidden_stride, kHalf)
+                                    : make_map(&ma, at<uint16_t>(c, p.hidden), c.dim, p.rows, p.pitch,
+                                               kHalf);
         e != cudaSuccess)
         return e;
     if (cudaError_t e = piece_map(&mb, c, p, first, kHalf); e != cudaSuccess) return e;
-    const HeadArgs a = product_args(c, p, first);
+    HeadArgs a = product_args(c, p, first);
+    if (as_they_are) {
+        a.counts = a.label = nullptr;
+        a.labels = c.labels;
+        a.label64 = c.label64;
+        a.n_rows = static_cast<int32_t>(c.n_tokens);
+    }
     return launch_product<kLoss>(ma, mb, a, p.rows / kPairTile * tiles_of(a.vocab), stream);
 }
 
 cudaError_t launch_head_join(const HeadCall& c, const HeadPlan& p, cudaStream_t stream) {
     const unsigned grid = static_cast<unsigned>((c.n_tokens + 7) / 8);
-    const int64_t parts = tiles_of(c.vocab);
-    return launch_after(head_join_kernel, grid, 256, 0, stream, at<int32_t>(c, p.counts),
-                        at<int32_t>(c, p.index), at<float2>(c, p.parts), parts, parts,
-                        at<float>(c, p.picked), c.loss, c.lse);
+    const bool as_they_are = head_rows_as_they_are(c);
+    return launch_after(head_join_kernel, grid, 256, 0, stream, c,
+                        as_they_are ? nullptr : at<int32_t>(c, p.counts), at<int32_t>(c, p.index),
+                        at<float2>(c, p.parts), tiles_of(c.vocab), at<float>(c, p.picked));
 }
 
 cudaError_t launch_head_dz(const HeadCall& c, const HeadPlan& p, int64_t first,
@@ -1109,8 +1182,8 @@ cudaError_t launch_head_finish(const HeadCall& c, const HeadPlan& p, cudaStream_
     const unsigned grid = static_cast<unsigned>((c.n_tokens * sections + 7) / 8);
     const bool wide = aligned_to(c.grad_hidden, 8) && c.grad_hidden_stride % 4 == 0;
     return launch_after(wide ? head_finish_kernel<true> : head_finish_kernel<false>, grid, 256, 0,
-                        stream, at<int32_t>(c, p.slot), at<float>(c, p.sums), p.rows, p.pitch,
-                        p.splits, c.n_tokens, c.dim, sections, c.grad_hidden, c.grad_hidden_stride);
+                        stream, at<int32_t>(c, p.slot), at<float>(c, p.sums), p.rows, p.splits,
+                        c.n_tokens, c.dim, sections, c.grad_hidden, c.grad_hidden_stride);
 }
 
 cudaError_t read_head_status(int* status, int clear, cudaStream_t stream) {

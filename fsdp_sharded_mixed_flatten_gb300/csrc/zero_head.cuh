@@ -40,6 +40,9 @@ struct HeadPlan {
 };
 HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back);
 
+// Whether the forward pass takes all tokens as they lie, without the first two launches.
+bool head_rows_as_they_are(const HeadCall& c);
+
 // The launches of a call, in order.
 cudaError_t launch_head_rows(const HeadCall& c, const HeadPlan& p, bool back, cudaStream_t stream);
 cudaError_t launch_head_gather(const HeadCall& c, const HeadPlan& p, cudaStream_t stream);

@@ -659,11 +659,14 @@ ZERO_API int zero_head_loss(const uint16_t* hidden, int64_t n_tokens, int64_t di
     c.lse = lse;
     c.workspace = workspace;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (int rc = cuda_call("head rows launch",
-                           [&] { return zf::launch_head_rows(c, p, false, s); }))
-        return rc;
-    if (int rc = cuda_call("head gather launch", [&] { return zf::launch_head_gather(c, p, s); }))
-        return rc;
+    if (!zf::head_rows_as_they_are(c)) {
+        if (int rc = cuda_call("head rows launch",
+                               [&] { return zf::launch_head_rows(c, p, false, s); }))
+            return rc;
+        if (int rc =
+                cuda_call("head gather launch", [&] { return zf::launch_head_gather(c, p, s); }))
+            return rc;
+    }
     for (int64_t first = 0; first < vocab; first += p.piece) {
         if (int rc = cuda_call("head loss launch",
                                [&] { return zf::launch_head_loss(c, p, first, s); }))

@@ -80,8 +80,8 @@ def test_nothing_to_do_is_done(lib):
 
 
 def test_injected_failure(lib, monkeypatch):
-    for call in (_loss, _grad):
-        monkeypatch.setenv("ZERO_INJECT_FAILURE", "head rows launch")
+    for call, label in ((_loss, "head loss launch"), (_grad, "head rows launch")):
+        monkeypatch.setenv("ZERO_INJECT_FAILURE", label)
         assert call(lib) == -4
         assert "injected failure" in zf.zero_last_error()
 
