@@ -33,7 +33,7 @@ using namespace tile;
 
 __device__ int g_head_status = 0;
 
-constexpr int kPairTile = 256;                  // rows and columns of a pair's tile
+constexpr int kPairTile = 256;                  // rows, and most columns, of a pair's tile
 constexpr int kTileK = 64;
 constexpr int kHalf = 128;                  // of the tile, a CTA's share of each operand
 constexpr int kStages = 6;
@@ -47,6 +47,9 @@ constexpr int kHeadThreads = 64 + 32 * kEpilogueWarps;
 constexpr uint32_t kTmemColumns = 512;      // two tiles' results
 constexpr uint64_t kHeadWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kInvLog2e = static_cast<float>(1.0 / static_cast<double>(kLog2e));
+constexpr float kInvLog2eLo = static_cast<float>(1.0 / static_cast<double>(kLog2e) -
+                                                 static_cast<double>(kInvLog2e));
 
 enum Mode { kLoss, kDz, kDh, kDw };
 
@@ -71,6 +74,8 @@ struct HeadArgs {
     int32_t blocks;               // of 64 columns of the piece
     int32_t add;                  // to the sums, or to the table's gradient, that are there
     int32_t wide;                 // rows of the table's gradient on 16-byte boundaries
+    int32_t width;                // columns of a tile, a multiple of 32 (kDz: of 64)
+    int32_t part;                 // of a row's maxima and sums, the piece's first
     int32_t n_rows;
     int32_t label64;
     int32_t group;                // tiles along M that are worked on together
@@ -122,14 +127,14 @@ struct Tiles {
         const int n = MODE == kLoss || MODE == kDz ? a.vocab : a.dim;
         const int k = MODE == kDh ? a.vocab : MODE == kDw ? live : a.dim;
         m_tiles = (m + kPairTile - 1) / kPairTile;
-        n_tiles = (n + kPairTile - 1) / kPairTile;
+        n_tiles = (n + a.width - 1) / a.width;
         steps = (k + kTileK - 1) / kTileK;
         splits = MODE == kDh ? a.splits : 1;
         group = a.group;
         total = m_tiles * n_tiles * splits;
     }
     struct At {
-        int m, n, split, begin, end;          // rows and columns / 256, steps along K
+        int m, n, split, begin, end;          // rows / 256, columns / width, steps along K
     };
     __device__ __forceinline__ At operator()(int i) const {
         At t;
@@ -200,14 +205,15 @@ struct Stage {
     }
 };
 
-// The result of a tile, by warps: each has 32 rows (its lanes') and 128 of the columns, in
-// four parts of 32.
+// The result of a tile, by warps: each has 32 rows (its lanes') and half of the columns, in
+// up to four parts of 32.
 template <int MODE>
 struct Epilogue {
     const HeadArgs& a;
     Stage stage;
     float2 (*both)[kHalf];        // what the second half of the columns found, by row
     int live, place, half, lane;  // place: this warp's first row of the CTA's 128
+    int begin, parts;             // this warp's columns: 32 begin ..., of the tile's
     __device__ Epilogue(const HeadArgs& args, char* staging, float2 (*found)[kHalf], int warp, int l)
         : a(args),
           stage{staging, l},
@@ -215,14 +221,20 @@ struct Epilogue {
           live(live_rows(args)),
           place(warp % 4 * 32),
           half((warp - 2) / 4),
-          lane(l) {}
+          lane(l) {
+        // the first half has the odd part
+        constexpr int kUnit = MODE == kDz ? 2 : 1;
+        const int all = a.width / 32, first = (all / kUnit + 1) / 2 * kUnit;
+        begin = half == 0 ? 0 : first;
+        parts = half == 0 ? first : all - first;
+    }
 
-    // `row` of the launch's M: this warp's first; n: columns / 256; `slot`: 0 and 1 in turn;
-    // `each(f)` calls f(c, v) with columns 32 c ... of this warp's half, c = 0 to 3
+    // `row0` of the launch's M: this warp's first; n: columns / width; `slot`: 0 and 1 in turn;
+    // `each(f)` calls f(c, v) with columns 32 c ... of this warp's, c < parts
     template <class Each>
     __device__ __forceinline__ void operator()(int row0, int n, int split, int slot,
                                                Each&& each) const {
-        const int column = n * kPairTile + half * kHalf;
+        const int column = n * a.width + 32 * begin;
         const int row = row0 + lane;
         if constexpr (MODE == kLoss) {
             const int left = a.vocab - column;           // columns that exist
@@ -257,14 +269,14 @@ struct Epilogue {
                 sum += s.x + s.y;
                 top = m;
             });
-            if (mine >= 0 && mine < min(kHalf, left)) a.picked[row] = z;
+            if (mine >= 0 && mine < min(32 * parts, left)) a.picked[row] = z;
             // the two halves of the columns
             if (half == 1) both[slot][place + lane] = make_float2(top, sum);
             asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpilogueWarps) : "memory");
             if (half == 0 && row < live) {
                 const float2 o = both[slot][place + lane];
                 const float m = fmaxf(top, o.x), from = m == -INFINITY ? 0.0f : m;
-                a.parts[row * a.parts_pitch + a.first / kPairTile + n] = make_float2(
+                a.parts[row * a.parts_pitch + a.part + n] = make_float2(
                     m, sum * exp2_fast(top - from) + o.y * exp2_fast(o.x - from));
             }
         } else if constexpr (MODE == kDz) {
@@ -318,12 +330,13 @@ struct Epilogue {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) y[i] = pair(v[2 * i], v[2 * i + 1]);
                 stage.put_half(y, c % 2);
-                if (c % 2 == 0) return;
+                if (c % 2 == 0 && c + 1 < parts) return;
                 __syncwarp();
-                const int first = column + 32 * (c - 1);              // 64 columns
+                const int first = column + 32 * (c - c % 2);          // 64 columns, or 32
+                const int end = min(a.dim, column + 32 * (c + 1));
                 if (a.wide) {
                     const int col = first + lane % 8 * 8;
-                    if (col < a.dim) {
+                    if (col < end) {
                         uint16_t* to =
                             a.grad_table + static_cast<int64_t>(row0 + lane / 8) * a.dim + col;
 #pragma unroll
@@ -337,7 +350,7 @@ struct Epilogue {
                 } else {
                     uint16_t* to = a.grad_table + static_cast<int64_t>(row0) * a.dim + first + lane;
                     const int rows = min(32, a.vocab - row0);
-                    const bool one = first + lane < a.dim, two = first + 32 + lane < a.dim;
+                    const bool one = first + lane < end, two = first + 32 + lane < end;
 #pragma unroll 8
                     for (int r = 0; r < rows; ++r) {
                         if (one) to[static_cast<int64_t>(r) * a.dim] = stage.value16(r, lane);
@@ -438,10 +451,13 @@ head_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             int s = 0;
             uint32_t phase = 1;
             bool run = true;
+            const bool two_chunks = a.width > 128;       // of B, where it is MN-major
+            const uint32_t bytes =
+                2 * (kOperandBytes + (kBmn ? (two_chunks ? 2 : 1) * kChunkBytes : a.width / 2 * 128));
             for (int i = pair; run && i < tiles.total; i += pairs) {
                 const auto t = tiles(i);
                 const int m0 = t.m * kPairTile + static_cast<int>(rank) * kHalf;
-                const int n0 = t.n * kPairTile + static_cast<int>(rank) * kHalf;
+                const int n0 = t.n * a.width + static_cast<int>(rank) * (a.width / 2);
                 for (int k = t.begin; k < t.end; ++k) {
                     if (!wait(sh, sh.empty[s], phase)) {
                         run = false;
@@ -449,7 +465,7 @@ head_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     }
                     const uint32_t bar = smem_address(&sh.full[s]);
                     const uint32_t to_a = ring + s * kStageBytes, to_b = to_a + kOperandBytes;
-                    if (rank == 0) bar_expect(bar, 2 * kStageBytes);
+                    if (rank == 0) bar_expect(bar, bytes);
                     if constexpr (MODE == kDw) {
                         tma_load(to_a, &map_a, 0, k * kTileK, m0 / 64, bar);
                         tma_load(to_a + kChunkBytes, &map_a, 0, k * kTileK, m0 / 64 + 1, bar);
@@ -460,7 +476,8 @@ head_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     }
                     if constexpr (kBmn) {
                         tma_load(to_b, &map_b, n0, k * kTileK, bar);
-                        tma_load(to_b + kChunkBytes, &map_b, n0 + 64, k * kTileK, bar);
+                        if (two_chunks)
+                            tma_load(to_b + kChunkBytes, &map_b, n0 + 64, k * kTileK, bar);
                     } else {
                         tma_load(to_b, &map_b, k * kTileK, n0, bar);
                     }
@@ -476,6 +493,7 @@ head_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             int s = 0, n = 0;
             uint32_t phase = 0;
             bool run = true;
+            const uint32_t form = product_form(kAmn, kBmn, a.width);
             for (int i = pair; run && i < tiles.total; i += pairs) {
                 const auto t = tiles(i);
                 if (t.begin == t.end) continue;
@@ -497,7 +515,7 @@ head_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     for (int j = 0; j < kTileK / 16; ++j) {
                         // 16 values along K: 32 bytes of a row, or 16 rows
                         product(d, da + (kAmn ? 16 * 128 : 32) / 16 * j,
-                                db + (kBmn ? 16 * 128 : 32) / 16 * j, product_form(kAmn, kBmn),
+                                db + (kBmn ? 16 * 128 : 32) / 16 * j, form,
                                 k != t.begin || j != 0);
                     }
                     products_arrive(smem_address(&sh.empty[s]));
@@ -514,15 +532,15 @@ head_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         char* const staging = dyn + (ring - smem_address(dyn)) + kStages * kStageBytes;
         const Epilogue<MODE> epilogue(a, staging + (warp - 2) * kStagingBytes,
                                       reinterpret_cast<float2(*)[kHalf]>(staging), warp, lane);
-        const int half = epilogue.half;
+        const int parts = epilogue.parts;
         int n = 0;
         for (int i = pair; i < tiles.total; i += pairs) {
             const auto t = tiles(i);
             const int row0 = t.m * kPairTile + static_cast<int>(rank) * kHalf + epilogue.place;
             if (t.begin == t.end) {                      // a sum of nothing
-                epilogue(row0, t.n, t.split, 0, [](auto&& f) {
+                epilogue(row0, t.n, t.split, 0, [&](auto&& f) {
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < parts; ++c) {
                         float v[32] = {};
                         f(c, v);
                     }
@@ -535,24 +553,43 @@ head_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             __syncwarp();
             ++n;
             fence_after_sync();
-            const uint32_t from =
-                tmem + slot * kPairTile + half * kHalf + (static_cast<uint32_t>(epilogue.place) << 16);
+            const uint32_t from = tmem + slot * kPairTile + 32 * epilogue.begin +
+                                  (static_cast<uint32_t>(epilogue.place) << 16);
             epilogue(row0, t.n, t.split, slot, [&](auto&& f) {
+                auto release = [&] {                     // the tile's place may be taken
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive_in_cluster(in_cta(smem_address(&sh.taken[slot]), 0));
+                };
+                if constexpr (MODE == kDw) {             // (registers are short)
+                    if (parts == 0) release();
+#pragma unroll 1
+                    for (int c = 0; c < parts; ++c) {
+                        float v[32];
+                        tmem_load(v, from + 32 * c);
+                        tmem_load_wait(v);
+                        if (c + 1 == parts) release();
+                        f(c, v);
+                        __syncwarp();
+                    }
+                    return;
+                }
                 // the next part is on its way while one is worked on
                 float v[2][32];
-                tmem_load(v[0], from);
-                tmem_load_wait(v[0]);
+                if (parts > 0) {
+                    tmem_load(v[0], from);
+                    tmem_load_wait(v[0]);
+                }
+                if (parts <= 1) release();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    if (c < 3) tmem_load(v[(c + 1) % 2], from + 32 * (c + 1));
+                    if (c >= parts) break;
+                    if (c < 3 && c + 1 < parts) tmem_load(v[(c + 1) % 2], from + 32 * (c + 1));
                     f(c, v[c % 2]);
                     __syncwarp();
-                    if (c < 3) tmem_load_wait(v[(c + 1) % 2]);
-                    if (c == 2) {                        // the tile's place may be taken
-                        fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0)
-                            bar_arrive_in_cluster(in_cta(smem_address(&sh.taken[slot]), 0));
+                    if (c < 3 && c + 1 < parts) {
+                        tmem_load_wait(v[(c + 1) % 2]);
+                        if (c + 2 == parts) release();
                     }
                 }
             });
@@ -796,15 +833,15 @@ head_join_kernel(const HeadCall c, const int32_t* counts, const int32_t* index,
         top = m;
     }
     if (lane == 0) {
-        // in 64 bits: the loss is a small difference of two such numbers, and never
-        // negative (the logit of `top` is top divided by the very constant it was
-        // multiplied by)
-        const double l = static_cast<double>(top) / static_cast<double>(kLog2e) +
-                         log(static_cast<double>(sum));
+        // The logit of `top` is top divided by the very constant it was multiplied by, a
+        // factor in two parts; the loss is what it lies above the label's, rounded once,
+        // and the sum's logarithm: two numbers that are not negative.
+        const float l = logf(sum);
         const int64_t t = as_they_are ? row : index[row];
-        const double d = l - static_cast<double>(picked[row]);
-        c.loss[t] = d < 0.0 ? 0.0f : static_cast<float>(d);
-        if (c.lse != nullptr) c.lse[t] = static_cast<float>(l);
+        const float d = __fmaf_rn(top, kInvLog2eLo, __fmaf_rn(top, kInvLog2e, -picked[row])) + l;
+        c.loss[t] = d < 0.0f ? 0.0f : d;
+        if (c.lse != nullptr)
+            c.lse[t] = __fmaf_rn(top, kInvLog2e, __fmaf_rn(top, kInvLog2eLo, l));
     }
 }
 
@@ -1013,7 +1050,7 @@ HeadArgs product_args(const HeadCall& c, const HeadPlan& p, int64_t first) {
     a.dz = at<uint16_t>(c, p.dz);
     a.sums = at<float>(c, p.sums);
     a.grad_table = c.grad_table == nullptr ? nullptr : c.grad_table + first * c.dim;
-    a.parts_pitch = (c.vocab + kPairTile - 1) / kPairTile;
+    a.parts_pitch = p.parts_a_row;
     a.rows = p.rows;
     a.first = static_cast<int32_t>(first);
     a.vocab = static_cast<int32_t>(piece_rows(c, p, first));
@@ -1025,7 +1062,27 @@ HeadArgs product_args(const HeadCall& c, const HeadPlan& p, int64_t first) {
 }
 
 int64_t whole(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
-int64_t tiles_of(int64_t x) { return (x + kPairTile - 1) / kPairTile; }
+int64_t tiles_of(int64_t x, int64_t width) { return (x + width - 1) / width; }
+
+// Clock cycles of a launch that takes m rows of tiles, n columns and `splits` parts of the
+// sum, each of `steps` steps, when a tile is `width` columns wide: rounds of tiles over the
+// GPU's pairs, in each the steps (256 + width, what the operands take on their way), the
+// results' way out and what comes before.  Measured: 12 steps of width 256 7500 to 8400
+// cycles, 64 steps 36000 to 40000.
+double launch_cost(int64_t m, int64_t n, int64_t steps, int64_t splits, int width) {
+    const int64_t pairs = device_sms() / 2 > 0 ? device_sms() / 2 : 1;
+    const int64_t rounds = (m * tiles_of(n, width) * splits + pairs - 1) / pairs;
+    return static_cast<double>(rounds) *
+           ((256.0 + width) * static_cast<double>(steps) / splits + 12.0 * width + 800.0);
+}
+
+int best_width(int64_t m, int64_t n, int64_t steps, int unit) {
+    int best = kPairTile;
+    for (int w = kPairTile - unit; w >= unit; w -= unit) {
+        if (launch_cost(m, n, steps, 1, w) < 0.98 * launch_cost(m, n, steps, 1, best)) best = w;
+    }
+    return best;
+}
 
 }  // namespace
 
@@ -1037,28 +1094,37 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back) {
     p.rows = whole(n_tokens < 1 ? 1 : n_tokens, kPairTile);
     p.pitch = whole(dim, 64);                // rows on 128-byte boundaries: fewer lines a box
     const int64_t per_row = 2 * (back && p.rows > p.pitch ? p.rows : p.pitch);
+    const int64_t m = p.rows / kPairTile;
     int64_t most = kMost / per_row / kPairTile * kPairTile;
     if (most < kPairTile) most = kPairTile;
     const int64_t pieces = (vocab + most - 1) / most;
     p.piece = whole((vocab + pieces - 1) / pieces, kPairTile);
     p.splits = 1;
+    const int64_t steps_dim = tiles_of(dim, kTileK);
     if (back) {
-        // the sum over a piece in as many parts as keep the GPU's pairs busy, in units of
-        // a step's 0.3 us; every part is written and read again, at 6 TB/s
-        const double way = 8.0 * p.rows * p.pitch / 6e12 / 0.3e-6;
-        const int64_t tiles = p.rows / kPairTile * tiles_of(dim), steps = whole(p.piece, 64) / 64;
-        const int64_t pairs = device_sms() / 2 > 0 ? device_sms() / 2 : 1;
+        p.width_z = best_width(m, p.piece < vocab ? p.piece : vocab, steps_dim, 64);
+        p.width_w = best_width(tiles_of(p.piece, kPairTile), dim, tiles_of(n_tokens, kTileK), 32);
+        // the sum over a piece in as many parts as keep the GPU's pairs busy; every part is
+        // written, and read again in the end, at 6 TB/s and 1.9 GHz
+        const int64_t steps = tiles_of(p.piece, kTileK);
+        const double way = 8.0 * p.rows * whole(dim, 32) / 6e12 * 1.9e9;
         double best = 0.0;
-        for (int64_t s = 1; s <= 64 && s * 4 <= steps && s * p.rows * p.pitch * 4 <= kMost; ++s) {
-            // rounds of tiles, each a share of the sum and the way out of it
-            const double cost =
-                static_cast<double>((tiles * s + pairs - 1) / pairs) * (steps / (double)s + 8.0) +
-                way * s;
-            if (s == 1 || cost < best) {
-                best = cost;
-                p.splits = static_cast<int32_t>(s);
+        for (int64_t s = 1;
+             s <= 64 && (s == 1 || (s * 4 <= steps && s * p.rows * p.pitch * 4 <= kMost)); ++s) {
+            for (int w = kPairTile; w >= 32; w -= 32) {
+                const double cost = launch_cost(m, dim, steps, s, w) + way * s;
+                if ((s == 1 && w == kPairTile) || cost < 0.98 * best) {
+                    best = cost;
+                    p.splits = static_cast<int32_t>(s);
+                    p.width_h = w;
+                }
             }
         }
+    } else {
+        p.width_z = best_width(m, p.piece < vocab ? p.piece : vocab, steps_dim, 32);
+        p.parts_a_piece = static_cast<int32_t>(tiles_of(p.piece, p.width_z));
+        p.parts_a_row = static_cast<int32_t>((pieces - 1) * p.parts_a_piece +
+                                             tiles_of(vocab - (pieces - 1) * p.piece, p.width_z));
     }
     int64_t end = 0;
     auto place = [&](int64_t bytes) {
@@ -1079,7 +1145,7 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back) {
         p.dz = place(2 * p.rows * whole(p.piece < vocab ? p.piece : vocab, 64));
         p.sums = place(4 * p.splits * p.rows * whole(dim, 32));
     } else {
-        p.parts = place(8 * n * tiles_of(vocab));
+        p.parts = place(8 * n * p.parts_a_row);
         p.picked = place(4 * n);
     }
     p.bytes = end;
@@ -1123,15 +1189,17 @@ cudaError_t launch_head_loss(const HeadCall& c, const HeadPlan& p, int64_t first
                                                kHalf);
         e != cudaSuccess)
         return e;
-    if (cudaError_t e = piece_map(&mb, c, p, first, kHalf); e != cudaSuccess) return e;
+    if (cudaError_t e = piece_map(&mb, c, p, first, p.width_z / 2); e != cudaSuccess) return e;
     HeadArgs a = product_args(c, p, first);
+    a.width = p.width_z;
+    a.part = static_cast<int32_t>(first / p.piece * p.parts_a_piece);
     if (as_they_are) {
         a.counts = a.label = nullptr;
         a.labels = c.labels;
         a.label64 = c.label64;
         a.n_rows = static_cast<int32_t>(c.n_tokens);
     }
-    return launch_product<kLoss>(ma, mb, a, p.rows / kPairTile * tiles_of(a.vocab), stream);
+    return launch_product<kLoss>(ma, mb, a, p.rows / kPairTile * tiles_of(a.vocab, a.width), stream);
 }
 
 cudaError_t launch_head_join(const HeadCall& c, const HeadPlan& p, cudaStream_t stream) {
@@ -1139,7 +1207,7 @@ cudaError_t launch_head_join(const HeadCall& c, const HeadPlan& p, cudaStream_t 
     const bool as_they_are = head_rows_as_they_are(c);
     return launch_after(head_join_kernel, grid, 256, 0, stream, c,
                         as_they_are ? nullptr : at<int32_t>(c, p.counts), at<int32_t>(c, p.index),
-                        at<float2>(c, p.parts), tiles_of(c.vocab), at<float>(c, p.picked));
+                        at<float2>(c, p.parts), p.parts_a_row, at<float>(c, p.picked));
 }
 
 cudaError_t launch_head_dz(const HeadCall& c, const HeadPlan& p, int64_t first,
@@ -1149,32 +1217,37 @@ cudaError_t launch_head_dz(const HeadCall& c, const HeadPlan& p, int64_t first,
     if (cudaError_t e = make_map(&ma, at<uint16_t>(c, p.hidden), c.dim, p.rows, p.pitch, kHalf);
         e != cudaSuccess)
         return e;
-    if (cudaError_t e = piece_map(&mb, c, p, first, kHalf); e != cudaSuccess) return e;
-    const HeadArgs a = product_args(c, p, first);
-    return launch_product<kDz>(ma, mb, a, p.rows / kPairTile * tiles_of(a.vocab), stream);
+    if (cudaError_t e = piece_map(&mb, c, p, first, p.width_z / 2); e != cudaSuccess) return e;
+    HeadArgs a = product_args(c, p, first);
+    a.width = p.width_z;
+    return launch_product<kDz>(ma, mb, a, p.rows / kPairTile * tiles_of(a.vocab, a.width), stream);
 }
 
 cudaError_t launch_head_dh(const HeadCall& c, const HeadPlan& p, int64_t first,
                            cudaStream_t stream) {
     HeadArgs a = product_args(c, p, first);
     a.add = first > 0;
+    a.width = p.width_h;
     CUtensorMap ma, mb;
     if (cudaError_t e = dz_map(&ma, a, kHalf); e != cudaSuccess) return e;
     if (cudaError_t e = piece_map(&mb, c, p, first, kTileK); e != cudaSuccess) return e;
-    return launch_product<kDh>(ma, mb, a, p.rows / kPairTile * tiles_of(c.dim) * p.splits, stream);
+    return launch_product<kDh>(ma, mb, a, p.rows / kPairTile * tiles_of(c.dim, a.width) * p.splits,
+                               stream);
 }
 
 cudaError_t launch_head_dw(const HeadCall& c, const HeadPlan& p, int64_t first,
                            cudaStream_t stream) {
     HeadArgs a = product_args(c, p, first);
     a.add = c.accumulate;
+    a.width = p.width_w;
     a.wide = aligned_to(c.grad_table, 16) && c.dim % 8 == 0;
     CUtensorMap ma, mb;
     if (cudaError_t e = dz_map(&ma, a, kTileK); e != cudaSuccess) return e;
     if (cudaError_t e = make_map(&mb, at<uint16_t>(c, p.hidden), c.dim, p.rows, p.pitch, kTileK);
         e != cudaSuccess)
         return e;
-    return launch_product<kDw>(ma, mb, a, tiles_of(a.vocab) * tiles_of(c.dim), stream);
+    return launch_product<kDw>(ma, mb, a, tiles_of(a.vocab, kPairTile) * tiles_of(c.dim, a.width),
+                               stream);
 }
 
 cudaError_t launch_head_finish(const HeadCall& c, const HeadPlan& p, cudaStream_t stream) {

@@ -34,6 +34,9 @@ struct HeadPlan {
     int64_t rows;                 // n_tokens rounded up to whole tiles
     int64_t pitch;                // elements of a row of the hidden states' copy
     int64_t piece;                // rows of the table worked on at a time
+    int32_t width_z, width_h, width_w;    // columns of a tile of each product
+    int32_t parts_a_piece;        // maxima and sums of a row, forward
+    int32_t parts_a_row;
     int32_t splits;               // of the sum over the vocabulary in the hidden gradient
     int64_t counts, index, slot, label, lse, grad, hidden, table, parts, picked, dz, sums;
     int64_t bytes;

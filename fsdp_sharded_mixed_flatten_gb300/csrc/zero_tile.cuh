@@ -1,9 +1,9 @@
 // Building blocks of matrix products on the tensor cores by pairs of CTAs: barriers,
 // TMA tile copies, tensor memory, descriptors of operands in shared memory.
 //
-// The pair (a cluster of two) works on one 256 x 256 tile of D = A B: CTA r holds rows
-// 128 r ... of A's tile and columns 128 r ... of B's, and its tensor memory gets D's rows
-// 128 r ... (256 columns of 32 bits).  CTA 0 issues the products for both.
+// The pair (a cluster of two) works on one tile of D = A B, 256 rows by up to 256 columns:
+// CTA r holds rows 128 r ... of A's tile and its half of B's columns, and its tensor memory
+// gets D's rows 128 r ... (all columns, of 32 bits).  CTA 0 issues the products for both.
 #pragma once
 
 #include <cstdint>
@@ -165,10 +165,11 @@ __device__ __forceinline__ uint64_t operand(uint32_t address, uint32_t chunk) {
     return d;
 }
 
-// bf16 operands, fp32 result, 256 x 256 x 16 of the pair.
-__host__ __device__ constexpr uint32_t product_form(bool a_mn, bool b_mn) {
+// bf16 operands, fp32 result, 256 x `width` x 16 of the pair (width: a multiple of 32, at
+// most 256).
+__device__ __forceinline__ uint32_t product_form(bool a_mn, bool b_mn, int width) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
-           ((256u >> 3) << 17) | ((256u >> 4) << 24);
+           (static_cast<uint32_t>(width >> 3) << 17) | ((256u >> 4) << 24);
 }
 
 __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t form,
