@@ -51,7 +51,11 @@ constexpr float kInvLog2e = static_cast<float>(1.0 / static_cast<double>(kLog2e)
 constexpr float kInvLog2eLo = static_cast<float>(1.0 / static_cast<double>(kLog2e) -
                                                  static_cast<double>(kInvLog2e));
 
-enum Mode { kLoss, kDz, kDh, kDw };
+// What a launch computes: rows' statistics, the logits' gradient, or both gradients that are
+// products of it: tiles of the hidden states' first, then of the table's.
+enum Mode { kLoss, kDz, kProducts };
+// What a tile of the last is.
+enum Kind { kDh, kDw };
 
 struct HeadArgs {
     const int32_t* counts;        // live tokens; null: tokens are rows as they are, n_rows of them
@@ -70,11 +74,13 @@ struct HeadArgs {
     int32_t first;                // the piece's first row of the table, and its rows
     int32_t vocab;
     int32_t dim;
-    int32_t splits;
+    int32_t splits;               // of the sum in the hidden states' gradient
     int32_t blocks;               // of 64 columns of the piece
-    int32_t add;                  // to the sums, or to the table's gradient, that are there
+    int32_t want_h, want_w;       // the hidden states' gradient, the table's
+    int32_t add_h, add_w;         // to the sums, to the table's gradient, that are there
     int32_t wide;                 // rows of the table's gradient on 16-byte boundaries
     int32_t width;                // columns of a tile, a multiple of 32 (kDz: of 64)
+    int32_t width_h, width_w;     // of the two products' tiles
     int32_t part;                 // of a row's maxima and sums, the piece's first
     int32_t n_rows;
     int32_t label64;
@@ -117,25 +123,24 @@ __device__ __forceinline__ int label_in_piece(const HeadArgs& a, int row) {
     return y >= a.first && y < a.first + a.vocab ? static_cast<int>(y - a.first) : -1;
 }
 
-// The tiles of a launch, in the order in which the pairs take them.
-template <int MODE>
-struct Tiles {
+// The operands of a launch; the last two of kProducts' second kind of tiles.
+struct HeadMaps {
+    CUtensorMap a, b, aw, bw;
+};
+
+// A grid of tiles.
+struct Grid {
     int m_tiles, n_tiles, steps, splits, group, total;
-    __device__ explicit Tiles(const HeadArgs& a) {
-        const int live = live_rows(a);
-        const int m = MODE == kDw ? a.vocab : live;
-        const int n = MODE == kLoss || MODE == kDz ? a.vocab : a.dim;
-        const int k = MODE == kDh ? a.vocab : MODE == kDw ? live : a.dim;
-        m_tiles = (m + kPairTile - 1) / kPairTile;
-        n_tiles = (n + a.width - 1) / a.width;
-        steps = (k + kTileK - 1) / kTileK;
-        splits = MODE == kDh ? a.splits : 1;
-        group = a.group;
-        total = m_tiles * n_tiles * splits;
-    }
     struct At {
         int m, n, split, begin, end;          // rows / 256, columns / width, steps along K
     };
+    __device__ Grid(int m, int n, int k, int width, int parts, int together)
+        : m_tiles((m + kPairTile - 1) / kPairTile),
+          n_tiles((n + width - 1) / width),
+          steps((k + kTileK - 1) / kTileK),
+          splits(parts),
+          group(together),
+          total(m_tiles * n_tiles * parts) {}
     __device__ __forceinline__ At operator()(int i) const {
         At t;
         const int per = m_tiles * n_tiles;
@@ -150,6 +155,31 @@ struct Tiles {
         t.end = splits == 1 ? steps
                             : static_cast<int>(static_cast<int64_t>(steps) * (t.split + 1) / splits);
         return t;
+    }
+};
+
+// The tiles of a launch, in the order in which the pairs take them: call(kind, tile).
+template <int MODE>
+struct Tiles {
+    Grid first, second;
+    int total;
+    __device__ Tiles(const HeadArgs& a, int live)
+        : first(MODE != kProducts ? Grid(live, a.vocab, a.dim, a.width, 1, a.group)
+                                  : Grid(a.want_h ? live : 0, a.dim, a.vocab, a.width_h, a.splits,
+                                         a.group)),
+          // (nothing to add: the table's gradient stays untouched)
+          second(MODE != kProducts || !a.want_w || (a.add_w && live == 0) ? 0 : a.vocab, a.dim, live,
+                 MODE != kProducts ? kPairTile : a.width_w, 1, a.group),
+          total(first.total + second.total) {}
+    template <class F>
+    __device__ __forceinline__ void operator()(int i, F&& call) const {
+        if constexpr (MODE != kProducts) {
+            call(std::integral_constant<int, -1>{}, first(i));
+        } else if (i < first.total) {
+            call(std::integral_constant<int, kDh>{}, first(i));
+        } else {
+            call(std::integral_constant<int, kDw>{}, second(i - first.total));
+        }
     }
 };
 
@@ -207,24 +237,26 @@ struct Stage {
 
 // The result of a tile, by warps: each has 32 rows (its lanes') and half of the columns, in
 // up to four parts of 32.
-template <int MODE>
+template <int MODE, int KIND>
 struct Epilogue {
     const HeadArgs& a;
     Stage stage;
     float2 (*both)[kHalf];        // what the second half of the columns found, by row
     int live, place, half, lane;  // place: this warp's first row of the CTA's 128
-    int begin, parts;             // this warp's columns: 32 begin ..., of the tile's
-    __device__ Epilogue(const HeadArgs& args, char* staging, float2 (*found)[kHalf], int warp, int l)
+    int width, begin, parts;             // this warp's columns: 32 begin ..., of the tile's
+    __device__ Epilogue(const HeadArgs& args, int n_live, char* staging, float2 (*found)[kHalf],
+                        int warp, int l)
         : a(args),
           stage{staging, l},
           both(found),
-          live(live_rows(args)),
+          live(n_live),
           place(warp % 4 * 32),
           half((warp - 2) / 4),
-          lane(l) {
+          lane(l),
+          width(MODE != kProducts ? args.width : KIND == kDh ? args.width_h : args.width_w) {
         // the first half has the odd part
         constexpr int kUnit = MODE == kDz ? 2 : 1;
-        const int all = a.width / 32, first = (all / kUnit + 1) / 2 * kUnit;
+        const int all = width / 32, first = (all / kUnit + 1) / 2 * kUnit;
         begin = half == 0 ? 0 : first;
         parts = half == 0 ? first : all - first;
     }
@@ -234,7 +266,7 @@ struct Epilogue {
     template <class Each>
     __device__ __forceinline__ void operator()(int row0, int n, int split, int slot,
                                                Each&& each) const {
-        const int column = n * a.width + 32 * begin;
+        const int column = n * width + 32 * begin;
         const int row = row0 + lane;
         if constexpr (MODE == kLoss) {
             const int left = a.vocab - column;           // columns that exist
@@ -314,7 +346,7 @@ struct Epilogue {
                 if (c % 2 == 1)
                     stage.send(a.dz + (first / 64 * a.rows + row0) * 64, false);
             });
-        } else if constexpr (MODE == kDh) {
+        } else if constexpr (KIND == kDh) {
             const int blocks = (a.dim + 31) / 32;
             each([&](int c, float (&v)[32]) {
                 const int block = column / 32 + c;
@@ -322,9 +354,10 @@ struct Epilogue {
                 stage.sent();
                 stage.put(v);
                 stage.send(a.sums + ((static_cast<int64_t>(split) * blocks + block) * a.rows + row0) * 32,
-                           a.add != 0);
+                           a.add_h != 0);
             });
-        } else if (a.add == 0) {
+        } else if (a.add_w == 0) {
+            stage.sent();                                // (an earlier tile's)
             each([&](int c, float (&v)[32]) {
                 Pair y[16];
 #pragma unroll
@@ -360,6 +393,7 @@ struct Epilogue {
                 __syncwarp();
             });
         } else {
+            stage.sent();
             each([&](int c, float (&v)[32]) {
                 stage.put(v);
                 __syncwarp();
@@ -415,9 +449,8 @@ struct Epilogue {
 
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
-head_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-            const __grid_constant__ HeadArgs a) {
-    constexpr bool kAmn = MODE == kDw, kBmn = MODE == kDh || MODE == kDw;
+head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadArgs a) {
+    constexpr bool kBmn = MODE == kProducts;             // B is MN-major; A for kDw
     extern __shared__ char dyn[];
     __shared__ Shared sh;
     const uint32_t ring = (smem_address(dyn) + 1023u) & ~1023u;
@@ -444,48 +477,57 @@ head_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     const uint32_t tmem = sh.tmem;
     let_next_launch_begin();
     wait_for_launch_before();
-    const Tiles<MODE> tiles(a);
+    const int live = live_rows(a);
+    const Tiles<MODE> tiles(a, live);
 
     if (warp == 0) {
         if (lane == 0) {
             int s = 0;
             uint32_t phase = 1;
             bool run = true;
-            const bool two_chunks = a.width > 128;       // of B, where it is MN-major
-            const uint32_t bytes =
-                2 * (kOperandBytes + (kBmn ? (two_chunks ? 2 : 1) * kChunkBytes : a.width / 2 * 128));
             for (int i = pair; run && i < tiles.total; i += pairs) {
-                const auto t = tiles(i);
-                const int m0 = t.m * kPairTile + static_cast<int>(rank) * kHalf;
-                const int n0 = t.n * a.width + static_cast<int>(rank) * (a.width / 2);
-                for (int k = t.begin; k < t.end; ++k) {
-                    if (!wait(sh, sh.empty[s], phase)) {
-                        run = false;
-                        break;
+                tiles(i, [&](auto kind, const Grid::At& t) {
+                    constexpr int KIND = decltype(kind)::value;
+                    const int width = KIND == kDh   ? a.width_h
+                                      : KIND == kDw ? a.width_w
+                                                    : a.width;
+                    const bool two_chunks = width > 128; // of B, where it is MN-major
+                    const uint32_t bytes =
+                        2 * (kOperandBytes +
+                             (kBmn ? (two_chunks ? 2 : 1) * kChunkBytes : width / 2 * 128));
+                    const int m0 = t.m * kPairTile + static_cast<int>(rank) * kHalf;
+                    const int n0 = t.n * width + static_cast<int>(rank) * (width / 2);
+                    const CUtensorMap* map_a = KIND == kDw ? &maps.aw : &maps.a;
+                    const CUtensorMap* map_b = KIND == kDw ? &maps.bw : &maps.b;
+                    for (int k = t.begin; k < t.end; ++k) {
+                        if (!wait(sh, sh.empty[s], phase)) {
+                            run = false;
+                            return;
+                        }
+                        const uint32_t bar = smem_address(&sh.full[s]);
+                        const uint32_t to_a = ring + s * kStageBytes, to_b = to_a + kOperandBytes;
+                        if (rank == 0) bar_expect(bar, bytes);
+                        if constexpr (KIND == kDw) {
+                            tma_load(to_a, map_a, 0, k * kTileK, m0 / 64, bar);
+                            tma_load(to_a + kChunkBytes, map_a, 0, k * kTileK, m0 / 64 + 1, bar);
+                        } else if constexpr (KIND == kDh) {
+                            tma_load(to_a, map_a, 0, m0, k, bar);
+                        } else {
+                            tma_load(to_a, map_a, k * kTileK, m0, bar);
+                        }
+                        if constexpr (kBmn) {
+                            tma_load(to_b, map_b, n0, k * kTileK, bar);
+                            if (two_chunks)
+                                tma_load(to_b + kChunkBytes, map_b, n0 + 64, k * kTileK, bar);
+                        } else {
+                            tma_load(to_b, map_b, k * kTileK, n0, bar);
+                        }
+                        if (++s == kStages) {
+                            s = 0;
+                            phase ^= 1;
+                        }
                     }
-                    const uint32_t bar = smem_address(&sh.full[s]);
-                    const uint32_t to_a = ring + s * kStageBytes, to_b = to_a + kOperandBytes;
-                    if (rank == 0) bar_expect(bar, bytes);
-                    if constexpr (MODE == kDw) {
-                        tma_load(to_a, &map_a, 0, k * kTileK, m0 / 64, bar);
-                        tma_load(to_a + kChunkBytes, &map_a, 0, k * kTileK, m0 / 64 + 1, bar);
-                    } else if constexpr (MODE == kDh) {
-                        tma_load(to_a, &map_a, 0, m0, k, bar);
-                    } else {
-                        tma_load(to_a, &map_a, k * kTileK, m0, bar);
-                    }
-                    if constexpr (kBmn) {
-                        tma_load(to_b, &map_b, n0, k * kTileK, bar);
-                        if (two_chunks)
-                            tma_load(to_b + kChunkBytes, &map_b, n0 + 64, k * kTileK, bar);
-                    } else {
-                        tma_load(to_b, &map_b, k * kTileK, n0, bar);
-                    }
-                    if (++s == kStages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
-                }
+                });
             }
         }
     } else if (warp == 1) {
@@ -493,108 +535,123 @@ head_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             int s = 0, n = 0;
             uint32_t phase = 0;
             bool run = true;
-            const uint32_t form = product_form(kAmn, kBmn, a.width);
             for (int i = pair; run && i < tiles.total; i += pairs) {
-                const auto t = tiles(i);
-                if (t.begin == t.end) continue;
-                const int slot = n % 2;
-                if (!wait(sh, sh.taken[slot], (n / 2 + 1) % 2)) break;
-                ++n;
-                fence_after_sync();
-                const uint32_t d = tmem + slot * kPairTile;
-                for (int k = t.begin; k < t.end; ++k) {
-                    if (!wait(sh, sh.full[s], phase)) {
-                        run = false;
-                        break;
-                    }
+                tiles(i, [&](auto kind, const Grid::At& t) {
+                    constexpr int KIND = decltype(kind)::value;
+                    constexpr bool kAmn = KIND == kDw;
+                    if (t.begin == t.end) return;
+                    const uint32_t form = product_form(kAmn, kBmn,
+                                                       KIND == kDh   ? a.width_h
+                                                       : KIND == kDw ? a.width_w
+                                                                     : a.width);
+                    const int slot = n % 2;
+                    run = wait(sh, sh.taken[slot], (n / 2 + 1) % 2);
+                    if (!run) return;
+                    ++n;
                     fence_after_sync();
-                    const uint32_t at = ring + s * kStageBytes;
-                    const uint64_t da = operand(at, kAmn ? kChunkBytes : 16);
-                    const uint64_t db = operand(at + kOperandBytes, kBmn ? kChunkBytes : 16);
+                    const uint32_t d = tmem + slot * kPairTile;
+                    for (int k = t.begin; k < t.end; ++k) {
+                        run = wait(sh, sh.full[s], phase);
+                        if (!run) return;
+                        fence_after_sync();
+                        const uint32_t at = ring + s * kStageBytes;
+                        const uint64_t da = operand(at, kAmn ? kChunkBytes : 16);
+                        const uint64_t db = operand(at + kOperandBytes, kBmn ? kChunkBytes : 16);
 #pragma unroll
-                    for (int j = 0; j < kTileK / 16; ++j) {
-                        // 16 values along K: 32 bytes of a row, or 16 rows
-                        product(d, da + (kAmn ? 16 * 128 : 32) / 16 * j,
-                                db + (kBmn ? 16 * 128 : 32) / 16 * j, form,
-                                k != t.begin || j != 0);
+                        for (int j = 0; j < kTileK / 16; ++j) {
+                            // 16 values along K: 32 bytes of a row, or 16 rows
+                            product(d, da + (kAmn ? 16 * 128 : 32) / 16 * j,
+                                    db + (kBmn ? 16 * 128 : 32) / 16 * j, form,
+                                    k != t.begin || j != 0);
+                        }
+                        products_arrive(smem_address(&sh.empty[s]));
+                        if (++s == kStages) {
+                            s = 0;
+                            phase ^= 1;
+                        }
                     }
-                    products_arrive(smem_address(&sh.empty[s]));
-                    if (++s == kStages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
-                }
-                if (run) products_arrive(smem_address(&sh.done[slot]));
+                    products_arrive(smem_address(&sh.done[slot]));
+                });
             }
         }
     } else {
         // (the forward pass stages nothing: its halves meet there)
         char* const staging = dyn + (ring - smem_address(dyn)) + kStages * kStageBytes;
-        const Epilogue<MODE> epilogue(a, staging + (warp - 2) * kStagingBytes,
-                                      reinterpret_cast<float2(*)[kHalf]>(staging), warp, lane);
-        const int parts = epilogue.parts;
+        char* const mine = staging + (warp - 2) * kStagingBytes;
+        float2(*const both)[kHalf] = reinterpret_cast<float2(*)[kHalf]>(staging);
+        const Epilogue<MODE, kDh> epilogue_h(a, live, mine, both, warp, lane);
+        const Epilogue<MODE, kDw> epilogue_w(a, live, mine, both, warp, lane);
         int n = 0;
         for (int i = pair; i < tiles.total; i += pairs) {
-            const auto t = tiles(i);
-            const int row0 = t.m * kPairTile + static_cast<int>(rank) * kHalf + epilogue.place;
-            if (t.begin == t.end) {                      // a sum of nothing
-                epilogue(row0, t.n, t.split, 0, [&](auto&& f) {
+            tiles(i, [&](auto kind, const Grid::At& t) {
+                constexpr int KIND = decltype(kind)::value;
+                const auto& epilogue = [&]() -> const auto& {
+                    if constexpr (KIND == kDw) return epilogue_w;
+                    else return epilogue_h;
+                }();
+                const int parts = epilogue.parts;
+                const int row0 = t.m * kPairTile + static_cast<int>(rank) * kHalf + epilogue.place;
+                if (t.begin == t.end) {                  // a sum of nothing
+                    epilogue(row0, t.n, t.split, 0, [&](auto&& f) {
 #pragma unroll 1
-                    for (int c = 0; c < parts; ++c) {
-                        float v[32] = {};
-                        f(c, v);
-                    }
-                });
-                continue;
-            }
-            const int slot = n % 2;
-            // (a wait that runs out: on with what is there, so that no warp waits for another)
-            wait(sh, sh.done[slot], (n / 2) % 2);
-            __syncwarp();
-            ++n;
-            fence_after_sync();
-            const uint32_t from = tmem + slot * kPairTile + 32 * epilogue.begin +
-                                  (static_cast<uint32_t>(epilogue.place) << 16);
-            epilogue(row0, t.n, t.split, slot, [&](auto&& f) {
-                auto release = [&] {                     // the tile's place may be taken
-                    fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive_in_cluster(in_cta(smem_address(&sh.taken[slot]), 0));
-                };
-                if constexpr (MODE == kDw) {             // (registers are short)
-                    if (parts == 0) release();
-#pragma unroll 1
-                    for (int c = 0; c < parts; ++c) {
-                        float v[32];
-                        tmem_load(v, from + 32 * c);
-                        tmem_load_wait(v);
-                        if (c + 1 == parts) release();
-                        f(c, v);
-                        __syncwarp();
-                    }
+                        for (int c = 0; c < parts; ++c) {
+                            float v[32] = {};
+                            f(c, v);
+                        }
+                    });
                     return;
                 }
-                // the next part is on its way while one is worked on
-                float v[2][32];
-                if (parts > 0) {
-                    tmem_load(v[0], from);
-                    tmem_load_wait(v[0]);
-                }
-                if (parts <= 1) release();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (c >= parts) break;
-                    if (c < 3 && c + 1 < parts) tmem_load(v[(c + 1) % 2], from + 32 * (c + 1));
-                    f(c, v[c % 2]);
-                    __syncwarp();
-                    if (c < 3 && c + 1 < parts) {
-                        tmem_load_wait(v[(c + 1) % 2]);
-                        if (c + 2 == parts) release();
+                const int slot = n % 2;
+                // (a wait that runs out: on with what is there, so that no warp waits for
+                // another)
+                wait(sh, sh.done[slot], (n / 2) % 2);
+                __syncwarp();
+                ++n;
+                fence_after_sync();
+                const uint32_t from = tmem + slot * kPairTile + 32 * epilogue.begin +
+                                      (static_cast<uint32_t>(epilogue.place) << 16);
+                epilogue(row0, t.n, t.split, slot, [&](auto&& f) {
+                    auto release = [&] {                 // the tile's place may be taken
+                        fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0)
+                            bar_arrive_in_cluster(in_cta(smem_address(&sh.taken[slot]), 0));
+                    };
+                    if constexpr (KIND == kDw) {         // (registers are short)
+                        if (parts == 0) release();
+#pragma unroll 1
+                        for (int c = 0; c < parts; ++c) {
+                            float v[32];
+                            tmem_load(v, from + 32 * c);
+                            tmem_load_wait(v);
+                            if (c + 1 == parts) release();
+                            f(c, v);
+                            __syncwarp();
+                        }
+                        return;
                     }
-                }
+                    // the next part is on its way while one is worked on
+                    float v[2][32];
+                    if (parts > 0) {
+                        tmem_load(v[0], from);
+                        tmem_load_wait(v[0]);
+                    }
+                    if (parts <= 1) release();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (c >= parts) break;
+                        if (c < 3 && c + 1 < parts) tmem_load(v[(c + 1) % 2], from + 32 * (c + 1));
+                        f(c, v[c % 2]);
+                        __syncwarp();
+                        if (c < 3 && c + 1 < parts) {
+                            tmem_load_wait(v[(c + 1) % 2]);
+                            if (c + 2 == parts) release();
+                        }
+                    }
+                });
             });
         }
-        if ((MODE == kDz || MODE == kDh) && lane == 0) bulk_wait();
+        if (MODE != kLoss && lane == 0) bulk_wait();
     }
     __syncwarp();
     __syncthreads();
@@ -845,22 +902,30 @@ head_join_kernel(const HeadCall c, const int32_t* counts, const int32_t* index,
     }
 }
 
-// The hidden states' gradient: the splits' sums of live tokens, zeros of the others; a warp
-// takes up to 512 columns of a row.
-template <bool WIDE>
-__global__ void __launch_bounds__(256)
+// The hidden states' gradient: the splits' sums of live tokens, zeros of the others.  512
+// columns of a row by a warp, or, where there are many splits, by the warps of a CTA, which
+// share them (MANY).
+constexpr int kFinishWarps = 8;
+
+template <bool WIDE, bool MANY>
+__global__ void __launch_bounds__(32 * kFinishWarps)
 head_finish_kernel(const int32_t* slot, const float* sums, int64_t rows, int32_t splits,
                    int64_t n_tokens, int32_t dim, int32_t sections, uint16_t* out,
                    int64_t stride) {
     constexpr int N = kCopyColumns / 128;
-    const int64_t id = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
+    __shared__ float4 shared[MANY ? kFinishWarps : 1][N][32];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t id = MANY ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kFinishWarps + warp;
     const int64_t t = id / sections;
     if (t >= n_tokens) return;
-    const int first = static_cast<int>(id - t * sections) * kCopyColumns + 4 * (threadIdx.x % 32);
+    const int first = static_cast<int>(id - t * sections) * kCopyColumns + 4 * lane;
     wait_for_launch_before();
     const int32_t j = slot[t];
     uint16_t* to = out + t * stride;
     float4 v[N];
+    auto add = [](float4& x, const float4& y) {
+        x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+    };
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (j >= 0) {
@@ -869,15 +934,24 @@ head_finish_kernel(const int32_t* slot, const float* sums, int64_t rows, int32_t
         const float* from =
             sums + (first / 32 * rows + j) * 32 + 4 * (first % 32 / 4 ^ (j & 7));
 #pragma unroll 4
-        for (int s = 0; s < splits; ++s) {
+        for (int s = MANY ? warp : 0; s < splits; s += MANY ? kFinishWarps : 1) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                if (first + 128 * i < dim) {
-                    const float4 w = *reinterpret_cast<const float4*>(
-                        from + (static_cast<int64_t>(s) * blocks + 4 * i) * rows * 32);
-                    v[i] = make_float4(v[i].x + w.x, v[i].y + w.y, v[i].z + w.z, v[i].w + w.w);
-                }
+                if (first + 128 * i < dim)
+                    add(v[i], *reinterpret_cast<const float4*>(
+                                  from + (static_cast<int64_t>(s) * blocks + 4 * i) * rows * 32));
             }
+        }
+    }
+    if constexpr (MANY) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) shared[warp][i][lane] = v[i];
+        __syncthreads();
+        if (warp != 0) return;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+            for (int w = 1; w < kFinishWarps; ++w) add(v[i], shared[w][i][lane]);
         }
     }
 #pragma unroll
@@ -1007,8 +1081,8 @@ cudaError_t dz_map(CUtensorMap* map, const HeadArgs& a, int box_rows) {
 }
 
 template <int MODE>
-cudaError_t launch_product(const CUtensorMap& map_a, const CUtensorMap& map_b, const HeadArgs& a,
-                           int64_t tiles, cudaStream_t stream) {
+cudaError_t launch_product(const HeadMaps& maps, const HeadArgs& a, int64_t tiles,
+                           cudaStream_t stream) {
     static std::once_flag once[64];
     static cudaError_t set[64];
     static int fit[64];                                  // pairs at a time
@@ -1036,7 +1110,7 @@ cudaError_t launch_product(const CUtensorMap& map_a, const CUtensorMap& map_b, c
     if (set[dev] != cudaSuccess) return set[dev];
     const int64_t pairs = tiles < fit[dev] ? tiles : fit[dev];
     return launch_after(head_kernel<MODE>, static_cast<unsigned>(2 * pairs), kHeadThreads, kHeadSmem,
-                        stream, map_a, map_b, a);
+                        stream, maps, a);
 }
 
 HeadArgs product_args(const HeadCall& c, const HeadPlan& p, int64_t first) {
@@ -1064,22 +1138,21 @@ HeadArgs product_args(const HeadCall& c, const HeadPlan& p, int64_t first) {
 int64_t whole(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 int64_t tiles_of(int64_t x, int64_t width) { return (x + width - 1) / width; }
 
-// Clock cycles of a launch that takes m rows of tiles, n columns and `splits` parts of the
-// sum, each of `steps` steps, when a tile is `width` columns wide: rounds of tiles over the
-// GPU's pairs, in each the steps (256 + width, what the operands take on their way), the
-// results' way out and what comes before.  Measured: 12 steps of width 256 7500 to 8400
+// Clock cycles of a tile of `steps` steps and `width` columns: the steps (256 + width, what
+// the operands take on their way), the result's way out and what comes before; and of a
+// launch of m rows of tiles, n columns, in rounds over the GPU's pairs.  Measured: 12 steps of width 256 7500 to 8400
 // cycles, 64 steps 36000 to 40000.
-double launch_cost(int64_t m, int64_t n, int64_t steps, int64_t splits, int width) {
-    const int64_t pairs = device_sms() / 2 > 0 ? device_sms() / 2 : 1;
-    const int64_t rounds = (m * tiles_of(n, width) * splits + pairs - 1) / pairs;
-    return static_cast<double>(rounds) *
-           ((256.0 + width) * static_cast<double>(steps) / splits + 12.0 * width + 800.0);
+double tile_cost(double steps, int width) { return (256.0 + width) * steps + 12.0 * width + 800.0; }
+int64_t pairs_of_gpu() { return device_sms() / 2 > 0 ? device_sms() / 2 : 1; }
+double launch_cost(int64_t m, int64_t n, int64_t steps, int width) {
+    const int64_t rounds = (m * tiles_of(n, width) + pairs_of_gpu() - 1) / pairs_of_gpu();
+    return static_cast<double>(rounds) * tile_cost(static_cast<double>(steps), width);
 }
 
 int best_width(int64_t m, int64_t n, int64_t steps, int unit) {
     int best = kPairTile;
     for (int w = kPairTile - unit; w >= unit; w -= unit) {
-        if (launch_cost(m, n, steps, 1, w) < 0.98 * launch_cost(m, n, steps, 1, best)) best = w;
+        if (launch_cost(m, n, steps, w) < 0.98 * launch_cost(m, n, steps, best)) best = w;
     }
     return best;
 }
@@ -1103,16 +1176,23 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back) {
     const int64_t steps_dim = tiles_of(dim, kTileK);
     if (back) {
         p.width_z = best_width(m, p.piece < vocab ? p.piece : vocab, steps_dim, 64);
-        p.width_w = best_width(tiles_of(p.piece, kPairTile), dim, tiles_of(n_tokens, kTileK), 32);
-        // the sum over a piece in as many parts as keep the GPU's pairs busy; every part is
-        // written, and read again in the end, at 6 TB/s and 1.9 GHz
-        const int64_t steps = tiles_of(p.piece, kTileK);
+        const int64_t steps = tiles_of(p.piece, kTileK), steps_w = tiles_of(n_tokens, kTileK);
+        p.width_w = best_width(tiles_of(p.piece, kPairTile), dim, steps_w, 32);
+        // The sum over a piece in as many parts as keep the GPU's pairs busy: the launch takes
+        // the tiles' average on a pair, half a tile more at its end, and every part is written,
+        // and read again in the end, at 6 TB/s and 1.9 GHz.
+        const double tile_w = tile_cost(steps_w, p.width_w);
+        const double all_w =
+            tile_w * tiles_of(p.piece, kPairTile) * tiles_of(dim, p.width_w) / pairs_of_gpu();
         const double way = 8.0 * p.rows * whole(dim, 32) / 6e12 * 1.9e9;
         double best = 0.0;
-        for (int64_t s = 1;
-             s <= 64 && (s == 1 || (s * 4 <= steps && s * p.rows * p.pitch * 4 <= kMost)); ++s) {
+        for (int64_t s : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 40, 48, 64}) {
+            if (s > 1 && (s * 4 > steps || s * p.rows * p.pitch * 4 > kMost)) break;
             for (int w = kPairTile; w >= 32; w -= 32) {
-                const double cost = launch_cost(m, dim, steps, s, w) + way * s;
+                const double tile = tile_cost(steps / static_cast<double>(s), w);
+                const double cost =
+                    tile * m * tiles_of(dim, w) * s / pairs_of_gpu() + all_w +
+                    0.5 * (tile > tile_w ? tile : tile_w) + way * s;
                 if ((s == 1 && w == kPairTile) || cost < 0.98 * best) {
                     best = cost;
                     p.splits = static_cast<int32_t>(s);
@@ -1183,13 +1263,13 @@ cudaError_t launch_head_loss(const HeadCall& c, const HeadPlan& p, int64_t first
                              cudaStream_t stream) {
     if (cudaError_t e = copy_piece(c, p, first, stream); e != cudaSuccess) return e;
     const bool as_they_are = head_rows_as_they_are(c);
-    CUtensorMap ma, mb;
-    if (cudaError_t e = as_they_are ? make_map(&ma, c.hidden, c.dim, c.n_tokens, c.hidden_stride, kHalf)
-                                    : make_map(&ma, at<uint16_t>(c, p.hidden), c.dim, p.rows, p.pitch,
+    HeadMaps maps{};
+    if (cudaError_t e = as_they_are ? make_map(&maps.a, c.hidden, c.dim, c.n_tokens, c.hidden_stride, kHalf)
+                                    : make_map(&maps.a, at<uint16_t>(c, p.hidden), c.dim, p.rows, p.pitch,
                                                kHalf);
         e != cudaSuccess)
         return e;
-    if (cudaError_t e = piece_map(&mb, c, p, first, p.width_z / 2); e != cudaSuccess) return e;
+    if (cudaError_t e = piece_map(&maps.b, c, p, first, p.width_z / 2); e != cudaSuccess) return e;
     HeadArgs a = product_args(c, p, first);
     a.width = p.width_z;
     a.part = static_cast<int32_t>(first / p.piece * p.parts_a_piece);
@@ -1199,7 +1279,7 @@ cudaError_t launch_head_loss(const HeadCall& c, const HeadPlan& p, int64_t first
         a.label64 = c.label64;
         a.n_rows = static_cast<int32_t>(c.n_tokens);
     }
-    return launch_product<kLoss>(ma, mb, a, p.rows / kPairTile * tiles_of(a.vocab, a.width), stream);
+    return launch_product<kLoss>(maps, a, p.rows / kPairTile * tiles_of(a.vocab, a.width), stream);
 }
 
 cudaError_t launch_head_join(const HeadCall& c, const HeadPlan& p, cudaStream_t stream) {
@@ -1213,49 +1293,49 @@ cudaError_t launch_head_join(const HeadCall& c, const HeadPlan& p, cudaStream_t 
 cudaError_t launch_head_dz(const HeadCall& c, const HeadPlan& p, int64_t first,
                            cudaStream_t stream) {
     if (cudaError_t e = copy_piece(c, p, first, stream); e != cudaSuccess) return e;
-    CUtensorMap ma, mb;
-    if (cudaError_t e = make_map(&ma, at<uint16_t>(c, p.hidden), c.dim, p.rows, p.pitch, kHalf);
+    HeadMaps maps{};
+    if (cudaError_t e = make_map(&maps.a, at<uint16_t>(c, p.hidden), c.dim, p.rows, p.pitch, kHalf);
         e != cudaSuccess)
         return e;
-    if (cudaError_t e = piece_map(&mb, c, p, first, p.width_z / 2); e != cudaSuccess) return e;
+    if (cudaError_t e = piece_map(&maps.b, c, p, first, p.width_z / 2); e != cudaSuccess) return e;
     HeadArgs a = product_args(c, p, first);
     a.width = p.width_z;
-    return launch_product<kDz>(ma, mb, a, p.rows / kPairTile * tiles_of(a.vocab, a.width), stream);
+    return launch_product<kDz>(maps, a, p.rows / kPairTile * tiles_of(a.vocab, a.width), stream);
 }
 
-cudaError_t launch_head_dh(const HeadCall& c, const HeadPlan& p, int64_t first,
-                           cudaStream_t stream) {
+cudaError_t launch_head_products(const HeadCall& c, const HeadPlan& p, int64_t first,
+                                 cudaStream_t stream) {
     HeadArgs a = product_args(c, p, first);
-    a.add = first > 0;
-    a.width = p.width_h;
-    CUtensorMap ma, mb;
-    if (cudaError_t e = dz_map(&ma, a, kHalf); e != cudaSuccess) return e;
-    if (cudaError_t e = piece_map(&mb, c, p, first, kTileK); e != cudaSuccess) return e;
-    return launch_product<kDh>(ma, mb, a, p.rows / kPairTile * tiles_of(c.dim, a.width) * p.splits,
-                               stream);
-}
-
-cudaError_t launch_head_dw(const HeadCall& c, const HeadPlan& p, int64_t first,
-                           cudaStream_t stream) {
-    HeadArgs a = product_args(c, p, first);
-    a.add = c.accumulate;
-    a.width = p.width_w;
+    a.want_h = c.grad_hidden != nullptr && c.n_tokens > 0;
+    a.want_w = c.grad_table != nullptr;
+    a.add_h = first > 0;
+    a.add_w = c.accumulate;
+    a.width_h = p.width_h;
+    a.width_w = p.width_w;
     a.wide = aligned_to(c.grad_table, 16) && c.dim % 8 == 0;
-    CUtensorMap ma, mb;
-    if (cudaError_t e = dz_map(&ma, a, kTileK); e != cudaSuccess) return e;
-    if (cudaError_t e = make_map(&mb, at<uint16_t>(c, p.hidden), c.dim, p.rows, p.pitch, kTileK);
+    HeadMaps maps{};
+    if (cudaError_t e = dz_map(&maps.a, a, kHalf); e != cudaSuccess) return e;
+    if (cudaError_t e = piece_map(&maps.b, c, p, first, kTileK); e != cudaSuccess) return e;
+    if (cudaError_t e = dz_map(&maps.aw, a, kTileK); e != cudaSuccess) return e;
+    if (cudaError_t e = make_map(&maps.bw, at<uint16_t>(c, p.hidden), c.dim, p.rows, p.pitch, kTileK);
         e != cudaSuccess)
         return e;
-    return launch_product<kDw>(ma, mb, a, tiles_of(a.vocab, kPairTile) * tiles_of(c.dim, a.width),
-                               stream);
+    const int64_t tiles =
+        (a.want_h ? p.rows / kPairTile * tiles_of(c.dim, a.width_h) * p.splits : 0) +
+        (a.want_w ? tiles_of(a.vocab, kPairTile) * tiles_of(c.dim, a.width_w) : 0);
+    return launch_product<kProducts>(maps, a, tiles, stream);
 }
 
 cudaError_t launch_head_finish(const HeadCall& c, const HeadPlan& p, cudaStream_t stream) {
     const int64_t sections = (c.dim + kCopyColumns - 1) / kCopyColumns;
-    const unsigned grid = static_cast<unsigned>((c.n_tokens * sections + 7) / 8);
     const bool wide = aligned_to(c.grad_hidden, 8) && c.grad_hidden_stride % 4 == 0;
-    return launch_after(wide ? head_finish_kernel<true> : head_finish_kernel<false>, grid, 256, 0,
-                        stream, at<int32_t>(c, p.slot), at<float>(c, p.sums), p.rows, p.splits,
+    const bool many = p.splits > 4;
+    const int64_t units = c.n_tokens * sections;
+    const unsigned grid =
+        static_cast<unsigned>(many ? units : (units + kFinishWarps - 1) / kFinishWarps);
+    const auto kernel = many ? (wide ? head_finish_kernel<true, true> : head_finish_kernel<false, true>)
+                             : (wide ? head_finish_kernel<true, false> : head_finish_kernel<false, false>);
+    return launch_after(kernel, grid, 32 * kFinishWarps, 0, stream, at<int32_t>(c, p.slot), at<float>(c, p.sums), p.rows, p.splits,
                         c.n_tokens, c.dim, sections, c.grad_hidden, c.grad_hidden_stride);
 }
 

@@ -53,14 +53,12 @@ cudaError_t launch_head_gather(const HeadCall& c, const HeadPlan& p, cudaStream_
 cudaError_t launch_head_loss(const HeadCall& c, const HeadPlan& p, int64_t first,
                              cudaStream_t stream);
 cudaError_t launch_head_join(const HeadCall& c, const HeadPlan& p, cudaStream_t stream);
-// backward: a piece's gradient of the logits, its share of the hidden states' gradient, the
-// piece of the table's gradient; then the hidden states' gradient
+// backward: a piece's gradient of the logits, its share of the hidden states' gradient with
+// the piece of the table's gradient; then the hidden states' gradient
 cudaError_t launch_head_dz(const HeadCall& c, const HeadPlan& p, int64_t first,
                            cudaStream_t stream);
-cudaError_t launch_head_dh(const HeadCall& c, const HeadPlan& p, int64_t first,
-                           cudaStream_t stream);
-cudaError_t launch_head_dw(const HeadCall& c, const HeadPlan& p, int64_t first,
-                           cudaStream_t stream);
+cudaError_t launch_head_products(const HeadCall& c, const HeadPlan& p, int64_t first,
+                                 cudaStream_t stream);
 cudaError_t launch_head_finish(const HeadCall& c, const HeadPlan& p, cudaStream_t stream);
 
 // Timeouts of this file's kernels, joined to the library's device status.

@@ -703,8 +703,7 @@ ZERO_API int zero_head_loss_grad(const uint16_t* hidden, int64_t n_tokens, int64
     if (accumulate != 0 && accumulate != 1)
         return fail(ZERO_ERR_INVALID_ARG, "accumulate = %d (0 or 1)", accumulate);
     const bool rows = grad_hidden != nullptr && n_tokens > 0;
-    const bool columns = grad_table != nullptr && (n_tokens > 0 || !accumulate);
-    if (!rows && !columns) return ok();
+    if (!rows && (grad_table == nullptr || (n_tokens == 0 && accumulate))) return ok();
     const zf::HeadPlan p = zf::head_plan(n_tokens, vocab, dim, true);
     if (int rc = check_workspace(workspace, workspace_bytes, p.bytes)) return rc;
     c.lse = const_cast<float*>(lse);
@@ -723,16 +722,9 @@ ZERO_API int zero_head_loss_grad(const uint16_t* hidden, int64_t n_tokens, int64
         if (int rc = cuda_call("head logits' gradient launch",
                                [&] { return zf::launch_head_dz(c, p, first, s); }))
             return rc;
-        if (rows) {
-            if (int rc = cuda_call("head hidden gradient launch",
-                                   [&] { return zf::launch_head_dh(c, p, first, s); }))
-                return rc;
-        }
-        if (columns) {
-            if (int rc = cuda_call("head table gradient launch",
-                                   [&] { return zf::launch_head_dw(c, p, first, s); }))
-                return rc;
-        }
+        if (int rc = cuda_call("head gradients launch",
+                               [&] { return zf::launch_head_products(c, p, first, s); }))
+            return rc;
     }
     if (!rows) return ok();
     return cuda_call("head gradient rows launch",

@@ -299,8 +299,8 @@ def test_capture_into_a_graph():
 
 
 @pytest.mark.parametrize("label", ["head rows", "head gather", "head loss launch", "head join",
-                                   "head logits' gradient", "head hidden gradient",
-                                   "head table gradient", "head gradient rows"])
+                                   "head logits' gradient", "head gradients launch",
+                                   "head gradient rows"])
 def test_injected_failure_is_reported_and_a_retry_is_clean(monkeypatch, label):
     call, got = _mixed_calls()
     call()
