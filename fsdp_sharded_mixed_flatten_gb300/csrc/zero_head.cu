@@ -381,13 +381,27 @@ struct Epilogue {
                         }
                     }
                 } else {
-                    uint16_t* to = a.grad_table + static_cast<int64_t>(row0) * a.dim + first + lane;
-                    const int rows = min(32, a.vocab - row0);
-                    const bool one = first + lane < end, two = first + 32 + lane < end;
-#pragma unroll 8
-                    for (int r = 0; r < rows; ++r) {
-                        if (one) to[static_cast<int64_t>(r) * a.dim] = stage.value16(r, lane);
-                        if (two) to[static_cast<int64_t>(r) * a.dim + 32] = stage.value16(r, 32 + lane);
+                    // Rows off the 16-byte grid: a row's whole aligned words, shifted into
+                    // place, by 8 lanes, and the values before and after them one by one.
+                    const int wide = end - first, rows = min(32, a.vocab - row0);
+                    uint16_t* const to = a.grad_table + static_cast<int64_t>(row0) * a.dim + first;
+                    auto head_of = [&](const uint16_t* p) {
+                        return min(static_cast<int>(-(reinterpret_cast<uintptr_t>(p) / 2) & 7), wide);
+                    };
+#pragma unroll 4
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = lane / 8 + 4 * i, w = lane % 8;
+                        if (r >= rows) continue;
+                        uint16_t* const p = to + static_cast<int64_t>(r) * a.dim;
+                        const int head = head_of(p), tail = head + (wide - head) / 8 * 8;
+                        if (head + 8 * w < tail)
+                            *reinterpret_cast<uint4*>(p + head + 8 * w) =
+                                shifted<uint16_t>(stage.word(r, w), stage.word(r, (w + 1) & 7), 2 * head);
+#pragma unroll
+                        for (int e = w; e < 16; e += 8) {
+                            const int at = e < head ? e : tail + e - head;
+                            if (at < wide) p[at] = stage.value16(r, at);
+                        }
                     }
                 }
                 __syncwarp();
@@ -740,6 +754,9 @@ head_rows_kernel(const HeadCall c, const HeadRows r, bool back) {
     }
 }
 
+constexpr int kCopyWarps = 8;
+constexpr int kCopyColumns = 512;
+
 // 16 bytes of a row that starts anywhere, from the aligned words that hold them (of the
 // row's first and last word bytes beside it are read, and not used).  All 16 are the row's.
 __device__ __forceinline__ uint4 row_word(const uint16_t* row, int column) {
@@ -750,6 +767,34 @@ __device__ __forceinline__ uint4 row_word(const uint16_t* row, int column) {
     return shifted<uint16_t>(lo, *reinterpret_cast<const uint4*>(p + 16), mis);
 }
 
+// A lane's columns of a row: 8 from `first` on, and each 256 further.
+__device__ __forceinline__ void copy_columns(const uint16_t* in, uint16_t* out, int first, int dim) {
+    uint4 v[kCopyColumns / 256];
+#pragma unroll
+    for (int i = 0; i < kCopyColumns / 256; ++i) {
+        if (first + 256 * i + 8 <= dim) v[i] = row_word(in, first + 256 * i);
+    }
+#pragma unroll
+    for (int i = 0; i < kCopyColumns / 256; ++i) {
+        const int c = first + 256 * i;
+        if (c + 8 <= dim) {
+            *reinterpret_cast<uint4*>(out + c) = v[i];
+        } else {
+            for (int e = c; e < dim; ++e) out[e] = in[e];
+        }
+    }
+}
+
+// Rows to copy beside other work: `count` rows of dim, side by side.
+struct HeadCopy {
+    const uint16_t* from;
+    uint16_t* to;
+    int64_t count;
+    int64_t pitch;
+    int32_t dim;
+    int32_t sections;
+};
+
 // The same and the copy of the live tokens' rows in one launch, where tokens are few: a CTA
 // has 8 of them, a warp each, and counts all by itself.
 constexpr int64_t kFewTokens = 8192;
@@ -757,7 +802,20 @@ constexpr int kPrepareThreads = 256;
 constexpr int kPrepareTokens = kPrepareThreads / 32;
 
 __global__ void __launch_bounds__(kPrepareThreads)
-head_prepare_kernel(const HeadCall c, const HeadRows r, bool back) {
+head_prepare_kernel(const HeadCall c, const HeadRows r, const HeadCopy copy, unsigned own_ctas,
+                    bool back) {
+    if (blockIdx.x >= own_ctas) {                        // the first piece of the table
+        let_next_launch_begin();
+        const int64_t id =
+            static_cast<int64_t>(blockIdx.x - own_ctas) * kPrepareTokens + threadIdx.x / 32;
+        const int64_t row = id / copy.sections;
+        if (row < copy.count)
+            copy_columns(copy.from + row * copy.dim, copy.to + row * copy.pitch,
+                         static_cast<int>(id - row * copy.sections) * kCopyColumns +
+                             8 * (threadIdx.x % 32),
+                         copy.dim);
+        return;
+    }
     __shared__ int32_t before[kPrepareTokens], total[kPrepareTokens];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int n = static_cast<int>(c.n_tokens), base = blockIdx.x * kPrepareTokens;
@@ -806,7 +864,7 @@ head_prepare_kernel(const HeadCall c, const HeadRows r, bool back) {
     if (!back) return;
     // zeros up to whole tiles: the sums over tokens go that far
     const int rows = (all + kPairTile - 1) / kPairTile * kPairTile;
-    for (int z = all + t; z < rows; z += gridDim.x * kPrepareTokens) {
+    for (int z = all + t; z < rows; z += own_ctas * kPrepareTokens) {
         for (int col = 8 * lane; col < r.pitch; col += 256)
             *reinterpret_cast<uint4*>(r.hidden + z * r.pitch + col) = make_uint4(0, 0, 0, 0);
     }
@@ -814,9 +872,6 @@ head_prepare_kernel(const HeadCall c, const HeadRows r, bool back) {
 
 // Rows of bf16 to rows on 16-byte boundaries, `pitch` apart; a warp takes up to 512 columns
 // of a row.  With an index: the live tokens' rows, and zeros up to whole tiles.
-constexpr int kCopyWarps = 8;
-constexpr int kCopyColumns = 512;
-
 __global__ void __launch_bounds__(32 * kCopyWarps)
 head_copy_kernel(const uint16_t* from, int64_t stride, const int32_t* index, const int32_t* counts,
                  int64_t rows, int32_t dim, int32_t sections, uint16_t* to, int64_t pitch) {
@@ -839,20 +894,7 @@ head_copy_kernel(const uint16_t* from, int64_t stride, const int32_t* index, con
         return;
     }
     const uint16_t* in = from + (index == nullptr ? row : index[row]) * stride;
-    uint4 v[kCopyColumns / 256];
-#pragma unroll
-    for (int i = 0; i < kCopyColumns / 256; ++i) {
-        if (first + 256 * i + 8 <= dim) v[i] = row_word(in, first + 256 * i);
-    }
-#pragma unroll
-    for (int i = 0; i < kCopyColumns / 256; ++i) {
-        const int c = first + 256 * i;
-        if (c + 8 <= dim) {
-            *reinterpret_cast<uint4*>(out + c) = v[i];
-        } else {
-            for (int e = c; e < dim; ++e) out[e] = in[e];
-        }
-    }
+    copy_columns(in, out, first, dim);
 }
 
 // The tiles' maxima and sums of a row joined: a warp a row, in a fixed order.
@@ -1032,7 +1074,17 @@ T* at(const HeadCall& c, int64_t offset) {
     return reinterpret_cast<T*>(static_cast<char*>(c.workspace) + offset);
 }
 
-bool table_in_place(const HeadCall& c) { return aligned_to(c.table, 16) && c.dim % 8 == 0; }
+// Forward, one tile of tokens that TMA reaches: nothing is saved by leaving tokens out, and
+// what they hold stays in their rows (32 x 50257 x 768: 41 us with a launch for the rows).
+bool rows_as_they_are(const HeadCall& c) {
+    return c.loss != nullptr && c.n_tokens <= kPairTile && aligned_to(c.hidden, 16) &&
+           c.hidden_stride % 8 == 0 && c.hidden_stride < int64_t{1} << 32;
+}
+bool rows_in_one_launch(const HeadCall& c) {
+    return c.n_tokens > 0 && c.n_tokens <= kFewTokens && !rows_as_they_are(c);
+}
+
+bool table_in_place(const HeadCall& c) { return head_table_in_place(c); }
 
 int64_t piece_rows(const HeadCall& c, const HeadPlan& p, int64_t first) {
     return p.piece < c.vocab - first ? p.piece : c.vocab - first;
@@ -1056,8 +1108,9 @@ cudaError_t copy_rows(const uint16_t* from, int64_t stride, const int32_t* index
                         counts, rows, dim, sections, to, pitch);
 }
 
+// (The first piece's copy goes with the tokens' rows where those take one launch.)
 cudaError_t copy_piece(const HeadCall& c, const HeadPlan& p, int64_t first, cudaStream_t stream) {
-    if (table_in_place(c)) return cudaSuccess;
+    if (table_in_place(c) || (first == 0 && rows_in_one_launch(c))) return cudaSuccess;
     const int64_t rows = piece_rows(c, p, first);
     const uint16_t* from = c.table + first * c.dim;
     return copy_rows(from, c.dim, nullptr, nullptr, rows, c.dim, at<uint16_t>(c, p.table), p.pitch,
@@ -1161,7 +1214,8 @@ int best_width(int64_t m, int64_t n, int64_t steps, int unit) {
 
 // Pieces of the vocabulary whose gradient, and whose copy of the table where it is off the
 // 16-byte grid, take at most 512 MB each; as even as whole tiles allow.
-HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back) {
+// Forward, a table that is read in place is one piece.
+HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, bool in_place) {
     constexpr int64_t kMost = int64_t{512} << 20;
     HeadPlan p{};
     p.rows = whole(n_tokens < 1 ? 1 : n_tokens, kPairTile);
@@ -1170,6 +1224,7 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back) {
     const int64_t m = p.rows / kPairTile;
     int64_t most = kMost / per_row / kPairTile * kPairTile;
     if (most < kPairTile) most = kPairTile;
+    if (!back && in_place) most = whole(vocab, kPairTile);
     const int64_t pieces = (vocab + most - 1) / most;
     p.piece = whole((vocab + pieces - 1) / pieces, kPairTile);
     p.splits = 1;
@@ -1218,7 +1273,7 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back) {
     p.slot = place(4 * n);
     p.label = place(4 * n);
     p.hidden = place(2 * p.rows * p.pitch);
-    p.table = place(2 * p.piece * p.pitch);
+    p.table = place(!back && in_place ? 0 : 2 * p.piece * p.pitch);
     if (back) {
         p.lse = place(4 * n);
         p.grad = place(4 * n);
@@ -1232,21 +1287,29 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back) {
     return p;
 }
 
-// Forward, one tile of tokens that TMA reaches: nothing is saved by leaving tokens out, and
-// what they hold stays in their rows (32 x 50257 x 768: 41 us with a launch for the rows).
-bool head_rows_as_they_are(const HeadCall& c) {
-    return c.n_tokens <= kPairTile && aligned_to(c.hidden, 16) && c.hidden_stride % 8 == 0 &&
-           c.hidden_stride < int64_t{1} << 32;
-}
+bool head_table_in_place(const HeadCall& c) { return aligned_to(c.table, 16) && c.dim % 8 == 0; }
+
+bool head_rows_as_they_are(const HeadCall& c) { return rows_as_they_are(c); }
 
 cudaError_t launch_head_rows(const HeadCall& c, const HeadPlan& p, bool back, cudaStream_t stream) {
     const HeadRows r{at<int32_t>(c, p.counts), at<int32_t>(c, p.index),  at<int32_t>(c, p.slot),
                      at<int32_t>(c, p.label),  at<float>(c, p.lse),      at<float>(c, p.grad),
                      at<uint16_t>(c, p.hidden), p.pitch};
-    if (c.n_tokens > 0 && c.n_tokens <= kFewTokens) {
-        const unsigned grid =
+    if (rows_in_one_launch(c)) {
+        const unsigned own =
             static_cast<unsigned>((c.n_tokens + kPrepareTokens - 1) / kPrepareTokens);
-        head_prepare_kernel<<<grid, kPrepareThreads, 0, stream>>>(c, r, back);
+        HeadCopy copy{};
+        if (!table_in_place(c)) {
+            copy.from = c.table;
+            copy.to = at<uint16_t>(c, p.table);
+            copy.count = piece_rows(c, p, 0);
+            copy.pitch = p.pitch;
+            copy.dim = static_cast<int32_t>(c.dim);
+            copy.sections = static_cast<int32_t>((c.dim + kCopyColumns - 1) / kCopyColumns);
+        }
+        const unsigned grid =
+            own + static_cast<unsigned>((copy.count * copy.sections + kPrepareTokens - 1) / kPrepareTokens);
+        head_prepare_kernel<<<grid, kPrepareThreads, 0, stream>>>(c, r, copy, own, back);
         return cudaGetLastError();
     }
     head_rows_kernel<<<1, kRowThreads, 0, stream>>>(c, r, back);

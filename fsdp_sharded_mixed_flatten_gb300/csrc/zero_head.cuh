@@ -41,7 +41,10 @@ struct HeadPlan {
     int64_t counts, index, slot, label, lse, grad, hidden, table, parts, picked, dz, sums;
     int64_t bytes;
 };
-HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back);
+HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, bool in_place);
+
+// Whether TMA reaches the table where it is.
+bool head_table_in_place(const HeadCall& c);
 
 // Whether the forward pass takes all tokens as they lie, without the first two launches.
 bool head_rows_as_they_are(const HeadCall& c);

@@ -624,7 +624,10 @@ int head_call(zf::HeadCall& c, const uint16_t* hidden, int64_t n_tokens, int64_t
 int head_workspace(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, int64_t* bytes) {
     if (bytes == nullptr) return fail(ZERO_ERR_INVALID_ARG, "bytes is NULL");
     if (int rc = check_head(n_tokens, vocab, dim)) return rc;
-    *bytes = zf::head_plan(n_tokens, vocab, dim, back).bytes;
+    // wherever the table lies
+    const int64_t in_place = zf::head_plan(n_tokens, vocab, dim, back, true).bytes;
+    const int64_t copied = zf::head_plan(n_tokens, vocab, dim, back, false).bytes;
+    *bytes = in_place > copied ? in_place : copied;
     return ok();
 }
 
@@ -653,7 +656,7 @@ ZERO_API int zero_head_loss(const uint16_t* hidden, int64_t n_tokens, int64_t di
     }
     if (int rc = check_optional(lse, 4, "lse")) return rc;
     if (n_tokens == 0) return ok();
-    const zf::HeadPlan p = zf::head_plan(n_tokens, vocab, dim, false);
+    const zf::HeadPlan p = zf::head_plan(n_tokens, vocab, dim, false, zf::head_table_in_place(c));
     if (int rc = check_workspace(workspace, workspace_bytes, p.bytes)) return rc;
     c.loss = loss;
     c.lse = lse;
@@ -704,7 +707,7 @@ ZERO_API int zero_head_loss_grad(const uint16_t* hidden, int64_t n_tokens, int64
         return fail(ZERO_ERR_INVALID_ARG, "accumulate = %d (0 or 1)", accumulate);
     const bool rows = grad_hidden != nullptr && n_tokens > 0;
     if (!rows && (grad_table == nullptr || (n_tokens == 0 && accumulate))) return ok();
-    const zf::HeadPlan p = zf::head_plan(n_tokens, vocab, dim, true);
+    const zf::HeadPlan p = zf::head_plan(n_tokens, vocab, dim, true, false);
     if (int rc = check_workspace(workspace, workspace_bytes, p.bytes)) return rc;
     c.lse = const_cast<float*>(lse);
     c.grad_loss = grad_loss;
