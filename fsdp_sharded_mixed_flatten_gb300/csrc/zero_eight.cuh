@@ -65,6 +65,31 @@ struct alignas(16) Octet {
     T x[8];
 };
 
+__device__ __forceinline__ int off_16(const void* p) {
+    return static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16);
+}
+
+// Eight values from the aligned 16-byte words that hold them (one or two words more than
+// eight values are, of which bytes beside the row are not used).
+template <class T>
+__device__ __forceinline__ Octet<T> shifted_octet(const char* words, int by) {
+    constexpr int N = sizeof(Octet<T>) / 16;
+    uint4 w[N + 1];
+#pragma unroll
+    for (int i = 0; i <= N; ++i) w[i] = reinterpret_cast<const uint4*>(words)[i];
+    Octet<T> v;
+#pragma unroll
+    for (int i = 0; i < N; ++i) reinterpret_cast<uint4*>(&v)[i] = shifted<T>(w[i], w[i + 1], by);
+    return v;
+}
+
+__device__ __forceinline__ uint2 shifted_codes(uint2 lo, uint2 hi, int bytes) {
+    const uint64_t a = static_cast<uint64_t>(lo.y) << 32 | lo.x;
+    const uint64_t b = static_cast<uint64_t>(hi.y) << 32 | hi.x;
+    const uint64_t v = bytes == 0 ? a : a >> (8 * bytes) | b << (64 - 8 * bytes);
+    return make_uint2(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32));
+}
+
 // A thread's K octets of a row's columns.
 //   WIDE   octet k holds columns 8 (k threads + t) ... + 7, reached by 16-byte words (8 of
 //          codes); half a warp holds a block of 128
@@ -123,36 +148,76 @@ struct Octets {
             w[e] = p == nullptr || !ok(k, e) ? 1.0f : ld_param(p, f32, at(k, e));
     }
 
+    // The same, and codes, of rows off the 16-byte grid (8-byte grid): aligned words are loaded
+    // and shifted into place, and codes stored after lanes have handed the next one what lies
+    // in its word.  (For the octets' mapping.)
+    template <class T>
+    __device__ __forceinline__ Octet<T> load_any(const T* row, int k) const {
+        const T* const p = row + at(k, 0);
+        const int mis = off_16(row);
+        if (at(k, 7) >= dim || mis == 0) return load<T>(row, k);
+        return shifted_octet<T>(reinterpret_cast<const char*>(p) - mis, mis);
+    }
+    __device__ __forceinline__ void store_eight_any(uint8_t* row, float* scales, int k,
+                                                    const float (&y)[8]) const {
+        uint32_t w[2];
+        const uint32_t s = codes_of(w, y);
+        const int c = at(k, 0), n = min(max(dim - c, 0), 8), rest = dim - c;
+        if (c < dim && c % kEightBlock == 0) scales[c / kEightBlock] = __uint_as_float(s << 23);
+        uint8_t* const p = row + c;
+        const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(row) % 8), head = (8 - mis) % 8;
+        const int lane = threadIdx.x % 32;
+        const uint2 next = make_uint2(__shfl_down_sync(0xFFFFFFFFu, w[0], 1),
+                                      __shfl_down_sync(0xFFFFFFFFu, w[1], 1));
+        // no whole word (with the next lane), and the lane before left this one's first codes
+        const bool last = rest < 8 + head || (mis != 0 && lane == 31);
+        const bool alone = lane == 0 || rest < head;
+        if (!last)
+            *reinterpret_cast<uint2*>(p + head) = shifted_codes(make_uint2(w[0], w[1]), next, head);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (e < n && (e < head ? alone : last))
+                p[e] = static_cast<uint8_t>(w[e / 4] >> (8 * (e % 4)));
+        }
+    }
+
+    // An octet's codes in the block of half a warp's; the scale's exponent field.
+    __device__ __forceinline__ static uint32_t codes_of(uint32_t (&w)[2], const float (&y)[8]) {
+        // (the larger of a number and NaN is the number)
+        float m = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        uint32_t s = eight_exponent(m);
+        if (__any_sync(0xFFFFFFFFu, s >= kEightTop)) {
+            m = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_magnitude(y[e]));
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            s = eight_exponent(m);
+            const float inverse = __uint_as_float((254 - s) << 23);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                w[i] = eight_codes_rare(y[4 * i], y[4 * i + 1], inverse, s == kEightTop) |
+                       eight_codes_rare(y[4 * i + 2], y[4 * i + 3], inverse, s == kEightTop)
+                           << 16;
+        } else {
+            const float inverse = __uint_as_float((254 - s) << 23);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                w[i] = eight_codes(y[4 * i], y[4 * i + 1], inverse) |
+                       eight_codes(y[4 * i + 2], y[4 * i + 3], inverse) << 16;
+        }
+        return s;
+    }
+
     __device__ __forceinline__ void store_eight(uint8_t* row, float* scales, int k,
                                                 const float (&y)[8]) const {
         if constexpr (WIDE) {
-            // (the larger of a number and NaN is the number)
-            float m = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            uint32_t s = eight_exponent(m), w[2];
-            if (__any_sync(0xFFFFFFFFu, s >= kEightTop)) {
-                m = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_magnitude(y[e]));
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                s = eight_exponent(m);
-                const float inverse = __uint_as_float((254 - s) << 23);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    w[i] = eight_codes_rare(y[4 * i], y[4 * i + 1], inverse, s == kEightTop) |
-                           eight_codes_rare(y[4 * i + 2], y[4 * i + 3], inverse, s == kEightTop)
-                               << 16;
-            } else {
-                const float inverse = __uint_as_float((254 - s) << 23);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    w[i] = eight_codes(y[4 * i], y[4 * i + 1], inverse) |
-                           eight_codes(y[4 * i + 2], y[4 * i + 3], inverse) << 16;
-            }
+            uint32_t w[2];
+            const uint32_t s = codes_of(w, y);
             const int c = at(k, 0);
             if (c + 7 < dim) {
                 *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
@@ -227,5 +292,15 @@ struct Octets {
         }
     }
 };
+
+__device__ __forceinline__ void values_of(float (&y)[8], uint2 codes, float scale) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        const uint32_t w = e < 4 ? codes.x : codes.y;
+        const float2 v = eight_values((w >> (8 * (e % 4))) & 0xFFFFu, scale);
+        y[e] = v.x;
+        y[e + 1] = v.y;
+    }
+}
 
 }  // namespace zf

@@ -208,8 +208,7 @@ rms_norm_grad_kernel(const __grid_constant__ RmsArgs a) {
     }
 }
 
-// The same through shared memory, for whole octets on 16-byte boundaries: every group has
-// a ring of slots, one row's arrays each, that its first thread fills by bulk copies, so
+// The same through shared memory: every group has a ring of slots, one row's arrays each, that its first thread fills by bulk copies, so
 // that several rows a group are on their way whatever the registers hold.  A slot is
 // filled again when the group's next exchange shows that all have done with it.
 // Threads of a CTA at most: more where a thread has one octet and few registers (forward of
@@ -258,27 +257,54 @@ __device__ __forceinline__ Octet<T> octet_at(const char* p) {
     return *reinterpret_cast<const Octet<T>*>(p);
 }
 
-__device__ __forceinline__ void values_of(float (&y)[8], uint2 codes, float scale) {
+// A row's array in a slot: the aligned words that hold it, which start up to 15 bytes before
+// (WIDE: rows on the 16-byte grid, of whole octets).
+template <bool WIDE, class T>
+__device__ __forceinline__ uint32_t row_bytes(const T* row, int dim) {
+    const int bytes = dim * static_cast<int>(sizeof(T));
+    return WIDE ? bytes : (off_16(row) + bytes + 15) / 16 * 16;
+}
+// ... of an array of rows at most
+__host__ __device__ constexpr int64_t row_room(int64_t dim, int64_t elem, bool wide) {
+    return wide ? dim * elem : (dim * elem + 15) / 16 * 16 + 16;
+}
+template <bool WIDE, class T>
+__device__ __forceinline__ void fetch_row(uint32_t to, const T* row, int dim, uint32_t bar) {
+    tile::bulk_load(to, reinterpret_cast<const char*>(row) - (WIDE ? 0 : off_16(row)),
+                    row_bytes<WIDE>(row, dim), bar);
+}
+// This thread's values of octet k of it; zeros where there are no columns, but for WIDE,
+// where those are some of the row's.
+template <class T, bool WIDE, int K>
+__device__ __forceinline__ Octet<T> octet_of(const char* array, int mis, const Octets<WIDE, K>& c,
+                                             int k) {
+    if constexpr (WIDE) {
+        return octet_at<T>(array + (c.at(k, 0) < c.dim ? c.at(k, 0) : 0) * sizeof(T));
+    } else {
+        Octet<T> v{};
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-        const uint32_t w = e < 4 ? codes.x : codes.y;
-        const float2 v = eight_values((w >> (8 * (e % 4))) & 0xFFFFu, scale);
-        y[e] = v.x;
-        y[e + 1] = v.y;
+        for (int e = 0; e < 8; ++e) {
+            if (c.ok(k, e)) v.x[e] = reinterpret_cast<const T*>(array + mis)[c.at(k, e)];
+        }
+        return v;
     }
 }
 
 // The weight: this thread's octets in registers, or, where there are four of them, all of
 // it in shared memory as it is.
-template <int K>
+template <bool WIDE, int K>
 struct Weight {
     float held[K <= 2 ? K : 1][8];
     const char* at;
     bool f32;
-    __device__ __forceinline__ void octet(float (&w)[8], int k, int column) const {
+    __device__ __forceinline__ void octet(float (&w)[8], int k, const Octets<WIDE, K>& c) const {
+        const int column = WIDE && c.at(k, 0) < c.dim ? c.at(k, 0) : 0;
         if constexpr (K <= 2) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[e] = held[k][e];
+        } else if constexpr (!WIDE) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = c.ok(k, e) ? ld_param(at, f32, c.at(k, e)) : 1.0f;
         } else if (f32) {
             const Octet<float> v = octet_at<float>(at + 4 * column);
 #pragma unroll
@@ -295,10 +321,10 @@ struct Weight {
 __host__ __device__ constexpr int weight_bytes(int k, bool f32) { return k <= 2 ? 0 : f32 ? 4 : 2; }
 
 // Sets up the CTA's rings, and the weight after them.
-template <int K>
+template <bool WIDE, int K>
 __device__ __forceinline__ RowsRing rows_begin(const RmsArgs& a, const RmsGroup& g,
-                                               const Octets<true, K>& c, char* dyn,
-                                               Weight<K>& weight, int* stop) {
+                                               const Octets<WIDE, K>& c, char* dyn,
+                                               Weight<WIDE, K>& weight, int* stop) {
     RowsRing r;
     r.slots = a.slots;
     r.slot_bytes = a.slot_bytes;
@@ -306,8 +332,8 @@ __device__ __forceinline__ RowsRing rows_begin(const RmsArgs& a, const RmsGroup&
     char* after = dyn + g.per_cta * a.slots * a.slot_bytes;
     weight.at = after;
     weight.f32 = a.weight != nullptr && a.param_f32;
-    // dim is a multiple of 8
-    r.bars = tile::smem_address(after + weight_bytes(K, weight.f32) * a.dim) + g.index * a.slots * 8;
+    const int padded = (a.dim + 7) / 8 * 8;
+    r.bars = tile::smem_address(after + weight_bytes(K, weight.f32) * padded) + g.index * a.slots * 8;
     r.at = 0;
     r.phase = 0;
     r.stop = stop;
@@ -339,6 +365,8 @@ __device__ __forceinline__ void rows_end(const int* stop) {
     }
 }
 
+// (Rows off the 16-byte grid go straight to registers: 8192 x 4001 bf16 60 us, through shared
+// memory by single elements 62, with the sum in 8 bits 79 / 88.)
 template <class T, int K>
 __global__ void __launch_bounds__(rows_threads(K, sizeof(T), false), 1)
 rms_rows_kernel(const __grid_constant__ RmsArgs a) {
@@ -349,19 +377,23 @@ rms_rows_kernel(const __grid_constant__ RmsArgs a) {
     const RmsGroup g(a.group_threads);
     const Octets<true, K> c(g.t, g.threads, a.dim);
     const float inv_d = 1.0f / static_cast<float>(a.dim);
-    Weight<K> weight;
+    Weight<true, K> weight;
     RowsRing ring = rows_begin(a, g, c, dyn, weight, &stop);
     const int64_t step = static_cast<int64_t>(gridDim.x) * g.per_cta;
     int64_t row = static_cast<int64_t>(blockIdx.x) * g.per_cta + g.index;
-    const uint32_t bytes = a.dim * sizeof(T);
+    const uint32_t second = row_room(a.dim, sizeof(T), true);
+    auto x_row = [&](int64_t at) { return static_cast<const T*>(a.x) + at * a.x_stride; };
+    auto residual_row = [&](int64_t at) {
+        return static_cast<const T*>(a.residual) + at * a.residual_stride;
+    };
     auto fill = [&](int64_t at, int s) {
         if (at >= a.n_rows) return;
         const uint32_t to = tile::smem_address(ring.base + s * ring.slot_bytes), bar = ring.bar(s);
-        tile::bar_expect(bar, a.residual != nullptr ? 2 * bytes : bytes);
-        tile::bulk_load(to, static_cast<const T*>(a.x) + at * a.x_stride, bytes, bar);
-        if (a.residual != nullptr)
-            tile::bulk_load(to + bytes,
-                            static_cast<const T*>(a.residual) + at * a.residual_stride, bytes, bar);
+        const bool two = a.residual != nullptr;
+        tile::bar_expect(bar, row_bytes<true>(x_row(at), a.dim) +
+                                  (two ? row_bytes<true>(residual_row(at), a.dim) : 0));
+        fetch_row<true>(to, x_row(at), a.dim, bar);
+        if (two) fetch_row<true>(to + second, residual_row(at), a.dim, bar);
     };
     if (g.t == 0) {
         for (int s = 0; s < ring.slots; ++s) fill(row + s * step, s);
@@ -373,11 +405,9 @@ rms_rows_kernel(const __grid_constant__ RmsArgs a) {
         float q = 0.0f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const bool in = c.at(k, 0) < a.dim;
-            const char* place = from + (in ? c.at(k, 0) : 0) * sizeof(T);
-            const Octet<T> x = octet_at<T>(place);
+            const Octet<T> x = octet_of<T>(from, 0, c, k);
             if (a.residual != nullptr) {
-                const Octet<T> r = octet_at<T>(place + bytes);
+                const Octet<T> r = octet_of<T>(from + second, 0, c, k);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s[k][e] = __fadd_rn(widen<T>(x.x[e]), widen<T>(r.x[e]));
             } else {
@@ -386,7 +416,7 @@ rms_rows_kernel(const __grid_constant__ RmsArgs a) {
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                if (!in) s[k][e] = 0.0f;
+                if (c.at(k, 0) >= a.dim) s[k][e] = 0.0f;
                 q = __fmaf_rn(s[k][e], s[k][e], q);
             }
         }
@@ -409,9 +439,8 @@ rms_rows_kernel(const __grid_constant__ RmsArgs a) {
         }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int col = c.at(k, 0) < a.dim ? c.at(k, 0) : 0;
             float w[8], y[8];
-            weight.octet(w, k, col);
+            weight.octet(w, k, c);
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = s[k][e] * r * w[e];
             if (a.out != nullptr)
@@ -424,7 +453,7 @@ rms_rows_kernel(const __grid_constant__ RmsArgs a) {
     rows_end(&stop);
 }
 
-template <class T, int K, bool EIGHT>
+template <class T, int K, bool WIDE, bool EIGHT>
 __global__ void __launch_bounds__(rows_threads(K, sizeof(T), true), 1)
 rms_rows_grad_kernel(const __grid_constant__ RmsArgs a) {
     // a row's values stay in registers as they come; four octets of them do not fit (held
@@ -436,29 +465,35 @@ rms_rows_grad_kernel(const __grid_constant__ RmsArgs a) {
     __shared__ int stop;
     int half = 0;
     const RmsGroup g(a.group_threads);
-    const Octets<true, K> c(g.t, g.threads, a.dim);
+    const Octets<WIDE, K> c(g.t, g.threads, a.dim);
     const float inv_d = 1.0f / static_cast<float>(a.dim);
-    Weight<K> weight;
+    Weight<WIDE, K> weight;
     RowsRing ring = rows_begin(a, g, c, dyn, weight, &stop);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t step = static_cast<int64_t>(gridDim.x) * g.per_cta;
     int64_t row = static_cast<int64_t>(blockIdx.x) * g.per_cta + g.index;
-    const uint32_t bytes = a.dim * sizeof(T), first = EIGHT ? a.dim : bytes;
+    const uint32_t first = row_room(a.dim, EIGHT ? 1 : sizeof(T), WIDE);
+    const uint32_t second = first + row_room(a.dim, sizeof(T), WIDE);
+    auto x_row = [&](int64_t at) { return static_cast<const T*>(a.x) + at * a.x_stride; };
+    auto codes_row = [&](int64_t at) { return a.total8 + at * a.total8_stride; };
+    auto dy_row = [&](int64_t at) {
+        return static_cast<const T*>(a.grad_out) + at * a.grad_out_stride;
+    };
+    auto dt_row = [&](int64_t at) {
+        return static_cast<const T*>(a.grad_total) + at * a.grad_total_stride;
+    };
     auto fill = [&](int64_t at, int s) {
         if (at >= a.n_rows) return;
         const uint32_t to = tile::smem_address(ring.base + s * ring.slot_bytes), bar = ring.bar(s);
-        tile::bar_expect(bar, first + (a.grad_total != nullptr ? 2 * bytes : bytes));
-        if constexpr (EIGHT) {
-            tile::bulk_load(to, a.total8 + at * a.total8_stride, first, bar);
-        } else {
-            tile::bulk_load(to, static_cast<const T*>(a.x) + at * a.x_stride, first, bar);
-        }
-        tile::bulk_load(to + first, static_cast<const T*>(a.grad_out) + at * a.grad_out_stride,
-                        bytes, bar);
-        if (a.grad_total != nullptr)
-            tile::bulk_load(to + first + bytes,
-                            static_cast<const T*>(a.grad_total) + at * a.grad_total_stride, bytes,
-                            bar);
+        const bool dt = a.grad_total != nullptr;
+        uint32_t bytes = row_bytes<WIDE>(dy_row(at), a.dim) + (dt ? row_bytes<WIDE>(dt_row(at), a.dim) : 0);
+        if constexpr (EIGHT) bytes += row_bytes<WIDE>(codes_row(at), a.dim);
+        else bytes += row_bytes<WIDE>(x_row(at), a.dim);
+        tile::bar_expect(bar, bytes);
+        if constexpr (EIGHT) fetch_row<WIDE>(to, codes_row(at), a.dim, bar);
+        else fetch_row<WIDE>(to, x_row(at), a.dim, bar);
+        fetch_row<WIDE>(to + first, dy_row(at), a.dim, bar);
+        if (dt) fetch_row<WIDE>(to + second, dt_row(at), a.dim, bar);
     };
     if (g.t == 0) {
         for (int s = 0; s < ring.slots; ++s) fill(row + s * step, s);
@@ -469,15 +504,21 @@ rms_rows_grad_kernel(const __grid_constant__ RmsArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[k][e] = 0.0f;
     }
-    float next_r = 0.0f, scale[K], next_scale[K];
+    constexpr int kScales = WIDE ? 1 : 2;
+    float next_r = 0.0f, scale[K][kScales], next_scale[K][kScales];
     auto load_small = [&](int64_t at) {
         if (at >= a.n_rows) return;
         next_r = a.rstd[at];
         if constexpr (EIGHT) {
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int col = c.at(k, 0) < a.dim ? c.at(k, 0) : 0;
-                next_scale[k] = a.total8_scales[at * a.blocks + col / kEightBlock];
+#pragma unroll
+                for (int b = 0; b < kScales; ++b) {
+                    // (the other mapping's octets are of two blocks)
+                    const int col = c.at(k, 4 * b);
+                    next_scale[k][b] =
+                        col < a.dim ? a.total8_scales[at * a.blocks + col / kEightBlock] : 0.0f;
+                }
             }
         }
     };
@@ -488,32 +529,45 @@ rms_rows_grad_kernel(const __grid_constant__ RmsArgs a) {
         const char* from = ring.here();
         const float r = next_r;
 #pragma unroll
-        for (int k = 0; k < K; ++k) scale[k] = next_scale[k];
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int b = 0; b < kScales; ++b) scale[k][b] = next_scale[k][b];
+        }
         load_small(row + step);
         struct Raw {
             Octet<T> x, dy, dt;
             uint2 codes;
         } raw[kHeld ? K : 1];
+        const int x_mis = WIDE ? 0 : EIGHT ? off_16(codes_row(row)) : off_16(x_row(row));
+        const int dy_mis = WIDE ? 0 : off_16(dy_row(row));
+        const int dt_mis = WIDE || a.grad_total == nullptr ? 0 : off_16(dt_row(row));
         auto fetch = [&](Raw& v, int k, bool with_dt) {
-            const int col = c.at(k, 0) < a.dim ? c.at(k, 0) : 0;
-            if constexpr (EIGHT) v.codes = *reinterpret_cast<const uint2*>(from + col);
-            else v.x = octet_at<T>(from + col * sizeof(T));
-            v.dy = octet_at<T>(from + first + col * sizeof(T));
+            if constexpr (!EIGHT) {
+                v.x = octet_of<T>(from, x_mis, c, k);
+            } else if constexpr (WIDE) {
+                v.codes = *reinterpret_cast<const uint2*>(from + (c.at(k, 0) < a.dim ? c.at(k, 0) : 0));
+            } else {
+                const Octet<uint8_t> q = octet_of<uint8_t>(from, x_mis, c, k);
+                v.codes = *reinterpret_cast<const uint2*>(&q);
+            }
+            v.dy = octet_of<T>(from + first, dy_mis, c, k);
             if (with_dt && a.grad_total != nullptr)
-                v.dt = octet_at<T>(from + first + bytes + col * sizeof(T));
+                v.dt = octet_of<T>(from + second, dt_mis, c, k);
         };
-        // xh, dy (0 where there is no octet) and the weight
+        // xh, dy (0 where there are no columns) and the weight
         auto open = [&](const Raw& v, int k, float (&xh)[8], float (&d)[8], float (&w)[8]) {
-            const bool in = c.at(k, 0) < a.dim;
             if constexpr (EIGHT) {
-                values_of(xh, v.codes, scale[k] * r);
+                values_of(xh, v.codes, 1.0f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) xh[e] *= scale[k][WIDE ? 0 : e / 4] * r;
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) xh[e] = widen<T>(v.x.x[e]) * r;
             }
-            weight.octet(w, k, in ? c.at(k, 0) : 0);
+            weight.octet(w, k, c);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = in ? widen<T>(v.dy.x[e]) : 0.0f;
+            for (int e = 0; e < 8; ++e)
+                d[e] = !WIDE || c.at(k, 0) < a.dim ? widen<T>(v.dy.x[e]) : 0.0f;
         };
         float q = 0.0f;
 #pragma unroll
@@ -564,10 +618,15 @@ rms_rows_grad_kernel(const __grid_constant__ RmsArgs a) {
     float* cols = reinterpret_cast<float*>(dyn);         // [groups][dim]
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        if (c.at(k, 0) < a.dim) {
+        if (WIDE && c.at(k, 0) < a.dim) {
             float4* to = reinterpret_cast<float4*>(cols + g.index * a.dim + c.at(k, 0));
             to[0] = make_float4(dw[k][0], dw[k][1], dw[k][2], dw[k][3]);
             to[1] = make_float4(dw[k][4], dw[k][5], dw[k][6], dw[k][7]);
+        } else if (!WIDE) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (c.ok(k, e)) cols[g.index * a.dim + c.at(k, e)] = dw[k][e];
+            }
         }
     }
     __syncthreads();
@@ -614,19 +673,27 @@ pack_kernel(const __grid_constant__ EightArgs a) {
     if (row >= a.n_rows) return;
     const int64_t first = (id - row * a.sections) * a.section;
     const int64_t rest = a.dim - first;
-    const Octets<WIDE, kPackOctets> c(threadIdx.x % 32, 32,
+    // rows off the 16-byte grid: bf16 by shifted words (8192 x 4001 42 us, by single elements
+    // 55), fp32 by single elements (5003 x 1501 13.9 us, by shifted words 15.5)
+    constexpr bool kShift = !WIDE && sizeof(T) == 2;
+    const Octets<WIDE || kShift, kPackOctets> c(threadIdx.x % 32, 32,
                                        static_cast<int>(rest < a.section ? rest : a.section));
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride + first;
     Octet<T> v[kPackOctets];
 #pragma unroll
-    for (int k = 0; k < kPackOctets; ++k) v[k] = c.template load<T>(x, k);
+    for (int k = 0; k < kPackOctets; ++k) {
+        if constexpr (kShift) v[k] = c.template load_any<T>(x, k);
+        else v[k] = c.template load<T>(x, k);
+    }
 #pragma unroll
     for (int k = 0; k < kPackOctets; ++k) {
         float f[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = widen<T>(v[k].x[e]);
-        c.store_eight(a.codes + row * a.codes_stride + first,
-                      a.scales + row * a.blocks + first / kEightBlock, k, f);
+        uint8_t* const codes = a.codes + row * a.codes_stride + first;
+        float* const scales = a.scales + row * a.blocks + first / kEightBlock;
+        if constexpr (kShift) c.store_eight_any(codes, scales, k, f);
+        else c.store_eight(codes, scales, k, f);
     }
 }
 
@@ -801,7 +868,7 @@ RowsShape rows_shape(int64_t dim, int elem, int64_t slot_bytes, bool weight_f32,
     s.k = dim <= (back ? 1024 : 2048) ? 1 : dim <= 8192 ? 2 : 4;
     s.group = static_cast<int>((dim + 256 * s.k - 1) / (256 * s.k) * 32);
     s.slot_bytes = slot_bytes;
-    const int64_t weight = weight_bytes(s.k, weight_f32) * dim;
+    const int64_t weight = weight_bytes(s.k, weight_f32) * ((dim + 7) / 8 * 8);
     const int64_t room = kRowsSmem - weight - 1024;
     s.per_cta = rows_threads(s.k, elem, back) / s.group;
     if (s.per_cta > 8) s.per_cta = 8;           // 16 hardware barriers a CTA
@@ -878,9 +945,9 @@ RmsPlan forward_plan(const RmsArgs& a, int act_bytes) {
              wide_rows(a.out, a.out_stride, act_bytes) && wide_codes(a.out8, a.out8_stride) &&
              wide_codes(a.total8, a.total8_stride);
     p.straight = rms_shape(a.dim);
-    p.through =
-        rows_shape(a.dim, act_bytes, static_cast<int64_t>(a.residual != nullptr ? 2 : 1) * act_bytes * a.dim,
-                   a.weight != nullptr && a.param_f32, false);
+    p.through = rows_shape(a.dim, act_bytes,
+                           (a.residual != nullptr ? 2 : 1) * row_room(a.dim, act_bytes, true),
+                           a.weight != nullptr && a.param_f32, false);
     p.rows = p.wide && a.dim % 8 == 0 && p.through.slots >= 2;
     p.grid = p.rows ? rms_grid({0, 0, p.through.per_cta}, a.n_rows, 1)
                     : rms_forward_grid(p.straight, a.n_rows);
@@ -896,23 +963,25 @@ RmsPlan backward_plan(const RmsArgs& a, int act_bytes) {
              wide_rows(a.grad_x, a.grad_x_stride, act_bytes) &&
              wide_rows(a.out, a.out_stride, act_bytes) && wide_codes(a.total8, a.total8_stride);
     p.straight = rms_shape(a.dim);
-    p.through = rows_shape(a.dim, act_bytes, static_cast<int64_t>(a.dim) *
-                                      ((a.grad_total != nullptr ? 2 : 1) * act_bytes +
-                                       (eight ? 1 : act_bytes)),
+    const bool grid = p.wide && a.dim % 8 == 0 &&
+                      (!eight || (a.dim % 16 == 0 && wide_rows(a.total8, a.total8_stride, 1)));
+    p.through = rows_shape(a.dim, act_bytes,
+                           (a.grad_total != nullptr ? 2 : 1) * row_room(a.dim, act_bytes, grid) +
+                               row_room(a.dim, eight ? 1 : act_bytes, grid),
                            a.weight != nullptr && a.param_f32, true);
-    p.rows = p.wide && a.dim % 8 == 0 && p.through.slots >= 2 &&
-             (!eight || (a.dim % 16 == 0 && wide_rows(a.total8, a.total8_stride, 1)));
+    p.rows = p.through.slots >= 2;
+    if (p.rows) p.wide = grid;
     p.grid = p.rows ? rms_grid({0, 0, p.through.per_cta}, a.n_rows, 1)
                     : rms_backward_grid(p.straight, a.n_rows);
     return p;
 }
 
-template <class T, int K, bool BACK, bool EIGHT>
+template <class T, int K, bool WIDE, bool BACK, bool EIGHT>
 cudaError_t launch_rows(const RmsArgs& a, const RmsPlan& p, cudaStream_t stream) {
     static std::once_flag once[64];
     static cudaError_t set[64];
     const auto kernel = [] {
-        if constexpr (BACK) return rms_rows_grad_kernel<T, K, EIGHT>;
+        if constexpr (BACK) return rms_rows_grad_kernel<T, K, WIDE, EIGHT>;
         else return rms_rows_kernel<T, K>;
     }();
     if (cudaError_t e = allow_smem(kernel, once, set); e != cudaSuccess) return e;
@@ -937,7 +1006,7 @@ cudaError_t launch_rms_norm(RmsArgs a, int act_bytes, cudaStream_t stream) {
         using T = decltype(t);
         return by_k(p.rows ? p.through.k : p.straight.k, [&](auto k) {
             constexpr int K = k.value;
-            if (p.rows) return launch_rows<T, K, false, false>(a, p, stream);
+            if (p.rows) return launch_rows<T, K, true, false, false>(a, p, stream);
             const unsigned grid = static_cast<unsigned>(p.grid);
             const int threads = p.straight.group * p.straight.per_cta;
             if (p.wide) rms_norm_kernel<T, K, true><<<grid, threads, 0, stream>>>(a);
@@ -957,8 +1026,11 @@ cudaError_t launch_rms_norm_grad(RmsArgs a, int act_bytes, cudaStream_t stream) 
         return by_k(p.rows ? p.through.k : p.straight.k, [&](auto k) {
             constexpr int K = k.value;
             if (p.rows)
-                return a.total8 != nullptr ? launch_rows<T, K, true, true>(a, p, stream)
-                                           : launch_rows<T, K, true, false>(a, p, stream);
+                return a.total8 != nullptr
+                           ? (p.wide ? launch_rows<T, K, true, true, true>(a, p, stream)
+                                     : launch_rows<T, K, false, true, true>(a, p, stream))
+                           : (p.wide ? launch_rows<T, K, true, true, false>(a, p, stream)
+                                     : launch_rows<T, K, false, true, false>(a, p, stream));
             const auto kernel = a.total8 != nullptr
                                     ? (p.wide ? rms_norm_grad_kernel<T, K, true, true>
                                               : rms_norm_grad_kernel<T, K, false, true>)
