@@ -45,6 +45,12 @@ constexpr int kEpilogueWarps = 8;
 constexpr size_t kHeadSmem = kStages * kStageBytes + kEpilogueWarps * kStagingBytes + 1024;
 constexpr int kHeadThreads = 64 + 32 * kEpilogueWarps;
 constexpr uint32_t kTmemColumns = 512;      // two tiles' results
+// Steps that are summed in tensor memory at a time where logits become a loss.  Sums there
+// are cut off, not rounded: a loss of 4096 columns summed in one go was 2.0e-6 of itself off,
+// four times as far as by plain fp32 products; in parts of 1536 columns that are added up in
+// registers 6.6e-7 (1024: 4.6e-7, 2048: 9.8e-7; the parts cost 4 to 6 % of the time).
+// The gradient's logits end in bf16 and are summed in one go.
+constexpr int kLossSteps = 24;
 constexpr uint64_t kHeadWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInvLog2e = static_cast<float>(1.0 / static_cast<double>(kLog2e));
@@ -53,7 +59,9 @@ constexpr float kInvLog2eLo = static_cast<float>(1.0 / static_cast<double>(kLog2
 
 // What a launch computes: rows' statistics, the logits' gradient, or both gradients that are
 // products of it: tiles of the hidden states' first, then of the table's.
-enum Mode { kLoss, kDz, kProducts };
+// (kLossLong: rows' statistics from logits that are summed in several parts.)
+enum Mode { kLoss, kLossLong, kDz, kProducts };
+__host__ __device__ constexpr bool is_loss(int mode) { return mode == kLoss || mode == kLossLong; }
 // What a tile of the last is.
 enum Kind { kDh, kDw };
 
@@ -268,7 +276,7 @@ struct Epilogue {
                                                Each&& each) const {
         const int column = n * width + 32 * begin;
         const int row = row0 + lane;
-        if constexpr (MODE == kLoss) {
+        if constexpr (is_loss(MODE)) {
             const int left = a.vocab - column;           // columns that exist
             const int mine = row < live ? label_in_piece(a, row) - column : -1;
             float top = -INFINITY, sum = 0.0f, z = 0.0f;
@@ -558,33 +566,38 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                                                        KIND == kDh   ? a.width_h
                                                        : KIND == kDw ? a.width_w
                                                                      : a.width);
-                    const int slot = n % 2;
-                    run = wait(sh, sh.taken[slot], (n / 2 + 1) % 2);
-                    if (!run) return;
-                    ++n;
-                    fence_after_sync();
-                    const uint32_t d = tmem + slot * kPairTile;
-                    for (int k = t.begin; k < t.end; ++k) {
-                        run = wait(sh, sh.full[s], phase);
+                    // a result in tensor memory: of all steps, or of some (kLossLong)
+                    for (int begin = t.begin; begin < t.end;) {
+                        const int end = MODE == kLossLong ? min(begin + kLossSteps, t.end) : t.end;
+                        const int slot = n % 2;
+                        run = wait(sh, sh.taken[slot], (n / 2 + 1) % 2);
                         if (!run) return;
+                        ++n;
                         fence_after_sync();
-                        const uint32_t at = ring + s * kStageBytes;
-                        const uint64_t da = operand(at, kAmn ? kChunkBytes : 16);
-                        const uint64_t db = operand(at + kOperandBytes, kBmn ? kChunkBytes : 16);
+                        const uint32_t d = tmem + slot * kPairTile;
+                        for (int k = begin; k < end; ++k) {
+                            run = wait(sh, sh.full[s], phase);
+                            if (!run) return;
+                            fence_after_sync();
+                            const uint32_t at = ring + s * kStageBytes;
+                            const uint64_t da = operand(at, kAmn ? kChunkBytes : 16);
+                            const uint64_t db = operand(at + kOperandBytes, kBmn ? kChunkBytes : 16);
 #pragma unroll
-                        for (int j = 0; j < kTileK / 16; ++j) {
-                            // 16 values along K: 32 bytes of a row, or 16 rows
-                            product(d, da + (kAmn ? 16 * 128 : 32) / 16 * j,
-                                    db + (kBmn ? 16 * 128 : 32) / 16 * j, form,
-                                    k != t.begin || j != 0);
+                            for (int j = 0; j < kTileK / 16; ++j) {
+                                // 16 values along K: 32 bytes of a row, or 16 rows
+                                product(d, da + (kAmn ? 16 * 128 : 32) / 16 * j,
+                                        db + (kBmn ? 16 * 128 : 32) / 16 * j, form,
+                                        k != begin || j != 0);
+                            }
+                            products_arrive(smem_address(&sh.empty[s]));
+                            if (++s == kStages) {
+                                s = 0;
+                                phase ^= 1;
+                            }
                         }
-                        products_arrive(smem_address(&sh.empty[s]));
-                        if (++s == kStages) {
-                            s = 0;
-                            phase ^= 1;
-                        }
+                        products_arrive(smem_address(&sh.done[slot]));
+                        begin = end;
                     }
-                    products_arrive(smem_address(&sh.done[slot]));
                 });
             }
         }
@@ -595,8 +608,8 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
         float2(*const both)[kHalf] = reinterpret_cast<float2(*)[kHalf]>(staging);
         const Epilogue<MODE, kDh> epilogue_h(a, live, mine, both, warp, lane);
         const Epilogue<MODE, kDw> epilogue_w(a, live, mine, both, warp, lane);
-        int n = 0;
-        for (int i = pair; i < tiles.total; i += pairs) {
+        int n = 0, turn = 0;
+        for (int i = pair; i < tiles.total; i += pairs, turn ^= 1) {
             tiles(i, [&](auto kind, const Grid::At& t) {
                 constexpr int KIND = decltype(kind)::value;
                 const auto& epilogue = [&]() -> const auto& {
@@ -615,22 +628,59 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                     });
                     return;
                 }
-                const int slot = n % 2;
-                // (a wait that runs out: on with what is there, so that no warp waits for
-                // another)
-                wait(sh, sh.done[slot], (n / 2) % 2);
-                __syncwarp();
-                ++n;
-                fence_after_sync();
-                const uint32_t from = tmem + slot * kPairTile + 32 * epilogue.begin +
-                                      (static_cast<uint32_t>(epilogue.place) << 16);
-                epilogue(row0, t.n, t.split, slot, [&](auto&& f) {
-                    auto release = [&] {                 // the tile's place may be taken
-                        fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0)
-                            bar_arrive_in_cluster(in_cta(smem_address(&sh.taken[slot]), 0));
-                    };
+                // the next result in tensor memory (a wait that runs out: on with what is
+                // there, so that no warp waits for another)
+                auto come = [&] {
+                    const int at = n % 2;
+                    wait(sh, sh.done[at], (n / 2) % 2);
+                    __syncwarp();
+                    ++n;
+                    fence_after_sync();
+                    return at;
+                };
+                auto place = [&](int at) {
+                    return tmem + at * kPairTile + 32 * epilogue.begin +
+                           (static_cast<uint32_t>(epilogue.place) << 16);
+                };
+                auto free_place = [&](int at) {          // ... may be taken again
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive_in_cluster(in_cta(smem_address(&sh.taken[at]), 0));
+                };
+                const int slot = come();
+                const uint32_t from = place(slot);
+                auto release = [&] { free_place(slot); };
+                epilogue(row0, t.n, t.split, turn, [&](auto&& f) {
+                    if constexpr (MODE == kLossLong) {
+                        float sum[4][32];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            if (c < parts) tmem_load(sum[c], from + 32 * c);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_load_wait(sum[c]);
+                        release();
+                        for (int k = kLossSteps; k < t.end; k += kLossSteps) {
+                            const int next = come();
+                            const uint32_t more = place(next);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                if (c >= 2 * parts) break;
+                                float v[16];
+                                tmem_load(v, more + 16 * c);
+                                tmem_load_wait(v);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    sum[c / 2][16 * (c % 2) + e] += v[e];
+                            }
+                            free_place(next);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            if (c < parts) f(c, sum[c]);
+                        }
+                        return;
+                    }
                     if constexpr (KIND == kDw) {         // (registers are short)
                         if (parts == 0) release();
 #pragma unroll 1
@@ -665,7 +715,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                 });
             });
         }
-        if (MODE != kLoss && lane == 0) bulk_wait();
+        if (!is_loss(MODE) && lane == 0) bulk_wait();
     }
     __syncwarp();
     __syncthreads();
@@ -1342,7 +1392,9 @@ cudaError_t launch_head_loss(const HeadCall& c, const HeadPlan& p, int64_t first
         a.label64 = c.label64;
         a.n_rows = static_cast<int32_t>(c.n_tokens);
     }
-    return launch_product<kLoss>(maps, a, p.rows / kPairTile * tiles_of(a.vocab, a.width), stream);
+    const int64_t tiles = p.rows / kPairTile * tiles_of(a.vocab, a.width);
+    return c.dim <= kLossSteps * kTileK ? launch_product<kLoss>(maps, a, tiles, stream)
+                                        : launch_product<kLossLong>(maps, a, tiles, stream);
 }
 
 cudaError_t launch_head_join(const HeadCall& c, const HeadPlan& p, cudaStream_t stream) {
