@@ -491,6 +491,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
         sh.stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (warp == 0 && lane < (MODE == kProducts ? 4 : 2)) prefetch_map(&maps.a + lane);
     if (warp == 1) tmem_alloc(smem_address(&sh.tmem), kTmemColumns);
     fence_before_sync();
     __syncthreads();

@@ -109,6 +109,9 @@ __device__ __forceinline__ void bulk_wait() {
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 // A box of a two-dimensional tensor map to shared memory; x times the element size is a
 // multiple of 16 bytes.  The bytes count on the barrier of the pair's CTA 0, at the same
 // place as `bar` is here.
