@@ -7,10 +7,17 @@
 // them, so that a training step keeps a byte an element of it.
 //
 // A row lives in the registers of a group of threads, 8 K elements each; a CTA holds
-// several groups, which work through the rows independently, the next row's loads under
-// way while a row is worked on.  The backward pass keeps its columns of dw in registers
-// over all rows; each CTA writes one partial row, which a second launch adds up in CTA
-// order.
+// several groups, which work through the rows independently, the next rows' loads under
+// way while a row is worked on: into rings in shared memory (rms_rows_kernel,
+// rms_rows_grad_kernel), or, for what those do not take, straight to registers.  The
+// backward pass keeps its columns of dw in registers over all rows; each CTA writes one
+// partial row, which a second launch adds up in CTA order.
+//
+// Bound by memory where rows are many: 16384 x 4096 bf16 with residual 85 us (6.3 TB/s), with
+// the sum in 8 bits 99 us; backward of 8192 x 4096 49 us (5.5 TB/s, 5 us of it the second
+// launch), of 16384 x 4096 from 8 bits with the output once more 102 us (5.9 TB/s); 16384 x
+// 14336 bf16 packed and unpacked 207 us (6.9 TB/s).  Few rows take as long as the host's call
+// (4 x 4096: 9 us).
 #include "zero_eight.cuh"
 
 #include <mutex>
@@ -842,7 +849,8 @@ unpack_wide_kernel(const __grid_constant__ EightArgs a) {
     }
 }
 
-// How rows are held: octets a thread, threads of a group, groups of a CTA.
+// How rows are held where they go straight to registers: octets a thread, threads of a
+// group, groups of a CTA.
 struct RmsShape {
     int k, group, per_cta;
 };
@@ -865,6 +873,8 @@ struct RowsShape {
 
 RowsShape rows_shape(int64_t dim, int elem, int64_t slot_bytes, bool weight_f32, bool back) {
     RowsShape s{};
+    // octets a thread (8192 x 2048 bf16 forward by one 28 us, by two 32, backward 35 / 33; 16384 x
+    // 4096 by one 105, by two 89, by four 105; 8192 x 8192 by two 92, by four 106)
     s.k = dim <= (back ? 1024 : 2048) ? 1 : dim <= 8192 ? 2 : 4;
     s.group = static_cast<int>((dim + 256 * s.k - 1) / (256 * s.k) * 32);
     s.slot_bytes = slot_bytes;
@@ -875,6 +885,9 @@ RowsShape rows_shape(int64_t dim, int elem, int64_t slot_bytes, bool weight_f32,
     const int least = back && s.k == 4 ? 3 : 2;
     while (s.per_cta > 1 && room / (s.per_cta * slot_bytes) < least) --s.per_cta;
     const int64_t one = s.per_cta * slot_bytes;
+    // 64 KB on their way an SM: 16384 x 4096 bf16 forward 89 us so (two slots a group), with
+    // three 101, with eight 106; backward 90, with one more 89 to 98; 8192 x 2048 forward 28,
+    // with 32 KB 31
     int64_t ahead = (64 * 1024 + one - 1) / one;
     ahead = ahead < least ? least : ahead > 8 ? 8 : ahead;
     s.slots = static_cast<int>(room / one < ahead ? room / one : ahead);
