@@ -25,6 +25,7 @@
 // 50257 x 768: 28 us, 2.7 TB/s).
 #include "zero_head.cuh"
 
+#include <cfloat>
 #include <mutex>
 
 #include "zero_kernels.cuh"
@@ -60,6 +61,7 @@ constexpr uint32_t kTmemColumns = 512;      // two tiles' results
 constexpr int kLossSteps = 24;
 constexpr uint64_t kHeadWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kInvLog2e = static_cast<float>(1.0 / static_cast<double>(kLog2e));
 constexpr float kInvLog2eLo = static_cast<float>(1.0 / static_cast<double>(kLog2e) -
                                                  static_cast<double>(kInvLog2e));
@@ -110,21 +112,22 @@ struct Shared {
 
 // Waits for a phase; false when the CTA is to stop: the wait has run out, here or in
 // another of its roles.
-__device__ __noinline__ bool wait_long(Shared& sh, uint32_t bar, uint32_t parity) {
+__device__ __noinline__ bool wait_long(volatile int* stop, uint32_t bar, uint32_t parity) {
     const uint64_t t0 = now_ns();
     while (!bar_try(bar, parity)) {
-        if (*static_cast<volatile int*>(&sh.stop)) return false;
+        if (*stop) return false;
         if (now_ns() - t0 > kHeadWaitNs) {
-            *static_cast<volatile int*>(&sh.stop) = 1;
+            *stop = 1;
             atomicCAS(&g_head_status, kDeviceOk, kDeviceTimeout);
             return false;
         }
     }
     return true;
 }
-__device__ __forceinline__ bool wait(Shared& sh, uint64_t& bar, uint32_t parity) {
+template <class S>
+__device__ __forceinline__ bool wait(S& sh, uint64_t& bar, uint32_t parity) {
     const uint32_t b = smem_address(&bar);
-    return bar_try(b, parity) || wait_long(sh, b, parity);
+    return bar_try(b, parity) || wait_long(&sh.stop, b, parity);
 }
 
 __device__ __forceinline__ int live_rows(const HeadArgs& a) {
@@ -738,6 +741,247 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
     if (warp == 1) tmem_free(tmem, kTmemColumns);
 }
 
+// ---------------------------------------------------------- few tokens ------
+
+// The forward pass of up to 64 tokens, bound by reading the table: the vocabulary on the
+// products' rows, 128 at a time, so that the tokens' side is small and a CTA by itself streams
+// its share of the table, even to 16 rows, by a deep ring.  A thread keeps a running maximum
+// and sum of each token over its rows of all tiles; they are joined at the end, one part of a
+// row's statistics a CTA.  32 tokens x 50257 x 768 19.5 us (head_kernel 26.4), of which 5.6
+// are two launches and an end of any size and the rest reads the table at 5.5 TB/s; 131072 x
+// 4096 158 to 162 us, 6.7 TB/s (1 to 8 tokens with head_kernel 216 to 233).  The maximum and sum kept
+// by one exponential a logit, labels found once a warp's 32 rows: 2 us of each call.
+constexpr int kFewMost = 64;
+constexpr int kFewUnit = 16;                         // rows of the table
+// (two warps that load and issue, and four that read 32 tokens' sums)
+__host__ __device__ constexpr int few_threads(int tokens) { return 64 + 4 * tokens; }
+constexpr int kFewMostStages = 10;
+__host__ __device__ constexpr uint32_t few_stage(int tokens) { return kOperandBytes + tokens * 128u; }
+__host__ __device__ constexpr int few_stages(int tokens) { return tokens == 32 ? 10 : 8; }
+__host__ __device__ constexpr size_t few_smem(int tokens) {
+    return few_stages(tokens) * few_stage(tokens) + 1024;
+}
+
+struct FewArgs {
+    const void* labels;
+    float2* parts;                // [n_rows][CTAs]
+    float* picked;
+    int32_t n_rows;
+    int32_t vocab;
+    int32_t dim;
+    int32_t label64;
+};
+struct FewMaps {
+    // 128 rows of the table, what the smaller and the larger shares have beyond whole tiles, and
+    // the tokens.  (A copy for each 16 rows instead:
+    // 32 tokens, 131072 x 4096 176 us, 163 with these.)
+    CUtensorMap tile, rest[2], tokens;
+};
+struct FewShared {
+    uint64_t full[kFewMostStages], empty[kFewMostStages], done[2], taken[2];
+    uint32_t tmem;
+    int stop;
+};
+
+// A maximum (times log2 e) and a sum of exponentials, joined with another.
+__device__ __forceinline__ void join(float& top, float& sum, float t, float s) {
+    const float m = fmaxf(top, t), from = m == -INFINITY ? 0.0f : m;
+    sum = sum * exp2_fast(top - from) + s * exp2_fast(t - from);
+    top = m;
+}
+
+template <int TOKENS>
+__global__ void __launch_bounds__(few_threads(TOKENS), 1)
+head_few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ FewArgs a) {
+    constexpr int kRing = few_stages(TOKENS);
+    extern __shared__ char dyn[];
+    __shared__ FewShared sh;
+    const uint32_t ring = (smem_address(dyn) + 1023u) & ~1023u;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kRing; ++s) {
+            bar_init(smem_address(&sh.full[s]), 1);
+            bar_init(smem_address(&sh.empty[s]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(smem_address(&sh.done[i]), 1);
+            bar_init(smem_address(&sh.taken[i]), TOKENS / 8);
+        }
+        sh.stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0 && lane < 4) prefetch_map(&maps.tile + lane);
+    if (warp == 1) single::tmem_alloc(smem_address(&sh.tmem), 2 * kFewMost);
+    let_next_launch_begin();
+    wait_for_launch_before();
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = sh.tmem;
+    const int64_t units = (a.vocab + kFewUnit - 1) / kFewUnit;
+    const int begin = static_cast<int>(units * blockIdx.x / gridDim.x);
+    const int end = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
+    const int steps = (a.dim + kTileK - 1) / kTileK;
+    constexpr int kUnits = kHalf / kFewUnit;             // of a tile
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t phase = 1;
+            bool run = true;
+            const bool more = end - begin > units / gridDim.x;
+            for (int u = begin; run && u < end; u += kUnits) {
+                const int n = min(kUnits, end - u);
+                const CUtensorMap* const rows = n == kUnits ? &maps.tile : &maps.rest[more];
+                for (int k = 0; k < steps; ++k) {
+                    run = wait(sh, sh.empty[s], phase);
+                    if (!run) break;
+                    const uint32_t bar = smem_address(&sh.full[s]);
+                    const uint32_t to = ring + s * few_stage(TOKENS);
+                    bar_expect(bar, n * kFewUnit * 128 + TOKENS * 128);
+                    single::tma_load(to, rows, k * kTileK, u * kFewUnit, bar);
+                    single::tma_load(to + kOperandBytes, &maps.tokens, k * kTileK, 0, bar);
+                    if (++s == kRing) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int s = 0, n = 0;
+            uint32_t phase = 0;
+            bool run = true;
+            for (int u = begin; run && u < end; u += kUnits) {
+                // (rows of a tile beyond the CTA's share: what an earlier tile left there)
+                for (int from = 0; run && from < steps; from += kLossSteps) {
+                    const int slot = n % 2;
+                    run = wait(sh, sh.taken[slot], (n / 2 + 1) % 2);
+                    if (!run) break;
+                    ++n;
+                    fence_after_sync();
+                    const uint32_t d = tmem + slot * kFewMost;
+                    for (int k = from; k < min(from + kLossSteps, steps); ++k) {
+                        run = wait(sh, sh.full[s], phase);
+                        if (!run) break;
+                        fence_after_sync();
+                        const uint32_t at = ring + s * few_stage(TOKENS);
+                        const uint64_t da = operand(at, 16), db = operand(at + kOperandBytes, 16);
+#pragma unroll
+                        for (int j = 0; j < kTileK / 16; ++j)
+                            single::product(d, da + 2 * j, db + 2 * j, single::product_form(TOKENS),
+                                            k != from || j != 0);
+                        single::products_arrive(smem_address(&sh.empty[s]));
+                        if (++s == kRing) {
+                            s = 0;
+                            phase ^= 1;
+                        }
+                    }
+                    if (run) single::products_arrive(smem_address(&sh.done[slot]));
+                }
+            }
+        }
+    } else {
+        const int part = warp % 4;                       // of tensor memory's lanes
+        const int first = (warp - 2) / 4 * 32;           // of the warp's tokens
+        int label = -1;                                  // of the lane's token
+        if (first + lane < a.n_rows) {
+            const int64_t y = a.label64 ? static_cast<const int64_t*>(a.labels)[first + lane]
+                                        : static_cast<const int32_t*>(a.labels)[first + lane];
+            if (y >= 0 && y < a.vocab) label = static_cast<int>(y);
+        }
+        float top[32], sum[32];
+#pragma unroll
+        for (int t = 0; t < 32; ++t) {
+            top[t] = -FLT_MAX;
+            sum[t] = 0.0f;
+        }
+        int n = 0;
+        for (int u = begin; u < end; u += kUnits) {
+            const int place = part * 32 + lane, row = u * kFewUnit + place;
+            const bool in = place < (end - u) * kFewUnit && row < a.vocab;
+            float z[32];
+            for (int from = 0; from < steps; from += kLossSteps) {
+                const int slot = n % 2;
+                wait(sh, sh.done[slot], (n / 2) % 2);
+                __syncwarp();
+                ++n;
+                fence_after_sync();
+                float v[32];
+                tmem_load(v, tmem + slot * kFewMost + first + (static_cast<uint32_t>(part * 32) << 16));
+                tmem_load_wait(v);
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) single::bar_arrive(smem_address(&sh.taken[slot]));
+#pragma unroll
+                for (int t = 0; t < 32; ++t) z[t] = from == 0 ? v[t] : z[t] + v[t];
+            }
+            // Few labels are in a warp's 32 rows.
+            if (__any_sync(0xFFFFFFFFu, static_cast<uint32_t>(label - (row - lane)) < 32u)) {
+#pragma unroll
+                for (int t = 0; t < 32; ++t) {
+                    const int of_t = __shfl_sync(0xFFFFFFFFu, label, t);
+                    if (in && of_t == row) a.picked[first + t] = z[t];
+                }
+            }
+            // One exponential a logit: a new maximum's own term is 1, but for the rounding of
+            // x log2 e to it, r.
+#pragma unroll
+            for (int t = 0; t < 32; ++t) {
+                const float x = in ? z[t] : -INFINITY, y = x * kLog2e;
+                const bool up = y > top[t];
+                const float e = exp2_fast(up ? top[t] - y : __fmaf_rn(x, kLog2e, -top[t]));
+                const float r = __fmaf_rn(x, kLog2e, -y);
+                sum[t] = up ? __fmaf_rn(sum[t], e, __fmaf_rn(r, kLn2, 1.0f)) : sum[t] + e;
+                top[t] = up ? y : top[t];
+            }
+        }
+        // Over the CTA's rows, through the ring: every copy into it and product from it has
+        // come before the last tile's sums.  A warp joins its own 32 rows of its tokens, a
+        // lane a token, and one of four those of all.
+        constexpr int kPitch = 33;
+        float2* const all = reinterpret_cast<float2*>(dyn + (ring - smem_address(dyn)));
+        float2* const own = all + (first * 4 + part * 32) * kPitch;
+#pragma unroll
+        for (int t = 0; t < 32; ++t) own[lane * kPitch + t] = make_float2(top[t], sum[t]);
+        __syncwarp();
+        float m = -FLT_MAX, l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float2 o = own[i * kPitch + lane];
+            top[i] = o.x;
+            sum[i] = o.y;
+            m = fmaxf(m, o.x);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) l += sum[i] * exp2_fast(top[i] - m);
+        __syncwarp();
+        own[lane] = make_float2(m, l);
+        asm volatile("bar.sync 1, %0;" ::"n"(4 * TOKENS) : "memory");
+        if (part == 0 && first + lane < a.n_rows) {
+#pragma unroll
+            for (int i = 1; i < 4; ++i) {
+                const float2 o = own[i * 32 * kPitch + lane];
+                join(m, l, o.x, o.y);
+            }
+            a.parts[(first + lane) * static_cast<int64_t>(gridDim.x) + blockIdx.x] =
+                make_float2(m, l);
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    if (sh.stop) {
+        // what is still on its way to shared or tensor memory gets time to come
+        const uint64_t t0 = now_ns();
+        while (now_ns() - t0 < 20000000ull) {}
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (warp == 1) single::tmem_free(tmem, 2 * kFewMost);
+}
+
 // ---------------------------------------------------------------- rows ------
 
 // The places in the workspace that the first launches fill.
@@ -964,13 +1208,9 @@ head_join_kernel(const HeadCall c, const int32_t* counts, const int32_t* index,
     wait_for_launch_before();
     const bool as_they_are = counts == nullptr;
     if (row >= (as_they_are ? c.n_tokens : *counts)) return;
-    if (as_they_are && live_label(c, row, false) < 0) {
-        if (lane == 0) {
-            c.loss[row] = 0.0f;
-            if (c.lse != nullptr) c.lse[row] = 0.0f;
-        }
-        return;
-    }
+    // (read beside the parts; of a token that does not count nothing has been written)
+    const bool live = !as_they_are || live_label(c, row, false) >= 0;
+    const float of_label = picked[row];
     const float2* p = parts + row * n_parts;
     float top = -INFINITY, sum = 0.0f;
 #pragma unroll 4
@@ -995,10 +1235,10 @@ head_join_kernel(const HeadCall c, const int32_t* counts, const int32_t* index,
         // and the sum's logarithm: two numbers that are not negative.
         const float l = logf(sum);
         const int64_t t = as_they_are ? row : index[row];
-        const float d = __fmaf_rn(top, kInvLog2eLo, __fmaf_rn(top, kInvLog2e, -picked[row])) + l;
-        c.loss[t] = d < 0.0f ? 0.0f : d;
+        const float d = __fmaf_rn(top, kInvLog2eLo, __fmaf_rn(top, kInvLog2e, -of_label)) + l;
+        c.loss[t] = !live || d < 0.0f ? 0.0f : d;
         if (c.lse != nullptr)
-            c.lse[t] = __fmaf_rn(top, kInvLog2e, __fmaf_rn(top, kInvLog2eLo, l));
+            c.lse[t] = live ? __fmaf_rn(top, kInvLog2e, __fmaf_rn(top, kInvLog2eLo, l)) : 0.0f;
     }
 }
 
@@ -1338,7 +1578,9 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, bool
         p.dz = place(2 * p.rows * whole(p.piece < vocab ? p.piece : vocab, 64));
         p.sums = place(4 * p.splits * p.rows * whole(dim, 32));
     } else {
-        p.parts = place(8 * n * p.parts_a_row);
+        // (of few tokens one part a CTA, perhaps)
+        const int64_t few = n <= kFewMost ? device_sms() : 0;
+        p.parts = place(8 * n * (p.parts_a_row > few ? p.parts_a_row : few));
         p.picked = place(4 * n);
     }
     p.bytes = end;
@@ -1380,8 +1622,64 @@ cudaError_t launch_head_gather(const HeadCall& c, const HeadPlan& p, cudaStream_
                      p.rows, c.dim, at<uint16_t>(c, p.hidden), p.pitch, stream);
 }
 
+// Few tokens that TMA reaches, as it does the table; more than 32 from 80 rows of the table an
+// SM on (64 tokens, us with head_few_kernel and with head_kernel: 5000 x 256 8.4 and 7.5,
+// 9728 x 256 8.4 and 8.0, 14000 x 256 8.8 and 9.0, 14000 x 2048 18.6 and 19.7; 32 tokens 6.4
+// and 7.4, 6.5 and 7.9, 6.7 and 8.8, 16.5 and 19.4).
+int64_t few_units(const HeadCall& c) { return (c.vocab + kFewUnit - 1) / kFewUnit; }
+int few_ctas(const HeadCall& c) {
+    const int64_t units = few_units(c), sms = device_sms();
+    return static_cast<int>(units < sms ? units : sms);
+}
+bool few_tokens(const HeadCall& c) {
+    return rows_as_they_are(c) && table_in_place(c) &&
+           (c.n_tokens <= 32 || (c.n_tokens <= kFewMost && few_units(c) >= 5 * device_sms()));
+}
+
+template <int TOKENS>
+cudaError_t launch_few(const HeadCall& c, const HeadPlan& p, cudaStream_t stream) {
+    static std::once_flag once[64];
+    static cudaError_t set[64];
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::call_once(once[dev], [&] {
+        set[dev] = cudaFuncSetAttribute(head_few_kernel<TOKENS>,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(few_smem(TOKENS)));
+    });
+    if (set[dev] != cudaSuccess) return set[dev];
+    FewMaps maps;
+    if (cudaError_t e = make_map(&maps.tile, c.table, c.dim, c.vocab, c.dim, kHalf); e != cudaSuccess)
+        return e;
+    const int64_t share = few_units(c) / few_ctas(c);
+    for (int more = 0; more < 2; ++more) {
+        const int rest = static_cast<int>((share + more) % (kHalf / kFewUnit));
+        if (cudaError_t e = make_map(&maps.rest[more], c.table, c.dim, c.vocab, c.dim,
+                                     (rest ? rest : 1) * kFewUnit);
+            e != cudaSuccess)
+            return e;
+    }
+    if (cudaError_t e = make_map(&maps.tokens, c.hidden, c.dim, c.n_tokens, c.hidden_stride, TOKENS);
+        e != cudaSuccess)
+        return e;
+    FewArgs a{};
+    a.labels = c.labels;
+    a.parts = at<float2>(c, p.parts);
+    a.picked = at<float>(c, p.picked);
+    a.n_rows = static_cast<int32_t>(c.n_tokens);
+    a.vocab = static_cast<int32_t>(c.vocab);
+    a.dim = static_cast<int32_t>(c.dim);
+    a.label64 = c.label64;
+    return launch_after(head_few_kernel<TOKENS>, static_cast<unsigned>(few_ctas(c)),
+                        few_threads(TOKENS),
+                        few_smem(TOKENS), stream, maps, a);
+}
+
 cudaError_t launch_head_loss(const HeadCall& c, const HeadPlan& p, int64_t first,
                              cudaStream_t stream) {
+    if (few_tokens(c))
+        return c.n_tokens <= 32 ? launch_few<32>(c, p, stream) : launch_few<kFewMost>(c, p, stream);
     if (cudaError_t e = copy_piece(c, p, first, stream); e != cudaSuccess) return e;
     const bool as_they_are = head_rows_as_they_are(c);
     HeadMaps maps{};
@@ -1410,7 +1708,8 @@ cudaError_t launch_head_join(const HeadCall& c, const HeadPlan& p, cudaStream_t 
     const bool as_they_are = head_rows_as_they_are(c);
     return launch_after(head_join_kernel, grid, 256, 0, stream, c,
                         as_they_are ? nullptr : at<int32_t>(c, p.counts), at<int32_t>(c, p.index),
-                        at<float2>(c, p.parts), p.parts_a_row, at<float>(c, p.picked));
+                        at<float2>(c, p.parts), few_tokens(c) ? few_ctas(c) : p.parts_a_row,
+                        at<float>(c, p.picked));
 }
 
 cudaError_t launch_head_dz(const HeadCall& c, const HeadPlan& p, int64_t first,

@@ -127,6 +127,47 @@ def test_head_loss(n, vocab, d, pad, offset, kind):
     assert torch.equal(alone[0], out[0]) and bool((alone[1] == 7.0).all())
 
 
+# Few tokens in place: one row of the table and one more than the even shares, a share that
+# ends inside a tile, columns summed in parts, tokens on both sides of a half, strided rows.
+@pytest.mark.parametrize("kind", ["all", "some", "last"])
+@pytest.mark.parametrize("n,vocab,d,pad", [
+    (1, 1, 8, 0), (1, 17, 64, 8), (2, 15, 72, 0), (3, 127, 1528, 0), (7, 129, 1544, 24),
+    (31, 2432, 128, 0), (32, 2433, 136, 0), (32, 33000, 64, 0), (33, 19457, 776, 8),
+    (63, 22000, 1600, 0), (64, 40009, 200, 0), (64, 1000, 4104, 0), (65, 1000, 200, 0)])
+def test_head_loss_of_few_tokens(n, vocab, d, pad, kind):
+    _, h, w, y = _inputs(("few",), n, vocab, d, pad, 0, kind)
+    out = _loss(h, w, y)
+    loss, lse = L.head_loss(h, w, y)
+    R.check(out[0], *(t.cpu() for t in loss), "loss")
+    R.check(out[1], *(t.cpu() for t in lse), "lse")
+    assert torch.equal(_loss(h, w, y), out)
+
+
+def test_head_loss_of_few_tokens_with_infinite_logits():
+    """Rows of the table that a token reaches at minus infinity leave the sum, one at plus
+    infinity or NaN takes its own token's loss and no other's."""
+    g = _gen("few", "infinite")
+    h, w = torch.zeros((40, 64)), torch.randn((3000, 64), generator=g) * 0.25
+    h[:, 0] = 1.0
+    h[:, 1:8] = torch.randn((40, 7), generator=g)
+    w[100:900, 0] = float("-inf")
+    w[2500:, 0] = float("-inf")
+    h[3, 5] = float("nan")
+    h[37, 0] = -1.0
+    y = torch.full((40,), 2000)
+    h, w, y = h.to(BF16).cuda(), w.to(BF16).cuda(), y.cuda()
+    out = _loss(h, w, y)
+    live = torch.ones(3000, dtype=torch.bool)
+    live[100:900] = False
+    live[2500:] = False
+    keep = [i for i in range(40) if i not in (3, 37)]
+    few_y = torch.full((38,), int(live[:2000].sum()), device="cuda")
+    loss, lse = L.head_loss(h[keep].contiguous(), w[live.cuda()].contiguous(), few_y)
+    R.check(out[0][keep], *(t.cpu() for t in loss), "loss")
+    R.check(out[1][keep], *(t.cpu() for t in lse), "lse")
+    assert bool(out[0][[3, 37]].isnan().all())
+
+
 @pytest.mark.parametrize("accumulate", [False, True])
 @pytest.mark.parametrize("kind", ["all", "some", "none", "last", "one"])
 @pytest.mark.parametrize("n,vocab,d,pad,offset", SIZES)
