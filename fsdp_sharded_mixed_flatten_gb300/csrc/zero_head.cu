@@ -21,8 +21,8 @@
 // tokens of a table of 131072 x 4096 15.5 ms (1.70 PFLOP/s), the loss of 5500 live ones 3.5
 // ms (1.67).  Shorter sums are bound by shared memory, which operands on their way in and out
 // fill at the tensor cores' rate, and results cross too: 8192 tokens, 50257 x 768, 1.27 ms
-// (1.49 PFLOP/s).  Few tokens: by reading the table, and a launch's start and end (32 tokens,
-// 50257 x 768: 28 us, 2.7 TB/s).
+// (1.49 PFLOP/s).  Few tokens, whose loss has a kernel of its own: by reading the table, and a
+// launch's start and end (8 tokens, 131072 x 4096 158 us, 6.8 TB/s; 32, 50257 x 768 19.5 us).
 #include "zero_head.cuh"
 
 #include <cfloat>
@@ -749,7 +749,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
 // and sum of each token over its rows of all tiles; they are joined at the end, one part of a
 // row's statistics a CTA.  32 tokens x 50257 x 768 19.5 us (head_kernel 26.4), of which 5.6
 // are two launches and an end of any size and the rest reads the table at 5.5 TB/s; 131072 x
-// 4096 158 to 162 us, 6.7 TB/s (1 to 8 tokens with head_kernel 216 to 233).  The maximum and sum kept
+// 4096 158 to 162 us, 6.8 to 6.6 TB/s (1 to 8 tokens with head_kernel 216 to 233).  The maximum and sum kept
 // by one exponential a logit, labels found once a warp's 32 rows: 2 us of each call.
 constexpr int kFewMost = 64;
 constexpr int kFewUnit = 16;                         // rows of the table
