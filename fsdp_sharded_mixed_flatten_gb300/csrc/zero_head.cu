@@ -61,7 +61,6 @@ constexpr uint32_t kTmemColumns = 512;      // two tiles' results
 constexpr int kLossSteps = 24;
 constexpr uint64_t kHeadWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kInvLog2e = static_cast<float>(1.0 / static_cast<double>(kLog2e));
 constexpr float kInvLog2eLo = static_cast<float>(1.0 / static_cast<double>(kLog2e) -
                                                  static_cast<double>(kInvLog2e));
@@ -749,14 +748,17 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
 // and sum of each token over its rows of all tiles; they are joined at the end, one part of a
 // row's statistics a CTA.  32 tokens x 50257 x 768 19.5 us (head_kernel 26.4), of which 5.6
 // are two launches and an end of any size and the rest reads the table at 5.5 TB/s; 131072 x
-// 4096 158 to 162 us, 6.8 to 6.6 TB/s (1 to 8 tokens with head_kernel 216 to 233).  The maximum and sum kept
-// by one exponential a logit, labels found once a warp's 32 rows: 2 us of each call.
+// 4096 158 to 162 us, 6.8 to 6.6 TB/s (1 to 8 tokens with head_kernel 216 to 233).  The
+// maximum and sum kept by one exponential a logit, labels looked for once in a warp's 32 rows:
+// 2 us less a call.
 constexpr int kFewMost = 64;
 constexpr int kFewUnit = 16;                         // rows of the table
 // (two warps that load and issue, and four that read 32 tokens' sums)
 __host__ __device__ constexpr int few_threads(int tokens) { return 64 + 4 * tokens; }
 constexpr int kFewMostStages = 10;
-__host__ __device__ constexpr uint32_t few_stage(int tokens) { return kOperandBytes + tokens * 128u; }
+__host__ __device__ constexpr uint32_t few_stage(int tokens) {
+    return kOperandBytes + tokens * 128u;
+}
 __host__ __device__ constexpr int few_stages(int tokens) { return tokens == 32 ? 10 : 8; }
 __host__ __device__ constexpr size_t few_smem(int tokens) {
     return few_stages(tokens) * few_stage(tokens) + 1024;
@@ -783,10 +785,10 @@ struct FewShared {
     int stop;
 };
 
-// A maximum (times log2 e) and a sum of exponentials, joined with another.
+// A maximum of logits, -FLT_MAX before any, and a sum of exponentials, joined with another.
 __device__ __forceinline__ void join(float& top, float& sum, float t, float s) {
-    const float m = fmaxf(top, t), from = m == -INFINITY ? 0.0f : m;
-    sum = sum * exp2_fast(top - from) + s * exp2_fast(t - from);
+    const float m = fmaxf(top, t);
+    sum = sum * exp2_fast((top - m) * kLog2e) + s * exp2_fast((t - m) * kLog2e);
     top = m;
 }
 
@@ -909,7 +911,8 @@ head_few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ Fe
                 ++n;
                 fence_after_sync();
                 float v[32];
-                tmem_load(v, tmem + slot * kFewMost + first + (static_cast<uint32_t>(part * 32) << 16));
+                tmem_load(v, tmem + slot * kFewMost + first +
+                                 (static_cast<uint32_t>(part * 32) << 16));
                 tmem_load_wait(v);
                 fence_before_sync();
                 __syncwarp();
@@ -925,16 +928,14 @@ head_few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ Fe
                     if (in && of_t == row) a.picked[first + t] = z[t];
                 }
             }
-            // One exponential a logit: a new maximum's own term is 1, but for the rounding of
-            // x log2 e to it, r.
+            // One exponential a logit: the larger of it and the maximum counts 1.
 #pragma unroll
             for (int t = 0; t < 32; ++t) {
-                const float x = in ? z[t] : -INFINITY, y = x * kLog2e;
-                const bool up = y > top[t];
-                const float e = exp2_fast(up ? top[t] - y : __fmaf_rn(x, kLog2e, -top[t]));
-                const float r = __fmaf_rn(x, kLog2e, -y);
-                sum[t] = up ? __fmaf_rn(sum[t], e, __fmaf_rn(r, kLn2, 1.0f)) : sum[t] + e;
-                top[t] = up ? y : top[t];
+                const float x = in ? z[t] : -INFINITY, d = x - top[t];
+                const bool up = x > top[t];
+                const float e = exp2_fast((up ? -d : d) * kLog2e);
+                sum[t] = up ? __fmaf_rn(sum[t], e, 1.0f) : sum[t] + e;
+                top[t] = up ? x : top[t];
             }
         }
         // Over the CTA's rows, through the ring: every copy into it and product from it has
@@ -955,7 +956,7 @@ head_few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ Fe
             m = fmaxf(m, o.x);
         }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) l += sum[i] * exp2_fast(top[i] - m);
+        for (int i = 0; i < 32; ++i) l += sum[i] * exp2_fast((top[i] - m) * kLog2e);
         __syncwarp();
         own[lane] = make_float2(m, l);
         asm volatile("bar.sync 1, %0;" ::"n"(4 * TOKENS) : "memory");
@@ -965,8 +966,11 @@ head_few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ Fe
                 const float2 o = own[i * 32 * kPitch + lane];
                 join(m, l, o.x, o.y);
             }
+            // The parts' maxima are rounded multiples of log2 e, the sums relative to those.
+            const float y = m * kLog2e;
+            if (l != 0.0f) l *= exp2_fast(__fmaf_rn(m, kLog2e, -y));
             a.parts[(first + lane) * static_cast<int64_t>(gridDim.x) + blockIdx.x] =
-                make_float2(m, l);
+                make_float2(y, l);
         }
     }
     __syncwarp();
@@ -1491,8 +1495,8 @@ int64_t tiles_of(int64_t x, int64_t width) { return (x + width - 1) / width; }
 
 // Clock cycles of a tile of `steps` steps and `width` columns: the steps (256 + width, what
 // the operands take on their way), the result's way out and what comes before; and of a
-// launch of m rows of tiles, n columns, in rounds over the GPU's pairs.  Measured: 12 steps of width 256 7500 to 8400
-// cycles, 64 steps 36000 to 40000.
+// launch of m rows of tiles, n columns, in rounds over the GPU's pairs.  Measured: 12 steps of
+// width 256 7500 to 8400 cycles, 64 steps 36000 to 40000.
 double tile_cost(double steps, int width) { return (256.0 + width) * steps + 12.0 * width + 800.0; }
 int64_t pairs_of_gpu() { return device_sms() / 2 > 0 ? device_sms() / 2 : 1; }
 double launch_cost(int64_t m, int64_t n, int64_t steps, int width) {
@@ -1650,7 +1654,8 @@ cudaError_t launch_few(const HeadCall& c, const HeadPlan& p, cudaStream_t stream
     });
     if (set[dev] != cudaSuccess) return set[dev];
     FewMaps maps;
-    if (cudaError_t e = make_map(&maps.tile, c.table, c.dim, c.vocab, c.dim, kHalf); e != cudaSuccess)
+    if (cudaError_t e = make_map(&maps.tile, c.table, c.dim, c.vocab, c.dim, kHalf);
+        e != cudaSuccess)
         return e;
     const int64_t share = few_units(c) / few_ctas(c);
     for (int more = 0; more < 2; ++more) {
@@ -1757,7 +1762,8 @@ cudaError_t launch_head_finish(const HeadCall& c, const HeadPlan& p, cudaStream_
         static_cast<unsigned>(many ? units : (units + kFinishWarps - 1) / kFinishWarps);
     const auto kernel = many ? (wide ? head_finish_kernel<true, true> : head_finish_kernel<false, true>)
                              : (wide ? head_finish_kernel<true, false> : head_finish_kernel<false, false>);
-    return launch_after(kernel, grid, 32 * kFinishWarps, 0, stream, at<int32_t>(c, p.slot), at<float>(c, p.sums), p.rows, p.splits,
+    return launch_after(kernel, grid, 32 * kFinishWarps, 0, stream, at<int32_t>(c, p.slot),
+                        at<float>(c, p.sums), p.rows, p.splits,
                         c.n_tokens, c.dim, sections, c.grad_hidden, c.grad_hidden_stride);
 }
 

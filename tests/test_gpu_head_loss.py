@@ -264,6 +264,26 @@ def test_head_loss_of_large_and_equal_logits():
     assert 0.0 <= float(out[0, 3]) <= 2.0 ** -22
 
 
+@pytest.mark.parametrize("n", [4, 32, 40, 300])
+def test_head_loss_of_equal_logits_of_any_size(n):
+    """Equal logits up to 5.6e7, each one product that fp32 holds: log(vocab).  Their
+    multiples of log2 e are rounded by up to 4 there, which the sum makes up for.  Off by
+    the sum's additions (at most 300 one after another, 2^-24 each), an exponential's error
+    (2^-22), the logarithm's (below 16: an ulp of 2^-20) and the roundings of the result's
+    parts (2^-20 in all): below 2^-15."""
+    vocab, d = 12288, 64
+    h = torch.zeros((n, d), dtype=BF16, device="cuda")
+    w = torch.zeros((vocab, d), dtype=BF16, device="cuda")
+    i = torch.arange(n, device="cuda")
+    h[:, 0] = ((128 + i % 128) * 2.0 ** (i % 4 * 3 - 2)).to(BF16)       # up to 32640
+    h[::2, 0] *= -1.0
+    w[:, 0] = 1696.0
+    y = torch.arange(n, device="cuda") * 37
+    out = _loss(h, w, y)
+    off = (out[0].to(F64) - torch.log(torch.tensor(float(vocab), dtype=F64))).abs()
+    assert float(off.max()) <= 2.0 ** -15
+
+
 def test_head_loss_of_nan_stays_in_its_row():
     g, h, w, y = _inputs(("nan",), 300, 700, 64, 0, 0, "all")
     clean = _loss(h, w, y)
@@ -305,6 +325,41 @@ def _mixed_calls(stream=None, key="mixed"):
         zf.zero_head_loss(h, w, y, out[0], out[1], ws, size, stream=stream)
         zf.zero_head_loss_grad(h, w, y, out[1], gl, dh, dw, False, ws, size, stream=stream)
     return call, (out, dh, dw)
+
+
+def _few_calls(stream, n):
+    g, h, w, y = _inputs(("few at once",), n, 20011, 264, 0, 0, "some")
+    out, size = torch.zeros((2, n), device="cuda"), zf.zero_head_loss_workspace_bytes(n, 20011, 264)
+    ws = _workspace(size)
+    torch.cuda.synchronize()
+    return lambda: zf.zero_head_loss(h, w, y, out[0], out[1], ws, size, stream=stream), out
+
+
+def test_few_tokens_on_streams_at_once_and_captured():
+    refs = {}
+    for n in (20, 50):
+        call, refs[n] = _few_calls(None, n)
+        call()
+    torch.cuda.synchronize()
+    calls = [(_few_calls(torch.cuda.Stream(), n), n) for n in (20, 50, 20)]
+    for _ in range(3):
+        for (call, _), _ in calls:
+            call()
+    torch.cuda.synchronize()
+    for (_, out), n in calls:
+        assert torch.equal(out, refs[n])
+    some = [_few_calls(None, n) for n in (20, 50)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for call, _ in some + some:
+            call()
+    for _, out in some:
+        out.zero_()
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    for (_, out), n in zip(some, (20, 50)):
+        assert torch.equal(out, refs[n])
 
 
 def test_streams_at_once_give_the_same_bits():
