@@ -215,9 +215,11 @@ rms_norm_grad_kernel(const __grid_constant__ RmsArgs a) {
     }
 }
 
-// The same through shared memory: every group has a ring of slots, one row's arrays each, that its first thread fills by bulk copies, so
-// that several rows a group are on their way whatever the registers hold.  A slot is
-// filled again when the group's next exchange shows that all have done with it.
+// The same through shared memory: every group has a ring of slots, one row's arrays each,
+// that its first thread fills by bulk copies, so that several rows a group are on their way
+// whatever the registers hold.  A slot is filled again when the group's next exchange shows
+// that all have done with it.
+//
 // Threads of a CTA at most: more where a thread has one octet and few registers (forward of
 // 8192 rows of bf16: 768 columns 15.1 us, by 512 threads 16.7; 2048 28.0 / 32.0; but 16384 x
 // 1024 fp32 55.7 / 48.6).
@@ -493,7 +495,8 @@ rms_rows_grad_kernel(const __grid_constant__ RmsArgs a) {
         if (at >= a.n_rows) return;
         const uint32_t to = tile::smem_address(ring.base + s * ring.slot_bytes), bar = ring.bar(s);
         const bool dt = a.grad_total != nullptr;
-        uint32_t bytes = row_bytes<WIDE>(dy_row(at), a.dim) + (dt ? row_bytes<WIDE>(dt_row(at), a.dim) : 0);
+        uint32_t bytes =
+            row_bytes<WIDE>(dy_row(at), a.dim) + (dt ? row_bytes<WIDE>(dt_row(at), a.dim) : 0);
         if constexpr (EIGHT) bytes += row_bytes<WIDE>(codes_row(at), a.dim);
         else bytes += row_bytes<WIDE>(x_row(at), a.dim);
         tile::bar_expect(bar, bytes);
@@ -803,7 +806,8 @@ pack_wide_kernel(const __grid_constant__ EightArgs a) {
         if (c < a.dim) {
             *reinterpret_cast<uint4*>(a.codes + row * a.codes_stride + c) =
                 make_uint4(q[0], q[1], q[2], q[3]);
-            if (c % kEightBlock == 0) a.scales[row * a.blocks + c / kEightBlock] = __uint_as_float(s << 23);
+            if (c % kEightBlock == 0)
+                a.scales[row * a.blocks + c / kEightBlock] = __uint_as_float(s << 23);
         }
     }
 }
@@ -1096,7 +1100,8 @@ cudaError_t launch_eight(EightArgs a, int act_bytes, cudaStream_t stream) {
     const unsigned grid = static_cast<unsigned>(ctas);
     return by_type(act_bytes, [&](auto t) {
         using T = decltype(t);
-        const auto kernel = words  ? (pack ? pack_wide_kernel<T, kWideUnits> : unpack_wide_kernel<T, kWideUnits>)
+        const auto kernel = words  ? (pack ? pack_wide_kernel<T, kWideUnits>
+                                           : unpack_wide_kernel<T, kWideUnits>)
                             : pack ? (wide ? pack_kernel<T, true> : pack_kernel<T, false>)
                                    : (wide ? unpack_kernel<T, true> : unpack_kernel<T, false>);
         kernel<<<grid, 32 * kEightWarps, 0, stream>>>(a);
