@@ -74,7 +74,9 @@ __host__ __device__ constexpr bool is_loss(int mode) { return mode == kLoss || m
 enum Kind { kDh, kDw };
 
 struct HeadArgs {
-    const int32_t* counts;        // live tokens; null: tokens are rows as they are, n_rows of them
+    // live tokens, and (backward) the scale taken out of dz; null: tokens are rows as they are,
+    // n_rows of them
+    const int32_t* counts;
     const int32_t* label;         // of the live tokens, as the rest; or null, and
     const void* labels;           // of all, int32 or int64
     const float* lse;
@@ -131,6 +133,16 @@ __device__ __forceinline__ bool wait(S& sh, uint64_t& bar, uint32_t parity) {
 
 __device__ __forceinline__ int live_rows(const HeadArgs& a) {
     return a.counts != nullptr ? *a.counts : a.n_rows;
+}
+// What is taken out of dz before it is rounded to bf16, and put back to the products' sums:
+// the mantissa, 1 <= m < 2, of the largest finite gradient of a loss.  Where all are alike
+// (one over the tokens), their rounding would be the same error in every term, which no sum
+// averages away; so it is none (817 live tokens 32003 x 770 0.0023 -> @@).
+__device__ __forceinline__ float scale_of(const int32_t* counts) {
+    return __int_as_float(counts[1]);
+}
+__device__ __forceinline__ int32_t scale_from(float largest) {
+    return (__float_as_int(largest) & 0x7FFFFF) | 0x3F800000;
 }
 // A row's label in the piece, or another number.
 __device__ __forceinline__ int label_in_piece(const HeadArgs& a, int row) {
@@ -331,7 +343,8 @@ struct Epilogue {
         } else if constexpr (MODE == kDz) {
             const bool in = row < live;
             const int mine = in ? a.label[row] - a.first - column : -1;
-            const float off = in ? -a.lse[row] * kLog2e : 0.0f, g = in ? a.grad[row] : 0.0f;
+            const float off = in ? -a.lse[row] * kLog2e : 0.0f;
+            const float g = in ? a.grad[row] / scale_of(a.counts) : 0.0f;
             const Pair by = pair(kLog2e, kLog2e), minus = pair(off, off), scale = pair(g, g);
             each([&](int c, float (&v)[32]) {
                 // (rows beyond the live ones are zeros in the hidden states' copy: z = 0, g = 0)
@@ -377,8 +390,9 @@ struct Epilogue {
             stage.sent();                                // (an earlier tile's)
             each([&](int c, float (&v)[32]) {
                 Pair y[16];
+                const float by = scale_of(a.counts);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = pair(v[2 * i], v[2 * i + 1]);
+                for (int i = 0; i < 16; ++i) y[i] = mul2(pair(v[2 * i], v[2 * i + 1]), pair(by, by));
                 stage.put_half(y, c % 2);
                 if (c % 2 == 0 && c + 1 < parts) return;
                 __syncwarp();
@@ -426,6 +440,9 @@ struct Epilogue {
         } else {
             stage.sent();
             each([&](int c, float (&v)[32]) {
+                const float by = scale_of(a.counts);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] *= by;
                 stage.put(v);
                 __syncwarp();
                 const int first = column + 32 * c;
@@ -990,7 +1007,7 @@ head_few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ Fe
 
 // The places in the workspace that the first launches fill.
 struct HeadRows {
-    int32_t* counts;
+    int32_t* counts;              // live tokens, and (backward) the scale taken out of dz
     int32_t* index;               // token of a live row
     int32_t* slot;                // live row of a token, or -1
     int32_t* label;
@@ -1006,6 +1023,12 @@ __device__ __forceinline__ int32_t live_label(const HeadCall& c, int64_t t, bool
                                 : static_cast<const int32_t*>(c.labels)[t];
     const bool in = (!back || c.grad_loss[t] != 0.0f) & (y >= 0) & (y < c.vocab);
     return in ? static_cast<int32_t>(y) : -1;
+}
+
+// The size of a token's gradient of the loss, if it is finite.
+__device__ __forceinline__ float finite_grad(const HeadCall& c, int64_t t) {
+    const float g = fabsf(c.grad_loss[t]);
+    return g <= FLT_MAX ? g : 0.0f;
 }
 
 __device__ __forceinline__ void put_token(const HeadCall& c, const HeadRows& r, int64_t t,
@@ -1030,6 +1053,7 @@ constexpr int kRowThreads = 1024;
 __global__ void __launch_bounds__(kRowThreads)
 head_rows_kernel(const HeadCall c, const HeadRows r, bool back) {
     __shared__ int32_t warps[32];
+    __shared__ float grads[32];
     // a warp's tokens: whole runs of 32
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int64_t runs = (c.n_tokens + kRowThreads - 1) / kRowThreads;
@@ -1037,18 +1061,31 @@ head_rows_kernel(const HeadCall c, const HeadRows r, bool back) {
     auto label_of = [&](int64_t t) { return t < c.n_tokens ? live_label(c, t, back) : -1; };
     let_next_launch_begin();
     int32_t n = 0;
+    float g = 0.0f;
 #pragma unroll 8
-    for (int64_t i = 0; i < runs; ++i)
-        n += __popc(__ballot_sync(0xFFFFFFFFu, label_of(begin + 32 * i + lane) >= 0));
-    if (lane == 0) warps[warp] = n;
+    for (int64_t i = 0; i < runs; ++i) {
+        const int64_t t = begin + 32 * i + lane;
+        const bool live = label_of(t) >= 0;
+        n += __popc(__ballot_sync(0xFFFFFFFFu, live));
+        if (back && live) g = fmaxf(g, finite_grad(c, t));
+    }
+    g = warp_max(g);
+    if (lane == 0) {
+        warps[warp] = n;
+        grads[warp] = g;
+    }
     __syncthreads();
+    g = warp_max(grads[lane]);
     int32_t at = lane < warp ? warps[lane] : 0, all = warps[lane];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         at += __shfl_xor_sync(0xFFFFFFFFu, at, o);
         all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
     }
-    if (threadIdx.x == 0) *r.counts = all;
+    if (threadIdx.x == 0) {
+        r.counts[0] = all;
+        r.counts[1] = scale_from(g);
+    }
 #pragma unroll 4
     for (int64_t i = 0; i < runs; ++i) {
         const int64_t t = begin + 32 * i + lane;
@@ -1123,6 +1160,7 @@ head_prepare_kernel(const HeadCall c, const HeadRows r, const HeadCopy copy, uns
         return;
     }
     __shared__ int32_t before[kPrepareTokens], total[kPrepareTokens];
+    __shared__ float grads[kPrepareTokens];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int n = static_cast<int>(c.n_tokens), base = blockIdx.x * kPrepareTokens;
     let_next_launch_begin();
@@ -1130,12 +1168,15 @@ head_prepare_kernel(const HeadCall c, const HeadRows r, const HeadCopy copy, uns
     const int32_t mine = lane < kPrepareTokens && base + lane < n ? live_label(c, base + lane, back) : -1;
     const uint32_t own = __ballot_sync(0xFFFFFFFFu, mine >= 0);
     int32_t b = 0, all = 0;
+    float g = 0.0f;
 #pragma unroll 8
     for (int t = threadIdx.x; t < n; t += kPrepareThreads) {
         const int live = live_label(c, t, back) >= 0;
         all += live;
         b += t < base ? live : 0;
+        if (back && live) g = fmaxf(g, finite_grad(c, t));
     }
+    g = warp_max(g);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
@@ -1144,6 +1185,7 @@ head_prepare_kernel(const HeadCall c, const HeadRows r, const HeadCopy copy, uns
     if (lane == 0) {
         before[warp] = b;
         total[warp] = all;
+        grads[warp] = g;
     }
     __syncthreads();
     b = all = 0;
@@ -1151,8 +1193,12 @@ head_prepare_kernel(const HeadCall c, const HeadRows r, const HeadCopy copy, uns
     for (int w = 0; w < kPrepareTokens; ++w) {
         b += before[w];
         all += total[w];
+        g = fmaxf(g, grads[w]);
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) *r.counts = all;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        r.counts[0] = all;
+        r.counts[1] = scale_from(g);
+    }
     const int32_t y = __shfl_sync(0xFFFFFFFFu, mine, warp);
     const int32_t j = b + __popc(own & ((1u << warp) - 1));
     const int t = base + warp;
@@ -1253,7 +1299,8 @@ constexpr int kFinishWarps = 8;
 
 template <bool WIDE, bool MANY>
 __global__ void __launch_bounds__(32 * kFinishWarps)
-head_finish_kernel(const int32_t* slot, const float* sums, int64_t rows, int32_t splits,
+head_finish_kernel(const int32_t* counts, const int32_t* slot, const float* sums, int64_t rows,
+                   int32_t splits,
                    int64_t n_tokens, int32_t dim, int32_t sections, uint16_t* out,
                    int64_t stride) {
     constexpr int N = kCopyColumns / 128;
@@ -1265,6 +1312,7 @@ head_finish_kernel(const int32_t* slot, const float* sums, int64_t rows, int32_t
     const int first = static_cast<int>(id - t * sections) * kCopyColumns + 4 * lane;
     wait_for_launch_before();
     const int32_t j = slot[t];
+    const float by = scale_of(counts);
     uint16_t* to = out + t * stride;
     float4 v[N];
     auto add = [](float4& x, const float4& y) {
@@ -1301,6 +1349,7 @@ head_finish_kernel(const int32_t* slot, const float* sums, int64_t rows, int32_t
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int c = first + 128 * i;
+        v[i] = make_float4(v[i].x * by, v[i].y * by, v[i].z * by, v[i].w * by);
         if (WIDE && c + 4 <= dim) {
             *reinterpret_cast<uint2*>(to + c) =
                 make_uint2(pack_bf16x2(v[i].x, v[i].y), pack_bf16x2(v[i].z, v[i].w));
@@ -1570,7 +1619,7 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, bool
         return here;
     };
     const int64_t n = n_tokens < 1 ? 1 : n_tokens;
-    p.counts = place(4);
+    p.counts = place(8);
     p.index = place(4 * n);
     p.slot = place(4 * n);
     p.label = place(4 * n);
@@ -1762,8 +1811,8 @@ cudaError_t launch_head_finish(const HeadCall& c, const HeadPlan& p, cudaStream_
         static_cast<unsigned>(many ? units : (units + kFinishWarps - 1) / kFinishWarps);
     const auto kernel = many ? (wide ? head_finish_kernel<true, true> : head_finish_kernel<false, true>)
                              : (wide ? head_finish_kernel<true, false> : head_finish_kernel<false, false>);
-    return launch_after(kernel, grid, 32 * kFinishWarps, 0, stream, at<int32_t>(c, p.slot),
-                        at<float>(c, p.sums), p.rows, p.splits,
+    return launch_after(kernel, grid, 32 * kFinishWarps, 0, stream, at<int32_t>(c, p.counts),
+                        at<int32_t>(c, p.slot), at<float>(c, p.sums), p.rows, p.splits,
                         c.n_tokens, c.dim, sections, c.grad_hidden, c.grad_hidden_stride);
 }
 

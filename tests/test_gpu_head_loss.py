@@ -310,6 +310,31 @@ def test_head_loss_of_no_tokens():
     assert bool((dw == 0.0).all())
 
 
+@pytest.mark.parametrize("n", [1, 12, 9000])
+def test_gradients_of_alike_losses_keep_their_size(n):
+    """Equal logits and one gradient of the loss, halfway between two of bf16 and of either
+    sign: softmax minus one is off by 2^-12 at most, and nothing else is rounded before the
+    result (2^-8 of it); 9000 terms' sum is off by 2^-10 of it more at most."""
+    vocab, d, size = 4096, 96, 0.5 + 2.0 ** -9
+    g = _gen("alike", n)
+    h = (torch.rand((n, d), generator=g) + 1.0).to(BF16).cuda()
+    w = torch.zeros((vocab, d), dtype=BF16, device="cuda")
+    y = torch.full((n,), 17, device="cuda")
+    lse = _loss(h, w, y)[1]
+    gl = torch.full((n,), -size if n == 12 else size, device="cuda")
+    if n > 1:
+        gl[1] = float("nan")
+        y[1] = -1
+    dh, dw = torch.empty_like(h), torch.empty_like(w)
+    _grad(h, w, y, lse, gl, dh, dw)
+    keep = (y >= 0).to(F64)[:, None]
+    total = (h.to(F64) * keep).sum(0) * gl[0].to(F64)
+    for row, want in ((17, total * (1.0 / vocab - 1.0)), (5, total / vocab)):
+        off = ((dw[row].to(F64) - want) / want).abs()
+        assert float(off.max()) <= 2.0 ** -8 + 2.0 ** -12 + 2.0 ** -10
+    assert bool((dh == 0.0).all())
+
+
 def _mixed_calls(stream=None, key="mixed"):
     g, h, w, y = _inputs((key,), 500, 3001, 136, 0, 0, "some")
     n, vocab, d = 500, 3001, 136
