@@ -137,7 +137,8 @@ __device__ __forceinline__ int live_rows(const HeadArgs& a) {
 // What is taken out of dz before it is rounded to bf16, and put back to the products' sums:
 // the mantissa, 1 <= m < 2, of the largest finite gradient of a loss.  Where all are alike
 // (one over the tokens), their rounding would be the same error in every term, which no sum
-// averages away; so it is none (817 live tokens 32003 x 770 0.0023 -> @@).
+// averages away; so it is none (817 live tokens, 32003 x 770: both gradients
+// 0.0023 off, 0.0019 so, of which 0.0017 is their own rounding).
 __device__ __forceinline__ float scale_of(const int32_t* counts) {
     return __int_as_float(counts[1]);
 }
@@ -273,6 +274,7 @@ struct Epilogue {
     float2 (*both)[kHalf];        // what the second half of the columns found, by row
     int live, place, half, lane;  // place: this warp's first row of the CTA's 128
     int width, begin, parts;             // this warp's columns: 32 begin ..., of the tile's
+    float scale;                         // taken out of dz
     __device__ Epilogue(const HeadArgs& args, int n_live, char* staging, float2 (*found)[kHalf],
                         int warp, int l)
         : a(args),
@@ -282,7 +284,8 @@ struct Epilogue {
           place(warp % 4 * 32),
           half((warp - 2) / 4),
           lane(l),
-          width(MODE != kProducts ? args.width : KIND == kDh ? args.width_h : args.width_w) {
+          width(MODE != kProducts ? args.width : KIND == kDh ? args.width_h : args.width_w),
+          scale(MODE == kDz || (MODE == kProducts && KIND == kDw) ? scale_of(args.counts) : 1.0f) {
         // the first half has the odd part
         constexpr int kUnit = MODE == kDz ? 2 : 1;
         const int all = width / 32, first = (all / kUnit + 1) / 2 * kUnit;
@@ -344,15 +347,15 @@ struct Epilogue {
             const bool in = row < live;
             const int mine = in ? a.label[row] - a.first - column : -1;
             const float off = in ? -a.lse[row] * kLog2e : 0.0f;
-            const float g = in ? a.grad[row] / scale_of(a.counts) : 0.0f;
-            const Pair by = pair(kLog2e, kLog2e), minus = pair(off, off), scale = pair(g, g);
+            const float g = in ? a.grad[row] / scale : 0.0f;
+            const Pair by = pair(kLog2e, kLog2e), minus = pair(off, off), times = pair(g, g);
             each([&](int c, float (&v)[32]) {
                 // (rows beyond the live ones are zeros in the hidden states' copy: z = 0, g = 0)
                 Pair y[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float2 x = unpair(fma2(pair(v[2 * i], v[2 * i + 1]), by, minus));
-                    y[i] = mul2(pair(exp2_fast(x.x), exp2_fast(x.y)), scale);
+                    y[i] = mul2(pair(exp2_fast(x.x), exp2_fast(x.y)), times);
                 }
                 if (mine >= 32 * c && mine < 32 * c + 32) {
 #pragma unroll
@@ -390,9 +393,9 @@ struct Epilogue {
             stage.sent();                                // (an earlier tile's)
             each([&](int c, float (&v)[32]) {
                 Pair y[16];
-                const float by = scale_of(a.counts);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = mul2(pair(v[2 * i], v[2 * i + 1]), pair(by, by));
+                for (int i = 0; i < 16; ++i)
+                    y[i] = mul2(pair(v[2 * i], v[2 * i + 1]), pair(scale, scale));
                 stage.put_half(y, c % 2);
                 if (c % 2 == 0 && c + 1 < parts) return;
                 __syncwarp();
@@ -440,9 +443,8 @@ struct Epilogue {
         } else {
             stage.sent();
             each([&](int c, float (&v)[32]) {
-                const float by = scale_of(a.counts);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= by;
+                for (int i = 0; i < 32; ++i) v[i] *= scale;
                 stage.put(v);
                 __syncwarp();
                 const int first = column + 32 * c;
@@ -477,15 +479,26 @@ struct Epilogue {
                                     narrow2(x[0]), narrow2(x[1]), narrow2(x[2]), narrow2(x[3]));
                         }
                     }
-                } else {                                 // a column a lane, row by row
+                } else {                                 // a column a lane, 8 rows at a time
+                    // (7 tokens, 100000 x 4000 1.61 ms; row by row 4.30, by 16 1.56 and
+                    // registers spilled, 3 % of the other forms)
                     const int col = first + lane;
                     if (col < a.dim) {
                         uint16_t* to = a.grad_table + static_cast<int64_t>(row0) * a.dim + col;
                         const int rows = min(32, a.vocab - row0);
-#pragma unroll 8
-                        for (int r = 0; r < rows; ++r) {
-                            uint16_t& w = to[static_cast<int64_t>(r) * a.dim];
-                            w = float_to_bf16_rn(stage.value(r, lane) + bf16_to_float(w));
+#pragma unroll 1
+                        for (int r0 = 0; r0 < rows; r0 += 8) {
+                            uint16_t old[8];
+#pragma unroll
+                            for (int r = 0; r < 8; ++r) {
+                                old[r] = 0;
+                                if (r0 + r < rows) old[r] = to[static_cast<int64_t>(r0 + r) * a.dim];
+                            }
+#pragma unroll
+                            for (int r = 0; r < 8; ++r)
+                                if (r0 + r < rows)
+                                    to[static_cast<int64_t>(r0 + r) * a.dim] = float_to_bf16_rn(
+                                        stage.value(r0 + r, lane) + bf16_to_float(old[r]));
                         }
                     }
                 }
