@@ -11,8 +11,11 @@
 // works through the vocabulary in pieces: the piece's z again, its dz in bf16 to the
 // workspace, then dz W, added up in fp32 over the pieces, and dz^T h.
 //
-// dz is rounded to bf16 because the tensor cores multiply bf16: 2^-8 of each term at most,
-// averaged over sums of many terms; its sums are held in fp32.
+// dz is rounded to bf16 because the tensor cores multiply bf16: 2^-8 of each term at most; its
+// sums are held in fp32.  Where many tokens are live these roundings are as large as the
+// result's own, and a second part of dz would cost as much again as the products of the first.
+// Up to 128 live tokens leave half of a tile's rows free, and these hold what the rounding
+// left, in bf16 too: 2^-16 of each term at most.
 //
 // Only live tokens take part: their hidden rows are copied side by side, so that a prompt's
 // tokens without a label cost nothing and their values reach nothing.
@@ -145,6 +148,10 @@ __device__ __forceinline__ float scale_of(const int32_t* counts) {
 __device__ __forceinline__ int32_t scale_from(float largest) {
     return (__float_as_int(largest) & 0x7FFFFF) | 0x3F800000;
 }
+// Whether dz is in two parts: so few live tokens that the rows of the tile's second half take
+// what rounding to bf16 left of the first half's.  (One live token, 20000 x 4096: gradients off
+// by up to 0.0041, 0.0017 so.  32 tokens, 50257 x 768 TIME1 us, in one part TIME0.)
+__device__ __forceinline__ bool dz_in_two(int live) { return live <= kHalf; }
 // A row's label in the piece, or another number.
 __device__ __forceinline__ int label_in_piece(const HeadArgs& a, int row) {
     if (a.label != nullptr) return a.label[row] - a.first;
@@ -197,8 +204,10 @@ struct Tiles {
         : first(MODE != kProducts ? Grid(live, a.vocab, a.dim, a.width, 1, a.group)
                                   : Grid(a.want_h ? live : 0, a.dim, a.vocab, a.width_h, a.splits,
                                          a.group)),
-          // (nothing to add: the table's gradient stays untouched)
-          second(MODE != kProducts || !a.want_w || (a.add_w && live == 0) ? 0 : a.vocab, a.dim, live,
+          // (nothing to add: the table's gradient stays untouched; dz in two parts: the steps
+          // along the tokens twice)
+          second(MODE != kProducts || !a.want_w || (a.add_w && live == 0) ? 0 : a.vocab, a.dim,
+                 dz_in_two(live) ? 2 * ((live + kTileK - 1) / kTileK) * kTileK : live,
                  MODE != kProducts ? kPairTile : a.width_w, 1, a.group),
           total(first.total + second.total) {}
     template <class F>
@@ -344,10 +353,12 @@ struct Epilogue {
                     m, sum * exp2_fast(top - from) + o.y * exp2_fast(o.x - from));
             }
         } else if constexpr (MODE == kDz) {
-            const bool in = row < live;
-            const int mine = in ? a.label[row] - a.first - column : -1;
-            const float off = in ? -a.lse[row] * kLog2e : 0.0f;
-            const float g = in ? a.grad[row] / scale : 0.0f;
+            const bool two = dz_in_two(live), rest = two && row0 >= kHalf;   // of the warp
+            const int token = two ? row % kHalf : row;
+            const bool in = token < live;
+            const int mine = in ? a.label[token] - a.first - column : -1;
+            const float off = in ? -a.lse[token] * kLog2e : 0.0f;
+            const float g = in ? a.grad[token] / scale : 0.0f;
             const Pair by = pair(kLog2e, kLog2e), minus = pair(off, off), times = pair(g, g);
             each([&](int c, float (&v)[32]) {
                 // (rows beyond the live ones are zeros in the hidden states' copy: z = 0, g = 0)
@@ -373,6 +384,11 @@ struct Epilogue {
                         y[i] = pair(first + 2 * i < a.vocab ? x.x : 0.0f,
                                     first + 2 * i + 1 < a.vocab ? x.y : 0.0f);
                     }
+                }
+                if (rest) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        y[i] = fma2(widen2(narrow2(y[i])), pair(-1.0f, -1.0f), y[i]);
                 }
                 if (c % 2 == 0) stage.sent();
                 stage.put_half(y, c % 2);
@@ -540,6 +556,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
     let_next_launch_begin();
     wait_for_launch_before();
     const int live = live_rows(a);
+    const bool two = !is_loss(MODE) && dz_in_two(live);
     const Tiles<MODE> tiles(a, live);
 
     if (warp == 0) {
@@ -557,7 +574,10 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                     const uint32_t bytes =
                         2 * (kOperandBytes +
                              (kBmn ? (two_chunks ? 2 : 1) * kChunkBytes : width / 2 * 128));
-                    const int m0 = t.m * kPairTile + static_cast<int>(rank) * kHalf;
+                    // (dz in two parts: both CTAs have the same tokens' logits)
+                    const int m0 = t.m * kPairTile +
+                                   (MODE == kDz && two ? 0 : static_cast<int>(rank) * kHalf);
+                    const int steps = t.end / 2;         // of a part of dz, for kDw
                     const int n0 = t.n * width + static_cast<int>(rank) * (width / 2);
                     const CUtensorMap* map_a = KIND == kDw ? &maps.aw : &maps.a;
                     const CUtensorMap* map_b = KIND == kDw ? &maps.bw : &maps.b;
@@ -569,18 +589,20 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                         const uint32_t bar = smem_address(&sh.full[s]);
                         const uint32_t to_a = ring + s * kStageBytes, to_b = to_a + kOperandBytes;
                         if (rank == 0) bar_expect(bar, bytes);
+                        const bool rest = KIND == kDw && two && k >= steps;
+                        const int k0 = (rest ? k - steps : k) * kTileK;
                         if constexpr (KIND == kDw) {
-                            tma_load(to_a, map_a, 0, k * kTileK, m0 / 64, bar);
-                            tma_load(to_a + kChunkBytes, map_a, 0, k * kTileK, m0 / 64 + 1, bar);
+                            const int row = k0 + (rest ? kHalf : 0);
+                            tma_load(to_a, map_a, 0, row, m0 / 64, bar);
+                            tma_load(to_a + kChunkBytes, map_a, 0, row, m0 / 64 + 1, bar);
                         } else if constexpr (KIND == kDh) {
                             tma_load(to_a, map_a, 0, m0, k, bar);
                         } else {
                             tma_load(to_a, map_a, k * kTileK, m0, bar);
                         }
                         if constexpr (kBmn) {
-                            tma_load(to_b, map_b, n0, k * kTileK, bar);
-                            if (two_chunks)
-                                tma_load(to_b + kChunkBytes, map_b, n0 + 64, k * kTileK, bar);
+                            tma_load(to_b, map_b, n0, k0, bar);
+                            if (two_chunks) tma_load(to_b + kChunkBytes, map_b, n0 + 64, k0, bar);
                         } else {
                             tma_load(to_b, map_b, k * kTileK, n0, bar);
                         }
@@ -1326,6 +1348,7 @@ head_finish_kernel(const int32_t* counts, const int32_t* slot, const float* sums
     wait_for_launch_before();
     const int32_t j = slot[t];
     const float by = scale_of(counts);
+    const bool two = dz_in_two(*counts);
     uint16_t* to = out + t * stride;
     float4 v[N];
     auto add = [](float4& x, const float4& y) {
@@ -1342,9 +1365,11 @@ head_finish_kernel(const int32_t* counts, const int32_t* slot, const float* sums
         for (int s = MANY ? warp : 0; s < splits; s += MANY ? kFinishWarps : 1) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                if (first + 128 * i < dim)
-                    add(v[i], *reinterpret_cast<const float4*>(
-                                  from + (static_cast<int64_t>(s) * blocks + 4 * i) * rows * 32));
+                if (first + 128 * i < dim) {
+                    const float* p = from + (static_cast<int64_t>(s) * blocks + 4 * i) * rows * 32;
+                    add(v[i], *reinterpret_cast<const float4*>(p));
+                    if (two) add(v[i], *reinterpret_cast<const float4*>(p + kHalf * 32));
+                }
             }
         }
     }
