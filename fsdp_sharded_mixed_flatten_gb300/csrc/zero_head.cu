@@ -149,8 +149,9 @@ __device__ __forceinline__ int32_t scale_from(float largest) {
     return (__float_as_int(largest) & 0x7FFFFF) | 0x3F800000;
 }
 // Whether dz is in two parts: so few live tokens that the rows of the tile's second half take
-// what rounding to bf16 left of the first half's.  (One live token, 20000 x 4096: gradients off
-// by up to 0.0041, 0.0017 so.  32 tokens, 50257 x 768 TIME1 us, in one part TIME0.)
+// what rounding to bf16 left of the first half's.  (One live token, 20000 x 4096: gradients
+// off by up to 0.0041, 0.0017 so.  32 tokens, 50257 x 768 91 us, in one part 89; 128 tokens,
+// 128000 x 4096 774 us and 745.)
 __device__ __forceinline__ bool dz_in_two(int live) { return live <= kHalf; }
 // A row's label in the piece, or another number.
 __device__ __forceinline__ int label_in_piece(const HeadArgs& a, int row) {
@@ -357,15 +358,18 @@ struct Epilogue {
             const int token = two ? row % kHalf : row;
             const bool in = token < live;
             const int mine = in ? a.label[token] - a.first - column : -1;
-            const float off = in ? -a.lse[token] * kLog2e : 0.0f;
+            const float off = in ? -a.lse[token] : 0.0f;
             const float g = in ? a.grad[token] / scale : 0.0f;
             const Pair by = pair(kLog2e, kLog2e), minus = pair(off, off), times = pair(g, g);
             each([&](int c, float (&v)[32]) {
                 // (rows beyond the live ones are zeros in the hidden states' copy: z = 0, g = 0)
+                // z - lse before anything is multiplied: of large logits only their
+                // difference counts, and where it is small it is exact.
                 Pair y[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float2 x = unpair(fma2(pair(v[2 * i], v[2 * i + 1]), by, minus));
+                    const float2 x =
+                        unpair(mul2(add2(pair(v[2 * i], v[2 * i + 1]), minus), by));
                     y[i] = mul2(pair(exp2_fast(x.x), exp2_fast(x.y)), times);
                 }
                 if (mine >= 32 * c && mine < 32 * c + 32) {
