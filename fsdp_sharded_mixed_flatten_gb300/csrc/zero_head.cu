@@ -56,12 +56,12 @@ constexpr int kEpilogueWarps = 8;
 constexpr size_t kHeadSmem = kStages * kStageBytes + kEpilogueWarps * kStagingBytes + 1024;
 constexpr int kHeadThreads = 64 + 32 * kEpilogueWarps;
 constexpr uint32_t kTmemColumns = 512;      // two tiles' results
-// Steps that are summed in tensor memory at a time where logits become a loss.  Sums there
-// are cut off, not rounded: a loss of 4096 columns summed in one go was 2.0e-6 of itself off,
-// four times as far as by plain fp32 products; in parts of 1536 columns that are added up in
-// registers 6.6e-7 (1024: 4.6e-7, 2048: 9.8e-7; the parts cost 4 to 6 % of the time).
-// The gradient's logits end in bf16 and are summed in one go.
-constexpr int kLossSteps = 24;
+// Steps of a logit's sum that are summed in tensor memory at a time.  Sums there are cut off,
+// not rounded: a loss of 4096 columns summed in one go was 2.0e-6 of itself off, four times as
+// far as by plain fp32 products; in parts of 1536 columns that are added up in registers
+// 6.6e-7 (1024: 4.6e-7, 2048: 9.8e-7; the parts cost 4 to 6 % of the time).  The gradient's
+// logits are summed in the same parts: its probabilities are next to 1 where the loss's are.
+constexpr int kLogitSteps = 24;
 constexpr uint64_t kHeadWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInvLog2e = static_cast<float>(1.0 / static_cast<double>(kLog2e));
@@ -70,9 +70,13 @@ constexpr float kInvLog2eLo = static_cast<float>(1.0 / static_cast<double>(kLog2
 
 // What a launch computes: rows' statistics, the logits' gradient, or both gradients that are
 // products of it: tiles of the hidden states' first, then of the table's.
-// (kLossLong: rows' statistics from logits that are summed in several parts.)
-enum Mode { kLoss, kLossLong, kDz, kProducts };
+// (kLossLong, kDzLong: from logits that are summed in several parts.)
+enum Mode { kLoss, kLossLong, kDz, kDzLong, kProducts };
 __host__ __device__ constexpr bool is_loss(int mode) { return mode == kLoss || mode == kLossLong; }
+__host__ __device__ constexpr bool is_dz(int mode) { return mode == kDz || mode == kDzLong; }
+__host__ __device__ constexpr bool is_long(int mode) {
+    return mode == kLossLong || mode == kDzLong;
+}
 // What a tile of the last is.
 enum Kind { kDh, kDw };
 
@@ -100,7 +104,7 @@ struct HeadArgs {
     int32_t want_h, want_w;       // the hidden states' gradient, the table's
     int32_t add_h, add_w;         // to the sums, to the table's gradient, that are there
     int32_t wide;                 // rows of the table's gradient on 16-byte boundaries
-    int32_t width;                // columns of a tile, a multiple of 32 (kDz: of 64)
+    int32_t width;                // columns of a tile, a multiple of 32 (dz: of 64)
     int32_t width_h, width_w;     // of the two products' tiles
     int32_t part;                 // of a row's maxima and sums, the piece's first
     int32_t n_rows;
@@ -295,9 +299,9 @@ struct Epilogue {
           half((warp - 2) / 4),
           lane(l),
           width(MODE != kProducts ? args.width : KIND == kDh ? args.width_h : args.width_w),
-          scale(MODE == kDz || (MODE == kProducts && KIND == kDw) ? scale_of(args.counts) : 1.0f) {
+          scale(is_dz(MODE) || (MODE == kProducts && KIND == kDw) ? scale_of(args.counts) : 1.0f) {
         // the first half has the odd part
-        constexpr int kUnit = MODE == kDz ? 2 : 1;
+        constexpr int kUnit = is_dz(MODE) ? 2 : 1;
         const int all = width / 32, first = (all / kUnit + 1) / 2 * kUnit;
         begin = half == 0 ? 0 : first;
         parts = half == 0 ? first : all - first;
@@ -353,7 +357,7 @@ struct Epilogue {
                 a.parts[row * a.parts_pitch + a.part + n] = make_float2(
                     m, sum * exp2_fast(top - from) + o.y * exp2_fast(o.x - from));
             }
-        } else if constexpr (MODE == kDz) {
+        } else if constexpr (is_dz(MODE)) {
             const bool two = dz_in_two(live), rest = two && row0 >= kHalf;   // of the warp
             const int token = two ? row % kHalf : row;
             const bool in = token < live;
@@ -580,7 +584,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                              (kBmn ? (two_chunks ? 2 : 1) * kChunkBytes : width / 2 * 128));
                     // (dz in two parts: both CTAs have the same tokens' logits)
                     const int m0 = t.m * kPairTile +
-                                   (MODE == kDz && two ? 0 : static_cast<int>(rank) * kHalf);
+                                   (is_dz(MODE) && two ? 0 : static_cast<int>(rank) * kHalf);
                     const int steps = t.end / 2;         // of a part of dz, for kDw
                     const int n0 = t.n * width + static_cast<int>(rank) * (width / 2);
                     const CUtensorMap* map_a = KIND == kDw ? &maps.aw : &maps.a;
@@ -632,9 +636,9 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                                                        KIND == kDh   ? a.width_h
                                                        : KIND == kDw ? a.width_w
                                                                      : a.width);
-                    // a result in tensor memory: of all steps, or of some (kLossLong)
+                    // a result in tensor memory: of all steps, or of some (kLossLong, kDzLong)
                     for (int begin = t.begin; begin < t.end;) {
-                        const int end = MODE == kLossLong ? min(begin + kLossSteps, t.end) : t.end;
+                        const int end = is_long(MODE) ? min(begin + kLogitSteps, t.end) : t.end;
                         const int slot = n % 2;
                         run = wait(sh, sh.taken[slot], (n / 2 + 1) % 2);
                         if (!run) return;
@@ -717,7 +721,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                 const uint32_t from = place(slot);
                 auto release = [&] { free_place(slot); };
                 epilogue(row0, t.n, t.split, turn, [&](auto&& f) {
-                    if constexpr (MODE == kLossLong) {
+                    if constexpr (is_long(MODE)) {
                         float sum[4][32];
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
@@ -726,7 +730,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
 #pragma unroll
                         for (int c = 0; c < 4; ++c) tmem_load_wait(sum[c]);
                         release();
-                        for (int k = kLossSteps; k < t.end; k += kLossSteps) {
+                        for (int k = kLogitSteps; k < t.end; k += kLogitSteps) {
                             const int next = come();
                             const uint32_t more = place(next);
 #pragma unroll
@@ -913,14 +917,14 @@ head_few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ Fe
             bool run = true;
             for (int u = begin; run && u < end; u += kUnits) {
                 // (rows of a tile beyond the CTA's share: what an earlier tile left there)
-                for (int from = 0; run && from < steps; from += kLossSteps) {
+                for (int from = 0; run && from < steps; from += kLogitSteps) {
                     const int slot = n % 2;
                     run = wait(sh, sh.taken[slot], (n / 2 + 1) % 2);
                     if (!run) break;
                     ++n;
                     fence_after_sync();
                     const uint32_t d = tmem + slot * kFewMost;
-                    for (int k = from; k < min(from + kLossSteps, steps); ++k) {
+                    for (int k = from; k < min(from + kLogitSteps, steps); ++k) {
                         run = wait(sh, sh.full[s], phase);
                         if (!run) break;
                         fence_after_sync();
@@ -960,7 +964,7 @@ head_few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ Fe
             const int place = part * 32 + lane, row = u * kFewUnit + place;
             const bool in = place < (end - u) * kFewUnit && row < a.vocab;
             float z[32];
-            for (int from = 0; from < steps; from += kLossSteps) {
+            for (int from = 0; from < steps; from += kLogitSteps) {
                 const int slot = n % 2;
                 wait(sh, sh.done[slot], (n / 2) % 2);
                 __syncwarp();
@@ -1795,8 +1799,8 @@ cudaError_t launch_head_loss(const HeadCall& c, const HeadPlan& p, int64_t first
         a.n_rows = static_cast<int32_t>(c.n_tokens);
     }
     const int64_t tiles = p.rows / kPairTile * tiles_of(a.vocab, a.width);
-    return c.dim <= kLossSteps * kTileK ? launch_product<kLoss>(maps, a, tiles, stream)
-                                        : launch_product<kLossLong>(maps, a, tiles, stream);
+    return c.dim <= kLogitSteps * kTileK ? launch_product<kLoss>(maps, a, tiles, stream)
+                                         : launch_product<kLossLong>(maps, a, tiles, stream);
 }
 
 cudaError_t launch_head_join(const HeadCall& c, const HeadPlan& p, cudaStream_t stream) {
@@ -1818,7 +1822,9 @@ cudaError_t launch_head_dz(const HeadCall& c, const HeadPlan& p, int64_t first,
     if (cudaError_t e = piece_map(&maps.b, c, p, first, p.width_z / 2); e != cudaSuccess) return e;
     HeadArgs a = product_args(c, p, first);
     a.width = p.width_z;
-    return launch_product<kDz>(maps, a, p.rows / kPairTile * tiles_of(a.vocab, a.width), stream);
+    const int64_t tiles = p.rows / kPairTile * tiles_of(a.vocab, a.width);
+    return c.dim <= kLogitSteps * kTileK ? launch_product<kDz>(maps, a, tiles, stream)
+                                         : launch_product<kDzLong>(maps, a, tiles, stream);
 }
 
 cudaError_t launch_head_products(const HeadCall& c, const HeadPlan& p, int64_t first,
