@@ -64,9 +64,6 @@ constexpr uint32_t kTmemColumns = 512;      // two tiles' results
 constexpr int kLogitSteps = 24;
 constexpr uint64_t kHeadWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kInvLog2e = static_cast<float>(1.0 / static_cast<double>(kLog2e));
-constexpr float kInvLog2eLo = static_cast<float>(1.0 / static_cast<double>(kLog2e) -
-                                                 static_cast<double>(kInvLog2e));
 
 // What a launch computes: rows' statistics, the logits' gradient, or both gradients that are
 // products of it: tiles of the hidden states' first, then of the table's.
@@ -88,7 +85,7 @@ struct HeadArgs {
     const void* labels;           // of all, int32 or int64
     const float* lse;
     const float* grad;
-    float2* parts;                // [rows][parts_pitch]: maximum (times log2 e) and sum of a tile
+    float2* parts;                // [rows][parts_pitch]: maximum and sum of a tile
     float* picked;                // z[label]
     // Row by row 128 bytes, whose 16-byte words are in the order that 128-byte swizzling
     // gives them in shared memory: word j of row r is at j ^ (r % 8).
@@ -332,15 +329,16 @@ struct Epilogue {
                 float m = v[0];
 #pragma unroll
                 for (int i = 1; i < 32; ++i) m = fmaxf(m, v[i]);
-                m = fmaxf(top, m * kLog2e);
-                // (-inf alone: no term)
+                m = fmaxf(top, m);
+                // Differences before anything is multiplied: they are as exact as logits of
+                // any size hold them.  (-inf alone: no term)
                 const float from = m == -INFINITY ? 0.0f : m;
                 const Pair by = pair(kLog2e, kLog2e), minus = pair(-from, -from);
-                sum *= exp2_fast(top - from);
+                sum *= exp2_fast((top - from) * kLog2e);
                 Pair t = 0;
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
-                    const float2 x = unpair(fma2(pair(v[i], v[i + 1]), by, minus));
+                    const float2 x = unpair(mul2(add2(pair(v[i], v[i + 1]), minus), by));
                     t = add2(t, pair(exp2_fast(x.x), exp2_fast(x.y)));
                 }
                 const float2 s = unpair(t);
@@ -355,7 +353,8 @@ struct Epilogue {
                 const float2 o = both[slot][place + lane];
                 const float m = fmaxf(top, o.x), from = m == -INFINITY ? 0.0f : m;
                 a.parts[row * a.parts_pitch + a.part + n] = make_float2(
-                    m, sum * exp2_fast(top - from) + o.y * exp2_fast(o.x - from));
+                    m, sum * exp2_fast((top - from) * kLog2e) +
+                           o.y * exp2_fast((o.x - from) * kLog2e));
             }
         } else if constexpr (is_dz(MODE)) {
             const bool two = dz_in_two(live), rest = two && row0 >= kHalf;   // of the warp
@@ -1026,11 +1025,8 @@ head_few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ Fe
                 const float2 o = own[i * 32 * kPitch + lane];
                 join(m, l, o.x, o.y);
             }
-            // The parts' maxima are rounded multiples of log2 e, the sums relative to those.
-            const float y = m * kLog2e;
-            if (l != 0.0f) l *= exp2_fast(__fmaf_rn(m, kLog2e, -y));
             a.parts[(first + lane) * static_cast<int64_t>(gridDim.x) + blockIdx.x] =
-                make_float2(y, l);
+                make_float2(m, l);
         }
     }
     __syncwarp();
@@ -1310,7 +1306,7 @@ head_join_kernel(const HeadCall c, const int32_t* counts, const int32_t* index,
     for (int i = lane; i < n_parts; i += 32) {
         const float2 v = p[i];
         const float m = fmaxf(top, v.x), from = m == -INFINITY ? 0.0f : m;
-        sum = sum * exp2f(top - from) + v.y * exp2f(v.x - from);
+        sum = sum * exp2f((top - from) * kLog2e) + v.y * exp2f((v.x - from) * kLog2e);
         top = m;
     }
 #pragma unroll
@@ -1318,20 +1314,17 @@ head_join_kernel(const HeadCall c, const int32_t* counts, const int32_t* index,
         const float t = __shfl_xor_sync(0xFFFFFFFFu, top, o), s = __shfl_xor_sync(0xFFFFFFFFu, sum, o);
         const float m = fmaxf(top, t), from = m == -INFINITY ? 0.0f : m;
         // (both lanes of a pair add the same two terms)
-        const float x = sum * exp2f(top - from), y = s * exp2f(t - from);
+        const float x = sum * exp2f((top - from) * kLog2e), y = s * exp2f((t - from) * kLog2e);
         sum = x + y;
         top = m;
     }
     if (lane == 0) {
-        // The logit of `top` is top divided by the very constant it was multiplied by, a
-        // factor in two parts; the loss is what it lies above the label's, rounded once,
-        // and the sum's logarithm: two numbers that are not negative.
+        // The loss is what the largest logit lies above the label's, and the logarithm of a
+        // sum that holds the largest one's 1: two numbers that are not negative.
         const float l = logf(sum);
         const int64_t t = as_they_are ? row : index[row];
-        const float d = __fmaf_rn(top, kInvLog2eLo, __fmaf_rn(top, kInvLog2e, -of_label)) + l;
-        c.loss[t] = !live || d < 0.0f ? 0.0f : d;
-        if (c.lse != nullptr)
-            c.lse[t] = live ? __fmaf_rn(top, kInvLog2e, __fmaf_rn(top, kInvLog2eLo, l)) : 0.0f;
+        c.loss[t] = live ? (top - of_label) + l : 0.0f;
+        if (c.lse != nullptr) c.lse[t] = live ? top + l : 0.0f;
     }
 }
 
