@@ -153,11 +153,12 @@ __device__ __forceinline__ uint4 shifted(uint4 lo, uint4 hi, int by) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 1 / sqrt(x): the approximation and one Newton step.
+// 1 / sqrt(x): the approximation and one Newton step (but for 0 and infinity, of which that
+// would make NaN).
 __device__ __forceinline__ float inv_sqrt(float x) {
     const float y = rsqrtf(x);
     const float z = y * __fmaf_rn(-0.5f * x * y, y, 1.5f);
-    return y == __builtin_huge_valf() ? y : z;
+    return y > 0.0f && y < __builtin_huge_valf() ? z : y;
 }
 
 // --------------------------------------------------------- token table ------

@@ -61,6 +61,29 @@ __device__ __forceinline__ float rms_group_sum(const RmsGroup& g, float v,
     return v;
 }
 
+// 1 / sqrt(mean(s^2) + eps) of a row whose squares this thread has added up to q.  Where the
+// row's sum leaves fp32 (values of 1e17 and more), it is made once more of values times 2^-72:
+// the largest, 2^128, then have squares of 2^112 and 16384 of them a sum that fp32 holds, and
+// what is small beside them counts for nothing.
+template <int K>
+__device__ __forceinline__ float row_rstd(const RmsGroup& g, const float (&s)[K][8], float q,
+                                          float inv_d, float eps, float (*red)[kRmsWarps],
+                                          int& half) {
+    float r = inv_sqrt(__fmaf_rn(rms_group_sum(g, q, red, half), inv_d, eps));
+    if (__builtin_expect(r == 0.0f, 0)) {
+        constexpr float kBy = 0x1p-72f;
+        q = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q = __fmaf_rn(s[k][e] * kBy, s[k][e] * kBy, q);
+        }
+        q = rms_group_sum(g, q, red, half);
+        r = inv_sqrt(__fmaf_rn(q, inv_d, eps * kBy * kBy)) * kBy;
+    }
+    return r;
+}
+
 template <class T, int K, bool WIDE>
 __global__ void __launch_bounds__(512, K == 1 ? 2 : 1)
 rms_norm_kernel(const __grid_constant__ RmsArgs a) {
@@ -112,7 +135,7 @@ rms_norm_kernel(const __grid_constant__ RmsArgs a) {
                 c.store_eight(a.total8 + row * a.total8_stride, a.total8_scales + row * a.blocks,
                               k, s[k]);
         }
-        const float r = inv_sqrt(__fmaf_rn(rms_group_sum(g, q, red, half), inv_d, a.eps));
+        const float r = row_rstd(g, s, q, inv_d, a.eps, red, half);
         if (g.t == 0 && a.rstd != nullptr) a.rstd[row] = r;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -429,7 +452,7 @@ rms_rows_kernel(const __grid_constant__ RmsArgs a) {
                 q = __fmaf_rn(s[k][e], s[k][e], q);
             }
         }
-        const float r = inv_sqrt(__fmaf_rn(rms_group_sum(g, q, red, half), inv_d, a.eps));
+        const float r = row_rstd(g, s, q, inv_d, a.eps, red, half);
         if (g.t == 0) {
             fill(row + ring.slots * step, ring.at);
             if (a.rstd != nullptr) a.rstd[row] = r;
