@@ -1679,6 +1679,17 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, bool
     return p;
 }
 
+// A smaller call's pieces may be larger and its splits more, and with them its needs.  A plan
+// goes by whole tiles and, for the table's gradient, steps of tokens, and grows within them.
+int64_t head_bytes(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, bool in_place) {
+    int64_t most = head_plan(n_tokens, vocab, dim, back, in_place).bytes;
+    for (int64_t n = kTileK; n < n_tokens; n += kTileK) {
+        const int64_t bytes = head_plan(n, vocab, dim, back, in_place).bytes;
+        if (bytes > most) most = bytes;
+    }
+    return most;
+}
+
 bool head_table_in_place(const HeadCall& c) { return aligned_to(c.table, 16) && c.dim % 8 == 0; }
 
 bool head_rows_as_they_are(const HeadCall& c) { return rows_as_they_are(c); }

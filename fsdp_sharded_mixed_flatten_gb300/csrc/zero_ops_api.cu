@@ -625,8 +625,8 @@ int head_workspace(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, int6
     if (bytes == nullptr) return fail(ZERO_ERR_INVALID_ARG, "bytes is NULL");
     if (int rc = check_head(n_tokens, vocab, dim)) return rc;
     // wherever the table lies
-    const int64_t in_place = zf::head_plan(n_tokens, vocab, dim, back, true).bytes;
-    const int64_t copied = zf::head_plan(n_tokens, vocab, dim, back, false).bytes;
+    const int64_t in_place = zf::head_bytes(n_tokens, vocab, dim, back, true);
+    const int64_t copied = zf::head_bytes(n_tokens, vocab, dim, back, false);
     *bytes = in_place > copied ? in_place : copied;
     return ok();
 }

@@ -146,6 +146,7 @@ def zero_rms_norm_grad(grad_out, total, weight, rstd, grad_x, grad_weight=None, 
 
 
 def zero_head_loss_workspace_bytes(n_tokens: int, vocab: int, dim: int) -> int:
+    """Bytes that zero_head_loss of up to n_tokens tokens needs."""
     out = ctypes.c_int64(0)
     f = "zero_head_loss_workspace_bytes"
     _check(load().zero_head_loss_workspace_bytes(n_tokens, vocab, dim, ctypes.byref(out)), f)
@@ -153,6 +154,7 @@ def zero_head_loss_workspace_bytes(n_tokens: int, vocab: int, dim: int) -> int:
 
 
 def zero_head_loss_grad_workspace_bytes(n_tokens: int, vocab: int, dim: int) -> int:
+    """Bytes that zero_head_loss_grad of up to n_tokens tokens needs."""
     out = ctypes.c_int64(0)
     f = "zero_head_loss_grad_workspace_bytes"
     _check(load().zero_head_loss_grad_workspace_bytes(n_tokens, vocab, dim, ctypes.byref(out)), f)

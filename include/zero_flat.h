@@ -734,7 +734,11 @@ int zero_head_loss_grad(const uint16_t* hidden, int64_t n_tokens, int64_t dim,
                         int64_t grad_hidden_stride, uint16_t* grad_table, int32_t accumulate,
                         void* workspace, int64_t workspace_bytes, void* stream);
 
-/* zero_head_loss_workspace_bytes, zero_head_loss_grad_workspace_bytes -- host. */
+/*
+ * zero_head_loss_workspace_bytes, zero_head_loss_grad_workspace_bytes -- host.  What calls
+ * of up to n_tokens tokens need on the current device, wherever the table lies.  (The call
+ * of fewer tokens may by itself need more than one of more.)
+ */
 int zero_head_loss_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t dim, int64_t* bytes);
 int zero_head_loss_grad_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t dim,
                                         int64_t* bytes);
