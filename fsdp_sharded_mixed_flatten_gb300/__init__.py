@@ -20,7 +20,9 @@ from .root_ops import (ZERO_MAX_NORM_DIM, ZERO_MAX_TEACHER, zero_distill_loss,
                        zero_layer_norm_grad_workspace_bytes)
 from .layer_ops import (ZERO_EIGHT_BLOCK, ZERO_MAX_HEAD_DIM, ZERO_MAX_HEAD_TOKENS,
                         ZERO_MAX_HEAD_VOCAB, zero_head_loss, zero_head_loss_grad,
-                        zero_head_loss_grad_workspace_bytes, zero_head_loss_workspace_bytes,
+                        zero_head_loss_grad_in_place_workspace_bytes,
+                        zero_head_loss_grad_workspace_bytes,
+                        zero_head_loss_in_place_workspace_bytes, zero_head_loss_workspace_bytes,
                         zero_pack_rows, zero_rms_norm, zero_rms_norm_grad,
                         zero_rms_norm_grad_workspace_bytes, zero_unpack_rows)
 
@@ -38,6 +40,7 @@ __all__ = [
     "ZERO_EIGHT_BLOCK", "zero_pack_rows", "zero_rms_norm", "zero_rms_norm_grad",
     "zero_rms_norm_grad_workspace_bytes", "zero_unpack_rows",
     "ZERO_MAX_HEAD_DIM", "ZERO_MAX_HEAD_TOKENS", "ZERO_MAX_HEAD_VOCAB", "zero_head_loss",
-    "zero_head_loss_grad", "zero_head_loss_grad_workspace_bytes",
+    "zero_head_loss_grad", "zero_head_loss_grad_in_place_workspace_bytes",
+    "zero_head_loss_grad_workspace_bytes", "zero_head_loss_in_place_workspace_bytes",
     "zero_head_loss_workspace_bytes",
 ]

@@ -1602,15 +1602,17 @@ int best_width(int64_t m, int64_t n, int64_t steps, int unit) {
 
 }  // namespace
 
-// Pieces of the vocabulary whose gradient, and whose copy of the table where it is off the
-// 16-byte grid, take at most 512 MB each; as even as whole tiles allow.
-// Forward, a table that is read in place is one piece.
+// Pieces of the vocabulary whose gradient, and whose copy of the table where that is off the
+// 16-byte grid, take at most 512 MB each (but 256 rows at least, whose gradient takes more
+// beyond 1M tokens); as even as whole tiles allow.  Forward, a table that is read in place is
+// one piece.
 HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, bool in_place) {
     constexpr int64_t kMost = int64_t{512} << 20;
     HeadPlan p{};
     p.rows = whole(n_tokens < 1 ? 1 : n_tokens, kPairTile);
     p.pitch = whole(dim, 64);                // rows on 128-byte boundaries: fewer lines a box
-    const int64_t per_row = 2 * (back && p.rows > p.pitch ? p.rows : p.pitch);
+    const int64_t copied = in_place ? 0 : p.pitch;
+    const int64_t per_row = 2 * (back && p.rows > copied ? p.rows : p.pitch);
     const int64_t m = p.rows / kPairTile;
     int64_t most = kMost / per_row / kPairTile * kPairTile;
     if (most < kPairTile) most = kPairTile;
@@ -1663,7 +1665,7 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, bool
     p.slot = place(4 * n);
     p.label = place(4 * n);
     p.hidden = place(2 * p.rows * p.pitch);
-    p.table = place(!back && in_place ? 0 : 2 * p.piece * p.pitch);
+    p.table = place(2 * p.piece * copied);
     if (back) {
         p.lse = place(4 * n);
         p.grad = place(4 * n);

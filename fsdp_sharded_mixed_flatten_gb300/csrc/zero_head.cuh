@@ -42,7 +42,8 @@ struct HeadPlan {
     int64_t bytes;
 };
 HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, bool in_place);
-// What calls of up to n_tokens tokens need.
+// What calls of up to n_tokens tokens need for a table that is read in place, or for one that
+// is not.
 int64_t head_bytes(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, bool in_place);
 
 // Whether TMA reaches the table where it is.

@@ -621,13 +621,19 @@ int head_call(zf::HeadCall& c, const uint16_t* hidden, int64_t n_tokens, int64_t
     return ZERO_OK;
 }
 
-int head_workspace(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, int64_t* bytes) {
+// Wherever the table lies, or of one that is read in place.
+int head_workspace(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, bool in_place,
+                   int64_t* bytes) {
     if (bytes == nullptr) return fail(ZERO_ERR_INVALID_ARG, "bytes is NULL");
     if (int rc = check_head(n_tokens, vocab, dim)) return rc;
-    // wherever the table lies
-    const int64_t in_place = zf::head_bytes(n_tokens, vocab, dim, back, true);
-    const int64_t copied = zf::head_bytes(n_tokens, vocab, dim, back, false);
-    *bytes = in_place > copied ? in_place : copied;
+    if (in_place && dim % 8 != 0)
+        return fail(ZERO_ERR_INVALID_ARG, "a table is read in place where dim is a multiple of 8");
+    int64_t need = dim % 8 == 0 ? zf::head_bytes(n_tokens, vocab, dim, back, true) : 0;
+    if (!in_place) {
+        const int64_t copied = zf::head_bytes(n_tokens, vocab, dim, back, false);
+        if (copied > need) need = copied;
+    }
+    *bytes = need;
     return ok();
 }
 
@@ -635,12 +641,22 @@ int head_workspace(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, int6
 
 ZERO_API int zero_head_loss_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t dim,
                                             int64_t* bytes) {
-    return head_workspace(n_tokens, vocab, dim, false, bytes);
+    return head_workspace(n_tokens, vocab, dim, false, false, bytes);
 }
 
 ZERO_API int zero_head_loss_grad_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t dim,
                                                  int64_t* bytes) {
-    return head_workspace(n_tokens, vocab, dim, true, bytes);
+    return head_workspace(n_tokens, vocab, dim, true, false, bytes);
+}
+
+ZERO_API int zero_head_loss_in_place_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t dim,
+                                                     int64_t* bytes) {
+    return head_workspace(n_tokens, vocab, dim, false, true, bytes);
+}
+
+ZERO_API int zero_head_loss_grad_in_place_workspace_bytes(int64_t n_tokens, int64_t vocab,
+                                                          int64_t dim, int64_t* bytes) {
+    return head_workspace(n_tokens, vocab, dim, true, true, bytes);
 }
 
 ZERO_API int zero_head_loss(const uint16_t* hidden, int64_t n_tokens, int64_t dim,
@@ -707,7 +723,7 @@ ZERO_API int zero_head_loss_grad(const uint16_t* hidden, int64_t n_tokens, int64
         return fail(ZERO_ERR_INVALID_ARG, "accumulate = %d (0 or 1)", accumulate);
     const bool rows = grad_hidden != nullptr && n_tokens > 0;
     if (!rows && (grad_table == nullptr || (n_tokens == 0 && accumulate))) return ok();
-    const zf::HeadPlan p = zf::head_plan(n_tokens, vocab, dim, true, false);
+    const zf::HeadPlan p = zf::head_plan(n_tokens, vocab, dim, true, zf::head_table_in_place(c));
     if (int rc = check_workspace(workspace, workspace_bytes, p.bytes)) return rc;
     c.lse = const_cast<float*>(lse);
     c.grad_loss = grad_loss;

@@ -145,20 +145,30 @@ def zero_rms_norm_grad(grad_out, total, weight, rstd, grad_x, grad_weight=None, 
         _on(dev, stream)), f)
 
 
-def zero_head_loss_workspace_bytes(n_tokens: int, vocab: int, dim: int) -> int:
-    """Bytes that zero_head_loss of up to n_tokens tokens needs."""
+def _head_workspace(f: str, n_tokens: int, vocab: int, dim: int) -> int:
     out = ctypes.c_int64(0)
-    f = "zero_head_loss_workspace_bytes"
-    _check(load().zero_head_loss_workspace_bytes(n_tokens, vocab, dim, ctypes.byref(out)), f)
+    _check(getattr(load(), f)(n_tokens, vocab, dim, ctypes.byref(out)), f)
     return int(out.value)
+
+
+def zero_head_loss_workspace_bytes(n_tokens: int, vocab: int, dim: int) -> int:
+    """Bytes that zero_head_loss of up to n_tokens tokens needs, wherever the table lies."""
+    return _head_workspace("zero_head_loss_workspace_bytes", n_tokens, vocab, dim)
 
 
 def zero_head_loss_grad_workspace_bytes(n_tokens: int, vocab: int, dim: int) -> int:
-    """Bytes that zero_head_loss_grad of up to n_tokens tokens needs."""
-    out = ctypes.c_int64(0)
-    f = "zero_head_loss_grad_workspace_bytes"
-    _check(load().zero_head_loss_grad_workspace_bytes(n_tokens, vocab, dim, ctypes.byref(out)), f)
-    return int(out.value)
+    """Bytes that zero_head_loss_grad of up to n_tokens tokens needs, wherever the table lies."""
+    return _head_workspace("zero_head_loss_grad_workspace_bytes", n_tokens, vocab, dim)
+
+
+def zero_head_loss_in_place_workspace_bytes(n_tokens: int, vocab: int, dim: int) -> int:
+    """The same of a table on a 16-byte boundary, dim a multiple of 8: without a copy of it."""
+    return _head_workspace("zero_head_loss_in_place_workspace_bytes", n_tokens, vocab, dim)
+
+
+def zero_head_loss_grad_in_place_workspace_bytes(n_tokens: int, vocab: int, dim: int) -> int:
+    """The same of a table on a 16-byte boundary, dim a multiple of 8: without a copy of it."""
+    return _head_workspace("zero_head_loss_grad_in_place_workspace_bytes", n_tokens, vocab, dim)
 
 
 def _head(hidden, table, labels, func: str, device: int):

@@ -144,6 +144,8 @@ def load() -> ctypes.CDLL:
                                     i64, p],
             "zero_head_loss_workspace_bytes": [i64, i64, i64, out64],
             "zero_head_loss_grad_workspace_bytes": [i64, i64, i64, out64],
+            "zero_head_loss_in_place_workspace_bytes": [i64, i64, i64, out64],
+            "zero_head_loss_grad_in_place_workspace_bytes": [i64, i64, i64, out64],
             "zero_distill_loss": [p, i32, i64, i64, i64, p, p, i32, i64, p, f64, p, p],
             "zero_distill_loss_grad": [p, i32, i64, i64, i64, p, p, i32, i64, p, f64, p, p, i64,
                                        p],

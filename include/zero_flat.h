@@ -738,10 +738,17 @@ int zero_head_loss_grad(const uint16_t* hidden, int64_t n_tokens, int64_t dim,
  * zero_head_loss_workspace_bytes, zero_head_loss_grad_workspace_bytes -- host.  What calls
  * of up to n_tokens tokens need on the current device, wherever the table lies.  (The call
  * of fewer tokens may by itself need more than one of more.)
+ * zero_head_loss_in_place_workspace_bytes, zero_head_loss_grad_in_place_workspace_bytes --
+ * host.  The same for a table on a 16-byte boundary, dim a multiple of 8: no copy of it
+ * (up to 512 MB) is made.
  */
 int zero_head_loss_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t dim, int64_t* bytes);
 int zero_head_loss_grad_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t dim,
                                         int64_t* bytes);
+int zero_head_loss_in_place_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t dim,
+                                            int64_t* bytes);
+int zero_head_loss_grad_in_place_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t dim,
+                                                 int64_t* bytes);
 
 /* Message for the last non-OK return on the calling thread ("" if none). */
 const char* zero_last_error(void);

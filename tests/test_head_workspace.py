@@ -52,3 +52,47 @@ def test_a_workspace_for_the_longest_batch_is_enough(vocab, dim, longest):
 def test_queries_of_the_most_tokens_answer():
     for query in QUERIES:
         assert query(zf.ZERO_MAX_HEAD_TOKENS, 1000, 64) > 0
+
+
+IN_PLACE = [zf.zero_head_loss_in_place_workspace_bytes,
+            zf.zero_head_loss_grad_in_place_workspace_bytes]
+
+
+@pytest.mark.parametrize("n,vocab,dim", [(1, 131072, 4096), (32, 131072, 4096),
+                                         (128, 128000, 4096), (8192, 131072, 4096),
+                                         (1, 128256, 8192), (1024, 32000, 768)])
+def test_a_table_read_in_place_needs_no_copy(n, vocab, dim):
+    """The gradient's copies of the tokens' rows, its dz (at most 512 MB) and its sums (at most
+    512 MB, or one part of them) in whole tiles of 256 tokens; nothing of the table's size."""
+    rows = (n + 255) // 256 * 256
+    loss, grad = (q(n, vocab, dim) for q in IN_PLACE)
+    small = 16 * 1024 + 16 * n
+    dz = min(2 * rows * (vocab + 255), 512 << 20)
+    sums = max(min(64 * 4 * rows * dim, 512 << 20), 4 * rows * dim)
+    assert loss <= 2 * rows * dim + 8 * n * (vocab // 32 + 1 + 1024) + 2 * small
+    assert grad <= 2 * rows * dim + dz + sums + 2 * small
+    for q, any_place in zip(IN_PLACE, QUERIES):
+        assert q(n, vocab, dim) <= any_place(n, vocab, dim)
+        needs = [q(m, vocab, dim) for m in (1, 64, 65, 300, 1000, 5000)]
+        assert needs == sorted(needs)
+
+
+def test_a_call_needs_what_its_own_table_needs():
+    """Fake addresses, as above: what is enough in place is refused off the 16-byte grid."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("fake addresses never reach a GPU")
+    lib = zf.load()
+    at = [0x100000 * (i + 1) for i in range(8)]
+    n, vocab, dim = 32, 131072, 4096
+    grad = IN_PLACE[1](n, vocab, dim)
+    call = lambda table: lib.zero_head_loss_grad(                # noqa: E731
+        at[0], n, dim, dim, table, vocab, at[2], 8, at[4], at[3], at[6], dim, at[7], 0, at[5], grad,
+        None)
+    assert call(at[1]) != SIZE and call(at[1] + 2) == SIZE
+
+
+def test_a_width_that_is_never_read_in_place_is_refused():
+    for query in IN_PLACE:
+        with pytest.raises(zf.ZeroError):
+            query(10, 100, 12)
