@@ -62,17 +62,29 @@ constexpr uint32_t kTmemColumns = 512;      // two tiles' results
 // 6.6e-7 (1024: 4.6e-7, 2048: 9.8e-7; the parts cost 4 to 6 % of the time).  The gradient's
 // logits are summed in the same parts: its probabilities are next to 1 where the loss's are.
 constexpr int kLogitSteps = 24;
+// The same of the gradients' sums, over the vocabulary or over the tokens: a step of 16
+// products cuts off up to two units of the sum so far, so that 65536 values of one sign end
+// 2^-11 low at most, beside bf16's own rounding of up to 2^-8.  2M tokens summed in one go were
+// 1.2e-2 low, 1.6 units a step.  (131072 tokens, 8000 x 768 4.78 ms, in one go 4.66.)
+constexpr int kSumSteps = 1024;
 constexpr uint64_t kHeadWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // What a launch computes: rows' statistics, the logits' gradient, or both gradients that are
 // products of it: tiles of the hidden states' first, then of the table's.
-// (kLossLong, kDzLong: from logits that are summed in several parts.)
-enum Mode { kLoss, kLossLong, kDz, kDzLong, kProducts };
+// (kLossLong, kDzLong: from logits that are summed in several parts; kProductsLong: so are the
+// gradients.)
+enum Mode { kLoss, kLossLong, kDz, kDzLong, kProducts, kProductsLong };
 __host__ __device__ constexpr bool is_loss(int mode) { return mode == kLoss || mode == kLossLong; }
 __host__ __device__ constexpr bool is_dz(int mode) { return mode == kDz || mode == kDzLong; }
+__host__ __device__ constexpr bool is_products(int mode) {
+    return mode == kProducts || mode == kProductsLong;
+}
 __host__ __device__ constexpr bool is_long(int mode) {
-    return mode == kLossLong || mode == kDzLong;
+    return mode == kLossLong || mode == kDzLong || mode == kProductsLong;
+}
+__host__ __device__ constexpr int steps_at_a_time(int mode) {
+    return is_products(mode) ? kSumSteps : kLogitSteps;
 }
 // What a tile of the last is.
 enum Kind { kDh, kDw };
@@ -203,18 +215,18 @@ struct Tiles {
     Grid first, second;
     int total;
     __device__ Tiles(const HeadArgs& a, int live)
-        : first(MODE != kProducts ? Grid(live, a.vocab, a.dim, a.width, 1, a.group)
+        : first(!is_products(MODE) ? Grid(live, a.vocab, a.dim, a.width, 1, a.group)
                                   : Grid(a.want_h ? live : 0, a.dim, a.vocab, a.width_h, a.splits,
                                          a.group)),
           // (nothing to add: the table's gradient stays untouched; dz in two parts: the steps
           // along the tokens twice)
-          second(MODE != kProducts || !a.want_w || (a.add_w && live == 0) ? 0 : a.vocab, a.dim,
+          second(!is_products(MODE) || !a.want_w || (a.add_w && live == 0) ? 0 : a.vocab, a.dim,
                  dz_in_two(live) ? 2 * ((live + kTileK - 1) / kTileK) * kTileK : live,
-                 MODE != kProducts ? kPairTile : a.width_w, 1, a.group),
+                 !is_products(MODE) ? kPairTile : a.width_w, 1, a.group),
           total(first.total + second.total) {}
     template <class F>
     __device__ __forceinline__ void operator()(int i, F&& call) const {
-        if constexpr (MODE != kProducts) {
+        if constexpr (!is_products(MODE)) {
             call(std::integral_constant<int, -1>{}, first(i));
         } else if (i < first.total) {
             call(std::integral_constant<int, kDh>{}, first(i));
@@ -295,8 +307,8 @@ struct Epilogue {
           place(warp % 4 * 32),
           half((warp - 2) / 4),
           lane(l),
-          width(MODE != kProducts ? args.width : KIND == kDh ? args.width_h : args.width_w),
-          scale(is_dz(MODE) || (MODE == kProducts && KIND == kDw) ? scale_of(args.counts) : 1.0f) {
+          width(!is_products(MODE) ? args.width : KIND == kDh ? args.width_h : args.width_w),
+          scale(is_dz(MODE) || (is_products(MODE) && KIND == kDw) ? scale_of(args.counts) : 1.0f) {
         // the first half has the odd part
         constexpr int kUnit = is_dz(MODE) ? 2 : 1;
         const int all = width / 32, first = (all / kUnit + 1) / 2 * kUnit;
@@ -534,7 +546,7 @@ struct Epilogue {
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
 head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadArgs a) {
-    constexpr bool kBmn = MODE == kProducts;             // B is MN-major; A for kDw
+    constexpr bool kBmn = is_products(MODE);             // B is MN-major; A for kDw
     extern __shared__ char dyn[];
     __shared__ Shared sh;
     const uint32_t ring = (smem_address(dyn) + 1023u) & ~1023u;
@@ -553,7 +565,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
         sh.stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0 && lane < (MODE == kProducts ? 4 : 2)) prefetch_map(&maps.a + lane);
+    if (warp == 0 && lane < (is_products(MODE) ? 4 : 2)) prefetch_map(&maps.a + lane);
     if (warp == 1) tmem_alloc(smem_address(&sh.tmem), kTmemColumns);
     fence_before_sync();
     __syncthreads();
@@ -635,9 +647,9 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                                                        KIND == kDh   ? a.width_h
                                                        : KIND == kDw ? a.width_w
                                                                      : a.width);
-                    // a result in tensor memory: of all steps, or of some (kLossLong, kDzLong)
+                    // a result in tensor memory: of all steps, or of some (is_long)
                     for (int begin = t.begin; begin < t.end;) {
-                        const int end = is_long(MODE) ? min(begin + kLogitSteps, t.end) : t.end;
+                        const int end = is_long(MODE) ? min(begin + steps_at_a_time(MODE), t.end) : t.end;
                         const int slot = n % 2;
                         run = wait(sh, sh.taken[slot], (n / 2 + 1) % 2);
                         if (!run) return;
@@ -720,6 +732,31 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                 const uint32_t from = place(slot);
                 auto release = [&] { free_place(slot); };
                 epilogue(row0, t.n, t.split, turn, [&](auto&& f) {
+                    constexpr int kPart = steps_at_a_time(MODE);
+                    if constexpr (MODE == kProductsLong) {
+                        // (sums in local memory: what they cost there is small beside the
+                        // many steps of a part, and the results' code stays as short as below)
+                        float sum[4][32];
+                        for (int k = t.begin; k < t.end; k += kPart) {
+                            const int at = k == t.begin ? slot : come();
+#pragma unroll 1
+                            for (int c = 0; c < parts; ++c) {
+                                float v[32];
+                                tmem_load(v, place(at) + 32 * c);
+                                tmem_load_wait(v);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    sum[c][e] = k == t.begin ? v[e] : sum[c][e] + v[e];
+                            }
+                            free_place(at);
+                        }
+#pragma unroll 1
+                        for (int c = 0; c < parts; ++c) {
+                            f(c, sum[c]);
+                            __syncwarp();
+                        }
+                        return;
+                    }
                     if constexpr (is_long(MODE)) {
                         float sum[4][32];
 #pragma unroll
@@ -729,7 +766,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
 #pragma unroll
                         for (int c = 0; c < 4; ++c) tmem_load_wait(sum[c]);
                         release();
-                        for (int k = kLogitSteps; k < t.end; k += kLogitSteps) {
+                        for (int k = t.begin + kPart; k < t.end; k += kPart) {
                             const int next = come();
                             const uint32_t more = place(next);
 #pragma unroll
@@ -1853,7 +1890,10 @@ cudaError_t launch_head_products(const HeadCall& c, const HeadPlan& p, int64_t f
     const int64_t tiles =
         (a.want_h ? p.rows / kPairTile * tiles_of(c.dim, a.width_h) * p.splits : 0) +
         (a.want_w ? tiles_of(a.vocab, kPairTile) * tiles_of(c.dim, a.width_w) : 0);
-    return launch_product<kProducts>(maps, a, tiles, stream);
+    const int64_t steps_h = tiles_of(tiles_of(p.piece, kTileK), p.splits);
+    return steps_h <= kSumSteps && tiles_of(c.n_tokens, kTileK) <= kSumSteps
+               ? launch_product<kProducts>(maps, a, tiles, stream)
+               : launch_product<kProductsLong>(maps, a, tiles, stream);
 }
 
 cudaError_t launch_head_finish(const HeadCall& c, const HeadPlan& p, cudaStream_t stream) {

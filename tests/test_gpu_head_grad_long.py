@@ -69,3 +69,60 @@ def test_the_gradients_logits_are_sums_of_short_parts(d):
     want = torch.exp(z - lse.to(F64)) - 1.0
     off = float((dz - want).mean().abs() / z.mean())
     assert off <= 56 * 2.0 ** -24, f"off by {off * 2.0 ** 24} 2^-24"
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n,d,offset", [(1 << 21, 64, 0), (70000, 600, 0), (70001, 77, 5)])
+def test_sums_over_many_tokens_of_one_sign(n, d, offset, accumulate):
+    """Equal logits of 32 rows and one label: dz is 2^-5 and 2^-5 - 1, bf16 values, so the
+    table's gradient is a sum of h.  Each element is bf16 (2^-8 of itself); a step of 16
+    tokens cuts off two units of 2^-23 of the sum so far at most, so parts of 65536, whose sums
+    grow evenly, end 4096 / 2 2^-22 = 2^-11 low at most, and exponentials are off by 2^-22.  The
+    columns' sums are spread over an octave, where roundings average out, to 2^-11 in the mean
+    of 64 of them."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    vocab = 32
+    spread = 1.0 + torch.arange(d, device="cuda") % 64 / 64.0
+    h = torch.empty((n, d), dtype=BF16, device="cuda")
+    h.copy_((torch.rand((n, d), generator=g, device="cuda") + 0.5) * spread)
+    w = torch.zeros(offset + vocab * d, dtype=BF16, device="cuda")[offset:].view(vocab, d)
+    y = torch.full((n,), 5, device="cuda")
+    ws, size = _workspace(n, vocab, d)
+    loss, lse = torch.empty((2, n), device="cuda")
+    zf.zero_head_loss(h, w, y, loss, lse, ws, size)
+    dw = torch.full((offset + vocab * d,), 3.0, dtype=BF16, device="cuda")[offset:].view(vocab, d)
+    zf.zero_head_loss_grad(h, w, y, lse, torch.full((n,), 1.0 / 1024, device="cuda"), None, dw,
+                           accumulate, ws, size)
+    total = torch.zeros(d, dtype=F64, device="cuda")
+    for a in range(0, n, 1 << 18):
+        total += h[a:a + (1 << 18)].to(F64).sum(0)
+    for v, p in ((5, 2.0 ** -5 - 1.0), (0, 2.0 ** -5), (31, 2.0 ** -5)):
+        want = total * p / 1024 + (3.0 if accumulate else 0.0)
+        off = (dw[v].to(F64) - want) / want.abs()
+        assert float(off.abs().max()) <= 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -20
+        assert abs(float(off.mean())) <= 2.0 ** -11 + 2.0 ** -11 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("n", [3, 200])
+def test_sums_over_a_long_vocabulary(n):
+    """No hidden states: every row of the table counts 1 / vocab in the gradient, as a sum of
+    262144 values of one sign.  dz is bf16 (2^-18 is one of its values; minus one, 1), the
+    result is (2^-8), and sums end 2^-11 low at most (as above)."""
+    vocab, d = 1 << 18, 8192
+    g = torch.Generator(device="cuda").manual_seed(n)
+    w = torch.empty((vocab, d), dtype=BF16, device="cuda")
+    mean = torch.zeros(d, dtype=F64, device="cuda")
+    for a in range(0, vocab, 1 << 14):
+        w[a:a + (1 << 14)] = (torch.rand((1 << 14, d), generator=g, device="cuda") + 0.5).to(BF16)
+        mean += w[a:a + (1 << 14)].to(F64).sum(0) / vocab
+    h = torch.zeros((n, d), dtype=BF16, device="cuda")
+    y = torch.arange(n, device="cuda") * 977
+    ws, size = _workspace(n, vocab, d)
+    loss, lse = torch.empty((2, n), device="cuda")
+    zf.zero_head_loss(h, w, y, loss, lse, ws, size)
+    dh = torch.empty_like(h)
+    zf.zero_head_loss_grad(h, w, y, lse, torch.ones(n, device="cuda"), dh, None, False, ws, size)
+    own = w[y].to(F64)
+    want = mean - own
+    off = (dh.to(F64) - want).abs()
+    assert bool((off <= 2.0 ** -8 * want.abs() + 2.0 ** -11 * mean + 2.0 ** -20 * own).all())
