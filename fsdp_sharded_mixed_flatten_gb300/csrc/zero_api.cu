@@ -15,10 +15,8 @@
 #include <vector>
 
 #include "zero_flat.h"
-#include "zero_head.cuh"
 #include "zero_host.cuh"
 #include "zero_kernels.cuh"
-#include "zero_ops.cuh"
 #include "zero_status.cuh"
 
 static_assert(zf::kMaxRanks == ZERO_MAX_RANKS, "rank limit mismatch");
@@ -901,13 +899,6 @@ ZERO_API int zero_device_status(void* stream, int32_t* status, int32_t clear) {
     if (int rc = cuda_status(zf::read_device_status(&v, clear != 0, static_cast<cudaStream_t>(stream)),
                              "device status read"))
         return rc;
-    for (auto read : {zf::read_head_status, zf::read_rms_status}) {
-        int w = 0;
-        if (int rc = cuda_status(read(&w, clear != 0, static_cast<cudaStream_t>(stream)),
-                                 "device status read"))
-            return rc;
-        if (v == 0) v = w;
-    }
     *status = v;
     return ok();
 }

@@ -42,8 +42,6 @@ namespace {
 
 using namespace tile;
 
-__device__ int g_head_status = 0;
-
 constexpr int kPairTile = 256;                  // rows, and most columns, of a pair's tile
 constexpr int kTileK = 64;
 constexpr int kHalf = 128;                  // of the tile, a CTA's share of each operand
@@ -119,23 +117,26 @@ struct HeadArgs {
     int32_t n_rows;
     int32_t label64;
     int32_t group;                // tiles along M that are worked on together
+    int* status;                  // the device status word (set by the launch)
 };
 
 struct Shared {
     uint64_t full[kStages], empty[kStages], done[2], taken[2];
+    int* status;
     uint32_t tmem;
     int stop;
 };
 
 // Waits for a phase; false when the CTA is to stop: the wait has run out, here or in
 // another of its roles.
-__device__ __noinline__ bool wait_long(volatile int* stop, uint32_t bar, uint32_t parity) {
+__device__ __noinline__ bool wait_long(volatile int* stop, int* status, uint32_t bar,
+                                       uint32_t parity) {
     const uint64_t t0 = now_ns();
     while (!bar_try(bar, parity)) {
         if (*stop) return false;
         if (now_ns() - t0 > kHeadWaitNs) {
             *stop = 1;
-            atomicCAS(&g_head_status, kDeviceOk, kDeviceTimeout);
+            atomicCAS(status, kDeviceOk, kDeviceTimeout);
             return false;
         }
     }
@@ -144,7 +145,7 @@ __device__ __noinline__ bool wait_long(volatile int* stop, uint32_t bar, uint32_
 template <class S>
 __device__ __forceinline__ bool wait(S& sh, uint64_t& bar, uint32_t parity) {
     const uint32_t b = smem_address(&bar);
-    return bar_try(b, parity) || wait_long(&sh.stop, b, parity);
+    return bar_try(b, parity) || wait_long(&sh.stop, sh.status, b, parity);
 }
 
 __device__ __forceinline__ int live_rows(const HeadArgs& a) {
@@ -563,6 +564,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
             bar_init(smem_address(&sh.taken[i]), 2 * kEpilogueWarps);
         }
         sh.stop = 0;
+        sh.status = a.status;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0 && lane < (is_products(MODE) ? 4 : 2)) prefetch_map(&maps.a + lane);
@@ -868,6 +870,7 @@ struct FewArgs {
     int32_t vocab;
     int32_t dim;
     int32_t label64;
+    int* status;                  // the device status word
 };
 struct FewMaps {
     // 128 rows of the table, what the smaller and the larger shares have beyond whole tiles, and
@@ -877,6 +880,7 @@ struct FewMaps {
 };
 struct FewShared {
     uint64_t full[kFewMostStages], empty[kFewMostStages], done[2], taken[2];
+    int* status;
     uint32_t tmem;
     int stop;
 };
@@ -906,6 +910,7 @@ head_few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ Fe
             bar_init(smem_address(&sh.taken[i]), TOKENS / 8);
         }
         sh.stop = 0;
+        sh.status = a.status;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0 && lane < 4) prefetch_map(&maps.tile + lane);
@@ -1561,8 +1566,8 @@ cudaError_t dz_map(CUtensorMap* map, const HeadArgs& a, int box_rows) {
 }
 
 template <int MODE>
-cudaError_t launch_product(const HeadMaps& maps, const HeadArgs& a, int64_t tiles,
-                           cudaStream_t stream) {
+cudaError_t launch_product(const HeadMaps& maps, HeadArgs a, int64_t tiles, cudaStream_t stream) {
+    if (cudaError_t e = device_status_word(&a.status); e != cudaSuccess) return e;
     static std::once_flag once[64];
     static cudaError_t set[64];
     static int fit[64];                                  // pairs at a time
@@ -1807,6 +1812,7 @@ cudaError_t launch_few(const HeadCall& c, const HeadPlan& p, cudaStream_t stream
         e != cudaSuccess)
         return e;
     FewArgs a{};
+    if (cudaError_t e = device_status_word(&a.status); e != cudaSuccess) return e;
     a.labels = c.labels;
     a.parts = at<float2>(c, p.parts);
     a.picked = at<float>(c, p.picked);
@@ -1908,10 +1914,6 @@ cudaError_t launch_head_finish(const HeadCall& c, const HeadPlan& p, cudaStream_
     return launch_after(kernel, grid, 32 * kFinishWarps, 0, stream, at<int32_t>(c, p.counts),
                         at<int32_t>(c, p.slot), at<float>(c, p.sums), p.rows, p.splits,
                         c.n_tokens, c.dim, sections, c.grad_hidden, c.grad_hidden_stride);
-}
-
-cudaError_t read_head_status(int* status, int clear, cudaStream_t stream) {
-    return read_status_word(g_head_status, status, clear, stream);
 }
 
 }  // namespace zf

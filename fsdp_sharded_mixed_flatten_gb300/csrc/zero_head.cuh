@@ -67,7 +67,4 @@ cudaError_t launch_head_products(const HeadCall& c, const HeadPlan& p, int64_t f
                                  cudaStream_t stream);
 cudaError_t launch_head_finish(const HeadCall& c, const HeadPlan& p, cudaStream_t stream);
 
-// Timeouts of this file's kernels, joined to the library's device status.
-cudaError_t read_head_status(int* status, int clear, cudaStream_t stream);
-
 }  // namespace zf

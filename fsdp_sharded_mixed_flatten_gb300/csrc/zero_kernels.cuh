@@ -175,6 +175,9 @@ int staged_grid(int mode, int total_tiles);
 int sched_slot(cudaStream_t stream);
 // One CTA waiting on a barrier that nothing completes (tests the bounded wait).
 cudaError_t launch_wait_timeout_selftest(uint64_t limit_ns, cudaStream_t stream);
+// Where the current device's status word lies (looked up once a device), for the kernels of
+// other files that record in it.
+cudaError_t device_status_word(int** word);
 // Read (and optionally clear) the device status word; synchronises `stream`.
 cudaError_t read_device_status(int* status, int clear, cudaStream_t stream);
 

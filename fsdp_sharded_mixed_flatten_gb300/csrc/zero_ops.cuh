@@ -259,6 +259,7 @@ struct RmsArgs {
     int32_t group_threads;    // threads that hold a row (this and on: set by the launch)
     int32_t slots;            // rows of a group under way in shared memory
     uint32_t slot_bytes;
+    int* status;              // the device status word
     float eps;
 };
 
@@ -267,8 +268,6 @@ int rms_grad_ctas(int64_t n_rows);
 cudaError_t launch_rms_norm(RmsArgs a, int act_bytes, cudaStream_t stream);
 cudaError_t launch_rms_norm_grad(RmsArgs a, int act_bytes, cudaStream_t stream);
 cudaError_t launch_rms_reduce(const RmsArgs& a, int act_bytes, cudaStream_t stream);
-// Timeouts of these kernels, joined to the library's device status.
-cudaError_t read_rms_status(int* status, int clear, cudaStream_t stream);
 
 struct EightArgs {
     const void* x;            // rows to pack

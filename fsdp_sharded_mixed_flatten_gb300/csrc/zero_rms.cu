@@ -251,14 +251,13 @@ __host__ __device__ constexpr int rows_threads(int k, int elem, bool back) {
 }
 constexpr uint64_t kRowsWaitNs = 2000000000ull;
 
-__device__ int g_rms_status = 0;
-
 struct RowsRing {
     char* base;
     uint32_t slot_bytes, bars;
     int slots, at;
     uint32_t phase;
     int* stop;
+    int* status;
     __device__ __forceinline__ const char* here() const { return base + at * slot_bytes; }
     __device__ __forceinline__ uint32_t bar(int s) const { return bars + 8 * s; }
     // The slot's row has come.  When a wait runs out the launch goes on with what is there
@@ -271,7 +270,7 @@ struct RowsRing {
             if (*static_cast<volatile int*>(stop)) return;
             if (tile::now_ns() - t0 > kRowsWaitNs) {
                 *static_cast<volatile int*>(stop) = 1;
-                atomicCAS(&g_rms_status, kDeviceOk, kDeviceTimeout);
+                atomicCAS(status, kDeviceOk, kDeviceTimeout);
                 return;
             }
         }
@@ -369,6 +368,7 @@ __device__ __forceinline__ RowsRing rows_begin(const RmsArgs& a, const RmsGroup&
     r.at = 0;
     r.phase = 0;
     r.stop = stop;
+    r.status = a.status;
     if (threadIdx.x == 0) *stop = 0;
     if (g.t == 0) {
         for (int s = 0; s < r.slots; ++s) tile::bar_init(r.bar(s), 1);
@@ -1017,7 +1017,8 @@ RmsPlan backward_plan(const RmsArgs& a, int act_bytes) {
 }
 
 template <class T, int K, bool WIDE, bool BACK, bool EIGHT>
-cudaError_t launch_rows(const RmsArgs& a, const RmsPlan& p, cudaStream_t stream) {
+cudaError_t launch_rows(RmsArgs a, const RmsPlan& p, cudaStream_t stream) {
+    if (cudaError_t e = device_status_word(&a.status); e != cudaSuccess) return e;
     static std::once_flag once[64];
     static cudaError_t set[64];
     const auto kernel = [] {
@@ -1102,10 +1103,6 @@ cudaError_t launch_rms_reduce(const RmsArgs& a, int act_bytes, cudaStream_t stre
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, rms_reduce_kernel, a, static_cast<int>(parts));
-}
-
-cudaError_t read_rms_status(int* status, int clear, cudaStream_t stream) {
-    return read_status_word(g_rms_status, status, clear, stream);
 }
 
 cudaError_t launch_eight(EightArgs a, int act_bytes, cudaStream_t stream) {

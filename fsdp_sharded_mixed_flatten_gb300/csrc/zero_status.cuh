@@ -26,22 +26,6 @@ int cuda_status(cudaError_t e, const char* what);
 // at every call.
 bool injected(const char* what);
 
-// A translation unit's device status word, read on `stream` and put back to 0 if asked.
-inline cudaError_t read_status_word(const int& symbol, int* status, int clear,
-                                    cudaStream_t stream) {
-    int v = 0;
-    cudaError_t e =
-        cudaMemcpyFromSymbolAsync(&v, symbol, sizeof(int), 0, cudaMemcpyDeviceToHost, stream);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-    if (e == cudaSuccess && clear && v != 0) {
-        const int zero = 0;
-        e = cudaMemcpyToSymbolAsync(symbol, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, stream);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-    }
-    *status = v;
-    return e;
-}
-
 // One CUDA call with its status converted, unless a test injects its failure.
 int injected_failure(const char* what);
 template <class F>

@@ -1434,6 +1434,22 @@ cudaError_t launch_wait_timeout_selftest(uint64_t limit_ns, cudaStream_t stream)
     return cudaGetLastError();
 }
 
+cudaError_t device_status_word(int** word) {
+    static std::atomic<int*> known[64];
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    int* at = known[dev].load(std::memory_order_relaxed);
+    if (at == nullptr) {
+        void* p = nullptr;
+        if (cudaError_t e = cudaGetSymbolAddress(&p, g_zf_device_status); e != cudaSuccess) return e;
+        at = static_cast<int*>(p);
+        known[dev].store(at, std::memory_order_relaxed);
+    }
+    *word = at;
+    return cudaSuccess;
+}
+
 cudaError_t read_device_status(int* status, int clear, cudaStream_t stream) {
     int v = 0;
     cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_zf_device_status, sizeof(int), 0,
