@@ -378,7 +378,6 @@ struct Epilogue {
             const float g = in ? a.grad[token] / scale : 0.0f;
             const Pair by = pair(kLog2e, kLog2e), minus = pair(off, off), times = pair(g, g);
             each([&](int c, float (&v)[32]) {
-                // (rows beyond the live ones are zeros in the hidden states' copy: z = 0, g = 0)
                 // z - lse before anything is multiplied: of large logits only their
                 // difference counts, and where it is small it is exact.
                 Pair y[16];
@@ -387,6 +386,12 @@ struct Epilogue {
                     const float2 x =
                         unpair(mul2(add2(pair(v[2 * i], v[2 * i + 1]), minus), by));
                     y[i] = mul2(pair(exp2_fast(x.x), exp2_fast(x.y)), times);
+                }
+                // Rows beyond the live ones are zeros in the hidden states' copy, but a table's
+                // infinity makes NaN of them.
+                if (!in) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) y[i] = 0;
                 }
                 if (mine >= 32 * c && mine < 32 * c + 32) {
 #pragma unroll
