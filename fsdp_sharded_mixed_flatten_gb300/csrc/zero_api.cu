@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "zero_flat.h"
+#include "zero_head.cuh"
 #include "zero_host.cuh"
 #include "zero_kernels.cuh"
 #include "zero_status.cuh"
@@ -907,6 +908,13 @@ ZERO_API int zero_selftest_wait_timeout(int64_t limit_ns, void* stream) {
     if (limit_ns < 1 || limit_ns > 1000000000) return fail(ZERO_ERR_INVALID_ARG, "limit_ns out of range");
     return cuda_status(zf::launch_wait_timeout_selftest(static_cast<uint64_t>(limit_ns),
                                                         static_cast<cudaStream_t>(stream)),
+                       "self-test launch");
+}
+
+ZERO_API int zero_selftest_tile_wait_timeout(int64_t limit_ns, void* stream) {
+    if (limit_ns < 1 || limit_ns > 1000000000) return fail(ZERO_ERR_INVALID_ARG, "limit_ns out of range");
+    return cuda_status(zf::launch_tile_wait_selftest(static_cast<uint64_t>(limit_ns),
+                                                     static_cast<cudaStream_t>(stream)),
                        "self-test launch");
 }
 

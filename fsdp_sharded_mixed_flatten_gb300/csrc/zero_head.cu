@@ -127,20 +127,10 @@ struct Shared {
     int stop;
 };
 
-// Waits for a phase; false when the CTA is to stop: the wait has run out, here or in
-// another of its roles.
+// Waits for a phase; false when the CTA is to stop.
 __device__ __noinline__ bool wait_long(volatile int* stop, int* status, uint32_t bar,
                                        uint32_t parity) {
-    const uint64_t t0 = now_ns();
-    while (!bar_try(bar, parity)) {
-        if (*stop) return false;
-        if (now_ns() - t0 > kHeadWaitNs) {
-            *stop = 1;
-            atomicCAS(status, kDeviceOk, kDeviceTimeout);
-            return false;
-        }
-    }
-    return true;
+    return bar_wait(bar, parity, stop, status, kHeadWaitNs);
 }
 template <class S>
 __device__ __forceinline__ bool wait(S& sh, uint64_t& bar, uint32_t parity) {
@@ -1089,6 +1079,19 @@ head_few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ Fe
     if (warp == 1) single::tmem_free(tmem, 2 * kFewMost);
 }
 
+// One CTA waiting for a phase that nothing completes.
+__global__ void wait_selftest_kernel(int* status, uint64_t limit_ns) {
+    __shared__ uint64_t bar;
+    __shared__ int stop;
+    if (threadIdx.x == 0) {
+        bar_init(smem_address(&bar), 1);
+        stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    bar_wait(smem_address(&bar), 0, &stop, status, limit_ns);
+}
+
 // ---------------------------------------------------------------- rows ------
 
 // The places in the workspace that the first launches fill.
@@ -1919,6 +1922,13 @@ cudaError_t launch_head_finish(const HeadCall& c, const HeadPlan& p, cudaStream_
     return launch_after(kernel, grid, 32 * kFinishWarps, 0, stream, at<int32_t>(c, p.counts),
                         at<int32_t>(c, p.slot), at<float>(c, p.sums), p.rows, p.splits,
                         c.n_tokens, c.dim, sections, c.grad_hidden, c.grad_hidden_stride);
+}
+
+cudaError_t launch_tile_wait_selftest(uint64_t limit_ns, cudaStream_t stream) {
+    int* status = nullptr;
+    if (cudaError_t e = device_status_word(&status); e != cudaSuccess) return e;
+    wait_selftest_kernel<<<1, 64, 0, stream>>>(status, limit_ns);
+    return cudaGetLastError();
 }
 
 }  // namespace zf

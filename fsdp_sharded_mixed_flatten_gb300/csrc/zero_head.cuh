@@ -67,4 +67,7 @@ cudaError_t launch_head_products(const HeadCall& c, const HeadPlan& p, int64_t f
                                  cudaStream_t stream);
 cudaError_t launch_head_finish(const HeadCall& c, const HeadPlan& p, cudaStream_t stream);
 
+// One CTA whose wait, the one that these kernels and the norm's use, runs out.
+cudaError_t launch_tile_wait_selftest(uint64_t limit_ns, cudaStream_t stream);
+
 }  // namespace zf

@@ -264,16 +264,7 @@ struct RowsRing {
     // (no group is left waiting for a part of itself) and the status tells.
     __device__ __forceinline__ void wait() const {
         const uint32_t b = bar(at);
-        if (tile::bar_try(b, phase)) return;
-        const uint64_t t0 = tile::now_ns();
-        while (!tile::bar_try(b, phase)) {
-            if (*static_cast<volatile int*>(stop)) return;
-            if (tile::now_ns() - t0 > kRowsWaitNs) {
-                *static_cast<volatile int*>(stop) = 1;
-                atomicCAS(status, kDeviceOk, kDeviceTimeout);
-                return;
-            }
-        }
+        if (!tile::bar_try(b, phase)) tile::bar_wait(b, phase, stop, status, kRowsWaitNs);
     }
     __device__ __forceinline__ void next() {
         if (++at == slots) {

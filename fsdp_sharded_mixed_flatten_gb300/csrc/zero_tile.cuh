@@ -11,6 +11,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "zero_kernels.cuh"
+
 namespace zf::tile {
 
 __device__ __forceinline__ uint32_t smem_address(const void* p) {
@@ -70,6 +72,22 @@ __device__ __forceinline__ uint64_t now_ns() {
     uint64_t t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
+}
+
+// Waits for a phase with a limit.  False when the CTA is to stop: the wait has run out, which
+// the status word then tells, here or in another of its roles.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* stop,
+                                         int* status, uint64_t limit_ns) {
+    const uint64_t t0 = now_ns();
+    while (!bar_try(bar, parity)) {
+        if (*stop) return false;
+        if (now_ns() - t0 > limit_ns) {
+            *stop = 1;
+            atomicCAS(status, kDeviceOk, kDeviceTimeout);
+            return false;
+        }
+    }
+    return true;
 }
 
 // ---------------------------------------------------------------- TMA -------

@@ -122,6 +122,8 @@ def load() -> ctypes.CDLL:
         lib.zero_device_status.restype = ctypes.c_int
         lib.zero_selftest_wait_timeout.argtypes = [i64, p]
         lib.zero_selftest_wait_timeout.restype = ctypes.c_int
+        lib.zero_selftest_tile_wait_timeout.argtypes = [i64, p]
+        lib.zero_selftest_tile_wait_timeout.restype = ctypes.c_int
         f64, out64 = ctypes.c_double, ctypes.POINTER(ctypes.c_int64)
         for name, args in {
             "zero_embedding": [p, i32, i64, p, i32, i64, i64, f64, p, i32, i64, p],
@@ -311,6 +313,12 @@ def zero_selftest_wait_timeout(limit_ns: int, stream=None):
     """Launch a kernel whose bounded barrier wait must run out after limit_ns."""
     _check(load().zero_selftest_wait_timeout(int(limit_ns), _stream(stream)),
            "zero_selftest_wait_timeout")
+
+
+def zero_selftest_tile_wait_timeout(limit_ns: int, stream=None):
+    """The same with the wait of the head's products and of the norm's rows."""
+    _check(load().zero_selftest_tile_wait_timeout(int(limit_ns), _stream(stream)),
+           "zero_selftest_tile_wait_timeout")
 
 
 class PreparedUnits:

@@ -273,7 +273,7 @@ int zero_step(const uint16_t* const* grads, float* const* master, float* const* 
 /*
  * zero_device_status -- host, synchronous.  Failure detection for the kernels
  * that wait on shared-memory barriers (the bulk-copy staged fused step and
- * reduce-scatter, the head's products): every such wait gives up after about 2 seconds, records
+ * reduce-scatter, the head's products, the root-mean-square norm's rows): every such wait gives up after about 2 seconds, records
  * ZERO_DEVICE_TIMEOUT in a device status word, and the kernel returns early
  * (its outputs are then incomplete).  A dynamically scheduled launch that
  * found its tile counter used by another launch at the same time records
@@ -297,6 +297,12 @@ int zero_device_status(void* stream, int32_t* status, int32_t clear);
  * without hanging or faulting the GPU.  No counterpart on the pages.
  */
 int zero_selftest_wait_timeout(int64_t limit_ns, void* stream);
+
+/*
+ * zero_selftest_tile_wait_timeout -- device.  The same with the wait of the head's products
+ * and of the root-mean-square norm's rows.
+ */
+int zero_selftest_tile_wait_timeout(int64_t limit_ns, void* stream);
 
 /*
  * zero_unit_t / zero_step_units -- device, fused, several FlatParameters per

@@ -1,4 +1,5 @@
 """The device status: one read of one word, whichever kernels record in it."""
+import math
 import os
 import subprocess
 import sys
@@ -77,3 +78,28 @@ def test_first_calls_of_a_process_may_be_captured():
     p = subprocess.run([sys.executable, "-c", textwrap.dedent(code)], cwd=ROOT, timeout=300,
                        capture_output=True, text=True)
     assert p.returncode == 0 and "captured" in p.stdout, p.stderr[-2000:]
+
+
+def test_bounded_waits_of_tiles_report_timeout():
+    """The wait of the head's products and the norm's rows, when nothing ends it: it runs out,
+    is reported, and the context stays usable."""
+    assert zf.zero_device_status() == zf.zero.ZERO_DEVICE_OK
+    zf.zero_selftest_tile_wait_timeout(20_000_000)          # 20 ms
+    assert zf.zero_device_status(clear=False) == zf.zero.ZERO_DEVICE_TIMEOUT
+    assert zf.zero_device_status(clear=True) == zf.zero.ZERO_DEVICE_TIMEOUT
+    assert zf.zero_device_status() == zf.zero.ZERO_DEVICE_OK
+    n, vocab, d = 40, 500, 128
+    h = torch.ones((n, d), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((vocab, d), dtype=torch.bfloat16, device="cuda")
+    size = zf.zero_head_loss_workspace_bytes(n, vocab, d)
+    loss, ws = torch.empty(n, device="cuda"), torch.empty(size, dtype=torch.uint8, device="cuda")
+    zf.zero_rms_norm(h, None, None, 1e-5, h)
+    zf.zero_head_loss(h, w, torch.arange(n, device="cuda"), loss, None, ws, size)
+    assert float((loss - math.log(vocab)).abs().max()) <= 1e-5
+    assert zf.zero_device_status() == zf.zero.ZERO_DEVICE_OK
+
+
+@pytest.mark.parametrize("limit", [0, -1, 10 ** 9 + 1])
+def test_a_limit_out_of_range_is_refused(limit):
+    with pytest.raises(zf.ZeroError):
+        zf.zero_selftest_tile_wait_timeout(limit)
