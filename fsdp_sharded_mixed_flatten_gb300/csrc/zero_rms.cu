@@ -151,10 +151,14 @@ rms_norm_kernel(const __grid_constant__ RmsArgs a) {
     }
 }
 
+// The backward pass of rows of which shared memory holds less than two: from 8225 columns on,
+// of fp32 (with s in 8 bits from 10465 on), of bf16 with an fp32 weight from 14393 on.
 // EIGHT: s comes in 8 bits.
-template <class T, int K, bool WIDE, bool EIGHT>
+constexpr int kWideOctets = 4;
+template <class T, bool WIDE, bool EIGHT>
 __global__ void __launch_bounds__(512, 1)
 rms_norm_grad_kernel(const __grid_constant__ RmsArgs a) {
+    constexpr int K = kWideOctets;
     extern __shared__ float cols[];                  // [groups][dim] at the end
     __shared__ float red[2][kRmsWarps];
     int half = 0;
@@ -170,9 +174,6 @@ rms_norm_grad_kernel(const __grid_constant__ RmsArgs a) {
         for (int e = 0; e < 8; ++e) dw[k][e] = 0.0f;
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    constexpr bool kHeld = K == 1;           // the weight in registers
-    float held[8];
-    if constexpr (kHeld) c.params(held, a.weight, a.param_f32, 0);
     for (; row < a.n_rows; row += step) {
         float xh[K][8], gr[K][8];
         const float r = a.rstd[row];
@@ -191,10 +192,9 @@ rms_norm_grad_kernel(const __grid_constant__ RmsArgs a) {
             const Octet<T> dy =
                 c.template load<T>(static_cast<const T*>(a.grad_out) + row * a.grad_out_stride, k);
             float w[8];
-            if constexpr (!kHeld) c.params(w, a.weight, a.param_f32, k);
+            c.params(w, a.weight, a.param_f32, k);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                if (kHeld) w[e] = held[e];
                 const float d = widen<T>(dy.x[e]);
                 xh[k][e] *= r;
                 gr[k][e] = d * w[e];
@@ -873,8 +873,7 @@ struct RmsShape {
     int k, group, per_cta;
 };
 
-RmsShape rms_shape(int64_t dim) {
-    const int k = dim <= 4096 ? 1 : dim <= 8192 ? 2 : 4;
+RmsShape rms_shape(int64_t dim, int k) {
     const int group = static_cast<int>((dim + 256 * k - 1) / (256 * k) * 32);
     int per_cta = 512 / group;
     if (per_cta > 8) per_cta = 8;               // 16 hardware barriers a CTA
@@ -975,7 +974,7 @@ RmsPlan forward_plan(const RmsArgs& a, int act_bytes) {
              wide_rows(a.total, a.total_stride, act_bytes) &&
              wide_rows(a.out, a.out_stride, act_bytes) && wide_codes(a.out8, a.out8_stride) &&
              wide_codes(a.total8, a.total8_stride);
-    p.straight = rms_shape(a.dim);
+    p.straight = rms_shape(a.dim, a.dim <= 4096 ? 1 : a.dim <= 8192 ? 2 : 4);
     p.through = rows_shape(a.dim, act_bytes,
                            (a.residual != nullptr ? 2 : 1) * row_room(a.dim, act_bytes, true),
                            a.weight != nullptr && a.param_f32, false);
@@ -993,7 +992,7 @@ RmsPlan backward_plan(const RmsArgs& a, int act_bytes) {
              wide_rows(a.grad_total, a.grad_total_stride, act_bytes) &&
              wide_rows(a.grad_x, a.grad_x_stride, act_bytes) &&
              wide_rows(a.out, a.out_stride, act_bytes) && wide_codes(a.total8, a.total8_stride);
-    p.straight = rms_shape(a.dim);
+    p.straight = rms_shape(a.dim, kWideOctets);
     const bool grid = p.wide && a.dim % 8 == 0 &&
                       (!eight || (a.dim % 16 == 0 && wide_rows(a.total8, a.total8_stride, 1)));
     p.through = rows_shape(a.dim, act_bytes,
@@ -1055,28 +1054,32 @@ cudaError_t launch_rms_norm_grad(RmsArgs a, int act_bytes, cudaStream_t stream) 
     a.slot_bytes = static_cast<uint32_t>(p.through.slot_bytes);
     return by_type(act_bytes, [&](auto t) {
         using T = decltype(t);
-        return by_k(p.rows ? p.through.k : p.straight.k, [&](auto k) {
-            constexpr int K = k.value;
-            if (p.rows)
+        if (p.rows)
+            return by_k(p.through.k, [&](auto k) {
+                constexpr int K = k.value;
                 return a.total8 != nullptr
                            ? (p.wide ? launch_rows<T, K, true, true, true>(a, p, stream)
                                      : launch_rows<T, K, false, true, true>(a, p, stream))
                            : (p.wide ? launch_rows<T, K, true, true, false>(a, p, stream)
                                      : launch_rows<T, K, false, true, false>(a, p, stream));
-            const auto kernel = a.total8 != nullptr
-                                    ? (p.wide ? rms_norm_grad_kernel<T, K, true, true>
-                                              : rms_norm_grad_kernel<T, K, false, true>)
-                                    : (p.wide ? rms_norm_grad_kernel<T, K, true, false>
-                                              : rms_norm_grad_kernel<T, K, false, false>);
-            // at most 64 KB: 4 groups of 4096 columns, 1 of 16384
-            if (cudaError_t e = cudaFuncSetAttribute(
-                    kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
-                e != cudaSuccess)
-                return e;
-            kernel<<<static_cast<unsigned>(p.grid), p.straight.group * p.straight.per_cta,
-                     sizeof(float) * p.straight.per_cta * a.dim, stream>>>(a);
-            return cudaGetLastError();
-        });
+            });
+        auto kernel =
+            p.wide ? rms_norm_grad_kernel<T, true, false> : rms_norm_grad_kernel<T, false, false>;
+        if (a.total8 != nullptr) {
+            // (shared memory holds two rows of bf16 beside 8 bits, however wide)
+            if constexpr (sizeof(T) == 2) return cudaErrorInvalidConfiguration;
+            else
+                kernel = p.wide ? rms_norm_grad_kernel<T, true, true>
+                                : rms_norm_grad_kernel<T, false, true>;
+        }
+        // one group of up to 16384 columns: 64 KB
+        if (cudaError_t e = cudaFuncSetAttribute(
+                kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+            e != cudaSuccess)
+            return e;
+        kernel<<<static_cast<unsigned>(p.grid), p.straight.group * p.straight.per_cta,
+                 sizeof(float) * p.straight.per_cta * a.dim, stream>>>(a);
+        return cudaGetLastError();
     });
 }
 

@@ -30,14 +30,6 @@ __device__ __forceinline__ void cluster_sync() {
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(p));
-    return p != 0;
-}
-
 // ------------------------------------------------------------ barriers ------
 
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
