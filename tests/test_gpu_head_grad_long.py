@@ -126,3 +126,17 @@ def test_sums_over_a_long_vocabulary(n):
     want = mean - own
     off = (dh.to(F64) - want).abs()
     assert bool((off <= 2.0 ** -8 * want.abs() + 2.0 ** -11 * mean + 2.0 ** -20 * own).all())
+
+
+@pytest.mark.parametrize("n", [20, 50, 200, 300])
+def test_the_losss_logits_are_sums_of_short_parts(n):
+    """The same of the loss, in the mean over tokens whose label's logit is 0: it is the other
+    logit itself."""
+    d = 4096
+    h, w, y = _sure(n, d, 300.0)
+    z = h.to(F64) @ w[11].to(F64)
+    ws, size = _workspace(n, 40, d)
+    loss, lse = torch.empty((2, n), device="cuda")
+    zf.zero_head_loss(h, w, torch.full_like(y, 3), loss, lse, ws, size)
+    off = float((loss.to(F64) - z).mean().abs() / z.mean())
+    assert off <= 56 * 2.0 ** -24, f"off by {off * 2.0 ** 24} 2^-24"
