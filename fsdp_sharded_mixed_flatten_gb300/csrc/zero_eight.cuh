@@ -5,7 +5,8 @@
 // largest finite magnitude to at most 448.  e4m3 is a floating format, so a power of two
 // loses no digits against amax / 448, and makes every product by the scale or its inverse
 // exact: the only rounding is the one to 4 significant bits (half a step, 2^-4 relative,
-// or 2^-10 of the scale below 2^-6 of it), and what is unpacked fits bf16 as it is.
+// or 2^-10 of the scale below 2^-6 of it), and what is unpacked fits bf16 as it is (of scales
+// below 2^-124 but for the last bits).
 #pragma once
 
 #include <cstdint>

@@ -6,8 +6,8 @@
 // The products run on the tensor cores (bf16 operands, fp32 sums) by pairs of CTAs on 256 x
 // 256 tiles: one thread streams operands by TMA into a ring in shared memory, one thread of
 // the pair issues the products, eight warps turn finished tiles of tensor memory into
-// results while the next tile's products run.  The forward pass leaves a maximum and a sum
-// of exponentials for each row and tile, joined by a second launch.  The backward pass
+// results while the next tile's products run.  The forward pass leaves a maximum of the logits
+// and a sum of exponentials for each row and tile, joined by a second launch.  The backward pass
 // works through the vocabulary in pieces: the piece's z again, its dz in bf16 to the
 // workspace, then dz W, added up in fp32 over the pieces, and dz^T h.
 //
@@ -21,11 +21,12 @@
 // tokens without a label cost nothing and their values reach nothing.
 //
 // Bound by the tensor cores under the power cap where products are long: gradients of 8192
-// tokens of a table of 131072 x 4096 15.5 ms (1.70 PFLOP/s), the loss of 5500 live ones 3.5
-// ms (1.67).  Shorter sums are bound by shared memory, which operands on their way in and out
-// fill at the tensor cores' rate, and results cross too: 8192 tokens, 50257 x 768, 1.27 ms
-// (1.49 PFLOP/s).  Few tokens, whose loss has a kernel of its own: by reading the table, and a
-// launch's start and end (8 tokens, 131072 x 4096 158 us, 6.8 TB/s; 32, 50257 x 768 19.5 us).
+// tokens of a table of 131072 x 4096 15.5 to 16.2 ms (1.70 to 1.63 PFLOP/s), the loss of 5500
+// live ones 3.1 to 3.7 ms (1.9 to 1.6).  Shorter sums are bound by shared memory, which operands
+// on their way in and out fill at the tensor cores' rate, and results cross too: 8192 tokens,
+// 50257 x 768, 1.18 to 1.34 ms (1.61 to 1.42 PFLOP/s).  Few tokens, whose loss has a kernel of
+// its own: by reading the table, and a launch's start and end (8 tokens, 131072 x 4096 158 to
+// 165 us, 6.8 to 6.5 TB/s; 32, 50257 x 768 19.5 to 21.7 us).
 #include "zero_head.cuh"
 
 #include <cfloat>

@@ -273,7 +273,8 @@ int zero_step(const uint16_t* const* grads, float* const* master, float* const* 
 /*
  * zero_device_status -- host, synchronous.  Failure detection for the kernels
  * that wait on shared-memory barriers (the bulk-copy staged fused step and
- * reduce-scatter, the head's products, the root-mean-square norm's rows): every such wait gives up after about 2 seconds, records
+ * reduce-scatter, the head's products, the root-mean-square norm's rows): every
+ * such wait gives up after about 2 seconds, records
  * ZERO_DEVICE_TIMEOUT in a device status word, and the kernel returns early
  * (its outputs are then incomplete).  A dynamically scheduled launch that
  * found its tile counter used by another launch at the same time records
@@ -625,8 +626,8 @@ int zero_distill_loss_grad(const void* logits, int32_t logits_bytes, int64_t n_r
  * infinity) and do not count for the scale.
  *   codes             n_rows rows of dim bytes, codes_stride apart
  *   scales            [n_rows][ceil(dim / 128)] fp32, contiguous
- * Every value fits bf16 as it is.  Rows in 8 bits keep activations for a backward pass
- * at 1.03 bytes a value.
+ * Values of a scale of 2^-124 and more fit bf16 as they are.  Rows in 8 bits keep
+ * activations for a backward pass at 1.03 bytes a value.
  *
  * zero_pack_rows -- device.  codes and scales of the rows of x.
  * zero_unpack_rows -- device.  out = code * scale, rounded to out's type.
@@ -644,13 +645,15 @@ int zero_unpack_rows(const uint8_t* codes, int64_t codes_stride, const float* sc
  * every row
  *   total = x + residual,  rstd = 1 / sqrt(sum(total^2) / dim + eps),
  *   out = total * rstd * weight
- * with the sum as it is in fp32, before any rounding.
+ * with the sum as it is in fp32, before any rounding, and rows of any finite sums (their
+ * squares may be beyond fp32).
  *   x, residual       n_rows rows of dim, of type act_bytes; residual NULL: total = x
  *   weight            dim values of type param_bytes; NULL: ones
  *   out, total        rows of type act_bytes, or NULL: not wanted; total may be x or
  *                     residual, out may be x (with the same stride), if they are not
  *                     the same array
- *   out8, total8      the same in 8 bits (codes; their scales beside them), or NULL
+ *   out8, total8      the same in 8 bits (codes; their scales beside them), or NULL;
+ *                     arrays of their own
  *   rstd              n_rows fp32, or NULL where no backward pass follows
  * Errors: INVALID_ARG (eps negative or not finite in fp32, codes without scales, ...),
  * MISALIGNED, SIZE (dim > ZERO_MAX_NORM_DIM, in place with another stride), CUDA.
@@ -697,7 +700,8 @@ int zero_rms_norm_grad_workspace_bytes(int64_t n_rows, int64_t dim, int64_t* byt
  * without the logits in memory:
  *   z = hidden table^T,  lse = log(sum_v exp(z_v)),  loss = lse - z[label]
  * for tokens with a label in [0, vocab); 0 in loss and lse for the others, whatever
- * their hidden states hold.  Products of bf16 are summed in fp32.
+ * their hidden states hold.  Products of bf16 are summed in fp32; logits may have any
+ * size that fp32 holds.
  *   hidden            n_tokens rows of dim, bf16
  *   table             [vocab][dim] contiguous, bf16 (of a flat parameter buffer, at any
  *                     element; on a 16-byte boundary with dim a multiple of 8 it is read
@@ -716,15 +720,17 @@ int zero_rms_norm_grad_workspace_bytes(int64_t n_rows, int64_t dim, int64_t* byt
  * zero_head_loss_grad -- device.  Its gradients from the forward's lse and the gradient
  * of each token's loss, with dz = grad_loss * (exp(z - lse) - [v = label]):
  *   grad_hidden = dz table,   grad_table = dz^T hidden   (added to it, if accumulate)
- * z is computed again, in pieces of the vocabulary; dz is rounded to bf16, sums are held
- * in fp32 and rounded once (to bf16).  Tokens without a label in [0, vocab) or with
+ * z is computed again, in pieces of the vocabulary, to the bits that the loss found; dz is
+ * rounded to bf16 (2^-8 of itself at most; 2^-16 where at most 128 tokens take part), sums
+ * are held in fp32 and rounded once (to bf16).  Tokens without a label in [0, vocab) or with
  * grad_loss 0 get a gradient of zeros and add nothing, whatever their rows hold.
  *   grad_loss         n_tokens fp32
  *   grad_hidden       n_tokens rows of dim, bf16; may be hidden (with the same stride);
  *                     NULL: not wanted
  *   grad_table        [vocab][dim] contiguous, bf16, at any element; NULL: not wanted
  *   accumulate        0 or 1
- *   workspace         as above, of zero_head_loss_grad_workspace_bytes
+ *   workspace         as above, of zero_head_loss_grad_workspace_bytes; dz takes 512 MB of it
+ *                     at most (more beyond 1M tokens), a copy of a piece of the table as much
  */
 #define ZERO_MAX_HEAD_TOKENS (1 << 22)
 #define ZERO_MAX_HEAD_VOCAB (1 << 22)
