@@ -1637,16 +1637,21 @@ int64_t tiles_of(int64_t x, int64_t width) { return (x + width - 1) / width; }
 // launch of m rows of tiles, n columns, in rounds over the GPU's pairs.  Measured: 12 steps of
 // width 256 7500 to 8400 cycles, 64 steps 36000 to 40000.
 double tile_cost(double steps, int width) { return (256.0 + width) * steps + 12.0 * width + 800.0; }
-int64_t pairs_of_gpu() { return device_sms() / 2 > 0 ? device_sms() / 2 : 1; }
-double launch_cost(int64_t m, int64_t n, int64_t steps, int width) {
-    const int64_t rounds = (m * tiles_of(n, width) + pairs_of_gpu() - 1) / pairs_of_gpu();
+int64_t pairs_of(int sms) { return sms / 2 > 0 ? sms / 2 : 1; }
+double launch_cost(int64_t m, int64_t n, int64_t steps, int width, int64_t pairs) {
+    const int64_t rounds = (m * tiles_of(n, width) + pairs - 1) / pairs;
     return static_cast<double>(rounds) * tile_cost(static_cast<double>(steps), width);
 }
 
-int best_width(int64_t m, int64_t n, int64_t steps, int unit) {
+int best_width(int64_t m, int64_t n, int64_t steps, int unit, int64_t pairs) {
     int best = kPairTile;
+    double least = launch_cost(m, n, steps, best, pairs);
     for (int w = kPairTile - unit; w >= unit; w -= unit) {
-        if (launch_cost(m, n, steps, w) < 0.98 * launch_cost(m, n, steps, best)) best = w;
+        const double cost = launch_cost(m, n, steps, w, pairs);
+        if (cost < 0.98 * least) {
+            best = w;
+            least = cost;
+        }
     }
     return best;
 }
@@ -1657,8 +1662,9 @@ int best_width(int64_t m, int64_t n, int64_t steps, int unit) {
 // 16-byte grid, take at most 512 MB each (but 256 rows at least, whose gradient takes more
 // beyond 1M tokens); as even as whole tiles allow.  Forward, a table that is read in place is
 // one piece.
-HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, bool in_place) {
+static HeadPlan plan_on(int sms, int64_t n_tokens, int64_t vocab, int64_t dim, bool back, bool in_place) {
     constexpr int64_t kMost = int64_t{512} << 20;
+    const int64_t pairs = pairs_of(sms);
     HeadPlan p{};
     p.rows = whole(n_tokens < 1 ? 1 : n_tokens, kPairTile);
     p.pitch = whole(dim, 64);                // rows on 128-byte boundaries: fewer lines a box
@@ -1673,23 +1679,26 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, bool
     p.splits = 1;
     const int64_t steps_dim = tiles_of(dim, kTileK);
     if (back) {
-        p.width_z = best_width(m, p.piece < vocab ? p.piece : vocab, steps_dim, 64);
+        p.width_z = best_width(m, p.piece < vocab ? p.piece : vocab, steps_dim, 64, pairs);
         const int64_t steps = tiles_of(p.piece, kTileK), steps_w = tiles_of(n_tokens, kTileK);
-        p.width_w = best_width(tiles_of(p.piece, kPairTile), dim, steps_w, 32);
+        p.width_w = best_width(tiles_of(p.piece, kPairTile), dim, steps_w, 32, pairs);
         // The sum over a piece in as many parts as keep the GPU's pairs busy: the launch takes
         // the tiles' average on a pair, half a tile more at its end, and every part is written,
         // and read again in the end, at 6 TB/s and 1.9 GHz.
         const double tile_w = tile_cost(steps_w, p.width_w);
         const double all_w =
-            tile_w * tiles_of(p.piece, kPairTile) * tiles_of(dim, p.width_w) / pairs_of_gpu();
+            tile_w * tiles_of(p.piece, kPairTile) * tiles_of(dim, p.width_w) / pairs;
         const double way = 8.0 * p.rows * whole(dim, 32) / 6e12 * 1.9e9;
+        double wide[kPairTile / 32 + 1];             // tiles of width 32 i
+        for (int i = 1; i <= kPairTile / 32; ++i)
+            wide[i] = static_cast<double>(m * tiles_of(dim, 32 * i));
         double best = 0.0;
         for (int64_t s : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 40, 48, 64}) {
             if (s > 1 && (s * 4 > steps || s * p.rows * p.pitch * 4 > kMost)) break;
             for (int w = kPairTile; w >= 32; w -= 32) {
                 const double tile = tile_cost(steps / static_cast<double>(s), w);
                 const double cost =
-                    tile * m * tiles_of(dim, w) * s / pairs_of_gpu() + all_w +
+                    tile * wide[w / 32] * s / pairs + all_w +
                     0.5 * (tile > tile_w ? tile : tile_w) + way * s;
                 if ((s == 1 && w == kPairTile) || cost < 0.98 * best) {
                     best = cost;
@@ -1699,7 +1708,7 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, bool
             }
         }
     } else {
-        p.width_z = best_width(m, p.piece < vocab ? p.piece : vocab, steps_dim, 32);
+        p.width_z = best_width(m, p.piece < vocab ? p.piece : vocab, steps_dim, 32, pairs);
         p.parts_a_piece = static_cast<int32_t>(tiles_of(p.piece, p.width_z));
         p.parts_a_row = static_cast<int32_t>((pieces - 1) * p.parts_a_piece +
                                              tiles_of(vocab - (pieces - 1) * p.piece, p.width_z));
@@ -1724,7 +1733,7 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, bool
         p.sums = place(4 * p.splits * p.rows * whole(dim, 32));
     } else {
         // (of few tokens one part a CTA, perhaps)
-        const int64_t few = n <= kFewMost ? device_sms() : 0;
+        const int64_t few = n <= kFewMost ? sms : 0;
         p.parts = place(8 * n * (p.parts_a_row > few ? p.parts_a_row : few));
         p.picked = place(4 * n);
     }
@@ -1732,12 +1741,17 @@ HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, bool
     return p;
 }
 
+HeadPlan head_plan(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, bool in_place) {
+    return plan_on(device_sms(), n_tokens, vocab, dim, back, in_place);
+}
+
 // A smaller call's pieces may be larger and its splits more, and with them its needs.  A plan
 // goes by whole tiles and, for the table's gradient, steps of tokens, and grows within them.
 int64_t head_bytes(int64_t n_tokens, int64_t vocab, int64_t dim, bool back, bool in_place) {
-    int64_t most = head_plan(n_tokens, vocab, dim, back, in_place).bytes;
+    const int sms = device_sms();
+    int64_t most = plan_on(sms, n_tokens, vocab, dim, back, in_place).bytes;
     for (int64_t n = kTileK; n < n_tokens; n += kTileK) {
-        const int64_t bytes = head_plan(n, vocab, dim, back, in_place).bytes;
+        const int64_t bytes = plan_on(sms, n, vocab, dim, back, in_place).bytes;
         if (bytes > most) most = bytes;
     }
     return most;
