@@ -22,8 +22,8 @@ def _gpu():
     zf.load()
 
 
-@pytest.mark.parametrize("n,vocab,d", [(1, 9000, 4096), (33, 50257, 64), (300, 2048, 768),
-                                       (8192, 50257, 64), (130, 70000, 4096), (9000, 600, 96)])
+@pytest.mark.parametrize("n,vocab,d", [(1, 9000, 1024), (33, 50257, 64), (300, 2048, 768),
+                                       (8192, 50257, 64), (130, 70000, 256), (9000, 600, 96)])
 def test_within_the_workspace_of_a_table_read_in_place(n, vocab, d):
     g = torch.Generator().manual_seed(n + vocab)
     h = (torch.randn((n, d), generator=g) * (8.0 / d ** 0.5)).to(BF16).cuda()
